@@ -13,6 +13,13 @@
  *   gemm_bias_relu_host     gemm_bias_relu on host buffers, copies overlapped
  *   staged_copy             gmem -> smem -> gmem through the ring (TMA both ways)
  *
+ * and the feed-forward operators around them (at the end of this file):
+ *
+ *   gemm_bias_act           C = residual + dropout(act(A * B + bias)), any row
+ *                           strides; gemm_bias_act_backward: its gradients
+ *   dropout_add             Y = residual + dropout(X), the mask never stored
+ *   moe_layer               router, experts and their sum for a few tokens
+ *
  * Conventions shared by every entry point
  *   - Tensors are contiguous, row-major, resident in device memory of the
  *     current CUDA device, allocated and owned by the caller.  The library
@@ -25,7 +32,8 @@
  *   - Device-side failures (a pipeline wait that exceeded its time limit) are
  *     reported by gbr_device_status(), which also clears them.  The status
  *     block keeps the FIRST timeout recorded since the last read.
- *   - Global addresses must be 16-byte aligned and every row pitch must be a
+ *   - Unless an entry point says otherwise,
+ *     global addresses must be 16-byte aligned and every row pitch must be a
  *     multiple of 16 bytes (the TMA rule): fp32 row lengths a multiple of 4,
  *     bf16 row lengths a multiple of 8.  Otherwise GBR_ERR_ALIGN.
  *   - The library keeps, per device, a 64-byte status block it allocates on
@@ -426,6 +434,89 @@ int gemm_bias_relu_tf32_noalloc(const float *A, const float *B, const float *bia
 int gbr_selftest_noalloc_skip_load(const float *A, const float *B, const float *bias, float *C,
                                    int64_t M, int64_t N, int64_t K, int stages, int cta, int item,
                                    uint64_t limit_ns, gbr_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The feed-forward operators: a linear layer with its epilogue and gradients,
+ * dropout, and an expert layer for a few tokens.
+ * ------------------------------------------------------------------------ */
+
+/* Activations.  GELU by the error function or by its tanh form. */
+typedef enum {
+    GBR_ACT_NONE = 0,
+    GBR_ACT_RELU = 1,
+    GBR_ACT_GELU = 2,
+    GBR_ACT_GELU_TANH = 3,
+    GBR_ACT_SILU = 4
+} gbr_act;
+
+/*
+ * Dropout, here and in gemm_bias_act: the mask is a function of (seed, offset,
+ * row, column) alone, by Philox-4x32-10 (key: the seed; counter: column / 8,
+ * row, offset; 16 random bits a column), and is never stored: whoever calls
+ * with the same seed and offset sees the same mask, the backward pass first of
+ * all.  threshold = round(65536 p) of 65536 columns are dropped on average and
+ * the rest multiplied by 65536 / (65536 - threshold); p = 0 keeps and p = 1
+ * drops everything.  A dropped value is an exact zero, also of Inf and NaN.
+ * Seed and offset are values of the call: a captured graph replays one mask.
+ *
+ * dropout_add -- Y = residual + drop(X), on [rows, cols] matrices.
+ *   X, residual (or NULL), Y: ldx, ldr, ldy elements from row to row, >= cols;
+ *   any alignment that the elements have.  Y may be X or residual itself
+ *   (same row stride), but not overlap them otherwise (GBR_ERR_INVALID).
+ *   dtype: GBR_BF16, or GBR_F32_FFMA (= GBR_F32_TF32 here) for fp32 elements.
+ *   Sums are fp32, rounded once.  The gradient of X is dropout_add of dY with
+ *   the same p, seed and offset and no residual; that of residual is dY.
+ */
+int dropout_add(const void *X, int64_t ldx, const void *residual, int64_t ldr, void *Y, int64_t ldy,
+                int64_t rows, int64_t cols, int dtype, double p, uint64_t seed, uint64_t offset,
+                gbr_stream_t stream);
+
+/*
+ * gemm_bias_act -- C = residual + drop(act(Z)), Z = A * B + bias.
+ *   A [M, K], B [K, N], residual [M, N], C [M, N], Z [M, N]: bf16, row-major,
+ *   lda ... elements from row to row; bias [N] fp32.  bias, residual and Z may
+ *   be NULL (no addition; Z not wanted).  C may be residual itself.  Otherwise
+ *   no output may overlap an input or the other output (GBR_ERR_INVALID).
+ *   dtype GBR_BF16 (GBR_ERR_UNSUPPORTED for the others); act a gbr_act.
+ *   fp32 accumulation and epilogue; C and Z are rounded once, from fp32.
+ *   K == 0: Z = bias.  M, N, K < 2^31; any sizes and row strides.
+ * gemm_bias_act_backward -- the gradients for dC = dLoss/dC, with the Z, p,
+ * seed and offset of the forward call:
+ *   dZ = drop(dC) * act'(Z);  dA = dZ B^T;  dB = A^T dZ;  dbias = column sums
+ *   of dZ (fp32, in an order that does not change).  The gradient of residual
+ *   is dC itself.  dA [M, K], dB [K, N] bf16, dbias [N] fp32; each may be NULL
+ *   (not wanted).  Z may be NULL when act is none, A when dB is, B when dA is.
+ *   dZ is rounded to bf16 as the products' operand; dbias sums it unrounded.
+ */
+int gemm_bias_act(const void *A, int64_t lda, const void *B, int64_t ldb, const float *bias,
+                  const void *residual, int64_t ldr, void *C, int64_t ldc, void *Z, int64_t ldz,
+                  int64_t M, int64_t N, int64_t K, int dtype, int act, double p, uint64_t seed,
+                  uint64_t offset, gbr_stream_t stream);
+int gemm_bias_act_backward(const void *dC, int64_t lddc, const void *A, int64_t lda, const void *B,
+                           int64_t ldb, const void *Z, int64_t ldz, void *dA, int64_t ldda, void *dB,
+                           int64_t lddb, float *dbias, int64_t M, int64_t N, int64_t K, int dtype,
+                           int act, double p, uint64_t seed, uint64_t offset, gbr_stream_t stream);
+
+/*
+ * moe_layer -- a whole mixture-of-experts layer for a few tokens (decoding):
+ *   logits = X Wr;  each token takes its top_k largest (ties: the lowest
+ *   expert; NaN ranks last), weighted by the softmax over those top_k;
+ *   y_t = sum over its experts e of w_te (h_te W2_e + b2_e),
+ *   h_te = act(x_t W1_e + b1_e), or with gated = 1, W1_e = [gate | up]:
+ *   act(x_t gate + b1) * (x_t up + b1'), elementwise.
+ *   X [T, D], W1 [E, D, F] ([E, D, 2F] gated), W2 [E, F, D], Y [T, D] bf16;
+ *   Wr [D, E], b1 [E, F] ([E, 2F]), b2 [E, D] fp32, b1 and b2 may be NULL.
+ *   expert_ids [T, top_k] int64 and expert_weights [T, top_k] fp32, in falling
+ *   order of the logits, are written unless NULL.
+ *   T 0..64, E 1..256, top_k 1..min(8, E); D and F multiples of 8; all buffers
+ *   contiguous and 16-byte aligned (GBR_ERR_ALIGN).  Outputs overlap nothing.
+ *   Products and sums are fp32; the hidden values are rounded to bf16 as the
+ *   operand of the second product.  The order of every sum is fixed.
+ */
+int moe_layer(const void *X, const float *Wr, const void *W1, const float *b1, const void *W2,
+              const float *b2, void *Y, int64_t *expert_ids, float *expert_weights, int64_t T,
+              int64_t D, int64_t F, int num_experts, int top_k, int act, int gated, int dtype,
+              gbr_stream_t stream);
 
 #ifdef __cplusplus
 }

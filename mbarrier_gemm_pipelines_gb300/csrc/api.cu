@@ -397,6 +397,30 @@ int check_umma_regs(DevCtx& c, int kind, bool grouped, int pair) {
 }  // namespace
 
 int report_error(int code, const char* msg) { return fail(code, "%s", msg); }
+int report_errorf(int code, const char* fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof(buf), fmt, ap);
+    va_end(ap);
+    return fail(code, "%s", buf);
+}
+int report_cuda(cudaError_t e, const char* what) { return cuda_fail(e, what); }
+int lib_ctx(LibCtx* out) {
+    DevCtx* c;
+    const int r = get_ctx(&c, &out->device);
+    if (r != GBR_OK) return r;
+    out->sm_count = c->sm_count;
+    out->smem_optin = c->smem_optin;
+    out->pool = c->pool;
+    out->ctl = make_ctl(*c);
+    return GBR_OK;
+}
+int encode_tensor_map(CUtensorMap* map, CUtensorMapDataType dt, uint32_t rank, const void* ptr,
+                      const uint64_t* dims, const uint64_t* strides_bytes, const uint32_t* box,
+                      CUtensorMapSwizzle swz, const char* what) {
+    return encode(map, dt, rank, ptr, dims, strides_bytes, box, swz, what);
+}
 void count_launch() { ++g_launches; }
 uint64_t wait_timeout_ns() { return t_timeout_override ? t_timeout_override : timeout_ns(); }
 FaultInjection injection_now() { return t_inject; }

@@ -195,6 +195,20 @@ int programmatic_launch_attr(cudaLaunchAttribute* attr);
 
 // ------------------------------------------------------------ api.cu services
 int report_error(int code, const char* msg);   // sets gbr_last_error(), returns code
+int report_errorf(int code, const char* fmt, ...);
+int report_cuda(cudaError_t e, const char* what);
+// What a call needs to know of the current device.
+struct LibCtx {
+    int device;
+    int sm_count;
+    int smem_optin;
+    cudaMemPool_t pool;
+    KernelCtl ctl;
+};
+int lib_ctx(LibCtx* out);                      // GBR_OK or an error code
+int encode_tensor_map(CUtensorMap* map, CUtensorMapDataType dt, uint32_t rank, const void* ptr,
+                      const uint64_t* dims, const uint64_t* strides_bytes, const uint32_t* box,
+                      CUtensorMapSwizzle swz, const char* what);
 void count_launch();                           // adds one to gbr_launch_count()
 uint64_t wait_timeout_ns();                    // per-wait limit of this thread's next launch
 FaultInjection injection_now();                // self-test fault of this thread's next launch
