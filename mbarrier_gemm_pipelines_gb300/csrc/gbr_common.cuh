@@ -26,6 +26,7 @@ enum WaitSite : uint32_t {
     kSiteEpiSplitSum = 0x42,
     kSiteEpiTile = 0x43,
     kSiteEpiBias = 0x44,
+    kSiteEpiResidual = 0x45,
     kSiteStorerFull = 0x51,
     kSiteSelfTest = 0x71,
 };

@@ -1,0 +1,290 @@
+// linear.cu -- host side of the fused linear layer and its gradients: operands
+// that TMA cannot read are re-pitched, tensor maps, the choice of the kernel
+// and the launches; and the kernel of dZ and dbias.
+#include "linear_pair.cuh"
+
+#include "gbr.h"
+
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <cstring>
+#include <map>
+#include <mutex>
+#include <utility>
+
+namespace gbr {
+
+void* linear_pair_forward_kernel(int act);
+void* linear_pair_da_kernel();
+void* linear_pair_db_kernel();
+
+namespace {
+
+using bf16 = __nv_bfloat16;
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// ------------------------------------------------------------ re-pitching
+// dst[r, c] = src[r, c] for bf16 matrices of any pitch and alignment: what TMA
+// cannot address (a pitch or a start that is no multiple of 16 bytes) passes
+// through an aligned copy.  One pass over that operand; a product that is not
+// tiny spends far longer on its tiles.
+__global__ void __launch_bounds__(256)
+    repitch_kernel(const bf16* src, int64_t lds, bf16* dst, int64_t ldd, int32_t rows, int32_t cols) {
+    ptx::griddep_wait();
+    for (int64_t r = blockIdx.y; r < rows; r += gridDim.y)
+        for (int64_t c = int64_t(blockIdx.x) * 256 + threadIdx.x; c < cols; c += int64_t(gridDim.x) * 256)
+            dst[r * ldd + c] = src[r * lds + c];
+}
+
+cudaError_t launch_plain(void* kernel, dim3 grid, int threads, size_t smem, int cluster, void** args,
+                         cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    unsigned n = 0;
+    if (cluster > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = unsigned(cluster);
+        attr[n].val.clusterDim.y = 1;
+        attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    n += unsigned(programmatic_launch_attr(attr + n));
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
+    return cudaLaunchKernelExC(&cfg, kernel, args);
+}
+
+int repitch(Mat src, Mat dst, int32_t rows, int32_t cols, cudaStream_t stream) {
+    const bf16* s = static_cast<const bf16*>(src.p);
+    bf16* d = static_cast<bf16*>(dst.w());
+    void* args[] = {&s, &src.ld, &d, &dst.ld, &rows, &cols};
+    const dim3 grid(unsigned(std::min<int64_t>(cdiv(cols, 256), 64)), unsigned(std::min<int64_t>(rows, 8192)));
+    const cudaError_t e = launch_plain(reinterpret_cast<void*>(&repitch_kernel), grid, 256, 0, 1, args, stream);
+    if (e != cudaSuccess) return report_cuda(e, "launching the re-pitching copy");
+    count_launch();
+    return GBR_OK;
+}
+
+bool tma_ready(const Mat& m) {
+    return reinterpret_cast<uintptr_t>(m.p) % 16 == 0 && m.ld % 8 == 0;
+}
+
+// Makes `m` readable by TMA (copy_in) or writable: itself, or an aligned copy.
+// A TMA store ends at whole 16 bytes: measured, a row of 201 bf16 columns takes
+// 7 columns of its pitch's padding along, so an output whose rows end inside
+// 16 bytes is written to a copy and copied back.
+int aligned_mat(Mat* m, int32_t rows, int32_t cols, bool copy_in, Scratch& ws, cudaStream_t stream) {
+    if (rows == 1) m->ld = cdiv(cols, 8) * 8;            // never stepped over
+    if (tma_ready(*m) && (copy_in || cols % 8 == 0)) return GBR_OK;
+    Mat t;
+    t.ld = cdiv(cols, 8) * 8;
+    void* p = nullptr;
+    const int r = ws.take(size_t(rows) * size_t(t.ld) * 2, "cudaMallocFromPoolAsync(aligned operand)", &p);
+    if (r != GBR_OK) return r;
+    t.p = p;
+    if (copy_in) {
+        const int r2 = repitch(*m, t, rows, cols, stream);
+        if (r2 != GBR_OK) return r2;
+    }
+    *m = t;
+    return GBR_OK;
+}
+
+// A 2-D map over rows x cols bf16 with the 128-byte swizzle.
+int map_2d(CUtensorMap* map, const Mat& m, int64_t rows, int64_t cols, uint32_t box_cols, uint32_t box_rows,
+           const char* what) {
+    const uint64_t dims[2] = {uint64_t(cols), uint64_t(rows)};
+    const uint64_t strides[1] = {uint64_t(m.ld) * 2};
+    const uint32_t box[2] = {box_cols, box_rows};
+    return encode_tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, m.p, dims, strides, box,
+                             CU_TENSOR_MAP_SWIZZLE_128B, what);
+}
+
+// ------------------------------------------------------------ CTA pairs
+struct Product {
+    Mat A, B;                      // as stored
+    bool a_mn, b_mn;               // A: stored [I, Kc] (k-major) or [Kc, I]; B: [J, Kc] or [Kc, J]
+    int32_t I, J, Kc;              // output rows, columns, contraction length
+    Mat C, Z, R;
+    const float* bias;
+    Dropout drop;
+    void* kernel;
+};
+
+int check_split(void* kernel) {
+    // setmaxnreg draws on the registers of the launch: 128 threads each side.
+    static std::mutex mu;
+    static std::map<void*, bool> known;
+    std::lock_guard<std::mutex> lk(mu);
+    auto it = known.find(kernel);
+    if (it == known.end()) {
+        cudaFuncAttributes fa;
+        const cudaError_t e = cudaFuncGetAttributes(&fa, kernel);
+        if (e != cudaSuccess) return report_cuda(e, "cudaFuncGetAttributes(linear)");
+        const bool ok = long(fa.numRegs) * linear::kThreads >= 128L * (linear::kRegsWG0 + linear::kRegsWG1);
+        it = known.emplace(kernel, ok).first;
+    }
+    if (!it->second)
+        return report_errorf(GBR_ERR_CUDA, "a linear kernel was built with too few registers for its role split");
+    return GBR_OK;
+}
+
+int raise_smem(void* kernel, size_t smem, int dev) {
+    static std::mutex mu;
+    static std::map<std::pair<void*, int>, size_t> set;
+    std::lock_guard<std::mutex> lk(mu);
+    const cudaError_t e = raise_smem_limit(kernel, smem, &set[{kernel, dev}]);
+    return e == cudaSuccess ? int(GBR_OK) : report_cuda(e, "cudaFuncSetAttribute(linear)");
+}
+
+int run_pair(const Product& p, const LibCtx& c, cudaStream_t stream) {
+    linear::PairParams P;
+    memset(&P, 0, sizeof(P));
+    int r;
+    if ((r = map_2d(&P.mapC, p.C, p.I, p.J, 64, 32, "C")) != GBR_OK) return r;
+    P.mapA = P.mapB = P.mapZ = P.mapR = P.mapC;          // where unused
+    if (p.Kc > 0) {
+        if ((r = p.a_mn ? map_2d(&P.mapA, p.A, p.Kc, p.I, 64, 64, "A") : map_2d(&P.mapA, p.A, p.I, p.Kc, 64, 128, "A")) !=
+            GBR_OK)
+            return r;
+        if ((r = p.b_mn ? map_2d(&P.mapB, p.B, p.Kc, p.J, 64, 64, "B") : map_2d(&P.mapB, p.B, p.J, p.Kc, 64, 128, "B")) !=
+            GBR_OK)
+            return r;
+    }
+    if (p.Z && (r = map_2d(&P.mapZ, p.Z, p.I, p.J, 64, 32, "Z")) != GBR_OK) return r;
+    if (p.R && (r = map_2d(&P.mapR, p.R, p.I, p.J, 64, 32, "residual")) != GBR_OK) return r;
+    P.has_z = bool(p.Z);
+    P.has_r = bool(p.R);
+    P.bias = p.bias;
+    P.M = p.I, P.N = p.J;
+    P.m_tiles = int32_t(cdiv(p.I, linear::kTile));
+    P.n_tiles = int32_t(cdiv(p.J, linear::kTile));
+    const int64_t tiles = int64_t(P.m_tiles) * P.n_tiles;
+    if (tiles >= (int64_t(1) << 31)) return report_errorf(GBR_ERR_INVALID, "linear: too many output tiles");
+    P.num_tiles = int32_t(tiles);
+    P.num_kb = int32_t(cdiv(p.Kc, 64 * linear::kSlices));
+    P.group_m = 8;
+    P.drop = p.drop;
+    P.ctl = c.ctl;
+    if ((r = check_split(p.kernel)) != GBR_OK || (r = raise_smem(p.kernel, linear::kSmemBytes, c.device)) != GBR_OK)
+        return r;
+    const int64_t units = std::min<int64_t>(c.sm_count / 2, tiles);
+    void* args[] = {&P};
+    const cudaError_t e = launch_plain(p.kernel, dim3(unsigned(2 * units)), linear::kThreads, linear::kSmemBytes, 2,
+                                       args, stream);
+    if (e != cudaSuccess) return report_cuda(e, "launching a linear kernel");
+    count_launch();
+    return GBR_OK;
+}
+
+// Runs the product with whatever TMA cannot address replaced by aligned copies.
+int run_product(Product p, const LibCtx& c, cudaStream_t stream) {
+    Scratch ws(c, stream);
+    int r;
+    const Mat C = p.C, Z = p.Z;
+    if (p.Kc > 0) {
+        if ((r = aligned_mat(&p.A, p.a_mn ? p.Kc : p.I, p.a_mn ? p.I : p.Kc, true, ws, stream)) != GBR_OK) return r;
+        if ((r = aligned_mat(&p.B, p.b_mn ? p.Kc : p.J, p.b_mn ? p.J : p.Kc, true, ws, stream)) != GBR_OK) return r;
+    }
+    if (p.R && (r = aligned_mat(&p.R, p.I, p.J, true, ws, stream)) != GBR_OK) return r;
+    if ((r = aligned_mat(&p.C, p.I, p.J, false, ws, stream)) != GBR_OK) return r;
+    if (p.Z && (r = aligned_mat(&p.Z, p.I, p.J, false, ws, stream)) != GBR_OK) return r;
+    if ((r = run_pair(p, c, stream)) != GBR_OK) return r;
+    if (p.C.p != C.p && (r = repitch(p.C, C, p.I, p.J, stream)) != GBR_OK) return r;
+    if (p.Z.p != Z.p && (r = repitch(p.Z, Z, p.I, p.J, stream)) != GBR_OK) return r;
+    return GBR_OK;
+}
+
+// ------------------------------------------------------------ dZ and dbias
+// One CTA per 32 columns: 8 rows of threads walk down the rows.
+template <int ACT>
+__global__ void __launch_bounds__(256) dz_kernel(const LinearGradArgs a) {
+    __shared__ float part[8][32];
+    ptx::griddep_wait();
+    const int n = int(blockIdx.x) * 32 + int(threadIdx.x) % 32;
+    float sum = 0.f;
+    for (int m = int(threadIdx.x) / 32; n < a.N && m < a.M; m += 8) {
+        float d = __bfloat162float(static_cast<const bf16*>(a.dC.p)[m * a.dC.ld + n]);
+        bool keep = true;
+        if (a.drop.threshold != 0) {
+            const uint4 bits = dropout_bits(a.drop, uint32_t(m), uint32_t(n / 8));
+            keep = dropout_keep(a.drop, bits, n % 8);
+            d *= a.drop.scale;
+        }
+        if (ACT != kActNone)
+            d *= act_slope<ACT>(__bfloat162float(static_cast<const bf16*>(a.Z.p)[m * a.Z.ld + n]));
+        if (!keep) d = 0.f;
+        if (a.dZ) static_cast<bf16*>(a.dZ.w())[m * a.dZ.ld + n] = __float2bfloat16_rn(d);
+        sum += d;
+    }
+    part[threadIdx.x / 32][threadIdx.x % 32] = sum;
+    __syncthreads();
+    if (threadIdx.x < 32 && n < a.N && a.dbias != nullptr) {
+        float t = 0.f;
+        for (int r = 0; r < 8; ++r) t += part[r][threadIdx.x];
+        a.dbias[n] = t;
+    }
+}
+
+void* dz_kernel_ptr(int act) {
+    switch (act) {
+        case kActRelu: return reinterpret_cast<void*>(&dz_kernel<kActRelu>);
+        case kActGelu: return reinterpret_cast<void*>(&dz_kernel<kActGelu>);
+        case kActGeluTanh: return reinterpret_cast<void*>(&dz_kernel<kActGeluTanh>);
+        case kActSilu: return reinterpret_cast<void*>(&dz_kernel<kActSilu>);
+        default: return reinterpret_cast<void*>(&dz_kernel<kActNone>);
+    }
+}
+
+}  // namespace
+
+int launch_linear(const LinearArgs& a, const LibCtx& c, cudaStream_t stream) {
+    Product p = {};
+    p.A = a.A, p.B = a.B;
+    p.a_mn = false, p.b_mn = true;
+    p.I = a.M, p.J = a.N, p.Kc = a.K;
+    p.C = a.C, p.Z = a.Z, p.R = a.R;
+    p.bias = a.bias;
+    p.drop = a.drop;
+    p.kernel = linear_pair_forward_kernel(a.act);
+    return run_product(p, c, stream);
+}
+
+int launch_linear_dz(const LinearGradArgs& a, const LibCtx&, cudaStream_t stream) {
+    LinearGradArgs arg = a;
+    void* args[] = {&arg};
+    const cudaError_t e = launch_plain(dz_kernel_ptr(a.act), dim3(unsigned(cdiv(a.N, 32))), 256, 0, 1, args, stream);
+    if (e != cudaSuccess) return report_cuda(e, "launching the gradient's dZ");
+    count_launch();
+    return GBR_OK;
+}
+
+int launch_linear_da(Mat dZ, Mat B, Mat dA, int32_t M, int32_t N, int32_t K, const LibCtx& c,
+                     cudaStream_t stream) {
+    Product p = {};
+    p.A = dZ, p.B = B;
+    p.a_mn = false, p.b_mn = false;
+    p.I = M, p.J = K, p.Kc = N;
+    p.C = dA;
+    p.kernel = linear_pair_da_kernel();
+    return run_product(p, c, stream);
+}
+
+int launch_linear_db(Mat A, Mat dZ, Mat dB, int32_t M, int32_t N, int32_t K, const LibCtx& c,
+                     cudaStream_t stream) {
+    Product p = {};
+    p.A = A, p.B = dZ;
+    p.a_mn = true, p.b_mn = true;
+    p.I = K, p.J = N, p.Kc = M;
+    p.C = dB;
+    p.kernel = linear_pair_db_kernel();
+    return run_product(p, c, stream);
+}
+
+}  // namespace gbr

@@ -1,0 +1,381 @@
+// linear_pair.cuh -- the fused linear layer and its gradients' products on
+// CTA pairs: the persistent warp-specialised tcgen05 pipeline of
+// gemm_umma.cuh (256 x 256 tiles, cta_group::2, a 3-slot ring of 128-K stages,
+// two accumulators in Tensor Memory) for operands of either orientation and
+// with another epilogue.
+//
+//   product            first operand        second operand
+//   C  = A B           A  K-major           B  MN-major
+//   dA = dZ B^T        dZ K-major           B  K-major
+//   dB = A^T dZ        A  MN-major          dZ MN-major
+//
+// A K-major operand is loaded as one box of 128 rows x 64 k; an MN-major one,
+// whose rows run along k, as two panels of 64 k rows x 64 columns: 16 KiB a
+// CTA and 64-k slice either way, and the matrix descriptors and the
+// instruction descriptor's transpose bits say which.  No operand is copied.
+//
+// Epilogue, per warp 32 rows x 64 columns at a time:
+//   tcgen05.ld -> + bias -> (Z: round, stage, TMA store) -> activation ->
+//   dropout -> + residual -> round, stage, TMA store
+// The residual's 4 KiB arrive by TMA in the very staging slot that the result
+// then overwrites, one chunk ahead; two slots a warp.
+#pragma once
+#include "gemm_umma.cuh"
+#include "operators.h"
+
+namespace gbr {
+namespace linear {
+
+using umma::kAccCols;
+using umma::kEpiBufBytes;
+using umma::kRegsWG0;
+using umma::kRegsWG1;
+using umma::kThreads;
+using umma::kTmemCols;
+using umma::sw128_desc;
+
+constexpr uint32_t kTile = 256;                        // rows and columns of a tile
+constexpr uint32_t kStages = 3, kSlices = 2;           // 64-k slices per ring stage
+constexpr uint32_t kSliceBytes = 128 * 128;            // one operand, one CTA, 64 k
+constexpr uint32_t kStageBytes = 2 * kSlices * kSliceBytes;
+constexpr uint32_t kPanelBytes = 64 * 128;
+constexpr uint32_t kBiasBytes = 4 * 64 * 4;            // 64 columns for each epilogue warp
+constexpr uint32_t kBarBytes = 256;
+constexpr size_t kSmemBytes = 1024 + kStages * kStageBytes + kUmmaEpiBytes + kBarBytes + kBiasBytes;
+
+struct PairParams {
+    CUtensorMap mapA, mapB, mapC, mapZ, mapR;
+    const float* bias;
+    int32_t M, N;                                      // of the output
+    int32_t m_tiles, n_tiles, num_tiles, num_kb, group_m;
+    uint32_t has_z, has_r;
+    Dropout drop;
+    KernelCtl ctl;
+};
+
+template <bool A_MN, bool B_MN>
+__host__ __device__ constexpr uint32_t pair_idesc() {
+    return (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(A_MN) << 15) | (uint32_t(B_MN) << 16) |
+           ((kTile >> 3) << 17) | ((kTile >> 4) << 24);
+}
+
+template <bool MN>
+__device__ __forceinline__ uint64_t operand_desc(uint32_t slice, uint32_t k) {
+    return MN ? sw128_desc(slice + k * 16u * 128u, kPanelBytes, 1024)
+              : sw128_desc(slice + k * 32u, 16, 1024);
+}
+
+// One 64-k slice of an operand: this CTA's 128 rows (or columns) from `r0`.
+template <bool MN>
+__device__ __forceinline__ void load_slice(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                           int32_t r0, int32_t k0) {
+    if (MN) {
+        ptx::tma_load_2d_pair(dst, map, bar, r0, k0);
+        ptx::tma_load_2d_pair(dst + kPanelBytes, map, bar, r0 + 64, k0);
+    } else {
+        ptx::tma_load_2d_pair(dst, map, bar, k0, r0);
+    }
+}
+
+template <bool A_MN, bool B_MN, int ACT, bool PLAIN>
+__global__ void __launch_bounds__(kThreads, 1)
+    linear_pair_kernel(const __grid_constant__ PairParams P) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* ring = align_1024(smem_raw);
+    uint8_t* epi = ring + kStages * kStageBytes;
+    uint64_t* full = reinterpret_cast<uint64_t*>(epi + kUmmaEpiBytes);
+    uint64_t* empty = full + kStages;
+    uint64_t* acc_full = empty + kStages;
+    uint64_t* acc_empty = acc_full + 2;
+    uint64_t* drain = acc_empty + 2;
+    uint64_t* res_full = drain + 1;                    // [4 warps][2 slots]
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(res_full + 8);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+    uint32_t* issued_word = tmem_holder + 2;
+    float* bias_sm = reinterpret_cast<float*>(epi + kUmmaEpiBytes + kBarBytes);
+
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u;
+    const uint32_t rank = ptx::cluster_ctarank();
+    const uint32_t unit = blockIdx.x / 2, units = gridDim.x / 2;
+
+    if (threadIdx.x == 0) {
+        for (uint32_t i = 0; i < kStages; ++i) {
+            ptx::mbar_init(ptx::smem_addr(full + i), 1);
+            ptx::mbar_init(ptx::smem_addr(empty + i), 1);
+        }
+        for (uint32_t a = 0; a < 2; ++a) {
+            ptx::mbar_init(ptx::smem_addr(acc_full + a), 1);
+            ptx::mbar_init(ptx::smem_addr(acc_empty + a), 8);
+        }
+        ptx::mbar_init(ptx::smem_addr(drain), 1);
+        for (uint32_t i = 0; i < 8; ++i) ptx::mbar_init(ptx::smem_addr(res_full + i), 1);
+        *abort_flag = 0;
+        *issued_word = 0;
+        ptx::fence_barrier_init();
+    } else if (threadIdx.x == 32) {
+        ptx::prefetch_tensormap(&P.mapA);
+        ptx::prefetch_tensormap(&P.mapB);
+        ptx::prefetch_tensormap(&P.mapC);
+    }
+    if (warp == 2) {
+        ptx::tmem_alloc_pair(ptx::smem_addr(tmem_holder), kTmemCols);
+        ptx::tmem_relinquish_alloc_permit_pair();
+    }
+    ptx::tc_fence_before_sync();
+    ptx::cluster_sync_all();
+    ptx::tc_fence_after_sync();
+    const uint32_t tmem_base = *tmem_holder;
+    ptx::griddep_wait();
+    uint32_t issued = 0;
+
+    if (warp < 4) {
+        ptx::setmaxnreg_dec<kRegsWG0>();
+        if (warp == 0 && lane == 0) {
+            // ---------------------------------------------------- TMA producer
+            const uint32_t ring_base = ptx::smem_addr(ring);
+            uint32_t it = 0;
+            bool ok = true;
+            for (uint32_t t = unit; ok && t < uint32_t(P.num_tiles); t += units) {
+                uint32_t mt, nt;
+                raster_tile(t, P.m_tiles, P.n_tiles, P.group_m, mt, nt);
+                const int32_t a0 = int32_t(mt * kTile + rank * 128), b0 = int32_t(nt * kTile + rank * 128);
+                for (int32_t kb = 0; kb < P.num_kb; ++kb, ++it) {
+                    const uint32_t slot = it % kStages, ph = (it / kStages) & 1u;
+                    if (!mbar_wait<true>(ptx::smem_addr(empty + slot), ph ^ 1u, P.ctl, abort_flag,
+                                         kSiteProducerEmpty, it)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t fb_local = ptx::smem_addr(full + slot);
+                    const uint32_t fb = ptx::mapa_shared(fb_local, 0);
+                    if (rank == 0) ptx::mbar_arrive_expect_tx(fb_local, 2 * kStageBytes);
+                    const uint32_t stage = ring_base + slot * kStageBytes;
+#pragma unroll
+                    for (uint32_t h = 0; h < kSlices; ++h) {
+                        const int32_t k0 = (kb * int32_t(kSlices) + int32_t(h)) * 64;
+                        load_slice<A_MN>(stage + h * kSliceBytes, &P.mapA, fb, a0, k0);
+                        load_slice<B_MN>(stage + (kSlices + h) * kSliceBytes, &P.mapB, fb, b0, k0);
+                    }
+                }
+            }
+            ptx::griddep_launch_dependents();
+            issued = it;
+            *issued_word = it;
+        } else if (warp == 1 && lane == 0 && rank == 0) {
+            // ---------------------------------------------------- MMA issuer
+            const uint32_t ring_base = ptx::smem_addr(ring);
+            constexpr uint32_t idesc = pair_idesc<A_MN, B_MN>();
+            uint32_t it = 0, tl = 0;
+            bool ok = true;
+            for (uint32_t t = unit; ok && t < uint32_t(P.num_tiles); t += units, ++tl) {
+                const uint32_t a = tl & 1u, aph = (tl >> 1) & 1u;
+                if (!mbar_wait<true>(ptx::smem_addr(acc_empty + a), aph ^ 1u, P.ctl, abort_flag,
+                                     kSiteMmaAccEmpty, tl))
+                    break;
+                ptx::tc_fence_after_sync();
+                const uint32_t d_tmem = tmem_base + a * kAccCols;
+                for (int32_t kb = 0; kb < P.num_kb; ++kb, ++it) {
+                    const uint32_t slot = it % kStages, ph = (it / kStages) & 1u;
+                    if (!mbar_wait<true>(ptx::smem_addr(full + slot), ph, P.ctl, abort_flag,
+                                         kSiteMmaFull, it)) {
+                        ok = false;
+                        break;
+                    }
+                    ptx::tc_fence_after_sync();
+                    const uint32_t stage = ring_base + slot * kStageBytes;
+#pragma unroll
+                    for (uint32_t h = 0; h < kSlices; ++h)
+#pragma unroll
+                        for (uint32_t k = 0; k < 4; ++k)
+                            ptx::mma_f16_pair(d_tmem, operand_desc<A_MN>(stage + h * kSliceBytes, k),
+                                              operand_desc<B_MN>(stage + (kSlices + h) * kSliceBytes, k),
+                                              idesc, (kb != 0 || h != 0 || k != 0) ? 1u : 0u);
+                    ptx::mma_commit_pair_multicast(ptx::smem_addr(empty + slot), 0x3);
+                }
+                if (!ok) break;
+                if (P.num_kb > 0) {
+                    ptx::mma_commit_pair_multicast(ptx::smem_addr(acc_full + a), 0x3);
+                } else {
+                    ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_addr(acc_full + a), 0));
+                    ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_addr(acc_full + a), 1));
+                }
+            }
+            ptx::mma_commit_pair_multicast(ptx::smem_addr(drain), 0x1);
+            mbar_wait_drain(ptx::smem_addr(drain), 0, P.ctl.timeout_ns);
+        }
+    } else {
+        ptx::setmaxnreg_inc<kRegsWG1>();
+        // -------------------------------------------------------- epilogue
+        const uint32_t q = warp & 3u;                  // TMEM lane quarter / row block
+        const uint32_t slot0 = ptx::smem_addr(epi) + q * 2u * kEpiBufBytes;
+        const uint32_t row_off = lane * 128u, swz = lane & 7u;
+        float* bias_w = bias_sm + q * 64u;
+        const bool has_z = !PLAIN && P.has_z != 0, has_r = !PLAIN && P.has_r != 0;
+        uint32_t use = 0;                              // staging-slot uses so far
+        uint32_t res_issued = 0, res_taken = 0, res_phase = 0, res_slot = 0;
+        const bool zero_acc = P.num_kb == 0;
+        bool ok = true;
+        uint32_t tl = 0;
+        for (uint32_t t = unit; ok && t < uint32_t(P.num_tiles); t += units, ++tl) {
+            uint32_t mt, nt;
+            raster_tile(t, P.m_tiles, P.n_tiles, P.group_m, mt, nt);
+            const int32_t row0 = int32_t(mt * kTile + rank * 128u + q * 32u), n0 = int32_t(nt * kTile);
+            const int32_t chunks = row0 < P.M ? min(4, (P.N - n0 + 63) / 64) : 0;
+            const uint32_t a = tl & 1u, aph = (tl >> 1) & 1u;
+            const uint32_t ae = ptx::smem_addr(acc_empty + a);
+            // The first chunk's residual and bias travel while the accumulator is not ready.
+            auto fetch_residual = [&](int32_t c, uint32_t next_use) {
+                res_slot = next_use & 1u;
+                if (lane == 0) {
+                    // The slot's last store (use next_use - 2) has read it.
+                    if (has_z) ptx::bulk_wait_group_read<0>();
+                    else ptx::bulk_wait_group_read<1>();
+                    const uint32_t bar = ptx::smem_addr(res_full + q * 2u + res_slot);
+                    ptx::mbar_arrive_expect_tx(bar, kEpiBufBytes);
+                    ptx::tma_load_2d(slot0 + res_slot * kEpiBufBytes, &P.mapR, bar, n0 + c * 64, row0);
+                }
+                ++res_issued;
+            };
+            float2 bnext = make_float2(0.f, 0.f);
+            auto fetch_bias = [&](int32_t c) {
+                const int32_t n = n0 + c * 64 + int32_t(lane) * 2;
+                bnext = make_float2(0.f, 0.f);
+                if (P.bias != nullptr) {
+                    if (n < P.N) bnext.x = __ldg(P.bias + n);
+                    if (n + 1 < P.N) bnext.y = __ldg(P.bias + n + 1);
+                }
+            };
+            if (!PLAIN && chunks > 0) {
+                if (has_r) fetch_residual(0, use + (has_z ? 1u : 0u));
+                fetch_bias(0);
+            }
+            if (!mbar_wait_warp<true>(ptx::smem_addr(acc_full + a), aph, P.ctl, abort_flag,
+                                      kSiteEpiAccFull, tl))
+                break;
+            ptx::tc_fence_after_sync();
+            if (chunks == 0) umma::acc_release<2>(ae, lane);
+            for (int32_t c = 0; c < chunks; ++c) {
+                const uint32_t taddr = tmem_base + ((q * 32u) << 16) + a * kAccCols + uint32_t(c) * 64u;
+                uint32_t r0[32], r1[32];
+                ptx::tmem_ld_32x32b_x32(taddr, r0);
+                ptx::tmem_ld_32x32b_x32(taddr + 32, r1);
+                if (!PLAIN) {
+                    __syncwarp();                      // the previous chunk's bias has been read
+                    reinterpret_cast<float2*>(bias_w)[lane] = bnext;
+                    __syncwarp();
+                    if (c + 1 < chunks) fetch_bias(c + 1);
+                }
+                ptx::tmem_ld_wait();
+                if (c + 1 == chunks) umma::acc_release<2>(ae, lane);
+                float z[64];
+#pragma unroll
+                for (int j = 0; j < 64; ++j) {
+                    z[j] = __uint_as_float(j < 32 ? r0[j] : r1[j - 32]);
+                    if (zero_acc) z[j] = 0.f;
+                }
+                if (!PLAIN) {
+#pragma unroll
+                    for (int j4 = 0; j4 < 16; ++j4) {
+                        const float4 b = reinterpret_cast<const float4*>(bias_w)[j4];
+                        z[4 * j4] += b.x;
+                        z[4 * j4 + 1] += b.y;
+                        z[4 * j4 + 2] += b.z;
+                        z[4 * j4 + 3] += b.w;
+                    }
+                }
+                auto stage_and_store = [&](const CUtensorMap* map) {
+                    const uint32_t buf = slot0 + (use & 1u) * kEpiBufBytes;
+#pragma unroll
+                    for (uint32_t j = 0; j < 8; ++j) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (uint32_t u = 0; u < 4; ++u) {
+                            const __nv_bfloat162 v = __floats2bfloat162_rn(z[8 * j + 2 * u], z[8 * j + 2 * u + 1]);
+                            w[u] = *reinterpret_cast<const uint32_t*>(&v);
+                        }
+                        ptx::st_shared_v4(buf + row_off + ((j ^ swz) << 4), w[0], w[1], w[2], w[3]);
+                    }
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        ptx::tma_store_2d(map, buf, n0 + c * 64, row0);
+                        ptx::bulk_commit_group();
+                    }
+                    ++use;
+                };
+                if (has_z) {
+                    if (lane == 0) ptx::bulk_wait_group_read<1>();
+                    __syncwarp();
+                    stage_and_store(&P.mapZ);
+                }
+                if (!PLAIN) {
+#pragma unroll
+                    for (int j = 0; j < 64; ++j) z[j] = act_value<ACT>(z[j]);
+                }
+                if (!PLAIN && P.drop.threshold != 0) {
+#pragma unroll
+                    for (int g = 0; g < 8; ++g) {
+                        const uint4 bits = dropout_bits(P.drop, uint32_t(row0) + lane,
+                                                        uint32_t(n0 + c * 64) / 8u + uint32_t(g));
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            z[8 * g + i] = dropout_keep(P.drop, bits, i) ? z[8 * g + i] * P.drop.scale : 0.f;
+                    }
+                }
+                if (has_r) {
+                    const uint32_t slot = use & 1u;
+                    if (!mbar_wait_warp(ptx::smem_addr(res_full + q * 2u + slot), (res_phase >> slot) & 1u,
+                                        P.ctl, abort_flag, kSiteEpiResidual, tl)) {
+                        ok = false;
+                        break;
+                    }
+                    res_phase ^= 1u << slot;
+                    ++res_taken;
+                    const uint32_t buf = slot0 + slot * kEpiBufBytes;
+#pragma unroll
+                    for (uint32_t j = 0; j < 8; ++j) {
+                        const uint4 v = ptx::ld_shared_v4(buf + row_off + ((j ^ swz) << 4));
+                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (uint32_t u = 0; u < 4; ++u) {
+                            z[8 * j + 2 * u] += __uint_as_float(w[u] << 16);
+                            z[8 * j + 2 * u + 1] += __uint_as_float(w[u] & 0xFFFF0000u);
+                        }
+                    }
+                } else {
+                    if (lane == 0) ptx::bulk_wait_group_read<1>();
+                    __syncwarp();
+                }
+                stage_and_store(&P.mapC);
+                if (has_r && c + 1 < chunks) fetch_residual(c + 1, use + (has_z ? 1u : 0u));
+            }
+        }
+        if (lane == 0) {
+            // After an abort a residual load may still be in flight.
+            if (res_issued != res_taken)
+                mbar_wait_drain(ptx::smem_addr(res_full + q * 2u + res_slot), (res_phase >> res_slot) & 1u,
+                                P.ctl.timeout_ns);
+            ptx::bulk_wait_group<0>();
+        }
+    }
+
+    __syncwarp();
+    ptx::tc_fence_before_sync();
+    ptx::cluster_sync_all();
+    if (warp == 0 && lane == 0 && rank == 0) {
+        const uint32_t flag = ptx::smem_addr(const_cast<int*>(abort_flag));
+        const bool aborted = *abort_flag != 0 || ptx::ld_shared_cluster_u32(ptx::mapa_shared(flag, 1)) != 0;
+        const uint32_t peer = ptx::ld_shared_cluster_u32(ptx::mapa_shared(ptx::smem_addr(issued_word), 1));
+        if (aborted)
+            umma::drain_ring<2>(full, kStages, issued, peer, kStageBytes, FaultInjection{0u, 0, 0}, unit,
+                                P.ctl.timeout_ns);
+    }
+    ptx::cluster_sync_all();
+    if (warp == 2) {
+        ptx::tc_fence_after_sync();
+        ptx::tmem_dealloc_pair(tmem_base, kTmemCols);
+    }
+}
+
+}  // namespace linear
+}  // namespace gbr

@@ -70,33 +70,16 @@ int check_sizes(const char* fn, int64_t M, int64_t N, int64_t K) {
     return GBR_OK;
 }
 
-// Scratch of one call, from the device's pool, in stream order.
-class Scratch {
-public:
-    Scratch(const LibCtx& c, cudaStream_t st) : c_(c), st_(st) {}
-    ~Scratch() {
-        if (p_ != nullptr) cudaFreeAsync(p_, st_);
-    }
-    Scratch(const Scratch&) = delete;
-    Scratch& operator=(const Scratch&) = delete;
-    int take(size_t bytes, const char* what) {
-        if (bytes == 0) return GBR_OK;
-        const cudaError_t e = cudaMallocFromPoolAsync(&p_, bytes, c_.pool, st_);
-        if (e != cudaSuccess) {
-            p_ = nullptr;
-            return report_cuda(e, what);
-        }
-        return GBR_OK;
-    }
-    void* get() const { return p_; }
-
-private:
-    const LibCtx& c_;
-    cudaStream_t st_;
-    void* p_ = nullptr;
-};
-
 }  // namespace
+
+int Scratch::take(size_t bytes, const char* what, void** out) {
+    if (n_ >= int(sizeof(p_) / sizeof(p_[0]))) return report_errorf(GBR_ERR_CUDA, "%s: too many blocks", what);
+    const cudaError_t e = cudaMallocFromPoolAsync(&p_[n_], bytes, c_.pool, st_);
+    if (e != cudaSuccess) return report_cuda(e, what);
+    *out = p_[n_++];
+    return GBR_OK;
+}
+
 }  // namespace gbr
 
 using namespace gbr;
@@ -162,10 +145,7 @@ int gemm_bias_act(const void* A, int64_t lda, const void* B, int64_t ldb, const 
     a.bias = bias;
     a.M = int32_t(M), a.N = int32_t(N), a.K = int32_t(K);
     a.act = act;
-    const cudaError_t e = launch_linear(a, c, reinterpret_cast<cudaStream_t>(stream));
-    if (e != cudaSuccess) return report_cuda(e, "launching gemm_bias_act");
-    count_launch();
-    return GBR_OK;
+    return launch_linear(a, c, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int gemm_bias_act_backward(const void* dC, int64_t lddc, const void* A, int64_t lda, const void* B,
@@ -197,7 +177,6 @@ int gemm_bias_act_backward(const void* dC, int64_t lddc, const void* A, int64_t 
     LibCtx c;
     if ((r = lib_ctx(&c)) != GBR_OK) return r;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e;
     // dZ is dC itself unless dropout or an activation lies between them.
     const bool plain = act == kActNone && g.drop.threshold == 0;
     const bool products = want_da || want_db;
@@ -210,24 +189,14 @@ int gemm_bias_act_backward(const void* dC, int64_t lddc, const void* A, int64_t 
     Mat dz = {dC, lddc};
     if (!plain && products && some) {
         const int64_t ld = (N + 7) / 8 * 8;
-        if ((r = ws.take(size_t(M) * size_t(ld) * 2, "cudaMallocFromPoolAsync(dZ)")) != GBR_OK) return r;
-        dz = {ws.get(), ld};
+        void* q;
+        if ((r = ws.take(size_t(M) * size_t(ld) * 2, "cudaMallocFromPoolAsync(dZ)", &q)) != GBR_OK) return r;
+        dz = {q, ld};
         g.dZ = dz;
     }
-    if (want_bias || g.dZ) {
-        if ((e = launch_linear_dz(g, c, st)) != cudaSuccess) return report_cuda(e, "launching the gradient's dZ");
-        count_launch();
-    }
-    if (want_da) {
-        if ((e = launch_linear_da(dz, {B, ldb}, {dA, ldda}, g.M, g.N, int32_t(K), c, st)) != cudaSuccess)
-            return report_cuda(e, "launching dA");
-        count_launch();
-    }
-    if (want_db) {
-        if ((e = launch_linear_db({A, lda}, dz, {dB, lddb}, g.M, g.N, int32_t(K), c, st)) != cudaSuccess)
-            return report_cuda(e, "launching dB");
-        count_launch();
-    }
+    if ((want_bias || g.dZ) && (r = launch_linear_dz(g, c, st)) != GBR_OK) return r;
+    if (want_da && (r = launch_linear_da(dz, {B, ldb}, {dA, ldda}, g.M, g.N, int32_t(K), c, st)) != GBR_OK) return r;
+    if (want_db && (r = launch_linear_db({A, lda}, dz, {dB, lddb}, g.M, g.N, int32_t(K), c, st)) != GBR_OK) return r;
     return GBR_OK;
 }
 
@@ -282,8 +251,9 @@ int moe_layer(const void* X, const float* Wr, const void* W1, const float* b1, c
     auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
     const size_t route = up(size_t(T * top_k) * 8), own = moe_scratch_bytes(a, c);
     Scratch ws(c, st);
-    if ((r = ws.take(2 * route + own, "cudaMallocFromPoolAsync(expert layer)")) != GBR_OK) return r;
-    uint8_t* base = static_cast<uint8_t*>(ws.get());
+    void* q;
+    if ((r = ws.take(2 * route + own, "cudaMallocFromPoolAsync(expert layer)", &q)) != GBR_OK) return r;
+    uint8_t* base = static_cast<uint8_t*>(q);
     a.ids = expert_ids ? expert_ids : reinterpret_cast<int64_t*>(base);
     a.weights = expert_weights ? expert_weights : reinterpret_cast<float*>(base + route);
     const cudaError_t e = launch_moe(a, base + 2 * route, c, st);

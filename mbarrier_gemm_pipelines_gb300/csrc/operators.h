@@ -15,6 +15,26 @@ struct Mat {
     __host__ __device__ explicit operator bool() const { return p != nullptr; }
 };
 
+// Scratch of one call, from the device's pool in stream order: given back on
+// the stream when the object goes.
+class Scratch {
+public:
+    Scratch(const LibCtx& c, cudaStream_t st) : c_(c), st_(st) {}
+    ~Scratch() {
+        for (int i = 0; i < n_; ++i) cudaFreeAsync(p_[i], st_);
+    }
+    Scratch(const Scratch&) = delete;
+    Scratch& operator=(const Scratch&) = delete;
+    int take(size_t bytes, const char* what, void** out);
+
+private:
+    const LibCtx& c_;
+    cudaStream_t st_;
+    void* p_[8] = {};
+    int n_ = 0;
+};
+
+// The launches below count themselves and return a gbr_status.
 // ------------------------------------------------------------ dropout_add
 struct DropoutAddArgs {
     const void* X;
@@ -36,7 +56,7 @@ struct LinearArgs {
     int act;
     Dropout drop;
 };
-cudaError_t launch_linear(const LinearArgs& a, const LibCtx& c, cudaStream_t stream);
+int launch_linear(const LinearArgs& a, const LibCtx& c, cudaStream_t stream);
 
 // dZ = drop(dC) * act'(Z) (bf16) and dbias = sum over rows of dZ (fp32).
 struct LinearGradArgs {
@@ -46,14 +66,12 @@ struct LinearGradArgs {
     int act;
     Dropout drop;
 };
-cudaError_t launch_linear_dz(const LinearGradArgs& a, const LibCtx& c, cudaStream_t stream);
+int launch_linear_dz(const LinearGradArgs& a, const LibCtx& c, cudaStream_t stream);
 
 // The gradients' products: dA[M, K] = dZ[M, N] B[K, N]^T and
 // dB[K, N] = A[M, K]^T dZ[M, N].
-cudaError_t launch_linear_da(Mat dZ, Mat B, Mat dA, int32_t M, int32_t N, int32_t K,
-                             const LibCtx& c, cudaStream_t stream);
-cudaError_t launch_linear_db(Mat A, Mat dZ, Mat dB, int32_t M, int32_t N, int32_t K,
-                             const LibCtx& c, cudaStream_t stream);
+int launch_linear_da(Mat dZ, Mat B, Mat dA, int32_t M, int32_t N, int32_t K, const LibCtx& c, cudaStream_t stream);
+int launch_linear_db(Mat A, Mat dZ, Mat dB, int32_t M, int32_t N, int32_t K, const LibCtx& c, cudaStream_t stream);
 
 // ------------------------------------------------------------ expert layer
 constexpr int kMoeMaxTokens = 64, kMoeMaxExperts = 256, kMoeMaxTopK = 8;

@@ -74,7 +74,7 @@ def example(steps=20, T=512, D=1024, F=4096):
     for step in range(steps):
         e = block.forward(x, step).float() - target.float()
         losses.append(e.square().mean())
-        block.sgd(block.backward((e * (2.0 / T)).bfloat16()), lr=0.02)
+        block.sgd(block.backward((e * (2.0 / T)).bfloat16()), lr=1e-3)
     experts = ExpertFeedForward(D, F, experts=8)
     y = experts.forward(x[:1])
     gbr.check_device()
