@@ -21,8 +21,6 @@ OK, ERR_INVALID, ERR_UNSUPPORTED, ERR_ALIGN, ERR_SMEM, ERR_CUDA, ERR_TIMEOUT = r
 STATUS_NAMES = {0: "GBR_OK", 1: "GBR_ERR_INVALID", 2: "GBR_ERR_UNSUPPORTED", 3: "GBR_ERR_ALIGN",
                 4: "GBR_ERR_SMEM", 5: "GBR_ERR_CUDA", 6: "GBR_ERR_TIMEOUT"}
 OP_GEMM, OP_COPY = 0, 1
-# gbr_act
-ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 
 # Every function the header declares: name -> (restype, argtypes).
 _vp, _i64, _i32, _u64 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_uint64
@@ -80,6 +78,8 @@ def library_path() -> str:
 def lib():
     """Loads libgbr.so (it must have been built: ``__graft_entry__.build()``)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = _build.LIB_PATH
@@ -368,202 +368,3 @@ def selftest_noalloc_skip_load(A, B, bias, C, stages, cta, item, limit_ns, strea
                                                C.data_ptr(), M, N, K, int(stages), int(cta),
                                                int(item), int(limit_ns), _stream_ptr(stream)))
     return C
-
-
-# --------------------------------------------------- feed-forward operators
-
-def _act_code(act):
-    if act not in ACTS:
-        raise ValueError("act must be one of %s, got %r" % (", ".join(ACTS), act))
-    return ACTS[act]
-
-
-def _u64_arg(v, name):
-    v = int(v)
-    if not 0 <= v < 1 << 64:
-        raise ValueError("%s must be in [0, 2^64)" % name)
-    return v
-
-
-def _rows_tensor(t, name, dtypes, shape=None):
-    """A 2-D CUDA tensor whose rows are contiguous; returns its row stride."""
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("%s must be a torch.Tensor" % name)
-    if not t.is_cuda:
-        raise ValueError("%s must be a CUDA tensor (this library has no CPU path)" % name)
-    if t.dtype not in dtypes:
-        raise TypeError("%s has dtype %s, expected one of %s" % (name, t.dtype, dtypes))
-    if t.dim() != 2:
-        raise ValueError("%s must be 2-D" % name)
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
-    if t.shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError("the rows of %s must be contiguous" % name)
-    return t.stride(0) if t.shape[0] > 1 else max(1, t.shape[1])
-
-
-def _same_device(*named):
-    import torch
-    dev = None
-    for t, name in named:
-        if t is None:
-            continue
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError("%s is on %s, the other tensors on %s" % (name, t.device, dev))
-    if dev is not None and dev.index != torch.cuda.current_device():
-        raise ValueError("the tensors are on %s, the current device is cuda:%d"
-                         % (dev, torch.cuda.current_device()))
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
-
-
-def dropout_add(X, residual=None, p=0.5, seed=0, offset=0, Y=None, stream=None):
-    """Y = residual + dropout(X) for bf16 or fp32 tensors; returns Y (which may
-    be X or residual itself).  The mask depends on (seed, offset) and the
-    position in X seen as [rows, last dimension] alone, so the gradient of X is
-    ``dropout_add(dY, p=p, seed=seed, offset=offset)``.  Tensors with more than
-    two dimensions must be contiguous."""
-    import torch
-    kinds = (torch.bfloat16, torch.float32)
-    if not isinstance(X, torch.Tensor) or X.dtype not in kinds:
-        raise TypeError("X must be a bf16 or fp32 torch.Tensor")
-    if X.dim() == 0:
-        raise ValueError("X must have at least one dimension")
-    if Y is None:
-        Y = torch.empty(X.shape, dtype=X.dtype, device=X.device)
-    views = []
-    for t, name in ((X, "X"), (residual, "residual"), (Y, "Y")):
-        if t is None:
-            views.append((None, 0))
-            continue
-        if not isinstance(t, torch.Tensor) or t.shape != X.shape:
-            raise ValueError("%s must be a tensor of X's shape %s" % (name, list(X.shape)))
-        if t.dim() != 2:
-            if not t.is_contiguous():
-                raise ValueError("%s must be contiguous (or 2-D with contiguous rows)" % name)
-            t = t.view(-1, t.shape[-1]) if t.numel() else t.reshape(0, t.shape[-1])
-        views.append((t, _rows_tensor(t, name, (X.dtype,))))
-    (x, ldx), (r, ldr), (y, ldy) = views
-    _same_device((X, "X"), (residual, "residual"), (Y, "Y"))
-    check(lib().dropout_add(x.data_ptr(), ldx, _ptr(r), ldr, y.data_ptr(), ldy, x.shape[0], x.shape[1],
-                            BF16 if X.dtype == torch.bfloat16 else F32_FFMA, float(p),
-                            _u64_arg(seed, "seed"), _u64_arg(offset, "offset"), _stream_ptr(stream)))
-    return Y
-
-
-def gemm_bias_act(A, B, bias=None, residual=None, act="none", p=0.0, seed=0, offset=0, C=None, Z=None,
-                  return_z=False, stream=None):
-    """C = residual + dropout(act(A @ B + bias)) for bf16 matrices (bias fp32);
-    returns C, or (C, Z) with the pre-activation Z = A @ B + bias (bf16, what
-    gemm_bias_act_backward needs) when return_z is true or Z is given."""
-    import torch
-    bf = (torch.bfloat16,)
-    lda, ldb = _rows_tensor(A, "A", bf), _rows_tensor(B, "B", bf)
-    M, K = A.shape
-    if B.shape[0] != K:
-        raise ValueError("shape mismatch: A %s, B %s" % (list(A.shape), list(B.shape)))
-    N = B.shape[1]
-    if bias is not None:
-        _cuda_tensor(bias, "bias", (torch.float32,))
-        if tuple(bias.shape) != (N,):
-            raise ValueError("bias must be [%d]" % N)
-    if C is None:
-        C = torch.empty((M, N), dtype=torch.bfloat16, device=A.device)
-    if Z is None and return_z:
-        Z = torch.empty((M, N), dtype=torch.bfloat16, device=A.device)
-    ldr, ldc, ldz = (0 if t is None else _rows_tensor(t, n, bf, (M, N))
-                     for t, n in ((residual, "residual"), (C, "C"), (Z, "Z")))
-    _same_device((A, "A"), (B, "B"), (bias, "bias"), (residual, "residual"), (C, "C"), (Z, "Z"))
-    check(lib().gemm_bias_act(A.data_ptr(), lda, B.data_ptr(), ldb, _ptr(bias), _ptr(residual), ldr,
-                              C.data_ptr(), ldc, _ptr(Z), ldz, M, N, K, BF16, _act_code(act), float(p),
-                              _u64_arg(seed, "seed"), _u64_arg(offset, "offset"), _stream_ptr(stream)))
-    return C if Z is None else (C, Z)
-
-
-def gemm_bias_act_backward(dC, A, B, Z=None, act="none", p=0.0, seed=0, offset=0, dA=None, dB=None,
-                           dbias=None, needs=(True, True, True), stream=None):
-    """Gradients (dA, dB, dbias) of gemm_bias_act for dC, with the Z, p, seed and
-    offset of the forward call; the residual's gradient is dC itself.  `needs`
-    says which of the three are wanted (None is returned for the others)."""
-    import torch
-    bf = (torch.bfloat16,)
-    code = _act_code(act)
-    lddc, lda, ldb = (_rows_tensor(t, n, bf) for t, n in ((dC, "dC"), (A, "A"), (B, "B")))
-    M, K = A.shape
-    N = B.shape[1]
-    if B.shape[0] != K or tuple(dC.shape) != (M, N):
-        raise ValueError("shape mismatch: dC %s, A %s, B %s" % (list(dC.shape), list(A.shape), list(B.shape)))
-    if code != 0 and Z is None:
-        raise ValueError("Z (the pre-activation of the forward call) is needed for act=%r" % act)
-    ldz = 0 if Z is None else _rows_tensor(Z, "Z", bf, (M, N))
-    want_a, want_b, want_bias = (bool(w) for w in needs)
-    if dA is None and want_a:
-        dA = torch.empty((M, K), dtype=torch.bfloat16, device=dC.device)
-    if dB is None and want_b:
-        dB = torch.empty((K, N), dtype=torch.bfloat16, device=dC.device)
-    if dbias is None and want_bias:
-        dbias = torch.empty((N,), dtype=torch.float32, device=dC.device)
-    if not want_a:
-        dA = None
-    if not want_b:
-        dB = None
-    if not want_bias:
-        dbias = None
-    ldda = 0 if dA is None else _rows_tensor(dA, "dA", bf, (M, K))
-    lddb = 0 if dB is None else _rows_tensor(dB, "dB", bf, (K, N))
-    if dbias is not None:
-        _cuda_tensor(dbias, "dbias", (torch.float32,))
-        if tuple(dbias.shape) != (N,):
-            raise ValueError("dbias must be [%d]" % N)
-    _same_device((dC, "dC"), (A, "A"), (B, "B"), (Z, "Z"), (dA, "dA"), (dB, "dB"), (dbias, "dbias"))
-    check(lib().gemm_bias_act_backward(dC.data_ptr(), lddc, A.data_ptr(), lda, B.data_ptr(), ldb, _ptr(Z),
-                                       ldz, _ptr(dA), ldda, _ptr(dB), lddb, _ptr(dbias), M, N, K, BF16,
-                                       code, float(p), _u64_arg(seed, "seed"), _u64_arg(offset, "offset"),
-                                       _stream_ptr(stream)))
-    return dA, dB, dbias
-
-
-def moe_layer(X, Wr, W1, b1, W2, b2, top_k=2, act="relu", gated=False, Y=None,
-              return_routing=False, stream=None):
-    """A whole mixture-of-experts layer for up to 64 tokens: router (X @ Wr, the
-    top_k largest, softmax over them), the chosen experts' two products and
-    their weighted sum.  X [T, D], W1 [E, D, F] (gated: [E, D, 2F], gate columns
-    first), W2 [E, F, D] bf16; Wr [D, E], b1 [E, F or 2F], b2 [E, D] fp32 (b1
-    and b2 may be None).  Returns Y [T, D] bf16, or (Y, expert_ids int64
-    [T, top_k], expert_weights fp32 [T, top_k])."""
-    import torch
-    bf, f32 = (torch.bfloat16,), (torch.float32,)
-    for t, n, d in ((X, "X", bf), (Wr, "Wr", f32), (W1, "W1", bf), (W2, "W2", bf)):
-        _cuda_tensor(t, n, d)
-    if X.dim() != 2 or W1.dim() != 3 or W2.dim() != 3:
-        raise ValueError("X must be 2-D, W1 and W2 3-D")
-    T, D = X.shape
-    E, F = W2.shape[0], W2.shape[1]
-    F1 = 2 * F if gated else F
-    for t, n, want in ((Wr, "Wr", (D, E)), (W1, "W1", (E, D, F1)), (W2, "W2", (E, F, D)), (b1, "b1", (E, F1)),
-                       (b2, "b2", (E, D))):
-        if t is None:
-            continue
-        if n in ("b1", "b2"):
-            _cuda_tensor(t, n, f32)
-        if tuple(t.shape) != want:
-            raise ValueError("%s must be %s, got %s" % (n, list(want), list(t.shape)))
-    if Y is None:
-        Y = torch.empty((T, D), dtype=torch.bfloat16, device=X.device)
-    _cuda_tensor(Y, "Y", bf)
-    if Y.shape != X.shape:
-        raise ValueError("Y must be [T, D]")
-    ids = weights = None
-    if return_routing:
-        ids = torch.empty((T, int(top_k)), dtype=torch.int64, device=X.device)
-        weights = torch.empty((T, int(top_k)), dtype=torch.float32, device=X.device)
-    _same_device((X, "X"), (Wr, "Wr"), (W1, "W1"), (b1, "b1"), (W2, "W2"), (b2, "b2"), (Y, "Y"))
-    check(lib().moe_layer(X.data_ptr(), Wr.data_ptr(), W1.data_ptr(), _ptr(b1), W2.data_ptr(), _ptr(b2),
-                          Y.data_ptr(), _ptr(ids), _ptr(weights), T, D, F, E, int(top_k), _act_code(act),
-                          int(bool(gated)), BF16, _stream_ptr(stream)))
-    return (Y, ids, weights) if return_routing else Y

@@ -15,7 +15,8 @@ from __future__ import annotations
 
 import torch
 
-from . import _binding as gbr
+from . import _operators as ops
+from ._binding import check_device
 
 
 def _weights(shape, std, g):
@@ -31,17 +32,17 @@ class FeedForward:
         self._saved = None
 
     def forward(self, x, step=0):
-        h, z = gbr.gemm_bias_act(x, self.W1, self.b1, act=self.act, return_z=True)
-        y = gbr.gemm_bias_act(h, self.W2, self.b2, residual=x, p=self.p, seed=self.seed, offset=step)
+        h, z = ops.gemm_bias_act(x, self.W1, self.b1, act=self.act, return_z=True)
+        y = ops.gemm_bias_act(h, self.W2, self.b2, residual=x, p=self.p, seed=self.seed, offset=step)
         self._saved = x, h, z, step
         return y
 
     def backward(self, dy):
         """Gradients of x and of the parameters for dy, by name."""
         x, h, z, step = self._saved
-        dh, dW2, db2 = gbr.gemm_bias_act_backward(dy, h, self.W2, p=self.p, seed=self.seed, offset=step)
-        dx, dW1, db1 = gbr.gemm_bias_act_backward(dh, x, self.W1, z, act=self.act)
-        gbr.dropout_add(dx, dy, p=0.0, Y=dx)
+        dh, dW2, db2 = ops.gemm_bias_act_backward(dy, h, self.W2, p=self.p, seed=self.seed, offset=step)
+        dx, dW1, db1 = ops.gemm_bias_act_backward(dh, x, self.W1, z, act=self.act)
+        ops.dropout_add(dx, dy, p=0.0, Y=dx)
         return {"x": dx, "W1": dW1, "b1": db1, "W2": dW2, "b2": db2}
 
     def sgd(self, grads, lr):
@@ -60,7 +61,7 @@ class ExpertFeedForward:
         self.b2 = torch.zeros(experts, D, device="cuda")
 
     def forward(self, x):
-        return gbr.moe_layer(x, self.Wr, self.W1, self.b1, self.W2, self.b2, top_k=self.top_k, act=self.act,
+        return ops.moe_layer(x, self.Wr, self.W1, self.b1, self.W2, self.b2, top_k=self.top_k, act=self.act,
                              gated=self.gated)
 
 
@@ -77,7 +78,7 @@ def example(steps=20, T=512, D=1024, F=4096):
         block.sgd(block.backward((e * (2.0 / T)).bfloat16()), lr=1e-3)
     experts = ExpertFeedForward(D, F, experts=8)
     y = experts.forward(x[:1])
-    gbr.check_device()
+    check_device()
     return [float(v) for v in losses], y
 
 
