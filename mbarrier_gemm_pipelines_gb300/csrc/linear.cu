@@ -2,12 +2,14 @@
 // that TMA cannot read are re-pitched, tensor maps, the choice of the kernel
 // and the launches; and the kernel of dZ and dbias.
 #include "linear_pair.cuh"
+#include "linear_tile.cuh"
 
 #include "gbr.h"
 
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstring>
 #include <map>
 #include <mutex>
@@ -18,6 +20,9 @@ namespace gbr {
 void* linear_pair_forward_kernel(int act);
 void* linear_pair_da_kernel();
 void* linear_pair_db_kernel();
+void* linear_tile_forward_kernel(int act);
+void* linear_tile_da_kernel();
+void* linear_tile_db_kernel();
 
 namespace {
 
@@ -114,7 +119,8 @@ struct Product {
     Mat C, Z, R;
     const float* bias;
     Dropout drop;
-    void* kernel;
+    void* pair_kernel;             // linear_pair.cuh
+    void* tile_kernel;             // linear_tile.cuh
 };
 
 int check_split(void* kernel) {
@@ -172,11 +178,109 @@ int run_pair(const Product& p, const LibCtx& c, cudaStream_t stream) {
     P.group_m = 8;
     P.drop = p.drop;
     P.ctl = c.ctl;
-    if ((r = check_split(p.kernel)) != GBR_OK || (r = raise_smem(p.kernel, linear::kSmemBytes, c.device)) != GBR_OK)
+    if ((r = check_split(p.pair_kernel)) != GBR_OK || (r = raise_smem(p.pair_kernel, linear::kSmemBytes, c.device)) != GBR_OK)
         return r;
     const int64_t units = std::min<int64_t>(c.sm_count / 2, tiles);
     void* args[] = {&P};
-    const cudaError_t e = launch_plain(p.kernel, dim3(unsigned(2 * units)), linear::kThreads, linear::kSmemBytes, 2,
+    const cudaError_t e = launch_plain(p.pair_kernel, dim3(unsigned(2 * units)), linear::kThreads, linear::kSmemBytes, 2,
+                                       args, stream);
+    if (e != cudaSuccess) return report_cuda(e, "launching a linear kernel");
+    count_launch();
+    return GBR_OK;
+}
+
+// ------------------------------------------------------------ single tiles
+struct TilePlan {
+    int32_t bt, split, stages;
+    double cycles;                 // estimate, see below
+};
+
+// Estimated SM cycles of the product on either kernel, for the choice between
+// them, of the tile and of the split; fitted to measured sweeps of M 1..4096
+// with (K, N) from (512, 512) to (4096, 14336) on a 152-SM GB300.
+//   An SM takes in about 64 bytes a cycle from L2, about 40 where the wide
+//   operand comes from HBM and no other row tile shares it; all SMs together
+//   3500 from HBM.  DSMEM moves about 12 bytes a cycle and SM.
+//   CTA pairs: 32 KiB a CTA and 64-k slice, 512 cycles at full rate (which is
+//   also the tensor core's), 640 where less than one round of tiles runs;
+//   11500 to start, fill the ring and drain the last tile.
+// Measured against each other (us, best single tile / CTA pairs): rows 1,
+// 4096 x 4096 9.2 / 25; rows 128 14 / 26; rows 512 21.7 / 26; rows 128,
+// 4096 x 14336 27.8 / 31; rows 256 35.4 / 32; 301 x 520 x 1000 6.2 / 10.6;
+// 2048 x 1024 x 1024 10.3 / 11.7; dB of 4096 x 512 x 512 10.8 / 23, of
+// 512 x 4096 x 4096 33.6 / 18.
+double pair_cycles(const Product& p, int sms) {
+    const int64_t rounds = cdiv(cdiv(p.I, linear::kTile) * cdiv(p.J, linear::kTile), sms / 2);
+    return 11500.0 + double(rounds) * double(cdiv(p.Kc, 64)) * (rounds == 1 ? 640.0 : 512.0);
+}
+
+TilePlan plan_tile(const Product& p, int sms) {
+    TilePlan best = {0, 0, 0, 1e30};
+    const int64_t nks = cdiv(p.Kc, 64);
+    const double hbm = double(p.Kc) * double(p.J) * 2.0 / 3500.0;
+    for (int bt : {int(std::min<int64_t>(256, cdiv(p.I, 16) * 16)), 64, 128, 256}) {
+        if (p.a_mn && bt % 64 != 0) continue;           // MN-major rows come in panels of 64
+        if (bt > 64 && bt >= p.I + 64) continue;
+        const int64_t stage = linear::tile_stage_bytes(bt);
+        const int64_t t_tiles = cdiv(p.I, bt), tiles = t_tiles * cdiv(p.J, 128);
+        const double rows = double(std::min<int64_t>(p.I, bt));
+        for (int s : {1, 2, 4, 8}) {
+            if (s > nks && s > 1) continue;
+            const int64_t n = cdiv(tiles * s, sms), slices = cdiv(nks, s);
+            // Two CTAs an SM where a tile's parts and a ring worth having fit
+            // twice, unless one each is all there is (of large clusters fewer
+            // fit: 120 CTAs in eights, 144 in fours).
+            const int per_sm = bt <= 128 && !(n == 1 && (s <= 2 || tiles * s <= 120)) ? 2 : 1;
+            const int64_t budget = per_sm == 2 ? 110 * 1024 : 218 * 1024, rounds = cdiv(n, per_sm);
+            const int stages = int(std::min<int64_t>(linear::kTileMaxStages, (budget - 2304) / stage));
+            // A CTA turns its ring over once in about 2200 cycles at best.
+            const double feed = std::max(
+                double(n) * double(slices) * (16384.0 / (t_tiles == 1 ? 40.0 : 64.0) + bt * 2.0),
+                double(rounds) * double(slices) * 2200.0 / double(stages));
+            // HBM gives its rate to all SMs together; fewer get less of it.
+            const double busy = std::sqrt(double(sms) / double(std::min<int64_t>(sms, tiles * s)));
+            const double parts = double(n) * rows * 512.0 * (double(s - 1) / s / 12.0 + 1.0 / 64.0);
+            const double cycles = 6000.0 + std::max(feed, hbm * busy) + parts + 3000.0 * double(rounds - 1);
+            if (cycles < best.cycles) best = {bt, s, stages, cycles};
+        }
+    }
+    return best;
+}
+
+bool vec16(const Mat& m) { return !m || tma_ready(m); }
+
+int run_tile(const Product& p, const TilePlan& plan, const LibCtx& c, cudaStream_t stream) {
+    linear::TileParams P;
+    memset(&P, 0, sizeof(P));
+    int r;
+    if (p.Kc > 0) {
+        if ((r = p.b_mn ? map_2d(&P.mapW, p.B, p.Kc, p.J, 64, 64, "wide operand")
+                        : map_2d(&P.mapW, p.B, p.J, p.Kc, 64, 128, "wide operand")) != GBR_OK)
+            return r;
+        if ((r = p.a_mn ? map_2d(&P.mapX, p.A, p.Kc, p.I, 64, 64, "narrow operand")
+                        : map_2d(&P.mapX, p.A, p.I, p.Kc, 64, uint32_t(plan.bt), "narrow operand")) != GBR_OK)
+            return r;
+    }
+    P.bias = p.bias;
+    P.R = static_cast<const bf16*>(p.R.p), P.ldr = p.R.ld;
+    P.C = static_cast<bf16*>(p.C.w()), P.ldc = p.C.ld;
+    P.Z = static_cast<bf16*>(p.Z.w()), P.ldz = p.Z.ld;
+    P.vec = vec16(p.R) && vec16(p.C) && vec16(p.Z);
+    P.I = p.I, P.J = p.J;
+    P.bt = plan.bt;
+    P.t_tiles = int32_t(cdiv(p.I, plan.bt));
+    P.num_ks = int32_t(cdiv(p.Kc, 64));
+    P.split = plan.split;
+    P.stages = plan.stages;
+    P.tmem_cols = 32;
+    while (int32_t(P.tmem_cols) < plan.bt) P.tmem_cols *= 2;
+    P.drop = p.drop;
+    P.ctl = c.ctl;
+    const size_t smem = linear::tile_smem_bytes(plan.bt, plan.stages);
+    if ((r = raise_smem(p.tile_kernel, smem, c.device)) != GBR_OK) return r;
+    const int64_t ctas = int64_t(P.t_tiles) * cdiv(p.J, 128) * plan.split;
+    void* args[] = {&P};
+    const cudaError_t e = launch_plain(p.tile_kernel, dim3(unsigned(ctas)), linear::kTileThreads, smem, plan.split,
                                        args, stream);
     if (e != cudaSuccess) return report_cuda(e, "launching a linear kernel");
     count_launch();
@@ -192,6 +296,9 @@ int run_product(Product p, const LibCtx& c, cudaStream_t stream) {
         if ((r = aligned_mat(&p.A, p.a_mn ? p.Kc : p.I, p.a_mn ? p.I : p.Kc, true, ws, stream)) != GBR_OK) return r;
         if ((r = aligned_mat(&p.B, p.b_mn ? p.Kc : p.J, p.b_mn ? p.J : p.Kc, true, ws, stream)) != GBR_OK) return r;
     }
+    // The kernel of single tiles reads and writes everything else with plain accesses.
+    const TilePlan plan = plan_tile(p, c.sm_count);
+    if (plan.cycles < pair_cycles(p, c.sm_count)) return run_tile(p, plan, c, stream);
     if (p.R && (r = aligned_mat(&p.R, p.I, p.J, true, ws, stream)) != GBR_OK) return r;
     if ((r = aligned_mat(&p.C, p.I, p.J, false, ws, stream)) != GBR_OK) return r;
     if (p.Z && (r = aligned_mat(&p.Z, p.I, p.J, false, ws, stream)) != GBR_OK) return r;
@@ -252,7 +359,8 @@ int launch_linear(const LinearArgs& a, const LibCtx& c, cudaStream_t stream) {
     p.C = a.C, p.Z = a.Z, p.R = a.R;
     p.bias = a.bias;
     p.drop = a.drop;
-    p.kernel = linear_pair_forward_kernel(a.act);
+    p.pair_kernel = linear_pair_forward_kernel(a.act);
+    p.tile_kernel = linear_tile_forward_kernel(a.act);
     return run_product(p, c, stream);
 }
 
@@ -272,7 +380,8 @@ int launch_linear_da(Mat dZ, Mat B, Mat dA, int32_t M, int32_t N, int32_t K, con
     p.a_mn = false, p.b_mn = false;
     p.I = M, p.J = K, p.Kc = N;
     p.C = dA;
-    p.kernel = linear_pair_da_kernel();
+    p.pair_kernel = linear_pair_da_kernel();
+    p.tile_kernel = linear_tile_da_kernel();
     return run_product(p, c, stream);
 }
 
@@ -283,7 +392,8 @@ int launch_linear_db(Mat A, Mat dZ, Mat dB, int32_t M, int32_t N, int32_t K, con
     p.a_mn = true, p.b_mn = true;
     p.I = K, p.J = N, p.Kc = M;
     p.C = dB;
-    p.kernel = linear_pair_db_kernel();
+    p.pair_kernel = linear_pair_db_kernel();
+    p.tile_kernel = linear_tile_db_kernel();
     return run_product(p, c, stream);
 }
 
