@@ -22,11 +22,13 @@ enum WaitSite : uint32_t {
     kSiteMmaAccEmpty = 0x32,
     kSiteMmaDrain = 0x33,
     kSiteMmaTile = 0x34,
+    kSiteMmaHidden = 0x35,
     kSiteEpiAccFull = 0x41,
     kSiteEpiSplitSum = 0x42,
     kSiteEpiTile = 0x43,
     kSiteEpiBias = 0x44,
     kSiteEpiResidual = 0x45,
+    kSiteEpiHidden = 0x46,
     kSiteStorerFull = 0x51,
     kSiteSelfTest = 0x71,
 };

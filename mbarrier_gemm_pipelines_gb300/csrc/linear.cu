@@ -43,34 +43,12 @@ __global__ void __launch_bounds__(256)
             dst[r * ldd + c] = src[r * lds + c];
 }
 
-cudaError_t launch_plain(void* kernel, dim3 grid, int threads, size_t smem, int cluster, void** args,
-                         cudaStream_t stream) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    unsigned n = 0;
-    if (cluster > 1) {
-        attr[n].id = cudaLaunchAttributeClusterDimension;
-        attr[n].val.clusterDim.x = unsigned(cluster);
-        attr[n].val.clusterDim.y = 1;
-        attr[n].val.clusterDim.z = 1;
-        ++n;
-    }
-    n += unsigned(programmatic_launch_attr(attr + n));
-    cfg.attrs = attr;
-    cfg.numAttrs = n;
-    return cudaLaunchKernelExC(&cfg, kernel, args);
-}
-
 int repitch(Mat src, Mat dst, int32_t rows, int32_t cols, cudaStream_t stream) {
     const bf16* s = static_cast<const bf16*>(src.p);
     bf16* d = static_cast<bf16*>(dst.w());
     void* args[] = {&s, &src.ld, &d, &dst.ld, &rows, &cols};
     const dim3 grid(unsigned(std::min<int64_t>(cdiv(cols, 256), 64)), unsigned(std::min<int64_t>(rows, 8192)));
-    const cudaError_t e = launch_plain(reinterpret_cast<void*>(&repitch_kernel), grid, 256, 0, 1, args, stream);
+    const cudaError_t e = launch_kernel(reinterpret_cast<void*>(&repitch_kernel), grid, 256, 0, 1, args, stream);
     if (e != cudaSuccess) return report_cuda(e, "launching the re-pitching copy");
     count_launch();
     return GBR_OK;
@@ -141,14 +119,6 @@ int check_split(void* kernel) {
     return GBR_OK;
 }
 
-int raise_smem(void* kernel, size_t smem, int dev) {
-    static std::mutex mu;
-    static std::map<std::pair<void*, int>, size_t> set;
-    std::lock_guard<std::mutex> lk(mu);
-    const cudaError_t e = raise_smem_limit(kernel, smem, &set[{kernel, dev}]);
-    return e == cudaSuccess ? int(GBR_OK) : report_cuda(e, "cudaFuncSetAttribute(linear)");
-}
-
 int run_pair(const Product& p, const LibCtx& c, cudaStream_t stream) {
     linear::PairParams P;
     memset(&P, 0, sizeof(P));
@@ -178,11 +148,11 @@ int run_pair(const Product& p, const LibCtx& c, cudaStream_t stream) {
     P.group_m = 8;
     P.drop = p.drop;
     P.ctl = c.ctl;
-    if ((r = check_split(p.pair_kernel)) != GBR_OK || (r = raise_smem(p.pair_kernel, linear::kSmemBytes, c.device)) != GBR_OK)
+    if ((r = check_split(p.pair_kernel)) != GBR_OK || (r = raise_kernel_smem(p.pair_kernel, linear::kSmemBytes, c.device)) != GBR_OK)
         return r;
     const int64_t units = std::min<int64_t>(c.sm_count / 2, tiles);
     void* args[] = {&P};
-    const cudaError_t e = launch_plain(p.pair_kernel, dim3(unsigned(2 * units)), linear::kThreads, linear::kSmemBytes, 2,
+    const cudaError_t e = launch_kernel(p.pair_kernel, dim3(unsigned(2 * units)), linear::kThreads, linear::kSmemBytes, 2,
                                        args, stream);
     if (e != cudaSuccess) return report_cuda(e, "launching a linear kernel");
     count_launch();
@@ -277,10 +247,10 @@ int run_tile(const Product& p, const TilePlan& plan, const LibCtx& c, cudaStream
     P.drop = p.drop;
     P.ctl = c.ctl;
     const size_t smem = linear::tile_smem_bytes(plan.bt, plan.stages);
-    if ((r = raise_smem(p.tile_kernel, smem, c.device)) != GBR_OK) return r;
+    if ((r = raise_kernel_smem(p.tile_kernel, smem, c.device)) != GBR_OK) return r;
     const int64_t ctas = int64_t(P.t_tiles) * cdiv(p.J, 128) * plan.split;
     void* args[] = {&P};
-    const cudaError_t e = launch_plain(p.tile_kernel, dim3(unsigned(ctas)), linear::kTileThreads, smem, plan.split,
+    const cudaError_t e = launch_kernel(p.tile_kernel, dim3(unsigned(ctas)), linear::kTileThreads, smem, plan.split,
                                        args, stream);
     if (e != cudaSuccess) return report_cuda(e, "launching a linear kernel");
     count_launch();
@@ -367,7 +337,7 @@ int launch_linear(const LinearArgs& a, const LibCtx& c, cudaStream_t stream) {
 int launch_linear_dz(const LinearGradArgs& a, const LibCtx&, cudaStream_t stream) {
     LinearGradArgs arg = a;
     void* args[] = {&arg};
-    const cudaError_t e = launch_plain(dz_kernel_ptr(a.act), dim3(unsigned(cdiv(a.N, 32))), 256, 0, 1, args, stream);
+    const cudaError_t e = launch_kernel(dz_kernel_ptr(a.act), dim3(unsigned(cdiv(a.N, 32))), 256, 0, 1, args, stream);
     if (e != cudaSuccess) return report_cuda(e, "launching the gradient's dZ");
     count_launch();
     return GBR_OK;

@@ -1,113 +1,734 @@
-// moe_layer.cu -- a whole mixture-of-experts layer for a few tokens, as plain
-// kernels: the router (one CTA per token), the experts' hidden values (one
-// thread per token, choice and hidden column), the outputs (one thread per
-// token and output column, choices added in the order they were picked).
+// moe_layer.cu -- a whole mixture-of-experts layer for a few tokens.
+//
+//   logits = X Wr; per token the top_k largest and the softmax over them;
+//   h_te = act(x_t W1_e + b1_e) (gated: act(gate) * up);
+//   y_t  = sum over its experts e of w_te (h_te W2_e + b2_e)
+//
+// Bound by the chosen experts' weights, each read once: one token through 2 of
+// 8 experts of 4096 x 14336 needs 470 MB.  Three launches that overlap
+// (programmatic dependent launch):
+//
+// moe_router_kernel   a cluster of 8 CTAs for each group of tokens, each CTA
+//     one eighth of the logits' sums; parts added over distributed shared
+//     memory in rank order; one warp a token picks the top_k.
+//
+// moe_expert_kernel   one persistent CTA an SM.  The hidden columns of all
+//     chosen experts, in units of 64, are one list that is cut into equal
+//     parts.  A part computes its hidden columns for every token (transposed:
+//     128 hidden columns are the MMA's M, the tokens its N of 16..64, so no
+//     token is gathered: an expert's tokens are picked when results are
+//     written), keeps them in shared memory as bf16, and multiplies them at
+//     once with its rows of W2: W1's columns and W2's rows of a part belong
+//     together, so nothing waits for another CTA and one ring of TMA loads
+//     runs through both products without a break.  What comes out is an fp32
+//     part of y for the expert's tokens, written to scratch.
+//
+// moe_combine_kernel  adds the parts of each token's experts in order, times
+//     the router's weights.  No atomics: a result depends on the routing alone.
+//
+// Roles of the expert kernel (192 threads):
+//   warps 0-3  TMEM -> hidden values (bias, activation, bf16, swizzled shared
+//              memory) and TMEM -> parts
+//   warp 4     TMA producer (one lane)
+//   warp 5     TMEM allocation, MMA issue (one lane)
+#include "gbr.h"
+#include "gemm_umma.cuh"
 #include "operators.h"
 
 #include <cuda_bf16.h>
+
+#include <algorithm>
+#include <cstring>
 
 namespace gbr {
 namespace {
 
 using bf16 = __nv_bfloat16;
 
-// Softmax over the top_k largest logits of each token; ties go to the lowest
-// expert.  Order: descending.  A NaN logit ranks last.
-__global__ void __launch_bounds__(256) moe_router_kernel(const MoeArgs a) {
-    __shared__ float logit[kMoeMaxExperts];
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// ------------------------------------------------------------ router
+constexpr int kRouterThreads = 1024, kRouterCluster = 8, kRouterTokens = 4;
+
+// Orders logits: a NaN below everything, +0 = -0; 0 is below any logit's key.
+__device__ __forceinline__ uint32_t logit_key(float x) {
+    const uint32_t u = __float_as_uint(x + 0.f);
+    return isnan(x) ? 1u : (u >> 31) ? ~u : u | 0x80000000u;
+}
+
+// TB tokens a cluster.  Thread (ty, tx) sums rows ty, ty + ny, ... of this
+// CTA's eighth of Wr for expert tx; one read of Wr serves TB tokens.
+template <int TB>
+__global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const MoeArgs a, int32_t lanes) {
+    __shared__ float red[TB][kRouterThreads];
+    __shared__ float logit[TB][kMoeMaxExperts];
+    ptx::griddep_launch_dependents();   // the expert kernel's set-up overlaps this one
     ptx::griddep_wait();
-    const int t = int(blockIdx.x), lane = int(threadIdx.x) % 32;
-    const bf16* x = static_cast<const bf16*>(a.X) + int64_t(t) * a.D;
-    for (int e = int(threadIdx.x) / 32; e < a.E; e += 8) {
-        float v = 0.f;
-        for (int d = lane; d < a.D; d += 32)
-            v = fmaf(__bfloat162float(x[d]), a.Wr[int64_t(d) * a.E + e], v);
-        for (int o = 16; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (lane == 0) logit[e] = v;
+    const uint32_t rank = ptx::cluster_ctarank();
+    const int t0 = int(blockIdx.x / kRouterCluster) * TB, tid = int(threadIdx.x);
+    const int e = tid % lanes, ty = tid / lanes, ny = kRouterThreads / lanes;
+    const int d0 = int(rank) * (a.D / kRouterCluster), d1 = d0 + a.D / kRouterCluster;
+    const bf16* x = static_cast<const bf16*>(a.X);
+    float acc[TB] = {};
+    if (e < a.E) {
+#pragma unroll 4
+        for (int d = d0 + ty; d < d1; d += ny) {
+            const float w = __ldg(a.Wr + int64_t(d) * a.E + e);
+#pragma unroll
+            for (int i = 0; i < TB; ++i)
+                if (t0 + i < a.T) acc[i] = fmaf(__bfloat162float(x[int64_t(t0 + i) * a.D + d]), w, acc[i]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < TB; ++i) red[i][tid] = acc[i];
+    for (int s = ny / 2; s > 0; s /= 2) {
+        __syncthreads();
+        if (ty < s)
+#pragma unroll
+            for (int i = 0; i < TB; ++i) red[i][tid] += red[i][tid + s * lanes];
+    }
+    ptx::cluster_sync_all();
+    if (rank == 0) {
+        for (int j = tid; j < TB * a.E; j += kRouterThreads) {
+            const int i = j / a.E, ee = j % a.E;
+            const uint32_t at = ptx::smem_addr(&red[i][ee]);
+            float v = 0.f;
+#pragma unroll
+            for (uint32_t r = 0; r < kRouterCluster; ++r)
+                v += __uint_as_float(ptx::ld_shared_cluster_u32(ptx::mapa_shared(at, r)));
+            logit[i][ee] = v;
+        }
+        __syncthreads();
+        const int i = tid / 32, lane = tid % 32;
+        if (i < TB && t0 + i < a.T) {
+            uint32_t key[kMoeMaxExperts / 32];
+#pragma unroll
+            for (int c = 0; c < kMoeMaxExperts / 32; ++c)
+                key[c] = lane + 32 * c < a.E ? logit_key(logit[i][lane + 32 * c]) : 0u;
+            int mine = 0;                              // lane k keeps the k-th choice
+            for (int k = 0; k < a.top_k; ++k) {
+                uint64_t best = 0;
+#pragma unroll
+                for (int c = 0; c < kMoeMaxExperts / 32; ++c) {
+                    const uint64_t q = (uint64_t(key[c]) << 32) | uint32_t(~(lane + 32 * c));
+                    if (key[c] != 0 && q > best) best = q;
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o /= 2) {
+                    const uint64_t other = __shfl_xor_sync(0xffffffffu, best, o);
+                    if (other > best) best = other;
+                }
+                const int pick = int(~uint32_t(best));
+#pragma unroll
+                for (int c = 0; c < kMoeMaxExperts / 32; ++c)
+                    if (pick == lane + 32 * c) key[c] = 0;
+                if (lane == k) mine = pick;
+            }
+            const float top = logit[i][__shfl_sync(0xffffffffu, mine, 0)];
+            const float w = lane < a.top_k ? expf(logit[i][mine] - top) : 0.f;
+            float sum = 0.f;
+            for (int k = 0; k < a.top_k; ++k) sum += __shfl_sync(0xffffffffu, w, k);
+            if (lane < a.top_k) {
+                a.ids[int64_t(t0 + i) * a.top_k + lane] = mine;
+                a.weights[int64_t(t0 + i) * a.top_k + lane] = w / sum;
+            }
+        }
+    }
+    ptx::cluster_sync_all();   // the peers' sums have been read
+}
+
+// ------------------------------------------------------------ experts
+constexpr int kThreads = 192;
+constexpr uint32_t kPanelBytes = 64 * 128, kGroupBytes = 2 * kPanelBytes;
+constexpr int kMaxStages = 12;
+constexpr int kUnit = 64;                               // hidden columns of a unit
+
+// Where the parts of one (token, choice) lie: rows row0, row0 + step, ...
+// (count of them) of the parts' buffer.
+struct PairParts {
+    int32_t row0, step, count, expert;
+};
+
+struct ExpertParams {
+    CUtensorMap mapX, mapW1, mapW2;
+    MoeArgs a;
+    float* parts;                                       // [rows][D] fp32
+    PairParts* pairs;                                   // [T * top_k]
+    int32_t t_pad;                                      // tokens, rounded up to 16
+    int32_t units;                                      // units of an expert
+    int32_t max_units;                                  // units of a part that fit in shared memory
+    int32_t stages;
+    int32_t sms;
+    KernelCtl ctl;
+};
+
+// The cut of the list of units, the same in every CTA.
+struct Cut {
+    int32_t total;                                      // units of all chosen experts
+    int32_t parts;
+    __device__ __forceinline__ int32_t begin(int32_t v) const {
+        return int32_t(int64_t(v) * total / parts);
+    }
+    // The part that holds unit u: the last v with begin(v) <= u.
+    __device__ __forceinline__ int32_t part_of(int32_t u) const {
+        return int32_t(((int64_t(u) + 1) * parts + total - 1) / total) - 1;
+    }
+};
+
+struct alignas(16) Tables {
+    uint64_t mask[kMoeMaxExperts];                      // tokens of expert e
+    int32_t active[kMoeMaxExperts];                     // a-th chosen expert
+    int32_t base[kMoeMaxExperts];                       // first row of its parts
+    int32_t first[kMoeMaxExperts];                      // its first part
+    int32_t num_active;
+};
+
+// Exclusive sum over the warp's lanes.
+__device__ __forceinline__ int32_t warp_exclusive(int32_t v, uint32_t lane, int32_t& total) {
+    int32_t x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const int32_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (int(lane) >= o) x += y;
+    }
+    total = __shfl_sync(0xffffffffu, x, 31);
+    return x - v;
+}
+
+__device__ __forceinline__ Cut make_cut(const ExpertParams& P, int32_t active) {
+    Cut c;
+    c.total = active * P.units;
+    const int32_t per = (c.total + P.sms - 1) / P.sms;
+    const int32_t rounds = (per + P.max_units - 1) / P.max_units;
+    c.parts = min(P.sms * rounds, c.total);
+    return c;
+}
+
+// Builds the tables from the router's choice (all threads of the CTA).
+__device__ __forceinline__ void build_tables(const ExpertParams& P, Tables& tb) {
+    const MoeArgs& a = P.a;
+    for (int e = int(threadIdx.x); e < kMoeMaxExperts; e += kThreads) tb.mask[e] = 0;
+    __syncthreads();
+    for (int i = int(threadIdx.x); i < a.T * a.top_k; i += kThreads) {
+        const int e = int(a.ids[i]);
+        atomicOr(reinterpret_cast<unsigned long long*>(&tb.mask[e]), 1ull << (i / a.top_k));
     }
     __syncthreads();
-    if (threadIdx.x != 0) return;
-    int id[kMoeMaxTopK];
-    float w[kMoeMaxTopK], sum = 0.f;
-    for (int k = 0; k < a.top_k; ++k) {
-        int best = -1;
-        for (int e = 0; e < a.E; ++e) {
-            bool taken = false;
-            for (int j = 0; j < k; ++j) taken |= id[j] == e;
-            if (taken) continue;
-            if (best < 0 || logit[e] > logit[best] || (isnan(logit[best]) && !isnan(logit[e]))) best = e;
+    if (threadIdx.x < 32) {
+        const uint32_t lane = threadIdx.x;
+        constexpr int kPer = kMoeMaxExperts / 32;
+        int32_t n = 0, total;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) n += tb.mask[lane * kPer + i] != 0;
+        int32_t at = warp_exclusive(n, lane, total);
+        for (int i = 0; i < kPer; ++i)
+            if (tb.mask[lane * kPer + i] != 0) tb.active[at++] = int32_t(lane) * kPer + i;
+        if (lane == 0) tb.num_active = total;
+        __syncwarp();
+        const Cut cut = make_cut(P, total);
+        int32_t rows = 0, all;
+        for (int i = 0; i < kPer; ++i) {
+            const int32_t x = int32_t(lane) * kPer + i;
+            if (x >= total) break;
+            const int32_t f = cut.part_of(x * P.units), l = cut.part_of((x + 1) * P.units - 1);
+            tb.first[x] = f;
+            tb.base[x] = rows;                          // within this lane's experts
+            rows += (l - f + 1) * __popcll(tb.mask[tb.active[x]]);
         }
-        id[k] = best;
-        w[k] = expf(logit[best] - logit[id[0]]);
-        sum += w[k];
+        const int32_t before = warp_exclusive(rows, lane, all);
+        for (int i = 0; i < kPer && int32_t(lane) * kPer + i < total; ++i) tb.base[int32_t(lane) * kPer + i] += before;
     }
-    for (int k = 0; k < a.top_k; ++k) {
-        a.ids[t * a.top_k + k] = id[k];
-        a.weights[t * a.top_k + k] = w[k] / sum;
+    __syncthreads();
+}
+
+// One run of units of one expert inside a part.
+struct Segment {
+    int32_t index;                                      // of the expert among the chosen
+    int32_t expert;
+    int32_t u0, n;                                      // first unit within the expert, units
+    int32_t part;
+};
+
+// Walks the segments of this CTA's parts in order.
+struct Walk {
+    int32_t v, v_end, at, end;
+    __device__ __forceinline__ Walk(const Cut& c, int32_t sms) {
+        v = int32_t(int64_t(blockIdx.x) * c.parts / sms);
+        v_end = int32_t(int64_t(blockIdx.x + 1) * c.parts / sms);
+        at = end = 0;
+        if (v < v_end) {
+            at = c.begin(v);
+            end = c.begin(v + 1);
+        }
+    }
+    __device__ __forceinline__ bool next(const Cut& c, const Tables& tb, int32_t units, Segment& s) {
+        if (v >= v_end) return false;
+        s.index = at / units;
+        s.expert = tb.active[s.index];
+        s.u0 = at - s.index * units;
+        s.n = min(end - at, units - s.u0);
+        s.part = v;
+        at += s.n;
+        if (at >= end && ++v < v_end) {
+            at = c.begin(v);
+            end = c.begin(v + 1);
+        }
+        return true;
+    }
+};
+
+// NG: 128-column groups of a stage, 1, or 2 when gated (gate and up columns in
+// the first product, 2 x 128 output columns in the second).
+template <int ACT, int NG>
+__global__ void __launch_bounds__(kThreads, 1) moe_expert_kernel(const __grid_constant__ ExpertParams P) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ Tables tb;
+    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], h_full, h_empty, drain;
+    __shared__ uint32_t tmem_holder;
+    __shared__ int abort_word;
+    volatile int* abort_flag = &abort_word;
+    const MoeArgs& a = P.a;
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u;
+    const uint32_t S = uint32_t(P.stages), t_pad = uint32_t(P.t_pad);
+    const uint32_t h_block = t_pad * 128u;              // 64 hidden columns of every token
+    uint8_t* h_mem = align_1024(smem_raw);
+    const uint32_t h_base = ptx::smem_addr(h_mem);
+    const uint32_t ring_base = h_base + uint32_t(P.max_units) * h_block;
+    const uint32_t stage_bytes = NG * kGroupBytes + t_pad * 128u;
+
+    if (threadIdx.x == 0) {
+        for (uint32_t i = 0; i < S; ++i) {
+            ptx::mbar_init(ptx::smem_addr(full + i), 1);
+            ptx::mbar_init(ptx::smem_addr(empty + i), 1);
+        }
+        for (uint32_t i = 0; i < 2; ++i) {
+            ptx::mbar_init(ptx::smem_addr(acc_full + i), 1);
+            ptx::mbar_init(ptx::smem_addr(acc_empty + i), 4);
+        }
+        ptx::mbar_init(ptx::smem_addr(&h_full), 4);
+        ptx::mbar_init(ptx::smem_addr(&h_empty), 1);
+        ptx::mbar_init(ptx::smem_addr(&drain), 1);
+        abort_word = 0;
+        ptx::fence_barrier_init();
+    } else if (threadIdx.x == 128) {
+        ptx::prefetch_tensormap(&P.mapX);
+        ptx::prefetch_tensormap(&P.mapW1);
+        ptx::prefetch_tensormap(&P.mapW2);
+    }
+    if (warp == 5) {
+        ptx::tmem_alloc(ptx::smem_addr(&tmem_holder), 256);
+        ptx::tmem_relinquish_alloc_permit();
+    }
+    ptx::tc_fence_before_sync();
+    __syncthreads();
+    ptx::tc_fence_after_sync();
+    const uint32_t tmem = tmem_holder;
+    ptx::griddep_wait();
+    build_tables(P, tb);
+    const Cut cut = make_cut(P, tb.num_active);
+    if (blockIdx.x == 0) {
+        for (int i = int(threadIdx.x); i < a.T * a.top_k; i += kThreads) {
+            const int e = int(a.ids[i]), t = i / a.top_k;
+            int x = 0;                                  // e's place among the chosen
+            for (int lo = 0, hi = tb.num_active; lo < hi;) {
+                x = (lo + hi) / 2;
+                if (tb.active[x] == e) break;
+                if (tb.active[x] < e) lo = x + 1;
+                else hi = x;
+            }
+            PairParts q;
+            q.row0 = tb.base[x] + __popcll(tb.mask[e] & ((1ull << t) - 1));
+            q.step = __popcll(tb.mask[e]);
+            q.count = cut.part_of((x + 1) * P.units - 1) - tb.first[x] + 1;
+            q.expert = e;
+            P.pairs[i] = q;
+        }
+    }
+    const int32_t ks = (a.D + 63) / 64;                 // 64-k slices of the first product
+    const int32_t d_tiles = (a.D + 128 * NG - 1) / (128 * NG);
+    uint32_t issued = 0;
+
+    if (warp == 4 && lane == 0) {
+        // ------------------------------------------------------ producer
+        bool ok = true;
+        auto stage = [&](uint32_t bytes) -> uint32_t {
+            const uint32_t slot = issued % S, ph = (issued / S) & 1u;
+            ok = mbar_wait(ptx::smem_addr(empty + slot), ph ^ 1u, P.ctl, abort_flag, kSiteProducerEmpty, issued);
+            if (ok) ptx::mbar_arrive_expect_tx(ptx::smem_addr(full + slot), bytes);
+            return slot;
+        };
+        Segment s;
+        for (Walk w(cut, P.sms); ok && w.next(cut, tb, P.units, s);) {
+            for (int32_t u = 0; ok && u < s.n; u += 2) {
+                const uint32_t panels = u + 1 < s.n ? 2u : 1u;
+                for (int32_t k = 0; k < ks; ++k) {
+                    const uint32_t slot = stage(NG * panels * kPanelBytes + t_pad * 128u);
+                    if (!ok) break;
+                    const uint32_t dst = ring_base + slot * stage_bytes, bar = ptx::smem_addr(full + slot);
+#pragma unroll
+                    for (uint32_t g = 0; g < NG; ++g)
+                        for (uint32_t j = 0; j < panels; ++j)
+                            ptx::tma_load_3d(dst + g * kGroupBytes + j * kPanelBytes, &P.mapW1, bar,
+                                             int32_t(g) * a.F + (s.u0 + u + int32_t(j)) * kUnit, k * 64, s.expert);
+                    ptx::tma_load_2d(dst + NG * kGroupBytes, &P.mapX, bar, k * 64, 0);
+                    ++issued;
+                }
+            }
+            for (int32_t dt = 0; ok && dt < d_tiles; ++dt)
+                for (int32_t b = 0; b < s.n; ++b) {
+                    const uint32_t slot = stage(NG * kGroupBytes);
+                    if (!ok) break;
+                    const uint32_t dst = ring_base + slot * stage_bytes, bar = ptx::smem_addr(full + slot);
+#pragma unroll
+                    for (uint32_t j = 0; j < 2 * NG; ++j)
+                        ptx::tma_load_3d(dst + j * kPanelBytes, &P.mapW2, bar, dt * 128 * NG + int32_t(j) * 64,
+                                         (s.u0 + b) * kUnit, s.expert);
+                    ++issued;
+                }
+        }
+        ptx::griddep_launch_dependents();
+    } else if (warp == 5 && lane == 0) {
+        // ------------------------------------------------------ MMA issuer
+        // fp32 += bf16 x bf16, the wide operand MN-major, M = 128, N = t_pad.
+        const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | ((t_pad >> 3) << 17) |
+                               ((128u >> 4) << 24);
+        uint32_t it = 0, tl = 0, hn = 0;
+        bool ok = true;
+        auto take = [&]() -> uint32_t {
+            const uint32_t slot = it % S, ph = (it / S) & 1u;
+            ok = mbar_wait(ptx::smem_addr(full + slot), ph, P.ctl, abort_flag, kSiteMmaFull, it);
+            ptx::tc_fence_after_sync();
+            return slot;
+        };
+        auto acc_take = [&]() -> uint32_t {
+            const uint32_t b = tl & 1u;
+            ok = mbar_wait(ptx::smem_addr(acc_empty + b), ((tl >> 1) & 1u) ^ 1u, P.ctl, abort_flag,
+                           kSiteMmaAccEmpty, tl);
+            ptx::tc_fence_after_sync();
+            return tmem + b * 2u * t_pad;
+        };
+        Segment s;
+        for (Walk w(cut, P.sms); ok && w.next(cut, tb, P.units, s); ++hn) {
+            for (int32_t u = 0; ok && u < s.n; u += 2) {
+                const uint32_t acc = acc_take();
+                for (int32_t k = 0; ok && k < ks; ++k) {
+                    const uint32_t slot = take();
+                    if (!ok) break;
+                    const uint32_t base = ring_base + slot * stage_bytes;
+#pragma unroll
+                    for (uint32_t g = 0; g < NG; ++g)
+#pragma unroll
+                        for (uint32_t q = 0; q < 4; ++q)
+                            ptx::mma_f16(acc + g * t_pad,
+                                         umma::sw128_desc(base + g * kGroupBytes + q * 2048u, kPanelBytes, 1024),
+                                         umma::sw128_desc(base + NG * kGroupBytes + q * 32u, 16, 1024), idesc,
+                                         (k != 0 || q != 0) ? 1u : 0u);
+                    ptx::mma_commit(ptx::smem_addr(empty + slot));
+                    ++it;
+                }
+                if (!ok) break;
+                ptx::mma_commit(ptx::smem_addr(acc_full + (tl & 1u)));
+                ++tl;
+            }
+            if (!ok || !(ok = mbar_wait(ptx::smem_addr(&h_full), hn & 1u, P.ctl, abort_flag, kSiteMmaHidden, hn)))
+                break;
+            ptx::tc_fence_after_sync();
+            for (int32_t dt = 0; ok && dt < d_tiles; ++dt) {
+                const uint32_t acc = acc_take();
+                for (int32_t b = 0; ok && b < s.n; ++b) {
+                    const uint32_t slot = take();
+                    if (!ok) break;
+                    const uint32_t base = ring_base + slot * stage_bytes;
+#pragma unroll
+                    for (uint32_t g = 0; g < NG; ++g)
+#pragma unroll
+                        for (uint32_t q = 0; q < 4; ++q)
+                            ptx::mma_f16(acc + g * t_pad,
+                                         umma::sw128_desc(base + g * kGroupBytes + q * 2048u, kPanelBytes, 1024),
+                                         umma::sw128_desc(h_base + uint32_t(b) * h_block + q * 32u, 16, 1024), idesc,
+                                         (b != 0 || q != 0) ? 1u : 0u);
+                    ptx::mma_commit(ptx::smem_addr(empty + slot));
+                    ++it;
+                }
+                if (!ok) break;
+                ptx::mma_commit(ptx::smem_addr(acc_full + (tl & 1u)));
+                ++tl;
+            }
+            if (ok) ptx::mma_commit(ptx::smem_addr(&h_empty));
+        }
+        // No MMA may still be running when TMEM is released.
+        ptx::mma_commit(ptx::smem_addr(&drain));
+        mbar_wait_drain(ptx::smem_addr(&drain), 0, P.ctl.timeout_ns);
+    } else if (warp < 4) {
+        // ------------------------------------------------------ epilogue
+        uint32_t tl = 0, hn = 0;
+        bool ok = true;
+        auto acc_wait = [&]() -> uint32_t {
+            const uint32_t b = tl & 1u;
+            ok = mbar_wait_warp(ptx::smem_addr(acc_full + b), (tl >> 1) & 1u, P.ctl, abort_flag, kSiteEpiAccFull, tl);
+            ptx::tc_fence_after_sync();
+            return tmem + ((warp * 32u) << 16) + b * 2u * t_pad;
+        };
+        auto acc_done = [&]() {
+            ptx::tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(acc_empty + (tl & 1u)));
+            ++tl;
+        };
+        Segment s;
+        for (Walk w(cut, P.sms); ok && w.next(cut, tb, P.units, s); ++hn) {
+            // The previous segment's second product has read the hidden values.
+            if (hn > 0 && !(ok = mbar_wait_warp(ptx::smem_addr(&h_empty), (hn - 1u) & 1u, P.ctl, abort_flag,
+                                                kSiteEpiHidden, hn)))
+                break;
+            const uint64_t mask = tb.mask[s.expert];
+            for (int32_t u = 0; ok && u < s.n; u += 2) {
+                const int32_t col = int32_t(warp * 32u + lane), f = (s.u0 + u) * kUnit + col;
+                const bool inside = f < a.F && (col < 64 || u + 1 < s.n);
+                float b_gate = 0.f, b_up = 0.f;
+                if (inside && a.b1 != nullptr) {
+                    const float* b1 = a.b1 + int64_t(s.expert) * a.F * NG;
+                    b_gate = __ldg(b1 + f);
+                    if (NG == 2) b_up = __ldg(b1 + a.F + f);
+                }
+                const uint32_t acc = acc_wait();
+                if (!ok) break;
+                // Row t of the 64-column block: 16-byte chunks swizzled by t % 8.
+                const uint32_t blk = h_base + uint32_t(u + col / 64) * h_block, c8 = uint32_t(col % 64) / 8u;
+                if (col < 64 || u + 1 < s.n) {          // uniform over the warp
+                    for (uint32_t t = 0; t < t_pad; t += 16) {
+                        uint32_t r[16], r2[16];
+                        ptx::tmem_ld_32x32b_x16(acc + t, r);
+                        if (NG == 2) ptx::tmem_ld_32x32b_x16(acc + t_pad + t, r2);
+                        ptx::tmem_ld_wait();
+#pragma unroll
+                        for (uint32_t i = 0; i < 16; ++i) {
+                            float z = act_value<ACT>(__uint_as_float(r[i]) + b_gate);
+                            if (NG == 2) z *= __uint_as_float(r2[i]) + b_up;
+                            // Columns past F meet zero rows of W2: they must be finite.
+                            const bf16 v = __float2bfloat16_rn(inside ? z : 0.f);
+                            ptx::st_shared_u16(blk + (t + i) * 128u + ((c8 ^ ((t + i) & 7u)) << 4) +
+                                                   uint32_t(col % 8) * 2u,
+                                               __bfloat16_as_ushort(v));
+                        }
+                    }
+                }
+                acc_done();
+            }
+            if (!ok) break;
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&h_full));
+            // Parts of y: lane = output column, TMEM column = token.
+            const int32_t count = __popcll(mask);
+            float* out = P.parts + (int64_t(tb.base[s.index]) + int64_t(s.part - tb.first[s.index]) * count) * a.D;
+            for (int32_t dt = 0; ok && dt < d_tiles; ++dt) {
+                const uint32_t acc = acc_wait();
+                if (!ok) break;
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    const int32_t d = (dt * NG + g) * 128 + int32_t(warp * 32u + lane);
+                    float* o = out + d;
+                    for (uint32_t t = 0; t < t_pad; t += 16) {
+                        const uint32_t bits = uint32_t(mask >> t) & 0xFFFFu;
+                        if (bits == 0) continue;
+                        uint32_t r[16];
+                        ptx::tmem_ld_32x32b_x16(acc + uint32_t(g) * t_pad + t, r);
+                        ptx::tmem_ld_wait();
+#pragma unroll
+                        for (uint32_t i = 0; i < 16; ++i)
+                            if ((bits >> i) & 1u) {
+                                if (d < a.D) *o = __uint_as_float(r[i]);
+                                o += a.D;
+                            }
+                    }
+                }
+                acc_done();
+            }
+        }
+    }
+
+    __syncwarp();
+    ptx::tc_fence_before_sync();
+    __syncthreads();
+    if (*abort_flag && warp == 4 && lane == 0)
+        // Stages registered but not consumed: their loads have to land first.
+        for (uint32_t j = issued > S ? issued - S : 0u; j < issued; ++j)
+            mbar_wait_drain(ptx::smem_addr(full + j % S), (j / S) & 1u, P.ctl.timeout_ns);
+    __syncthreads();
+    if (warp == 5) {
+        ptx::tc_fence_after_sync();
+        ptx::tmem_dealloc(tmem, 256);
     }
 }
 
-__global__ void __launch_bounds__(128) moe_hidden_kernel(const MoeArgs a, float* h) {
+// ------------------------------------------------------------ combination
+constexpr int kCombineThreads = 256, kCombineLanes = 8;
+
+// 128 columns of one token a CTA; 8 threads share a column's parts and are
+// added in order.
+__global__ void __launch_bounds__(kCombineThreads)
+    moe_combine_kernel(const MoeArgs a, const float* parts, const PairParts* pairs) {
+    __shared__ float4 red[kCombineLanes][32];
     ptx::griddep_wait();
-    const int pair = int(blockIdx.y), t = pair / a.top_k;
-    const int f = int(blockIdx.x) * 128 + int(threadIdx.x);
-    if (f >= a.F) return;
-    const int e = int(a.ids[pair]);
-    const int64_t F1 = a.gated ? 2 * int64_t(a.F) : a.F;
-    const bf16* x = static_cast<const bf16*>(a.X) + int64_t(t) * a.D;
-    const bf16* w = static_cast<const bf16*>(a.W1) + int64_t(e) * a.D * F1;
-    float z = 0.f, u = 0.f;
-    for (int d = 0; d < a.D; ++d) {
-        const float xv = __bfloat162float(x[d]);
-        z = fmaf(xv, __bfloat162float(w[d * F1 + f]), z);
-        if (a.gated) u = fmaf(xv, __bfloat162float(w[d * F1 + a.F + f]), u);
+    const int t = int(blockIdx.y), quad = int(threadIdx.x) % 32, sl = int(threadIdx.x) / 32;
+    const int d = (int(blockIdx.x) * 32 + quad) * 4;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (d < a.D) {
+        for (int k = 0; k < a.top_k; ++k) {
+            const PairParts q = pairs[t * a.top_k + k];
+            const float w = a.weights[t * a.top_k + k];
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (sl == 0 && a.b2 != nullptr)
+                v = __ldg(reinterpret_cast<const float4*>(a.b2 + int64_t(q.expert) * a.D + d));
+            const float* p = parts + int64_t(q.row0) * a.D + d;
+#pragma unroll 8
+            for (int i = sl; i < q.count; i += kCombineLanes) {
+                const float4 x = __ldcg(reinterpret_cast<const float4*>(p + int64_t(i) * q.step * a.D));
+                v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+            }
+            y.x = fmaf(w, v.x, y.x), y.y = fmaf(w, v.y, y.y), y.z = fmaf(w, v.z, y.z), y.w = fmaf(w, v.w, y.w);
+        }
     }
-    if (a.b1 != nullptr) {
-        z += a.b1[e * F1 + f];
-        if (a.gated) u += a.b1[e * F1 + a.F + f];
+    red[sl][quad] = y;
+    __syncthreads();
+    if (sl == 0 && d < a.D) {
+#pragma unroll
+        for (int i = 1; i < kCombineLanes; ++i) {
+            const float4 x = red[i][quad];
+            y.x += x.x, y.y += x.y, y.z += x.z, y.w += x.w;
+        }
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(y.x, y.y), hi = __floats2bfloat162_rn(y.z, y.w);
+        uint2 v;
+        v.x = *reinterpret_cast<const uint32_t*>(&lo);
+        v.y = *reinterpret_cast<const uint32_t*>(&hi);
+        *reinterpret_cast<uint2*>(static_cast<bf16*>(a.Y) + int64_t(t) * a.D + d) = v;
     }
-    z = act_value(a.act, z);
-    h[int64_t(pair) * a.F + f] = a.gated ? z * u : z;
 }
 
-__global__ void __launch_bounds__(128) moe_output_kernel(const MoeArgs a, const float* h) {
-    ptx::griddep_wait();
-    const int t = int(blockIdx.y), d = int(blockIdx.x) * 128 + int(threadIdx.x);
-    if (d >= a.D) return;
-    float y = 0.f;
-    for (int k = 0; k < a.top_k; ++k) {
-        const int pair = t * a.top_k + k, e = int(a.ids[pair]);
-        const bf16* w = static_cast<const bf16*>(a.W2) + int64_t(e) * a.F * a.D;
-        float v = a.b2 != nullptr ? a.b2[int64_t(e) * a.D + d] : 0.f;
-        for (int f = 0; f < a.F; ++f)
-            v = fmaf(h[int64_t(pair) * a.F + f], __bfloat162float(w[int64_t(f) * a.D + d]), v);
-        y = fmaf(a.weights[pair], v, y);
+// ------------------------------------------------------------ host side
+template <int NG>
+void* expert_kernel(int act) {
+    switch (act) {
+        case kActRelu: return reinterpret_cast<void*>(&moe_expert_kernel<kActRelu, NG>);
+        case kActGelu: return reinterpret_cast<void*>(&moe_expert_kernel<kActGelu, NG>);
+        case kActGeluTanh: return reinterpret_cast<void*>(&moe_expert_kernel<kActGeluTanh, NG>);
+        case kActSilu: return reinterpret_cast<void*>(&moe_expert_kernel<kActSilu, NG>);
+        default: return reinterpret_cast<void*>(&moe_expert_kernel<kActNone, NG>);
     }
-    static_cast<bf16*>(a.Y)[int64_t(t) * a.D + d] = __float2bfloat16_rn(y);
+}
+
+struct ExpertPlan {
+    int32_t t_pad, units, max_units, stages, groups;
+    size_t smem;
+    int64_t max_rows;              // of the parts' buffer, whatever the routing
+};
+
+ExpertPlan plan_experts(const MoeArgs& a, const LibCtx& c) {
+    ExpertPlan p;
+    p.t_pad = int32_t(cdiv(a.T, 16) * 16);
+    p.units = int32_t(cdiv(a.F, kUnit));
+    p.groups = a.gated ? 2 : 1;
+    const int64_t budget = int64_t(c.smem_optin) - 1024 - 10 * 1024;   // alignment; tables and barriers
+    const int64_t stage = p.groups * int64_t(kGroupBytes) + p.t_pad * 128, block = p.t_pad * 128;
+    const int64_t experts = std::min<int64_t>(a.E, int64_t(a.T) * a.top_k);
+    // Room for a part's hidden columns if every expert that can be chosen is,
+    // as long as a ring of about 100 KiB remains.
+    const int64_t want = cdiv(experts * p.units, c.sm_count);
+    const int64_t ring = cdiv(100 * 1024, stage) * stage;
+    p.max_units = int32_t(std::max<int64_t>(1, std::min(want, (budget - ring) / block)));
+    p.stages = int32_t(std::min<int64_t>(kMaxStages, (budget - p.max_units * block) / stage));
+    p.smem = size_t(1024 + p.max_units * block + p.stages * stage);
+    // Rows: an expert's tokens times the parts it meets.  x chosen experts
+    // share at most parts + x - 1 meetings, no expert has more than T tokens,
+    // and the pairs are T * top_k: largest with as few experts as can be.
+    const int64_t parts = int64_t(c.sm_count) *
+                          cdiv(cdiv(experts * p.units, c.sm_count), p.max_units);
+    p.max_rows = int64_t(a.T) * (parts + experts);
+    return p;
+}
+
+size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+
+template <class... Args>
+cudaError_t launch_overlapped(void (*kernel)(Args...), dim3 grid, int threads, int cluster, cudaStream_t stream,
+                              Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    unsigned n = 0;
+    if (cluster > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = unsigned(cluster);
+        attr[n].val.clusterDim.y = 1;
+        attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    n += unsigned(programmatic_launch_attr(attr + n));
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 }  // namespace
 
-size_t moe_scratch_bytes(const MoeArgs& a, const LibCtx&) {
-    return size_t(a.T) * size_t(a.top_k) * size_t(a.F) * sizeof(float);
+size_t moe_scratch_bytes(const MoeArgs& a, const LibCtx& c) {
+    const ExpertPlan p = plan_experts(a, c);
+    return up256(size_t(a.T) * a.top_k * sizeof(PairParts)) + size_t(p.max_rows) * size_t(a.D) * sizeof(float);
 }
 
-cudaError_t launch_moe(const MoeArgs& a, void* scratch, const LibCtx&, cudaStream_t stream) {
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    cfg.numAttrs = programmatic_launch_attr(attr);
-    cfg.attrs = attr;
-    cfg.stream = stream;
-    cfg.gridDim = dim3(a.T);
-    cfg.blockDim = dim3(256);
-    cudaError_t e = cudaLaunchKernelEx(&cfg, moe_router_kernel, a);
-    if (e != cudaSuccess) return e;
-    float* h = static_cast<float*>(scratch);
-    cfg.blockDim = dim3(128);
-    cfg.gridDim = dim3((a.F + 127) / 128, a.T * a.top_k);
-    if ((e = cudaLaunchKernelEx(&cfg, moe_hidden_kernel, a, h)) != cudaSuccess) return e;
-    cfg.gridDim = dim3((a.D + 127) / 128, a.T);
-    return cudaLaunchKernelEx(&cfg, moe_output_kernel, a, static_cast<const float*>(h));
+int launch_moe(const MoeArgs& a, void* scratch, const LibCtx& c, cudaStream_t stream) {
+    const ExpertPlan plan = plan_experts(a, c);
+    ExpertParams P;
+    memset(&P, 0, sizeof(P));
+    const int64_t F1 = a.gated ? 2 * int64_t(a.F) : a.F;
+    const uint64_t xd[2] = {uint64_t(a.D), uint64_t(a.T)}, xs[1] = {uint64_t(a.D) * 2};
+    const uint64_t d1[3] = {uint64_t(F1), uint64_t(a.D), uint64_t(a.E)};
+    const uint64_t s1[2] = {uint64_t(F1) * 2, uint64_t(F1) * uint64_t(a.D) * 2};
+    const uint64_t d2[3] = {uint64_t(a.D), uint64_t(a.F), uint64_t(a.E)};
+    const uint64_t s2[2] = {uint64_t(a.D) * 2, uint64_t(a.F) * uint64_t(a.D) * 2};
+    const uint32_t bx[2] = {64, uint32_t(plan.t_pad)}, bw[3] = {64, 64, 1};
+    const auto bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
+    int r;
+    if ((r = encode_tensor_map(&P.mapX, bf, 2, a.X, xd, xs, bx, sw, "X")) != GBR_OK ||
+        (r = encode_tensor_map(&P.mapW1, bf, 3, a.W1, d1, s1, bw, sw, "W1")) != GBR_OK ||
+        (r = encode_tensor_map(&P.mapW2, bf, 3, a.W2, d2, s2, bw, sw, "W2")) != GBR_OK)
+        return r;
+    P.a = a;
+    P.pairs = static_cast<PairParts*>(scratch);
+    P.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) +
+                                       up256(size_t(a.T) * a.top_k * sizeof(PairParts)));
+    P.t_pad = plan.t_pad, P.units = plan.units, P.max_units = plan.max_units, P.stages = plan.stages;
+    P.sms = c.sm_count;
+    P.ctl = c.ctl;
+
+    int lanes = 1;
+    while (lanes < a.E) lanes *= 2;
+    // Few tokens: a cluster each, for latency; more share the reads of Wr.
+    const int tb = a.T * kRouterCluster <= c.sm_count ? 1 : kRouterTokens;
+    const dim3 rg(unsigned(cdiv(a.T, tb)) * kRouterCluster);
+    cudaError_t e = tb == 1 ? launch_overlapped(moe_router_kernel<1>, rg, kRouterThreads, kRouterCluster, stream, a,
+                                                int32_t(lanes))
+                            : launch_overlapped(moe_router_kernel<kRouterTokens>, rg, kRouterThreads, kRouterCluster,
+                                                stream, a, int32_t(lanes));
+    if (e != cudaSuccess) return report_cuda(e, "launching the router");
+    count_launch();
+
+    void* kernel = a.gated ? expert_kernel<2>(a.act) : expert_kernel<1>(a.act);
+    if ((r = raise_kernel_smem(kernel, plan.smem, c.device)) != GBR_OK) return r;
+    void* args[] = {&P};
+    if ((e = launch_kernel(kernel, dim3(unsigned(c.sm_count)), kThreads, plan.smem, 1, args, stream)) != cudaSuccess)
+        return report_cuda(e, "launching the experts");
+    count_launch();
+    const dim3 cg(unsigned(cdiv(a.D, 128)), unsigned(a.T));
+    e = launch_overlapped(moe_combine_kernel, cg, kCombineThreads, 1, stream, a, static_cast<const float*>(P.parts),
+                          static_cast<const PairParts*>(P.pairs));
+    if (e != cudaSuccess) return report_cuda(e, "launching the combination");
+    count_launch();
+    return GBR_OK;
 }
 
 }  // namespace gbr

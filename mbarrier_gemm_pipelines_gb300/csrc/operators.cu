@@ -4,6 +4,9 @@
 #include "operators.h"
 
 #include <cmath>
+#include <map>
+#include <mutex>
+#include <utility>
 
 namespace gbr {
 namespace {
@@ -71,6 +74,36 @@ int check_sizes(const char* fn, int64_t M, int64_t N, int64_t K) {
 }
 
 }  // namespace
+
+cudaError_t launch_kernel(void* kernel, dim3 grid, int threads, size_t smem, int cluster, void** args,
+                         cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    unsigned n = 0;
+    if (cluster > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = unsigned(cluster);
+        attr[n].val.clusterDim.y = 1;
+        attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    n += unsigned(programmatic_launch_attr(attr + n));
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
+    return cudaLaunchKernelExC(&cfg, kernel, args);
+}
+
+int raise_kernel_smem(void* kernel, size_t smem, int dev) {
+    static std::mutex mu;
+    static std::map<std::pair<void*, int>, size_t> set;
+    std::lock_guard<std::mutex> lk(mu);
+    const cudaError_t e = raise_smem_limit(kernel, smem, &set[{kernel, dev}]);
+    return e == cudaSuccess ? int(GBR_OK) : report_cuda(e, "cudaFuncSetAttribute(shared memory)");
+}
 
 int Scratch::take(size_t bytes, const char* what, void** out) {
     if (n_ >= int(sizeof(p_) / sizeof(p_[0]))) return report_errorf(GBR_ERR_CUDA, "%s: too many blocks", what);
@@ -256,9 +289,7 @@ int moe_layer(const void* X, const float* Wr, const void* W1, const float* b1, c
     uint8_t* base = static_cast<uint8_t*>(q);
     a.ids = expert_ids ? expert_ids : reinterpret_cast<int64_t*>(base);
     a.weights = expert_weights ? expert_weights : reinterpret_cast<float*>(base + route);
-    const cudaError_t e = launch_moe(a, base + 2 * route, c, st);
-    if (e != cudaSuccess) return report_cuda(e, "launching moe_layer");
-    return GBR_OK;
+    return launch_moe(a, base + 2 * route, c, st);
 }
 
 }  // extern "C"

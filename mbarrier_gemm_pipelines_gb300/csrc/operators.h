@@ -34,6 +34,12 @@ private:
     int n_ = 0;
 };
 
+// A launch with programmatic overlap and an optional cluster along x.
+cudaError_t launch_kernel(void* kernel, dim3 grid, int threads, size_t smem, int cluster, void** args,
+                          cudaStream_t stream);
+// Raises a kernel's dynamic shared-memory limit on a device as far as needed.
+int raise_kernel_smem(void* kernel, size_t smem, int dev);
+
 // The launches below count themselves and return a gbr_status.
 // ------------------------------------------------------------ dropout_add
 struct DropoutAddArgs {
@@ -90,6 +96,6 @@ struct MoeArgs {
     bool gated;
 };
 size_t moe_scratch_bytes(const MoeArgs& a, const LibCtx& c);
-cudaError_t launch_moe(const MoeArgs& a, void* scratch, const LibCtx& c, cudaStream_t stream);
+int launch_moe(const MoeArgs& a, void* scratch, const LibCtx& c, cudaStream_t stream);
 
 }  // namespace gbr
