@@ -24,6 +24,7 @@
 // (one K-major box, or BT / 64 MN-major panels).
 #pragma once
 #include "gemm_umma.cuh"
+#include "mma_issue.cuh"
 #include "operators.h"
 #include "vec8.cuh"
 
@@ -158,8 +159,8 @@ __global__ void __launch_bounds__(kTileThreads)
 
     uint32_t issued = 0;
     if (warp == 4 && lane == 0) {
+        uint32_t slot = 0, ph = 0;
         for (int32_t ks = ks0; ks < ks1; ++ks, ++issued) {
-            const uint32_t slot = issued % stages, ph = (issued / stages) & 1u;
             if (!mbar_wait(ptx::smem_addr(empty + slot), ph ^ 1u, P.ctl, abort_flag, kSiteProducerEmpty, issued))
                 break;
             const uint32_t bar = ptx::smem_addr(full + slot), dst = ring_base + slot * stage_bytes;
@@ -177,27 +178,34 @@ __global__ void __launch_bounds__(kTileThreads)
             } else {
                 ptx::tma_load_2d(dst + kWideBytes, &P.mapX, bar, k0, i0);
             }
+            if (++slot == stages) {
+                slot = 0;
+                ph ^= 1u;
+            }
         }
         ptx::griddep_launch_dependents();
     } else if (warp == 5 && lane == 0) {
         // Instruction descriptor: fp32 += bf16 x bf16, M = 128, N = bt.
         const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(W_MN) << 15) |
                                (uint32_t(X_MN) << 16) | ((uint32_t(P.bt) >> 3) << 17) | ((128u >> 4) << 24);
-        uint32_t it = 0;
+        constexpr uint32_t hi = desc_hi(1024), lbo_w = W_MN ? 64 * 128 : 16, lbo_x = X_MN ? 64 * 128 : 16;
+        const uint32_t w_first = desc_lo(ring_base, lbo_w), x_first = desc_lo(ring_base + kWideBytes, lbo_x);
+        const uint32_t full0 = ptx::smem_addr(full), to_empty = ptx::smem_addr(empty) - full0;
+        uint32_t at = 0, bar = full0, left = stages, ph = 0, it = 0;
         for (int32_t ks = ks0; ks < ks1; ++ks, ++it) {
-            const uint32_t slot = it % stages, ph = (it / stages) & 1u;
-            if (!mbar_wait(ptx::smem_addr(full + slot), ph, P.ctl, abort_flag, kSiteMmaFull, it)) break;
+            if (!mbar_wait(bar, ph, P.ctl, abort_flag, kSiteMmaFull, it)) break;
             ptx::tc_fence_after_sync();
-            const uint32_t w = ring_base + slot * stage_bytes, x = w + kWideBytes;
-#pragma unroll
-            for (uint32_t k = 0; k < 4; ++k) {
-                const uint64_t wd = W_MN ? umma::sw128_desc(w + k * 2048u, 64 * 128, 1024)
-                                         : umma::sw128_desc(w + k * 32u, 16, 1024);
-                const uint64_t xd = X_MN ? umma::sw128_desc(x + k * 2048u, 64 * 128, 1024)
-                                         : umma::sw128_desc(x + k * 32u, 16, 1024);
-                ptx::mma_f16(tmem, wd, xd, idesc, (it != 0 || k != 0) ? 1u : 0u);
+            mma_slice<W_MN ? kStepMN : kStepK, X_MN ? kStepMN : kStepK>(tmem, w_first + at, x_first + at, hi, idesc,
+                                                                        it);
+            ptx::mma_commit(bar + to_empty);
+            bar += 8;
+            at += stage_bytes / 16;
+            if (--left == 0) {
+                left = stages;
+                at = 0;
+                bar = full0;
+                ph ^= 1u;
             }
-            ptx::mma_commit(ptx::smem_addr(empty + slot));
         }
         // Completes when every MMA issued has: also what the exit path waits for.
         ptx::mma_commit(ptx::smem_addr(acc_full));

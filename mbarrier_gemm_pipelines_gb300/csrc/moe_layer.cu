@@ -33,6 +33,7 @@
 //   warp 5     TMEM allocation, MMA issue (one lane)
 #include "gbr.h"
 #include "gemm_umma.cuh"
+#include "mma_issue.cuh"
 #include "operators.h"
 
 #include <cuda_bf16.h>
@@ -139,9 +140,26 @@ __global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const MoeArg
 
 // ------------------------------------------------------------ experts
 constexpr int kThreads = 192;
-constexpr uint32_t kPanelBytes = 64 * 128, kGroupBytes = 2 * kPanelBytes;
+constexpr uint32_t kSliceBytes = 64 * 128;              // 64 weight rows x 64 columns
 constexpr int kMaxStages = 12;
+constexpr uint32_t kXStages = 4;
 constexpr int kUnit = 64;                               // hidden columns of a unit
+// 128-column tiles that are accumulated side by side: the tokens' tile of a
+// k step is loaded once for all of them, and a row of W1 or W2 is read 1 KiB
+// at a time (four tiles' panels one after the other).
+constexpr int kWide = 4;
+
+// A position in a ring of n slots.
+struct Ring {
+    uint32_t slot = 0, phase = 0, count = 0;
+    __device__ __forceinline__ void step(uint32_t n) {
+        ++count;
+        if (++slot == n) {
+            slot = 0;
+            phase ^= 1u;
+        }
+    }
+};
 
 // Where the parts of one (token, choice) lie: rows row0, row0 + step, ...
 // (count of them) of the parts' buffer.
@@ -150,7 +168,7 @@ struct PairParts {
 };
 
 struct ExpertParams {
-    CUtensorMap mapX, mapW1, mapW2;
+    CUtensorMap mapX, mapW1, mapW2, mapW2half;          // W boxes: 64 ksub rows (half: 64)
     MoeArgs a;
     float* parts;                                       // [rows][D] fp32
     PairParts* pairs;                                   // [T * top_k]
@@ -158,6 +176,7 @@ struct ExpertParams {
     int32_t units;                                      // units of an expert
     int32_t max_units;                                  // units of a part that fit in shared memory
     int32_t stages;
+    int32_t ksub;                                       // 64-row slices of a stage, 1 or 2
     int32_t sms;
     KernelCtl ctl;
 };
@@ -277,29 +296,39 @@ struct Walk {
     }
 };
 
-// NG: 128-column groups of a stage, 1, or 2 when gated (gate and up columns in
-// the first product, 2 x 128 output columns in the second).
+// NG: 1, or 2 when gated: of the first product's kWide tiles, which are then
+// gate and up columns in turn.
 template <int ACT, int NG>
 __global__ void __launch_bounds__(kThreads, 1) moe_expert_kernel(const __grid_constant__ ExpertParams P) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ Tables tb;
-    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], h_full, h_empty, drain;
+    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], x_full[kXStages], x_empty[kXStages], acc_full[2],
+        acc_empty[2], h_full, h_empty, drain;
     __shared__ uint32_t tmem_holder;
     __shared__ int abort_word;
     volatile int* abort_flag = &abort_word;
     const MoeArgs& a = P.a;
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u;
-    const uint32_t S = uint32_t(P.stages), t_pad = uint32_t(P.t_pad);
+    const uint32_t S = uint32_t(P.stages), t_pad = uint32_t(P.t_pad), ksub = uint32_t(P.ksub);
     const uint32_t h_block = t_pad * 128u;              // 64 hidden columns of every token
+    const uint32_t x_bytes = ksub * h_block;            // 64 ksub columns of X of every token
+    const uint32_t panel = ksub * kSliceBytes, stage_bytes = 2 * panel;
     uint8_t* h_mem = align_1024(smem_raw);
     const uint32_t h_base = ptx::smem_addr(h_mem);
-    const uint32_t ring_base = h_base + uint32_t(P.max_units) * h_block;
-    const uint32_t stage_bytes = NG * kGroupBytes + t_pad * 128u;
+    const uint32_t x_base = h_base + uint32_t(P.max_units) * h_block;
+    const uint32_t ring_base = x_base + kXStages * x_bytes;
+    // Two accumulators of kWide tiles: a power of two of columns, at most 512.
+    const uint32_t tmem_cols = t_pad > 32 ? 512u : 8u * t_pad;
+    constexpr int32_t kUnitsPass = 2 * kWide / NG;      // units accumulated side by side
 
     if (threadIdx.x == 0) {
         for (uint32_t i = 0; i < S; ++i) {
             ptx::mbar_init(ptx::smem_addr(full + i), 1);
             ptx::mbar_init(ptx::smem_addr(empty + i), 1);
+        }
+        for (uint32_t i = 0; i < kXStages; ++i) {
+            ptx::mbar_init(ptx::smem_addr(x_full + i), 1);
+            ptx::mbar_init(ptx::smem_addr(x_empty + i), 1);
         }
         for (uint32_t i = 0; i < 2; ++i) {
             ptx::mbar_init(ptx::smem_addr(acc_full + i), 1);
@@ -316,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_expert_kernel(const __grid_co
         ptx::prefetch_tensormap(&P.mapW2);
     }
     if (warp == 5) {
-        ptx::tmem_alloc(ptx::smem_addr(&tmem_holder), 256);
+        ptx::tmem_alloc(ptx::smem_addr(&tmem_holder), tmem_cols);
         ptx::tmem_relinquish_alloc_permit();
     }
     ptx::tc_fence_before_sync();
@@ -344,46 +373,58 @@ __global__ void __launch_bounds__(kThreads, 1) moe_expert_kernel(const __grid_co
             P.pairs[i] = q;
         }
     }
-    const int32_t ks = (a.D + 63) / 64;                 // 64-k slices of the first product
-    const int32_t d_tiles = (a.D + 128 * NG - 1) / (128 * NG);
-    uint32_t issued = 0;
+    const int32_t kstep = 64 * int32_t(ksub);
+    Ring ring, xring;                                   // of the producer; of the MMA lane
 
     if (warp == 4 && lane == 0) {
         // ------------------------------------------------------ producer
         bool ok = true;
         auto stage = [&](uint32_t bytes) -> uint32_t {
-            const uint32_t slot = issued % S, ph = (issued / S) & 1u;
-            ok = mbar_wait(ptx::smem_addr(empty + slot), ph ^ 1u, P.ctl, abort_flag, kSiteProducerEmpty, issued);
-            if (ok) ptx::mbar_arrive_expect_tx(ptx::smem_addr(full + slot), bytes);
-            return slot;
+            ok = mbar_wait(ptx::smem_addr(empty + ring.slot), ring.phase ^ 1u, P.ctl, abort_flag,
+                           kSiteProducerEmpty, ring.count);
+            if (ok) ptx::mbar_arrive_expect_tx(ptx::smem_addr(full + ring.slot), bytes);
+            return ring_base + ring.slot * stage_bytes;
         };
         Segment s;
         for (Walk w(cut, P.sms); ok && w.next(cut, tb, P.units, s);) {
-            for (int32_t u = 0; ok && u < s.n; u += 2) {
-                const uint32_t panels = u + 1 < s.n ? 2u : 1u;
-                for (int32_t k = 0; k < ks; ++k) {
-                    const uint32_t slot = stage(NG * panels * kPanelBytes + t_pad * 128u);
-                    if (!ok) break;
-                    const uint32_t dst = ring_base + slot * stage_bytes, bar = ptx::smem_addr(full + slot);
+            for (int32_t g0 = 0; ok && g0 < s.n; g0 += kUnitsPass) {
+                const int32_t g1 = min(g0 + kUnitsPass, s.n);
+                for (int32_t k = 0; ok && k < a.D; k += kstep) {
+                    if (!(ok = mbar_wait(ptx::smem_addr(x_empty + xring.slot), xring.phase ^ 1u, P.ctl, abort_flag,
+                                         kSiteProducerEmpty, xring.count)))
+                        break;
+                    const uint32_t xbar = ptx::smem_addr(x_full + xring.slot), xdst = x_base + xring.slot * x_bytes;
+                    ptx::mbar_arrive_expect_tx(xbar, x_bytes);
+                    for (uint32_t h = 0; h < ksub; ++h)
+                        ptx::tma_load_2d(xdst + h * h_block, &P.mapX, xbar, k + int32_t(h) * 64, 0);
+                    xring.step(kXStages);
+                    for (int32_t u = g0; ok && u < g1; u += 2) {
+                        const bool two = u + 1 < g1;
 #pragma unroll
-                    for (uint32_t g = 0; g < NG; ++g)
-                        for (uint32_t j = 0; j < panels; ++j)
-                            ptx::tma_load_3d(dst + g * kGroupBytes + j * kPanelBytes, &P.mapW1, bar,
-                                             int32_t(g) * a.F + (s.u0 + u + int32_t(j)) * kUnit, k * 64, s.expert);
-                    ptx::tma_load_2d(dst + NG * kGroupBytes, &P.mapX, bar, k * 64, 0);
-                    ++issued;
+                        for (int32_t g = 0; g < NG; ++g) {
+                            const uint32_t dst = stage(two ? stage_bytes : panel);
+                            if (!ok) break;
+                            const uint32_t bar = ptx::smem_addr(full + ring.slot);
+                            const int32_t col = g * a.F + (s.u0 + u) * kUnit;
+                            ptx::tma_load_3d(dst, &P.mapW1, bar, col, k, s.expert);
+                            if (two) ptx::tma_load_3d(dst + panel, &P.mapW1, bar, col + kUnit, k, s.expert);
+                            ring.step(S);
+                        }
+                    }
                 }
             }
-            for (int32_t dt = 0; ok && dt < d_tiles; ++dt)
-                for (int32_t b = 0; b < s.n; ++b) {
-                    const uint32_t slot = stage(NG * kGroupBytes);
-                    if (!ok) break;
-                    const uint32_t dst = ring_base + slot * stage_bytes, bar = ptx::smem_addr(full + slot);
-#pragma unroll
-                    for (uint32_t j = 0; j < 2 * NG; ++j)
-                        ptx::tma_load_3d(dst + j * kPanelBytes, &P.mapW2, bar, dt * 128 * NG + int32_t(j) * 64,
-                                         (s.u0 + b) * kUnit, s.expert);
-                    ++issued;
+            for (int32_t d0 = 0; ok && d0 < a.D; d0 += 128 * kWide)
+                for (int32_t b = 0; ok && b < s.n; b += int32_t(ksub)) {
+                    const bool half = b + int32_t(ksub) > s.n;   // 64 rows are left, of 128
+                    const CUtensorMap* map = half ? &P.mapW2half : &P.mapW2;
+                    for (int32_t d = d0; d < min(d0 + 128 * kWide, a.D); d += 128) {
+                        const uint32_t dst = stage(half ? 2 * kSliceBytes : stage_bytes);
+                        if (!ok) break;
+                        const uint32_t bar = ptx::smem_addr(full + ring.slot);
+                        ptx::tma_load_3d(dst, map, bar, d, (s.u0 + b) * kUnit, s.expert);
+                        ptx::tma_load_3d(dst + panel, map, bar, d + 64, (s.u0 + b) * kUnit, s.expert);
+                        ring.step(S);
+                    }
                 }
         }
         ptx::griddep_launch_dependents();
@@ -392,67 +433,72 @@ __global__ void __launch_bounds__(kThreads, 1) moe_expert_kernel(const __grid_co
         // fp32 += bf16 x bf16, the wide operand MN-major, M = 128, N = t_pad.
         const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | ((t_pad >> 3) << 17) |
                                ((128u >> 4) << 24);
-        uint32_t it = 0, tl = 0, hn = 0;
+        uint32_t tl = 0, hn = 0;
         bool ok = true;
-        auto take = [&]() -> uint32_t {
-            const uint32_t slot = it % S, ph = (it / S) & 1u;
-            ok = mbar_wait(ptx::smem_addr(full + slot), ph, P.ctl, abort_flag, kSiteMmaFull, it);
-            ptx::tc_fence_after_sync();
-            return slot;
-        };
         auto acc_take = [&]() -> uint32_t {
             const uint32_t b = tl & 1u;
             ok = mbar_wait(ptx::smem_addr(acc_empty + b), ((tl >> 1) & 1u) ^ 1u, P.ctl, abort_flag,
                            kSiteMmaAccEmpty, tl);
             ptx::tc_fence_after_sync();
-            return tmem + b * 2u * t_pad;
+            return tmem + b * kWide * t_pad;
+        };
+        auto acc_give = [&]() {
+            ptx::mma_commit(ptx::smem_addr(acc_full + (tl & 1u)));
+            ++tl;
+        };
+        // One stage into accumulator acc: `slices` (1 or 2) of 64 k; addresses in
+        // descriptor units, the tokens' slices x_next apart.
+        constexpr uint32_t hi = desc_hi(1024);
+        const uint32_t w_first = desc_lo(ring_base, panel), x_next = h_block / 16;
+        const uint32_t full0 = ptx::smem_addr(full), to_empty = ptx::smem_addr(empty) - full0;
+        uint32_t w_lo = w_first, bar = full0, left = S;
+        auto multiply = [&](uint32_t acc, uint32_t x_lo, uint32_t slices, uint32_t accumulate) {
+            if (!(ok = mbar_wait(bar, ring.phase, P.ctl, abort_flag, kSiteMmaFull, ring.count))) return;
+            ptx::tc_fence_after_sync();
+            mma_slice<kStepMN, kStepK>(acc, w_lo, x_lo, hi, idesc, accumulate);
+            if (slices == 2)
+                mma_slice<kStepMN, kStepK>(acc, w_lo + kSliceBytes / 16, x_lo + x_next, hi, idesc, 1u);
+            ptx::mma_commit(bar + to_empty);
+            ++ring.count;
+            bar += 8;
+            w_lo += stage_bytes / 16;
+            if (--left == 0) {
+                left = S;
+                bar = full0;
+                w_lo = w_first;
+                ring.phase ^= 1u;
+            }
         };
         Segment s;
         for (Walk w(cut, P.sms); ok && w.next(cut, tb, P.units, s); ++hn) {
-            for (int32_t u = 0; ok && u < s.n; u += 2) {
+            for (int32_t g0 = 0; ok && g0 < s.n; g0 += kUnitsPass) {
+                const int32_t tiles = (min(kUnitsPass, s.n - g0) + 1) / 2 * NG;
                 const uint32_t acc = acc_take();
-                for (int32_t k = 0; ok && k < ks; ++k) {
-                    const uint32_t slot = take();
-                    if (!ok) break;
-                    const uint32_t base = ring_base + slot * stage_bytes;
-#pragma unroll
-                    for (uint32_t g = 0; g < NG; ++g)
-#pragma unroll
-                        for (uint32_t q = 0; q < 4; ++q)
-                            ptx::mma_f16(acc + g * t_pad,
-                                         umma::sw128_desc(base + g * kGroupBytes + q * 2048u, kPanelBytes, 1024),
-                                         umma::sw128_desc(base + NG * kGroupBytes + q * 32u, 16, 1024), idesc,
-                                         (k != 0 || q != 0) ? 1u : 0u);
-                    ptx::mma_commit(ptx::smem_addr(empty + slot));
-                    ++it;
+                for (int32_t k = 0; ok && k < a.D; k += kstep) {
+                    if (!(ok = mbar_wait(ptx::smem_addr(x_full + xring.slot), xring.phase, P.ctl, abort_flag,
+                                         kSiteMmaFull, xring.count)))
+                        break;
+                    const uint32_t x_lo = desc_lo(x_base + xring.slot * x_bytes, 16);
+                    for (int32_t j = 0; ok && j < tiles; ++j)
+                        multiply(acc + uint32_t(j) * t_pad, x_lo, ksub, k != 0);
+                    ptx::mma_commit(ptx::smem_addr(x_empty + xring.slot));
+                    xring.step(kXStages);
                 }
-                if (!ok) break;
-                ptx::mma_commit(ptx::smem_addr(acc_full + (tl & 1u)));
-                ++tl;
+                if (ok) acc_give();
             }
             if (!ok || !(ok = mbar_wait(ptx::smem_addr(&h_full), hn & 1u, P.ctl, abort_flag, kSiteMmaHidden, hn)))
                 break;
             ptx::tc_fence_after_sync();
-            for (int32_t dt = 0; ok && dt < d_tiles; ++dt) {
+            for (int32_t d0 = 0; ok && d0 < a.D; d0 += 128 * kWide) {
+                const int32_t tiles = min(kWide, (a.D - d0 + 127) / 128);
                 const uint32_t acc = acc_take();
-                for (int32_t b = 0; ok && b < s.n; ++b) {
-                    const uint32_t slot = take();
-                    if (!ok) break;
-                    const uint32_t base = ring_base + slot * stage_bytes;
-#pragma unroll
-                    for (uint32_t g = 0; g < NG; ++g)
-#pragma unroll
-                        for (uint32_t q = 0; q < 4; ++q)
-                            ptx::mma_f16(acc + g * t_pad,
-                                         umma::sw128_desc(base + g * kGroupBytes + q * 2048u, kPanelBytes, 1024),
-                                         umma::sw128_desc(h_base + uint32_t(b) * h_block + q * 32u, 16, 1024), idesc,
-                                         (b != 0 || q != 0) ? 1u : 0u);
-                    ptx::mma_commit(ptx::smem_addr(empty + slot));
-                    ++it;
+                for (int32_t b = 0; ok && b < s.n; b += int32_t(ksub)) {
+                    const uint32_t x_lo = desc_lo(h_base + uint32_t(b) * h_block, 16);
+                    const uint32_t slices = uint32_t(min(int32_t(ksub), s.n - b));
+                    for (int32_t j = 0; ok && j < tiles; ++j)
+                        multiply(acc + uint32_t(j) * t_pad, x_lo, slices, b != 0);
                 }
-                if (!ok) break;
-                ptx::mma_commit(ptx::smem_addr(acc_full + (tl & 1u)));
-                ++tl;
+                if (ok) acc_give();
             }
             if (ok) ptx::mma_commit(ptx::smem_addr(&h_empty));
         }
@@ -467,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_expert_kernel(const __grid_co
             const uint32_t b = tl & 1u;
             ok = mbar_wait_warp(ptx::smem_addr(acc_full + b), (tl >> 1) & 1u, P.ctl, abort_flag, kSiteEpiAccFull, tl);
             ptx::tc_fence_after_sync();
-            return tmem + ((warp * 32u) << 16) + b * 2u * t_pad;
+            return tmem + ((warp * 32u) << 16) + b * kWide * t_pad;
         };
         auto acc_done = [&]() {
             ptx::tc_fence_before_sync();
@@ -482,20 +528,22 @@ __global__ void __launch_bounds__(kThreads, 1) moe_expert_kernel(const __grid_co
                                                 kSiteEpiHidden, hn)))
                 break;
             const uint64_t mask = tb.mask[s.expert];
-            for (int32_t u = 0; ok && u < s.n; u += 2) {
-                const int32_t col = int32_t(warp * 32u + lane), f = (s.u0 + u) * kUnit + col;
-                const bool inside = f < a.F && (col < 64 || u + 1 < s.n);
-                float b_gate = 0.f, b_up = 0.f;
-                if (inside && a.b1 != nullptr) {
-                    const float* b1 = a.b1 + int64_t(s.expert) * a.F * NG;
-                    b_gate = __ldg(b1 + f);
-                    if (NG == 2) b_up = __ldg(b1 + a.F + f);
-                }
-                const uint32_t acc = acc_wait();
+            for (int32_t g0 = 0; ok && g0 < s.n; g0 += kUnitsPass) {
+                const uint32_t acc0 = acc_wait();
                 if (!ok) break;
-                // Row t of the 64-column block: 16-byte chunks swizzled by t % 8.
-                const uint32_t blk = h_base + uint32_t(u + col / 64) * h_block, c8 = uint32_t(col % 64) / 8u;
-                if (col < 64 || u + 1 < s.n) {          // uniform over the warp
+                for (int32_t u = g0; u < min(g0 + kUnitsPass, s.n); u += 2) {
+                    const int32_t col = int32_t(warp * 32u + lane), f = (s.u0 + u) * kUnit + col;
+                    if (col >= 64 && u + 1 >= s.n) continue;   // uniform over the warp
+                    const bool inside = f < a.F;
+                    float b_gate = 0.f, b_up = 0.f;
+                    if (inside && a.b1 != nullptr) {
+                        const float* b1 = a.b1 + int64_t(s.expert) * a.F * NG;
+                        b_gate = __ldg(b1 + f);
+                        if (NG == 2) b_up = __ldg(b1 + a.F + f);
+                    }
+                    const uint32_t acc = acc0 + uint32_t(u - g0) / 2u * NG * t_pad;
+                    // Row t of the 64-column block: 16-byte chunks swizzled by t % 8.
+                    const uint32_t blk = h_base + uint32_t(u + col / 64) * h_block, c8 = uint32_t(col % 64) / 8u;
                     for (uint32_t t = 0; t < t_pad; t += 16) {
                         uint32_t r[16], r2[16];
                         ptx::tmem_ld_32x32b_x16(acc + t, r);
@@ -522,12 +570,13 @@ __global__ void __launch_bounds__(kThreads, 1) moe_expert_kernel(const __grid_co
             // Parts of y: lane = output column, TMEM column = token.
             const int32_t count = __popcll(mask);
             float* out = P.parts + (int64_t(tb.base[s.index]) + int64_t(s.part - tb.first[s.index]) * count) * a.D;
-            for (int32_t dt = 0; ok && dt < d_tiles; ++dt) {
+            for (int32_t d0 = 0; ok && d0 < a.D; d0 += 128 * kWide) {
                 const uint32_t acc = acc_wait();
                 if (!ok) break;
 #pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    const int32_t d = (dt * NG + g) * 128 + int32_t(warp * 32u + lane);
+                for (int g = 0; g < kWide; ++g) {
+                    const int32_t d = d0 + g * 128 + int32_t(warp * 32u + lane);
+                    if (d0 + g * 128 >= a.D) break;
                     float* o = out + d;
                     for (uint32_t t = 0; t < t_pad; t += 16) {
                         const uint32_t bits = uint32_t(mask >> t) & 0xFFFFu;
@@ -553,12 +602,16 @@ __global__ void __launch_bounds__(kThreads, 1) moe_expert_kernel(const __grid_co
     __syncthreads();
     if (*abort_flag && warp == 4 && lane == 0)
         // Stages registered but not consumed: their loads have to land first.
-        for (uint32_t j = issued > S ? issued - S : 0u; j < issued; ++j)
+    {
+        for (uint32_t j = ring.count > S ? ring.count - S : 0u; j < ring.count; ++j)
             mbar_wait_drain(ptx::smem_addr(full + j % S), (j / S) & 1u, P.ctl.timeout_ns);
+        for (uint32_t j = xring.count > kXStages ? xring.count - kXStages : 0u; j < xring.count; ++j)
+            mbar_wait_drain(ptx::smem_addr(x_full + j % kXStages), (j / kXStages) & 1u, P.ctl.timeout_ns);
+    }
     __syncthreads();
     if (warp == 5) {
         ptx::tc_fence_after_sync();
-        ptx::tmem_dealloc(tmem, 256);
+        ptx::tmem_dealloc(tmem, tmem_cols);
     }
 }
 
@@ -619,7 +672,7 @@ void* expert_kernel(int act) {
 }
 
 struct ExpertPlan {
-    int32_t t_pad, units, max_units, stages, groups;
+    int32_t t_pad, units, max_units, stages, ksub;
     size_t smem;
     int64_t max_rows;              // of the parts' buffer, whatever the routing
 };
@@ -628,17 +681,19 @@ ExpertPlan plan_experts(const MoeArgs& a, const LibCtx& c) {
     ExpertPlan p;
     p.t_pad = int32_t(cdiv(a.T, 16) * 16);
     p.units = int32_t(cdiv(a.F, kUnit));
-    p.groups = a.gated ? 2 : 1;
     const int64_t budget = int64_t(c.smem_optin) - 1024 - 10 * 1024;   // alignment; tables and barriers
-    const int64_t stage = p.groups * int64_t(kGroupBytes) + p.t_pad * 128, block = p.t_pad * 128;
+    const int64_t block = p.t_pad * 128, slice = 2 * int64_t(kSliceBytes);
     const int64_t experts = std::min<int64_t>(a.E, int64_t(a.T) * a.top_k);
     // Room for a part's hidden columns if every expert that can be chosen is,
-    // as long as a ring of about 100 KiB remains.
+    // as long as a ring of 80 KiB remains beside it.
     const int64_t want = cdiv(experts * p.units, c.sm_count);
-    const int64_t ring = cdiv(100 * 1024, stage) * stage;
-    p.max_units = int32_t(std::max<int64_t>(1, std::min(want, (budget - ring) / block)));
-    p.stages = int32_t(std::min<int64_t>(kMaxStages, (budget - p.max_units * block) / stage));
-    p.smem = size_t(1024 + p.max_units * block + p.stages * stage);
+    const int64_t xring = int64_t(kXStages) * block;
+    p.max_units = int32_t(std::max<int64_t>(1, std::min(want, (budget - xring - 80 * 1024) / block)));
+    // Stages of 128 weight rows where four of them fit, else of 64: a stage
+    // costs its handshakes, whatever its size.
+    p.ksub = (budget - p.max_units * block - 2 * xring) / (2 * slice) >= 4 ? 2 : 1;
+    p.stages = int32_t(std::min<int64_t>(kMaxStages, (budget - p.max_units * block - p.ksub * xring) / (p.ksub * slice)));
+    p.smem = size_t(1024 + p.max_units * block + p.ksub * xring + p.stages * p.ksub * slice);
     // Rows: an expert's tokens times the parts it meets.  x chosen experts
     // share at most parts + x - 1 meetings, no expert has more than T tokens,
     // and the pairs are T * top_k: largest with as few experts as can be.
@@ -689,19 +744,21 @@ int launch_moe(const MoeArgs& a, void* scratch, const LibCtx& c, cudaStream_t st
     const uint64_t s1[2] = {uint64_t(F1) * 2, uint64_t(F1) * uint64_t(a.D) * 2};
     const uint64_t d2[3] = {uint64_t(a.D), uint64_t(a.F), uint64_t(a.E)};
     const uint64_t s2[2] = {uint64_t(a.D) * 2, uint64_t(a.F) * uint64_t(a.D) * 2};
-    const uint32_t bx[2] = {64, uint32_t(plan.t_pad)}, bw[3] = {64, 64, 1};
+    const uint32_t bx[2] = {64, uint32_t(plan.t_pad)}, bw[3] = {64, 64u * uint32_t(plan.ksub), 1},
+                   bh[3] = {64, 64, 1};
     const auto bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
     int r;
     if ((r = encode_tensor_map(&P.mapX, bf, 2, a.X, xd, xs, bx, sw, "X")) != GBR_OK ||
         (r = encode_tensor_map(&P.mapW1, bf, 3, a.W1, d1, s1, bw, sw, "W1")) != GBR_OK ||
-        (r = encode_tensor_map(&P.mapW2, bf, 3, a.W2, d2, s2, bw, sw, "W2")) != GBR_OK)
+        (r = encode_tensor_map(&P.mapW2, bf, 3, a.W2, d2, s2, bw, sw, "W2")) != GBR_OK ||
+        (r = encode_tensor_map(&P.mapW2half, bf, 3, a.W2, d2, s2, bh, sw, "W2")) != GBR_OK)
         return r;
     P.a = a;
     P.pairs = static_cast<PairParts*>(scratch);
     P.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) +
                                        up256(size_t(a.T) * a.top_k * sizeof(PairParts)));
-    P.t_pad = plan.t_pad, P.units = plan.units, P.max_units = plan.max_units, P.stages = plan.stages;
+    P.t_pad = plan.t_pad, P.units = plan.units, P.max_units = plan.max_units, P.stages = plan.stages, P.ksub = plan.ksub;
     P.sms = c.sm_count;
     P.ctl = c.ctl;
 
