@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const MoeArg
     const bf16* x = static_cast<const bf16*>(a.X);
     float acc[TB] = {};
     if (e < a.E) {
-#pragma unroll 4
+#pragma unroll 8
         for (int d = d0 + ty; d < d1; d += ny) {
             const float w = __ldg(a.Wr + int64_t(d) * a.E + e);
 #pragma unroll
@@ -181,16 +181,25 @@ struct ExpertParams {
     KernelCtl ctl;
 };
 
-// The cut of the list of units, the same in every CTA.
+// floor(a b / c), in 32 bits where the product fits.
+__device__ __forceinline__ int32_t mul_div(int32_t a, int32_t b, int32_t c) {
+    const uint64_t p = uint64_t(uint32_t(a)) * uint32_t(b);
+    return int32_t((p >> 32) == 0 ? uint32_t(p) / uint32_t(c) : uint32_t(p / uint32_t(c)));
+}
+
+// The cut of the list of units, the same in every CTA.  It is made in grains
+// of one unit, or of two where that leaves the largest part no larger: two
+// units fill a 128-column tile, one costs the tensor core as much.
 struct Cut {
-    int32_t total;                                      // units of all chosen experts
+    int32_t grain;                                      // units
+    int32_t per_expert;                                 // grains of an expert
+    int32_t total;                                      // grains of all chosen experts
     int32_t parts;
-    __device__ __forceinline__ int32_t begin(int32_t v) const {
-        return int32_t(int64_t(v) * total / parts);
-    }
-    // The part that holds unit u: the last v with begin(v) <= u.
+    __device__ __forceinline__ int32_t begin(int32_t v) const { return mul_div(v, total, parts); }
+    // The part that holds grain u: the last v with begin(v) <= u.
     __device__ __forceinline__ int32_t part_of(int32_t u) const {
-        return int32_t(((int64_t(u) + 1) * parts + total - 1) / total) - 1;
+        const uint64_t p = (uint64_t(uint32_t(u)) + 1) * uint32_t(parts) + uint32_t(total) - 1;
+        return int32_t((p >> 32) == 0 ? uint32_t(p) / uint32_t(total) : uint32_t(p / uint32_t(total))) - 1;
     }
 };
 
@@ -216,46 +225,51 @@ __device__ __forceinline__ int32_t warp_exclusive(int32_t v, uint32_t lane, int3
 
 __device__ __forceinline__ Cut make_cut(const ExpertParams& P, int32_t active) {
     Cut c;
-    c.total = active * P.units;
-    const int32_t per = (c.total + P.sms - 1) / P.sms;
+    const int32_t twos = (P.units + 1) / 2;
+    const int32_t per1 = (active * P.units + P.sms - 1) / P.sms, per2 = 2 * ((active * twos + P.sms - 1) / P.sms);
+    c.grain = P.max_units >= 2 && per2 <= per1 ? 2 : 1;
+    c.per_expert = c.grain == 2 ? twos : P.units;
+    c.total = active * c.per_expert;
+    const int32_t per = c.grain == 2 ? per2 : per1;
     const int32_t rounds = (per + P.max_units - 1) / P.max_units;
     c.parts = min(P.sms * rounds, c.total);
     return c;
 }
 
-// Builds the tables from the router's choice (all threads of the CTA).
+// Builds the tables from the router's choice (all threads of the CTA; the
+// masks are zero already).
 __device__ __forceinline__ void build_tables(const ExpertParams& P, Tables& tb) {
     const MoeArgs& a = P.a;
-    for (int e = int(threadIdx.x); e < kMoeMaxExperts; e += kThreads) tb.mask[e] = 0;
-    __syncthreads();
     for (int i = int(threadIdx.x); i < a.T * a.top_k; i += kThreads) {
-        const int e = int(a.ids[i]);
+        const int e = int(__ldcg(a.ids + i));
         atomicOr(reinterpret_cast<unsigned long long*>(&tb.mask[e]), 1ull << (i / a.top_k));
     }
     __syncthreads();
     if (threadIdx.x < 32) {
         const uint32_t lane = threadIdx.x;
-        constexpr int kPer = kMoeMaxExperts / 32;
-        int32_t n = 0, total;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) n += tb.mask[lane * kPer + i] != 0;
-        int32_t at = warp_exclusive(n, lane, total);
-        for (int i = 0; i < kPer; ++i)
-            if (tb.mask[lane * kPer + i] != 0) tb.active[at++] = int32_t(lane) * kPer + i;
-        if (lane == 0) tb.num_active = total;
-        __syncwarp();
-        const Cut cut = make_cut(P, total);
-        int32_t rows = 0, all;
-        for (int i = 0; i < kPer; ++i) {
-            const int32_t x = int32_t(lane) * kPer + i;
-            if (x >= total) break;
-            const int32_t f = cut.part_of(x * P.units), l = cut.part_of((x + 1) * P.units - 1);
-            tb.first[x] = f;
-            tb.base[x] = rows;                          // within this lane's experts
-            rows += (l - f + 1) * __popcll(tb.mask[tb.active[x]]);
+        int32_t active = 0;
+        for (int32_t e0 = 0; e0 < a.E; e0 += 32) {      // in the order of the experts
+            const bool on = e0 + int32_t(lane) < kMoeMaxExperts && tb.mask[e0 + lane] != 0;
+            const uint32_t b = __ballot_sync(0xffffffffu, on);
+            if (on) tb.active[active + __popc(b & ((1u << lane) - 1u))] = e0 + int32_t(lane);
+            active += __popc(b);
         }
-        const int32_t before = warp_exclusive(rows, lane, all);
-        for (int i = 0; i < kPer && int32_t(lane) * kPer + i < total; ++i) tb.base[int32_t(lane) * kPer + i] += before;
+        if (lane == 0) tb.num_active = active;
+        __syncwarp();
+        const Cut cut = make_cut(P, active);
+        int32_t base = 0;
+        for (int32_t x0 = 0; x0 < active; x0 += 32) {
+            const int32_t x = x0 + int32_t(lane);
+            int32_t rows = 0, sum;
+            if (x < active) {
+                const int32_t f = cut.part_of(x * cut.per_expert), l = cut.part_of((x + 1) * cut.per_expert - 1);
+                tb.first[x] = f;
+                rows = (l - f + 1) * __popcll(tb.mask[tb.active[x]]);
+            }
+            const int32_t before = warp_exclusive(rows, lane, sum);
+            if (x < active) tb.base[x] = base + before;
+            base += sum;
+        }
     }
     __syncthreads();
 }
@@ -272,8 +286,8 @@ struct Segment {
 struct Walk {
     int32_t v, v_end, at, end;
     __device__ __forceinline__ Walk(const Cut& c, int32_t sms) {
-        v = int32_t(int64_t(blockIdx.x) * c.parts / sms);
-        v_end = int32_t(int64_t(blockIdx.x + 1) * c.parts / sms);
+        v = mul_div(int32_t(blockIdx.x), c.parts, sms);
+        v_end = mul_div(int32_t(blockIdx.x) + 1, c.parts, sms);
         at = end = 0;
         if (v < v_end) {
             at = c.begin(v);
@@ -282,12 +296,13 @@ struct Walk {
     }
     __device__ __forceinline__ bool next(const Cut& c, const Tables& tb, int32_t units, Segment& s) {
         if (v >= v_end) return false;
-        s.index = at / units;
+        s.index = at / c.per_expert;
         s.expert = tb.active[s.index];
-        s.u0 = at - s.index * units;
-        s.n = min(end - at, units - s.u0);
+        const int32_t first = at - s.index * c.per_expert, n = min(end - at, c.per_expert - first);
+        s.u0 = first * c.grain;
+        s.n = min(n * c.grain, units - s.u0);
         s.part = v;
-        at += s.n;
+        at += n;
         if (at >= end && ++v < v_end) {
             at = c.begin(v);
             end = c.begin(v + 1);
@@ -348,6 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_expert_kernel(const __grid_co
         ptx::tmem_alloc(ptx::smem_addr(&tmem_holder), tmem_cols);
         ptx::tmem_relinquish_alloc_permit();
     }
+    for (int e = int(threadIdx.x); e < kMoeMaxExperts; e += kThreads) tb.mask[e] = 0;
     ptx::tc_fence_before_sync();
     __syncthreads();
     ptx::tc_fence_after_sync();
@@ -355,24 +371,6 @@ __global__ void __launch_bounds__(kThreads, 1) moe_expert_kernel(const __grid_co
     ptx::griddep_wait();
     build_tables(P, tb);
     const Cut cut = make_cut(P, tb.num_active);
-    if (blockIdx.x == 0) {
-        for (int i = int(threadIdx.x); i < a.T * a.top_k; i += kThreads) {
-            const int e = int(a.ids[i]), t = i / a.top_k;
-            int x = 0;                                  // e's place among the chosen
-            for (int lo = 0, hi = tb.num_active; lo < hi;) {
-                x = (lo + hi) / 2;
-                if (tb.active[x] == e) break;
-                if (tb.active[x] < e) lo = x + 1;
-                else hi = x;
-            }
-            PairParts q;
-            q.row0 = tb.base[x] + __popcll(tb.mask[e] & ((1ull << t) - 1));
-            q.step = __popcll(tb.mask[e]);
-            q.count = cut.part_of((x + 1) * P.units - 1) - tb.first[x] + 1;
-            q.expert = e;
-            P.pairs[i] = q;
-        }
-    }
     const int32_t kstep = 64 * int32_t(ksub);
     Ring ring, xring;                                   // of the producer; of the MMA lane
 
@@ -507,6 +505,25 @@ __global__ void __launch_bounds__(kThreads, 1) moe_expert_kernel(const __grid_co
         mbar_wait_drain(ptx::smem_addr(&drain), 0, P.ctl.timeout_ns);
     } else if (warp < 4) {
         // ------------------------------------------------------ epilogue
+        // Where the combination finds the parts.
+        if (blockIdx.x == 0) {
+            for (int i = int(threadIdx.x); i < a.T * a.top_k; i += 128) {
+                const int e = int(a.ids[i]), t = i / a.top_k;
+                int x = 0;                                  // e's place among the chosen
+                for (int lo = 0, hi = tb.num_active; lo < hi;) {
+                    x = (lo + hi) / 2;
+                    if (tb.active[x] == e) break;
+                    if (tb.active[x] < e) lo = x + 1;
+                    else hi = x;
+                }
+                PairParts q;
+                q.row0 = tb.base[x] + __popcll(tb.mask[e] & ((1ull << t) - 1));
+                q.step = __popcll(tb.mask[e]);
+                q.count = cut.part_of((x + 1) * cut.per_expert - 1) - tb.first[x] + 1;
+                q.expert = e;
+                P.pairs[i] = q;
+            }
+        }
         uint32_t tl = 0, hn = 0;
         bool ok = true;
         auto acc_wait = [&]() -> uint32_t {
@@ -616,30 +633,33 @@ __global__ void __launch_bounds__(kThreads, 1) moe_expert_kernel(const __grid_co
 }
 
 // ------------------------------------------------------------ combination
-constexpr int kCombineThreads = 256, kCombineLanes = 8;
-
-// 128 columns of one token a CTA; 8 threads share a column's parts and are
-// added in order.
-__global__ void __launch_bounds__(kCombineThreads)
+// 128 columns of one token a CTA; L warps share the parts, whose sums are then
+// added in order.  With few tokens L is 32: a token's parts (about 150 of a
+// lone token's) are all under way at once.
+template <int L>
+__global__ void __launch_bounds__(32 * L)
     moe_combine_kernel(const MoeArgs a, const float* parts, const PairParts* pairs) {
-    __shared__ float4 red[kCombineLanes][32];
+    __shared__ float4 red[L][32];
     ptx::griddep_wait();
     const int t = int(blockIdx.y), quad = int(threadIdx.x) % 32, sl = int(threadIdx.x) / 32;
     const int d = (int(blockIdx.x) * 32 + quad) * 4;
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
     if (d < a.D) {
+        int skip = sl;                                  // this warp's first part of the next choice
         for (int k = 0; k < a.top_k; ++k) {
             const PairParts q = pairs[t * a.top_k + k];
             const float w = a.weights[t * a.top_k + k];
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (sl == 0 && a.b2 != nullptr)
-                v = __ldg(reinterpret_cast<const float4*>(a.b2 + int64_t(q.expert) * a.D + d));
             const float* p = parts + int64_t(q.row0) * a.D + d;
-#pragma unroll 8
-            for (int i = sl; i < q.count; i += kCombineLanes) {
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (skip == 0 && a.b2 != nullptr)
+                v = __ldg(reinterpret_cast<const float4*>(a.b2 + int64_t(q.expert) * a.D + d));
+            int i = skip;
+#pragma unroll 4
+            for (; i < q.count; i += L) {
                 const float4 x = __ldcg(reinterpret_cast<const float4*>(p + int64_t(i) * q.step * a.D));
                 v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
             }
+            skip = i - q.count;
             y.x = fmaf(w, v.x, y.x), y.y = fmaf(w, v.y, y.y), y.z = fmaf(w, v.z, y.z), y.w = fmaf(w, v.w, y.w);
         }
     }
@@ -647,7 +667,7 @@ __global__ void __launch_bounds__(kCombineThreads)
     __syncthreads();
     if (sl == 0 && d < a.D) {
 #pragma unroll
-        for (int i = 1; i < kCombineLanes; ++i) {
+        for (int i = 1; i < L; ++i) {
             const float4 x = red[i][quad];
             y.x += x.x, y.y += x.y, y.z += x.z, y.w += x.w;
         }
@@ -689,6 +709,7 @@ ExpertPlan plan_experts(const MoeArgs& a, const LibCtx& c) {
     const int64_t want = cdiv(experts * p.units, c.sm_count);
     const int64_t xring = int64_t(kXStages) * block;
     p.max_units = int32_t(std::max<int64_t>(1, std::min(want, (budget - xring - 80 * 1024) / block)));
+    if (p.max_units > 1) p.max_units = (p.max_units + 1) / 2 * 2;   // grains of two fit whole
     // Stages of 128 weight rows where four of them fit, else of 64: a stage
     // costs its handshakes, whatever its size.
     p.ksub = (budget - p.max_units * block - 2 * xring) / (2 * slice) >= 4 ? 2 : 1;
@@ -781,8 +802,10 @@ int launch_moe(const MoeArgs& a, void* scratch, const LibCtx& c, cudaStream_t st
         return report_cuda(e, "launching the experts");
     count_launch();
     const dim3 cg(unsigned(cdiv(a.D, 128)), unsigned(a.T));
-    e = launch_overlapped(moe_combine_kernel, cg, kCombineThreads, 1, stream, a, static_cast<const float*>(P.parts),
-                          static_cast<const PairParts*>(P.pairs));
+    const float* parts = P.parts;
+    const PairParts* pairs = P.pairs;
+    e = a.T <= 8 ? launch_overlapped(moe_combine_kernel<32>, cg, 32 * 32, 1, stream, a, parts, pairs)
+                 : launch_overlapped(moe_combine_kernel<8>, cg, 32 * 8, 1, stream, a, parts, pairs);
     if (e != cudaSuccess) return report_cuda(e, "launching the combination");
     count_launch();
     return GBR_OK;
