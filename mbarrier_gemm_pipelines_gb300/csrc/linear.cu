@@ -279,43 +279,96 @@ int run_product(Product p, const LibCtx& c, cudaStream_t stream) {
 }
 
 // ------------------------------------------------------------ dZ and dbias
-// One CTA per 32 columns: 8 rows of threads walk down the rows.
-template <int ACT>
-__global__ void __launch_bounds__(256) dz_kernel(const LinearGradArgs a) {
-    __shared__ float part[8][32];
-    ptx::griddep_wait();
-    const int n = int(blockIdx.x) * 32 + int(threadIdx.x) % 32;
-    float sum = 0.f;
-    for (int m = int(threadIdx.x) / 32; n < a.N && m < a.M; m += 8) {
-        float d = __bfloat162float(static_cast<const bf16*>(a.dC.p)[m * a.dC.ld + n]);
-        bool keep = true;
-        if (a.drop.threshold != 0) {
-            const uint4 bits = dropout_bits(a.drop, uint32_t(m), uint32_t(n / 8));
-            keep = dropout_keep(a.drop, bits, n % 8);
-            d *= a.drop.scale;
-        }
-        if (ACT != kActNone)
-            d *= act_slope<ACT>(__bfloat162float(static_cast<const bf16*>(a.Z.p)[m * a.Z.ld + n]));
-        if (!keep) d = 0.f;
-        if (a.dZ) static_cast<bf16*>(a.dZ.w())[m * a.dZ.ld + n] = __float2bfloat16_rn(d);
-        sum += d;
-    }
-    part[threadIdx.x / 32][threadIdx.x % 32] = sum;
-    __syncthreads();
-    if (threadIdx.x < 32 && n < a.N && a.dbias != nullptr) {
-        float t = 0.f;
-        for (int r = 0; r < 8; ++r) t += part[r][threadIdx.x];
-        a.dbias[n] = t;
+// dZ = drop(dC) act'(Z), and dbias = its column sums before the rounding.
+// Bound by memory: dC and Z are read and dZ is written once.  A thread stands
+// on 8 columns and walks down its rows, two at a time; a CTA is TX threads
+// along the columns and 256 / TX along the rows, and a cluster of 8 CTAs shares
+// the rows.  Sums: in a thread, then over the CTA's rows of threads, then over
+// the cluster's CTAs in rank order, so that they never depend on timing.
+constexpr int kDzThreads = 256, kDzCluster = 8, kDzRows = 2;
+
+__device__ __forceinline__ void load8_any(const bf16* p, int32_t left, bool vec, float (&v)[8]) {
+    if (vec && left >= 8) {
+        load8(p, v);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = j < left ? __bfloat162float(p[j]) : 0.f;
     }
 }
 
+template <int ACT, int TX>
+__global__ void __launch_bounds__(kDzThreads) dz_kernel(const LinearGradArgs a, uint32_t vec) {
+    __shared__ float part[kDzThreads / TX][TX * 8];
+    ptx::griddep_wait();
+    const uint32_t rank = ptx::cluster_ctarank();
+    const int32_t tx = int32_t(threadIdx.x) % TX, ty = int32_t(threadIdx.x) / TX;
+    const int32_t c = (int32_t(blockIdx.x / kDzCluster) * TX + tx) * 8, left = a.N - c;
+    constexpr int32_t kPer = kDzThreads / TX;
+    const int32_t r0 = int32_t(int64_t(a.M) * rank / kDzCluster), r1 = int32_t(int64_t(a.M) * (rank + 1) / kDzCluster);
+    const bf16 *dC = static_cast<const bf16*>(a.dC.p) + c, *Z = static_cast<const bf16*>(a.Z.p) + c;
+    bf16* dZ = static_cast<bf16*>(a.dZ.w());
+    float sum[8] = {};
+    for (int64_t r = r0 + ty; left > 0 && r < r1; r += kPer * kDzRows) {
+        float d[kDzRows][8], z[kDzRows][8];
+#pragma unroll
+        for (int i = 0; i < kDzRows; ++i) {
+            const int64_t row = r + i * kPer;
+            if (row >= r1) continue;
+            load8_any(dC + row * a.dC.ld, left, vec != 0, d[i]);
+            if (ACT != kActNone) load8_any(Z + row * a.Z.ld, left, vec != 0, z[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < kDzRows; ++i) {
+            const int64_t row = r + i * kPer;
+            if (row >= r1) continue;
+            if (ACT != kActNone)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) d[i][j] *= act_slope<ACT>(z[i][j]);
+            if (a.drop.threshold != 0) {
+                const uint4 bits = dropout_bits(a.drop, uint32_t(row), uint32_t(c / 8));
+#pragma unroll
+                for (int j = 0; j < 8; ++j) d[i][j] = dropout_keep(a.drop, bits, j) ? d[i][j] * a.drop.scale : 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum[j] += d[i][j];
+            // dZ is this library's scratch: 16-byte aligned rows, padded to 8 columns.
+            if (dZ != nullptr) store8(dZ + row * a.dZ.ld + c, d[i]);
+        }
+    }
+    if (a.dbias == nullptr) return;                     // uniform over the cluster
+#pragma unroll
+    for (int j = 0; j < 8; ++j) part[ty][tx * 8 + j] = sum[j];
+    __syncthreads();
+    for (int32_t j = int32_t(threadIdx.x); j < TX * 8; j += kDzThreads) {
+        float t = 0.f;
+#pragma unroll
+        for (int y = 0; y < kPer; ++y) t += part[y][j];
+        part[0][j] = t;
+    }
+    ptx::cluster_sync_all();
+    // Each CTA finishes one eighth of the columns.
+    constexpr int32_t kShare = TX * 8 / kDzCluster;
+    const int32_t j = int32_t(rank) * kShare + int32_t(threadIdx.x);
+    const int32_t n = int32_t(blockIdx.x / kDzCluster) * TX * 8 + j;
+    if (int32_t(threadIdx.x) < kShare && n < a.N) {
+        const uint32_t at = ptx::smem_addr(&part[0][j]);
+        float t = 0.f;
+#pragma unroll
+        for (uint32_t s = 0; s < kDzCluster; ++s)
+            t += __uint_as_float(ptx::ld_shared_cluster_u32(ptx::mapa_shared(at, s)));
+        a.dbias[n] = t;
+    }
+    ptx::cluster_sync_all();   // the peers' sums have been read
+}
+
+template <int TX>
 void* dz_kernel_ptr(int act) {
     switch (act) {
-        case kActRelu: return reinterpret_cast<void*>(&dz_kernel<kActRelu>);
-        case kActGelu: return reinterpret_cast<void*>(&dz_kernel<kActGelu>);
-        case kActGeluTanh: return reinterpret_cast<void*>(&dz_kernel<kActGeluTanh>);
-        case kActSilu: return reinterpret_cast<void*>(&dz_kernel<kActSilu>);
-        default: return reinterpret_cast<void*>(&dz_kernel<kActNone>);
+        case kActRelu: return reinterpret_cast<void*>(&dz_kernel<kActRelu, TX>);
+        case kActGelu: return reinterpret_cast<void*>(&dz_kernel<kActGelu, TX>);
+        case kActGeluTanh: return reinterpret_cast<void*>(&dz_kernel<kActGeluTanh, TX>);
+        case kActSilu: return reinterpret_cast<void*>(&dz_kernel<kActSilu, TX>);
+        default: return reinterpret_cast<void*>(&dz_kernel<kActNone, TX>);
     }
 }
 
@@ -334,10 +387,15 @@ int launch_linear(const LinearArgs& a, const LibCtx& c, cudaStream_t stream) {
     return run_product(p, c, stream);
 }
 
-int launch_linear_dz(const LinearGradArgs& a, const LibCtx&, cudaStream_t stream) {
+int launch_linear_dz(const LinearGradArgs& a, const LibCtx& c, cudaStream_t stream) {
     LinearGradArgs arg = a;
-    void* args[] = {&arg};
-    const cudaError_t e = launch_kernel(dz_kernel_ptr(a.act), dim3(unsigned(cdiv(a.N, 32))), 256, 0, 1, args, stream);
+    uint32_t vec = vec16(a.dC) && vec16(a.Z);
+    void* args[] = {&arg, &vec};
+    // 256 columns a CTA where that gives every SM a few CTAs, else 64.
+    const bool wide = cdiv(a.N, 256) * kDzCluster >= 2 * int64_t(c.sm_count);
+    const int64_t tiles = cdiv(a.N, wide ? 256 : 64);
+    const cudaError_t e = launch_kernel(wide ? dz_kernel_ptr<32>(a.act) : dz_kernel_ptr<8>(a.act),
+                                        dim3(unsigned(tiles * kDzCluster)), kDzThreads, 0, kDzCluster, args, stream);
     if (e != cudaSuccess) return report_cuda(e, "launching the gradient's dZ");
     count_launch();
     return GBR_OK;
