@@ -57,18 +57,19 @@ template <int ACT>
 __device__ __forceinline__ float act_slope(float z) {
     if (ACT == kActRelu) return z > 0.f ? 1.f : 0.f;
     if (ACT == kActNone) return 1.f;
-    if (z > kActTail) return 1.f;
-    if (z < -kActTail) return 0.f;
+    float d;
     if (ACT == kActGelu) {
         const float e = __expf(-0.5f * z * z);
-        return fmaf(z * kInvSqrt2Pi, e, normal_cdf(z, e));
-    }
-    if (ACT == kActGeluTanh) {
+        d = fmaf(z * kInvSqrt2Pi, e, normal_cdf(z, e));
+    } else if (ACT == kActGeluTanh) {
         const float s = logistic(2.f * kSqrt2OverPi * (z + kGeluCubic * z * z * z));
-        return s + 2.f * z * s * (1.f - s) * kSqrt2OverPi * (1.f + 3.f * kGeluCubic * z * z);
+        d = s + 2.f * z * s * (1.f - s) * kSqrt2OverPi * (1.f + 3.f * kGeluCubic * z * z);
+    } else {
+        const float q = logistic(z);
+        d = q + z * q * (1.f - q);
     }
-    const float q = logistic(z);
-    return q + z * q * (1.f - q);
+    d = z > kActTail ? 1.f : d;
+    return z < -kActTail ? 0.f : d;
 }
 
 // The same with the activation as a run-time value (uniform over the launch).

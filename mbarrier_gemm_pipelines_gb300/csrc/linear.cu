@@ -111,12 +111,37 @@ int check_split(void* kernel) {
         cudaFuncAttributes fa;
         const cudaError_t e = cudaFuncGetAttributes(&fa, kernel);
         if (e != cudaSuccess) return report_cuda(e, "cudaFuncGetAttributes(linear)");
-        const bool ok = long(fa.numRegs) * linear::kThreads >= 128L * (linear::kRegsWG0 + linear::kRegsWG1);
+        const bool ok = long(fa.numRegs) * linear::kThreads >= 128L * (linear::kRegsRoles + 2 * linear::kRegsEpilogue);
         it = known.emplace(kernel, ok).first;
     }
     if (!it->second)
         return report_errorf(GBR_ERR_CUDA, "a linear kernel was built with too few registers for its role split");
     return GBR_OK;
+}
+
+// The tiles of a product on `units` CTA pairs.  The last round is split where
+// it has tiles for at most half of the pairs and half a tile's products are
+// worth more than the exchange of the parts (about 5 us: 16 k-blocks of 128).
+linear::PairWork pair_work(const Product& p, int64_t units) {
+    linear::PairWork w;
+    memset(&w, 0, sizeof(w));
+    w.m_tiles = int32_t(cdiv(p.I, linear::kTile));
+    w.n_tiles = int32_t(cdiv(p.J, linear::kTile));
+    w.num_tiles = int32_t(std::min<int64_t>(int64_t(w.m_tiles) * w.n_tiles, INT32_MAX));
+    w.num_kb = int32_t(cdiv(p.Kc, 64 * linear::kSlices));
+    w.group_m = 8;
+    const int64_t rest = w.num_tiles % units;
+    if (2 * rest <= units && w.num_kb / 2 >= 16) w.split = int32_t(rest);
+    w.whole = w.num_tiles - w.split;
+    return w;
+}
+
+// Zeroes words in the order of the stream, without a memset between kernels
+// that overlap their launches.
+__global__ void __launch_bounds__(256) zero_kernel(uint32_t* p, int32_t words) {
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+    for (int32_t i = int32_t(blockIdx.x * 256 + threadIdx.x); i < words; i += int32_t(gridDim.x) * 256) p[i] = 0;
 }
 
 int run_pair(const Product& p, const LibCtx& c, cudaStream_t stream) {
@@ -139,20 +164,34 @@ int run_pair(const Product& p, const LibCtx& c, cudaStream_t stream) {
     P.has_r = bool(p.R);
     P.bias = p.bias;
     P.M = p.I, P.N = p.J;
-    P.m_tiles = int32_t(cdiv(p.I, linear::kTile));
-    P.n_tiles = int32_t(cdiv(p.J, linear::kTile));
-    const int64_t tiles = int64_t(P.m_tiles) * P.n_tiles;
+    P.bias_vec = reinterpret_cast<uintptr_t>(p.bias) % 16 == 0;
+    const int64_t tiles = cdiv(p.I, linear::kTile) * cdiv(p.J, linear::kTile);
     if (tiles >= (int64_t(1) << 31)) return report_errorf(GBR_ERR_INVALID, "linear: too many output tiles");
-    P.num_tiles = int32_t(tiles);
-    P.num_kb = int32_t(cdiv(p.Kc, 64 * linear::kSlices));
-    P.group_m = 8;
+    const int64_t units = c.sm_count / 2;
+    P.w = pair_work(p, units);
+    Scratch ws(c, stream);
+    if (P.w.split > 0) {
+        const size_t counts = (linear::pair_count_bytes(P.w.split) + 255) & ~size_t(255);
+        void* q;
+        if ((r = ws.take(counts + linear::pair_part_bytes(P.w.split), "cudaMallocFromPoolAsync(split tiles)", &q)) !=
+            GBR_OK)
+            return r;
+        P.w.count = static_cast<uint32_t*>(q);
+        P.w.parts = reinterpret_cast<float4*>(static_cast<uint8_t*>(q) + counts);
+        int32_t words = int32_t(counts / 4);
+        void* zargs[] = {&P.w.count, &words};
+        const cudaError_t e =
+            launch_kernel(reinterpret_cast<void*>(&zero_kernel), dim3(1), 256, 0, 1, zargs, stream);
+        if (e != cudaSuccess) return report_cuda(e, "launching the zeroing of the split tiles' counts");
+        count_launch();
+    }
     P.drop = p.drop;
     P.ctl = c.ctl;
     if ((r = check_split(p.pair_kernel)) != GBR_OK || (r = raise_kernel_smem(p.pair_kernel, linear::kSmemBytes, c.device)) != GBR_OK)
         return r;
-    const int64_t units = std::min<int64_t>(c.sm_count / 2, tiles);
     void* args[] = {&P};
-    const cudaError_t e = launch_kernel(p.pair_kernel, dim3(unsigned(2 * units)), linear::kThreads, linear::kSmemBytes, 2,
+    const int64_t busy = std::min<int64_t>(units, P.w.whole > 0 && P.w.split > 0 ? units : P.w.whole + 2 * P.w.split);
+    const cudaError_t e = launch_kernel(p.pair_kernel, dim3(unsigned(2 * busy)), linear::kThreads, linear::kSmemBytes, 2,
                                        args, stream);
     if (e != cudaSuccess) return report_cuda(e, "launching a linear kernel");
     count_launch();
@@ -180,8 +219,10 @@ struct TilePlan {
 // 2048 x 1024 x 1024 10.3 / 11.7; dB of 4096 x 512 x 512 10.8 / 23, of
 // 512 x 4096 x 4096 33.6 / 18.
 double pair_cycles(const Product& p, int sms) {
-    const int64_t rounds = cdiv(cdiv(p.I, linear::kTile) * cdiv(p.J, linear::kTile), sms / 2);
-    return 11500.0 + double(rounds) * double(cdiv(p.Kc, 64)) * (rounds == 1 ? 640.0 : 512.0);
+    const linear::PairWork w = pair_work(p, sms / 2);
+    const double whole = double(cdiv(w.whole, sms / 2)), half = w.split > 0 ? 0.5 : 0.0;
+    return 11500.0 + (w.split > 0 ? 8000.0 : 0.0) +
+           (whole + half) * double(cdiv(p.Kc, 64)) * (whole + half <= 1.0 ? 640.0 : 512.0);
 }
 
 TilePlan plan_tile(const Product& p, int sms) {
@@ -285,19 +326,12 @@ int run_product(Product p, const LibCtx& c, cudaStream_t stream) {
 // along the columns and 256 / TX along the rows, and a cluster of 8 CTAs shares
 // the rows.  Sums: in a thread, then over the CTA's rows of threads, then over
 // the cluster's CTAs in rank order, so that they never depend on timing.
-constexpr int kDzThreads = 256, kDzCluster = 8, kDzRows = 2;
+constexpr int kDzThreads = 256, kDzCluster = 8, kDzRows = 4;
 
-__device__ __forceinline__ void load8_any(const bf16* p, int32_t left, bool vec, float (&v)[8]) {
-    if (vec && left >= 8) {
-        load8(p, v);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = j < left ? __bfloat162float(p[j]) : 0.f;
-    }
-}
-
-template <int ACT, int TX>
-__global__ void __launch_bounds__(kDzThreads) dz_kernel(const LinearGradArgs a, uint32_t vec) {
+// VEC: rows of dC and Z start on 16 bytes.  The loads of kDzRows rows are
+// issued, as raw 16 bytes, before the first is used.
+template <int ACT, int TX, bool VEC>
+__global__ void __launch_bounds__(kDzThreads) dz_kernel(const LinearGradArgs a) {
     __shared__ float part[kDzThreads / TX][TX * 8];
     ptx::griddep_wait();
     const uint32_t rank = ptx::cluster_ctarank();
@@ -307,32 +341,43 @@ __global__ void __launch_bounds__(kDzThreads) dz_kernel(const LinearGradArgs a, 
     const int32_t r0 = int32_t(int64_t(a.M) * rank / kDzCluster), r1 = int32_t(int64_t(a.M) * (rank + 1) / kDzCluster);
     const bf16 *dC = static_cast<const bf16*>(a.dC.p) + c, *Z = static_cast<const bf16*>(a.Z.p) + c;
     bf16* dZ = static_cast<bf16*>(a.dZ.w());
+    const bool whole = VEC && left >= 8;
     float sum[8] = {};
-    for (int64_t r = r0 + ty; left > 0 && r < r1; r += kPer * kDzRows) {
-        float d[kDzRows][8], z[kDzRows][8];
+    if (left > 0) {
+        for (int64_t r = r0 + ty; r < r1; r += kPer * kDzRows) {
+            uint4 rd[kDzRows], rz[kDzRows];
 #pragma unroll
-        for (int i = 0; i < kDzRows; ++i) {
-            const int64_t row = r + i * kPer;
-            if (row >= r1) continue;
-            load8_any(dC + row * a.dC.ld, left, vec != 0, d[i]);
-            if (ACT != kActNone) load8_any(Z + row * a.Z.ld, left, vec != 0, z[i]);
-        }
-#pragma unroll
-        for (int i = 0; i < kDzRows; ++i) {
-            const int64_t row = r + i * kPer;
-            if (row >= r1) continue;
-            if (ACT != kActNone)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) d[i][j] *= act_slope<ACT>(z[i][j]);
-            if (a.drop.threshold != 0) {
-                const uint4 bits = dropout_bits(a.drop, uint32_t(row), uint32_t(c / 8));
-#pragma unroll
-                for (int j = 0; j < 8; ++j) d[i][j] = dropout_keep(a.drop, bits, j) ? d[i][j] * a.drop.scale : 0.f;
+            for (int i = 0; i < kDzRows; ++i) {
+                const int64_t row = r + i * kPer;
+                rd[i] = rz[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (row < r1) {
+                    rd[i] = whole ? *reinterpret_cast<const uint4*>(dC + row * a.dC.ld) : load8_raw(dC + row * a.dC.ld, left);
+                    if (ACT != kActNone)
+                        rz[i] = whole ? *reinterpret_cast<const uint4*>(Z + row * a.Z.ld) : load8_raw(Z + row * a.Z.ld, left);
+                }
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum[j] += d[i][j];
-            // dZ is this library's scratch: 16-byte aligned rows, padded to 8 columns.
-            if (dZ != nullptr) store8(dZ + row * a.dZ.ld + c, d[i]);
+            for (int i = 0; i < kDzRows; ++i) {
+                const int64_t row = r + i * kPer;
+                if (row < r1) {
+                    float d[8], z[8];
+                    unpack8(rd[i], d);
+                    if (ACT != kActNone) {
+                        unpack8(rz[i], z);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) d[j] *= act_slope<ACT>(z[j]);
+                    }
+                    if (a.drop.threshold != 0) {
+                        const uint4 bits = dropout_bits(a.drop, uint32_t(row), uint32_t(c / 8));
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) d[j] = dropout_keep(a.drop, bits, j) ? d[j] * a.drop.scale : 0.f;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) sum[j] += d[j];
+                    // dZ is this library's scratch: 16-byte aligned rows, padded to 8 columns.
+                    if (dZ != nullptr) store8(dZ + row * a.dZ.ld + c, d);
+                }
+            }
         }
     }
     if (a.dbias == nullptr) return;                     // uniform over the cluster
@@ -361,14 +406,14 @@ __global__ void __launch_bounds__(kDzThreads) dz_kernel(const LinearGradArgs a, 
     ptx::cluster_sync_all();   // the peers' sums have been read
 }
 
-template <int TX>
+template <int TX, bool VEC>
 void* dz_kernel_ptr(int act) {
     switch (act) {
-        case kActRelu: return reinterpret_cast<void*>(&dz_kernel<kActRelu, TX>);
-        case kActGelu: return reinterpret_cast<void*>(&dz_kernel<kActGelu, TX>);
-        case kActGeluTanh: return reinterpret_cast<void*>(&dz_kernel<kActGeluTanh, TX>);
-        case kActSilu: return reinterpret_cast<void*>(&dz_kernel<kActSilu, TX>);
-        default: return reinterpret_cast<void*>(&dz_kernel<kActNone, TX>);
+        case kActRelu: return reinterpret_cast<void*>(&dz_kernel<kActRelu, TX, VEC>);
+        case kActGelu: return reinterpret_cast<void*>(&dz_kernel<kActGelu, TX, VEC>);
+        case kActGeluTanh: return reinterpret_cast<void*>(&dz_kernel<kActGeluTanh, TX, VEC>);
+        case kActSilu: return reinterpret_cast<void*>(&dz_kernel<kActSilu, TX, VEC>);
+        default: return reinterpret_cast<void*>(&dz_kernel<kActNone, TX, VEC>);
     }
 }
 
@@ -389,12 +434,12 @@ int launch_linear(const LinearArgs& a, const LibCtx& c, cudaStream_t stream) {
 
 int launch_linear_dz(const LinearGradArgs& a, const LibCtx& c, cudaStream_t stream) {
     LinearGradArgs arg = a;
-    uint32_t vec = vec16(a.dC) && vec16(a.Z);
-    void* args[] = {&arg, &vec};
-    // 256 columns a CTA where that gives every SM a few CTAs, else 64.
-    const bool wide = cdiv(a.N, 256) * kDzCluster >= 2 * int64_t(c.sm_count);
-    const int64_t tiles = cdiv(a.N, wide ? 256 : 64);
-    const cudaError_t e = launch_kernel(wide ? dz_kernel_ptr<32>(a.act) : dz_kernel_ptr<8>(a.act),
+    const bool vec = vec16(a.dC) && vec16(a.Z);
+    void* args[] = {&arg};
+    // 128 columns a CTA (4096 x 14336, GELU, 8 / 16 / 32 threads along the columns: 95 / 94 / 101 us).
+    constexpr int kTx = 16;
+    const int64_t tiles = cdiv(a.N, kTx * 8);
+    const cudaError_t e = launch_kernel(vec ? dz_kernel_ptr<kTx, true>(a.act) : dz_kernel_ptr<kTx, false>(a.act),
                                         dim3(unsigned(tiles * kDzCluster)), kDzThreads, 0, kDzCluster, args, stream);
     if (e != cudaSuccess) return report_cuda(e, "launching the gradient's dZ");
     count_launch();

@@ -14,11 +14,19 @@
 // CTA and 64-k slice either way, and the matrix descriptors and the
 // instruction descriptor's transpose bits say which.  No operand is copied.
 //
-// Epilogue, per warp 32 rows x 64 columns at a time:
+// Epilogue, 8 warps, each 32 rows x 128 columns of a tile, 64 columns at a time:
 //   tcgen05.ld -> + bias -> (Z: round, stage, TMA store) -> activation ->
 //   dropout -> + residual -> round, stage, TMA store
-// The residual's 4 KiB arrive by TMA in the very staging slot that the result
-// then overwrites, one chunk ahead; two slots a warp.
+// through one 4 KiB staging slot a warp; the residual arrives by TMA in the
+// very slot that the result then overwrites.  Two warps a scheduler, not one:
+// with 4 warps the GELU of a tile took longer than the next tile's products
+// (4096 x 4096 x 14336 with Z: 324 us against 254 without activation).
+//
+// Split tail: where the last, partial round has tiles for at most half of the
+// pairs, each of those tiles is cut in two along K and given to two pairs.  A
+// part goes to scratch; whoever finishes second adds the other's part to its
+// own accumulator and runs the epilogue.  Nobody waits, and since a + b = b + a
+// the result does not depend on who was second.
 #pragma once
 #include "gemm_umma.cuh"
 #include "operators.h"
@@ -28,9 +36,6 @@ namespace linear {
 
 using umma::kAccCols;
 using umma::kEpiBufBytes;
-using umma::kRegsWG0;
-using umma::kRegsWG1;
-using umma::kThreads;
 using umma::kTmemCols;
 using umma::sw128_desc;
 
@@ -39,16 +44,60 @@ constexpr uint32_t kStages = 3, kSlices = 2;           // 64-k slices per ring s
 constexpr uint32_t kSliceBytes = 128 * 128;            // one operand, one CTA, 64 k
 constexpr uint32_t kStageBytes = 2 * kSlices * kSliceBytes;
 constexpr uint32_t kPanelBytes = 64 * 128;
-constexpr uint32_t kBiasBytes = 4 * 64 * 4;            // 64 columns for each epilogue warp
 constexpr uint32_t kBarBytes = 256;
-constexpr size_t kSmemBytes = 1024 + kStages * kStageBytes + kUmmaEpiBytes + kBarBytes + kBiasBytes;
+constexpr size_t kSmemBytes = 1024 + kStages * kStageBytes + kUmmaEpiBytes + kBarBytes;
+constexpr int kThreads = 384;                          // 4 warps of roles, 8 of the epilogue
+constexpr uint32_t kEpiWarps = 8;
+static_assert(kEpiWarps * kEpiBufBytes == kUmmaEpiBytes, "one staging slot a warp");
+// Registers a thread: 72 + 216 + 216 = 3 x 168, what the launch has.
+constexpr uint32_t kRegsRoles = 72, kRegsEpilogue = 216;
+// fp32 parts of split tiles: per tile, part, CTA of the pair and warp 32 rows x
+// 128 columns as [column / 4][row] float4; before them one arrival count per
+// tile, CTA and warp, zeroed.
+constexpr int64_t kPartVecs = 32 * 32;
+inline size_t pair_count_bytes(int64_t split_tiles) { return size_t(split_tiles) * 2 * kEpiWarps * 4; }
+inline size_t pair_part_bytes(int64_t split_tiles) { return size_t(split_tiles) * 4 * kEpiWarps * kPartVecs * 16; }
+
+// The work of a product on `units` pairs: tiles 0 .. whole - 1 in rounds, then
+// (if split > 0) the last `split` tiles in halves.
+struct PairWork {
+    int32_t m_tiles, n_tiles, num_tiles, num_kb, group_m;
+    int32_t whole, split;
+    uint32_t* count;
+    float4* parts;
+};
+
+struct PairItem {
+    uint32_t tile;
+    int32_t kb0, kb1;
+    int32_t part;                                      // 0 or 1 of a split tile, -1: whole
+    int32_t sk;                                        // split tile
+};
+
+// Item j of a pair; every role walks the same sequence.
+__device__ __forceinline__ bool pair_item(const PairWork& w, uint32_t unit, uint32_t units, uint32_t j, PairItem& x) {
+    x.tile = unit + j * units;
+    x.kb0 = 0;
+    x.kb1 = w.num_kb;
+    x.part = -1;
+    x.sk = 0;
+    if (x.tile < uint32_t(w.whole)) return true;
+    if (w.split == 0 || unit >= 2u * uint32_t(w.split) || j != uint32_t(w.whole) / units) return false;
+    x.sk = int32_t(unit / 2u);
+    x.tile = uint32_t(w.whole + x.sk);
+    x.part = int32_t(unit & 1u);
+    if (x.part == 0) x.kb1 = w.num_kb / 2;
+    else x.kb0 = w.num_kb / 2;
+    return true;
+}
 
 struct PairParams {
     CUtensorMap mapA, mapB, mapC, mapZ, mapR;
     const float* bias;
     int32_t M, N;                                      // of the output
-    int32_t m_tiles, n_tiles, num_tiles, num_kb, group_m;
+    PairWork w;
     uint32_t has_z, has_r;
+    uint32_t bias_vec;                                 // bias starts on 16 bytes
     Dropout drop;
     KernelCtl ctl;
 };
@@ -88,11 +137,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* acc_full = empty + kStages;
     uint64_t* acc_empty = acc_full + 2;
     uint64_t* drain = acc_empty + 2;
-    uint64_t* res_full = drain + 1;                    // [4 warps][2 slots]
+    uint64_t* res_full = drain + 1;                    // [8 warps]
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(res_full + 8);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
     uint32_t* issued_word = tmem_holder + 2;
-    float* bias_sm = reinterpret_cast<float*>(epi + kUmmaEpiBytes + kBarBytes);
 
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u;
     const uint32_t rank = ptx::cluster_ctarank();
@@ -105,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (uint32_t a = 0; a < 2; ++a) {
             ptx::mbar_init(ptx::smem_addr(acc_full + a), 1);
-            ptx::mbar_init(ptx::smem_addr(acc_empty + a), 8);
+            ptx::mbar_init(ptx::smem_addr(acc_empty + a), 2 * kEpiWarps);
         }
         ptx::mbar_init(ptx::smem_addr(drain), 1);
         for (uint32_t i = 0; i < 8; ++i) ptx::mbar_init(ptx::smem_addr(res_full + i), 1);
@@ -129,17 +177,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t issued = 0;
 
     if (warp < 4) {
-        ptx::setmaxnreg_dec<kRegsWG0>();
+        ptx::setmaxnreg_dec<kRegsRoles>();
         if (warp == 0 && lane == 0) {
             // ---------------------------------------------------- TMA producer
             const uint32_t ring_base = ptx::smem_addr(ring);
             uint32_t it = 0;
             bool ok = true;
-            for (uint32_t t = unit; ok && t < uint32_t(P.num_tiles); t += units) {
+            PairItem w;
+            for (uint32_t j = 0; ok && pair_item(P.w, unit, units, j, w); ++j) {
                 uint32_t mt, nt;
-                raster_tile(t, P.m_tiles, P.n_tiles, P.group_m, mt, nt);
+                raster_tile(w.tile, P.w.m_tiles, P.w.n_tiles, P.w.group_m, mt, nt);
                 const int32_t a0 = int32_t(mt * kTile + rank * 128), b0 = int32_t(nt * kTile + rank * 128);
-                for (int32_t kb = 0; kb < P.num_kb; ++kb, ++it) {
+                for (int32_t kb = w.kb0; kb < w.kb1; ++kb, ++it) {
                     const uint32_t slot = it % kStages, ph = (it / kStages) & 1u;
                     if (!mbar_wait<true>(ptx::smem_addr(empty + slot), ph ^ 1u, P.ctl, abort_flag,
                                          kSiteProducerEmpty, it)) {
@@ -167,14 +216,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr uint32_t idesc = pair_idesc<A_MN, B_MN>();
             uint32_t it = 0, tl = 0;
             bool ok = true;
-            for (uint32_t t = unit; ok && t < uint32_t(P.num_tiles); t += units, ++tl) {
+            PairItem w;
+            for (; ok && pair_item(P.w, unit, units, tl, w); ++tl) {
                 const uint32_t a = tl & 1u, aph = (tl >> 1) & 1u;
                 if (!mbar_wait<true>(ptx::smem_addr(acc_empty + a), aph ^ 1u, P.ctl, abort_flag,
                                      kSiteMmaAccEmpty, tl))
                     break;
                 ptx::tc_fence_after_sync();
                 const uint32_t d_tmem = tmem_base + a * kAccCols;
-                for (int32_t kb = 0; kb < P.num_kb; ++kb, ++it) {
+                for (int32_t kb = w.kb0; kb < w.kb1; ++kb, ++it) {
                     const uint32_t slot = it % kStages, ph = (it / kStages) & 1u;
                     if (!mbar_wait<true>(ptx::smem_addr(full + slot), ph, P.ctl, abort_flag,
                                          kSiteMmaFull, it)) {
@@ -189,11 +239,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (uint32_t k = 0; k < 4; ++k)
                             ptx::mma_f16_pair(d_tmem, operand_desc<A_MN>(stage + h * kSliceBytes, k),
                                               operand_desc<B_MN>(stage + (kSlices + h) * kSliceBytes, k),
-                                              idesc, (kb != 0 || h != 0 || k != 0) ? 1u : 0u);
+                                              idesc, (kb != w.kb0 || h != 0 || k != 0) ? 1u : 0u);
                     ptx::mma_commit_pair_multicast(ptx::smem_addr(empty + slot), 0x3);
                 }
                 if (!ok) break;
-                if (P.num_kb > 0) {
+                if (w.kb1 > w.kb0) {
                     ptx::mma_commit_pair_multicast(ptx::smem_addr(acc_full + a), 0x3);
                 } else {
                     ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_addr(acc_full + a), 0));
@@ -204,109 +254,133 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_wait_drain(ptx::smem_addr(drain), 0, P.ctl.timeout_ns);
         }
     } else {
-        ptx::setmaxnreg_inc<kRegsWG1>();
+        ptx::setmaxnreg_inc<kRegsEpilogue>();
         // -------------------------------------------------------- epilogue
-        const uint32_t q = warp & 3u;                  // TMEM lane quarter / row block
-        const uint32_t slot0 = ptx::smem_addr(epi) + q * 2u * kEpiBufBytes;
+        const uint32_t q = warp & 3u, ew = warp - 4u;  // TMEM lane quarter; epilogue warp
+        const int32_t col0 = ew < 4u ? 0 : 128;        // first of this warp's columns in the tile
+        const uint32_t slot = ptx::smem_addr(epi) + ew * kEpiBufBytes;
+        const uint32_t res_bar = ptx::smem_addr(res_full + ew);
         const uint32_t row_off = lane * 128u, swz = lane & 7u;
-        float* bias_w = bias_sm + q * 64u;
         const bool has_z = !PLAIN && P.has_z != 0, has_r = !PLAIN && P.has_r != 0;
-        uint32_t use = 0;                              // staging-slot uses so far
-        uint32_t res_issued = 0, res_taken = 0, res_phase = 0, res_slot = 0;
-        const bool zero_acc = P.num_kb == 0;
+        uint32_t res_issued = 0, res_taken = 0;
         bool ok = true;
-        uint32_t tl = 0;
-        for (uint32_t t = unit; ok && t < uint32_t(P.num_tiles); t += units, ++tl) {
+        PairItem w;
+        for (uint32_t tl = 0; ok && pair_item(P.w, unit, units, tl, w); ++tl) {
             uint32_t mt, nt;
-            raster_tile(t, P.m_tiles, P.n_tiles, P.group_m, mt, nt);
-            const int32_t row0 = int32_t(mt * kTile + rank * 128u + q * 32u), n0 = int32_t(nt * kTile);
-            const int32_t chunks = row0 < P.M ? min(4, (P.N - n0 + 63) / 64) : 0;
+            raster_tile(w.tile, P.w.m_tiles, P.w.n_tiles, P.w.group_m, mt, nt);
+            const int32_t row0 = int32_t(mt * kTile + rank * 128u + q * 32u), n0 = int32_t(nt * kTile) + col0;
+            // 64-column chunks that hold something.
+            const int32_t chunks = row0 < P.M && n0 < P.N ? min(2, (P.N - n0 + 63) / 64) : 0;
             const uint32_t a = tl & 1u, aph = (tl >> 1) & 1u;
             const uint32_t ae = ptx::smem_addr(acc_empty + a);
-            // The first chunk's residual and bias travel while the accumulator is not ready.
-            auto fetch_residual = [&](int32_t c, uint32_t next_use) {
-                res_slot = next_use & 1u;
+            // The residual of a chunk, into the staging slot once its last store has read it.
+            auto fetch_residual = [&](int32_t c) {
                 if (lane == 0) {
-                    // The slot's last store (use next_use - 2) has read it.
-                    if (has_z) ptx::bulk_wait_group_read<0>();
-                    else ptx::bulk_wait_group_read<1>();
-                    const uint32_t bar = ptx::smem_addr(res_full + q * 2u + res_slot);
-                    ptx::mbar_arrive_expect_tx(bar, kEpiBufBytes);
-                    ptx::tma_load_2d(slot0 + res_slot * kEpiBufBytes, &P.mapR, bar, n0 + c * 64, row0);
+                    ptx::bulk_wait_group_read<0>();
+                    ptx::mbar_arrive_expect_tx(res_bar, kEpiBufBytes);
+                    ptx::tma_load_2d(slot, &P.mapR, res_bar, n0 + c * 64, row0);
                 }
                 ++res_issued;
             };
-            float2 bnext = make_float2(0.f, 0.f);
-            auto fetch_bias = [&](int32_t c) {
-                const int32_t n = n0 + c * 64 + int32_t(lane) * 2;
-                bnext = make_float2(0.f, 0.f);
-                if (P.bias != nullptr) {
-                    if (n < P.N) bnext.x = __ldg(P.bias + n);
-                    if (n + 1 < P.N) bnext.y = __ldg(P.bias + n + 1);
-                }
-            };
-            if (!PLAIN && chunks > 0) {
-                if (has_r) fetch_residual(0, use + (has_z ? 1u : 0u));
-                fetch_bias(0);
-            }
+            const bool early = has_r && !has_z && w.part < 0 && chunks > 0;
+            if (early) fetch_residual(0);
             if (!mbar_wait_warp<true>(ptx::smem_addr(acc_full + a), aph, P.ctl, abort_flag,
                                       kSiteEpiAccFull, tl))
                 break;
             ptx::tc_fence_after_sync();
-            if (chunks == 0) umma::acc_release<2>(ae, lane);
+            const uint32_t acc = tmem_base + ((q * 32u) << 16) + a * kAccCols + uint32_t(col0);
+            if (chunks == 0) {
+                umma::acc_release<2>(ae, lane);
+                continue;
+            }
+            const float4* other = nullptr;             // the other half of a split tile: this warp's block
+            if (w.part >= 0) {
+                const int64_t half = 2 * kEpiWarps * kPartVecs;
+                float4* blk = P.w.parts + (int64_t(w.sk) * 4 * kEpiWarps + rank * kEpiWarps + ew) * kPartVecs + lane;
+                uint32_t* count = P.w.count + (uint32_t(w.sk) * 2u + rank) * kEpiWarps + ew;
+                float4* mine = blk + w.part * half;
+                for (int32_t c = 0; c < 2 * chunks; ++c) {
+                    uint32_t x[32];
+                    ptx::tmem_ld_32x32b_x32(acc + uint32_t(c * 32), x);
+                    ptx::tmem_ld_wait();
+#pragma unroll
+                    for (int v = 0; v < 8; ++v)
+                        mine[(c * 8 + v) * 32] =
+                            make_float4(__uint_as_float(x[4 * v]), __uint_as_float(x[4 * v + 1]),
+                                        __uint_as_float(x[4 * v + 2]), __uint_as_float(x[4 * v + 3]));
+                }
+                __threadfence();
+                __syncwarp();
+                uint32_t before = 0;
+                if (lane == 0) before = atomicAdd(count, 1u);
+                if (__shfl_sync(0xffffffffu, before, 0) == 0u) {
+                    umma::acc_release<2>(ae, lane);    // the other pair finishes the tile
+                    continue;
+                }
+                __threadfence();
+                other = blk + (1 - w.part) * half;
+            }
+            if (has_r && !has_z && !early) fetch_residual(0);
             for (int32_t c = 0; c < chunks; ++c) {
-                const uint32_t taddr = tmem_base + ((q * 32u) << 16) + a * kAccCols + uint32_t(c) * 64u;
-                uint32_t r0[32], r1[32];
-                ptx::tmem_ld_32x32b_x32(taddr, r0);
-                ptx::tmem_ld_32x32b_x32(taddr + 32, r1);
-                if (!PLAIN) {
-                    __syncwarp();                      // the previous chunk's bias has been read
-                    reinterpret_cast<float2*>(bias_w)[lane] = bnext;
-                    __syncwarp();
-                    if (c + 1 < chunks) fetch_bias(c + 1);
-                }
-                ptx::tmem_ld_wait();
-                if (c + 1 == chunks) umma::acc_release<2>(ae, lane);
                 float z[64];
+                {
+                    uint32_t r0[32], r1[32];
+                    ptx::tmem_ld_32x32b_x32(acc + uint32_t(c) * 64u, r0);
+                    ptx::tmem_ld_32x32b_x32(acc + uint32_t(c) * 64u + 32u, r1);
+                    ptx::tmem_ld_wait();
 #pragma unroll
-                for (int j = 0; j < 64; ++j) {
-                    z[j] = __uint_as_float(j < 32 ? r0[j] : r1[j - 32]);
-                    if (zero_acc) z[j] = 0.f;
+                    for (int j = 0; j < 64; ++j) {
+                        z[j] = __uint_as_float(j < 32 ? r0[j] : r1[j - 32]);
+                        if (w.kb1 == w.kb0) z[j] = 0.f;
+                    }
                 }
-                if (!PLAIN) {
+                if (other != nullptr) {
+                    float4 x[16];
 #pragma unroll
-                    for (int j4 = 0; j4 < 16; ++j4) {
-                        const float4 b = reinterpret_cast<const float4*>(bias_w)[j4];
-                        z[4 * j4] += b.x;
-                        z[4 * j4 + 1] += b.y;
-                        z[4 * j4 + 2] += b.z;
-                        z[4 * j4 + 3] += b.w;
+                    for (int v = 0; v < 16; ++v) x[v] = __ldcg(other + (c * 16 + v) * 32);
+#pragma unroll
+                    for (int v = 0; v < 16; ++v)
+                        z[4 * v] += x[v].x, z[4 * v + 1] += x[v].y, z[4 * v + 2] += x[v].z, z[4 * v + 3] += x[v].w;
+                }
+                if (c + 1 == chunks) umma::acc_release<2>(ae, lane);
+                if (!PLAIN && P.bias != nullptr) {
+                    const int32_t n = n0 + c * 64;
+                    const float* b = P.bias + n;
+                    if (P.bias_vec != 0 && n + 64 <= P.N) {
+#pragma unroll
+                        for (int v = 0; v < 16; ++v) {
+                            const float4 x = __ldg(reinterpret_cast<const float4*>(b) + v);
+                            z[4 * v] += x.x, z[4 * v + 1] += x.y, z[4 * v + 2] += x.z, z[4 * v + 3] += x.w;
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 64; ++j)
+                            if (n + j < P.N) z[j] += __ldg(b + j);
                     }
                 }
                 auto stage_and_store = [&](const CUtensorMap* map) {
-                    const uint32_t buf = slot0 + (use & 1u) * kEpiBufBytes;
 #pragma unroll
                     for (uint32_t j = 0; j < 8; ++j) {
-                        uint32_t w[4];
+                        uint32_t x[4];
 #pragma unroll
                         for (uint32_t u = 0; u < 4; ++u) {
                             const __nv_bfloat162 v = __floats2bfloat162_rn(z[8 * j + 2 * u], z[8 * j + 2 * u + 1]);
-                            w[u] = *reinterpret_cast<const uint32_t*>(&v);
+                            x[u] = *reinterpret_cast<const uint32_t*>(&v);
                         }
-                        ptx::st_shared_v4(buf + row_off + ((j ^ swz) << 4), w[0], w[1], w[2], w[3]);
+                        ptx::st_shared_v4(slot + row_off + ((j ^ swz) << 4), x[0], x[1], x[2], x[3]);
                     }
                     ptx::fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
-                        ptx::tma_store_2d(map, buf, n0 + c * 64, row0);
+                        ptx::tma_store_2d(map, slot, n0 + c * 64, row0);
                         ptx::bulk_commit_group();
                     }
-                    ++use;
                 };
                 if (has_z) {
-                    if (lane == 0) ptx::bulk_wait_group_read<1>();
+                    if (lane == 0) ptx::bulk_wait_group_read<0>();
                     __syncwarp();
                     stage_and_store(&P.mapZ);
+                    if (has_r) fetch_residual(c);      // while the activation is computed
                 }
                 if (!PLAIN) {
 #pragma unroll
@@ -323,38 +397,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (has_r) {
-                    const uint32_t slot = use & 1u;
-                    if (!mbar_wait_warp(ptx::smem_addr(res_full + q * 2u + slot), (res_phase >> slot) & 1u,
-                                        P.ctl, abort_flag, kSiteEpiResidual, tl)) {
+                    if (!mbar_wait_warp(res_bar, res_taken & 1u, P.ctl, abort_flag, kSiteEpiResidual, tl)) {
                         ok = false;
                         break;
                     }
-                    res_phase ^= 1u << slot;
                     ++res_taken;
-                    const uint32_t buf = slot0 + slot * kEpiBufBytes;
 #pragma unroll
                     for (uint32_t j = 0; j < 8; ++j) {
-                        const uint4 v = ptx::ld_shared_v4(buf + row_off + ((j ^ swz) << 4));
-                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                        const uint4 v = ptx::ld_shared_v4(slot + row_off + ((j ^ swz) << 4));
+                        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                         for (uint32_t u = 0; u < 4; ++u) {
-                            z[8 * j + 2 * u] += __uint_as_float(w[u] << 16);
-                            z[8 * j + 2 * u + 1] += __uint_as_float(w[u] & 0xFFFF0000u);
+                            z[8 * j + 2 * u] += __uint_as_float(x[u] << 16);
+                            z[8 * j + 2 * u + 1] += __uint_as_float(x[u] & 0xFFFF0000u);
                         }
                     }
                 } else {
-                    if (lane == 0) ptx::bulk_wait_group_read<1>();
+                    if (lane == 0) ptx::bulk_wait_group_read<0>();
                     __syncwarp();
                 }
                 stage_and_store(&P.mapC);
-                if (has_r && c + 1 < chunks) fetch_residual(c + 1, use + (has_z ? 1u : 0u));
+                if (has_r && !has_z && c + 1 < chunks) fetch_residual(c + 1);
             }
         }
         if (lane == 0) {
             // After an abort a residual load may still be in flight.
-            if (res_issued != res_taken)
-                mbar_wait_drain(ptx::smem_addr(res_full + q * 2u + res_slot), (res_phase >> res_slot) & 1u,
-                                P.ctl.timeout_ns);
+            if (res_issued != res_taken) mbar_wait_drain(res_bar, res_taken & 1u, P.ctl.timeout_ns);
             ptx::bulk_wait_group<0>();
         }
     }

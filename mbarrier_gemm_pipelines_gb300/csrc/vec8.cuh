@@ -24,6 +24,15 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
     return make_uint4(x[0], x[1], x[2], x[3]);
 }
 
+// The first `count` (below 8: the rest zero) of eight elements at any address.
+__device__ __forceinline__ uint4 load8_raw(const __nv_bfloat16* p, int32_t count) {
+    uint32_t x[4] = {};
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (j < count) x[j / 2] |= uint32_t(__bfloat16_as_ushort(p[j])) << (16 * (j % 2));
+    return make_uint4(x[0], x[1], x[2], x[3]);
+}
+
 // 16-byte aligned addresses.
 __device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
     unpack8(*reinterpret_cast<const uint4*>(p), v);
