@@ -19,6 +19,9 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
 
 
+_LIMIT = 1 << 64
+
+
 def _check(code):
     if code:
         raise GbrError(code, last_error())
@@ -31,20 +34,31 @@ def _act_code(act):
     return code
 
 
-def _bits64(v, name):
-    v = int(v)
-    if v < 0 or v >> 64:
-        raise ValueError("%s must be in [0, 2^64)" % name)
-    return v
+def _check_bits(seed, offset):
+    for v, name in ((seed, "seed"), (offset, "offset")):
+        if not isinstance(v, int) or not 0 <= v < _LIMIT:
+            raise ValueError("%s must be an integer in [0, 2^64)" % name)
 
 
-def _refuse_type(t, name, dtype):
+def _refuse(t, name, dtype, dev, rows=None, cols=None):
+    """Says what is wrong with a tensor that the short checks below turned down."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
-    raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
+    if t.dtype is not dtype:
+        raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
+    if t.get_device() < 0:
+        raise ValueError("%s must be a CUDA tensor (this library has no CPU path)" % name)
+    if t.get_device() != dev:
+        raise ValueError("%s is on cuda:%d, not on cuda:%d" % (name, t.get_device(), dev))
+    if t.dim() != 2:
+        raise ValueError("%s must be 2-D" % name)
+    if rows is not None and tuple(t.shape) != (rows, cols):
+        raise ValueError("%s must be [%d, %d], got %s" % (name, rows, cols, list(t.shape)))
+    raise ValueError("the rows of %s must be contiguous" % name)
 
 
 def _device_of(t, name):
+    """The current device, on which the first tensor has to be."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     dev = t.get_device()
@@ -55,41 +69,48 @@ def _device_of(t, name):
     return dev
 
 
-def _mat(t, name, dtype, dev):
-    """(rows, columns, row stride) of a 2-D tensor on `dev` whose rows are contiguous."""
-    if getattr(t, "dtype", None) is not dtype:
-        _refuse_type(t, name, dtype)
-    if t.get_device() != dev:
-        raise ValueError("%s is on %s, the first tensor on cuda:%d" % (name, t.device, dev))
-    shape = t.shape
-    if len(shape) != 2:
-        raise ValueError("%s must be 2-D" % name)
-    rows, cols = shape
+def _step(t, rows, cols):
+    """Row stride of a 2-D tensor that is not contiguous; -1 where its rows are not either."""
     step, inner = t.stride()
     if inner != 1 and cols > 1:
-        raise ValueError("the rows of %s must be contiguous" % name)
-    return rows, cols, step if rows > 1 else cols or 1
+        return -1
+    return step if rows > 1 else cols or 1
+
+
+def _mat(t, name, dtype, dev):
+    """(rows, columns, row stride) of a 2-D tensor on `dev` whose rows are contiguous."""
+    if getattr(t, "dtype", None) is not dtype or t.get_device() != dev or t.dim() != 2:
+        _refuse(t, name, dtype, dev)
+    rows, cols = t.shape
+    step = (cols or 1) if t.is_contiguous() else _step(t, rows, cols)
+    if step < 0:
+        _refuse(t, name, dtype, dev)
+    return rows, cols, step
 
 
 def _mat_of(t, name, dtype, dev, rows, cols):
     """Row stride of a [rows, cols] matrix."""
-    r, c, step = _mat(t, name, dtype, dev)
-    if r != rows or c != cols:
-        raise ValueError("%s must be [%d, %d], got [%d, %d]" % (name, rows, cols, r, c))
+    if getattr(t, "dtype", None) is not dtype or t.get_device() != dev or t.shape != (rows, cols):
+        _refuse(t, name, dtype, dev, rows, cols)
+    step = (cols or 1) if t.is_contiguous() else _step(t, rows, cols)
+    if step < 0:
+        _refuse(t, name, dtype, dev, rows, cols)
     return step
 
 
 def _packed(t, name, dtype, dev, shape):
     """Data pointer of a contiguous tensor of that shape."""
-    if getattr(t, "dtype", None) is not dtype:
-        _refuse_type(t, name, dtype)
+    if getattr(t, "dtype", None) is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.dtype is not dtype:
+        raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
     if t.get_device() != dev:
-        raise ValueError("%s is on %s, the first tensor on cuda:%d" % (name, t.device, dev))
+        raise ValueError("%s is on %s, not on cuda:%d" % (name, t.device, dev))
     if t.shape != shape:
         raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
-    return t.data_ptr()
+    raise ValueError("%s must be contiguous" % name)
 
 
 def _stream_of(stream, dev):
@@ -108,11 +129,11 @@ def dropout_add(X, residual=None, p=0.5, seed=0, offset=0, Y=None, stream=None):
     if dtype is not _bf16 and dtype is not _f32:
         raise TypeError("X must be a bf16 or fp32 torch.Tensor, got %s" % (dtype or type(X)))
     dev = _device_of(X, "X")
-    shape = X.shape
     if Y is None:
-        Y = _empty(shape, dtype=dtype, device=X.device)
+        Y = _empty(X.shape, dtype=dtype, device=X.device)
     x, r, y = X, residual, Y
-    if len(shape) != 2:
+    if X.dim() != 2:
+        shape = X.shape
         if not shape:
             raise ValueError("X must have at least one dimension")
         flat = (shape[:-1].numel(), shape[-1])
@@ -122,10 +143,12 @@ def dropout_add(X, residual=None, p=0.5, seed=0, offset=0, Y=None, stream=None):
         x, y, r = x.view(flat), y.view(flat), None if r is None else r.view(flat)
     rows, cols, ldx = _mat(x, "X", dtype, dev)
     ldy = _mat_of(y, "Y", dtype, dev, rows, cols)
-    ldr = 0 if r is None else _mat_of(r, "residual", dtype, dev, rows, cols)
-    _check(lib().dropout_add(x.data_ptr(), ldx, None if r is None else r.data_ptr(), ldr, y.data_ptr(), ldy,
-                             rows, cols, BF16 if dtype is _bf16 else F32_FFMA, p, _bits64(seed, "seed"),
-                             _bits64(offset, "offset"), _stream_of(stream, dev)))
+    pr, ldr = (None, 0) if r is None else (r.data_ptr(), _mat_of(r, "residual", dtype, dev, rows, cols))
+    if seed or offset:
+        _check_bits(seed, offset)
+    _check(lib().dropout_add(x.data_ptr(), ldx, pr, ldr, y.data_ptr(), ldy, rows, cols,
+                             BF16 if dtype is _bf16 else F32_FFMA, p, seed, offset,
+                             _raw_stream(dev) if stream is None else _stream_of(stream, dev)))
     return Y
 
 
@@ -139,23 +162,27 @@ def gemm_bias_act(A, B, bias=None, residual=None, act="none", p=0.0, seed=0, off
     K2, N, ldb = _mat(B, "B", _bf16, dev)
     if K2 != K:
         raise ValueError("shape mismatch: A %s, B %s" % (list(A.shape), list(B.shape)))
-    pb = None if bias is None else _packed(bias, "bias", _f32, dev, (N,))
+    pb = pr = pz = None
+    ldr = ldz = 0
+    if bias is not None:
+        pb = _packed(bias, "bias", _f32, dev, (N,))
+    if residual is not None:
+        pr, ldr = residual.data_ptr(), _mat_of(residual, "residual", _bf16, dev, M, N)
     if C is None:
         C = _empty((M, N), dtype=_bf16, device=A.device)
         ldc = N or 1
     else:
         ldc = _mat_of(C, "C", _bf16, dev, M, N)
-    if Z is None and return_z:
-        Z = _empty((M, N), dtype=_bf16, device=A.device)
-    pr = pz = None
-    ldr = ldz = 0
-    if residual is not None:
-        pr, ldr = residual.data_ptr(), _mat_of(residual, "residual", _bf16, dev, M, N)
     if Z is not None:
         pz, ldz = Z.data_ptr(), _mat_of(Z, "Z", _bf16, dev, M, N)
+    elif return_z:
+        Z = _empty((M, N), dtype=_bf16, device=A.device)
+        pz, ldz = Z.data_ptr(), N or 1
+    if seed or offset:
+        _check_bits(seed, offset)
     _check(lib().gemm_bias_act(A.data_ptr(), lda, B.data_ptr(), ldb, pb, pr, ldr, C.data_ptr(), ldc, pz, ldz,
-                               M, N, K, BF16, _act_code(act), p, _bits64(seed, "seed"),
-                               _bits64(offset, "offset"), _stream_of(stream, dev)))
+                               M, N, K, BF16, _act_code(act), p, seed, offset,
+                               _raw_stream(dev) if stream is None else _stream_of(stream, dev)))
     return C if Z is None else (C, Z)
 
 
@@ -179,15 +206,17 @@ def gemm_bias_act_backward(dC, A, B, Z=None, act="none", p=0.0, seed=0, offset=0
     ldda = lddb = 0
     if not want_a:
         dA = None
+    elif dA is None:
+        dA = _empty((M, K), dtype=_bf16, device=dC.device)
+        pa, ldda = dA.data_ptr(), K or 1
     else:
-        if dA is None:
-            dA = _empty((M, K), dtype=_bf16, device=dC.device)
         pa, ldda = dA.data_ptr(), _mat_of(dA, "dA", _bf16, dev, M, K)
     if not want_b:
         dB = None
+    elif dB is None:
+        dB = _empty((K, N), dtype=_bf16, device=dC.device)
+        pb, lddb = dB.data_ptr(), N or 1
     else:
-        if dB is None:
-            dB = _empty((K, N), dtype=_bf16, device=dC.device)
         pb, lddb = dB.data_ptr(), _mat_of(dB, "dB", _bf16, dev, K, N)
     if not want_bias:
         dbias = None
@@ -195,9 +224,11 @@ def gemm_bias_act_backward(dC, A, B, Z=None, act="none", p=0.0, seed=0, offset=0
         if dbias is None:
             dbias = _empty((N,), dtype=_f32, device=dC.device)
         pbias = _packed(dbias, "dbias", _f32, dev, (N,))
+    if seed or offset:
+        _check_bits(seed, offset)
     _check(lib().gemm_bias_act_backward(dC.data_ptr(), lddc, A.data_ptr(), lda, B.data_ptr(), ldb, pz, ldz, pa,
-                                        ldda, pb, lddb, pbias, M, N, K, BF16, code, p, _bits64(seed, "seed"),
-                                        _bits64(offset, "offset"), _stream_of(stream, dev)))
+                                        ldda, pb, lddb, pbias, M, N, K, BF16, code, p, seed, offset,
+                                        _raw_stream(dev) if stream is None else _stream_of(stream, dev)))
     return dA, dB, dbias
 
 
