@@ -198,7 +198,8 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 
 int encode(CUtensorMap* map, CUtensorMapDataType dt, uint32_t rank, const void* ptr,
            const uint64_t* dims, const uint64_t* strides_bytes, const uint32_t* box,
-           CUtensorMapSwizzle swz, const char* what) {
+           CUtensorMapSwizzle swz, const char* what,
+           CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B) {
     auto fn = encode_fn();
     if (!fn) return fail(GBR_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable from the driver");
     cuuint64_t d[5];
@@ -211,7 +212,7 @@ int encode(CUtensorMap* map, CUtensorMapDataType dt, uint32_t rank, const void* 
     }
     for (uint32_t i = 0; i + 1 < rank; ++i) st[i] = strides_bytes[i];
     CUresult r = fn(map, dt, rank, const_cast<void*>(ptr), d, st, b, es,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, swz, promotion,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS)
         return fail(GBR_ERR_INVALID, "cuTensorMapEncodeTiled(%s) failed with CUresult %d", what,
@@ -418,8 +419,8 @@ int lib_ctx(LibCtx* out) {
 }
 int encode_tensor_map(CUtensorMap* map, CUtensorMapDataType dt, uint32_t rank, const void* ptr,
                       const uint64_t* dims, const uint64_t* strides_bytes, const uint32_t* box,
-                      CUtensorMapSwizzle swz, const char* what) {
-    return encode(map, dt, rank, ptr, dims, strides_bytes, box, swz, what);
+                      CUtensorMapSwizzle swz, const char* what, CUtensorMapL2promotion promotion) {
+    return encode(map, dt, rank, ptr, dims, strides_bytes, box, swz, what, promotion);
 }
 void count_launch() { ++g_launches; }
 uint64_t wait_timeout_ns() { return t_timeout_override ? t_timeout_override : timeout_ns(); }

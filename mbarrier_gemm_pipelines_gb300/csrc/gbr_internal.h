@@ -208,7 +208,8 @@ struct LibCtx {
 int lib_ctx(LibCtx* out);                      // GBR_OK or an error code
 int encode_tensor_map(CUtensorMap* map, CUtensorMapDataType dt, uint32_t rank, const void* ptr,
                       const uint64_t* dims, const uint64_t* strides_bytes, const uint32_t* box,
-                      CUtensorMapSwizzle swz, const char* what);
+                      CUtensorMapSwizzle swz, const char* what,
+                      CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 void count_launch();                           // adds one to gbr_launch_count()
 uint64_t wait_timeout_ns();                    // per-wait limit of this thread's next launch
 FaultInjection injection_now();                // self-test fault of this thread's next launch

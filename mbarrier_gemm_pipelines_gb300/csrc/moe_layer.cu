@@ -58,84 +58,117 @@ __device__ __forceinline__ uint32_t logit_key(float x) {
 }
 
 // TB tokens a cluster.  Thread (ty, tx) sums rows ty, ty + ny, ... of this
-// CTA's eighth of Wr for expert tx; one read of Wr serves TB tokens.
-template <int TB>
-__global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const MoeArgs a, int32_t lanes) {
-    __shared__ float red[TB][kRouterThreads];
-    __shared__ float logit[TB][kMoeMaxExperts];
+// CTA's eighth of Wr for experts 4 tx .. 4 tx + 3 (VEC: rows of Wr start on 16
+// bytes; 2^shift threads along the experts); one read of Wr serves TB tokens.
+// Sums over ty: shuffles within a warp, then over the warps, then over the
+// CTAs in rank order, all in a fixed order.
+template <int TB, bool VEC>
+__global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const MoeArgs a, int32_t shift) {
+    constexpr int kWarps = kRouterThreads / 32;
+    extern __shared__ __align__(16) float router_mem[];
+    const int wide = 4 << shift;                        // experts, rounded up
+    float* red = router_mem;                            // [TB][kWarps][wide]: a warp's sums
+    float* sums = red + TB * kWarps * wide;             // of rank 0: [CTA][TB][wide]
     ptx::griddep_launch_dependents();   // the expert kernel's set-up overlaps this one
     ptx::griddep_wait();
     const uint32_t rank = ptx::cluster_ctarank();
-    const int t0 = int(blockIdx.x / kRouterCluster) * TB, tid = int(threadIdx.x);
-    const int e = tid % lanes, ty = tid / lanes, ny = kRouterThreads / lanes;
+    const int t0 = int(blockIdx.x / kRouterCluster) * TB, tid = int(threadIdx.x), lane = tid % 32, warp = tid / 32;
+    const int lanes = 1 << shift, e = (tid & (lanes - 1)) * 4, ty = tid >> shift, ny = kRouterThreads >> shift;
     const int d0 = int(rank) * (a.D / kRouterCluster), d1 = d0 + a.D / kRouterCluster;
-    const bf16* x = static_cast<const bf16*>(a.X);
-    float acc[TB] = {};
-    if (e < a.E) {
-#pragma unroll 8
+    const bf16* x = static_cast<const bf16*>(a.X) + int64_t(t0) * a.D;
+    const int tokens = min(TB, a.T - t0), left = a.E - e;
+    float acc[TB][4] = {};
+    if (left > 0) {
+#pragma unroll 4
         for (int d = d0 + ty; d < d1; d += ny) {
-            const float w = __ldg(a.Wr + int64_t(d) * a.E + e);
+            const float* wp = a.Wr + int64_t(d) * a.E + e;
+            float w[4] = {};
+            if (VEC) {
+                const float4 v = __ldg(reinterpret_cast<const float4*>(wp));
+                w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (j < left) w[j] = __ldg(wp + j);
+            }
 #pragma unroll
             for (int i = 0; i < TB; ++i)
-                if (t0 + i < a.T) acc[i] = fmaf(__bfloat162float(x[int64_t(t0 + i) * a.D + d]), w, acc[i]);
-        }
-    }
+                if (i < tokens) {
+                    const float xv = __bfloat162float(x[int64_t(i) * a.D + d]);
 #pragma unroll
-    for (int i = 0; i < TB; ++i) red[i][tid] = acc[i];
-    for (int s = ny / 2; s > 0; s /= 2) {
-        __syncthreads();
-        if (ty < s)
-#pragma unroll
-            for (int i = 0; i < TB; ++i) red[i][tid] += red[i][tid + s * lanes];
-    }
-    ptx::cluster_sync_all();
-    if (rank == 0) {
-        for (int j = tid; j < TB * a.E; j += kRouterThreads) {
-            const int i = j / a.E, ee = j % a.E;
-            const uint32_t at = ptx::smem_addr(&red[i][ee]);
-            float v = 0.f;
-#pragma unroll
-            for (uint32_t r = 0; r < kRouterCluster; ++r)
-                v += __uint_as_float(ptx::ld_shared_cluster_u32(ptx::mapa_shared(at, r)));
-            logit[i][ee] = v;
-        }
-        __syncthreads();
-        const int i = tid / 32, lane = tid % 32;
-        if (i < TB && t0 + i < a.T) {
-            uint32_t key[kMoeMaxExperts / 32];
-#pragma unroll
-            for (int c = 0; c < kMoeMaxExperts / 32; ++c)
-                key[c] = lane + 32 * c < a.E ? logit_key(logit[i][lane + 32 * c]) : 0u;
-            int mine = 0;                              // lane k keeps the k-th choice
-            for (int k = 0; k < a.top_k; ++k) {
-                uint64_t best = 0;
-#pragma unroll
-                for (int c = 0; c < kMoeMaxExperts / 32; ++c) {
-                    const uint64_t q = (uint64_t(key[c]) << 32) | uint32_t(~(lane + 32 * c));
-                    if (key[c] != 0 && q > best) best = q;
+                    for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(xv, w[j], acc[i][j]);
                 }
-#pragma unroll
-                for (int o = 16; o > 0; o /= 2) {
-                    const uint64_t other = __shfl_xor_sync(0xffffffffu, best, o);
-                    if (other > best) best = other;
-                }
-                const int pick = int(~uint32_t(best));
-#pragma unroll
-                for (int c = 0; c < kMoeMaxExperts / 32; ++c)
-                    if (pick == lane + 32 * c) key[c] = 0;
-                if (lane == k) mine = pick;
-            }
-            const float top = logit[i][__shfl_sync(0xffffffffu, mine, 0)];
-            const float w = lane < a.top_k ? expf(logit[i][mine] - top) : 0.f;
-            float sum = 0.f;
-            for (int k = 0; k < a.top_k; ++k) sum += __shfl_sync(0xffffffffu, w, k);
-            if (lane < a.top_k) {
-                a.ids[int64_t(t0 + i) * a.top_k + lane] = mine;
-                a.weights[int64_t(t0 + i) * a.top_k + lane] = w / sum;
-            }
         }
     }
-    ptx::cluster_sync_all();   // the peers' sums have been read
+    // Lanes with the same experts lie `lanes` apart (fewer than 32 lanes), or
+    // the warp's lanes all have different ones.
+    for (int o = 16; o >= lanes; o /= 2)
+#pragma unroll
+        for (int i = 0; i < TB; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][j] += __shfl_xor_sync(0xffffffffu, acc[i][j], o);
+    if (lane < lanes)
+#pragma unroll
+        for (int i = 0; i < TB; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (j < left) red[(i * kWarps + warp) * wide + e + j] = acc[i][j];
+    __syncthreads();
+    // Of 64 threads along the experts a warp has one half: its row holds those.
+    const int stride = lanes > 32 ? lanes / 32 : 1;
+    for (int q = warp; q < TB * a.E; q += kWarps) {
+        const int i = q / a.E, ee = q % a.E;
+        const int first = lanes > 32 ? ee / 128 : 0;    // the warps whose lanes have expert ee
+        const int row = first + lane * stride;
+        float v = row < kWarps ? red[(i * kWarps + row) * wide + ee] : 0.f;
+#pragma unroll
+        for (int o = 16; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+        if (lane == 0)
+            ptx::st_shared_cluster_u32(ptx::mapa_shared(ptx::smem_addr(sums + (rank * TB + uint32_t(i)) * uint32_t(wide) + uint32_t(ee)), 0), __float_as_uint(v));
+    }
+    ptx::cluster_sync_all();            // every CTA's sums are in rank 0
+    const int i = warp;
+    if (rank != 0 || i >= tokens) return;
+    float logit[kMoeMaxExperts / 32];
+    uint32_t key[kMoeMaxExperts / 32];
+#pragma unroll
+    for (int c = 0; c < kMoeMaxExperts / 32; ++c) {
+        logit[c] = 0.f;
+        key[c] = 0u;
+        if (32 * c < a.E && lane + 32 * c < a.E) {
+#pragma unroll
+            for (int r = 0; r < kRouterCluster; ++r) logit[c] += sums[(r * TB + i) * wide + lane + 32 * c];
+            key[c] = logit_key(logit[c]);
+        }
+    }
+    int mine = 0;                                       // lane k keeps the k-th choice
+    float value = 0.f, top = 0.f;
+    for (int k = 0; k < a.top_k; ++k) {
+        uint32_t best = 0;
+        int at = kMoeMaxExperts;
+#pragma unroll
+        for (int c = 0; c < kMoeMaxExperts / 32; ++c)
+            if (32 * c < a.E && key[c] > best) best = key[c], at = lane + 32 * c;
+        const uint32_t most = __reduce_max_sync(0xffffffffu, best);
+        const int pick = __reduce_min_sync(0xffffffffu, best == most ? at : kMoeMaxExperts);
+        float v = 0.f;
+#pragma unroll
+        for (int c = 0; c < kMoeMaxExperts / 32; ++c)
+            if (pick == lane + 32 * c) {
+                key[c] = 0;
+                v = logit[c];
+            }
+        v = __shfl_sync(0xffffffffu, v, pick % 32);
+        if (k == 0) top = v;
+        if (lane == k) mine = pick, value = v;
+    }
+    const float w = lane < a.top_k ? expf(value - top) : 0.f;
+    float sum = 0.f;
+    for (int k = 0; k < a.top_k; ++k) sum += __shfl_sync(0xffffffffu, w, k);
+    if (lane < a.top_k) {
+        a.ids[int64_t(t0 + i) * a.top_k + lane] = mine;
+        a.weights[int64_t(t0 + i) * a.top_k + lane] = w / sum;
+    }
 }
 
 // ------------------------------------------------------------ experts
@@ -724,6 +757,10 @@ ExpertPlan plan_experts(const MoeArgs& a, const LibCtx& c) {
     return p;
 }
 
+size_t router_smem_bytes(int tb, int32_t shift) {
+    return size_t(tb) * size_t(kRouterThreads / 32 + kRouterCluster) * (size_t(4) << shift) * sizeof(float);
+}
+
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 template <class... Args>
@@ -769,11 +806,18 @@ int launch_moe(const MoeArgs& a, void* scratch, const LibCtx& c, cudaStream_t st
                    bh[3] = {64, 64, 1};
     const auto bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
+    // A 128-byte row of a box is fetched with its 256-byte neighbourhood only
+    // where that is the next panel's row, not where every row starts elsewhere
+    // (1000 gated columns: 163 us with, 155 without).
+    auto promotion = [](uint64_t pitch) {
+        return pitch % 256 == 0 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B;
+    };
+    const auto p1 = promotion(s1[0]), p2 = promotion(s2[0]);
     int r;
     if ((r = encode_tensor_map(&P.mapX, bf, 2, a.X, xd, xs, bx, sw, "X")) != GBR_OK ||
-        (r = encode_tensor_map(&P.mapW1, bf, 3, a.W1, d1, s1, bw, sw, "W1")) != GBR_OK ||
-        (r = encode_tensor_map(&P.mapW2, bf, 3, a.W2, d2, s2, bw, sw, "W2")) != GBR_OK ||
-        (r = encode_tensor_map(&P.mapW2half, bf, 3, a.W2, d2, s2, bh, sw, "W2")) != GBR_OK)
+        (r = encode_tensor_map(&P.mapW1, bf, 3, a.W1, d1, s1, bw, sw, "W1", p1)) != GBR_OK ||
+        (r = encode_tensor_map(&P.mapW2, bf, 3, a.W2, d2, s2, bw, sw, "W2", p2)) != GBR_OK ||
+        (r = encode_tensor_map(&P.mapW2half, bf, 3, a.W2, d2, s2, bh, sw, "W2", p2)) != GBR_OK)
         return r;
     P.a = a;
     P.pairs = static_cast<PairParts*>(scratch);
@@ -783,15 +827,19 @@ int launch_moe(const MoeArgs& a, void* scratch, const LibCtx& c, cudaStream_t st
     P.sms = c.sm_count;
     P.ctl = c.ctl;
 
-    int lanes = 1;
-    while (lanes < a.E) lanes *= 2;
+    int32_t shift = 0;
+    while ((4 << shift) < a.E) ++shift;
     // Few tokens: a cluster each, for latency; more share the reads of Wr.
     const int tb = a.T * kRouterCluster <= c.sm_count ? 1 : kRouterTokens;
-    const dim3 rg(unsigned(cdiv(a.T, tb)) * kRouterCluster);
-    cudaError_t e = tb == 1 ? launch_overlapped(moe_router_kernel<1>, rg, kRouterThreads, kRouterCluster, stream, a,
-                                                int32_t(lanes))
-                            : launch_overlapped(moe_router_kernel<kRouterTokens>, rg, kRouterThreads, kRouterCluster,
-                                                stream, a, int32_t(lanes));
+    const bool vec = a.E % 4 == 0;
+    void (*router)(const MoeArgs, int32_t) =
+        tb == 1 ? (vec ? moe_router_kernel<1, true> : moe_router_kernel<1, false>)
+                : (vec ? moe_router_kernel<kRouterTokens, true> : moe_router_kernel<kRouterTokens, false>);
+    const size_t router_smem = router_smem_bytes(tb, shift);
+    if ((r = raise_kernel_smem(reinterpret_cast<void*>(router), router_smem, c.device)) != GBR_OK) return r;
+    void* rargs[] = {const_cast<MoeArgs*>(&a), &shift};
+    cudaError_t e = launch_kernel(reinterpret_cast<void*>(router), dim3(unsigned(cdiv(a.T, tb)) * kRouterCluster),
+                                  kRouterThreads, router_smem, kRouterCluster, rargs, stream);
     if (e != cudaSuccess) return report_cuda(e, "launching the router");
     count_launch();
 
