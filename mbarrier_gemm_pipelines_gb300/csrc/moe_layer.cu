@@ -482,22 +482,31 @@ __global__ void __launch_bounds__(kThreads, 1) moe_expert_kernel(const __grid_co
         constexpr uint32_t hi = desc_hi(1024);
         const uint32_t w_first = desc_lo(ring_base, panel), x_next = h_block / 16;
         const uint32_t full0 = ptx::smem_addr(full), to_empty = ptx::smem_addr(empty) - full0;
-        uint32_t w_lo = w_first, bar = full0, left = S;
-        auto multiply = [&](uint32_t acc, uint32_t x_lo, uint32_t slices, uint32_t accumulate) {
-            if (!(ok = mbar_wait(bar, ring.phase, P.ctl, abort_flag, kSiteMmaFull, ring.count))) return;
-            ptx::tc_fence_after_sync();
-            mma_slice<kStepMN, kStepK>(acc, w_lo, x_lo, hi, idesc, accumulate);
-            if (slices == 2)
-                mma_slice<kStepMN, kStepK>(acc, w_lo + kSliceBytes / 16, x_lo + x_next, hi, idesc, 1u);
-            ptx::mma_commit(bar + to_empty);
-            ++ring.count;
-            bar += 8;
-            w_lo += stage_bytes / 16;
-            if (--left == 0) {
-                left = S;
-                bar = full0;
-                w_lo = w_first;
-                ring.phase ^= 1u;
+        const uint32_t bar_end = full0 + 8u * S;
+        uint32_t w_lo = w_first, bar = full0, phase = 0;
+        // Whether the next stage is full is asked before the present one's MMAs are
+        // issued, so that the answer is there when it is needed.
+        bool ready = false;
+        auto k_step = [&](int32_t tiles, uint32_t acc, uint32_t x_lo, uint32_t slices, uint32_t accumulate) {
+#pragma unroll
+            for (int32_t j = 0; j < kWide; ++j) {
+                if (j >= tiles) break;
+                if (!ready && !(ok = mbar_wait(bar, phase, P.ctl, abort_flag, kSiteMmaFull, tl))) break;
+                ptx::tc_fence_after_sync();
+                const uint32_t give = bar + to_empty, from = w_lo;
+                bar += 8;
+                w_lo += stage_bytes / 16;
+                if (bar == bar_end) {
+                    bar = full0;
+                    w_lo = w_first;
+                    phase ^= 1u;
+                }
+                ready = mbar_test<false>(bar, phase);
+                mma_slice<kStepMN, kStepK>(acc, from, x_lo, hi, idesc, accumulate);
+                if (slices == 2)
+                    mma_slice<kStepMN, kStepK>(acc, from + kSliceBytes / 16, x_lo + x_next, hi, idesc, 1u);
+                ptx::mma_commit(give);
+                acc += t_pad;
             }
         };
         Segment s;
@@ -510,8 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_expert_kernel(const __grid_co
                                          kSiteMmaFull, xring.count)))
                         break;
                     const uint32_t x_lo = desc_lo(x_base + xring.slot * x_bytes, 16);
-                    for (int32_t j = 0; ok && j < tiles; ++j)
-                        multiply(acc + uint32_t(j) * t_pad, x_lo, ksub, k != 0);
+                    k_step(tiles, acc, x_lo, ksub, uint32_t(k));
                     ptx::mma_commit(ptx::smem_addr(x_empty + xring.slot));
                     xring.step(kXStages);
                 }
@@ -526,8 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_expert_kernel(const __grid_co
                 for (int32_t b = 0; ok && b < s.n; b += int32_t(ksub)) {
                     const uint32_t x_lo = desc_lo(h_base + uint32_t(b) * h_block, 16);
                     const uint32_t slices = uint32_t(min(int32_t(ksub), s.n - b));
-                    for (int32_t j = 0; ok && j < tiles; ++j)
-                        multiply(acc + uint32_t(j) * t_pad, x_lo, slices, b != 0);
+                    k_step(tiles, acc, x_lo, slices, uint32_t(b));
                 }
                 if (ok) acc_give();
             }
