@@ -384,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (!PLAIN) {
 #pragma unroll
-                    for (int j = 0; j < 64; ++j) z[j] = act_value<ACT>(z[j]);
+                    for (int j = 0; j < 64; j += 2) act_value2<ACT>(z[j], z[j + 1]);
                 }
                 if (!PLAIN && P.drop.threshold != 0) {
 #pragma unroll

@@ -85,7 +85,7 @@ __device__ __forceinline__ void finish8(const TileParams& P, int32_t i, int32_t 
             }
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = act_value<ACT>(v[e]);
+        for (int e = 0; e < 8; e += 2) act_value2<ACT>(v[e], v[e + 1]);
         if (P.drop.threshold != 0) {
             const uint4 bits = dropout_bits(P.drop, uint32_t(i), uint32_t(j) / 8u);
 #pragma unroll

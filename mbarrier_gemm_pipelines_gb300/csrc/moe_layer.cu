@@ -607,8 +607,15 @@ __global__ void __launch_bounds__(kThreads, 1) moe_expert_kernel(const __grid_co
                         if (NG == 2) ptx::tmem_ld_32x32b_x16(acc + t_pad + t, r2);
                         ptx::tmem_ld_wait();
 #pragma unroll
+                        for (uint32_t i = 0; i < 16; i += 2) {
+                            float z0 = __uint_as_float(r[i]) + b_gate, z1 = __uint_as_float(r[i + 1]) + b_gate;
+                            act_value2<ACT>(z0, z1);
+                            r[i] = __float_as_uint(z0);
+                            r[i + 1] = __float_as_uint(z1);
+                        }
+#pragma unroll
                         for (uint32_t i = 0; i < 16; ++i) {
-                            float z = act_value<ACT>(__uint_as_float(r[i]) + b_gate);
+                            float z = __uint_as_float(r[i]);
                             if (NG == 2) z *= __uint_as_float(r2[i]) + b_up;
                             // Columns past F meet zero rows of W2: they must be finite.
                             const bf16 v = __float2bfloat16_rn(inside ? z : 0.f);
