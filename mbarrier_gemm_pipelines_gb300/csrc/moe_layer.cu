@@ -222,14 +222,28 @@ __device__ __forceinline__ int32_t mul_div(int32_t a, int32_t b, int32_t c) {
 
 // The cut of the list of units, the same in every CTA.  It is made in grains
 // of one unit, or of two where that leaves the largest part no larger: two
-// units fill a 128-column tile, one costs the tensor core as much.
+// units fill a 128-column tile, one costs the tensor core as much.  Where that
+// leaves the largest part no larger either, every expert gets its own equal
+// number of parts; else parts run on from one expert into the next.
 struct Cut {
     int32_t grain;                                      // units
     int32_t per_expert;                                 // grains of an expert
     int32_t total;                                      // grains of all chosen experts
     int32_t parts;
-    __device__ __forceinline__ int32_t begin(int32_t v) const { return mul_div(v, total, parts); }
-    // The part that holds grain u: the last v with begin(v) <= u.
+    int32_t own;                                        // parts of each expert, 0: running on
+    __device__ __forceinline__ int32_t begin(int32_t v) const {
+        if (own == 0) return mul_div(v, total, parts);
+        const int32_t x = v / own;
+        return x * per_expert + mul_div(v - x * own, per_expert, own);
+    }
+    // The parts of the x-th chosen expert: the first, and how many.
+    __device__ __forceinline__ int32_t first(int32_t x) const { return own ? x * own : part_of(x * per_expert); }
+    __device__ __forceinline__ int32_t count(int32_t x) const {
+        return own ? own : part_of((x + 1) * per_expert - 1) - part_of(x * per_expert) + 1;
+    }
+
+private:
+    // Running on: the part that holds grain u, the last v with begin(v) <= u.
     __device__ __forceinline__ int32_t part_of(int32_t u) const {
         const uint64_t p = (uint64_t(uint32_t(u)) + 1) * uint32_t(parts) + uint32_t(total) - 1;
         return int32_t((p >> 32) == 0 ? uint32_t(p) / uint32_t(total) : uint32_t(p / uint32_t(total))) - 1;
@@ -266,6 +280,10 @@ __device__ __forceinline__ Cut make_cut(const ExpertParams& P, int32_t active) {
     const int32_t per = c.grain == 2 ? per2 : per1;
     const int32_t rounds = (per + P.max_units - 1) / P.max_units;
     c.parts = min(P.sms * rounds, c.total);
+    c.own = min(P.sms * rounds / active, c.per_expert);
+    const int32_t largest = c.own > 0 ? (c.per_expert + c.own - 1) / c.own * c.grain : per + 1;
+    if (largest <= per && largest <= P.max_units) c.parts = active * c.own;
+    else c.own = 0;
     return c;
 }
 
@@ -295,9 +313,8 @@ __device__ __forceinline__ void build_tables(const ExpertParams& P, Tables& tb) 
             const int32_t x = x0 + int32_t(lane);
             int32_t rows = 0, sum;
             if (x < active) {
-                const int32_t f = cut.part_of(x * cut.per_expert), l = cut.part_of((x + 1) * cut.per_expert - 1);
-                tb.first[x] = f;
-                rows = (l - f + 1) * __popcll(tb.mask[tb.active[x]]);
+                tb.first[x] = cut.first(x);
+                rows = cut.count(x) * __popcll(tb.mask[tb.active[x]]);
             }
             const int32_t before = warp_exclusive(rows, lane, sum);
             if (x < active) tb.base[x] = base + before;
@@ -559,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_expert_kernel(const __grid_co
                 PairParts q;
                 q.row0 = tb.base[x] + __popcll(tb.mask[e] & ((1ull << t) - 1));
                 q.step = __popcll(tb.mask[e]);
-                q.count = cut.part_of((x + 1) * cut.per_expert - 1) - tb.first[x] + 1;
+                q.count = cut.count(x);
                 q.expert = e;
                 P.pairs[i] = q;
             }
