@@ -666,11 +666,11 @@ __global__ void __launch_bounds__(kThreads, 1) moe_expert_kernel(const __grid_co
                         ptx::tmem_ld_32x32b_x16(acc + uint32_t(g) * t_pad + t, r);
                         ptx::tmem_ld_wait();
 #pragma unroll
-                        for (uint32_t i = 0; i < 16; ++i)
-                            if ((bits >> i) & 1u) {
-                                if (d < a.D) *o = __uint_as_float(r[i]);
-                                o += a.D;
-                            }
+                        for (uint32_t i = 0; i < 16; ++i) {
+                            const uint32_t on = (bits >> i) & 1u;
+                            if (on != 0 && d < a.D) *o = __uint_as_float(r[i]);
+                            o += on * uint32_t(a.D);
+                        }
                     }
                 }
                 acc_done();
