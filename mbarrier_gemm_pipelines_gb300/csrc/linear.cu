@@ -365,7 +365,10 @@ int run_product(Product p, const LibCtx& c, cudaStream_t stream) {
 // on 8 columns and walks down its rows, two at a time; a CTA is TX threads
 // along the columns and 256 / TX along the rows, and a cluster of 8 CTAs shares
 // the rows.  Sums: in a thread, then over the CTA's rows of threads, then over
-// the cluster's CTAs in rank order, so that they never depend on timing.
+// the cluster's CTAs in rank order, so that they never depend on timing.  Where
+// the columns alone do not fill the GPU the rows are cut into `chunks` as well
+// (blockIdx.y), whose sums go to scratch and are added in order by a second,
+// small kernel (7954 x 88: 48 us with one cluster, whose CTAs read 1000 rows each).
 // Two rows a turn and registers for four CTAs an SM: 58 us of 4096 x 14336
 // GELU (235 MB read, 4 TB/s; no dZ); four rows 68, six CTAs 72.
 constexpr int kDzThreads = 256, kDzCluster = 8, kDzRows = 2, kDzCtas = 4;
@@ -373,14 +376,15 @@ constexpr int kDzThreads = 256, kDzCluster = 8, kDzRows = 2, kDzCtas = 4;
 // VEC: rows of dC and Z start on 16 bytes.  The loads of kDzRows rows are
 // issued, as raw 16 bytes, before the first is used.
 template <int ACT, int TX, bool VEC>
-__global__ void __launch_bounds__(kDzThreads, kDzCtas) dz_kernel(const LinearGradArgs a) {
+__global__ void __launch_bounds__(kDzThreads, kDzCtas) dz_kernel(const LinearGradArgs a, float* sums) {
     __shared__ float part[kDzThreads / TX][TX * 8];
     ptx::griddep_wait();
     const uint32_t rank = ptx::cluster_ctarank();
     const int32_t tx = int32_t(threadIdx.x) % TX, ty = int32_t(threadIdx.x) / TX;
     const int32_t c = (int32_t(blockIdx.x / kDzCluster) * TX + tx) * 8, left = a.N - c;
     constexpr int32_t kPer = kDzThreads / TX;
-    const int32_t r0 = int32_t(int64_t(a.M) * rank / kDzCluster), r1 = int32_t(int64_t(a.M) * (rank + 1) / kDzCluster);
+    const int64_t share = int64_t(blockIdx.y) * kDzCluster + rank, shares = int64_t(gridDim.y) * kDzCluster;
+    const int32_t r0 = int32_t(a.M * share / shares), r1 = int32_t(a.M * (share + 1) / shares);
     const bf16 *dC = static_cast<const bf16*>(a.dC.p) + c, *Z = static_cast<const bf16*>(a.Z.p) + c;
     bf16* dZ = static_cast<bf16*>(a.dZ.w());
     float sum[8] = {};
@@ -443,9 +447,20 @@ __global__ void __launch_bounds__(kDzThreads, kDzCtas) dz_kernel(const LinearGra
 #pragma unroll
         for (uint32_t s = 0; s < kDzCluster; ++s)
             t += __uint_as_float(ptx::ld_shared_cluster_u32(ptx::mapa_shared(at, s)));
-        a.dbias[n] = t;
+        if (sums != nullptr) sums[int64_t(blockIdx.y) * a.N + n] = t;
+        else a.dbias[n] = t;
     }
     ptx::cluster_sync_all();   // the peers' sums have been read
+}
+
+__global__ void __launch_bounds__(256) dbias_kernel(const float* sums, float* dbias, int32_t N, int32_t chunks) {
+    ptx::griddep_wait();
+    const int32_t n = int32_t(blockIdx.x * 256 + threadIdx.x);
+    if (n >= N) return;
+    float t = 0.f;
+#pragma unroll 8
+    for (int32_t c = 0; c < chunks; ++c) t += sums[int64_t(c) * N + n];
+    dbias[n] = t;
 }
 
 template <int TX, bool VEC>
@@ -477,14 +492,31 @@ int launch_linear(const LinearArgs& a, const LibCtx& c, cudaStream_t stream) {
 int launch_linear_dz(const LinearGradArgs& a, const LibCtx& c, cudaStream_t stream) {
     LinearGradArgs arg = a;
     const bool vec = vec16(a.dC) && vec16(a.Z);
-    void* args[] = {&arg};
-    // 128 columns a CTA.
+    // 128 columns a CTA; rows cut until there are two CTAs an SM, as long as a
+    // CTA keeps 128 rows.
     constexpr int kTx = 16;
     const int64_t tiles = cdiv(a.N, kTx * 8);
-    const cudaError_t e = launch_kernel(vec ? dz_kernel_ptr<kTx, true>(a.act) : dz_kernel_ptr<kTx, false>(a.act),
-                                        dim3(unsigned(tiles * kDzCluster)), kDzThreads, 0, kDzCluster, args, stream);
+    const int64_t chunks = std::max<int64_t>(
+        1, std::min<int64_t>(2 * int64_t(c.sm_count) / (tiles * kDzCluster), a.M / (128 * kDzCluster)));
+    Scratch ws(c, stream);
+    void* sums = nullptr;
+    if (chunks > 1 && a.dbias != nullptr) {
+        const int r = ws.take(size_t(chunks) * size_t(a.N) * sizeof(float), "cudaMallocFromPoolAsync(dbias)", &sums);
+        if (r != GBR_OK) return r;
+    }
+    void* args[] = {&arg, &sums};
+    cudaError_t e = launch_kernel(vec ? dz_kernel_ptr<kTx, true>(a.act) : dz_kernel_ptr<kTx, false>(a.act),
+                                  dim3(unsigned(tiles * kDzCluster), unsigned(chunks)), kDzThreads, 0, kDzCluster,
+                                  args, stream);
     if (e != cudaSuccess) return report_cuda(e, "launching the gradient's dZ");
     count_launch();
+    if (sums != nullptr) {
+        int32_t n = int32_t(chunks);
+        void* bargs[] = {&sums, &arg.dbias, &arg.N, &n};
+        e = launch_kernel(reinterpret_cast<void*>(&dbias_kernel), dim3(unsigned(cdiv(a.N, 256))), 256, 0, 1, bargs, stream);
+        if (e != cudaSuccess) return report_cuda(e, "launching the sums of dbias");
+        count_launch();
+    }
     return GBR_OK;
 }
 
