@@ -442,3 +442,59 @@ def test_feed_forward_block(gbr):
         # Two products in a row: the operand roundings of both.
         assert rel(grads[name], w) <= 2 * TWO, name
     gbr.check_device()
+
+
+@pytest.mark.parametrize("K", [16, 24])
+def test_linear_past_32_bits(gbr, K):
+    """More than 2^31 outputs, and than 2^32 bytes: the first and last rows of C, Z and dA."""
+    M, N = 270336, 8008
+    g = rng(K)
+    A, B = normal(g, (M, K)), normal(g, (K, N), 1 / math.sqrt(K))
+    R = torch.zeros(M, N, device="cuda", dtype=BF)
+    R[-3:] = 1.0
+    C, Z = gbr.gemm_bias_act(A, B, residual=R, act="silu", p=0.25, seed=8, C=R, return_z=True)
+    gbr.check_device()
+    for rows in (slice(0, 4), slice(M // 2, M // 2 + 4), slice(M - 4, M)):
+        z = A[rows].double() @ B.double()
+        close(Z[rows], z, ONE)
+        scale = ref.keep_mask(1, 8, 0.25, 8, 0)[1]
+        kept = C[rows].double() - (torch.arange(M)[rows] >= M - 3).double().cuda()[:, None]
+        on = (kept != 0).double()
+        close(kept, on * ref.act(z, "silu") * scale, 2 * TWO)     # (the residual 1 is rounded along)
+        assert abs(on.mean().item() - 0.75) <= 0.02
+    assert torch.equal(C[:4] != 0, ref.keep_mask(4, N, 0.25, 8, 0, "cuda")[0])
+    dA, dB, db = gbr.gemm_bias_act_backward(Z, A, B, needs=(True, True, True))
+    gbr.check_device()
+    for rows in (slice(0, 4), slice(M - 4, M)):
+        close(dA[rows], Z[rows].double() @ B.double().t(), TWO)
+    close(db, Z.sum(0, dtype=torch.float64), 2.0 ** -12)
+
+
+def test_moe_past_32_bits(gbr):
+    """Experts whose weights start beyond 2^31 elements."""
+    T, D, F, E = 3, 2048, 8192, 160
+    g = rng(6)
+    X, Wr = normal(g, (T, D)), torch.zeros(D, E, device="cuda")
+    Wr[0, E - 1], Wr[0, E // 2], Wr[0, 0] = 3.0, 2.0, 1.0
+    X[:, 0] = 1.0
+    W1, W2 = (torch.zeros(E, *s, device="cuda", dtype=BF) for s in ((D, F), (F, D)))
+    for e in (0, E // 2, E - 1):
+        W1[e], W2[e] = normal(g, (D, F), D ** -0.5), normal(g, (F, D), F ** -0.5)
+    Y, ids, w = gbr.moe_layer(X, Wr, W1, None, W2, None, top_k=3, return_routing=True)
+    gbr.check_device()
+    assert torch.equal(ids.cpu(), torch.tensor([E - 1, E // 2, 0]).expand(T, 3))
+    close(Y, ref.moe(X, Wr, W1, None, W2, None, 3, "relu", False)[0], TWO)
+
+
+def test_more_rows_than_tiles_of_a_launch(gbr):
+    """Few columns and very many rows: every row tile is visited."""
+    M, K, N = 600011, 8, 8
+    g = rng(1)
+    A, B = normal(g, (M, K)), normal(g, (K, N))
+    close(gbr.gemm_bias_act(A, B), A.double() @ B.double(), ONE)
+    dA, dB, db = gbr.gemm_bias_act_backward(A, A, B)
+    gbr.check_device()
+    close(dA, A.double() @ B.double().t(), TWO)
+    close(dB, A.double().t() @ A.double(), TWO)
+    bound = (2.0 ** -19 + M * 2.0 ** -24) * A.double().abs().sum(0)
+    assert ((db.double() - A.double().sum(0)).abs() <= bound).all()
