@@ -427,6 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_expert_kernel(const __grid_co
     if (warp == 4 && lane == 0) {
         // ------------------------------------------------------ producer
         bool ok = true;
+        const uint64_t once = ptx::l2_policy_evict_first();
         auto stage = [&](uint32_t bytes) -> uint32_t {
             ok = mbar_wait(ptx::smem_addr(empty + ring.slot), ring.phase ^ 1u, P.ctl, abort_flag,
                            kSiteProducerEmpty, ring.count);
@@ -454,8 +455,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_expert_kernel(const __grid_co
                             if (!ok) break;
                             const uint32_t bar = ptx::smem_addr(full + ring.slot);
                             const int32_t col = g * a.F + (s.u0 + u) * kUnit;
-                            ptx::tma_load_3d(dst, &P.mapW1, bar, col, k, s.expert);
-                            if (two) ptx::tma_load_3d(dst + panel, &P.mapW1, bar, col + kUnit, k, s.expert);
+                            ptx::tma_load_3d_hint(dst, &P.mapW1, bar, col, k, s.expert, once);
+                            if (two) ptx::tma_load_3d_hint(dst + panel, &P.mapW1, bar, col + kUnit, k, s.expert, once);
                             ring.step(S);
                         }
                     }
@@ -469,8 +470,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_expert_kernel(const __grid_co
                         const uint32_t dst = stage(half ? 2 * kSliceBytes : stage_bytes);
                         if (!ok) break;
                         const uint32_t bar = ptx::smem_addr(full + ring.slot);
-                        ptx::tma_load_3d(dst, map, bar, d, (s.u0 + b) * kUnit, s.expert);
-                        ptx::tma_load_3d(dst + panel, map, bar, d + 64, (s.u0 + b) * kUnit, s.expert);
+                        ptx::tma_load_3d_hint(dst, map, bar, d, (s.u0 + b) * kUnit, s.expert, once);
+                        ptx::tma_load_3d_hint(dst + panel, map, bar, d + 64, (s.u0 + b) * kUnit, s.expert, once);
                         ring.step(S);
                     }
                 }
