@@ -119,14 +119,14 @@ int aligned_mat(Mat* m, int32_t rows, int32_t cols, bool copy_in, Scratch& ws, c
     return GBR_OK;
 }
 
-// A 2-D map over rows x cols bf16 with the 128-byte swizzle.
+// A 2-D map over rows x cols bf16.
 int map_2d(CUtensorMap* map, const Mat& m, int64_t rows, int64_t cols, uint32_t box_cols, uint32_t box_rows,
-           const char* what) {
+           const char* what, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
     const uint64_t dims[2] = {uint64_t(cols), uint64_t(rows)};
     const uint64_t strides[1] = {uint64_t(m.ld) * 2};
     const uint32_t box[2] = {box_cols, box_rows};
     return encode_tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, m.p, dims, strides, box,
-                             CU_TENSOR_MAP_SWIZZLE_128B, what);
+                             swizzle, what);
 }
 
 // ------------------------------------------------------------ CTA pairs
@@ -140,24 +140,6 @@ struct Product {
     void* pair_kernel;             // linear_pair.cuh
     void* tile_kernel;             // linear_tile.cuh
 };
-
-int check_split(void* kernel) {
-    // setmaxnreg draws on the registers of the launch: 128 threads each side.
-    static std::mutex mu;
-    static std::map<void*, bool> known;
-    std::lock_guard<std::mutex> lk(mu);
-    auto it = known.find(kernel);
-    if (it == known.end()) {
-        cudaFuncAttributes fa;
-        const cudaError_t e = cudaFuncGetAttributes(&fa, kernel);
-        if (e != cudaSuccess) return report_cuda(e, "cudaFuncGetAttributes(linear)");
-        const bool ok = long(fa.numRegs) * linear::kThreads >= 128L * (linear::kRegsRoles + 2 * linear::kRegsEpilogue);
-        it = known.emplace(kernel, ok).first;
-    }
-    if (!it->second)
-        return report_errorf(GBR_ERR_CUDA, "a linear kernel was built with too few registers for its role split");
-    return GBR_OK;
-}
 
 // The tiles of a product on `units` CTA pairs.  The last round is split where
 // it has tiles for at most half of the pairs and half a tile's products are
@@ -188,7 +170,8 @@ int run_pair(const Product& p, const LibCtx& c, cudaStream_t stream) {
     linear::PairParams P;
     memset(&P, 0, sizeof(P));
     int r;
-    if ((r = map_2d(&P.mapC, p.C, p.I, p.J, 64, 32, "C")) != GBR_OK) return r;
+    constexpr auto kSw64 = CU_TENSOR_MAP_SWIZZLE_64B;     // the epilogue's 32 x 32 boxes
+    if ((r = map_2d(&P.mapC, p.C, p.I, p.J, 32, 32, "C", kSw64)) != GBR_OK) return r;
     P.mapA = P.mapB = P.mapZ = P.mapR = P.mapC;          // where unused
     if (p.Kc > 0) {
         if ((r = p.a_mn ? map_2d(&P.mapA, p.A, p.Kc, p.I, 64, 64, "A") : map_2d(&P.mapA, p.A, p.I, p.Kc, 64, 128, "A")) !=
@@ -198,8 +181,8 @@ int run_pair(const Product& p, const LibCtx& c, cudaStream_t stream) {
             GBR_OK)
             return r;
     }
-    if (p.Z && (r = map_2d(&P.mapZ, p.Z, p.I, p.J, 64, 32, "Z")) != GBR_OK) return r;
-    if (p.R && (r = map_2d(&P.mapR, p.R, p.I, p.J, 64, 32, "residual")) != GBR_OK) return r;
+    if (p.Z && (r = map_2d(&P.mapZ, p.Z, p.I, p.J, 32, 32, "Z", kSw64)) != GBR_OK) return r;
+    if (p.R && (r = map_2d(&P.mapR, p.R, p.I, p.J, 32, 32, "residual", kSw64)) != GBR_OK) return r;
     P.has_z = bool(p.Z);
     P.has_r = bool(p.R);
     P.bias = p.bias;
@@ -227,8 +210,7 @@ int run_pair(const Product& p, const LibCtx& c, cudaStream_t stream) {
     }
     P.drop = p.drop;
     P.ctl = c.ctl;
-    if ((r = check_split(p.pair_kernel)) != GBR_OK || (r = raise_kernel_smem(p.pair_kernel, linear::kSmemBytes, c.device)) != GBR_OK)
-        return r;
+    if ((r = raise_kernel_smem(p.pair_kernel, linear::kSmemBytes, c.device)) != GBR_OK) return r;
     void* args[] = {&P};
     const int64_t busy = std::min<int64_t>(units, P.w.whole > 0 && P.w.split > 0 ? units : P.w.whole + 2 * P.w.split);
     const cudaError_t e = launch_kernel(p.pair_kernel, dim3(unsigned(2 * busy)), linear::kThreads, linear::kSmemBytes, 2,

@@ -14,14 +14,16 @@
 // CTA and 64-k slice either way, and the matrix descriptors and the
 // instruction descriptor's transpose bits say which.  No operand is copied.
 //
-// Epilogue, 8 warps, each 32 rows x 128 columns of a tile, 64 columns at a time:
+// Epilogue, 16 warps, each 32 rows x 64 columns of a tile, 32 columns at a time:
 //   tcgen05.ld -> + bias -> (Z: round, stage, TMA store) -> activation ->
 //   dropout -> + residual -> round, stage, TMA store
-// through one 4 KiB staging slot a warp; the residual arrives by TMA in the
-// very slot that the result then overwrites.  Two warps a scheduler, not one:
-// with 4 warps the GELU of a tile took longer than the next tile's products
-// (4096 x 4096 x 14336 with Z: 324 us against 254 without activation).
-//
+// through one 2 KiB staging slot a warp; the residual arrives by TMA in the
+// very slot that the result then overwrites.  The chain from the accumulator
+// to the store is long and its parts wait for one another, so it takes warps,
+// four a scheduler, to keep it going.  GELU with Z, 4 / 8 / 16 warps: 4096 x
+// 4096 x 14336 324 / 268 / 265 us (253 without an epilogue), 8192 x 64 x 14336,
+// where it decides, - / 145 / 125 us.
+
 // Split tail: where the last, partial round has tiles for at most half of the
 // pairs, each of those tiles is cut in two along K and given to two pairs.  A
 // part goes to scratch; whoever finishes second adds the other's part to its
@@ -35,7 +37,6 @@ namespace gbr {
 namespace linear {
 
 using umma::kAccCols;
-using umma::kEpiBufBytes;
 using umma::kTmemCols;
 using umma::sw128_desc;
 
@@ -46,15 +47,14 @@ constexpr uint32_t kStageBytes = 2 * kSlices * kSliceBytes;
 constexpr uint32_t kPanelBytes = 64 * 128;
 constexpr uint32_t kBarBytes = 256;
 constexpr size_t kSmemBytes = 1024 + kStages * kStageBytes + kUmmaEpiBytes + kBarBytes;
-constexpr int kThreads = 384;                          // 4 warps of roles, 8 of the epilogue
-constexpr uint32_t kEpiWarps = 8;
-static_assert(kEpiWarps * kEpiBufBytes == kUmmaEpiBytes, "one staging slot a warp");
-// Registers a thread: 72 + 216 + 216 = 3 x 168, what the launch has.
-constexpr uint32_t kRegsRoles = 72, kRegsEpilogue = 216;
+constexpr int kThreads = 640;                          // 4 warps of roles, 16 of the epilogue
+constexpr uint32_t kEpiWarps = 16;
+constexpr uint32_t kSlotBytes = 32 * 64;               // 32 rows x 32 columns
+static_assert(kEpiWarps * kSlotBytes == kUmmaEpiBytes, "one staging slot a warp");
 // fp32 parts of split tiles: per tile, part, CTA of the pair and warp 32 rows x
-// 128 columns as [column / 4][row] float4; before them one arrival count per
+// 64 columns as [column / 4][row] float4; before them one arrival count per
 // tile, CTA and warp, zeroed.
-constexpr int64_t kPartVecs = 32 * 32;
+constexpr int64_t kPartVecs = 16 * 32;
 inline size_t pair_count_bytes(int64_t split_tiles) { return size_t(split_tiles) * 2 * kEpiWarps * 4; }
 inline size_t pair_part_bytes(int64_t split_tiles) { return size_t(split_tiles) * 4 * kEpiWarps * kPartVecs * 16; }
 
@@ -137,8 +137,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* acc_full = empty + kStages;
     uint64_t* acc_empty = acc_full + 2;
     uint64_t* drain = acc_empty + 2;
-    uint64_t* res_full = drain + 1;                    // [8 warps]
-    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(res_full + 8);
+    uint64_t* res_full = drain + 1;                    // [16 warps]
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(res_full + kEpiWarps);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
     uint32_t* issued_word = tmem_holder + 2;
 
@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_init(ptx::smem_addr(acc_empty + a), 2 * kEpiWarps);
         }
         ptx::mbar_init(ptx::smem_addr(drain), 1);
-        for (uint32_t i = 0; i < 8; ++i) ptx::mbar_init(ptx::smem_addr(res_full + i), 1);
+        for (uint32_t i = 0; i < kEpiWarps; ++i) ptx::mbar_init(ptx::smem_addr(res_full + i), 1);
         *abort_flag = 0;
         *issued_word = 0;
         ptx::fence_barrier_init();
@@ -177,7 +177,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t issued = 0;
 
     if (warp < 4) {
-        ptx::setmaxnreg_dec<kRegsRoles>();
         if (warp == 0 && lane == 0) {
             // ---------------------------------------------------- TMA producer
             const uint32_t ring_base = ptx::smem_addr(ring);
@@ -254,13 +253,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_wait_drain(ptx::smem_addr(drain), 0, P.ctl.timeout_ns);
         }
     } else {
-        ptx::setmaxnreg_inc<kRegsEpilogue>();
         // -------------------------------------------------------- epilogue
         const uint32_t q = warp & 3u, ew = warp - 4u;  // TMEM lane quarter; epilogue warp
-        const int32_t col0 = ew < 4u ? 0 : 128;        // first of this warp's columns in the tile
-        const uint32_t slot = ptx::smem_addr(epi) + ew * kEpiBufBytes;
+        const int32_t col0 = int32_t(ew / 4u) * 64;    // first of this warp's columns in the tile
+        const uint32_t slot = ptx::smem_addr(epi) + ew * kSlotBytes;
         const uint32_t res_bar = ptx::smem_addr(res_full + ew);
-        const uint32_t row_off = lane * 128u, swz = lane & 7u;
+        const uint32_t row_off = lane * 64u, swz = (lane >> 1) & 3u;   // 64-byte swizzle
         const bool has_z = !PLAIN && P.has_z != 0, has_r = !PLAIN && P.has_r != 0;
         uint32_t res_issued = 0, res_taken = 0;
         bool ok = true;
@@ -269,16 +267,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t mt, nt;
             raster_tile(w.tile, P.w.m_tiles, P.w.n_tiles, P.w.group_m, mt, nt);
             const int32_t row0 = int32_t(mt * kTile + rank * 128u + q * 32u), n0 = int32_t(nt * kTile) + col0;
-            // 64-column chunks that hold something.
-            const int32_t chunks = row0 < P.M && n0 < P.N ? min(2, (P.N - n0 + 63) / 64) : 0;
+            // 32-column chunks that hold something.
+            const int32_t chunks = row0 < P.M && n0 < P.N ? min(2, (P.N - n0 + 31) / 32) : 0;
             const uint32_t a = tl & 1u, aph = (tl >> 1) & 1u;
             const uint32_t ae = ptx::smem_addr(acc_empty + a);
             // The residual of a chunk, into the staging slot once its last store has read it.
             auto fetch_residual = [&](int32_t c) {
                 if (lane == 0) {
                     ptx::bulk_wait_group_read<0>();
-                    ptx::mbar_arrive_expect_tx(res_bar, kEpiBufBytes);
-                    ptx::tma_load_2d(slot, &P.mapR, res_bar, n0 + c * 64, row0);
+                    ptx::mbar_arrive_expect_tx(res_bar, kSlotBytes);
+                    ptx::tma_load_2d(slot, &P.mapR, res_bar, n0 + c * 32, row0);
                 }
                 ++res_issued;
             };
@@ -299,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float4* blk = P.w.parts + (int64_t(w.sk) * 4 * kEpiWarps + rank * kEpiWarps + ew) * kPartVecs + lane;
                 uint32_t* count = P.w.count + (uint32_t(w.sk) * 2u + rank) * kEpiWarps + ew;
                 float4* mine = blk + w.part * half;
-                for (int32_t c = 0; c < 2 * chunks; ++c) {
+                for (int32_t c = 0; c < chunks; ++c) {
                     uint32_t x[32];
                     ptx::tmem_ld_32x32b_x32(acc + uint32_t(c * 32), x);
                     ptx::tmem_ld_wait();
@@ -322,45 +320,45 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (has_r && !has_z && !early) fetch_residual(0);
             for (int32_t c = 0; c < chunks; ++c) {
-                float z[64];
+                float z[32];
                 {
-                    uint32_t r0[32], r1[32];
-                    ptx::tmem_ld_32x32b_x32(acc + uint32_t(c) * 64u, r0);
-                    ptx::tmem_ld_32x32b_x32(acc + uint32_t(c) * 64u + 32u, r1);
+                    uint32_t raw[32];
+                    ptx::tmem_ld_32x32b_x32(acc + uint32_t(c) * 32u, raw);
                     ptx::tmem_ld_wait();
 #pragma unroll
-                    for (int j = 0; j < 64; ++j) {
-                        z[j] = __uint_as_float(j < 32 ? r0[j] : r1[j - 32]);
-                        if (w.kb1 == w.kb0) z[j] = 0.f;
+                    for (int j = 0; j < 32; ++j) z[j] = __uint_as_float(raw[j]);
+                    if (w.kb1 == w.kb0) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) z[j] = 0.f;
                     }
                 }
                 if (other != nullptr) {
-                    float4 x[16];
+                    float4 x[8];
 #pragma unroll
-                    for (int v = 0; v < 16; ++v) x[v] = __ldcg(other + (c * 16 + v) * 32);
+                    for (int v = 0; v < 8; ++v) x[v] = __ldcg(other + (c * 8 + v) * 32);
 #pragma unroll
-                    for (int v = 0; v < 16; ++v)
+                    for (int v = 0; v < 8; ++v)
                         z[4 * v] += x[v].x, z[4 * v + 1] += x[v].y, z[4 * v + 2] += x[v].z, z[4 * v + 3] += x[v].w;
                 }
                 if (c + 1 == chunks) umma::acc_release<2>(ae, lane);
                 if (!PLAIN && P.bias != nullptr) {
-                    const int32_t n = n0 + c * 64;
+                    const int32_t n = n0 + c * 32;
                     const float* b = P.bias + n;
-                    if (P.bias_vec != 0 && n + 64 <= P.N) {
+                    if (P.bias_vec != 0 && n + 32 <= P.N) {
 #pragma unroll
-                        for (int v = 0; v < 16; ++v) {
+                        for (int v = 0; v < 8; ++v) {
                             const float4 x = __ldg(reinterpret_cast<const float4*>(b) + v);
                             z[4 * v] += x.x, z[4 * v + 1] += x.y, z[4 * v + 2] += x.z, z[4 * v + 3] += x.w;
                         }
                     } else {
 #pragma unroll
-                        for (int j = 0; j < 64; ++j)
+                        for (int j = 0; j < 32; ++j)
                             if (n + j < P.N) z[j] += __ldg(b + j);
                     }
                 }
                 auto stage_and_store = [&](const CUtensorMap* map) {
 #pragma unroll
-                    for (uint32_t j = 0; j < 8; ++j) {
+                    for (uint32_t j = 0; j < 4; ++j) {
                         uint32_t x[4];
 #pragma unroll
                         for (uint32_t u = 0; u < 4; ++u) {
@@ -372,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ptx::fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
-                        ptx::tma_store_2d(map, slot, n0 + c * 64, row0);
+                        ptx::tma_store_2d(map, slot, n0 + c * 32, row0);
                         ptx::bulk_commit_group();
                     }
                 };
@@ -384,13 +382,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (!PLAIN) {
 #pragma unroll
-                    for (int j = 0; j < 64; j += 2) act_value2<ACT>(z[j], z[j + 1]);
+                    for (int j = 0; j < 32; j += 2) act_value2<ACT>(z[j], z[j + 1]);
                 }
                 if (!PLAIN && P.drop.threshold != 0) {
 #pragma unroll
-                    for (int g = 0; g < 8; ++g) {
+                    for (int g = 0; g < 4; ++g) {
                         const uint4 bits = dropout_bits(P.drop, uint32_t(row0) + lane,
-                                                        uint32_t(n0 + c * 64) / 8u + uint32_t(g));
+                                                        uint32_t(n0 + c * 32) / 8u + uint32_t(g));
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
                             z[8 * g + i] = dropout_keep(P.drop, bits, i) ? z[8 * g + i] * P.drop.scale : 0.f;
@@ -403,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     ++res_taken;
 #pragma unroll
-                    for (uint32_t j = 0; j < 8; ++j) {
+                    for (uint32_t j = 0; j < 4; ++j) {
                         const uint4 v = ptx::ld_shared_v4(slot + row_off + ((j ^ swz) << 4));
                         const uint32_t x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
