@@ -518,6 +518,23 @@ int moe_layer(const void *X, const float *Wr, const void *W1, const float *b1, c
               int64_t D, int64_t F, int num_experts, int top_k, int act, int gated, int dtype,
               gbr_stream_t stream);
 
+/*
+ * Failure-detection self tests of these operators' pipelines, as
+ * gbr_selftest_gemm_skip_load: the normal call (contiguous operands, no
+ * epilogue but the rounding; ReLU experts without biases) with the loads of
+ * ring item `item` of CTA `cta` left out (`cta` names the CTA pair where the
+ * product runs on pairs).  The wait for that stage gives up after limit_ns,
+ * every role leaves, and gbr_device_status() reports GBR_ERR_TIMEOUT; the
+ * output is undefined.  An item that the launch does not have plants nothing.
+ */
+int gbr_selftest_linear_skip_load(const void *A, const void *B, void *C, int64_t M, int64_t N,
+                                  int64_t K, int cta, int item, uint64_t limit_ns,
+                                  gbr_stream_t stream);
+int gbr_selftest_moe_skip_load(const void *X, const float *Wr, const void *W1, const void *W2,
+                               void *Y, int64_t T, int64_t D, int64_t F, int num_experts,
+                               int top_k, int cta, int item, uint64_t limit_ns,
+                               gbr_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -20,10 +20,12 @@ from ._binding import (BF16, F32_FFMA, F32_TF32, OP_COPY, OP_GEMM, GbrError, che
                        selftest_noalloc_skip_load, selftest_wait_timeout,
                        set_wait_timeout_ns, sm_count, staged_copy)
 from ._build import build
-from ._operators import (ACTS, dropout_add, gemm_bias_act, gemm_bias_act_backward, moe_layer)
+from ._operators import (ACTS, dropout_add, gemm_bias_act, gemm_bias_act_backward, moe_layer,
+                         selftest_linear_skip_load, selftest_moe_skip_load)
 
 __all__ = [
     "ACTS", "dropout_add", "gemm_bias_act", "gemm_bias_act_backward", "moe_layer",
+    "selftest_linear_skip_load", "selftest_moe_skip_load",
     "BF16", "F32_FFMA", "F32_TF32", "OP_COPY", "OP_GEMM", "GbrError", "build", "check",
     "check_device", "copy_tuning", "device_status", "ffma_tuning", "gemm_dynamic_schedule", "gemm_split_tail", "gemm_thin_tail", "gemm_tuning", "gemm_bias_relu", "gemm_bias_relu_grouped", "gemm_bias_relu_host",
     "last_error", "launch_count", "launch_overlap", "lib", "library_path", "max_stages", "selftest_copy_skip_load",

@@ -57,6 +57,9 @@ SIGNATURES = {
     "gemm_bias_act_backward": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp,
                                       _i64, _vp, _i64, _i64, _i64, _i32, _i32, _f64, _u64, _u64,
                                       _vp]),
+    "gbr_selftest_linear_skip_load": (_i32, [_vp, _vp, _vp, _i64, _i64, _i64, _i32, _i32, _u64, _vp]),
+    "gbr_selftest_moe_skip_load": (_i32, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _i32, _i32,
+                                          _i32, _u64, _vp]),
     "moe_layer": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _i32,
                          _i32, _i32, _i32, _vp]),
 }

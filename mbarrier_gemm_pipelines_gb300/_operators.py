@@ -263,3 +263,28 @@ def moe_layer(X, Wr, W1, b1, W2, b2, top_k=2, act="relu", gated=False, Y=None, r
     _check(lib().moe_layer(px, pr, p1, pb1, p2, pb2, py, pi, pw, T, D, F, E, top_k, _act_code(act),
                            1 if gated else 0, BF16, _stream_of(stream, dev)))
     return (Y, ids, weights) if return_routing else Y
+
+
+def selftest_linear_skip_load(A, B, cta, item, limit_ns, stream=None):
+    """Runs gemm_bias_act (A @ B alone) with one stage of CTA (or CTA pair) `cta`,
+    ring item `item`, left unfilled (see gbr.h); returns the undefined output."""
+    dev = _device_of(A, "A")
+    M, K, N = A.shape[0], A.shape[1], B.shape[1]
+    C = _empty((M, N), dtype=_bf16, device=A.device)
+    _check(lib().gbr_selftest_linear_skip_load(_packed(A, "A", _bf16, dev, (M, K)), _packed(B, "B", _bf16, dev, (K, N)),
+                                               C.data_ptr(), M, N, K, cta, item, limit_ns, _stream_of(stream, dev)))
+    return C
+
+
+def selftest_moe_skip_load(X, Wr, W1, W2, top_k, cta, item, limit_ns, stream=None):
+    """Runs moe_layer (ReLU, no biases) with one stage of CTA `cta`, ring item
+    `item`, left unfilled (see gbr.h); returns the undefined output."""
+    dev = _device_of(X, "X")
+    T, D = X.shape
+    E, F = W2.shape[:2]
+    Y = _empty((T, D), dtype=_bf16, device=X.device)
+    _check(lib().gbr_selftest_moe_skip_load(_packed(X, "X", _bf16, dev, (T, D)), _packed(Wr, "Wr", _f32, dev, (D, E)),
+                                            _packed(W1, "W1", _bf16, dev, (E, D, F)),
+                                            _packed(W2, "W2", _bf16, dev, (E, F, D)), Y.data_ptr(), T, D, F, E,
+                                            top_k, cta, item, limit_ns, _stream_of(stream, dev)))
+    return Y

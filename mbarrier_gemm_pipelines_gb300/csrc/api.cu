@@ -170,14 +170,10 @@ KernelCtl make_ctl(const DevCtx& c) {
 // Runs `call` with a fault injected into the next pipeline launch of this thread.
 template <class F>
 int with_injection(int cta, int item, uint64_t limit_ns, F&& call) {
-    if (cta < 0 || item < 0) return fail(GBR_ERR_INVALID, "self test: cta and item must be >= 0");
-    if (limit_ns == 0 || limit_ns > 10000000000ull)
-        return fail(GBR_ERR_INVALID, "self test: limit must be in (0, 10 s]");
-    t_inject = FaultInjection{1u, cta, item};
-    t_timeout_override = limit_ns;
-    const int r = call();
-    t_inject = FaultInjection{0u, 0, 0};
-    t_timeout_override = 0;
+    int r = begin_injection(cta, item, limit_ns);
+    if (r != GBR_OK) return r;
+    r = call();
+    end_injection();
     return r;
 }
 
@@ -415,6 +411,7 @@ int lib_ctx(LibCtx* out) {
     out->smem_optin = c->smem_optin;
     out->pool = c->pool;
     out->ctl = make_ctl(*c);
+    out->inject = t_inject;
     return GBR_OK;
 }
 int encode_tensor_map(CUtensorMap* map, CUtensorMapDataType dt, uint32_t rank, const void* ptr,
@@ -425,6 +422,18 @@ int encode_tensor_map(CUtensorMap* map, CUtensorMapDataType dt, uint32_t rank, c
 void count_launch() { ++g_launches; }
 uint64_t wait_timeout_ns() { return t_timeout_override ? t_timeout_override : timeout_ns(); }
 FaultInjection injection_now() { return t_inject; }
+int begin_injection(int cta, int item, uint64_t limit_ns) {
+    if (cta < 0 || item < 0) return fail(GBR_ERR_INVALID, "self test: cta and item must be >= 0");
+    if (limit_ns == 0 || limit_ns > 10000000000ull)
+        return fail(GBR_ERR_INVALID, "self test: limit must be in (0, 10 s]");
+    t_inject = FaultInjection{1u, cta, item};
+    t_timeout_override = limit_ns;
+    return GBR_OK;
+}
+void end_injection() {
+    t_inject = FaultInjection{0u, 0, 0};
+    t_timeout_override = 0;
+}
 
 int programmatic_launch_attr(cudaLaunchAttribute* attr) {
     {

@@ -204,6 +204,7 @@ struct LibCtx {
     int smem_optin;
     cudaMemPool_t pool;
     KernelCtl ctl;
+    FaultInjection inject;                     // self-test fault of this thread's next launches
 };
 int lib_ctx(LibCtx* out);                      // GBR_OK or an error code
 int encode_tensor_map(CUtensorMap* map, CUtensorMapDataType dt, uint32_t rank, const void* ptr,
@@ -213,6 +214,9 @@ int encode_tensor_map(CUtensorMap* map, CUtensorMapDataType dt, uint32_t rank, c
 void count_launch();                           // adds one to gbr_launch_count()
 uint64_t wait_timeout_ns();                    // per-wait limit of this thread's next launch
 FaultInjection injection_now();                // self-test fault of this thread's next launch
+// Plants a fault and a wait limit for this thread's launches until end_injection().
+int begin_injection(int cta, int item, uint64_t limit_ns);
+void end_injection();
 
 // ------------------------------------------------------------ self test
 cudaError_t launch_wait_selftest(KernelCtl ctl, cudaStream_t stream);

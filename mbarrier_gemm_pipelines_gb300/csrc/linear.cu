@@ -210,6 +210,7 @@ int run_pair(const Product& p, const LibCtx& c, cudaStream_t stream) {
     }
     P.drop = p.drop;
     P.ctl = c.ctl;
+    P.inject = c.inject;
     if ((r = raise_kernel_smem(p.pair_kernel, linear::kSmemBytes, c.device)) != GBR_OK) return r;
     void* args[] = {&P};
     const int64_t busy = std::min<int64_t>(units, P.w.whole > 0 && P.w.split > 0 ? units : P.w.whole + 2 * P.w.split);
@@ -309,6 +310,7 @@ int run_tile(const Product& p, const TilePlan& plan, const LibCtx& c, cudaStream
     while (int32_t(P.tmem_cols) < plan.bt) P.tmem_cols *= 2;
     P.drop = p.drop;
     P.ctl = c.ctl;
+    P.inject = c.inject;
     const size_t smem = linear::tile_smem_bytes(plan.bt, plan.stages);
     if ((r = raise_kernel_smem(p.tile_kernel, smem, c.device)) != GBR_OK) return r;
     const int64_t ctas = int64_t(P.t_tiles) * cdiv(p.J, 128) * plan.split;

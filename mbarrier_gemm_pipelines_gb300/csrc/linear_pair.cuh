@@ -100,6 +100,7 @@ struct PairParams {
     uint32_t bias_vec;                                 // bias starts on 16 bytes
     Dropout drop;
     KernelCtl ctl;
+    FaultInjection inject;                             // self test only
 };
 
 template <bool A_MN, bool B_MN>
@@ -197,6 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t fb_local = ptx::smem_addr(full + slot);
                     const uint32_t fb = ptx::mapa_shared(fb_local, 0);
                     if (rank == 0) ptx::mbar_arrive_expect_tx(fb_local, 2 * kStageBytes);
+                    if (inject_skip_unit(P.inject, unit, it)) continue;   // self test
                     const uint32_t stage = ring_base + slot * kStageBytes;
 #pragma unroll
                     for (uint32_t h = 0; h < kSlices; ++h) {
@@ -433,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool aborted = *abort_flag != 0 || ptx::ld_shared_cluster_u32(ptx::mapa_shared(flag, 1)) != 0;
         const uint32_t peer = ptx::ld_shared_cluster_u32(ptx::mapa_shared(ptx::smem_addr(issued_word), 1));
         if (aborted)
-            umma::drain_ring<2>(full, kStages, issued, peer, kStageBytes, FaultInjection{0u, 0, 0}, unit,
+            umma::drain_ring<2>(full, kStages, issued, peer, kStageBytes, P.inject, unit,
                                 P.ctl.timeout_ns);
     }
     ptx::cluster_sync_all();

@@ -50,6 +50,7 @@ struct TileParams {
     uint32_t vec;                                      // 16-byte accesses to R, C and Z are aligned
     Dropout drop;
     KernelCtl ctl;
+    FaultInjection inject;                             // self test only
 };
 
 __host__ __device__ constexpr uint32_t tile_stage_bytes(int32_t bt) { return kWideBytes + uint32_t(bt) * 128u; }
@@ -166,17 +167,21 @@ __global__ void __launch_bounds__(kTileThreads)
             const uint32_t bar = ptx::smem_addr(full + slot), dst = ring_base + slot * stage_bytes;
             ptx::mbar_arrive_expect_tx(bar, stage_bytes);
             const int32_t k0 = ks * 64;
-            if (W_MN) {
-                ptx::tma_load_2d(dst, &P.mapW, bar, j0, k0);
-                ptx::tma_load_2d(dst + 64 * 128, &P.mapW, bar, j0 + 64, k0);
+            if (inject_skip(P.inject, issued)) {
+                // self test: the stage's loads are left out
             } else {
-                ptx::tma_load_2d(dst, &P.mapW, bar, k0, j0);
-            }
-            if (X_MN) {
-                for (int32_t b = 0; b < P.bt; b += 64)
-                    ptx::tma_load_2d(dst + kWideBytes + uint32_t(b) * 128u, &P.mapX, bar, i0 + b, k0);
-            } else {
-                ptx::tma_load_2d(dst + kWideBytes, &P.mapX, bar, k0, i0);
+                if (W_MN) {
+                    ptx::tma_load_2d(dst, &P.mapW, bar, j0, k0);
+                    ptx::tma_load_2d(dst + 64 * 128, &P.mapW, bar, j0 + 64, k0);
+                } else {
+                    ptx::tma_load_2d(dst, &P.mapW, bar, k0, j0);
+                }
+                if (X_MN) {
+                    for (int32_t b = 0; b < P.bt; b += 64)
+                        ptx::tma_load_2d(dst + kWideBytes + uint32_t(b) * 128u, &P.mapX, bar, i0 + b, k0);
+                } else {
+                    ptx::tma_load_2d(dst + kWideBytes, &P.mapX, bar, k0, i0);
+                }
             }
             if (++slot == stages) {
                 slot = 0;
@@ -237,7 +242,7 @@ __global__ void __launch_bounds__(kTileThreads)
     if (*abort_flag) {
         if (warp == 5 && lane == 0) mbar_wait_drain(ptx::smem_addr(acc_full), 0, P.ctl.timeout_ns);
         if (warp == 4 && lane == 0)
-            umma::drain_ring<1>(full, stages, issued, 0, stage_bytes, FaultInjection{0u, 0, 0}, blockIdx.x,
+            umma::drain_ring<1>(full, stages, issued, 0, stage_bytes, P.inject, blockIdx.x,
                                 P.ctl.timeout_ns);
     } else {
         const uint32_t part0 = ring_base;

@@ -212,6 +212,7 @@ struct ExpertParams {
     int32_t ksub;                                       // 64-row slices of a stage, 1 or 2
     int32_t sms;
     KernelCtl ctl;
+    FaultInjection inject;                              // self test only
 };
 
 // floor(a b / c), in 32 bits where the product fits.
@@ -455,8 +456,9 @@ __global__ void __launch_bounds__(kThreads, 1) moe_expert_kernel(const __grid_co
                             if (!ok) break;
                             const uint32_t bar = ptx::smem_addr(full + ring.slot);
                             const int32_t col = g * a.F + (s.u0 + u) * kUnit;
-                            ptx::tma_load_3d_hint(dst, &P.mapW1, bar, col, k, s.expert, once);
-                            if (two) ptx::tma_load_3d_hint(dst + panel, &P.mapW1, bar, col + kUnit, k, s.expert, once);
+                            const bool skip = inject_skip(P.inject, ring.count);
+                            if (!skip) ptx::tma_load_3d_hint(dst, &P.mapW1, bar, col, k, s.expert, once);
+                            if (two && !skip) ptx::tma_load_3d_hint(dst + panel, &P.mapW1, bar, col + kUnit, k, s.expert, once);
                             ring.step(S);
                         }
                     }
@@ -470,8 +472,10 @@ __global__ void __launch_bounds__(kThreads, 1) moe_expert_kernel(const __grid_co
                         const uint32_t dst = stage(half ? 2 * kSliceBytes : stage_bytes);
                         if (!ok) break;
                         const uint32_t bar = ptx::smem_addr(full + ring.slot);
-                        ptx::tma_load_3d_hint(dst, map, bar, d, (s.u0 + b) * kUnit, s.expert, once);
-                        ptx::tma_load_3d_hint(dst + panel, map, bar, d + 64, (s.u0 + b) * kUnit, s.expert, once);
+                        if (!inject_skip(P.inject, ring.count)) {
+                            ptx::tma_load_3d_hint(dst, map, bar, d, (s.u0 + b) * kUnit, s.expert, once);
+                            ptx::tma_load_3d_hint(dst + panel, map, bar, d + 64, (s.u0 + b) * kUnit, s.expert, once);
+                        }
                         ring.step(S);
                     }
                 }
@@ -682,11 +686,11 @@ __global__ void __launch_bounds__(kThreads, 1) moe_expert_kernel(const __grid_co
     __syncwarp();
     ptx::tc_fence_before_sync();
     __syncthreads();
-    if (*abort_flag && warp == 4 && lane == 0)
+    if (*abort_flag && warp == 4 && lane == 0) {
         // Stages registered but not consumed: their loads have to land first.
-    {
         for (uint32_t j = ring.count > S ? ring.count - S : 0u; j < ring.count; ++j)
-            mbar_wait_drain(ptx::smem_addr(full + j % S), (j / S) & 1u, P.ctl.timeout_ns);
+            if (!inject_skip(P.inject, j))
+                mbar_wait_drain(ptx::smem_addr(full + j % S), (j / S) & 1u, P.ctl.timeout_ns);
         for (uint32_t j = xring.count > kXStages ? xring.count - kXStages : 0u; j < xring.count; ++j)
             mbar_wait_drain(ptx::smem_addr(x_full + j % kXStages), (j / kXStages) & 1u, P.ctl.timeout_ns);
     }
@@ -858,6 +862,7 @@ int launch_moe(const MoeArgs& a, void* scratch, const LibCtx& c, cudaStream_t st
     P.t_pad = plan.t_pad, P.units = plan.units, P.max_units = plan.max_units, P.stages = plan.stages, P.ksub = plan.ksub;
     P.sms = c.sm_count;
     P.ctl = c.ctl;
+    P.inject = c.inject;
 
     int32_t shift = 0;
     while ((4 << shift) < a.E) ++shift;

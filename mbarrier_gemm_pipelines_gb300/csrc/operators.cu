@@ -317,4 +317,27 @@ int moe_layer(const void* X, const float* Wr, const void* W1, const float* b1, c
     });
 }
 
+// The self tests of the operators' pipelines: the normal call with one stage
+// left unfilled (see gbr_selftest_gemm_skip_load).
+int gbr_selftest_linear_skip_load(const void* A, const void* B, void* C, int64_t M, int64_t N, int64_t K, int cta,
+                                  int item, uint64_t limit_ns, gbr_stream_t stream) {
+    int r = begin_injection(cta, item, limit_ns);
+    if (r != GBR_OK) return r;
+    r = gemm_bias_act(A, K, B, N, nullptr, nullptr, 0, C, N, nullptr, 0, M, N, K, GBR_BF16, GBR_ACT_NONE, 0.0, 0, 0,
+                      stream);
+    end_injection();
+    return r;
+}
+
+int gbr_selftest_moe_skip_load(const void* X, const float* Wr, const void* W1, const void* W2, void* Y, int64_t T,
+                               int64_t D, int64_t F, int num_experts, int top_k, int cta, int item,
+                               uint64_t limit_ns, gbr_stream_t stream) {
+    int r = begin_injection(cta, item, limit_ns);
+    if (r != GBR_OK) return r;
+    r = moe_layer(X, Wr, W1, nullptr, W2, nullptr, Y, nullptr, nullptr, T, D, F, num_experts, top_k, GBR_ACT_RELU, 0,
+                  GBR_BF16, stream);
+    end_injection();
+    return r;
+}
+
 }  // extern "C"

@@ -498,3 +498,45 @@ def test_more_rows_than_tiles_of_a_launch(gbr):
     close(dB, A.double().t() @ A.double(), TWO)
     bound = (2.0 ** -19 + M * 2.0 ** -24) * A.double().abs().sum(0)
     assert ((db.double() - A.double().sum(0)).abs() <= bound).all()
+
+
+LIMIT_NS = 50_000_000
+
+
+def expect_timeout(gbr):
+    with pytest.raises(gbr.GbrError) as e:
+        gbr.check_device()
+    assert e.value.code == 6                                    # GBR_ERR_TIMEOUT
+    gbr.check_device()                                          # reported once
+
+
+@pytest.mark.parametrize("M,K,N,cta,item", [
+    (37, 512, 4096, 0, 0),          # single tiles shared by a cluster: the first CTA's first stage
+    (37, 4096, 4096, 5, 3),         # another CTA, a later stage
+    (2048, 512, 4096, 0, 0),        # CTA pairs: the first item
+    (2048, 2048, 4096, 3, 9),       # another pair, past the ring
+    (2304, 4352, 4096, 1, 40),      # the cut last round
+])
+def test_linear_stage_never_filled(gbr, M, K, N, cta, item):
+    """A stage that is never filled: the wait gives up, the call reports it, the next one is right."""
+    g = rng(M)
+    A, B = normal(g, (M, K)), normal(g, (K, N), 1 / math.sqrt(K))
+    want = gbr.gemm_bias_act(A, B)
+    gbr.check_device()
+    for _ in range(2):
+        gbr.selftest_linear_skip_load(A, B, cta, item, LIMIT_NS)
+        expect_timeout(gbr)
+    assert torch.equal(gbr.gemm_bias_act(A, B), want)
+    gbr.selftest_linear_skip_load(A, B, 100000, 0, LIMIT_NS)    # no such CTA: nothing planted
+    gbr.check_device()
+
+
+@pytest.mark.parametrize("T,cta,item", [(1, 0, 0), (1, 7, 9), (40, 3, 12)])
+def test_moe_stage_never_filled(gbr, T, cta, item):
+    X, Wr, W1, _, W2, _ = moe_inputs(T, 1024, 10240, 4, False, False, T)      # work for every CTA
+    want = gbr.moe_layer(X, Wr, W1, None, W2, None)
+    gbr.check_device()
+    for _ in range(2):
+        gbr.selftest_moe_skip_load(X, Wr, W1, W2, 2, cta, item, LIMIT_NS)
+        expect_timeout(gbr)
+    assert torch.equal(gbr.moe_layer(X, Wr, W1, None, W2, None), want)
