@@ -158,11 +158,4 @@ __device__ __forceinline__ void act_slope2(float& a, float& b, float za, float z
     split2(mul2(f2(a, b), d), a, b);
 }
 
-template <int ACT>
-__device__ __forceinline__ float act_value(float z) {
-    float other = 0.f;
-    act_value2<ACT>(z, other);
-    return z;
-}
-
 }  // namespace gbr

@@ -250,8 +250,10 @@ int gemm_bias_act_backward(const void* dC, int64_t lddc, const void* A, int64_t 
             g.dZ = dz;
         }
         if ((want_bias || g.dZ) && (r = launch_linear_dz(g, c, st)) != GBR_OK) return r;
-        if (want_da && (r = launch_linear_da(dz, {B, ldb}, {dA, ldda}, g.M, g.N, int32_t(K), c, st)) != GBR_OK) return r;
-        if (want_db && (r = launch_linear_db({A, lda}, dz, {dB, lddb}, g.M, g.N, int32_t(K), c, st)) != GBR_OK) return r;
+        if (want_da && (r = launch_linear_da(dz, {B, ldb}, {dA, ldda}, g.M, g.N, int32_t(K), c, st)) != GBR_OK)
+            return r;
+        if (want_db && (r = launch_linear_db({A, lda}, dz, {dB, lddb}, g.M, g.N, int32_t(K), c, st)) != GBR_OK)
+            return r;
         return GBR_OK;
     });
 }
@@ -268,8 +270,8 @@ int moe_layer(const void* X, const float* Wr, const void* W1, const float* b1, c
         if (r != GBR_OK) return r;
         if (F >= kLim / 2) return report_errorf(GBR_ERR_INVALID, "%s: F must be below 2^30", fn);
         if (T > kMoeMaxTokens)
-            return report_errorf(GBR_ERR_INVALID, "%s: at most %d tokens a call (gemm_bias_relu_grouped serves more)", fn,
-                                 kMoeMaxTokens);
+            return report_errorf(GBR_ERR_INVALID, "%s: at most %d tokens a call (gemm_bias_relu_grouped serves more)",
+                                 fn, kMoeMaxTokens);
         if (num_experts < 1 || num_experts > kMoeMaxExperts)
             return report_errorf(GBR_ERR_INVALID, "%s: num_experts must be 1..%d", fn, kMoeMaxExperts);
         if (top_k < 1 || top_k > kMoeMaxTopK || top_k > num_experts)
