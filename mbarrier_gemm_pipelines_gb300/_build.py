@@ -1,17 +1,22 @@
-"""Builds ``libgbr.so`` (the C-ABI library of this package) with nvcc.
+"""Builds ``libgbr.so`` (the C-ABI library of this package) with nvcc, and the
+compiled Python binding of the feed-forward operators with the host compiler.
 
 Every translation unit under ``csrc/`` is compiled for sm_103a only, in
-parallel, then linked into one shared library next to this file.  The result
-is git-ignored and rebuilt on each machine (the library is host-architecture
-specific).
+parallel, then linked into one shared library next to this file.
+``csrc/python/operators_ext.cpp`` becomes ``_operators_ext.so``, the only part
+that is compiled against PyTorch; it is linked to ``libgbr.so``.  The results
+are git-ignored and rebuilt on each machine (they are specific to the host's
+architecture and to its PyTorch).
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
@@ -19,6 +24,8 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJ_DIR = os.path.join(PKG_DIR, "_build")
 LIB_PATH = os.path.join(PKG_DIR, "libgbr.so")
+EXT_SRC = os.path.join(CSRC, "python", "operators_ext.cpp")
+EXT_PATH = os.path.join(PKG_DIR, "_operators_ext.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -38,14 +45,42 @@ def _sources():
 
 def _deps():
     return (_sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
-            + glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)])
+            + glob.glob(os.path.join(INCLUDE, "*.h")) + [EXT_SRC, os.path.abspath(__file__)])
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not (os.path.exists(LIB_PATH) and os.path.exists(EXT_PATH)):
         return False
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(EXT_PATH))
     return all(os.path.getmtime(p) <= t for p in _deps())
+
+
+def _compile_ext(obj: str) -> str:
+    """Compiles the Python binding to an object file; returns PyTorch's folder."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        raise RuntimeError("PyTorch not found; the Python binding is compiled against its headers")
+    torch_dir = list(spec.submodule_search_locations)[0]
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    include = [INCLUDE, os.path.join(torch_dir, "include"),
+               os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    cmd = (["g++", "-O2", "-std=c++17", "-fPIC", "-c", EXT_SRC, "-o", obj] + ["-I" + i for i in include])
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("g++ failed for %s:\n%s\n%s" % (EXT_SRC, res.stdout, res.stderr))
+    return torch_dir
+
+
+def _link_ext(obj: str, torch_dir: str) -> None:
+    tmp = EXT_PATH + ".tmp%d" % os.getpid()
+    lib = os.path.join(torch_dir, "lib")
+    cmd = ["g++", "-shared", "-o", tmp, obj, LIB_PATH, "-Wl,-rpath,$ORIGIN", "-L" + lib, "-ltorch_python", "-ltorch",
+           "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("link of the Python binding failed:\n%s\n%s" % (res.stdout, res.stderr))
+    os.replace(tmp, EXT_PATH)
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
@@ -65,18 +100,22 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
         return obj, res.stderr
 
     srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    ext_obj = os.path.join(OBJ_DIR, "operators_ext.o")
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
+        ext = ex.submit(_compile_ext, ext_obj)
         results = list(ex.map(compile_one, srcs))
+        torch_dir = ext.result()
     if verbose or ptxas_verbose:
         for _, log in results:
             if log.strip():
                 print(log)
     tmp = LIB_PATH + ".tmp%d" % os.getpid()
-    cmd = [nvcc] + ARCH + ["-shared", "-o", tmp] + [o for o, _ in results]
+    cmd = [nvcc] + ARCH + ["-shared", "-Xlinker", "-soname=libgbr.so", "-o", tmp] + [o for o, _ in results]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError("link failed:\n%s\n%s" % (res.stdout, res.stderr))
     os.replace(tmp, LIB_PATH)
+    _link_ext(ext_obj, torch_dir)
     return LIB_PATH
 
 

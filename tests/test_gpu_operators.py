@@ -12,6 +12,7 @@ mean square over values of all sizes; U = 2^-9 = 1.95e-3 is that with a margin)
   dropout, fp32  three roundings: 2^-22 (|x| scale + |r|), elementwise
 """
 import math
+import sys
 
 import pytest
 import torch
@@ -540,3 +541,67 @@ def test_moe_stage_never_filled(gbr, T, cta, item):
         gbr.selftest_moe_skip_load(X, Wr, W1, W2, 2, cta, item, LIMIT_NS)
         expect_timeout(gbr)
     assert torch.equal(gbr.moe_layer(X, Wr, W1, None, W2, None), want)
+
+
+def test_binding_arguments(gbr):
+    """What the binding refuses on a GPU tensor, with the exception's type; and it keeps no reference."""
+    A, B = (torch.ones(16, 16, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    f, dC, Z = A.float(), A.clone(), A.clone()
+    vec = torch.ones(16, device="cuda")
+
+    def refused(kind, fn, *a, **kw):
+        with pytest.raises(kind):
+            fn(*a, **kw)
+
+    fwd, bwd = gbr.gemm_bias_act, gbr.gemm_bias_act_backward
+    for t in (f, A.half()):
+        refused(TypeError, fwd, t, B)
+        refused(TypeError, fwd, A, t)
+        refused(TypeError, fwd, A, B, residual=t)
+        refused(TypeError, fwd, A, B, C=t)
+        refused(TypeError, bwd, t, A, B)
+    refused(TypeError, fwd, A, B, vec.bfloat16())
+    refused(TypeError, fwd, A, B, p="0.5")
+    for bad in (A[:, :15], A[0], A[None]):
+        refused(ValueError, fwd, bad, B)
+        refused(ValueError, fwd, A, B, residual=bad)
+        refused(ValueError, fwd, A, B, C=bad)
+        refused(ValueError, fwd, A, B, Z=bad)
+        refused(ValueError, bwd, dC, A, B, dA=bad)
+    refused(ValueError, fwd, torch.ones(16, 32, device="cuda", dtype=torch.bfloat16)[:, ::2], B)
+    refused(ValueError, fwd, A, B, vec[:8])
+    refused(ValueError, fwd, A, B, vec.cpu())
+    refused(ValueError, fwd, A, B, torch.ones(32, device="cuda")[::2])
+    for act in ("tanh", 1, None, "relu\0"):
+        refused(ValueError, fwd, A, B, act=act)
+    for seed in (-1, 1 << 64, 0.5, "1", None):
+        refused(ValueError, fwd, A, B, seed=seed, p=0.5)
+        refused(ValueError, gbr.dropout_add, A, offset=seed)
+    refused(ValueError, bwd, dC, A, B, act="relu")
+    refused(ValueError, bwd, dC, A, B, needs=(True, True))
+    refused(TypeError, bwd, dC, A, B, needs=3)
+    refused(ValueError, bwd, dC, A, B, dbias=vec[:8])
+    refused(gbr.GbrError, fwd, A, B, p=1.5)
+    refused(gbr.GbrError, gbr.dropout_add, A, p=-0.5)
+    W1, W2, Wr = A[None].expand(4, 16, 16).contiguous(), A[None].expand(4, 16, 16).contiguous(), f[:, :4].contiguous()
+    refused(ValueError, gbr.moe_layer, A, Wr, W1, None, W2, None, gated=True)
+    refused(ValueError, gbr.moe_layer, A, f, W1, None, W2, None)
+    refused(ValueError, gbr.moe_layer, A, Wr, A, None, W2, None)
+    refused(ValueError, gbr.moe_layer, A, Wr, W1, vec, W2, None)
+    for k in (-1, 0, 5, 1 << 40):
+        refused(gbr.GbrError, gbr.moe_layer, A, Wr, W1, None, W2, None, top_k=k)
+
+    C = torch.empty_like(A)
+    held = [sys.getrefcount(t) for t in (A, B, C, Z, vec)]
+    needs = (True, False, True)
+    for _ in range(20):
+        assert fwd(A, B, vec, C=C) is C
+        c, z = fwd(A, B, vec, C=C, Z=Z)
+        assert c is C and z is Z
+        assert gbr.dropout_add(A, A, p=0.5, Y=C) is C
+        dA, dB, db = bwd(dC, A, B, Z, act="relu", dA=C, needs=needs)
+        assert dA is C and dB is None and db.dtype == torch.float32 and db.shape == (16,)
+        assert gbr.moe_layer(A, Wr, W1, None, W2, None, Y=C) is C
+        refused(gbr.GbrError, fwd, A, B, vec, C=C, p=1.5)
+    del c, z, dA
+    assert held == [sys.getrefcount(t) for t in (A, B, C, Z, vec)]

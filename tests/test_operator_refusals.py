@@ -121,6 +121,28 @@ def test_binding_refuses_cpu_tensors(lib):
         gbr.dropout_add(a.half())
 
 
+def test_binding_refuses_other_objects(lib):
+    import mbarrier_gemm_pipelines_gb300 as gbr
+    for bad in (None, 1, [[1.0]], "A"):
+        with pytest.raises(TypeError):
+            gbr.gemm_bias_act(bad, bad)
+        with pytest.raises(TypeError):
+            gbr.gemm_bias_act_backward(bad, bad, bad)
+        with pytest.raises(TypeError):
+            gbr.dropout_add(bad)
+        with pytest.raises(TypeError):
+            gbr.moe_layer(bad, bad, bad, None, bad, None)
+
+
+def test_binding_missing_build(lib, monkeypatch, tmp_path):
+    """Without its compiled part the binding raises; it has nothing to fall back to."""
+    from mbarrier_gemm_pipelines_gb300 import _build, _operators
+    monkeypatch.setattr(_operators, "_ext", None)
+    monkeypatch.setattr(_build, "EXT_PATH", str(tmp_path / "absent.so"))
+    with pytest.raises(RuntimeError, match="not built"):
+        _operators.dropout_add(torch.zeros(2, 2))
+
+
 @pytest.mark.parametrize("counter,key,out", [
     ((0,) * 4, (0,) * 2, (0x6627e8d5, 0xe169c58d, 0xbc57ac4c, 0x9b00dbd8)),
     ((0xffffffff,) * 4, (0xffffffff,) * 2, (0x408f276d, 0x41c83b0e, 0xa20bc7c6, 0x6d5451fd)),
