@@ -48,6 +48,7 @@ struct TileParams {
     int32_t stages;
     uint32_t tmem_cols;
     uint32_t vec;                                      // 16-byte accesses to R, C and Z are aligned
+    uint32_t beside;                                   // runs next to the grid before it
     Dropout drop;
     KernelCtl ctl;
     FaultInjection inject;                             // self test only
@@ -156,7 +157,7 @@ __global__ void __launch_bounds__(kTileThreads)
     ptx::tc_fence_after_sync();
     const uint32_t tmem = *tmem_holder;
     const uint32_t ring_base = ptx::smem_addr(ring);
-    ptx::griddep_wait();
+    if (!P.beside) ptx::griddep_wait();
 
     uint32_t issued = 0;
     if (warp == 4 && lane == 0) {
@@ -280,6 +281,7 @@ __global__ void __launch_bounds__(kTileThreads)
         ptx::tc_fence_after_sync();
         ptx::tmem_dealloc(tmem, P.tmem_cols);
     }
+    if (P.beside) ptx::griddep_wait();   // this grid ends after the one before it
 }
 
 }  // namespace linear

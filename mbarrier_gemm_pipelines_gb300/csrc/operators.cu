@@ -250,9 +250,12 @@ int gemm_bias_act_backward(const void* dC, int64_t lddc, const void* A, int64_t 
             g.dZ = dz;
         }
         if ((want_bias || g.dZ) && (r = launch_linear_dz(g, c, st)) != GBR_OK) return r;
-        if (want_da && (r = launch_linear_da(dz, {B, ldb}, {dA, ldda}, g.M, g.N, int32_t(K), c, st)) != GBR_OK)
+        bool beside = false;
+        if (want_da &&
+            (r = launch_linear_da(dz, {B, ldb}, {dA, ldda}, g.M, g.N, int32_t(K), c, st, &beside)) != GBR_OK)
             return r;
-        if (want_db && (r = launch_linear_db({A, lda}, dz, {dB, lddb}, g.M, g.N, int32_t(K), c, st)) != GBR_OK)
+        if (want_db &&
+            (r = launch_linear_db({A, lda}, dz, {dB, lddb}, g.M, g.N, int32_t(K), c, st, beside)) != GBR_OK)
             return r;
         return GBR_OK;
     });

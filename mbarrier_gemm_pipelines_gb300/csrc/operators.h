@@ -76,8 +76,12 @@ int launch_linear_dz(const LinearGradArgs& a, const LibCtx& c, cudaStream_t stre
 
 // The gradients' products: dA[M, K] = dZ[M, N] B[K, N]^T and
 // dB[K, N] = A[M, K]^T dZ[M, N].
-int launch_linear_da(Mat dZ, Mat B, Mat dA, int32_t M, int32_t N, int32_t K, const LibCtx& c, cudaStream_t stream);
-int launch_linear_db(Mat A, Mat dZ, Mat dB, int32_t M, int32_t N, int32_t K, const LibCtx& c, cudaStream_t stream);
+// `one_launch`: the product was a single launch without scratch, so that the
+// product of dB may run `beside` it if it is the next launch.
+int launch_linear_da(Mat dZ, Mat B, Mat dA, int32_t M, int32_t N, int32_t K, const LibCtx& c, cudaStream_t stream,
+                     bool* one_launch);
+int launch_linear_db(Mat A, Mat dZ, Mat dB, int32_t M, int32_t N, int32_t K, const LibCtx& c, cudaStream_t stream,
+                     bool beside);
 
 // ------------------------------------------------------------ expert layer
 constexpr int kMoeMaxTokens = 64, kMoeMaxExperts = 256, kMoeMaxTopK = 8;

@@ -605,3 +605,27 @@ def test_binding_arguments(gbr):
         refused(gbr.GbrError, fwd, A, B, vec, C=C, p=1.5)
     del c, z, dA
     assert held == [sys.getrefcount(t) for t in (A, B, C, Z, vec)]
+
+
+@pytest.mark.parametrize("M,K,N", [(301, 520, 1000), (64, 512, 8192), (2048, 64, 64), (16, 4096, 16),
+                                   (1536, 1536, 4096), (300, 4096, 2560)])
+@pytest.mark.parametrize("act", ["none", "gelu"])
+def test_gradients_side_by_side(gbr, M, K, N, act):
+    """dA and dB may run next to one another: each has the bits of a call for it alone, and what follows the call in
+    its stream (an operator whose launch overlaps, or any other kernel) finds both finished."""
+    g = torch.Generator(device="cuda").manual_seed(M + K + N)
+    A, B, dC, Z = (torch.randn(s, generator=g, device="cuda").to(BF) for s in ((M, K), (K, N), (M, N), (M, N)))
+    one = gbr.gemm_bias_act_backward(dC, A, B, Z, act=act, needs=(True, False, False))[0]
+    two = gbr.gemm_bias_act_backward(dC, A, B, Z, act=act, needs=(False, True, False))[1]
+    dA, dB = torch.empty_like(A), torch.empty_like(B)
+    wrong = torch.zeros((), dtype=torch.int64, device="cuda")
+    for i in range(20):
+        dA.fill_(math.nan)
+        dB.fill_(math.nan)
+        gbr.gemm_bias_act_backward(dC, A, B, Z, act=act, dA=dA, dB=dB)
+        if i % 2:
+            a, b = gbr.dropout_add(dA, p=0.0), dB
+        else:
+            b, a = gbr.dropout_add(dB, p=0.0), dA
+        wrong += (a != one).sum() + (b != two).sum()
+    assert int(wrong) == 0
