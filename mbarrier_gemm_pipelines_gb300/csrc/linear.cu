@@ -234,22 +234,31 @@ struct TilePlan {
 //   operand comes from HBM and no other row tile shares it; all SMs together
 //   3500 from HBM.  DSMEM moves about 12 bytes a cycle and SM.
 //   CTA pairs: 32 KiB a CTA and 64-k slice, 512 cycles at full rate (which is
-//   also the tensor core's), 640 where less than one round of tiles runs;
-//   11500 to start, fill the ring and drain the last tile.
-// Measured against each other (us, best single tile / CTA pairs): rows 1,
-// 4096 x 4096 9.2 / 25; rows 128 14 / 26; rows 512 21.7 / 26; rows 128,
-// 4096 x 14336 27.8 / 31; rows 256 35.4 / 32; 301 x 520 x 1000 6.2 / 10.6;
-// 2048 x 1024 x 1024 10.3 / 11.7; dB of 4096 x 512 x 512 10.8 / 23, of
-// 512 x 4096 x 4096 33.6 / 18.
+//   also the tensor core's), 640 where less than one round of tiles runs; a
+//   round is never below the 4800 of a tile's epilogue; 13500 to start, fill
+//   the ring and drain the last tile.
+// A tile's rows are finished at about 28 cycles each by the CTAs that share it;
+// that decides against the pairs, among single tiles it hides under the others'
+// loads, and counting it there picks worse ones (256 x 512 x 512: 6.1 -> 8.5 us).
+// Measured against each other (us, single tiles / CTA pairs; forward unless
+// said): rows 1 of 4096 x 4096 7.0 / 22, 128 12.9 / 20, 512 19.4 / 21.7, 1024
+// 28.6 / 25; rows 128 of 4096 x 14336 27 / 30, 256 37 / 31; 301 x 520 x 1000
+// 6.4 / 10.7; 1024^3 8.1 / 11.0; 4096 x 1024 x 1024 15.4 / 12.0; 2048 x 256 x
+// 2048 11.5 / 8.3; dB of 512 x 1024 x 4096 13.2 / 9.2, of 4096 x 512 x 512
+// 10.1 / 20, of 512 x 4096 x 4096 51 / 18.  Over 540 products (M 256..8192,
+// K 64..4096, N 256..4096, all three directions) the choice is 1 % slower in
+// the mean than the best of what was measured, and 10 % at worst.
 double pair_cycles(const Product& p, int sms) {
     const linear::PairWork w = pair_work(p, sms / 2);
     const double whole = double(cdiv(w.whole, sms / 2)), half = w.split > 0 ? 0.5 : 0.0;
-    return 11500.0 + (w.split > 0 ? 8000.0 : 0.0) +
-           (whole + half) * double(cdiv(p.Kc, 64)) * (whole + half <= 1.0 ? 640.0 : 512.0);
+    const double rounds = whole + half, slices = double(cdiv(p.Kc, 64));
+    return 13500.0 + (w.split > 0 ? 8000.0 : 0.0) +
+           rounds * (rounds <= 1.0 ? 640.0 * slices : std::max(512.0 * slices, 4800.0));
 }
 
 TilePlan plan_tile(const Product& p, int sms) {
     TilePlan best = {0, 0, 0, 1e30};
+    double finish = 0.0;
     const int64_t nks = cdiv(p.Kc, 64);
     const double hbm = double(p.Kc) * double(p.J) * 2.0 / 3500.0;
     for (int bt : {int(std::min<int64_t>(256, cdiv(p.I, 16) * 16)), 64, 128, 256}) {
@@ -260,24 +269,37 @@ TilePlan plan_tile(const Product& p, int sms) {
         const double rows = double(std::min<int64_t>(p.I, bt));
         for (int s : {1, 2, 4, 8}) {
             if (s > nks && s > 1) continue;
-            const int64_t n = cdiv(tiles * s, sms), slices = cdiv(nks, s);
+            // Of large clusters fewer fit at once: 144 CTAs in fours, 120 in
+            // eights; two an SM, what fits in fours and pairs.
+            const int64_t fours = sms * 18 / 19, fit = s == 8 ? sms * 15 / 19 : s == 4 ? fours : sms;
+            const int64_t fit2 = 2 * (s == 8 ? fours : sms), slices = cdiv(nks, s);
+            // A slice's loads; the wide operand from HBM or shared through L2.
+            const double load = 16384.0 / (t_tiles == 1 ? 40.0 : 64.0) + bt * 2.0;
             // Two CTAs an SM where a tile's parts and a ring worth having fit
-            // twice, unless one each is all there is (of large clusters fewer
-            // fit: 120 CTAs in eights, 144 in fours).
-            const int per_sm = bt <= 128 && !(n == 1 && (s <= 2 || tiles * s <= 120)) ? 2 : 1;
-            const int64_t budget = per_sm == 2 ? 110 * 1024 : 218 * 1024, rounds = cdiv(n, per_sm);
+            // twice, unless one each is all there is and gains by the larger
+            // ring: more slices than the smaller one holds, and its turn, about
+            // 2200 cycles at best, not hidden by its loads (512^3, two slices a
+            // CTA: 6.5 us one an SM, whose memory leaves no room for the next
+            // launch's set-up, 5.8 two; one row of 4096^2 7.5 and 6.9; dB of
+            // 8192 x 512 x 512, 32 slices: 14.2 and 18.1).
+            constexpr int64_t kHalf = 110 * 1024, kWhole = 218 * 1024;
+            const int64_t small = (kHalf - 2304) / stage;
+            const bool ample = slices <= small || load >= 2200.0 / double(small);
+            const int per_sm = bt <= 128 && (ample || tiles * s > fit) ? 2 : 1;
+            const int64_t n = per_sm == 2 ? cdiv(tiles * s, sms) : cdiv(tiles * s, fit);
+            const int64_t budget = per_sm == 2 ? kHalf : kWhole, rounds = cdiv(tiles * s, per_sm == 2 ? fit2 : fit);
             const int stages = int(std::min<int64_t>(linear::kTileMaxStages, (budget - 2304) / stage));
-            // A CTA turns its ring over once in about 2200 cycles at best.
-            const double feed = std::max(
-                double(n) * double(slices) * (16384.0 / (t_tiles == 1 ? 40.0 : 64.0) + bt * 2.0),
-                double(rounds) * double(slices) * 2200.0 / double(stages));
+            const double feed =
+                std::max(double(n * slices) * load, ample ? 0.0 : double(rounds * slices) * 2200.0 / double(stages));
             // HBM gives its rate to all SMs together; fewer get less of it.
             const double busy = std::sqrt(double(sms) / double(std::min<int64_t>(sms, tiles * s)));
             const double parts = double(n) * rows * 512.0 * (double(s - 1) / s / 12.0 + 1.0 / 64.0);
-            const double cycles = 6000.0 + std::max(feed, hbm * busy) + parts + 3000.0 * double(rounds - 1);
-            if (cycles < best.cycles) best = {bt, s, stages, cycles};
+            const double cycles = 6000.0 + std::max(feed, hbm * busy) + parts + 60.0 * (s - 1) +
+                                  3000.0 * double(rounds - 1);      // the cluster's barriers; rounds
+            if (cycles < best.cycles) best = {bt, s, stages, cycles}, finish = double(n) * rows * 28.0 / s;
         }
     }
+    best.cycles += finish;
     return best;
 }
 
