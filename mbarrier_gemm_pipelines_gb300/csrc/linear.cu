@@ -37,13 +37,34 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // else the other way round.  A warp takes 256 columns of a row, the any-aligned
 // side two bytes a lane (whole lines), the other 16; shared memory turns one
 // into the other.  4096 x 14335, 117 MB in and out: one element a thread and turn 270 us.
+// The copies before a product, and those after it, are one launch (blockIdx.z
+// names the copy; 2047^3 with residual and Z: 42 us with one launch a copy, 36
+// together), unless their sizes differ so much that more than 4096 CTAs would
+// have nothing to do (37 x 4097 and 4097 x 14335, 14,600 such: 67.7 us one by
+// one and 72 together; 554 x 234 and 234 x 2359, 270: 26.6 and 24.9 of both
+// gradients).
 constexpr int kRepitchRows = 2;
 
+struct Repitch {
+    const bf16* src;
+    bf16* dst;
+    int64_t lds, ldd;
+    int32_t rows, cols;
+};
+
+struct Repitches {
+    Repitch of[3];
+};
+
 template <bool IN>
-__global__ void __launch_bounds__(256)
-    repitch_kernel(const bf16* src, int64_t lds, bf16* dst, int64_t ldd, int32_t rows, int32_t cols) {
+__global__ void __launch_bounds__(256) repitch_kernel(const __grid_constant__ Repitches all) {
     __shared__ __align__(16) uint16_t buf[8][kRepitchRows][256];
     ptx::griddep_wait();
+    const Repitch& m = all.of[blockIdx.z];
+    const bf16* src = m.src;
+    bf16* dst = m.dst;
+    const int64_t lds = m.lds, ldd = m.ldd;
+    const int32_t rows = m.rows, cols = m.cols;
     const int32_t lane = int32_t(threadIdx.x) % 32, warp = int32_t(threadIdx.x) / 32, c0 = int32_t(blockIdx.x) * 256;
     const int32_t step = int32_t(gridDim.y) * 8 * kRepitchRows;
     for (int64_t r0 = (int64_t(blockIdx.y) * 8 + warp) * kRepitchRows; r0 < rows; r0 += step) {
@@ -81,18 +102,45 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-int repitch(Mat src, Mat dst, int32_t rows, int32_t cols, bool in, cudaStream_t stream) {
-    const bf16* s = static_cast<const bf16*>(src.p);
-    bf16* d = static_cast<bf16*>(dst.w());
-    void* args[] = {&s, &src.ld, &d, &dst.ld, &rows, &cols};
-    const dim3 grid(unsigned(cdiv(cols, 256)), unsigned(std::min<int64_t>(cdiv(rows, 8 * kRepitchRows), 4096)));
-    const cudaError_t e = launch_kernel(in ? reinterpret_cast<void*>(&repitch_kernel<true>)
-                                           : reinterpret_cast<void*>(&repitch_kernel<false>),
-                                        grid, 256, 0, 1, args, stream);
-    if (e != cudaSuccess) return report_cuda(e, "launching the re-pitching copy");
-    count_launch();
-    return GBR_OK;
-}
+// Copies collected for a launch.
+struct RepitchList {
+    Repitches all = {};
+    dim3 grid[3];                  // each copy's own
+    int n = 0;
+
+    void add(Mat src, Mat dst, int32_t rows, int32_t cols) {
+        all.of[n] = {static_cast<const bf16*>(src.p), static_cast<bf16*>(dst.w()), src.ld, dst.ld, rows, cols};
+        grid[n++] = dim3(unsigned(cdiv(cols, 256)),
+                         unsigned(std::min<int64_t>(cdiv(rows, 8 * kRepitchRows), 4096)));
+    }
+    int launch(bool in, cudaStream_t stream) {
+        if (n == 0) return GBR_OK;
+        dim3 over(1, 1, unsigned(n));
+        double busy = 0;
+        for (int i = 0; i < n; ++i) {
+            over.x = std::max(over.x, grid[i].x);
+            over.y = std::max(over.y, grid[i].y);
+            busy += double(grid[i].x) * grid[i].y;
+        }
+        if (double(over.x) * over.y * n - busy <= 4096.0) return launch(all, over, in, stream);
+        for (int i = 0; i < n; ++i) {
+            const int r = launch({{all.of[i]}}, grid[i], in, stream);
+            if (r != GBR_OK) return r;
+        }
+        return GBR_OK;
+    }
+
+private:
+    static int launch(Repitches some, dim3 ctas, bool in, cudaStream_t stream) {
+        void* args[] = {&some};
+        const cudaError_t e = launch_kernel(in ? reinterpret_cast<void*>(&repitch_kernel<true>)
+                                               : reinterpret_cast<void*>(&repitch_kernel<false>),
+                                            ctas, 256, 0, 1, args, stream);
+        if (e != cudaSuccess) return report_cuda(e, "launching the re-pitching copy");
+        count_launch();
+        return GBR_OK;
+    }
+};
 
 bool tma_ready(const Mat& m) {
     return reinterpret_cast<uintptr_t>(m.p) % 16 == 0 && m.ld % 8 == 0;
@@ -102,7 +150,7 @@ bool tma_ready(const Mat& m) {
 // A TMA store ends at whole 16 bytes: measured, a row of 201 bf16 columns takes
 // 7 columns of its pitch's padding along, so an output whose rows end inside
 // 16 bytes is written to a copy and copied back.
-int aligned_mat(Mat* m, int32_t rows, int32_t cols, bool copy_in, Scratch& ws, cudaStream_t stream) {
+int aligned_mat(Mat* m, int32_t rows, int32_t cols, bool copy_in, Scratch& ws, RepitchList* copies) {
     if (rows == 1) m->ld = cdiv(cols, 8) * 8;            // never stepped over
     if (tma_ready(*m) && (copy_in || cols % 8 == 0)) return GBR_OK;
     Mat t;
@@ -111,10 +159,7 @@ int aligned_mat(Mat* m, int32_t rows, int32_t cols, bool copy_in, Scratch& ws, c
     const int r = ws.take(size_t(rows) * size_t(t.ld) * 2, "cudaMallocFromPoolAsync(aligned operand)", &p);
     if (r != GBR_OK) return r;
     t.p = p;
-    if (copy_in) {
-        const int r2 = repitch(*m, t, rows, cols, true, stream);
-        if (r2 != GBR_OK) return r2;
-    }
+    if (copy_in) copies->add(*m, t, rows, cols);
     *m = t;
     return GBR_OK;
 }
@@ -362,26 +407,28 @@ int run_product(Product p, const LibCtx& c, cudaStream_t stream, bool* one_launc
     int r;
     const Mat A = p.A, B = p.B, C = p.C, Z = p.Z;
     if (one_launch != nullptr) *one_launch = false;
-    if (p.Kc > 0) {
-        if ((r = aligned_mat(&p.A, p.a_mn ? p.Kc : p.I, p.a_mn ? p.I : p.Kc, true, ws, stream)) != GBR_OK) return r;
-        if ((r = aligned_mat(&p.B, p.b_mn ? p.Kc : p.J, p.b_mn ? p.J : p.Kc, true, ws, stream)) != GBR_OK) return r;
-    }
-    p.beside = p.beside && p.A.p == A.p && p.B.p == B.p;
-    // The kernel of single tiles reads and writes everything else with plain accesses.
     const TilePlan plan = plan_tile(p, c.sm_count);
-    if (plan.cycles < pair_cycles(p, c.sm_count)) {
-        if (one_launch != nullptr) *one_launch = p.A.p == A.p && p.B.p == B.p;
-        return run_tile(p, plan, c, stream);
+    const bool tile = plan.cycles < pair_cycles(p, c.sm_count);
+    RepitchList in, out;
+    if (p.Kc > 0) {
+        if ((r = aligned_mat(&p.A, p.a_mn ? p.Kc : p.I, p.a_mn ? p.I : p.Kc, true, ws, &in)) != GBR_OK) return r;
+        if ((r = aligned_mat(&p.B, p.b_mn ? p.Kc : p.J, p.b_mn ? p.J : p.Kc, true, ws, &in)) != GBR_OK) return r;
     }
-    if (p.R && (r = aligned_mat(&p.R, p.I, p.J, true, ws, stream)) != GBR_OK) return r;
-    if ((r = aligned_mat(&p.C, p.I, p.J, false, ws, stream)) != GBR_OK) return r;
-    if (p.Z && (r = aligned_mat(&p.Z, p.I, p.J, false, ws, stream)) != GBR_OK) return r;
+    const bool in_place = in.n == 0;
+    p.beside = p.beside && in_place;
+    // The kernel of single tiles reads and writes everything else with plain accesses.
+    if (!tile) {
+        if (p.R && (r = aligned_mat(&p.R, p.I, p.J, true, ws, &in)) != GBR_OK) return r;
+        if ((r = aligned_mat(&p.C, p.I, p.J, false, ws, nullptr)) != GBR_OK) return r;
+        if (p.Z && (r = aligned_mat(&p.Z, p.I, p.J, false, ws, nullptr)) != GBR_OK) return r;
+        if (p.C.p != C.p) out.add(p.C, C, p.I, p.J);
+        if (p.Z.p != Z.p) out.add(p.Z, Z, p.I, p.J);
+    }
     if (one_launch != nullptr)
-        *one_launch = p.A.p == A.p && p.B.p == B.p && p.C.p == C.p && pair_work(p, c.sm_count / 2).split == 0;
-    if ((r = run_pair(p, c, stream)) != GBR_OK) return r;
-    if (p.C.p != C.p && (r = repitch(p.C, C, p.I, p.J, false, stream)) != GBR_OK) return r;
-    if (p.Z.p != Z.p && (r = repitch(p.Z, Z, p.I, p.J, false, stream)) != GBR_OK) return r;
-    return GBR_OK;
+        *one_launch = in_place && out.n == 0 && (tile || pair_work(p, c.sm_count / 2).split == 0);
+    if ((r = in.launch(true, stream)) != GBR_OK) return r;
+    if ((r = tile ? run_tile(p, plan, c, stream) : run_pair(p, c, stream)) != GBR_OK) return r;
+    return out.launch(false, stream);
 }
 
 // ------------------------------------------------------------ dZ and dbias

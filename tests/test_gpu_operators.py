@@ -629,3 +629,10 @@ def test_gradients_side_by_side(gbr, M, K, N, act):
             b, a = gbr.dropout_add(dB, p=0.0), dA
         wrong += (a != one).sum() + (b != two).sum()
     assert int(wrong) == 0
+
+
+@pytest.mark.parametrize("lay", [padded, spaced])
+@pytest.mark.parametrize("M,K,N", [(1537, 1031, 1543), (37, 2049, 5003), (4096, 72, 1030)])
+def test_strides_large(gbr, lay, M, K, N):
+    """The same for products that run on CTA pairs, whose copies are launched together, and for lopsided ones."""
+    test_strides(gbr, lay, M, K, N)
