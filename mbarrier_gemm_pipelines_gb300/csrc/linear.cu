@@ -567,10 +567,17 @@ int launch_linear_dz(const LinearGradArgs& a, const LibCtx& c, cudaStream_t stre
     // 128 columns a CTA; rows cut until there are four CTAs an SM, what fits at
     // once, as long as a CTA keeps 128 rows (8192 x 4096, GELU: 47 us with two an
     // SM, 35 with four, 37 with eight).
-    constexpr int kTx = 16;
-    const int64_t tiles = cdiv(a.N, kTx * 8);
-    const int64_t chunks = std::max<int64_t>(
-        1, std::min<int64_t>(4 * int64_t(c.sm_count) / (tiles * kDzCluster), a.M / (128 * kDzCluster)));
+    // Where that leaves SMs idle, 32 columns, unless the cut rows make up for it
+    // (with GELU and dA, us: 1024^3 17.2 / 12.2, 2048 x 512 x 1024 17.3 / 14.1;
+    // 8000 x 100 x 101, which would come down from 56 CTAs to 32, 14.1 / 18.1).
+    auto cut = [&](int tx, int64_t* tiles) {
+        *tiles = cdiv(a.N, tx * 8);
+        return std::max<int64_t>(1, std::min<int64_t>(4 * int64_t(c.sm_count) / (*tiles * kDzCluster),
+                                                      a.M / (8 * (kDzThreads / tx) * kDzCluster)));
+    };
+    int64_t tiles, chunks = cut(16, &tiles), tiles4, chunks4 = cut(4, &tiles4);
+    const bool narrow = tiles * chunks * kDzCluster < c.sm_count && tiles4 * chunks4 >= tiles * chunks;
+    if (narrow) tiles = tiles4, chunks = chunks4;
     Scratch ws(c, stream);
     void* sums = nullptr;
     if (chunks > 1 && a.dbias != nullptr) {
@@ -578,7 +585,9 @@ int launch_linear_dz(const LinearGradArgs& a, const LibCtx& c, cudaStream_t stre
         if (r != GBR_OK) return r;
     }
     void* args[] = {&arg, &sums};
-    cudaError_t e = launch_kernel(vec ? dz_kernel_ptr<kTx, true>(a.act) : dz_kernel_ptr<kTx, false>(a.act),
+    void* kernel = narrow ? (vec ? dz_kernel_ptr<4, true>(a.act) : dz_kernel_ptr<4, false>(a.act))
+                          : (vec ? dz_kernel_ptr<16, true>(a.act) : dz_kernel_ptr<16, false>(a.act));
+    cudaError_t e = launch_kernel(kernel,
                                   dim3(unsigned(tiles * kDzCluster), unsigned(chunks)), kDzThreads, 0, kDzCluster,
                                   args, stream);
     if (e != cudaSuccess) return report_cuda(e, "launching the gradient's dZ");
