@@ -75,6 +75,7 @@ __global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const MoeArg
     const int wide = 4 << shift;                        // experts, rounded up
     float* red = router_mem;                            // [TB][kWarps][wide]: a warp's sums
     float* sums = red + TB * kWarps * wide;             // of rank 0: [CTA][TB][wide]
+    ptx::cluster_arrive();              // this CTA has started
     ptx::griddep_launch_dependents();   // the expert kernel's set-up overlaps this one
     ptx::griddep_wait();
     const uint32_t rank = ptx::cluster_ctarank();
@@ -120,6 +121,7 @@ __global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const MoeArg
             for (int j = 0; j < 4; ++j)
                 if (j < left) red[(i * kWarps + warp) * wide + e + j] = acc[i][j];
     __syncthreads();
+    ptx::cluster_wait();                // rank 0 has started: its memory may be written
     // Of 64 threads along the experts a warp has one half: its row holds those.
     const int stride = lanes > 32 ? lanes / 32 : 1;
     for (int q = warp; q < TB * a.E; q += kWarps) {
