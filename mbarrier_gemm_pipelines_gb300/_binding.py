@@ -6,6 +6,7 @@ is missing or the tensors are not on a CUDA device the call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -113,6 +114,16 @@ def _stream_ptr(stream):
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _outputs_on(stream):
+    """Context in which new tensors belong to `stream` (None: the current one), as PyTorch's allocator counts them."""
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    handle = _stream_ptr(stream)
+    # 1 is cudaStreamLegacy, the null stream by another name.
+    return torch.cuda.stream(torch.cuda.default_stream() if handle in (0, 1) else torch.cuda.ExternalStream(handle))
 
 
 def _cuda_tensor(t, name, dtypes):

@@ -4,6 +4,12 @@ The functions here give the arguments their names, defaults and documentation;
 ``csrc/python/operators_ext.cpp`` checks the tensors, makes the outputs and
 calls the library.  There is no CPU fallback: a missing build or a CPU tensor
 raises.
+
+`stream` is a torch stream or a raw handle; without it a call runs on the
+current stream.  With it the outputs that the call makes belong to that stream,
+as if made under ``torch.cuda.stream(stream)``: use them there, or after an
+event, and ``record_stream`` what another stream goes on using.  Inputs have to
+be ready on that stream.
 """
 from __future__ import annotations
 
@@ -12,7 +18,7 @@ import importlib.util
 import os
 
 from . import _build
-from ._binding import GbrError, _cuda_tensor, _stream_ptr, check, lib
+from ._binding import GbrError, _cuda_tensor, _outputs_on, _stream_ptr, check, lib
 
 # gbr_act
 ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
@@ -76,7 +82,8 @@ def moe_layer(X, Wr, W1, b1, W2, b2, top_k=2, act="relu", gated=False, Y=None, r
 def selftest_linear_skip_load(A, B, cta, item, limit_ns, stream=None):
     """Runs gemm_bias_act (A @ B alone) with one stage of CTA (or CTA pair) `cta`,
     ring item `item`, left unfilled (see gbr.h); returns the undefined output."""
-    C = A.new_empty(A.shape[0], B.shape[1])
+    with _outputs_on(stream):
+        C = A.new_empty(A.shape[0], B.shape[1])
     check(lib().gbr_selftest_linear_skip_load(
         *(_cuda_tensor(t, n, (C.dtype,)).data_ptr() for t, n in ((A, "A"), (B, "B"), (C, "C"))), A.shape[0],
         B.shape[1], A.shape[1], cta, item, limit_ns, _stream_ptr(stream)))
@@ -86,7 +93,8 @@ def selftest_linear_skip_load(A, B, cta, item, limit_ns, stream=None):
 def selftest_moe_skip_load(X, Wr, W1, W2, top_k, cta, item, limit_ns, stream=None):
     """Runs moe_layer (ReLU, no biases) with one stage of CTA `cta`, ring item
     `item`, left unfilled (see gbr.h); returns the undefined output."""
-    Y = X.new_empty(X.shape)
+    with _outputs_on(stream):
+        Y = X.new_empty(X.shape)
     E, F = W2.shape[:2]
     for t, n in ((X, "X"), (Wr, "Wr"), (W1, "W1"), (W2, "W2")):
         _cuda_tensor(t, n, (Wr.dtype if n == "Wr" else X.dtype,))

@@ -11,6 +11,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -154,15 +155,31 @@ bool truth(PyObject* o) {
     return v != 0;
 }
 
-gbr_stream_t stream_of(PyObject* o, int dev) {
-    if (o == Py_None) return reinterpret_cast<gbr_stream_t>(c10::cuda::getCurrentCUDAStream(dev).stream());
-    PyObject* v = PyLong_Check(o) ? Py_NewRef(o) : PyObject_GetAttrString(o, "cuda_stream");
-    if (v == nullptr) throw Refused();
-    void* p = PyLong_AsVoidPtr(v);
-    Py_DECREF(v);
-    if (p == nullptr && PyErr_Occurred()) throw Refused();
-    return reinterpret_cast<gbr_stream_t>(p);
-}
+// The call's stream: the current one, or the `stream` argument, which is then the current one until the call
+// ends, so that the outputs made here are that stream's to PyTorch's allocator.  From the current stream's share it could
+// hand out memory that a kernel there still reads, and give an output away while the other stream writes it.
+class CallStream {
+public:
+    CallStream(PyObject* o, int dev) : handle_(c10::cuda::getCurrentCUDAStream(dev).stream()) {
+        if (o == Py_None) return;
+        PyObject* v = PyLong_Check(o) ? Py_NewRef(o) : PyObject_GetAttrString(o, "cuda_stream");
+        if (v == nullptr) throw Refused();
+        const cudaStream_t given = static_cast<cudaStream_t>(PyLong_AsVoidPtr(v));
+        Py_DECREF(v);
+        if (given == nullptr && PyErr_Occurred()) throw Refused();
+        if (given == handle_) return;
+        handle_ = given;
+        // cudaStreamLegacy is the null stream by another name.
+        guard_.reset_stream(given == nullptr || given == cudaStreamLegacy
+                                ? c10::cuda::getDefaultCUDAStream(dev)
+                                : c10::cuda::getStreamFromExternal(given, c10::DeviceIndex(dev)));
+    }
+    operator gbr_stream_t() const { return reinterpret_cast<gbr_stream_t>(handle_); }
+
+private:
+    cudaStream_t handle_;
+    c10::cuda::OptionalCUDAStreamGuard guard_;
+};
 
 // An output: the caller's, or a new one.
 struct Out {
@@ -221,6 +238,7 @@ PyObject* dropout_add_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
             refuse(PyExc_TypeError, "X must be bf16 or fp32, got %s", c10::toString(type));
         const int dev = first_device(X, "X");
         if (X.dim() == 0) refuse(PyExc_ValueError, "X must have at least one dimension");
+        const CallStream st(a[6], dev);
         const bool has_r = a[1] != Py_None, has_y = a[5] != Py_None;
         at::Tensor made;
         if (!has_y) made = at::empty(X.sizes(), X.options());
@@ -242,7 +260,6 @@ PyObject* dropout_add_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
         }
         const double p = number(a[2]);
         const uint64_t seed = bits64(a[3], "seed"), offset = bits64(a[4], "offset");
-        const gbr_stream_t st = stream_of(a[6], dev);
         call([&] {
             return dropout_add(x.p, x.ld, has_r ? r.p : nullptr, r.ld, y.p, y.ld, x.rows, x.cols,
                                type == at::kBFloat16 ? GBR_BF16 : GBR_F32_FFMA, p, seed, offset, st);
@@ -270,7 +287,7 @@ PyObject* gemm_bias_act_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const double p = number(a[5]);
         const uint64_t seed = bits64(a[6], "seed"), offset = bits64(a[7], "offset");
         const bool want_z = a[9] != Py_None || truth(a[10]);
-        const gbr_stream_t st = stream_of(a[11], dev);
+        const CallStream st(a[11], dev);
         const Out C = out_mat(a[8], "C", tA, dev, M, N);
         Out Z;
         if (want_z) Z = out_mat(a[9], "Z", tA, dev, M, N);
@@ -314,7 +331,7 @@ PyObject* gemm_bias_act_backward_py(PyObject*, PyObject* const* a, Py_ssize_t n)
         Py_DECREF(needs);
         if (bad) throw Refused();
         if (!three) refuse(PyExc_ValueError, "needs must be three truth values");
-        const gbr_stream_t st = stream_of(a[12], dev);
+        const CallStream st(a[12], dev);
         Out dA, dB, db;
         if (want[0]) dA = out_mat(a[8], "dA", tA, dev, M, K);
         if (want[1]) dB = out_mat(a[9], "dB", tA, dev, K, N);
@@ -353,6 +370,7 @@ PyObject* moe_layer_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const void* w2 = packed(W2, "W2", at::kBFloat16, dev, {E, F, D});
         const void* b1 = a[3] == Py_None ? nullptr : packed(tensor(a[3], "b1"), "b1", at::kFloat, dev, {E, F1});
         const void* b2 = a[5] == Py_None ? nullptr : packed(tensor(a[5], "b2"), "b2", at::kFloat, dev, {E, D});
+        const CallStream st(a[11], dev);
         Out Y;
         if (a[9] != Py_None) {
             Y.given = a[9];
@@ -368,7 +386,6 @@ PyObject* moe_layer_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
             ids = at::empty({T, k}, X.options().dtype(at::kLong));
             weights = at::empty({T, k}, X.options().dtype(at::kFloat));
         }
-        const gbr_stream_t st = stream_of(a[11], dev);
         call([&] {
             return moe_layer(x, static_cast<const float*>(wr), w1, static_cast<const float*>(b1), w2,
                              static_cast<const float*>(b2), Y.m.p,
