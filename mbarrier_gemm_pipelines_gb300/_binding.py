@@ -153,7 +153,8 @@ def gemm_bias_relu(A, B, bias, C=None, dtype="bf16", stages=4, stream=None):
         raise ValueError("shape mismatch: A %s, B %s, bias %s" % (tuple(A.shape), tuple(B.shape),
                                                                   tuple(bias.shape)))
     if C is None:
-        C = torch.empty((M, N), dtype=in_t, device=A.device)
+        with _outputs_on(stream):
+            C = torch.empty((M, N), dtype=in_t, device=A.device)
     _cuda_tensor(C, "C", (in_t,))
     if tuple(C.shape) != (M, N):
         raise ValueError("C must be [M, N]")
@@ -206,7 +207,8 @@ def gemm_bias_relu_grouped(X, W, bias, counts, C=None, stages=4, stream=None):
     if X.shape[0] != T:
         raise ValueError("X must have sum(counts) rows")
     if C is None:
-        C = torch.empty((T, N), dtype=torch.bfloat16, device=X.device)
+        with _outputs_on(stream):
+            C = torch.empty((T, N), dtype=torch.bfloat16, device=X.device)
     _cuda_tensor(C, "C", (torch.bfloat16,))
     arr = (ctypes.c_int32 * G)(*counts)
     check(lib().gemm_bias_relu_grouped(X.data_ptr(), W.data_ptr(), bias.data_ptr(), C.data_ptr(),
@@ -223,7 +225,8 @@ def staged_copy(src, dst=None, tile=(128, 64), stages=4, stream=None):
     if src.dim() != 2:
         raise ValueError("src must be 2-D")
     if dst is None:
-        dst = torch.empty_like(src)
+        with _outputs_on(stream):
+            dst = torch.empty_like(src)
     _cuda_tensor(dst, "dst", ok)
     if dst.shape != src.shape:
         raise ValueError("dst must match src")
@@ -320,7 +323,8 @@ def selftest_gemm_skip_load(A, B, bias, dtype, stages, cta, item, limit_ns, stre
     _cuda_tensor(bias, "bias", (torch.float32,))
     M, K = A.shape
     N = B.shape[1]
-    C = torch.empty((M, N), dtype=A.dtype, device=A.device)
+    with _outputs_on(stream):
+        C = torch.empty((M, N), dtype=A.dtype, device=A.device)
     check(lib().gbr_selftest_gemm_skip_load(A.data_ptr(), B.data_ptr(), bias.data_ptr(),
                                             C.data_ptr(), M, N, K, code, int(stages), int(cta),
                                             int(item), int(limit_ns), _stream_ptr(stream)))
@@ -332,7 +336,8 @@ def selftest_copy_skip_load(src, stages, cta, item, limit_ns, stream=None):
     `item`, left unfilled (see gbr.h); returns the (undefined) output tensor."""
     import torch
     _cuda_tensor(src, "src", (torch.float32,))
-    dst = torch.empty_like(src)
+    with _outputs_on(stream):
+        dst = torch.empty_like(src)
     rows, cols = src.shape
     check(lib().gbr_selftest_copy_skip_load(src.data_ptr(), dst.data_ptr(), rows, cols,
                                             int(stages), int(cta), int(item), int(limit_ns),

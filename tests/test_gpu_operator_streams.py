@@ -1,4 +1,4 @@
-"""The `stream` argument of the feed-forward operators: the results, and whose memory the outputs are made from."""
+"""The `stream` argument of the operators: the results, and whose memory the outputs are made from."""
 import math
 
 import pytest
@@ -107,4 +107,28 @@ def test_self_tests_outputs(gbr):
     # No such CTA: nothing is planted.
     assert owner(gbr.selftest_linear_skip_load(A, B, 100000, 0, 50_000_000, stream=side)) == side.cuda_stream
     side.synchronize()
+    gbr.check_device()
+
+
+@pytest.mark.parametrize("how", ["stream", "handle", "null"])
+def test_older_operators_outputs(gbr, how):
+    side = torch.cuda.Stream()
+    g = torch.Generator(device="cuda").manual_seed(6)
+    A, B = torch.randn(300, 128, generator=g, device="cuda"), torch.randn(128, 264, generator=g, device="cuda")
+    bias, src = torch.randn(264, generator=g, device="cuda"), torch.randn(100, 64, generator=g, device="cuda")
+    W, b2, A16, B16 = B[None].repeat(2, 1, 1).to(BF), bias[None].repeat(2, 1), A.to(BF), B.to(BF)
+    given, mine = {"stream": (side, side.cuda_stream), "handle": (side.cuda_stream, side.cuda_stream), "null": (0, 0)}[how]
+    for call in (lambda s: gbr.gemm_bias_relu(A, B, bias, dtype="ffma", stream=s),
+                 lambda s: gbr.gemm_bias_relu(A16, B16, bias, stream=s),
+                 lambda s: gbr.gemm_bias_relu_grouped(A16, W, b2, [100, 200], stream=s),
+                 lambda s: gbr.staged_copy(src, stream=s)):
+        want = call(None)
+        torch.cuda.synchronize()
+        if how == "null":
+            with torch.cuda.stream(side):
+                got = call(given)
+        else:
+            got = call(given)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and owner(got) == mine
     gbr.check_device()
