@@ -40,6 +40,7 @@
 #include "gbr.h"
 #include "gemm_umma.cuh"
 #include "mma_issue.cuh"
+#include "moe_cut.cuh"
 #include "operators.h"
 
 #include <cuda_bf16.h>
@@ -50,6 +51,7 @@
 namespace gbr {
 namespace {
 
+using namespace moe;
 using bf16 = __nv_bfloat16;
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -183,10 +185,6 @@ __global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const MoeArg
 
 // ------------------------------------------------------------ experts
 constexpr int kThreads = 192;
-constexpr uint32_t kSliceBytes = 64 * 128;              // 64 weight rows x 64 columns
-constexpr int kMaxStages = 12;
-constexpr uint32_t kXStages = 4;
-constexpr int kUnit = 64;                               // hidden columns of a unit
 // 128-column tiles that are accumulated side by side: the tokens' tile of a
 // k step is loaded once for all of them, and a row of W1 or W2 is read 1 KiB
 // at a time (four tiles' panels one after the other).
@@ -216,49 +214,11 @@ struct ExpertParams {
     float* parts;                                       // [rows][D] fp32
     PairParts* pairs;                                   // [T * top_k]
     int32_t t_pad;                                      // tokens, rounded up to 16
-    int32_t units;                                      // units of an expert
-    int32_t max_units;                                  // units of a part that fit in shared memory
+    CutSizes sizes;
     int32_t stages;
     int32_t ksub;                                       // 64-row slices of a stage, 1 or 2
-    int32_t sms;
     KernelCtl ctl;
     FaultInjection inject;                              // self test only
-};
-
-// floor(a b / c), in 32 bits where the product fits.
-__device__ __forceinline__ int32_t mul_div(int32_t a, int32_t b, int32_t c) {
-    const uint64_t p = uint64_t(uint32_t(a)) * uint32_t(b);
-    return int32_t((p >> 32) == 0 ? uint32_t(p) / uint32_t(c) : uint32_t(p / uint32_t(c)));
-}
-
-// The cut of the list of units, the same in every CTA.  It is made in grains
-// of one unit, or of two where that leaves the largest part no larger: two
-// units fill a 128-column tile, one costs the tensor core as much.  Where that
-// leaves the largest part no larger either, every expert gets its own equal
-// number of parts; else parts run on from one expert into the next.
-struct Cut {
-    int32_t grain;                                      // units
-    int32_t per_expert;                                 // grains of an expert
-    int32_t total;                                      // grains of all chosen experts
-    int32_t parts;
-    int32_t own;                                        // parts of each expert, 0: running on
-    __device__ __forceinline__ int32_t begin(int32_t v) const {
-        if (own == 0) return mul_div(v, total, parts);
-        const int32_t x = v / own;
-        return x * per_expert + mul_div(v - x * own, per_expert, own);
-    }
-    // The parts of the x-th chosen expert: the first, and how many.
-    __device__ __forceinline__ int32_t first(int32_t x) const { return own ? x * own : part_of(x * per_expert); }
-    __device__ __forceinline__ int32_t count(int32_t x) const {
-        return own ? own : part_of((x + 1) * per_expert - 1) - part_of(x * per_expert) + 1;
-    }
-
-private:
-    // Running on: the part that holds grain u, the last v with begin(v) <= u.
-    __device__ __forceinline__ int32_t part_of(int32_t u) const {
-        const uint64_t p = (uint64_t(uint32_t(u)) + 1) * uint32_t(parts) + uint32_t(total) - 1;
-        return int32_t((p >> 32) == 0 ? uint32_t(p) / uint32_t(total) : uint32_t(p / uint32_t(total))) - 1;
-    }
 };
 
 struct alignas(16) Tables {
@@ -281,23 +241,6 @@ __device__ __forceinline__ int32_t warp_exclusive(int32_t v, uint32_t lane, int3
     return x - v;
 }
 
-__device__ __forceinline__ Cut make_cut(const ExpertParams& P, int32_t active) {
-    Cut c;
-    const int32_t twos = (P.units + 1) / 2;
-    const int32_t per1 = (active * P.units + P.sms - 1) / P.sms, per2 = 2 * ((active * twos + P.sms - 1) / P.sms);
-    c.grain = P.max_units >= 2 && per2 <= per1 ? 2 : 1;
-    c.per_expert = c.grain == 2 ? twos : P.units;
-    c.total = active * c.per_expert;
-    const int32_t per = c.grain == 2 ? per2 : per1;
-    const int32_t rounds = (per + P.max_units - 1) / P.max_units;
-    c.parts = min(P.sms * rounds, c.total);
-    c.own = min(P.sms * rounds / active, c.per_expert);
-    const int32_t largest = c.own > 0 ? (c.per_expert + c.own - 1) / c.own * c.grain : per + 1;
-    if (largest <= per && largest <= P.max_units) c.parts = active * c.own;
-    else c.own = 0;
-    return c;
-}
-
 // Builds the tables from the router's choice (all threads of the CTA; the
 // masks are zero already).
 __device__ __forceinline__ void build_tables(const ExpertParams& P, Tables& tb) {
@@ -318,7 +261,7 @@ __device__ __forceinline__ void build_tables(const ExpertParams& P, Tables& tb) 
         }
         if (lane == 0) tb.num_active = active;
         __syncwarp();
-        const Cut cut = make_cut(P, active);
+        const Cut cut = make_cut(P.sizes, active);
         int32_t base = 0;
         for (int32_t x0 = 0; x0 < active; x0 += 32) {
             const int32_t x = x0 + int32_t(lane);
@@ -334,43 +277,6 @@ __device__ __forceinline__ void build_tables(const ExpertParams& P, Tables& tb) 
     }
     __syncthreads();
 }
-
-// One run of units of one expert inside a part.
-struct Segment {
-    int32_t index;                                      // of the expert among the chosen
-    int32_t expert;
-    int32_t u0, n;                                      // first unit within the expert, units
-    int32_t part;
-};
-
-// Walks the segments of this CTA's parts in order.
-struct Walk {
-    int32_t v, v_end, at, end;
-    __device__ __forceinline__ Walk(const Cut& c, int32_t sms) {
-        v = mul_div(int32_t(blockIdx.x), c.parts, sms);
-        v_end = mul_div(int32_t(blockIdx.x) + 1, c.parts, sms);
-        at = end = 0;
-        if (v < v_end) {
-            at = c.begin(v);
-            end = c.begin(v + 1);
-        }
-    }
-    __device__ __forceinline__ bool next(const Cut& c, const Tables& tb, int32_t units, Segment& s) {
-        if (v >= v_end) return false;
-        s.index = at / c.per_expert;
-        s.expert = tb.active[s.index];
-        const int32_t first = at - s.index * c.per_expert, n = min(end - at, c.per_expert - first);
-        s.u0 = first * c.grain;
-        s.n = min(n * c.grain, units - s.u0);
-        s.part = v;
-        at += n;
-        if (at >= end && ++v < v_end) {
-            at = c.begin(v);
-            end = c.begin(v + 1);
-        }
-        return true;
-    }
-};
 
 // NG: 1, or 2 when gated: of the first product's kWide tiles, which are then
 // gate and up columns in turn.
@@ -391,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_expert_kernel(const __grid_co
     const uint32_t panel = ksub * kSliceBytes, stage_bytes = 2 * panel;
     uint8_t* h_mem = align_1024(smem_raw);
     const uint32_t h_base = ptx::smem_addr(h_mem);
-    const uint32_t x_base = h_base + uint32_t(P.max_units) * h_block;
+    const uint32_t x_base = h_base + uint32_t(P.sizes.max_units) * h_block;
     const uint32_t ring_base = x_base + kXStages * x_bytes;
     // Two accumulators of kWide tiles: a power of two of columns, at most 512.
     const uint32_t tmem_cols = t_pad > 32 ? 512u : 8u * t_pad;
@@ -431,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_expert_kernel(const __grid_co
     const uint32_t tmem = tmem_holder;
     ptx::griddep_wait();
     build_tables(P, tb);
-    const Cut cut = make_cut(P, tb.num_active);
+    const Cut cut = make_cut(P.sizes, tb.num_active);
     const int32_t kstep = 64 * int32_t(ksub);
     Ring ring, xring;                                   // of the producer; of the MMA lane
 
@@ -446,7 +352,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_expert_kernel(const __grid_co
             return ring_base + ring.slot * stage_bytes;
         };
         Segment s;
-        for (Walk w(cut, P.sms); ok && w.next(cut, tb, P.units, s);) {
+        for (Walk w(cut, int32_t(blockIdx.x), P.sizes.sms); ok && w.next(cut, P.sizes.units, s);) {
+            const int32_t expert = tb.active[s.index];
             for (int32_t g0 = 0; ok && g0 < s.n; g0 += kUnitsPass) {
                 const int32_t g1 = min(g0 + kUnitsPass, s.n);
                 for (int32_t k = 0; ok && k < a.D; k += kstep) {
@@ -467,9 +374,9 @@ __global__ void __launch_bounds__(kThreads, 1) moe_expert_kernel(const __grid_co
                             const uint32_t bar = ptx::smem_addr(full + ring.slot);
                             const int32_t col = g * a.F + (s.u0 + u) * kUnit;
                             const bool skip = inject_skip(P.inject, ring.count);
-                            if (!skip) ptx::tma_load_3d_hint(dst, &P.mapW1, bar, col, k, s.expert, once);
+                            if (!skip) ptx::tma_load_3d_hint(dst, &P.mapW1, bar, col, k, expert, once);
                             if (two && !skip)
-                                ptx::tma_load_3d_hint(dst + panel, &P.mapW1, bar, col + kUnit, k, s.expert, once);
+                                ptx::tma_load_3d_hint(dst + panel, &P.mapW1, bar, col + kUnit, k, expert, once);
                             ring.step(S);
                         }
                     }
@@ -484,8 +391,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_expert_kernel(const __grid_co
                         if (!ok) break;
                         const uint32_t bar = ptx::smem_addr(full + ring.slot);
                         if (!inject_skip(P.inject, ring.count)) {
-                            ptx::tma_load_3d_hint(dst, map, bar, d, (s.u0 + b) * kUnit, s.expert, once);
-                            ptx::tma_load_3d_hint(dst + panel, map, bar, d + 64, (s.u0 + b) * kUnit, s.expert, once);
+                            ptx::tma_load_3d_hint(dst, map, bar, d, (s.u0 + b) * kUnit, expert, once);
+                            ptx::tma_load_3d_hint(dst + panel, map, bar, d + 64, (s.u0 + b) * kUnit, expert, once);
                         }
                         ring.step(S);
                     }
@@ -543,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_expert_kernel(const __grid_co
             }
         };
         Segment s;
-        for (Walk w(cut, P.sms); ok && w.next(cut, tb, P.units, s); ++hn) {
+        for (Walk w(cut, int32_t(blockIdx.x), P.sizes.sms); ok && w.next(cut, P.sizes.units, s); ++hn) {
             for (int32_t g0 = 0; ok && g0 < s.n; g0 += kUnitsPass) {
                 const int32_t tiles = (min(kUnitsPass, s.n - g0) + 1) / 2 * NG;
                 const uint32_t acc = acc_take();
@@ -612,12 +519,13 @@ __global__ void __launch_bounds__(kThreads, 1) moe_expert_kernel(const __grid_co
             ++tl;
         };
         Segment s;
-        for (Walk w(cut, P.sms); ok && w.next(cut, tb, P.units, s); ++hn) {
+        for (Walk w(cut, int32_t(blockIdx.x), P.sizes.sms); ok && w.next(cut, P.sizes.units, s); ++hn) {
             // The previous segment's second product has read the hidden values.
             if (hn > 0 && !(ok = mbar_wait_warp(ptx::smem_addr(&h_empty), (hn - 1u) & 1u, P.ctl, abort_flag,
                                                 kSiteEpiHidden, hn)))
                 break;
-            const uint64_t mask = tb.mask[s.expert];
+            const int32_t expert = tb.active[s.index];
+            const uint64_t mask = tb.mask[expert];
             for (int32_t g0 = 0; ok && g0 < s.n; g0 += kUnitsPass) {
                 const uint32_t acc0 = acc_wait();
                 if (!ok) break;
@@ -627,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_expert_kernel(const __grid_co
                     const bool inside = f < a.F;
                     float b_gate = 0.f, b_up = 0.f;
                     if (inside && a.b1 != nullptr) {
-                        const float* b1 = a.b1 + int64_t(s.expert) * a.F * NG;
+                        const float* b1 = a.b1 + int64_t(expert) * a.F * NG;
                         b_gate = __ldg(b1 + f);
                         if (NG == 2) b_up = __ldg(b1 + a.F + f);
                     }
@@ -771,40 +679,6 @@ void* expert_kernel(int act) {
     }
 }
 
-struct ExpertPlan {
-    int32_t t_pad, units, max_units, stages, ksub;
-    size_t smem;
-    int64_t max_rows;              // of the parts' buffer, whatever the routing
-};
-
-ExpertPlan plan_experts(const MoeArgs& a, const LibCtx& c) {
-    ExpertPlan p;
-    p.t_pad = int32_t(cdiv(a.T, 16) * 16);
-    p.units = int32_t(cdiv(a.F, kUnit));
-    const int64_t budget = int64_t(c.smem_optin) - 1024 - 10 * 1024;   // alignment; tables and barriers
-    const int64_t block = p.t_pad * 128, slice = 2 * int64_t(kSliceBytes);
-    const int64_t experts = std::min<int64_t>(a.E, int64_t(a.T) * a.top_k);
-    // Room for a part's hidden columns if every expert that can be chosen is,
-    // as long as a ring of 80 KiB remains beside it.
-    const int64_t want = cdiv(experts * p.units, c.sm_count);
-    const int64_t xring = int64_t(kXStages) * block;
-    p.max_units = int32_t(std::max<int64_t>(1, std::min(want, (budget - xring - 80 * 1024) / block)));
-    if (p.max_units > 1) p.max_units = (p.max_units + 1) / 2 * 2;   // grains of two fit whole
-    // Stages of 128 weight rows where four of them fit, else of 64: a stage
-    // costs its handshakes, whatever its size.
-    p.ksub = (budget - p.max_units * block - 2 * xring) / (2 * slice) >= 4 ? 2 : 1;
-    const int64_t rest = budget - p.max_units * block - p.ksub * xring;
-    p.stages = int32_t(std::min<int64_t>(kMaxStages, rest / (p.ksub * slice)));
-    p.smem = size_t(1024 + p.max_units * block + p.ksub * xring + p.stages * p.ksub * slice);
-    // Rows: an expert's tokens times the parts it meets.  x chosen experts
-    // share at most parts + x - 1 meetings, no expert has more than T tokens,
-    // and the pairs are T * top_k: largest with as few experts as can be.
-    const int64_t parts = int64_t(c.sm_count) *
-                          cdiv(cdiv(experts * p.units, c.sm_count), p.max_units);
-    p.max_rows = int64_t(a.T) * (parts + experts);
-    return p;
-}
-
 size_t router_smem_bytes(int tb, int32_t shift) {
     return size_t(tb) * size_t(kRouterThreads / 32 + kRouterCluster) * (size_t(4) << shift) * sizeof(float);
 }
@@ -836,12 +710,13 @@ cudaError_t launch_overlapped(void (*kernel)(Args...), dim3 grid, int threads, i
 }  // namespace
 
 size_t moe_scratch_bytes(const MoeArgs& a, const LibCtx& c) {
-    const ExpertPlan p = plan_experts(a, c);
-    return up256(size_t(a.T) * a.top_k * sizeof(PairParts)) + size_t(p.max_rows) * size_t(a.D) * sizeof(float);
+    const ExpertPlan p = plan_experts(a, c.sm_count, c.smem_optin);
+    const int64_t rows = most_part_rows(a, {p.units, p.max_units, c.sm_count});
+    return up256(size_t(a.T) * a.top_k * sizeof(PairParts)) + size_t(rows) * size_t(a.D) * sizeof(float);
 }
 
 int launch_moe(const MoeArgs& a, void* scratch, const LibCtx& c, cudaStream_t stream) {
-    const ExpertPlan plan = plan_experts(a, c);
+    const ExpertPlan plan = plan_experts(a, c.sm_count, c.smem_optin);
     ExpertParams P;
     memset(&P, 0, sizeof(P));
     const int64_t F1 = a.gated ? 2 * int64_t(a.F) : a.F;
@@ -877,9 +752,8 @@ int launch_moe(const MoeArgs& a, void* scratch, const LibCtx& c, cudaStream_t st
     P.pairs = static_cast<PairParts*>(scratch);
     P.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) +
                                        up256(size_t(a.T) * a.top_k * sizeof(PairParts)));
-    P.t_pad = plan.t_pad, P.units = plan.units, P.max_units = plan.max_units;
+    P.t_pad = plan.t_pad, P.sizes = {plan.units, plan.max_units, c.sm_count};
     P.stages = plan.stages, P.ksub = plan.ksub;
-    P.sms = c.sm_count;
     P.ctl = c.ctl;
     P.inject = c.inject;
 
