@@ -23,6 +23,7 @@ void* linear_pair_db_kernel();
 void* linear_tile_forward_kernel(int act);
 void* linear_tile_da_kernel();
 void* linear_tile_db_kernel();
+void* linear_tile_grads_kernel();
 
 namespace {
 
@@ -146,12 +147,17 @@ bool tma_ready(const Mat& m) {
     return reinterpret_cast<uintptr_t>(m.p) % 16 == 0 && m.ld % 8 == 0;
 }
 
+// The pitch of a single row is never stepped over: one that TMA takes.
+void one_row(Mat* m, int32_t rows, int32_t cols) {
+    if (rows == 1) m->ld = cdiv(cols, 8) * 8;
+}
+
 // Makes `m` readable by TMA (copy_in) or writable: itself, or an aligned copy.
 // A TMA store ends at whole 16 bytes: measured, a row of 201 bf16 columns takes
 // 7 columns of its pitch's padding along, so an output whose rows end inside
 // 16 bytes is written to a copy and copied back.
 int aligned_mat(Mat* m, int32_t rows, int32_t cols, bool copy_in, Scratch& ws, RepitchList* copies) {
-    if (rows == 1) m->ld = cdiv(cols, 8) * 8;            // never stepped over
+    one_row(m, rows, cols);
     if (tma_ready(*m) && (copy_in || cols % 8 == 0)) return GBR_OK;
     Mat t;
     t.ld = cdiv(cols, 8) * 8;
@@ -184,7 +190,6 @@ struct Product {
     Dropout drop;
     void* pair_kernel;             // linear_pair.cuh
     void* tile_kernel;             // linear_tile.cuh
-    bool beside;                   // may run next to the launch before it, see run_product
 };
 
 // The tiles of a product on `units` CTA pairs.  The last round is split where
@@ -252,7 +257,6 @@ int run_pair(const Product& p, const LibCtx& c, cudaStream_t stream) {
         if (e != cudaSuccess) return report_cuda(e, "launching the zeroing of the split tiles' counts");
         count_launch();
     }
-    P.beside = p.beside && P.w.split == 0;
     P.drop = p.drop;
     P.ctl = c.ctl;
     P.inject = c.inject;
@@ -301,6 +305,15 @@ double pair_cycles(const Product& p, int sms) {
            rounds * (rounds <= 1.0 ? 640.0 * slices : std::max(512.0 * slices, 4800.0));
 }
 
+// Shared memory of one of two CTAs an SM, and of one alone; the stages that fit.
+constexpr int64_t kTileHalf = 110 * 1024, kTileWhole = 218 * 1024;
+int tile_stages(int bt, int64_t budget) {
+    return int(std::min<int64_t>(linear::kTileMaxStages, (budget - 2304) / linear::tile_stage_bytes(bt)));
+}
+// CTAs that fit at once, one an SM.  Of large clusters fewer do: 144 CTAs in
+// fours, 120 in eights.
+int64_t tile_fit(int cluster, int sms) { return cluster == 8 ? sms * 15 / 19 : cluster == 4 ? sms * 18 / 19 : sms; }
+
 TilePlan plan_tile(const Product& p, int sms) {
     TilePlan best = {0, 0, 0, 1e30};
     double finish = 0.0;
@@ -314,10 +327,8 @@ TilePlan plan_tile(const Product& p, int sms) {
         const double rows = double(std::min<int64_t>(p.I, bt));
         for (int s : {1, 2, 4, 8}) {
             if (s > nks && s > 1) continue;
-            // Of large clusters fewer fit at once: 144 CTAs in fours, 120 in
-            // eights; two an SM, what fits in fours and pairs.
-            const int64_t fours = sms * 18 / 19, fit = s == 8 ? sms * 15 / 19 : s == 4 ? fours : sms;
-            const int64_t fit2 = 2 * (s == 8 ? fours : sms), slices = cdiv(nks, s);
+            // Two an SM, eights fit as fours do alone.
+            const int64_t fit = tile_fit(s, sms), fit2 = 2 * (s == 8 ? tile_fit(4, sms) : sms), slices = cdiv(nks, s);
             // A slice's loads; the wide operand from HBM or shared through L2.
             const double load = 16384.0 / (t_tiles == 1 ? 40.0 : 64.0) + bt * 2.0;
             // Two CTAs an SM where a tile's parts and a ring worth having fit
@@ -327,13 +338,12 @@ TilePlan plan_tile(const Product& p, int sms) {
             // CTA: 6.5 us one an SM, whose memory leaves no room for the next
             // launch's set-up, 5.8 two; one row of 4096^2 7.5 and 6.9; dB of
             // 8192 x 512 x 512, 32 slices: 14.2 and 18.1).
-            constexpr int64_t kHalf = 110 * 1024, kWhole = 218 * 1024;
-            const int64_t small = (kHalf - 2304) / stage;
+            const int64_t small = (kTileHalf - 2304) / stage;
             const bool ample = slices <= small || load >= 2200.0 / double(small);
             const int per_sm = bt <= 128 && (ample || tiles * s > fit) ? 2 : 1;
             const int64_t n = per_sm == 2 ? cdiv(tiles * s, sms) : cdiv(tiles * s, fit);
-            const int64_t budget = per_sm == 2 ? kHalf : kWhole, rounds = cdiv(tiles * s, per_sm == 2 ? fit2 : fit);
-            const int stages = int(std::min<int64_t>(linear::kTileMaxStages, (budget - 2304) / stage));
+            const int64_t budget = per_sm == 2 ? kTileHalf : kTileWhole, rounds = cdiv(tiles * s, per_sm == 2 ? fit2 : fit);
+            const int stages = tile_stages(bt, budget);
             const double feed =
                 std::max(double(n * slices) * load, ample ? 0.0 : double(rounds * slices) * 2200.0 / double(stages));
             // HBM gives its rate to all SMs together; fewer get less of it.
@@ -350,8 +360,10 @@ TilePlan plan_tile(const Product& p, int sms) {
 
 bool vec16(const Mat& m) { return !m || tma_ready(m); }
 
-int run_tile(const Product& p, const TilePlan& plan, const LibCtx& c, cudaStream_t stream) {
-    linear::TileParams P;
+int tile_params(Product p, const TilePlan& plan, const LibCtx& c, linear::TileParams* out) {
+    one_row(&p.A, p.a_mn ? p.Kc : p.I, p.a_mn ? p.I : p.Kc);
+    one_row(&p.B, p.b_mn ? p.Kc : p.J, p.b_mn ? p.J : p.Kc);
+    linear::TileParams& P = *out;
     memset(&P, 0, sizeof(P));
     int r;
     if (p.Kc > 0) {
@@ -375,38 +387,38 @@ int run_tile(const Product& p, const TilePlan& plan, const LibCtx& c, cudaStream
     P.stages = plan.stages;
     P.tmem_cols = 32;
     while (int32_t(P.tmem_cols) < plan.bt) P.tmem_cols *= 2;
-    P.beside = p.beside;
     P.drop = p.drop;
     P.ctl = c.ctl;
     P.inject = c.inject;
-    const size_t smem = linear::tile_smem_bytes(plan.bt, plan.stages);
-    if ((r = raise_kernel_smem(p.tile_kernel, smem, c.device)) != GBR_OK) return r;
-    const int64_t ctas = int64_t(P.t_tiles) * cdiv(p.J, 128) * plan.split;
-    void* args[] = {&P};
-    const cudaError_t e = launch_kernel(p.tile_kernel, dim3(unsigned(ctas)), linear::kTileThreads, smem, plan.split,
-                                       args, stream);
+    return GBR_OK;
+}
+
+int64_t tile_ctas(const Product& p, const TilePlan& plan) { return cdiv(p.I, plan.bt) * cdiv(p.J, 128) * plan.split; }
+
+int launch_tiles(void* kernel, void* params, int64_t ctas, size_t smem, int cluster, const LibCtx& c,
+                 cudaStream_t stream) {
+    const int r = raise_kernel_smem(kernel, smem, c.device);
+    if (r != GBR_OK) return r;
+    void* args[] = {params};
+    const cudaError_t e = launch_kernel(kernel, dim3(unsigned(ctas)), linear::kTileThreads, smem, cluster, args, stream);
     if (e != cudaSuccess) return report_cuda(e, "launching a linear kernel");
     count_launch();
     return GBR_OK;
 }
 
+int run_tile(const Product& p, const TilePlan& plan, const LibCtx& c, cudaStream_t stream) {
+    linear::TileParams P;
+    const int r = tile_params(p, plan, c, &P);
+    if (r != GBR_OK) return r;
+    return launch_tiles(p.tile_kernel, &P, tile_ctas(p, plan), linear::tile_smem_bytes(plan.bt, plan.stages),
+                        plan.split, c, stream);
+}
+
 // Runs the product with whatever TMA cannot address replaced by aligned copies.
-//
-// Two products that do not depend on one another run side by side: the second
-// (`beside`) does not wait for the first before it starts, but before it ends,
-// so that whoever waits for the second has waited for both.  It starts when
-// every CTA of the first has issued its loads, hence after everything that the
-// first one waited for.  That holds where the first is one launch that took no
-// scratch (the second one's could be the same memory) and nothing, no copy of
-// an operand and no zeroing, is launched between them; *one_launch says so of
-// this product.  Gradients (with dZ) one after the other / side by side, us:
-// 64 x 512 x 512 13.4 / 10.1, 301 x 520 x 1000 16.8 / 15.6, 512 x 4096 x 4096
-// 48.0 / 46.1, 4096 x 4096 x 4096 the same.
-int run_product(Product p, const LibCtx& c, cudaStream_t stream, bool* one_launch = nullptr) {
+int run_product(Product p, const LibCtx& c, cudaStream_t stream) {
     Scratch ws(c, stream);
     int r;
-    const Mat A = p.A, B = p.B, C = p.C, Z = p.Z;
-    if (one_launch != nullptr) *one_launch = false;
+    const Mat C = p.C, Z = p.Z;
     const TilePlan plan = plan_tile(p, c.sm_count);
     const bool tile = plan.cycles < pair_cycles(p, c.sm_count);
     RepitchList in, out;
@@ -414,8 +426,6 @@ int run_product(Product p, const LibCtx& c, cudaStream_t stream, bool* one_launc
         if ((r = aligned_mat(&p.A, p.a_mn ? p.Kc : p.I, p.a_mn ? p.I : p.Kc, true, ws, &in)) != GBR_OK) return r;
         if ((r = aligned_mat(&p.B, p.b_mn ? p.Kc : p.J, p.b_mn ? p.J : p.Kc, true, ws, &in)) != GBR_OK) return r;
     }
-    const bool in_place = in.n == 0;
-    p.beside = p.beside && in_place;
     // The kernel of single tiles reads and writes everything else with plain accesses.
     if (!tile) {
         if (p.R && (r = aligned_mat(&p.R, p.I, p.J, true, ws, &in)) != GBR_OK) return r;
@@ -424,11 +434,49 @@ int run_product(Product p, const LibCtx& c, cudaStream_t stream, bool* one_launc
         if (p.C.p != C.p) out.add(p.C, C, p.I, p.J);
         if (p.Z.p != Z.p) out.add(p.Z, Z, p.I, p.J);
     }
-    if (one_launch != nullptr)
-        *one_launch = in_place && out.n == 0 && (tile || pair_work(p, c.sm_count / 2).split == 0);
     if ((r = in.launch(true, stream)) != GBR_OK) return r;
     if ((r = tile ? run_tile(p, plan, c, stream) : run_pair(p, c, stream)) != GBR_OK) return r;
     return out.launch(false, stream);
+}
+
+// The gradients' products, dA and dB: one grid, which waits for dZ as any launch
+// does, where both take single tiles and nothing has to be copied first.  The
+// larger cluster serves both (the smaller split divides it, all being powers of
+// two), and where that is more CTAs than fit one an SM, rings that let two in,
+// which each product for itself may not want.  Tiles of more than 128 rows leave
+// no room for two: with those, no more CTAs than two rounds.
+// Gradients with dZ and dbias (GELU), one after the other / in one grid, us:
+// 64 x 512 x 512 13.4 / 9.1, 301 x 520 x 1000 17.6 / 13.6, 1024^3 22.4 / 16.0,
+// 4096 x 512 x 512 29.2 / 20.2, 700 x 1032 x 264 17.3 / 13.4.  Over 46 sizes drawn
+// at random that share a grid dA and dB take 0.65 of the time in the mean, over 45
+// more with two rounds or more 0.90, and 1.12 at worst, with one row, where dB alone
+// would go without dA's cluster (1 x 1400 x 3424 14.1 / 15.8).  2 x 12136 x 336,
+// three rounds with tiles of 256 rows: 16.2 / 19.3.
+int run_grads(const Product& da, const Product& db, const LibCtx& c, cudaStream_t stream) {
+    // What TMA reads, or a matrix of one row, whose pitch does not matter.
+    auto ready = [](Mat m, int32_t rows) {
+        one_row(&m, rows, 8);
+        return tma_ready(m);
+    };
+    TilePlan pa = plan_tile(da, c.sm_count), pb = plan_tile(db, c.sm_count);
+    const int cluster = std::max(pa.split, pb.split);
+    const int64_t first = cdiv(tile_ctas(da, pa), cluster) * cluster, second = cdiv(tile_ctas(db, pb), cluster) * cluster;
+    const int64_t fit = tile_fit(cluster, c.sm_count);
+    const bool pairable = pa.bt <= 128 && pb.bt <= 128;
+    int r;
+    if (pa.cycles >= pair_cycles(da, c.sm_count) || pb.cycles >= pair_cycles(db, c.sm_count) || da.Kc == 0 || db.Kc == 0 ||
+        (!pairable && first + second > 2 * fit) || !ready(da.A, da.I) || !ready(da.B, da.J) || !ready(db.A, db.Kc)) {
+        if ((r = run_product(da, c, stream)) != GBR_OK) return r;
+        return run_product(db, c, stream);
+    }
+    if (pairable && first + second > fit)
+        for (TilePlan* p : {&pa, &pb}) p->stages = std::min(p->stages, tile_stages(p->bt, kTileHalf));
+    linear::TileGradParams G;
+    if ((r = tile_params(da, pa, c, &G.da)) != GBR_OK || (r = tile_params(db, pb, c, &G.db)) != GBR_OK) return r;
+    G.first = uint32_t(first);
+    G.cluster = uint32_t(cluster);
+    const size_t smem = std::max(linear::tile_smem_bytes(pa.bt, pa.stages), linear::tile_smem_bytes(pb.bt, pb.stages));
+    return launch_tiles(linear_tile_grads_kernel(), &G, first + second, smem, cluster, c, stream);
 }
 
 // ------------------------------------------------------------ dZ and dbias
@@ -603,29 +651,23 @@ int launch_linear_dz(const LinearGradArgs& a, const LibCtx& c, cudaStream_t stre
     return GBR_OK;
 }
 
-int launch_linear_da(Mat dZ, Mat B, Mat dA, int32_t M, int32_t N, int32_t K, const LibCtx& c, cudaStream_t stream,
-                     bool* one_launch) {
-    Product p = {};
-    p.A = dZ, p.B = B;
-    p.a_mn = false, p.b_mn = false;
-    p.I = M, p.J = K, p.Kc = N;
-    p.C = dA;
-    p.pair_kernel = linear_pair_da_kernel();
-    p.tile_kernel = linear_tile_da_kernel();
-    return run_product(p, c, stream, one_launch);
-}
-
-int launch_linear_db(Mat A, Mat dZ, Mat dB, int32_t M, int32_t N, int32_t K, const LibCtx& c, cudaStream_t stream,
-                     bool beside) {
-    Product p = {};
-    p.beside = beside;
-    p.A = A, p.B = dZ;
-    p.a_mn = true, p.b_mn = true;
-    p.I = K, p.J = N, p.Kc = M;
-    p.C = dB;
-    p.pair_kernel = linear_pair_db_kernel();
-    p.tile_kernel = linear_tile_db_kernel();
-    return run_product(p, c, stream);
+int launch_linear_grads(Mat A, Mat B, Mat dZ, Mat dA, Mat dB, int32_t M, int32_t N, int32_t K, const LibCtx& c,
+                        cudaStream_t stream) {
+    Product a = {}, b = {};
+    a.A = dZ, a.B = B;
+    a.a_mn = false, a.b_mn = false;
+    a.I = M, a.J = K, a.Kc = N;
+    a.C = dA;
+    a.pair_kernel = linear_pair_da_kernel();
+    a.tile_kernel = linear_tile_da_kernel();
+    b.A = A, b.B = dZ;
+    b.a_mn = true, b.b_mn = true;
+    b.I = K, b.J = N, b.Kc = M;
+    b.C = dB;
+    b.pair_kernel = linear_pair_db_kernel();
+    b.tile_kernel = linear_tile_db_kernel();
+    if (dA && dB) return run_grads(a, b, c, stream);
+    return dA ? run_product(a, c, stream) : run_product(b, c, stream);
 }
 
 }  // namespace gbr

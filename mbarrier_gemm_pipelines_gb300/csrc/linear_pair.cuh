@@ -98,7 +98,6 @@ struct PairParams {
     PairWork w;
     uint32_t has_z, has_r;
     uint32_t bias_vec;                                 // bias starts on 16 bytes
-    uint32_t beside;                                   // runs next to the grid before it
     Dropout drop;
     KernelCtl ctl;
     FaultInjection inject;                             // self test only
@@ -175,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::cluster_sync_all();
     ptx::tc_fence_after_sync();
     const uint32_t tmem_base = *tmem_holder;
-    if (!P.beside) ptx::griddep_wait();
+    ptx::griddep_wait();
     uint32_t issued = 0;
 
     if (warp < 4) {
@@ -444,7 +443,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tc_fence_after_sync();
         ptx::tmem_dealloc_pair(tmem_base, kTmemCols);
     }
-    if (P.beside) ptx::griddep_wait();   // this grid ends after the one before it
 }
 
 }  // namespace linear

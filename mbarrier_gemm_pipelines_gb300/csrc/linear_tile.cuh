@@ -50,7 +50,6 @@ struct TileParams {
     int32_t stages;
     uint32_t tmem_cols;
     uint32_t vec;                                      // 16-byte accesses to R, C and Z are aligned
-    uint32_t beside;                                   // runs next to the grid before it
     Dropout drop;
     KernelCtl ctl;
     FaultInjection inject;                             // self test only
@@ -119,9 +118,10 @@ __device__ __forceinline__ void finish8(const TileParams& P, int32_t i, int32_t 
     }
 }
 
+// One CTA: `block` among those of the product, in clusters of `cluster` CTAs, a
+// multiple of P.split that divides the number of the first of them.
 template <bool W_MN, bool X_MN, int ACT, bool PLAIN>
-__global__ void __launch_bounds__(kTileThreads)
-    linear_tile_kernel(const __grid_constant__ TileParams P) {
+__device__ __forceinline__ void tile_cta(const TileParams& P, uint32_t block, uint32_t cluster) {
     extern __shared__ uint8_t smem_raw[];
     uint64_t* full = reinterpret_cast<uint64_t*>(align_1024(smem_raw));
     uint64_t* empty = full + kTileMaxStages;
@@ -131,11 +131,14 @@ __global__ void __launch_bounds__(kTileThreads)
     uint8_t* ring = align_1024(reinterpret_cast<uint8_t*>(full) + kTileBarBytes);
 
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u;
-    const uint32_t rank = ptx::cluster_ctarank();
     const uint32_t S = uint32_t(P.split), stages = uint32_t(P.stages);
-    const uint32_t tile = blockIdx.x / S;
+    const uint32_t tile = block / S, rank = block % S;
+    const uint32_t peer0 = cluster > 1 ? ptx::cluster_ctarank() - rank : 0u;   // of those that share the tile
     const int32_t i0 = int32_t(tile % uint32_t(P.t_tiles)) * P.bt, j0 = int32_t(tile / uint32_t(P.t_tiles)) * 128;
-    const int32_t ks0 = int32_t(int64_t(P.num_ks) * rank / S), ks1 = int32_t(int64_t(P.num_ks) * (rank + 1) / S);
+    // A CTA past the last tile only keeps its cluster whole (unsigned: up to 2^31).
+    const bool idle = tile / uint32_t(P.t_tiles) * 128u >= uint32_t(P.J);
+    const int32_t num_ks = idle ? 0 : P.num_ks;
+    const int32_t ks0 = int32_t(int64_t(num_ks) * rank / S), ks1 = int32_t(int64_t(num_ks) * (rank + 1) / S);
     const uint32_t stage_bytes = tile_stage_bytes(P.bt);
 
     if (threadIdx.x == 0) {
@@ -159,7 +162,7 @@ __global__ void __launch_bounds__(kTileThreads)
     ptx::tc_fence_after_sync();
     const uint32_t tmem = *tmem_holder;
     const uint32_t ring_base = ptx::smem_addr(ring);
-    if (!P.beside) ptx::griddep_wait();
+    ptx::griddep_wait();
 
     uint32_t issued = 0;
     if (warp == 4 && lane == 0) {
@@ -223,7 +226,7 @@ __global__ void __launch_bounds__(kTileThreads)
     // All MMAs of this CTA are done: their operands' memory may be reused.
     const bool done = mbar_wait_warp(ptx::smem_addr(acc_full), 0, P.ctl, abort_flag, kSiteEpiAccFull, 0);
     ptx::tc_fence_after_sync();
-    const int32_t rows = min(P.bt, P.I - i0);
+    const int32_t rows = idle ? 0 : min(P.bt, P.I - i0);
     if (warp < 4 && done) {
         // Part of the tile: [row][128 columns] fp32.
         float* part = reinterpret_cast<float*>(ring) + warp * 32u + lane;
@@ -237,7 +240,7 @@ __global__ void __launch_bounds__(kTileThreads)
     }
     ptx::tc_fence_before_sync();
     __syncwarp();
-    if (S > 1)
+    if (cluster > 1)
         ptx::cluster_sync_all();
     else
         __syncthreads();
@@ -260,7 +263,7 @@ __global__ void __launch_bounds__(kTileThreads)
 #pragma unroll
             for (uint32_t s = 0; s < 8; ++s)
                 if (s < S) {
-                    const uint32_t from = ptx::mapa_shared(at, s);
+                    const uint32_t from = ptx::mapa_shared(at, peer0 + s);
                     a[s] = ptx::ld_shared_cluster_v4_f32(from);
                     b[s] = ptx::ld_shared_cluster_v4_f32(from + 16);
                 }
@@ -275,7 +278,7 @@ __global__ void __launch_bounds__(kTileThreads)
         }
     }
     __syncwarp();
-    if (S > 1)
+    if (cluster > 1)
         ptx::cluster_sync_all();   // no CTA leaves while a peer may read its part
     else
         __syncthreads();
@@ -283,8 +286,20 @@ __global__ void __launch_bounds__(kTileThreads)
         ptx::tc_fence_after_sync();
         ptx::tmem_dealloc(tmem, P.tmem_cols);
     }
-    if (P.beside) ptx::griddep_wait();   // this grid ends after the one before it
 }
+
+template <bool W_MN, bool X_MN, int ACT, bool PLAIN>
+__global__ void __launch_bounds__(kTileThreads)
+    linear_tile_kernel(const __grid_constant__ TileParams P) {
+    tile_cta<W_MN, X_MN, ACT, PLAIN>(P, blockIdx.x, uint32_t(P.split));
+}
+
+// Both products of the gradients in one grid: dA in the first `first` CTAs, dB in
+// the others.
+struct TileGradParams {
+    TileParams da, db;
+    uint32_t first, cluster;
+};
 
 }  // namespace linear
 }  // namespace gbr

@@ -250,14 +250,9 @@ int gemm_bias_act_backward(const void* dC, int64_t lddc, const void* A, int64_t 
             g.dZ = dz;
         }
         if ((want_bias || g.dZ) && (r = launch_linear_dz(g, c, st)) != GBR_OK) return r;
-        bool beside = false;
-        if (want_da &&
-            (r = launch_linear_da(dz, {B, ldb}, {dA, ldda}, g.M, g.N, int32_t(K), c, st, &beside)) != GBR_OK)
-            return r;
-        if (want_db &&
-            (r = launch_linear_db({A, lda}, dz, {dB, lddb}, g.M, g.N, int32_t(K), c, st, beside)) != GBR_OK)
-            return r;
-        return GBR_OK;
+        if (!products) return GBR_OK;
+        return launch_linear_grads({A, lda}, {B, ldb}, dz, {want_da ? dA : nullptr, ldda}, {want_db ? dB : nullptr, lddb},
+                                   g.M, g.N, int32_t(K), c, st);
     });
 }
 

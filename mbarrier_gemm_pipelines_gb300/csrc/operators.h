@@ -76,12 +76,9 @@ int launch_linear_dz(const LinearGradArgs& a, const LibCtx& c, cudaStream_t stre
 
 // The gradients' products: dA[M, K] = dZ[M, N] B[K, N]^T and
 // dB[K, N] = A[M, K]^T dZ[M, N].
-// `one_launch`: the product was a single launch without scratch, so that the
-// product of dB may run `beside` it if it is the next launch.
-int launch_linear_da(Mat dZ, Mat B, Mat dA, int32_t M, int32_t N, int32_t K, const LibCtx& c, cudaStream_t stream,
-                     bool* one_launch);
-int launch_linear_db(Mat A, Mat dZ, Mat dB, int32_t M, int32_t N, int32_t K, const LibCtx& c, cudaStream_t stream,
-                     bool beside);
+// Either may be wanted alone (the other's p NULL).
+int launch_linear_grads(Mat A, Mat B, Mat dZ, Mat dA, Mat dB, int32_t M, int32_t N, int32_t K, const LibCtx& c,
+                        cudaStream_t stream);
 
 // ------------------------------------------------------------ expert layer
 constexpr int kMoeMaxTokens = 64, kMoeMaxExperts = 256, kMoeMaxTopK = 8;

@@ -13,12 +13,13 @@ BARRIER = re.compile(r"\b(cluster_sync_all|cluster_wait)\s*\(")
 
 
 def kernels():
-    """(file, name, body) of every __global__ function with a body."""
+    """(file, name, body) of every __global__ function with a body, and of every device function that is a kernel's
+    whole body (their names end in _cta)."""
     for path in sorted(glob.glob(os.path.join(CSRC, "*.cu*"))):
         with open(path) as f:
             text = re.sub(r"//[^\n]*|/\*.*?\*/", "", f.read(), flags=re.S)
-        for m in re.finditer(r"__global__", text):
-            name = re.compile(r"(\w+_kernel)\s*\(").search(text, m.end())
+        for m in re.finditer(r"__global__|__device__ __forceinline__ void (?=\w+_cta\()", text):
+            name = re.compile(r"(\w+_(?:kernel|cta))\s*\(").search(text, m.end())
             start = text.index("{", name.end())
             depth, at = 0, start
             while True:
@@ -34,7 +35,7 @@ FOUND = [(f, n, b) for f, n, b in kernels() if REMOTE.search(b)]
 
 def test_kernels_are_found():
     names = {n for _, n, _ in FOUND}
-    assert {"moe_router_kernel", "dz_kernel", "linear_tile_kernel", "linear_pair_kernel"} <= names
+    assert {"moe_router_kernel", "dz_kernel", "tile_cta", "linear_pair_kernel"} <= names
 
 
 @pytest.mark.parametrize("file,name,body", FOUND, ids=[n for _, n, _ in FOUND])
