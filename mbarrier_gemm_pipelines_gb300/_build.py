@@ -7,6 +7,9 @@ parallel, then linked into one shared library next to this file.
 that is compiled against PyTorch; it is linked to ``libgbr.so``.  The results
 are git-ignored and rebuilt on each machine (they are specific to the host's
 architecture and to its PyTorch).
+
+The library needs nvcc alone and is linked first.  Where PyTorch, its headers
+or Python's are missing, the binding is left out, with a warning.
 """
 from __future__ import annotations
 
@@ -17,6 +20,7 @@ import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
@@ -48,19 +52,35 @@ def _deps():
             + glob.glob(os.path.join(INCLUDE, "*.h")) + [EXT_SRC, os.path.abspath(__file__)])
 
 
+def _torch_dir():
+    spec = importlib.util.find_spec("torch")
+    return list(spec.submodule_search_locations)[0] if spec is not None and spec.submodule_search_locations else None
+
+
+def binding_lacks():
+    """What the Python binding cannot be compiled without and is not there, or None."""
+    torch_dir = _torch_dir()
+    if torch_dir is None:
+        return "PyTorch"
+    if not os.path.exists(os.path.join(torch_dir, "include", "ATen", "ATen.h")):
+        return "PyTorch's headers"
+    if not os.path.exists(os.path.join(torch_dir, "lib", "libc10_cuda.so")):
+        return "PyTorch for CUDA"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "Python.h"
+    return None
+
+
 def up_to_date() -> bool:
-    if not (os.path.exists(LIB_PATH) and os.path.exists(EXT_PATH)):
+    made = [LIB_PATH] if binding_lacks() else [LIB_PATH, EXT_PATH]
+    if not all(os.path.exists(p) for p in made):
         return False
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(EXT_PATH))
+    t = min(os.path.getmtime(p) for p in made)
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
-def _compile_ext(obj: str) -> str:
-    """Compiles the Python binding to an object file; returns PyTorch's folder."""
-    spec = importlib.util.find_spec("torch")
-    if spec is None or not spec.submodule_search_locations:
-        raise RuntimeError("PyTorch not found; the Python binding is compiled against its headers")
-    torch_dir = list(spec.submodule_search_locations)[0]
+def _compile_ext(obj: str, torch_dir: str) -> None:
+    """Compiles the Python binding to an object file."""
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
     include = [INCLUDE, os.path.join(torch_dir, "include"),
                os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
@@ -69,7 +89,6 @@ def _compile_ext(obj: str) -> str:
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError("g++ failed for %s:\n%s\n%s" % (EXT_SRC, res.stdout, res.stderr))
-    return torch_dir
 
 
 def _link_ext(obj: str, torch_dir: str) -> None:
@@ -87,6 +106,9 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
     """Compile and link; returns the library path."""
     if not force and up_to_date():
         return LIB_PATH
+    lacks, torch_dir = binding_lacks(), _torch_dir()
+    if lacks:
+        warnings.warn("the Python binding of the feed-forward operators is not built: %s not found" % lacks)
     nvcc = _nvcc()
     os.makedirs(OBJ_DIR, exist_ok=True)
     extra = ["-Xptxas", "-v"] if ptxas_verbose else []
@@ -102,9 +124,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
     srcs = _sources()
     ext_obj = os.path.join(OBJ_DIR, "operators_ext.o")
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
-        ext = ex.submit(_compile_ext, ext_obj)
+        ext = None if lacks else ex.submit(_compile_ext, ext_obj, torch_dir)
         results = list(ex.map(compile_one, srcs))
-        torch_dir = ext.result()
     if verbose or ptxas_verbose:
         for _, log in results:
             if log.strip():
@@ -115,7 +136,9 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
     if res.returncode != 0:
         raise RuntimeError("link failed:\n%s\n%s" % (res.stdout, res.stderr))
     os.replace(tmp, LIB_PATH)
-    _link_ext(ext_obj, torch_dir)
+    if ext is not None:
+        ext.result()
+        _link_ext(ext_obj, torch_dir)
     return LIB_PATH
 
 
