@@ -5,6 +5,10 @@ The functions here give the arguments their names, defaults and documentation;
 calls the library.  There is no CPU fallback: a missing build or a CPU tensor
 raises.
 
+Outputs have no autograd history: a caller connects the gradients' functions to
+its graph.  A tensor that a call writes in place (Y=, C=, Z=, dA=, ...) moves its
+version, so that autograd refuses a graph that saved it before.
+
 `stream` is a torch stream or a raw handle; without it a call runs on the
 current stream.  With it the outputs that the call makes belong to that stream,
 as if made under ``torch.cuda.stream(stream)``: use them there, or after an

@@ -181,12 +181,20 @@ private:
     c10::cuda::OptionalCUDAStreamGuard guard_;
 };
 
+// A tensor of the caller's that the call has written: its version moves, so that autograd refuses a graph that saved
+// it before.  (A tensor made in inference mode has none.)
+PyObject* written(PyObject* o) {
+    const at::Tensor& t = THPVariable_Unpack(o);
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+    return Py_NewRef(o);
+}
+
 // An output: the caller's, or a new one.
 struct Out {
     PyObject* given = nullptr;
     at::Tensor made;
     Mat m;
-    PyObject* wrap() const { return given != nullptr ? Py_NewRef(given) : THPVariable_Wrap(made); }
+    PyObject* wrap() const { return given != nullptr ? written(given) : THPVariable_Wrap(made); }
 };
 
 Out out_mat(PyObject* o, const char* name, const at::Tensor& like, int dev, int64_t rows, int64_t cols) {
@@ -264,7 +272,7 @@ PyObject* dropout_add_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
             return dropout_add(x.p, x.ld, has_r ? r.p : nullptr, r.ld, y.p, y.ld, x.rows, x.cols,
                                type == at::kBFloat16 ? GBR_BF16 : GBR_F32_FFMA, p, seed, offset, st);
         });
-        return has_y ? Py_NewRef(a[5]) : THPVariable_Wrap(made);
+        return has_y ? written(a[5]) : THPVariable_Wrap(made);
     });
 }
 

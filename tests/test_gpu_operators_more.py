@@ -46,3 +46,28 @@ def test_gradients_together_and_alone(gbr, M, K, N):
         rA, rB, _, _ = ref.linear_grad(dC, A, B, Z, act, 0.1, 3, 0)
         close(dA, rA, TWO)
         close(dB, rB, TWO)
+
+
+def test_versions_of_given_outputs(gbr):
+    """A tensor written in place moves its version once a call; a refused call and a new output leave versions alone."""
+    A, B = torch.ones(16, 24, device="cuda", dtype=BF), torch.ones(24, 32, device="cuda", dtype=BF)
+    C, Z, dA, dB = (torch.zeros(s, device="cuda", dtype=BF) for s in ((16, 32), (16, 32), (16, 24), (24, 32)))
+    db, X, Wr = torch.zeros(32, device="cuda"), torch.zeros(16, 24, device="cuda", dtype=BF), torch.ones(24, 2, device="cuda")
+    W1, W2 = torch.ones(2, 24, 8, device="cuda", dtype=BF), torch.ones(2, 8, 24, device="cuda", dtype=BF)
+    gbr.gemm_bias_act(A, B, C=C, Z=Z)
+    gbr.gemm_bias_act_backward(C, A, B, dA=dA, dB=dB, dbias=db)
+    gbr.dropout_add(X, Y=X)
+    gbr.moe_layer(A, Wr, W1, None, W2, None, Y=dA)
+    with pytest.raises(gbr.GbrError):
+        gbr.gemm_bias_act(A, B, C=C, p=2.0)
+    assert [t._version for t in (A, B, C, Z, dA, dB, db, X, Wr, W1, W2)] == [0, 0, 1, 1, 2, 1, 1, 1, 0, 0, 0]
+    assert gbr.dropout_add(X)._version == 0
+    w = torch.ones(4, 8, device="cuda", requires_grad=True)
+    x = torch.ones(4, 8, device="cuda")
+    y = (w * x).sum()
+    gbr.dropout_add(x, Y=x)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    with torch.inference_mode():
+        x = torch.ones(4, 8, device="cuda")
+    assert gbr.dropout_add(x, p=0.0, Y=x) is x
