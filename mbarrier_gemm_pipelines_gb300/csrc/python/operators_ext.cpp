@@ -390,7 +390,7 @@ PyObject* moe_layer_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const bool routing = truth(a[10]);
         at::Tensor ids, weights;
         if (routing) {
-            const int64_t k = top_k < 0 ? 0 : top_k;        // a wrong top_k is refused by the call
+            const int64_t k = top_k < 0 || top_k > E ? 0 : top_k;       // a wrong top_k is refused by the call
             ids = at::empty({T, k}, X.options().dtype(at::kLong));
             weights = at::empty({T, k}, X.options().dtype(at::kFloat));
         }

@@ -71,3 +71,11 @@ def test_versions_of_given_outputs(gbr):
     with torch.inference_mode():
         x = torch.ones(4, 8, device="cuda")
     assert gbr.dropout_add(x, p=0.0, Y=x) is x
+
+
+@pytest.mark.parametrize("top_k", [-1, 0, 5, 1 << 40, 1 << 62])
+def test_wrong_top_k_with_routing(gbr, top_k):
+    """Refused as such, before the routing's tensors are made in that size."""
+    A, W = torch.ones(16, 16, device="cuda", dtype=BF), torch.ones(4, 16, 16, device="cuda", dtype=BF)
+    with pytest.raises(gbr.GbrError, match="top_k"):
+        gbr.moe_layer(A, torch.ones(16, 4, device="cuda"), W, None, W, None, top_k=top_k, return_routing=True)
