@@ -34,7 +34,7 @@ def _load():
     """The compiled binding (it must have been built: ``__graft_entry__.build()``)."""
     global _ext
     if _ext is None:
-        import torch  # noqa: F401  (its libraries are what the binding is linked to)
+        import torch                    # its libraries are what the binding is linked to
         lib()
         path = _build.EXT_PATH
         if not os.path.exists(path):
@@ -42,7 +42,7 @@ def _load():
         loader = importlib.machinery.ExtensionFileLoader("_operators_ext", path)
         module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_operators_ext", loader))
         loader.exec_module(module)
-        module.set_error(GbrError)
+        module.set_errors(GbrError, torch.OutOfMemoryError)
         _ext = module
     return _ext
 

@@ -25,6 +25,7 @@
 namespace {
 
 PyObject* g_error = nullptr;       // mbarrier_gemm_pipelines_gb300.GbrError
+PyObject* g_no_memory = nullptr;   // torch.OutOfMemoryError
 
 // Raised by the checks once a Python exception is set.
 struct Refused {};
@@ -210,7 +211,7 @@ Out out_mat(PyObject* o, const char* name, const at::Tensor& like, int dev, int6
     return r;
 }
 
-// Runs `body` with C++ exceptions turned into Python's.
+// Runs `body` with C++ exceptions turned into Python's; an output that finds no memory raises what torch.empty would.
 template <class F>
 PyObject* guarded(Py_ssize_t got, Py_ssize_t want, F&& body) {
     if (got != want) {
@@ -220,6 +221,12 @@ PyObject* guarded(Py_ssize_t got, Py_ssize_t want, F&& body) {
     try {
         return body();
     } catch (const Refused&) {
+        return nullptr;
+    } catch (const c10::OutOfMemoryError& e) {
+        PyErr_SetString(g_no_memory, e.what_without_backtrace());
+        return nullptr;
+    } catch (const c10::Error& e) {
+        PyErr_SetString(PyExc_RuntimeError, e.what_without_backtrace());
         return nullptr;
     } catch (const std::exception& e) {
         PyErr_SetString(PyExc_RuntimeError, e.what());
@@ -406,10 +413,13 @@ PyObject* moe_layer_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
-// set_error(GbrError)
-PyObject* set_error_py(PyObject*, PyObject* kind) {
-    Py_XSETREF(g_error, Py_NewRef(kind));
-    Py_RETURN_NONE;
+// set_errors(GbrError, torch.OutOfMemoryError)
+PyObject* set_errors_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 2, [&]() -> PyObject* {
+        Py_XSETREF(g_error, Py_NewRef(a[0]));
+        Py_XSETREF(g_no_memory, Py_NewRef(a[1]));
+        Py_RETURN_NONE;
+    });
 }
 
 template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
@@ -422,7 +432,7 @@ PyMethodDef g_methods[] = {
     {"gemm_bias_act", fast<gemm_bias_act_py>(), METH_FASTCALL, nullptr},
     {"gemm_bias_act_backward", fast<gemm_bias_act_backward_py>(), METH_FASTCALL, nullptr},
     {"moe_layer", fast<moe_layer_py>(), METH_FASTCALL, nullptr},
-    {"set_error", set_error_py, METH_O, nullptr},
+    {"set_errors", fast<set_errors_py>(), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 

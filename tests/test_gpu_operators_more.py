@@ -79,3 +79,13 @@ def test_wrong_top_k_with_routing(gbr, top_k):
     A, W = torch.ones(16, 16, device="cuda", dtype=BF), torch.ones(4, 16, 16, device="cuda", dtype=BF)
     with pytest.raises(gbr.GbrError, match="top_k"):
         gbr.moe_layer(A, torch.ones(16, 4, device="cuda"), W, None, W, None, top_k=top_k, return_routing=True)
+
+
+def test_no_memory_for_an_output(gbr):
+    """Outputs of 2 TB: PyTorch's own error, as for any of its tensors, and the next call works."""
+    n = 1 << 20
+    A, B = torch.ones(n, 8, device="cuda", dtype=BF), torch.ones(8, n, device="cuda", dtype=BF)
+    with pytest.raises(torch.OutOfMemoryError):
+        gbr.gemm_bias_act(A, B)
+    assert (gbr.gemm_bias_act(A[:16], B[:, :16].contiguous()) == 8).all()
+    gbr.check_device()
