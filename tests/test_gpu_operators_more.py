@@ -1,4 +1,5 @@
-"""More of the feed-forward operators' paths on the GPU: the gradients' products in one grid and one after the other."""
+"""More of the feed-forward operators' paths on the GPU: the gradients' products in one grid and one after the other,
+expert layers of more parts than SMs and of many experts, and rows past 32 bits.  Bars as in test_gpu_operators.py."""
 import math
 import random
 
@@ -7,7 +8,7 @@ import torch
 
 import ffn_reference as ref
 from gpu_helpers import load_library, require_gpu
-from test_gpu_operators import BF, TWO, close, normal, rng
+from test_gpu_operators import BF, TWO, close, moe_inputs, normal, rng
 
 pytestmark = pytest.mark.gpu
 
@@ -89,3 +90,79 @@ def test_no_memory_for_an_output(gbr):
         gbr.gemm_bias_act(A, B)
     assert (gbr.gemm_bias_act(A[:16], B[:, :16].contiguous()) == 8).all()
     gbr.check_device()
+
+
+MOE = [
+    # T, D, F, E, top_k, act, gated, biases
+    (64, 256, 14336, 64, 8, "relu", False, True),     # more units a part than fit: several parts a CTA
+    (64, 256, 14336, 64, 8, "silu", True, True),
+    (1, 64, 65536, 2, 2, "gelu", False, True),
+    (48, 128, 16384, 40, 7, "gelu_tanh", True, False),
+    (40, 512, 72, 250, 8, "silu", True, True),        # four tokens a router cluster, 64 lanes along the experts
+    (64, 128, 64, 256, 8, "relu", False, True),
+    (33, 8, 8, 129, 1, "gelu", True, True),
+    (20, 64, 520, 128, 8, "silu", False, True),
+    (64, 1000, 200, 3, 3, "silu", True, True),        # every expert has every token
+    (2, 8, 4096, 256, 8, "relu", True, False),
+]
+
+
+@pytest.mark.parametrize("T,D,F,E,top_k,act,gated,biases", MOE)
+def test_moe_cuts_and_routers(gbr, T, D, F, E, top_k, act, gated, biases):
+    x = moe_inputs(T, D, F, E, gated, biases, 3 * T + D + F)
+    Y, ids, w = gbr.moe_layer(*x, top_k=top_k, act=act, gated=gated, return_routing=True)
+    gbr.check_device()
+    ry, rids, rw = ref.moe(*x, top_k, act, gated)
+    assert torch.equal(ids, rids)
+    assert (w.double() - rw).abs().max().item() <= 1e-5
+    close(Y, ry, TWO)
+    for _ in range(10):
+        assert torch.equal(Y, gbr.moe_layer(*x, top_k=top_k, act=act, gated=gated))
+
+
+@pytest.mark.parametrize("chosen", [8, 9, 40, 250])
+def test_moe_skewed_routing(gbr, chosen):
+    """All tokens on the same 8 experts, or spread over as many as are given: what the scratch has to hold."""
+    T, D, F, E, top_k = 64, 64, 8192, 250, 8
+    x = moe_inputs(T, D, F, E, False, True, chosen)
+    # Column t of X is one for token t alone, so that row t of Wr is its logits.
+    x[0].zero_()
+    x[0][:, :T] = torch.eye(T, device="cuda").to(BF)
+    x[1].copy_(torch.arange(E, 0, -1, device="cuda").float() * -1e-3)
+    pick = torch.stack([(torch.arange(top_k) + t * 5) % chosen for t in range(T)]).cuda()
+    x[1].scatter_(1, pick, torch.linspace(1.0, 2.0, top_k, device="cuda").expand(T, top_k))
+    Y, ids, w = gbr.moe_layer(*x, top_k=top_k, return_routing=True)
+    gbr.check_device()
+    ry, rids, rw = ref.moe(*x, top_k, "relu", False)
+    assert torch.equal(ids, rids) and ids.unique().numel() == chosen
+    assert (w.double() - rw).abs().max().item() <= 1e-5
+    close(Y, ry, TWO)
+
+
+def test_linear_mask_and_weights_past_32_bits(gbr):
+    """More than 2^31 outputs: the mask of every row against the generator's reference (its first 16 columns; the last
+    by the narrow and the whole call of dropout_add), and dB, whose contraction runs along those rows."""
+    M, K, N = 270336, 16, 8008
+    g = rng(77)
+    A, B = normal(g, (M, K)), normal(g, (K, N), K ** -0.5)
+    C = gbr.gemm_bias_act(A, B, act="none", p=0.25, seed=8, offset=3)
+    keep = ref.keep_mask(M, 16, 0.25, 8, 3, "cuda")[0]
+    assert (C[:, :16][~keep] == 0).all()
+    # A kept product that is exactly zero is rarer than 2^-16: 16 bf16 products would have to cancel to the bit.
+    assert ((C[:, :16] == 0) & keep).sum() <= keep.numel() * 2.0 ** -16
+    ones = gbr.dropout_add(torch.ones(M, N, device="cuda", dtype=BF), p=0.25, seed=8, offset=3)
+    assert torch.equal(ones[:, :16] != 0, keep)
+    dropped = ones == 0
+    assert (C[dropped] == 0).all()
+    del ones
+    dC = C
+    dA, dB, db = gbr.gemm_bias_act_backward(dC, A, B, p=0.25, seed=8, offset=3)
+    gbr.check_device()
+    want, sums, total, scale = 0.0, 0.0, 0.0, 65536 / 49152
+    for r in range(0, M, 16896):
+        rows = slice(r, r + 16896)
+        dz = dC[rows].double().masked_fill(dropped[rows], 0.0) * scale
+        close(dA[rows], dz @ B.double().t(), TWO)
+        want, sums, total = want + A[rows].double().t() @ dz, sums + dz.sum(0), total + dz.abs().sum(0)
+    close(dB, want, TWO)
+    assert ((db.double() - sums).abs() <= (2.0 ** -19 + M * 2.0 ** -24) * total).all()
