@@ -95,7 +95,7 @@ __device__ __forceinline__ F2 logistic2(F2 x) {
 
 // Phi(z), given e = exp(-z^2 / 2): formula 7.1.26 of Abramowitz and Stegun,
 // "Handbook of Mathematical Functions" (1964), erfc(x) ~ t (a1 + t (a2 + ...))
-// exp(-x^2) with t = 1 / (1 + 0.3275911 x), off by at most 1.5e-7, taken at
+// exp(-x^2) with t = 1 / (1 + 0.3275911 x), off by at most 1.5e-7 (absolute), taken at
 // x = |z| / sqrt(2) and halved.  One exponential serves Phi and the density,
 // and nothing cancels for z < 0.
 __device__ __forceinline__ F2 normal_cdf2(F2 z, F2 e) {

@@ -18,8 +18,9 @@
 // Bound: with few rows, the weights' bytes (each read once); several CTAs an
 // SM and a ring of 64-k stages keep the loads in flight.  The parts alias the
 // ring, which is idle by then.  Measured, calls back to back: one row of 4096 x
-// 4096 7.0 us (34 MB, kept in L2 from call to call), 37 rows of 4096 x 14336 22
-// (117 MB at 5.3 TB/s), 512 rows of 4096 x 4096 19.4, 301 x 520 x 1000 6.4.
+// 4096 7.4 us (34 MB, kept in L2 from call to call) or 9.8 (from HBM, 3.4 TB/s), 37
+// rows of 4096 x 14336 23 either way (117 MB at 5.1 TB/s), 512 rows of 4096 x 4096
+// 19.4, 301 x 520 x 1000 6.4.
 //
 // Shared-memory stage: 128 columns of the wide operand, 16 KiB (one K-major
 // box or two MN-major panels), then BT rows of the narrow one, BT x 128 bytes

@@ -26,10 +26,10 @@
 // moe_combine_kernel  adds the parts of each token's experts in order, times
 //     the router's weights.  No atomics: a result depends on the routing alone.
 //
-// Measured: that token 81 us, of which about 10 pass before the first weights
+// Measured: that token 80 us, of which about 10 pass before the first weights
 // arrive (the router, the tables, the first load) and 4 after the last, and 67
 // stream the 470 MB at 7.0 TB/s; 64 tokens on all 8 experts, 1.9 GB, 310 us;
-// 19 tokens through 6 of 64 gated experts of 2048 x 1000 141 us (rows of 4000
+// 19 tokens through 6 of 64 gated experts of 2048 x 1000 131 us (rows of 4000
 // bytes: HBM reads 812 MB for the 665 that are asked for).
 //
 // Roles of the expert kernel (192 threads):
