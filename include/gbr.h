@@ -479,7 +479,8 @@ int dropout_add(const void *X, int64_t ldx, const void *residual, int64_t ldr, v
  *   no output may overlap an input or the other output (GBR_ERR_INVALID).
  *   dtype GBR_BF16 (GBR_ERR_UNSUPPORTED for the others); act a gbr_act.
  *   fp32 accumulation and epilogue; C and Z are rounded once, from fp32.
- *   K == 0: Z = bias.  M, N, K < 2^31; any sizes and row strides.
+ *   K == 0: Z = bias.  M, N, K < 2^31; any sizes, and any row strides of at
+ *   least the columns.
  * gemm_bias_act_backward -- the gradients for dC = dLoss/dC, with the Z, p,
  * seed and offset of the forward call:
  *   dZ = drop(dC) * act'(Z);  dA = dZ B^T;  dB = A^T dZ;  dbias = column sums
