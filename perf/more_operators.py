@@ -127,6 +127,11 @@ def _choices(g, case):
     return ids.contiguous()
 
 
+def _two_to(exponent):
+    """2^exponent in 32 bits, exactly (exponents of normal numbers)."""
+    return ((exponent.int() + 127) << 23).view(torch.float32)
+
+
 def _weights_mxfp4(g, rows, cols, std):
     """Weights as a program that serves them in 4 bits keeps them: two values a byte, blocks of 32
     along the columns, and the blocks' exponents in tiles of 128 rows x 4 blocks."""
@@ -134,8 +139,8 @@ def _weights_mxfp4(g, rows, cols, std):
     w = torch.zeros((rows, blocks * 32), device="cuda")
     w[:, :cols] = torch.randn((rows, cols), generator=g, device="cuda").mul_(std)
     w = w.view(rows, blocks, 32)
-    exponent = (torch.frexp(w.abs().amax(2)).exponent - 3).clamp_(-127, 127)
-    w = torch.ldexp(w, -exponent[:, :, None])
+    exponent = (torch.frexp(w.abs().amax(2)).exponent - 3).clamp_(-126, 126)
+    w = w * _two_to(-exponent)[:, :, None]
     size = w.abs()
     code = sum((size > edge).to(torch.uint8) for edge in (0.25, 1.25, 2.5, 5.0))
     code += sum((size >= edge).to(torch.uint8) for edge in (0.75, 1.75, 3.5))
@@ -297,17 +302,17 @@ def _plain_mxfp4(s):
     a = torch.zeros((M, blocks * 32), device=s["A"].device)
     a[:, :K] = s["A"].float()
     a = a.view(M, blocks, 32)
-    exponent = (torch.frexp(a.abs().amax(2, keepdim=True)).exponent - 3).clamp(-127, 127)
-    v = torch.ldexp(a, -exponent).clamp(-6.0, 6.0)
+    exponent = (torch.frexp(a.abs().amax(2, keepdim=True)).exponent - 3).clamp(-126, 126)
+    v = (a * _two_to(-exponent)).clamp(-6.0, 6.0)
     step = torch.where(v.abs() < 2.0, 0.5, torch.where(v.abs() < 4.0, 1.0, 2.0))
-    a = torch.ldexp(torch.round(v / step) * step, exponent).view(M, -1)
+    a = (torch.round(v / step) * step * _two_to(exponent)).view(M, -1)
     # The weights' values.
     table = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], device=a.device)
     table = torch.cat([table, -table])
     w = torch.stack([table[(s["W"] & 15).long()], table[(s["W"] >> 4).long()]], 2)
     t = s["W_scales"].view(*s["W_scales"].shape[:2], 32, 4, 4).permute(0, 3, 2, 1, 4)
     t = t.reshape(t.shape[0] * 128, -1)[:w.shape[0], :blocks].int() - 127
-    w = torch.ldexp(w.view(w.shape[0], blocks, 32), t[..., None]).view(w.shape[0], -1)
+    w = (w.view(w.shape[0], blocks, 32) * _two_to(t)[..., None]).view(w.shape[0], -1)
     c = _act(a @ w.t() + s["bias"], s["act"])
     if s["R"] is not None:
         c = c + s["R"].float()
@@ -415,7 +420,8 @@ def _exact_mxfp4_values(x):
     pad = -K % 32
     b = torch.nn.functional.pad(x.double(), (0, pad)).unflatten(1, (-1, 32))
     top = b.abs().amax(2, keepdim=True)
-    scale = torch.exp2(torch.floor(torch.log2(torch.where(top > 0, top, 1.0))) - 2.0)
+    # The largest value's exponent, from the bits of the double.
+    scale = ((((top.view(torch.int64) >> 52) & 0x7FF) - 2).clamp(min=1) << 52).view(torch.float64)
     size = b.abs() / scale
     best, dist = torch.zeros_like(size), size.clone()
     for code, value in enumerate((0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0), 1):
