@@ -19,6 +19,12 @@
  *                           strides; gemm_bias_act_backward: its gradients
  *   dropout_add             Y = residual + dropout(X), the mask never stored
  *   moe_layer               router, experts and their sum for a few tokens
+ *   residual_norm           S = R + scale * gate * norm(X), H = norm(S);
+ *                           residual_norm_backward: its gradients
+ *   moe_sort, moe_dispatch, moe_combine, moe_combine_backward
+ *                           rows sorted by expert and back, any number of tokens
+ *   quantize_mxfp4, dequantize_mxfp4, gemm_mxfp4
+ *                           products of 4-bit blocks
  *
  * Conventions shared by every entry point
  *   - Tensors are contiguous, row-major, resident in device memory of the
@@ -520,6 +526,115 @@ int moe_layer(const void *X, const float *Wr, const void *W1, const float *b1, c
               gbr_stream_t stream);
 
 /*
+ * residual_norm -- what stands between two blocks of a transformer, in one pass:
+ *   y = norm(X) * post   (post NULL: y = X)
+ *   S = R + scale * gate * y
+ *   H = norm(S) * pre    (with pre)
+ * where norm divides a row by sqrt(mean of its squares + eps).
+ *   X, R, S, H [rows, cols], ld... elements from row to row, >= cols, any
+ *   alignment that the elements have; R may be NULL (zero).  post, pre [cols] fp32.  gate
+ *   [gates, cols] or NULL (one): rows must be a multiple of gates, and row i uses
+ *   gate row i / (rows / gates), so gates = 1 is a gate per channel and
+ *   gates = rows one per element.  S and H may be NULL (not wanted); H and pre go together.
+ *   dtype: GBR_BF16, or GBR_F32_FFMA (= GBR_F32_TF32 here), of X, R, gate, S and H.
+ *   All arithmetic is fp32; each output is rounded once, H from the sum before
+ *   its rounding to S.  S and H may each be X or R itself (same row stride); otherwise
+ *   no output overlaps anything (GBR_ERR_INVALID).
+ * residual_norm_backward -- gradients for dS and dH, with X, S (as the forward
+ * call wrote it), post, gate, scale, pre and eps:
+ *   ds = dS + gradient of norm(S) * pre for dH;  dR = ds;
+ *   dgate = scale * y * ds, summed over the rows that share a gate row;
+ *   dX = gradient of norm(X) * post for scale * gate * ds;  dpost, dpre: summed over all rows.
+ *   dS may be NULL with pre (zero); dH and S are needed with pre, X with post or gate.  dX, dR
+ *   [rows, cols], dgate [gates, cols], dpost, dpre [cols] fp32; each may be NULL (not
+ *   wanted).  Outputs overlap nothing.  Sums over rows are fp32, in an order that does
+ *   not change.  rows = 0 gives zero sums.
+ */
+int residual_norm(const void *X, int64_t ldx, const void *R, int64_t ldr, const float *post,
+                  const void *gate, int64_t ldg, int64_t gates, double scale, const float *pre,
+                  double eps, void *S, int64_t lds, void *H, int64_t ldh, int64_t rows,
+                  int64_t cols, int dtype, gbr_stream_t stream);
+int residual_norm_backward(const void *dS, int64_t ldds, const void *dH, int64_t lddh,
+                           const void *X, int64_t ldx, const void *S, int64_t lds,
+                           const float *post, const void *gate, int64_t ldg, int64_t gates,
+                           double scale, const float *pre, double eps, void *dX, int64_t lddx,
+                           void *dR, int64_t lddr, float *dpost, void *dgate, int64_t lddg,
+                           float *dpre, int64_t rows, int64_t cols, int dtype,
+                           gbr_stream_t stream);
+
+/*
+ * Rows sorted by expert, for the experts' products (gemm_bias_relu_grouped, or
+ * gemm_bias_act on each expert's rows), and back.  A choice is a (token, place)
+ * pair, top_k of them a token, in order of t * top_k + j.
+ *
+ * moe_sort -- positions[t, j] (int32): the row of the choice when rows are sorted
+ *   by expert, choices of one expert in their own order; -1 where expert_ids[t, j]
+ *   (int64) is outside [0, num_experts): a choice that is struck out, as for padding.
+ *   offsets [num_experts + 1] (int32): expert e has rows offsets[e] .. offsets[e + 1] - 1.
+ *   choices = T * top_k in [0, 2^31); num_experts 1..1024.
+ * moe_dispatch -- Xs[positions[t, j]] = X[t]; rows of Xs from offsets[num_experts]
+ *   on are zero.  X [T, D], Xs [T * top_k, D].  Its gradient is moe_combine without weights.
+ * moe_combine -- Y[t] = residual[t] + sum over j of weights[t, j] * Ys[positions[t, j]],
+ *   without choices that are struck out, whatever their weight; a token that has
+ *   none left gets its residual.  Ys [rows, D] (any number: positions outside are
+ *   taken for struck out), residual (or NULL), Y [T, D]; weights [T, top_k] fp32 or NULL
+ *   (one).  Y may be residual itself.  fp32 sums in the order of j, rounded once.
+ * moe_combine_backward -- dYs[positions[t, j]] = weights[t, j] * dY[t], zero rows as in
+ *   moe_dispatch; dweights[t, j] = <dY[t], Ys[positions[t, j]]> (fp32), 0 where struck out.
+ *   dYs or dweights may be NULL (not wanted; Ys may be NULL without dweights).
+ *   The residual's gradient is dY itself.
+ * Positions and offsets are those of moe_sort (a position twice would leave either
+ * row).  dtype as in residual_norm; D any, row strides >= D, any alignment that the
+ * elements have.  Outputs overlap nothing else.
+ */
+int moe_sort(const int64_t *expert_ids, int64_t choices, int num_experts, int32_t *positions,
+             int32_t *offsets, gbr_stream_t stream);
+int moe_dispatch(const void *X, int64_t ldx, const int32_t *positions, const int32_t *offsets,
+                 int num_experts, void *Xs, int64_t ldxs, int64_t T, int64_t top_k, int64_t D,
+                 int dtype, gbr_stream_t stream);
+int moe_combine(const void *Ys, int64_t ldys, int64_t rows, const int32_t *positions,
+                const float *weights, const void *residual, int64_t ldr, void *Y, int64_t ldy,
+                int64_t T, int64_t top_k, int64_t D, int dtype, gbr_stream_t stream);
+int moe_combine_backward(const void *dY, int64_t lddy, const void *Ys, int64_t ldys,
+                         const int32_t *positions, const int32_t *offsets, int num_experts,
+                         const float *weights, void *dYs, int64_t lddys, float *dweights,
+                         int64_t T, int64_t top_k, int64_t D, int dtype, gbr_stream_t stream);
+
+/*
+ * Microscaled 4-bit floating point (MXFP4): 32 neighbouring values of a row share a
+ * power of two.  A matrix of rows x cols is
+ *   data    mxfp4_data_bytes(rows, cols) = rows * 16 * ceil(cols / 32) bytes, row by row,
+ *           two values a byte, the lower column in the low bits: sign, two bits
+ *           of exponent, one of mantissa (0, 0.5, 1, 1.5, 2, 3, 4, 6); a last block
+ *           that the columns do not fill ends in zeros;
+ *   scales  mxfp4_scale_bytes(rows, cols) bytes: byte s stands for 2^(s - 127), 255
+ *           for NaN.  Tiles of 128 rows x 4 blocks, 512 bytes each, those of the same
+ *           rows one after the other; in a tile, row r and block b are byte
+ *           (r % 32) * 16 + (r % 128) / 32 * 4 + b % 4.  Bytes of rows and blocks that are not
+ *           there are 0 (gemm_mxfp4 wants no NaN in them).
+ * Both 16-byte aligned (GBR_ERR_ALIGN).
+ *
+ * quantize_mxfp4 -- the scale of a block is 2^(floor(log2 of its largest size) - 2),
+ *   at least 2^-127; values are divided by it and rounded to the nearest (ties to the
+ *   even mantissa, sizes above 6 to 6).  A block that holds Inf or NaN becomes NaN.
+ *   X: bf16 or fp32 [rows, cols], or with transposed = 1 [cols, rows] (weights stored
+ *   [K, N] give the rows of N that gemm_mxfp4 takes); any row stride.
+ * dequantize_mxfp4 -- the values, to bf16 or fp32 X [rows, cols]; exact (beyond fp32: Inf).
+ * gemm_mxfp4 -- C = residual + act(A * B^T + bias), A [M, K] and B [N, K] 4-bit,
+ *   C [M, N] and residual bf16, bias [N] fp32; bias and residual may be NULL, C may be
+ *   residual itself.  Products of the stored values, fp32 sums, rounded once.
+ */
+int64_t mxfp4_data_bytes(int64_t rows, int64_t cols);
+int64_t mxfp4_scale_bytes(int64_t rows, int64_t cols);
+int quantize_mxfp4(const void *X, int64_t ldx, void *data, void *scales, int64_t rows,
+                   int64_t cols, int transposed, int dtype, gbr_stream_t stream);
+int dequantize_mxfp4(const void *data, const void *scales, void *X, int64_t ldx, int64_t rows,
+                     int64_t cols, int dtype, gbr_stream_t stream);
+int gemm_mxfp4(const void *A, const void *A_scales, const void *B, const void *B_scales,
+               const float *bias, const void *residual, int64_t ldr, void *C, int64_t ldc,
+               int64_t M, int64_t N, int64_t K, int act, gbr_stream_t stream);
+
+/*
  * Failure-detection self tests of these operators' pipelines, as
  * gbr_selftest_gemm_skip_load: the normal call (contiguous operands, no
  * epilogue but the rounding; ReLU experts without biases) with the loads of
@@ -535,6 +650,9 @@ int gbr_selftest_moe_skip_load(const void *X, const float *Wr, const void *W1, c
                                void *Y, int64_t T, int64_t D, int64_t F, int num_experts,
                                int top_k, int cta, int item, uint64_t limit_ns,
                                gbr_stream_t stream);
+int gbr_selftest_mxfp4_skip_load(const void *A, const void *A_scales, const void *B,
+                                 const void *B_scales, void *C, int64_t M, int64_t N, int64_t K,
+                                 int cta, int item, uint64_t limit_ns, gbr_stream_t stream);
 
 #ifdef __cplusplus
 }

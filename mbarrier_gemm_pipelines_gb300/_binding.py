@@ -63,6 +63,21 @@ SIGNATURES = {
                                           _i32, _u64, _vp]),
     "moe_layer": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _i32,
                          _i32, _i32, _i32, _vp]),
+    "residual_norm": (_i32, [_vp, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _f64, _vp, _f64, _vp, _i64, _vp, _i64, _i64,
+                             _i64, _i32, _vp]),
+    "residual_norm_backward": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _f64, _vp, _f64,
+                                      _vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _i64, _i64, _i32, _vp]),
+    "moe_sort": (_i32, [_vp, _i64, _i32, _vp, _vp, _vp]),
+    "moe_dispatch": (_i32, [_vp, _i64, _vp, _vp, _i32, _vp, _i64, _i64, _i64, _i64, _i32, _vp]),
+    "moe_combine": (_i32, [_vp, _i64, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _i64, _i64, _i64, _i32, _vp]),
+    "moe_combine_backward": (_i32, [_vp, _i64, _vp, _i64, _vp, _vp, _i32, _vp, _vp, _i64, _vp, _i64, _i64, _i64, _i32,
+                                    _vp]),
+    "mxfp4_data_bytes": (_i64, [_i64, _i64]),
+    "mxfp4_scale_bytes": (_i64, [_i64, _i64]),
+    "quantize_mxfp4": (_i32, [_vp, _i64, _vp, _vp, _i64, _i64, _i32, _i32, _vp]),
+    "dequantize_mxfp4": (_i32, [_vp, _vp, _vp, _i64, _i64, _i64, _i32, _vp]),
+    "gemm_mxfp4": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _i64, _i64, _i64, _i32, _vp]),
+    "gbr_selftest_mxfp4_skip_load": (_i32, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _i32, _u64, _vp]),
 }
 
 _lib = None

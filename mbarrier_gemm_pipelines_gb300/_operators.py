@@ -20,6 +20,7 @@ from __future__ import annotations
 import importlib.machinery
 import importlib.util
 import os
+from typing import NamedTuple
 
 from . import _build
 from ._binding import GbrError, _cuda_tensor, _outputs_on, _stream_ptr, check, lib
@@ -81,6 +82,98 @@ def moe_layer(X, Wr, W1, b1, W2, b2, top_k=2, act="relu", gated=False, Y=None, r
     and b2 may be None).  Returns Y [T, D] bf16, or (Y, expert_ids int64
     [T, top_k], expert_weights fp32 [T, top_k])."""
     return (_ext or _load()).moe_layer(X, Wr, W1, b1, W2, b2, top_k, act, gated, Y, return_routing, stream)
+
+
+def residual_norm(X, R=None, post=None, gate=None, scale=1.0, pre=None, eps=1e-6, S=None, H=None, stream=None):
+    """What stands between two blocks: S = R + scale * gate * norm(X) * post and
+    H = norm(S) * pre, norm dividing each row by sqrt(mean square + eps).
+    X (the block's output), R (the residual stream; None: zero) [rows, cols] bf16
+    or fp32; post, pre [cols] fp32 and gate [gates, cols] of X's type may be None.
+    gate row i * gates // rows goes with row i: one row is a gate per channel,
+    as many as X has one per element.  Returns (S, H), H None without pre."""
+    return (_ext or _load()).residual_norm(X, R, post, gate, scale, pre, eps, S, H, stream)
+
+
+def residual_norm_backward(dS, dH, X, S, post=None, gate=None, scale=1.0, pre=None, eps=1e-6, dX=None, dR=None,
+                           dpost=None, dgate=None, dpre=None, needs=(True, True, True, True, True), stream=None):
+    """Gradients (dX, dR, dpost, dgate, dpre) of residual_norm for dS and dH, with the
+    X, post, gate, scale, pre and eps of the forward call and the S it returned.  dS may be
+    None with pre (zero), dH and S without it, X without post and gate.  `needs`
+    says which are wanted; None is returned for the others and for what the forward call did without."""
+    return (_ext or _load()).residual_norm_backward(dS, dH, X, S, post, gate, scale, pre, eps, dX, dR, dpost, dgate,
+                                                    dpre, needs, stream)
+
+
+def moe_sort(expert_ids, num_experts, positions=None, offsets=None, stream=None):
+    """Where each choice's row goes when rows are sorted by expert: expert_ids int64
+    [T, top_k] -> (positions int32 [T, top_k], offsets int32 [num_experts + 1]).
+    Choices of an expert keep their order; an id outside [0, num_experts) is
+    struck out (position -1).  Expert e has rows offsets[e] .. offsets[e + 1] - 1."""
+    return (_ext or _load()).moe_sort(expert_ids, num_experts, positions, offsets, stream)
+
+
+def moe_dispatch(X, positions, offsets, Xs=None, stream=None):
+    """Rows in the experts' order: Xs[positions[t, j]] = X[t]; rows of Xs [T * top_k, D] from
+    offsets[-1] on are zero.  X [T, D] bf16 or fp32.  The gradient of X is
+    ``moe_combine(dXs, positions)``."""
+    return (_ext or _load()).moe_dispatch(X, positions, offsets, Xs, stream)
+
+
+def moe_combine(Ys, positions, weights=None, residual=None, Y=None, stream=None):
+    """Back to the tokens: Y[t] = residual[t] + sum over j of weights[t, j] *
+    Ys[positions[t, j]]; struck-out choices count nothing.  Ys [rows, D] bf16 or
+    fp32, weights fp32 [T, top_k] (None: one), residual [T, D] (None: zero)."""
+    return (_ext or _load()).moe_combine(Ys, positions, weights, residual, Y, stream)
+
+
+def moe_combine_backward(dY, Ys, positions, offsets, weights, dYs=None, dweights=None, needs=(True, True), stream=None):
+    """Gradients (dYs, dweights) of moe_combine for dY: dYs[positions[t, j]] =
+    weights[t, j] * dY[t] (zero from offsets[-1] on), dweights[t, j] = <dY[t],
+    Ys[positions[t, j]]> in fp32, 0 for struck-out choices.  The residual's gradient is
+    dY itself.  `needs` says which are wanted (Ys may be None without dweights)."""
+    return (_ext or _load()).moe_combine_backward(dY, Ys, positions, offsets, weights, dYs, dweights, needs, stream)
+
+
+class Mxfp4(NamedTuple):
+    """A matrix in microscaled 4-bit floating point: blocks of 32 values along
+    the columns (layout: gbr.h)."""
+    data: "torch.Tensor"            # uint8 [rows, 16 * ceil(columns / 32)]
+    scales: "torch.Tensor"          # uint8 [ceil(rows / 128), ceil(columns / 128), 512]
+    columns: int
+
+
+def quantize_mxfp4(X, transposed=False, out=None, stream=None):
+    """X [rows, columns] (bf16 or fp32) in 4 bits: each block's scale is
+    2^(floor(log2 of its largest size) - 2), its values are rounded to the nearest of
+    0, 0.5, 1, 1.5, 2, 3, 4, 6 times that.  With `transposed` X is [columns, rows]:
+    weights stored [K, N] give what gemm_mxfp4 takes as B.  `out`: an Mxfp4 to write."""
+    data, scales = (None, None) if out is None else (out.data, out.scales)
+    columns, data, scales = (_ext or _load()).quantize_mxfp4(X, transposed, data, scales, stream)
+    return Mxfp4(data, scales, columns) if out is None or out.columns != columns else out
+
+
+def dequantize_mxfp4(Q, dtype=None, X=None, stream=None):
+    """The values of an Mxfp4, as `dtype` (torch.bfloat16 unless given; or torch.float32)."""
+    return (_ext or _load()).dequantize_mxfp4(Q.data, Q.scales, Q.columns, dtype, X, stream)
+
+
+def gemm_mxfp4(A, B, bias=None, residual=None, act="none", C=None, stream=None):
+    """C = residual + act(A @ B.T + bias) of two Mxfp4, A [M, K] and B [N, K]; C and
+    residual [M, N] bf16, bias [N] fp32."""
+    return (_ext or _load()).gemm_mxfp4(A.data, A.scales, A.columns, B.data, B.scales, B.columns, bias, residual, act, C,
+                                        stream)
+
+
+def selftest_mxfp4_skip_load(A, B, cta, item, limit_ns, stream=None):
+    """Runs gemm_mxfp4 (A @ B.T alone) with one stage left unfilled, as
+    selftest_linear_skip_load; returns the undefined output."""
+    import torch
+    with _outputs_on(stream):
+        C = torch.empty((A.data.shape[0], B.data.shape[0]), dtype=torch.bfloat16, device=A.data.device)
+    tensors = [_cuda_tensor(t, "operand", (torch.uint8,)) for t in (A.data, A.scales, B.data, B.scales)]
+    check(lib().gbr_selftest_mxfp4_skip_load(*(t.data_ptr() for t in tensors), C.data_ptr(), C.shape[0], C.shape[1],
+                                             A.columns, cta, item, limit_ns, _stream_ptr(stream)))
+    return C
 
 
 def selftest_linear_skip_load(A, B, cta, item, limit_ns, stream=None):

@@ -274,6 +274,7 @@ int run_pair(const Product& p, const LibCtx& c, cudaStream_t stream) {
 struct TilePlan {
     int32_t bt, split, stages;
     double cycles;                 // estimate, see below
+    int64_t budget;                // of shared memory
 };
 
 // Estimated SM cycles of the product on either kernel, for the choice between
@@ -315,7 +316,7 @@ int tile_stages(int bt, int64_t budget) {
 int64_t tile_fit(int cluster, int sms) { return cluster == 8 ? sms * 15 / 19 : cluster == 4 ? sms * 18 / 19 : sms; }
 
 TilePlan plan_tile(const Product& p, int sms) {
-    TilePlan best = {0, 0, 0, 1e30};
+    TilePlan best = {0, 0, 0, 1e30, 0};
     double finish = 0.0;
     const int64_t nks = cdiv(p.Kc, 64);
     const double hbm = double(p.Kc) * double(p.J) * 2.0 / 3500.0;
@@ -351,7 +352,7 @@ TilePlan plan_tile(const Product& p, int sms) {
             const double parts = double(n) * rows * 512.0 * (double(s - 1) / s / 12.0 + 1.0 / 64.0);
             const double cycles = 6000.0 + std::max(feed, hbm * busy) + parts + 60.0 * (s - 1) +
                                   3000.0 * double(rounds - 1);      // the cluster's barriers; rounds
-            if (cycles < best.cycles) best = {bt, s, stages, cycles}, finish = double(n) * rows * 28.0 / s;
+            if (cycles < best.cycles) best = {bt, s, stages, cycles, budget}, finish = double(n) * rows * 28.0 / s;
         }
     }
     best.cycles += finish;
@@ -595,6 +596,14 @@ void* dz_kernel_ptr(int act) {
 }
 
 }  // namespace
+
+LinearPlan plan_linear(int32_t rows, int32_t cols, int32_t contraction, int sms) {
+    Product p = {};
+    p.b_mn = true;
+    p.I = rows, p.J = cols, p.Kc = contraction;
+    const TilePlan t = plan_tile(p, sms);
+    return {t.cycles >= pair_cycles(p, sms), t.bt, t.split, t.budget};
+}
 
 int launch_linear(const LinearArgs& a, const LibCtx& c, cudaStream_t stream) {
     Product p = {};

@@ -1,0 +1,229 @@
+// mxfp4_tile.cuh -- C = R + act(A B^T + bias) from microscaled 4-bit operands
+// where the output has too few 256 x 256 tiles to fill the GPU: down to one row.
+//
+// The layout of linear_tile.cuh: 128 output COLUMNS are the MMA's M, so that the
+// weights stream through the tensor core as its wide operand, BT output ROWS its
+// N; a cluster of 1, 2, 4 or 8 CTAs shares a tile along K and adds its fp32
+// parts in rank order over distributed shared memory.  A 128-byte slice of a row
+// is 256 values here, so bytes, ring and MMAs are those of a bf16 product with a
+// quarter of the contraction, and the choice of tile and split is the same.
+//
+// Stage: 128 columns of B (16 KiB), BT rows of A (BT x 128 bytes), the scales of
+// both (1 KiB for 128 rows and 8 blocks).  The MMA's thread copies the scales to
+// Tensor Memory in front of the stage's MMAs; the tensor core runs both in
+// order.  Two sets of columns alternate, so that a copy need not wait for the
+// MMAs before it.
+#pragma once
+#include "linear_tile.cuh"
+#include "mxfp4.cuh"
+
+namespace gbr {
+namespace mx {
+
+using linear::kTileBarBytes;
+using linear::kTileMaxStages;
+using linear::kTileThreads;
+using linear::kWideBytes;
+
+constexpr uint32_t kScaleBytes = 2 * kMxTileBytes;     // 128 rows, one stage
+constexpr int32_t kSliceK = 256;                       // values of a stage
+
+struct TileParams {
+    linear::TileParams t;                              // maps, epilogue, split; num_ks: stages' worth of K
+    CUtensorMap mapWs, mapXs;                          // scales
+    int32_t blocks;
+};
+
+// Row tiles of 128 whose scales a tile of BT rows needs.
+__host__ __device__ constexpr uint32_t tile_row_tiles(int32_t bt) { return bt > 128 ? 2u : 1u; }
+__host__ __device__ constexpr uint32_t tile_stage_bytes(int32_t bt) {
+    return kWideBytes + uint32_t(bt) * 128u + kScaleBytes * (1u + tile_row_tiles(bt));
+}
+// Tensor Memory: the accumulator, then two sets of scales (8 columns for B, 8 or 16 for A).
+__host__ __device__ constexpr uint32_t tile_scale_col(int32_t bt) { return bt < 32 ? 32u : (uint32_t(bt) + 31u) / 32u * 32u; }
+__host__ __device__ constexpr uint32_t tile_tmem_cols(int32_t bt) {
+    const uint32_t need = tile_scale_col(bt) + 2u * 8u * (1u + tile_row_tiles(bt));
+    return need <= 64u ? 64u : need <= 128u ? 128u : need <= 256u ? 256u : 512u;
+}
+// As for linear_tile.cuh never below 108 KiB; tiles that take all of Tensor
+// Memory never share an SM with another that waits for some.
+__host__ __device__ constexpr size_t tile_smem_bytes(int32_t bt, int32_t stages) {
+    const size_t ring = size_t(stages) * tile_stage_bytes(bt), part = size_t(bt) * 512u;
+    const size_t need = 1024 + kTileBarBytes + 1024 + (ring > part ? ring : part);
+    const size_t least = tile_tmem_cols(bt) > 256u ? 124 * 1024 : 108 * 1024;
+    return need > least ? need : least;
+}
+
+// 512 bytes of scales in shared memory: 32 rows of 16 bytes, groups of 8 rows 128 bytes apart, no swizzle.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) {
+    return uint64_t((saddr >> 4) & 0x3FFFu) | (uint64_t(128u >> 4) << 32) | (uint64_t(1) << 46);
+}
+// fp32 += e2m1 x e2m1 with E8M0 scales; `m` and `n` the MMA's shape, `pair` (0 or 1) which two of four scale bytes.
+__host__ __device__ constexpr uint32_t mx_idesc(uint32_t m, uint32_t n, uint32_t pair) {
+    return (pair * 2u << 4) | (1u << 7) | (1u << 10) | ((n >> 3) << 17) | (1u << 23) | ((m >> 4) << 24) |
+           (pair * 2u << 29);
+}
+
+template <int ACT>
+__global__ void __launch_bounds__(kTileThreads) mxfp4_tile_kernel(const __grid_constant__ TileParams Q) {
+    extern __shared__ uint8_t smem_raw[];
+    const linear::TileParams& P = Q.t;
+    uint64_t* full = reinterpret_cast<uint64_t*>(align_1024(smem_raw));
+    uint64_t* empty = full + kTileMaxStages;
+    uint64_t* acc_full = empty + kTileMaxStages;
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(acc_full + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+    uint8_t* ring = align_1024(reinterpret_cast<uint8_t*>(full) + kTileBarBytes);
+
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u;
+    const uint32_t S = uint32_t(P.split), stages = uint32_t(P.stages);
+    const uint32_t tile = blockIdx.x / S, rank = blockIdx.x % S;
+    const int32_t i0 = int32_t(tile % uint32_t(P.t_tiles)) * P.bt, j0 = int32_t(tile / uint32_t(P.t_tiles)) * 128;
+    const int32_t ks0 = int32_t(int64_t(P.num_ks) * rank / S), ks1 = int32_t(int64_t(P.num_ks) * (rank + 1) / S);
+    const uint32_t stage_bytes = tile_stage_bytes(P.bt), row_tiles = tile_row_tiles(P.bt);
+    const uint32_t tmem_cols = tile_tmem_cols(P.bt);
+
+    if (threadIdx.x == 0) {
+        for (uint32_t i = 0; i < stages; ++i) {
+            ptx::mbar_init(ptx::smem_addr(full + i), 1);
+            ptx::mbar_init(ptx::smem_addr(empty + i), 1);
+        }
+        ptx::mbar_init(ptx::smem_addr(acc_full), 1);
+        *abort_flag = 0;
+        ptx::fence_barrier_init();
+    } else if (threadIdx.x == 128 && P.num_ks > 0) {
+        ptx::prefetch_tensormap(&P.mapW);
+        ptx::prefetch_tensormap(&P.mapX);
+        ptx::prefetch_tensormap(&Q.mapWs);
+        ptx::prefetch_tensormap(&Q.mapXs);
+    }
+    if (warp == 5) {
+        ptx::tmem_alloc(ptx::smem_addr(tmem_holder), tmem_cols);
+        ptx::tmem_relinquish_alloc_permit();
+    }
+    ptx::tc_fence_before_sync();
+    __syncthreads();
+    ptx::tc_fence_after_sync();
+    const uint32_t tmem = *tmem_holder;
+    const uint32_t ring_base = ptx::smem_addr(ring);
+    ptx::griddep_wait();
+
+    uint32_t issued = 0;
+    if (warp == 4 && lane == 0) {
+        uint32_t slot = 0, ph = 0;
+        for (int32_t ks = ks0; ks < ks1; ++ks, ++issued) {
+            if (!mbar_wait(ptx::smem_addr(empty + slot), ph ^ 1u, P.ctl, abort_flag, kSiteProducerEmpty, issued))
+                break;
+            const uint32_t bar = ptx::smem_addr(full + slot), dst = ring_base + slot * stage_bytes;
+            const uint32_t scales = dst + kWideBytes + uint32_t(P.bt) * 128u;
+            ptx::mbar_arrive_expect_tx(bar, stage_bytes);
+            if (!inject_skip(P.inject, issued)) {       // self test: the stage's loads are left out
+                ptx::tma_load_2d(dst, &P.mapW, bar, ks * 128, j0);
+                ptx::tma_load_2d(dst + kWideBytes, &P.mapX, bar, ks * 128, i0);
+                ptx::tma_load_2d(scales, &Q.mapWs, bar, ks * 256, j0 / 128);
+                ptx::tma_load_2d(scales + kScaleBytes, &Q.mapXs, bar, ks * 256, i0 / 128);
+            }
+            if (++slot == stages) {
+                slot = 0;
+                ph ^= 1u;
+            }
+        }
+        ptx::griddep_launch_dependents();
+    } else if (warp == 5 && lane == 0) {
+        const uint32_t idesc0 = mx_idesc(128, uint32_t(P.bt), 0), idesc1 = mx_idesc(128, uint32_t(P.bt), 1);
+        const uint32_t sf = tmem + tile_scale_col(P.bt);
+        const uint32_t x_col = uint32_t(i0 % 128) / 32u;   // a tile may start inside 128 rows, at a multiple of 32
+        uint32_t slot = 0, ph = 0, it = 0;
+        for (int32_t ks = ks0; ks < ks1; ++ks, ++it) {
+            if (!mbar_wait(ptx::smem_addr(full + slot), ph, P.ctl, abort_flag, kSiteMmaFull, it)) break;
+            ptx::tc_fence_after_sync();
+            const uint32_t w = ring_base + slot * stage_bytes, x = w + kWideBytes, scales = x + uint32_t(P.bt) * 128u;
+            const uint32_t sfw = sf + (it & 1u) * 8u * (1u + row_tiles), sfx = sfw + 8u;
+            // Pairs of blocks that the matrix has.
+            const int32_t steps = min(4, (Q.blocks - ks * 8 + 1) / 2);
+            for (uint32_t h = 0; h < 2; ++h) {
+                ptx::tmem_copy_32x128b(sfw + h * 4u, scale_desc(scales + h * kMxTileBytes));
+                for (uint32_t r = 0; r < row_tiles; ++r)
+                    ptx::tmem_copy_32x128b(sfx + (h * row_tiles + r) * 4u,
+                                           scale_desc(scales + kScaleBytes * (1u + r) + h * kMxTileBytes));
+            }
+            for (int32_t k = 0; k < steps; ++k) {
+                const uint32_t h = uint32_t(k) / 2u;
+                ptx::mma_mxf4(tmem, umma::sw128_desc(w + uint32_t(k) * 32u, 16, 1024),
+                              umma::sw128_desc(x + uint32_t(k) * 32u, 16, 1024), k % 2 ? idesc1 : idesc0, sfw + h * 4u,
+                              sfx + h * row_tiles * 4u + x_col, it != 0 || k != 0 ? 1u : 0u);
+            }
+            ptx::mma_commit(ptx::smem_addr(empty + slot));
+            if (++slot == stages) {
+                slot = 0;
+                ph ^= 1u;
+            }
+        }
+        // Completes when every MMA issued has: also what the exit path waits for.
+        ptx::mma_commit(ptx::smem_addr(acc_full));
+    }
+    __syncwarp();
+
+    // All MMAs of this CTA are done: their operands' memory may be reused.
+    const bool done = mbar_wait_warp(ptx::smem_addr(acc_full), 0, P.ctl, abort_flag, kSiteEpiAccFull, 0);
+    ptx::tc_fence_after_sync();
+    const int32_t rows = min(P.bt, P.I - i0);
+    if (warp < 4 && done) {
+        // Part of the tile: [row][128 columns] fp32.
+        float* part = reinterpret_cast<float*>(ring) + warp * 32u + lane;
+        for (int32_t c = 0; c < rows; c += 16) {
+            uint32_t r[16];
+            ptx::tmem_ld_32x32b_x16(tmem + ((warp * 32u) << 16) + uint32_t(c), r);
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) part[(c + e) * 128] = ks1 > ks0 ? __uint_as_float(r[e]) : 0.f;
+        }
+    }
+    ptx::tc_fence_before_sync();
+    __syncwarp();
+    if (S > 1)
+        ptx::cluster_sync_all();
+    else
+        __syncthreads();
+    // After an abort loads may still be in flight; no part is complete then.
+    if (*abort_flag) {
+        if (warp == 5 && lane == 0) mbar_wait_drain(ptx::smem_addr(acc_full), 0, P.ctl.timeout_ns);
+        if (warp == 4 && lane == 0)
+            umma::drain_ring<1>(full, stages, issued, 0, stage_bytes, P.inject, blockIdx.x, P.ctl.timeout_ns);
+    } else {
+        for (int32_t u = int32_t(rank * kTileThreads + threadIdx.x); u < rows * 16; u += int32_t(S * kTileThreads)) {
+            const int32_t t = u >> 4, j = j0 + (u & 15) * 8;
+            if (j >= P.J) continue;
+            const uint32_t at = ring_base + uint32_t(t) * 512u + uint32_t(u & 15) * 32u;
+            // Every part's load is under way before the first is added.
+            float4 a[8], b[8];
+#pragma unroll
+            for (uint32_t s = 0; s < 8; ++s)
+                if (s < S) {
+                    const uint32_t from = ptx::mapa_shared(at, s);
+                    a[s] = ptx::ld_shared_cluster_v4_f32(from);
+                    b[s] = ptx::ld_shared_cluster_v4_f32(from + 16);
+                }
+            float v[8] = {};
+#pragma unroll
+            for (uint32_t s = 0; s < 8; ++s)
+                if (s < S) {
+                    v[0] += a[s].x, v[1] += a[s].y, v[2] += a[s].z, v[3] += a[s].w;
+                    v[4] += b[s].x, v[5] += b[s].y, v[6] += b[s].z, v[7] += b[s].w;
+                }
+            linear::finish8<ACT, false>(P, i0 + t, j, v);
+        }
+    }
+    __syncwarp();
+    if (S > 1)
+        ptx::cluster_sync_all();   // no CTA leaves while a peer may read its part
+    else
+        __syncthreads();
+    if (warp == 5) {
+        ptx::tc_fence_after_sync();
+        ptx::tmem_dealloc(tmem, tmem_cols);
+    }
+}
+
+}  // namespace mx
+}  // namespace gbr

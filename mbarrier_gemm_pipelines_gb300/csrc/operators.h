@@ -64,6 +64,15 @@ struct LinearArgs {
 };
 int launch_linear(const LinearArgs& a, const LibCtx& c, cudaStream_t stream);
 
+// Which kernel a bf16 product [rows, contraction] x [contraction, cols] runs on:
+// CTA pairs, or single tiles of bt rows, `split` CTAs each, rings within `budget` bytes.
+struct LinearPlan {
+    bool pair;
+    int32_t bt, split;
+    int64_t budget;
+};
+LinearPlan plan_linear(int32_t rows, int32_t cols, int32_t contraction, int sms);
+
 // dZ = drop(dC) * act'(Z) (bf16) and dbias = sum over rows of dZ (fp32).
 struct LinearGradArgs {
     Mat dC, Z, dZ;                 // Z: unless act is none; dZ optional (not wanted)
@@ -98,5 +107,86 @@ struct MoeArgs {
 };
 size_t moe_scratch_bytes(const MoeArgs& a, const LibCtx& c);
 int launch_moe(const MoeArgs& a, void* scratch, const LibCtx& c, cudaStream_t stream);
+
+// ------------------------------------------------------------ residual_norm
+// y = norm(X) post;  S = R + scale G y;  H = norm(S) pre.  Rows of G are shared
+// by per_gate rows each; gates = rows / per_gate, or 0 without G.
+struct ResidualNormArgs {
+    Mat X, R, G, S, H;             // R, G, S and H optional
+    const float *post, *pre;       // optional; pre with H
+    int32_t rows, cols, gates, per_gate;
+    float scale, eps;
+    bool bf16;                     // else fp32
+};
+int launch_residual_norm(const ResidualNormArgs& a, const LibCtx& c, cudaStream_t stream);
+
+struct ResidualNormGradArgs {
+    Mat dS, dH, X, S, G;           // dS optional; dH and S with pre; X unless there is neither post nor G
+    const float *post, *pre;
+    Mat dX, dR, dG;                // each optional (not wanted)
+    float *dpost, *dpre;           // the same
+    int32_t rows, cols, gates, per_gate;
+    float scale, eps;
+    bool bf16;
+};
+int launch_residual_norm_grad(const ResidualNormGradArgs& a, const LibCtx& c, cudaStream_t stream);
+
+// ------------------------------------------------------------ rows by expert
+constexpr int kSortMaxExperts = 1024;
+struct MoeSortArgs {
+    const int64_t* ids;            // [n]
+    int32_t *positions, *offsets;  // [n], [experts + 1]
+    int32_t n, experts;
+};
+int launch_moe_sort(const MoeSortArgs& a, const LibCtx& c, cudaStream_t stream);
+
+// Rows of tokens [T, D] and of choices [T * k, D]; positions say where a choice's row is.
+struct MoeRowsArgs {
+    Mat X, Ys, R, Y;               // dispatch: X -> Ys; combine: Ys (and R) -> Y
+    const int32_t *positions, *offsets;
+    const float* weights;          // optional
+    int32_t T, k, D, experts;
+    bool bf16;
+};
+int launch_moe_dispatch(const MoeRowsArgs& a, const LibCtx& c, cudaStream_t stream);
+int launch_moe_combine(const MoeRowsArgs& a, int64_t rows, const LibCtx& c, cudaStream_t stream);
+
+struct MoeCombineGradArgs {
+    Mat dY, Ys, dYs;               // Ys with dweights; dYs optional
+    const int32_t *positions, *offsets;
+    const float* weights;
+    float* dweights;               // optional
+    int32_t T, k, D, experts;
+    bool bf16;
+};
+int launch_moe_combine_grad(const MoeCombineGradArgs& a, const LibCtx& c, cudaStream_t stream);
+
+// ------------------------------------------------------------ 4-bit products
+// Blocks of 32 along the columns: data [rows, 16 * blocks] bytes, scales in
+// tiles of 128 rows x 4 blocks, 512 bytes each.
+struct Mxfp4Quantize {
+    Mat X;                         // [rows, cols], or [cols, rows] where transposed
+    uint8_t *data, *scales;
+    int32_t rows, cols;
+    bool bf16, transposed;
+};
+int launch_mxfp4_quantize(const Mxfp4Quantize& a, const LibCtx& c, cudaStream_t stream);
+struct Mxfp4Dequantize {
+    const uint8_t *data, *scales;
+    Mat X;
+    int32_t rows, cols;
+    bool bf16;
+};
+int launch_mxfp4_dequantize(const Mxfp4Dequantize& a, const LibCtx& c, cudaStream_t stream);
+
+// C = R + act(A B^T + bias).
+struct Mxfp4Args {
+    const uint8_t *A, *As, *B, *Bs;
+    const float* bias;             // optional
+    Mat R, C;                      // R optional
+    int32_t M, N, blocks;
+    int act;
+};
+int launch_mxfp4(const Mxfp4Args& a, const LibCtx& c, cudaStream_t stream);
 
 }  // namespace gbr

@@ -13,6 +13,7 @@
 #include <ATen/ATen.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <algorithm>
@@ -413,6 +414,349 @@ PyObject* moe_layer_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// bf16 or fp32.
+at::ScalarType element_type(const at::Tensor& t, const char* name) {
+    const at::ScalarType type = t.scalar_type();
+    if (type != at::kBFloat16 && type != at::kFloat)
+        refuse(PyExc_TypeError, "%s must be bf16 or fp32, got %s", name, c10::toString(type));
+    return type;
+}
+int type_code(at::ScalarType type) { return type == at::kBFloat16 ? GBR_BF16 : GBR_F32_FFMA; }
+
+const float* optional_vector(PyObject* o, const char* name, int dev, int64_t n) {
+    return o == Py_None ? nullptr : static_cast<const float*>(packed(tensor(o, name), name, at::kFloat, dev, {n}));
+}
+
+// The `count` truth values of `needs`.
+void truths(PyObject* o, bool* want, int count) {
+    PyObject* needs = PySequence_Fast(o, "needs must be a sequence of truth values");
+    if (needs == nullptr) throw Refused();
+    const bool fits = PySequence_Fast_GET_SIZE(needs) == count;
+    int bad = 0;
+    for (int i = 0; fits && i < count; ++i) {
+        const int v = PyObject_IsTrue(PySequence_Fast_GET_ITEM(needs, i));
+        bad |= v < 0;
+        want[i] = v > 0;
+    }
+    Py_DECREF(needs);
+    if (bad) throw Refused();
+    if (!fits) refuse(PyExc_ValueError, "needs must be %d truth values", count);
+}
+
+// A contiguous output: the caller's, or a new one.
+Out out_packed(PyObject* o, const char* name, const at::Tensor& like, at::ScalarType type, int dev, at::IntArrayRef shape) {
+    Out r;
+    if (o != Py_None) {
+        r.given = o;
+        r.m.p = packed(tensor(o, name), name, type, dev, shape);
+    } else {
+        r.made = at::empty(shape, like.options().dtype(type));
+        r.m.p = r.made.data_ptr();
+    }
+    return r;
+}
+
+PyObject* wrap_or_none(bool want, const Out& o) { return want ? o.wrap() : Py_NewRef(Py_None); }
+
+// residual_norm(X, R, post, gate, scale, pre, eps, S, H, stream)
+PyObject* residual_norm_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 10, [&]() -> PyObject* {
+        const at::Tensor& tX = tensor(a[0], "X");
+        const at::ScalarType type = element_type(tX, "X");
+        const int dev = first_device(tX, "X");
+        const Mat X = mat(tX, "X", type, dev);
+        Mat R, G;
+        if (a[1] != Py_None) R = mat_of(a[1], "R", type, dev, X.rows, X.cols);
+        const float* post = optional_vector(a[2], "post", dev, X.cols);
+        if (a[3] != Py_None) {
+            G = mat(tensor(a[3], "gate"), "gate", type, dev);
+            if (G.cols != X.cols)
+                refuse(PyExc_ValueError, "gate must have %lld columns, got %lld", static_cast<long long>(X.cols),
+                       static_cast<long long>(G.cols));
+            if (G.rows == 0 ? X.rows != 0 : X.rows % G.rows != 0)
+                refuse(PyExc_ValueError, "the %lld rows of X are no multiple of gate's %lld",
+                       static_cast<long long>(X.rows), static_cast<long long>(G.rows));
+        }
+        const double scale = number(a[4]), eps = number(a[6]);
+        const float* pre = optional_vector(a[5], "pre", dev, X.cols);
+        const bool want_h = a[5] != Py_None;
+        if (!want_h && a[8] != Py_None) refuse(PyExc_ValueError, "H needs pre");
+        const CallStream st(a[9], dev);
+        const Out S = out_mat(a[7], "S", tX, dev, X.rows, X.cols);
+        Out H;
+        if (want_h) H = out_mat(a[8], "H", tX, dev, X.rows, X.cols);
+        // Vectors of no columns have no address.
+        if (X.cols > 0)
+            call([&] {
+                return residual_norm(X.p, X.ld, R.p, R.ld, post, G.p, G.ld, G.rows, scale, pre, eps, S.m.p, S.m.ld, H.m.p,
+                                     H.m.ld, X.rows, X.cols, type_code(type), st);
+            });
+        return Py_BuildValue("NN", S.wrap(), wrap_or_none(want_h, H));
+    });
+}
+
+// residual_norm_backward(dS, dH, X, S, post, gate, scale, pre, eps, dX, dR, dpost, dgate, dpre, needs, stream)
+PyObject* residual_norm_backward_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 16, [&]() -> PyObject* {
+        const bool has_post = a[4] != Py_None, has_gate = a[5] != Py_None, has_pre = a[7] != Py_None;
+        if (a[0] == Py_None && !has_pre) refuse(PyExc_ValueError, "dS is needed without pre");
+        const int first = a[0] != Py_None ? 0 : 1;
+        const char* first_name = first == 0 ? "dS" : "dH";
+        const at::Tensor& like = tensor(a[first], first_name);
+        const at::ScalarType type = element_type(like, first_name);
+        const int dev = first_device(like, first_name);
+        const Mat m = mat(like, first_name, type, dev);
+        const int64_t rows = m.rows, cols = m.cols;
+        Mat dS, dH, X, S, G;
+        if (a[0] != Py_None) dS = m;
+        if (has_pre) {
+            if (a[1] == Py_None || a[3] == Py_None) refuse(PyExc_ValueError, "dH and S are needed with pre");
+            dH = mat_of(a[1], "dH", type, dev, rows, cols);
+            S = mat_of(a[3], "S", type, dev, rows, cols);
+        }
+        if (has_post || has_gate) {
+            if (a[2] == Py_None) refuse(PyExc_ValueError, "X is needed with post or gate");
+            X = mat_of(a[2], "X", type, dev, rows, cols);
+        }
+        const float* post = optional_vector(a[4], "post", dev, cols);
+        if (has_gate) {
+            G = mat(tensor(a[5], "gate"), "gate", type, dev);
+            if (G.cols != cols || (G.rows == 0 ? rows != 0 : rows % G.rows != 0))
+                refuse(PyExc_ValueError, "gate must have %lld columns and rows that divide %lld",
+                       static_cast<long long>(cols), static_cast<long long>(rows));
+        }
+        const double scale = number(a[6]), eps = number(a[8]);
+        const float* pre = optional_vector(a[7], "pre", dev, cols);
+        bool want[5] = {};
+        truths(a[14], want, 5);
+        want[2] = want[2] && has_post, want[3] = want[3] && has_gate, want[4] = want[4] && has_pre;
+        const CallStream st(a[15], dev);
+        Out dX, dR, dpost, dG, dpre;
+        if (want[0]) dX = out_mat(a[9], "dX", like, dev, rows, cols);
+        if (want[1]) dR = out_mat(a[10], "dR", like, dev, rows, cols);
+        if (want[2]) dpost = out_packed(a[11], "dpost", like, at::kFloat, dev, {cols});
+        if (want[3]) dG = out_mat(a[12], "dgate", like, dev, G.rows, cols);
+        if (want[4]) dpre = out_packed(a[13], "dpre", like, at::kFloat, dev, {cols});
+        if (cols > 0)
+            call([&] {
+                return residual_norm_backward(dS.p, dS.ld, dH.p, dH.ld, X.p, X.ld, S.p, S.ld, post, G.p, G.ld, G.rows, scale,
+                                              pre, eps, dX.m.p, dX.m.ld, dR.m.p, dR.m.ld, static_cast<float*>(dpost.m.p),
+                                              dG.m.p, dG.m.ld, static_cast<float*>(dpre.m.p), rows, cols, type_code(type),
+                                              st);
+            });
+        return Py_BuildValue("NNNNN", wrap_or_none(want[0], dX), wrap_or_none(want[1], dR), wrap_or_none(want[2], dpost),
+                             wrap_or_none(want[3], dG), wrap_or_none(want[4], dpre));
+    });
+}
+
+// moe_sort(expert_ids, num_experts, positions, offsets, stream)
+PyObject* moe_sort_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 5, [&]() -> PyObject* {
+        const at::Tensor& ids = tensor(a[0], "expert_ids");
+        const int dev = first_device(ids, "expert_ids");
+        if (ids.dim() != 2) refuse(PyExc_ValueError, "expert_ids must be 2-D");
+        const void* p = packed(ids, "expert_ids", at::kLong, dev, ids.sizes());
+        const int64_t E = integer(a[1]);
+        if (E < 1 || E > INT32_MAX - 1) refuse(PyExc_ValueError, "num_experts must be positive");
+        const CallStream st(a[4], dev);
+        const Out pos = out_packed(a[2], "positions", ids, at::kInt, dev, ids.sizes());
+        const Out off = out_packed(a[3], "offsets", ids, at::kInt, dev, {std::min<int64_t>(E, 1 << 20) + 1});
+        call([&] {
+            return moe_sort(static_cast<const int64_t*>(p), ids.numel(), as_int(E), static_cast<int32_t*>(pos.m.p),
+                            static_cast<int32_t*>(off.m.p), st);
+        });
+        return Py_BuildValue("NN", pos.wrap(), off.wrap());
+    });
+}
+
+// Positions [T, top_k] and, unless null, the offsets of the experts.
+struct Places {
+    int64_t T = 0, k = 0, experts = 1;
+    const int32_t *positions = nullptr, *offsets = nullptr;
+};
+Places places(PyObject* positions, PyObject* offsets, int dev) {
+    const at::Tensor& p = tensor(positions, "positions");
+    if (p.dim() != 2) refuse(PyExc_ValueError, "positions must be 2-D");
+    Places r;
+    r.positions = static_cast<const int32_t*>(packed(p, "positions", at::kInt, dev, p.sizes()));
+    r.T = p.size(0), r.k = p.size(1);
+    if (offsets != nullptr) {
+        const at::Tensor& o = tensor(offsets, "offsets");
+        if (o.dim() != 1 || o.size(0) < 2) refuse(PyExc_ValueError, "offsets must be [num_experts + 1]");
+        r.offsets = static_cast<const int32_t*>(packed(o, "offsets", at::kInt, dev, o.sizes()));
+        r.experts = o.size(0) - 1;
+    }
+    return r;
+}
+
+// moe_dispatch(X, positions, offsets, Xs, stream)
+PyObject* moe_dispatch_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 5, [&]() -> PyObject* {
+        const at::Tensor& tX = tensor(a[0], "X");
+        const at::ScalarType type = element_type(tX, "X");
+        const int dev = first_device(tX, "X");
+        const Mat X = mat(tX, "X", type, dev);
+        const Places p = places(a[1], a[2], dev);
+        if (p.T != X.rows)
+            refuse(PyExc_ValueError, "positions are of %lld tokens, X has %lld rows", static_cast<long long>(p.T),
+                   static_cast<long long>(X.rows));
+        const CallStream st(a[4], dev);
+        const Out Xs = out_mat(a[3], "Xs", tX, dev, p.T * p.k, X.cols);
+        call([&] {
+            return moe_dispatch(X.p, X.ld, p.positions, p.offsets, as_int(p.experts), Xs.m.p, Xs.m.ld, p.T, p.k, X.cols,
+                                type_code(type), st);
+        });
+        return Xs.wrap();
+    });
+}
+
+// moe_combine(Ys, positions, weights, residual, Y, stream)
+PyObject* moe_combine_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 6, [&]() -> PyObject* {
+        const at::Tensor& tYs = tensor(a[0], "Ys");
+        const at::ScalarType type = element_type(tYs, "Ys");
+        const int dev = first_device(tYs, "Ys");
+        const Mat Ys = mat(tYs, "Ys", type, dev);
+        const Places p = places(a[1], nullptr, dev);
+        const void* w = a[2] == Py_None ? nullptr : packed(tensor(a[2], "weights"), "weights", at::kFloat, dev, {p.T, p.k});
+        Mat R;
+        if (a[3] != Py_None) R = mat_of(a[3], "residual", type, dev, p.T, Ys.cols);
+        const CallStream st(a[5], dev);
+        const Out Y = out_mat(a[4], "Y", tYs, dev, p.T, Ys.cols);
+        call([&] {
+            return moe_combine(Ys.p, Ys.ld, Ys.rows, p.positions, static_cast<const float*>(w), R.p, R.ld, Y.m.p, Y.m.ld,
+                               p.T, p.k, Ys.cols, type_code(type), st);
+        });
+        return Y.wrap();
+    });
+}
+
+// moe_combine_backward(dY, Ys, positions, offsets, weights, dYs, dweights, needs, stream)
+PyObject* moe_combine_backward_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 9, [&]() -> PyObject* {
+        const at::Tensor& tdY = tensor(a[0], "dY");
+        const at::ScalarType type = element_type(tdY, "dY");
+        const int dev = first_device(tdY, "dY");
+        const Mat dY = mat(tdY, "dY", type, dev);
+        const Places p = places(a[2], a[3], dev);
+        if (p.T != dY.rows)
+            refuse(PyExc_ValueError, "positions are of %lld tokens, dY has %lld rows", static_cast<long long>(p.T),
+                   static_cast<long long>(dY.rows));
+        const void* w = packed(tensor(a[4], "weights"), "weights", at::kFloat, dev, {p.T, p.k});
+        bool want[2] = {};
+        truths(a[7], want, 2);
+        Mat Ys;
+        if (want[1]) Ys = mat_of(a[1], "Ys", type, dev, p.T * p.k, dY.cols);
+        const CallStream st(a[8], dev);
+        Out dYs, dw;
+        if (want[0]) dYs = out_mat(a[5], "dYs", tdY, dev, p.T * p.k, dY.cols);
+        if (want[1]) dw = out_packed(a[6], "dweights", tdY, at::kFloat, dev, {p.T, p.k});
+        call([&] {
+            return moe_combine_backward(dY.p, dY.ld, Ys.p, Ys.ld, p.positions, p.offsets, as_int(p.experts),
+                                        static_cast<const float*>(w), dYs.m.p, dYs.m.ld, static_cast<float*>(dw.m.p), p.T,
+                                        p.k, dY.cols, type_code(type), st);
+        });
+        return Py_BuildValue("NN", wrap_or_none(want[0], dYs), wrap_or_none(want[1], dw));
+    });
+}
+
+// A 4-bit matrix's data and scales, given as two tensors and its columns.
+struct Blocks {
+    void *data = nullptr, *scales = nullptr;
+    int64_t rows = 0, cols = 0;
+};
+Blocks blocks(PyObject* data, PyObject* scales, PyObject* columns, const char* data_name, const char* scales_name, int dev) {
+    const at::Tensor& d = tensor(data, data_name);
+    if (d.dim() != 2) refuse(PyExc_ValueError, "%s must be 2-D", data_name);
+    Blocks b;
+    b.rows = d.size(0), b.cols = integer(columns);
+    if (b.cols < 0 || b.cols > INT32_MAX) refuse(PyExc_ValueError, "columns must be in [0, 2^31)");
+    b.data = packed(d, data_name, at::kByte, dev, {b.rows, (b.cols + 31) / 32 * 16});
+    b.scales = packed(tensor(scales, scales_name), scales_name, at::kByte, dev,
+                      {(b.rows + 127) / 128, (b.cols + 127) / 128, 512});
+    return b;
+}
+
+// quantize_mxfp4(X, transposed, data, scales, stream) -> (columns, data, scales)
+PyObject* quantize_mxfp4_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 5, [&]() -> PyObject* {
+        const at::Tensor& tX = tensor(a[0], "X");
+        const at::ScalarType type = element_type(tX, "X");
+        const int dev = first_device(tX, "X");
+        const Mat X = mat(tX, "X", type, dev);
+        const bool transposed = truth(a[1]);
+        const int64_t rows = transposed ? X.cols : X.rows, cols = transposed ? X.rows : X.cols;
+        const CallStream st(a[4], dev);
+        const Out data = out_packed(a[2], "data", tX, at::kByte, dev, {rows, (cols + 31) / 32 * 16});
+        const Out scales = out_packed(a[3], "scales", tX, at::kByte, dev, {(rows + 127) / 128, (cols + 127) / 128, 512});
+        call([&] {
+            return quantize_mxfp4(X.p, X.ld, data.m.p, scales.m.p, rows, cols, transposed ? 1 : 0, type_code(type), st);
+        });
+        return Py_BuildValue("LNN", static_cast<long long>(cols), data.wrap(), scales.wrap());
+    });
+}
+
+// dequantize_mxfp4(data, scales, columns, dtype, X, stream)
+PyObject* dequantize_mxfp4_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 6, [&]() -> PyObject* {
+        const at::Tensor& d = tensor(a[0], "data");
+        const int dev = first_device(d, "data");
+        const Blocks q = blocks(a[0], a[1], a[2], "data", "scales", dev);
+        at::ScalarType type = at::kBFloat16;
+        if (a[3] != Py_None) {
+            if (!THPDtype_Check(a[3])) refuse(PyExc_TypeError, "dtype must be torch.bfloat16 or torch.float32");
+            type = reinterpret_cast<THPDtype*>(a[3])->scalar_type;
+            if (type != at::kBFloat16 && type != at::kFloat)
+                refuse(PyExc_TypeError, "dtype must be torch.bfloat16 or torch.float32");
+        } else if (a[4] != Py_None) {
+            type = element_type(tensor(a[4], "X"), "X");
+        }
+        const CallStream st(a[5], dev);
+        Out X;
+        if (a[4] != Py_None) {
+            X.given = a[4];
+            X.m = mat_of(a[4], "X", type, dev, q.rows, q.cols);
+        } else {
+            X.made = at::empty({q.rows, q.cols}, d.options().dtype(type));
+            X.m.p = X.made.data_ptr();
+            X.m.ld = q.cols > 0 ? q.cols : 1;
+        }
+        call([&] { return dequantize_mxfp4(q.data, q.scales, X.m.p, X.m.ld, q.rows, q.cols, type_code(type), st); });
+        return X.wrap();
+    });
+}
+
+// gemm_mxfp4(A, A_scales, A_columns, B, B_scales, B_columns, bias, residual, act, C, stream)
+PyObject* gemm_mxfp4_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 11, [&]() -> PyObject* {
+        const at::Tensor& tA = tensor(a[0], "A");
+        const int dev = first_device(tA, "A");
+        const Blocks A = blocks(a[0], a[1], a[2], "A", "A's scales", dev), B = blocks(a[3], a[4], a[5], "B", "B's scales", dev);
+        if (A.cols != B.cols)
+            refuse(PyExc_ValueError, "shape mismatch: A [%lld, %lld], B [%lld, %lld]", static_cast<long long>(A.rows),
+                   static_cast<long long>(A.cols), static_cast<long long>(B.rows), static_cast<long long>(B.cols));
+        const float* bias = optional_vector(a[6], "bias", dev, B.rows);
+        Mat R;
+        if (a[7] != Py_None) R = mat_of(a[7], "residual", at::kBFloat16, dev, A.rows, B.rows);
+        const int act = act_code(a[8]);
+        const CallStream st(a[10], dev);
+        Out C;
+        if (a[9] != Py_None) {
+            C.given = a[9];
+            C.m = mat_of(a[9], "C", at::kBFloat16, dev, A.rows, B.rows);
+        } else {
+            C.made = at::empty({A.rows, B.rows}, tA.options().dtype(at::kBFloat16));
+            C.m.p = C.made.data_ptr();
+            C.m.ld = B.rows > 0 ? B.rows : 1;
+        }
+        call([&] {
+            return gemm_mxfp4(A.data, A.scales, B.data, B.scales, bias, R.p, R.ld, C.m.p, C.m.ld, A.rows, B.rows, A.cols,
+                              act, st);
+        });
+        return C.wrap();
+    });
+}
+
 // set_errors(GbrError, torch.OutOfMemoryError)
 PyObject* set_errors_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 2, [&]() -> PyObject* {
@@ -432,6 +776,15 @@ PyMethodDef g_methods[] = {
     {"gemm_bias_act", fast<gemm_bias_act_py>(), METH_FASTCALL, nullptr},
     {"gemm_bias_act_backward", fast<gemm_bias_act_backward_py>(), METH_FASTCALL, nullptr},
     {"moe_layer", fast<moe_layer_py>(), METH_FASTCALL, nullptr},
+    {"residual_norm", fast<residual_norm_py>(), METH_FASTCALL, nullptr},
+    {"residual_norm_backward", fast<residual_norm_backward_py>(), METH_FASTCALL, nullptr},
+    {"moe_sort", fast<moe_sort_py>(), METH_FASTCALL, nullptr},
+    {"moe_dispatch", fast<moe_dispatch_py>(), METH_FASTCALL, nullptr},
+    {"moe_combine", fast<moe_combine_py>(), METH_FASTCALL, nullptr},
+    {"moe_combine_backward", fast<moe_combine_backward_py>(), METH_FASTCALL, nullptr},
+    {"quantize_mxfp4", fast<quantize_mxfp4_py>(), METH_FASTCALL, nullptr},
+    {"dequantize_mxfp4", fast<dequantize_mxfp4_py>(), METH_FASTCALL, nullptr},
+    {"gemm_mxfp4", fast<gemm_mxfp4_py>(), METH_FASTCALL, nullptr},
     {"set_errors", fast<set_errors_py>(), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

@@ -1,0 +1,584 @@
+// residual_norm.cu -- the norms before and after a block with its gate and the
+// residual, and their gradients.
+//
+//   y = X q post,  q = 1 / sqrt(mean X^2 + eps)      (no post: y = X)
+//   S = R + scale gate y
+//   H = S r pre,   r = 1 / sqrt(mean S^2 + eps)
+//
+//   u = dH pre;  ds = dS + r u - S r^3 mean(u S)      dR = ds, dpre = sum dH S r
+//   dy = scale gate ds                                dgate = sum scale y ds
+//   v = dy post; dX = q v - X q^3 mean(v X)           dpost = sum dy X q
+//
+// Bound by memory: every operand is read once and every output written once; a
+// group of threads holds its row in registers between the passes that the two
+// means need.  Statistics and sums are fp32.  H comes from the sum before it is
+// rounded to S.
+#include "gbr.h"
+#include "operators.h"
+#include "row8.cuh"
+
+#include <algorithm>
+#include <cstdint>
+
+namespace gbr {
+namespace {
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+template <typename T>
+struct Args {
+    const T *X, *R, *G;
+    const float *post, *pre;
+    T *S, *H;
+    int64_t ldx, ldr, ldg, lds, ldh;
+    int32_t rows, cols, per_gate;      // rows that share a row of G
+    float scale, eps, inv_cols;
+};
+
+__device__ __forceinline__ float root(float sum, float inv_cols, float eps) { return rsqrtf(fmaf(sum, inv_cols, eps)); }
+
+// ------------------------------------------------------------ forward
+// blockDim.x / tpr rows a CTA, V * 8 columns a thread.
+template <typename T, int V, bool VEC>
+__global__ void __launch_bounds__(1024) residual_norm_kernel(const Args<T> a, int32_t tpr) {
+    __shared__ float buf[2][1][32];
+    ptx::griddep_wait();
+    const int32_t t = int32_t(threadIdx.x) % tpr;
+    const int64_t row = int64_t(blockIdx.x) * (int32_t(blockDim.x) / tpr) + int32_t(threadIdx.x) / tpr;
+    const int32_t cols = row < a.rows ? a.cols : 0;    // a group past the end only keeps the barriers
+    float s[V][8];
+#pragma unroll
+    for (int v = 0; v < V; ++v) load_row8<T, VEC>(s[v], a.X + row * a.ldx, v, t, tpr, cols);
+    if (a.R != nullptr || a.G != nullptr || a.post != nullptr || a.scale != 1.f) {
+        Raw8<T> r[V] = {}, g[V];
+        if (a.R != nullptr)
+#pragma unroll
+            for (int v = 0; v < V; ++v) load_raw8<VEC>(r[v], a.R + row * a.ldr, v, t, tpr, cols);
+        if (a.G != nullptr)
+#pragma unroll
+            for (int v = 0; v < V; ++v) load_raw8<VEC>(g[v], a.G + row / a.per_gate * a.ldg, v, t, tpr, cols);
+        float q = 1.f;
+        if (a.post != nullptr) {
+            float sum[1] = {};
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum[0] = fmaf(s[v][j], s[v][j], sum[0]);
+            group_sum(sum, buf[0], tpr);
+            q = root(sum[0], a.inv_cols, a.eps);
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            float w[8];
+            if (a.post != nullptr) load_row8<float, VEC>(w, a.post, v, t, tpr, cols);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float y = s[v][j];
+                if (a.post != nullptr) y = y * q * w[j];
+                if (a.G != nullptr) y *= raw_at(g[v], j);
+                s[v][j] = fmaf(a.scale, y, raw_at(r[v], j));
+            }
+        }
+    }
+    if (a.S != nullptr)
+#pragma unroll
+        for (int v = 0; v < V; ++v) store_row8<T, VEC>(a.S + row * a.lds, s[v], v, t, tpr, cols);
+    if (a.H == nullptr) return;
+    float sum[1] = {};
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[0] = fmaf(s[v][j], s[v][j], sum[0]);
+    group_sum(sum, buf[1], tpr);
+    const float q = root(sum[0], a.inv_cols, a.eps);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        float w[8];
+        load_row8<float, VEC>(w, a.pre, v, t, tpr, cols);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = s[v][j] * q * w[j];
+        store_row8<T, VEC>(a.H + row * a.ldh, w, v, t, tpr, cols);
+    }
+}
+
+// Rows that no CTA can hold: a CTA a row, read again for each mean.
+template <typename T>
+__device__ __forceinline__ float sum_at(const Args<T>& a, int64_t row, float q, int32_t c) {
+    float y = to_f32(a.X[row * a.ldx + c]);
+    if (a.post != nullptr) y = y * q * a.post[c];
+    if (a.G != nullptr) y *= to_f32(a.G[row / a.per_gate * a.ldg + c]);
+    if (a.R == nullptr && a.scale == 1.f) return y;
+    return fmaf(a.scale, y, a.R != nullptr ? to_f32(a.R[row * a.ldr + c]) : 0.f);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(1024) residual_norm_long_kernel(const Args<T> a) {
+    __shared__ float buf[2][1][32];
+    ptx::griddep_wait();
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        float sum[1] = {}, q = 1.f;
+        if (a.post != nullptr) {
+            for (int32_t c = int32_t(threadIdx.x); c < a.cols; c += 1024) {
+                const float x = to_f32(a.X[row * a.ldx + c]);
+                sum[0] = fmaf(x, x, sum[0]);
+            }
+            group_sum(sum, buf[0], 1024);
+            q = root(sum[0], a.inv_cols, a.eps);
+        }
+        float r = 0.f;
+        if (a.H != nullptr) {
+            sum[0] = 0.f;
+            for (int32_t c = int32_t(threadIdx.x); c < a.cols; c += 1024) {
+                const float s = sum_at(a, row, q, c);
+                sum[0] = fmaf(s, s, sum[0]);
+            }
+            group_sum(sum, buf[1], 1024);
+            r = root(sum[0], a.inv_cols, a.eps);
+        }
+        for (int32_t c = int32_t(threadIdx.x); c < a.cols; c += 1024) {
+            const float s = sum_at(a, row, q, c);
+            if (a.S != nullptr) from_f32(s, a.S + row * a.lds + c);
+            if (a.H != nullptr) from_f32(s * r * a.pre[c], a.H + row * a.ldh + c);
+        }
+        __syncthreads();                                // buf, for the next row
+    }
+}
+
+// ------------------------------------------------------------ gradients
+template <typename T>
+struct GradArgs {
+    const T *dS, *dH, *X, *S, *G;
+    const float *post, *pre;
+    T *dX, *dR, *dG;
+    int64_t ldds, lddh, ldx, lds, ldg, lddx, lddr, lddg;
+    int32_t rows, cols, per_gate;
+    float scale, eps, inv_cols;
+    // Sums over rows: `items` runs of rows, `segments` of them to a gate; each CTA takes a
+    // contiguous share of the items.  part: per CTA [post][pre] rows of cols, or null; gate_part:
+    // per item, where a gate has several segments (one segment: dG itself).
+    int32_t items, segments, span;     // span: rows of a gate (all rows where the items are one run)
+    float *post_part, *pre_part, *gate_part;
+    bool want_post, want_pre, want_gate;
+};
+
+// One CTA: its items' rows, blockDim.x / tpr at a time.  Thread t of each group keeps the sums of
+// its columns; groups are joined in order through shared memory.
+template <typename T, int V, bool VEC>
+__global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<T> a, int32_t tpr) {
+    __shared__ float buf[2][3][32];
+    extern __shared__ float joined[];                   // [groups][tpr * 8 * V] where groups > 1
+    ptx::griddep_wait();
+    const int32_t t = int32_t(threadIdx.x) % tpr, group = int32_t(threadIdx.x) / tpr;
+    const int32_t groups = int32_t(blockDim.x) / tpr;
+    const int32_t i0 = int32_t(int64_t(a.items) * blockIdx.x / gridDim.x);
+    const int32_t i1 = int32_t(int64_t(a.items) * (blockIdx.x + 1) / gridDim.x);
+    float wpost[V][8], wpre[V][8], spost[V][8] = {}, spre[V][8] = {}, sgate[V][8] = {};
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        if (a.post != nullptr) load_row8<float, VEC>(wpost[v], a.post, v, t, tpr, a.cols);
+        if (a.pre != nullptr) load_row8<float, VEC>(wpre[v], a.pre, v, t, tpr, a.cols);
+    }
+    // Adds the groups' sums in order; the result is in group 0.
+    auto join = [&](float (&s)[V][8]) {
+        if (groups == 1) return;
+        __syncthreads();
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) joined[(group * V * 8 + v * 8 + j) * tpr + t] = s[v][j];
+        __syncthreads();
+        if (group != 0) return;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                for (int32_t g = 1; g < groups; ++g) s[v][j] += joined[(g * V * 8 + v * 8 + j) * tpr + t];
+    };
+    const bool gate_rows = a.per_gate == 1;             // dG row by row, nothing to add
+    for (int32_t item = i0; item < i1; ++item) {
+        const int32_t g = item / a.segments, seg = item % a.segments;
+        const int64_t base = int64_t(g) * a.span;
+        const int64_t r0 = base + int64_t(a.span) * seg / a.segments, r1 = base + int64_t(a.span) * (seg + 1) / a.segments;
+        for (int64_t first = r0; first < r1; first += groups) {
+            const int64_t row = first + group;
+            const int32_t cols = row < r1 ? a.cols : 0;
+            Raw8<T> x[V] = {}, s[V] = {}, dh[V] = {}, ds[V] = {}, gt[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                if (a.X != nullptr) load_raw8<VEC>(x[v], a.X + row * a.ldx, v, t, tpr, cols);
+                if (a.pre != nullptr) {
+                    load_raw8<VEC>(s[v], a.S + row * a.lds, v, t, tpr, cols);
+                    load_raw8<VEC>(dh[v], a.dH + row * a.lddh, v, t, tpr, cols);
+                }
+                if (a.dS != nullptr) load_raw8<VEC>(ds[v], a.dS + row * a.ldds, v, t, tpr, cols);
+                if (a.G != nullptr) load_raw8<VEC>(gt[v], a.G + row / a.per_gate * a.ldg, v, t, tpr, cols);
+            }
+            float sum[3] = {};
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float xs = raw_at(s[v], j), xx = raw_at(x[v], j);
+                    if (a.pre != nullptr) {
+                        sum[0] = fmaf(xs, xs, sum[0]);
+                        sum[1] = fmaf(raw_at(dh[v], j) * wpre[v][j], xs, sum[1]);
+                    }
+                    if (a.post != nullptr) sum[2] = fmaf(xx, xx, sum[2]);
+                }
+            if (a.pre != nullptr || a.post != nullptr) group_sum(sum, buf[0], tpr);
+            const float r = root(sum[0], a.inv_cols, a.eps), rc = r * r * r * sum[1] * a.inv_cols;
+            const float q = a.post != nullptr ? root(sum[2], a.inv_cols, a.eps) : 1.f;
+            float d[V][8], dot[1] = {};
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                float dg[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    float e = raw_at(ds[v], j);
+                    if (a.pre != nullptr) {
+                        const float h = raw_at(dh[v], j), xs = raw_at(s[v], j);
+                        e = e + r * (h * wpre[v][j]) - xs * rc;
+                        if (cols > 0) spre[v][j] = fmaf(h, xs * r, spre[v][j]);
+                    }
+                    d[v][j] = e;
+                }
+                if (a.dR != nullptr) store_row8<T, VEC>(a.dR + row * a.lddr, d[v], v, t, tpr, cols);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float n = raw_at(x[v], j) * q;           // X normalised
+                    float e = a.scale * d[v][j];
+                    dg[j] = e * (a.post != nullptr ? n * wpost[v][j] : n);
+                    if (a.G != nullptr) e *= raw_at(gt[v], j);
+                    if (cols > 0) {
+                        sgate[v][j] += dg[j];
+                        if (a.post != nullptr) spost[v][j] = fmaf(e, n, spost[v][j]);
+                    }
+                    if (a.post != nullptr) e *= wpost[v][j];
+                    d[v][j] = e;
+                    dot[0] = fmaf(e, raw_at(x[v], j), dot[0]);
+                }
+                if (a.want_gate && gate_rows) store_row8<T, VEC>(a.dG + row * a.lddg, dg, v, t, tpr, cols);
+            }
+            if (a.dX != nullptr) {
+                if (a.post != nullptr) {
+                    group_sum(dot, buf[1], tpr);
+                    const float qc = q * q * q * dot[0] * a.inv_cols;
+#pragma unroll
+                    for (int v = 0; v < V; ++v)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) d[v][j] = q * d[v][j] - raw_at(x[v], j) * qc;
+                }
+#pragma unroll
+                for (int v = 0; v < V; ++v) store_row8<T, VEC>(a.dX + row * a.lddx, d[v], v, t, tpr, cols);
+            }
+            if (tpr > 32 && (a.dX == nullptr || a.post == nullptr)) __syncthreads();   // buf[0], for the next rows
+        }
+        if (a.want_gate && !gate_rows) {
+            join(sgate);
+            if (group == 0)
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    if (a.segments > 1)
+                        store_row8<float, VEC>(a.gate_part + int64_t(item) * a.cols, sgate[v], v, t, tpr, a.cols);
+                    else
+                        store_row8<T, VEC>(a.dG + g * a.lddg, sgate[v], v, t, tpr, a.cols);
+                }
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sgate[v][j] = 0.f;
+        }
+    }
+    if (a.want_post) {
+        join(spost);
+        if (group == 0)
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                store_row8<float, VEC>(a.post_part + int64_t(blockIdx.x) * a.cols, spost[v], v, t, tpr, a.cols);
+    }
+    if (a.want_pre) {
+        join(spre);
+        if (group == 0)
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                store_row8<float, VEC>(a.pre_part + int64_t(blockIdx.x) * a.cols, spre[v], v, t, tpr, a.cols);
+    }
+}
+
+// Rows that no CTA can hold: their means first (a CTA a row), then everything else column by column.
+template <typename T>
+__device__ __forceinline__ float sum_grad_at(const GradArgs<T>& a, int64_t row, int32_t c, float r, float rc) {
+    float e = a.dS != nullptr ? to_f32(a.dS[row * a.ldds + c]) : 0.f;
+    if (a.pre != nullptr) {
+        const float h = to_f32(a.dH[row * a.lddh + c]);
+        e = e + r * (h * a.pre[c]) - to_f32(a.S[row * a.lds + c]) * rc;
+    }
+    return e;
+}
+
+// stats[row] = {r, r^3 mean(u S), q, q^3 mean(v X)}
+template <typename T>
+__global__ void __launch_bounds__(1024) residual_norm_stats_kernel(const GradArgs<T> a, float4* stats) {
+    __shared__ float buf[2][3][32];
+    ptx::griddep_wait();
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        float sum[3] = {}, dot[1] = {};
+        for (int32_t c = int32_t(threadIdx.x); c < a.cols; c += 1024) {
+            if (a.pre != nullptr) {
+                const float s = to_f32(a.S[row * a.lds + c]);
+                sum[0] = fmaf(s, s, sum[0]);
+                sum[1] = fmaf(to_f32(a.dH[row * a.lddh + c]) * a.pre[c], s, sum[1]);
+            }
+            if (a.post != nullptr) {
+                const float x = to_f32(a.X[row * a.ldx + c]);
+                sum[2] = fmaf(x, x, sum[2]);
+            }
+        }
+        group_sum(sum, buf[0], 1024);
+        const float r = root(sum[0], a.inv_cols, a.eps), rc = r * r * r * sum[1] * a.inv_cols;
+        const float q = a.post != nullptr ? root(sum[2], a.inv_cols, a.eps) : 1.f;
+        if (a.post != nullptr)
+            for (int32_t c = int32_t(threadIdx.x); c < a.cols; c += 1024) {
+                float e = a.scale * sum_grad_at(a, row, c, r, rc);
+                if (a.G != nullptr) e *= to_f32(a.G[row / a.per_gate * a.ldg + c]);
+                dot[0] = fmaf(e * a.post[c], to_f32(a.X[row * a.ldx + c]), dot[0]);
+            }
+        group_sum(dot, buf[1], 1024);
+        if (threadIdx.x == 0) stats[row] = make_float4(r, rc, q, q * q * q * dot[0] * a.inv_cols);
+    }
+}
+
+// A column a thread; blockIdx.y: the share of the items.
+template <typename T>
+__global__ void __launch_bounds__(256) residual_norm_grad_long_kernel(const GradArgs<T> a, const float4* stats) {
+    ptx::griddep_wait();
+    const int32_t c = int32_t(blockIdx.x) * 256 + int32_t(threadIdx.x);
+    if (c >= a.cols) return;
+    const int32_t i0 = int32_t(int64_t(a.items) * blockIdx.y / gridDim.y);
+    const int32_t i1 = int32_t(int64_t(a.items) * (blockIdx.y + 1) / gridDim.y);
+    const float wpost = a.post != nullptr ? a.post[c] : 1.f;
+    float spost = 0.f, spre = 0.f;
+    for (int32_t item = i0; item < i1; ++item) {
+        const int32_t g = item / a.segments, seg = item % a.segments;
+        const int64_t base = int64_t(g) * a.span;
+        const int64_t r0 = base + int64_t(a.span) * seg / a.segments, r1 = base + int64_t(a.span) * (seg + 1) / a.segments;
+        float sgate = 0.f;
+        for (int64_t row = r0; row < r1; ++row) {
+            const float4 st = stats[row];
+            float e = sum_grad_at(a, row, c, st.x, st.y);
+            if (a.pre != nullptr) spre = fmaf(to_f32(a.dH[row * a.lddh + c]), to_f32(a.S[row * a.lds + c]) * st.x, spre);
+            if (a.dR != nullptr) from_f32(e, a.dR + row * a.lddr + c);
+            e *= a.scale;
+            const float x = a.X != nullptr ? to_f32(a.X[row * a.ldx + c]) : 0.f, n = x * st.z;
+            const float dg = e * n * wpost;
+            sgate += dg;
+            if (a.want_gate && a.per_gate == 1) from_f32(dg, a.dG + row * a.lddg + c);
+            if (a.G != nullptr) e *= to_f32(a.G[row / a.per_gate * a.ldg + c]);
+            spost = fmaf(e, n, spost);
+            if (a.dX != nullptr) from_f32(a.post != nullptr ? st.z * (e * wpost) - x * st.w : e, a.dX + row * a.lddx + c);
+        }
+        if (a.want_gate && a.per_gate != 1) {
+            if (a.segments > 1)
+                a.gate_part[int64_t(item) * a.cols + c] = sgate;
+            else
+                from_f32(sgate, a.dG + g * a.lddg + c);
+        }
+    }
+    if (a.want_post) a.post_part[int64_t(blockIdx.y) * a.cols + c] = spost;
+    if (a.want_pre) a.pre_part[int64_t(blockIdx.y) * a.cols + c] = spre;
+}
+
+// Sums of runs of `count` rows of a [runs * count, cols] fp32 matrix, 32 columns a CTA: the rows dealt to
+// 32 warps, then the warps' sums added in order.  blockIdx.y: which of the up to three outputs' runs.
+struct PartSums {
+    struct Of {
+        const float* in;
+        void* out;
+        int64_t ldo;
+        int32_t runs, count;
+        bool bf16;
+    } of[3];
+    int32_t n, cols;
+};
+
+__global__ void __launch_bounds__(1024) norm_sums_kernel(const PartSums p) {
+    __shared__ float part[32][33];
+    ptx::griddep_wait();
+    int32_t run = int32_t(blockIdx.y), i = 0;
+    while (i + 1 < p.n && run >= p.of[i].runs) run -= p.of[i++].runs;
+    const PartSums::Of& o = p.of[i];
+    const int32_t lane = int32_t(threadIdx.x) % 32, warp = int32_t(threadIdx.x) / 32;
+    const int32_t c = int32_t(blockIdx.x) * 32 + lane;
+    float s = 0.f;
+    if (c < p.cols)
+#pragma unroll 8
+        for (int32_t k = warp; k < o.count; k += 32) s += o.in[(int64_t(run) * o.count + k) * p.cols + c];
+    part[warp][lane] = s;
+    __syncthreads();
+    s = warp_sum(part[lane][warp]);                     // column `warp` of the 32
+    const int32_t d = int32_t(blockIdx.x) * 32 + warp;
+    if (lane == 0 && d < p.cols) {
+        if (o.bf16)
+            static_cast<__nv_bfloat16*>(o.out)[run * o.ldo + d] = __float2bfloat16_rn(s);
+        else
+            static_cast<float*>(o.out)[run * o.ldo + d] = s;
+    }
+}
+
+// ------------------------------------------------------------ launches
+// Rows on 16 bytes; a single row's pitch does not matter.
+template <typename T>
+bool aligned16(const void* p, int64_t ld, int64_t rows) {
+    return p == nullptr ||
+           (reinterpret_cast<uintptr_t>(p) % 16 == 0 && (rows <= 1 || ld % int64_t(16 / sizeof(T)) == 0));
+}
+
+// Threads a row: the fewest warps that hold it with V vectors each.
+int threads_for(int64_t cols, int V) {
+    int tpr = 32;
+    while (int64_t(tpr) * 8 * V < cols) tpr *= 2;
+    return tpr;
+}
+
+template <typename T, int V>
+void* forward_kernel(bool vec) {
+    return vec ? reinterpret_cast<void*>(&residual_norm_kernel<T, V, true>)
+               : reinterpret_cast<void*>(&residual_norm_kernel<T, V, false>);
+}
+
+template <typename T>
+int run_forward(const ResidualNormArgs& s, const LibCtx& c, cudaStream_t stream) {
+    Args<T> a = {static_cast<const T*>(s.X.p), static_cast<const T*>(s.R.p), static_cast<const T*>(s.G.p), s.post, s.pre,
+                 static_cast<T*>(s.S.w()), static_cast<T*>(s.H.w()), s.X.ld, s.R.ld, s.G.ld, s.S.ld, s.H.ld, s.rows,
+                 s.cols, s.per_gate, s.scale, s.eps, float(1.0 / double(s.cols))};
+    bool vec = s.cols % 8 == 0 && aligned16<float>(s.post, 0, 1) && aligned16<float>(s.pre, 0, 1) &&
+               aligned16<T>(s.G.p, s.G.ld, s.gates);
+    for (const Mat* m : {&s.X, &s.R, &s.S, &s.H}) vec = vec && aligned16<T>(m->p, m->ld, s.rows);
+    cudaError_t e;
+    if (s.cols > 1024 * 32) {
+        void* args[] = {&a};
+        e = launch_kernel(reinterpret_cast<void*>(&residual_norm_long_kernel<T>),
+                          dim3(unsigned(std::min<int64_t>(s.rows, 2 * c.sm_count))), 1024, 0, 1, args, stream);
+    } else {
+        const int V = s.cols > 1024 * 16 ? 4 : s.cols > 1024 * 8 ? 2 : 1;
+        int32_t tpr = threads_for(s.cols, V);
+        const int threads = std::max(256, int(tpr));
+        void* kernel = V == 4 ? forward_kernel<T, 4>(vec) : V == 2 ? forward_kernel<T, 2>(vec) : forward_kernel<T, 1>(vec);
+        void* args[] = {&a, &tpr};
+        e = launch_kernel(kernel, dim3(unsigned(cdiv(s.rows, threads / tpr))), threads, 0, 1, args, stream);
+    }
+    if (e != cudaSuccess) return report_cuda(e, "launching residual_norm");
+    count_launch();
+    return GBR_OK;
+}
+
+template <typename T, int V>
+void* grad_kernel(bool vec) {
+    return vec ? reinterpret_cast<void*>(&residual_norm_grad_kernel<T, V, true>)
+               : reinterpret_cast<void*>(&residual_norm_grad_kernel<T, V, false>);
+}
+
+// Cuts the rows into items and the items into at most `ctas` shares: without a gate that several
+// rows share, one run of equal pieces; else so many segments a gate that the largest share is the
+// smallest (an item's sums cost about as much as two rows).
+template <typename T>
+int64_t cut_rows(GradArgs<T>* a, int32_t gates, int64_t ctas, int32_t groups) {
+    const int64_t turns = cdiv(a->rows, groups);
+    if (!a->want_gate || a->per_gate == 1) {
+        a->items = a->segments = int32_t(std::max<int64_t>(1, std::min(turns, ctas)));
+        a->span = a->rows;
+        return a->items;
+    }
+    a->span = a->per_gate;
+    int64_t best = INT64_MAX;
+    const int64_t most = std::max<int64_t>(1, std::min<int64_t>(a->per_gate, 4 * ctas / gates));
+    for (int64_t s = 1; s <= most; ++s) {
+        const int64_t cost = cdiv(gates * s, ctas) * (cdiv(cdiv(a->per_gate, s), groups) + 2);
+        if (cost < best) best = cost, a->segments = int32_t(s);
+    }
+    a->items = gates * a->segments;
+    return std::min<int64_t>(a->items, ctas);
+}
+
+template <typename T>
+int run_backward(const ResidualNormGradArgs& s, const LibCtx& c, cudaStream_t stream) {
+    GradArgs<T> a = {};
+    a.dS = static_cast<const T*>(s.dS.p), a.dH = static_cast<const T*>(s.dH.p), a.X = static_cast<const T*>(s.X.p);
+    a.S = static_cast<const T*>(s.S.p), a.G = static_cast<const T*>(s.G.p);
+    a.post = s.post, a.pre = s.pre;
+    a.dX = static_cast<T*>(s.dX.w()), a.dR = static_cast<T*>(s.dR.w()), a.dG = static_cast<T*>(s.dG.w());
+    a.ldds = s.dS.ld, a.lddh = s.dH.ld, a.ldx = s.X.ld, a.lds = s.S.ld, a.ldg = s.G.ld;
+    a.lddx = s.dX.ld, a.lddr = s.dR.ld, a.lddg = s.dG.ld;
+    a.rows = s.rows, a.cols = s.cols, a.per_gate = s.per_gate;
+    a.scale = s.scale, a.eps = s.eps, a.inv_cols = float(1.0 / double(s.cols));
+    a.want_post = s.dpost != nullptr, a.want_pre = s.dpre != nullptr, a.want_gate = s.dG.p != nullptr && s.gates > 0;
+    const bool long_rows = s.cols > 8192;
+    const int V = s.cols > 4096 ? 2 : 1;
+    int32_t tpr = long_rows ? 1024 : threads_for(s.cols, V);
+    const int threads = std::max(256, int(tpr)), groups = long_rows ? 1 : threads / tpr;
+    const int64_t col_ctas = cdiv(s.cols, 256);
+    const int64_t ctas = long_rows ? std::max<int64_t>(1, 8 * c.sm_count / col_ctas) : c.sm_count * (threads > 256 ? 1 : 2);
+    const int64_t grid = cut_rows(&a, s.gates, ctas, groups);
+    Scratch ws(c, stream);
+    void* q;
+    int r;
+    const size_t row_bytes = size_t(s.cols) * 4;
+    PartSums sums = {};
+    sums.cols = s.cols;
+    int32_t runs = 0;
+    auto part = [&](bool want, int64_t n, int64_t count, void* out, int64_t ldo, bool bf16, float** p) -> int {
+        if (!want) return GBR_OK;
+        const int e = ws.take(size_t(n * count) * row_bytes, "cudaMallocFromPoolAsync(sums over rows)", &q);
+        if (e != GBR_OK) return e;
+        *p = static_cast<float*>(q);
+        sums.of[sums.n++] = {*p, out, ldo, int32_t(n), int32_t(count), bf16};
+        runs += int32_t(n);
+        return GBR_OK;
+    };
+    if ((r = part(a.want_post, 1, grid, s.dpost, 0, false, &a.post_part)) != GBR_OK) return r;
+    if ((r = part(a.want_pre, 1, grid, s.dpre, 0, false, &a.pre_part)) != GBR_OK) return r;
+    if ((r = part(a.want_gate && a.per_gate != 1 && a.segments > 1, s.gates, a.segments, s.dG.w(), s.dG.ld, s.bf16,
+                  &a.gate_part)) != GBR_OK)
+        return r;
+    cudaError_t e;
+    if (long_rows) {
+        if ((r = ws.take(size_t(s.rows) * sizeof(float4), "cudaMallocFromPoolAsync(row statistics)", &q)) != GBR_OK) return r;
+        float4* stats = static_cast<float4*>(q);
+        void* args[] = {&a, &stats};
+        e = launch_kernel(reinterpret_cast<void*>(&residual_norm_stats_kernel<T>),
+                          dim3(unsigned(std::min<int64_t>(s.rows, 2 * c.sm_count))), 1024, 0, 1, args, stream);
+        if (e != cudaSuccess) return report_cuda(e, "launching residual_norm_backward");
+        count_launch();
+        e = launch_kernel(reinterpret_cast<void*>(&residual_norm_grad_long_kernel<T>),
+                          dim3(unsigned(col_ctas), unsigned(grid)), 256, 0, 1, args, stream);
+    } else {
+        bool vec = s.cols % 8 == 0 && aligned16<T>(s.G.p, s.G.ld, s.gates) && aligned16<T>(s.dG.p, s.dG.ld, s.gates);
+        for (const Mat* m : {&s.dS, &s.dH, &s.X, &s.S, &s.dX, &s.dR}) vec = vec && aligned16<T>(m->p, m->ld, s.rows);
+        for (const float* w : {s.post, s.pre}) vec = vec && aligned16<float>(w, 0, 1);
+        void* kernel = V == 2 ? grad_kernel<T, 2>(vec) : grad_kernel<T, 1>(vec);
+        void* args[] = {&a, &tpr};
+        const size_t smem = groups > 1 ? size_t(threads) * 8 * V * sizeof(float) : 0;
+        e = launch_kernel(kernel, dim3(unsigned(grid)), threads, smem, 1, args, stream);
+    }
+    if (e != cudaSuccess) return report_cuda(e, "launching residual_norm_backward");
+    count_launch();
+    if (runs == 0) return GBR_OK;
+    void* args[] = {&sums};
+    e = launch_kernel(reinterpret_cast<void*>(&norm_sums_kernel), dim3(unsigned(cdiv(s.cols, 32)), unsigned(runs)), 1024,
+                      0, 1, args, stream);
+    if (e != cudaSuccess) return report_cuda(e, "launching the sums of residual_norm_backward");
+    count_launch();
+    return GBR_OK;
+}
+
+}  // namespace
+
+int launch_residual_norm(const ResidualNormArgs& a, const LibCtx& c, cudaStream_t stream) {
+    return a.bf16 ? run_forward<__nv_bfloat16>(a, c, stream) : run_forward<float>(a, c, stream);
+}
+
+int launch_residual_norm_grad(const ResidualNormGradArgs& a, const LibCtx& c, cudaStream_t stream) {
+    return a.bf16 ? run_backward<__nv_bfloat16>(a, c, stream) : run_backward<float>(a, c, stream);
+}
+
+}  // namespace gbr

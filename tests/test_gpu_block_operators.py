@@ -1,0 +1,612 @@
+"""The operators around a feed-forward block (residual_norm, rows by expert, 4-bit
+products) on the GPU against their definitions in 64 bits.
+
+Bars, elementwise.  half: a rounding to the output's type, finfo.eps / 2 of the
+value (bf16 2^-8, fp32 2^-24).  m: the sum of the sizes of what is added.
+  residual_norm     S: five fp32 operations and a root whose sum of squares (all
+      positive) adds at most 40 in a row: below 2^-20 m.  H multiplies that by root
+      and weight and has a root of its own: 2^-19 (m root |pre| + |H|)
+  its gradients     the same twice over, with a mean of signed products, whose error
+      is relative to the mean of their sizes: 2^-18 m; sums over rows add rows 2^-24 m
+  combine           a product and a sum each: (k + 2) 2^-23 m
+  its gradients     dYs one product: 2^-23 |dYs|; dweights at most 128 terms a thread
+      and 10 levels: 2^-17 m
+  4-bit values      equal
+  4-bit product     products are exact; each of the K / 64 steps and the split's sums add to
+      fp32 with at most 2^-22 of m: (K / 64 + 16) 2^-22 m.  Activations: in the
+      norm, one rounding as for gemm_bias_act
+"""
+import math
+
+import pytest
+import torch
+
+import block_reference as ref
+from gpu_helpers import load_library, require_gpu
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+TYPES = {"bf16": BF, "fp32": F32}
+
+
+@pytest.fixture(scope="module")
+def gbr():
+    require_gpu()
+    return load_library()
+
+
+def rng(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def normal(g, shape, std=1.0, dtype=BF):
+    return (torch.randn(shape, generator=g, device="cuda") * std).to(dtype)
+
+
+def odd(t):
+    """The same values as a view with odd strides and an odd start."""
+    if t is None:
+        return None
+    big = torch.full((t.shape[0], t.shape[1] + 8), float("nan"), device=t.device, dtype=t.dtype)
+    big[:, 3:3 + t.shape[1]] = t
+    return big[:, 3:3 + t.shape[1]]
+
+
+def within(got, want, slack, name=""):
+    assert got.shape == want.shape, name
+    bar = torch.finfo(got.dtype).eps / 2 * want.abs() + slack
+    err = (got.double() - want).abs()
+    assert torch.isfinite(got.double()).all(), name
+    worst = (err - bar).max().item() if err.numel() else 0.0
+    assert worst <= 0, "%s: %g over its bar" % (name, worst)
+
+
+# ------------------------------------------------------------ residual_norm
+NORM = [
+    # rows, cols, type, post, gates, pre, residual, scale
+    (1, 1, "bf16", True, 0, True, True, 1.0),
+    (1, 4096, "bf16", True, 1, True, True, 1.0),
+    (3, 31, "fp32", True, 3, True, True, 0.5),
+    (7, 256, "bf16", False, 0, True, False, 1.0),
+    (12, 257, "bf16", True, 4, False, True, -2.0),
+    (30, 1000, "fp32", False, 5, True, True, 0.25),
+    (301, 1000, "bf16", True, 7, True, True, 0.25),
+    (64, 2048, "bf16", True, 64, True, True, 1.0),
+    (65, 4095, "fp32", True, 1, True, True, 0.25),
+    (9, 4104, "fp32", True, 9, True, True, 1.0),
+    (1000, 96, "bf16", True, 250, True, True, 1.0),
+    (513, 4096, "bf16", True, 1, True, True, 0.25),
+    (40, 8192, "bf16", True, 2, True, True, 1.0),
+    (6, 8191, "fp32", True, 1, True, True, 1.0),
+    (5, 8200, "bf16", True, 5, True, True, 1.0),
+    (11, 16384, "fp32", True, 1, True, True, 1.0),
+    (4, 32768, "bf16", True, 0, True, True, 1.0),
+    (3, 32769, "bf16", True, 1, True, True, 0.5),
+    (2, 70000, "fp32", False, 2, True, True, 1.0),
+    (700, 8, "fp32", True, 1, True, True, 1.0),
+]
+NORM_IDS = ["-".join(map(str, c)) for c in NORM]
+EPS = 1e-6
+
+
+def norm_inputs(case, seed=1):
+    rows, cols, dt, post, gates, pre, residual, scale = case
+    g, t = rng(seed), TYPES[dt]
+    return dict(X=normal(g, (rows, cols), 1.5, t), R=normal(g, (rows, cols), 2.0, t) if residual else None,
+                post=1 + normal(g, (cols,), 0.2, F32) if post else None,
+                gate=normal(g, (gates, cols), 1.0, t) if gates else None, scale=scale,
+                pre=1 + normal(g, (cols,), 0.2, F32) if pre else None, eps=EPS)
+
+
+def check_norm(a, S, H):
+    s, h, m = ref.residual_norm(**a)
+    within(S, s, 2.0 ** -20 * m, "S")
+    assert (H is None) == (h is None)
+    if h is not None:
+        within(H, h, 2.0 ** -19 * (m * ref.root(s, a["eps"]) * a["pre"].double().abs() + h.abs()), "H")
+
+
+@pytest.mark.parametrize("case", NORM, ids=NORM_IDS)
+def test_residual_norm(gbr, case):
+    a = norm_inputs(case)
+    check_norm(a, *gbr.residual_norm(**a))
+    b = dict(a, X=odd(a["X"]), R=odd(a["R"]), gate=odd(a["gate"]))
+    check_norm(a, *gbr.residual_norm(**b))
+    gbr.check_device()
+
+
+def norm_grad_inputs(case, seed=2):
+    a = norm_inputs(case, seed)
+    g = rng(seed + 100)
+    R = a.pop("R")
+    a["S"] = normal(g, a["X"].shape, 2.0, a["X"].dtype)
+    a["dS"] = normal(g, a["X"].shape, 1.0, a["X"].dtype)
+    a["dH"] = normal(g, a["X"].shape, 1.0, a["X"].dtype) if a["pre"] is not None else None
+    return a
+
+
+NAMES = ("dX", "dR", "dpost", "dgate", "dpre")
+
+
+def check_norm_grads(a, grads, names=NAMES):
+    g, m = ref.residual_norm_backward(**a)
+    rows = len(a["dS"] if a["dS"] is not None else a["dH"])
+    for name, got in zip(NAMES, grads):
+        if name not in g or name not in names:
+            assert got is None, name
+            continue
+        sums = rows * 2.0 ** -24 if name in ("dpost", "dgate", "dpre") else 0.0
+        within(got, g[name], (2.0 ** -18 + sums) * m[name], name)
+
+
+@pytest.mark.parametrize("case", NORM, ids=NORM_IDS)
+def test_residual_norm_backward(gbr, case):
+    a = norm_grad_inputs(case)
+    grads = gbr.residual_norm_backward(**a)
+    check_norm_grads(a, grads)
+    b = dict(a, **{n: odd(a[n]) for n in ("dS", "dH", "X", "S", "gate")})
+    check_norm_grads(a, gbr.residual_norm_backward(**b))
+    # The same call gives the same bits.
+    for x, y in zip(grads, gbr.residual_norm_backward(**a)):
+        assert (x is None and y is None) or torch.equal(x, y)
+    gbr.check_device()
+
+
+@pytest.mark.parametrize("needs", [(True, False, False, False, False), (False, True, False, False, False),
+                                   (False, False, True, False, True), (False, False, False, True, False)])
+@pytest.mark.parametrize("case", [(33, 1000, "bf16", True, 11, True, True, 0.5), (20, 9000, "fp32", True, 1, True, True, 1.0)])
+def test_residual_norm_backward_needs(gbr, case, needs):
+    a = norm_grad_inputs(case)
+    grads = gbr.residual_norm_backward(**a, needs=needs)
+    check_norm_grads(a, grads, [n for n, w in zip(NAMES, needs) if w])
+    a["dS"] = None
+    check_norm_grads(a, gbr.residual_norm_backward(**a, needs=needs), [n for n, w in zip(NAMES, needs) if w])
+
+
+@pytest.mark.parametrize("gates", [0, 1, 5, 10])
+@pytest.mark.parametrize("post", [False, True])
+def test_residual_norm_backward_against_differences(gbr, gates, post):
+    """<gradient, direction> against central differences of the 64-bit forward pass, whose error in h = 1e-5 is far
+    below the gradients' 2^-18."""
+    a = norm_inputs((10, 72, "fp32", post, gates, True, True, 0.5), 5)
+    g = rng(6)
+    s, _, _ = ref.residual_norm(**a)
+    dS, dH = normal(g, s.shape, 1.0, F32), normal(g, s.shape, 1.0, F32)
+    grads = dict(zip(NAMES, gbr.residual_norm_backward(dS, dH, a["X"], s.float(), post=a["post"], gate=a["gate"],
+                                                       scale=a["scale"], pre=a["pre"], eps=EPS)))
+    for name in ("X", "R", "post", "gate", "pre"):
+        if a[name] is None:
+            continue
+        v, h = normal(g, a[name].shape, 1.0, F32).double(), 1e-5
+        loss = []
+        for sign in (1, -1):
+            S, H, _ = ref.residual_norm(**dict(a, **{name: a[name].double() + sign * h * v}))
+            loss.append((S * dS.double()).sum() + (H * dH.double()).sum())
+        want = (loss[0] - loss[1]).item() / (2 * h)
+        got = (grads["d" + name].double() * v).sum().item()
+        # S is rounded to 24 bits between the passes: another 2^-22 of every term.
+        size = (grads["d" + name].double() * v).abs().sum().item()
+        assert abs(got - want) <= 2.0 ** -16 * size + 1e-7 * size, name
+
+
+def test_residual_norm_plain_sum_and_norm_alone(gbr):
+    g = rng(3)
+    X, w = normal(g, (37, 520)), 1 + normal(g, (520,), 0.1, F32)
+    S, H = gbr.residual_norm(X, pre=w)
+    assert torch.equal(S, X)
+    check_norm(dict(X=X, R=None, post=None, gate=None, scale=1.0, pre=w, eps=1e-6), S, H)
+    S, H = gbr.residual_norm(X, X, scale=-1.0)
+    assert H is None and not S.any()
+
+
+def test_residual_norm_in_place(gbr):
+    for cols in (1000, 4096, 40000):
+        a = norm_inputs((9, cols, "bf16", True, 3, True, True, 0.5))
+        want = gbr.residual_norm(**a)
+        for S, H in (("R", "X"), ("X", "R"), ("R", None)):
+            b = dict(a, X=a["X"].clone(), R=a["R"].clone())
+            out = gbr.residual_norm(**b, S=b[S], H=b[H] if H else None)
+            assert out[0] is b[S] and torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+
+
+def test_residual_norm_special_values(gbr):
+    """A row of zeros stays zero; Inf and NaN spoil their own row alone."""
+    g = rng(4)
+    X, R, w = normal(g, (6, 300)), normal(g, (6, 300)), torch.ones(300, device="cuda")
+    X[1], R[1] = 0, 0
+    X[2, 7], X[4, 299] = float("inf"), float("nan")
+    S, H = gbr.residual_norm(X, R, post=w, pre=w)
+    assert not S[1].any() and not H[1].any()
+    good = [0, 3, 5]
+    check_norm(dict(X=X[good], R=R[good], post=w, gate=None, scale=1.0, pre=w, eps=1e-6), S[good], H[good])
+    assert torch.isnan(H[2]).any() and torch.isnan(S[4]).all()
+    dX = gbr.residual_norm_backward(R, R, X, R, post=w, pre=w)[0]
+    assert torch.isfinite(dX[good].float()).all() and torch.isnan(dX[4].float()).all()
+
+
+def test_residual_norm_empty(gbr):
+    w = torch.ones(64, device="cuda")
+    e = torch.empty(0, 64, device="cuda", dtype=BF)
+    S, H = gbr.residual_norm(e, e, post=w, pre=w)
+    assert S.shape == H.shape == (0, 64)
+    gate = torch.ones(1, 64, device="cuda", dtype=BF)
+    dX, dR, dpost, dgate, dpre = gbr.residual_norm_backward(e, e, e, e, post=w, gate=gate, pre=w)
+    assert dX.shape == dR.shape == (0, 64)
+    for t in (dpost, dgate, dpre):
+        assert t.numel() == 64 and not t.any()
+    n = torch.empty(5, 0, device="cuda", dtype=BF)
+    S, H = gbr.residual_norm(n, n, pre=w[:0])
+    assert S.shape == H.shape == (5, 0)
+
+
+# ------------------------------------------------------------ rows by expert
+SORT = [(0, 2, 4), (1, 1, 1), (1, 8, 8), (5, 3, 7), (100, 6, 64), (301, 6, 64), (1000, 8, 1024), (4096, 2, 8), (4097, 2, 8),
+        (9000, 1, 3), (16384, 8, 256), (70000, 4, 1000)]
+
+
+def choices(T, k, E, seed=1, masked=0.0):
+    g = rng(seed)
+    ids = torch.randint(0, E, (T, k), generator=g, device="cuda")
+    if masked:
+        ids[torch.rand((T, k), generator=g, device="cuda") < masked] = -1
+    return ids
+
+
+@pytest.mark.parametrize("T,k,E", SORT)
+@pytest.mark.parametrize("how", ["all", "some", "none", "one", "wild"])
+def test_moe_sort(gbr, T, k, E, how):
+    ids = choices(T, k, E, masked={"some": 0.3, "none": 1.1}.get(how, 0.0))
+    if how == "one":
+        ids.fill_(E - 1)
+    if how == "wild":
+        ids = ids * 3 - E
+        if T:
+            ids[0, 0], ids[-1, -1] = 2 ** 40, -2 ** 63
+    positions, offsets = gbr.moe_sort(ids, E)
+    p, o = ref.moe_sort(ids.cpu(), E)
+    assert torch.equal(positions.cpu(), p) and torch.equal(offsets.cpu(), o)
+    assert positions.dtype == offsets.dtype == torch.int32
+
+
+ROWS = [
+    # T, k, D, E, type, masked
+    (1, 1, 1, 1, "bf16", 0.0), (1, 2, 4096, 8, "bf16", 0.0), (5, 3, 7, 4, "fp32", 0.5), (100, 6, 2048, 64, "bf16", 0.0),
+    (301, 6, 1000, 64, "bf16", 0.25), (300, 2, 1001, 8, "bf16", 0.0), (64, 8, 260, 16, "fp32", 0.25), (33, 9, 64, 16, "bf16", 0.0),
+    (17, 4, 8200, 4, "bf16", 0.5), (700, 1, 36, 3, "fp32", 0.9), (19, 2, 4100, 5, "fp32", 1.1), (3000, 2, 512, 8, "bf16", 0.1),
+]
+
+
+def row_inputs(case, seed=3):
+    T, k, D, E, dt, masked = case
+    g, t = rng(seed), TYPES[dt]
+    ids = choices(T, k, E, seed, masked)
+    p, o = ref.moe_sort(ids.cpu(), E)
+    return dict(X=normal(g, (T, D), 1.0, t), Ys=normal(g, (T * k, D), 1.0, t), dY=normal(g, (T, D), 1.0, t),
+                R=normal(g, (T, D), 1.0, t), w=torch.rand((T, k), generator=g, device="cuda"), p=p.cuda(), o=o.cuda())
+
+
+def picked(a):
+    """The choices' rows [T, k, D] and weights, zero where struck out."""
+    on = a["p"] >= 0
+    return a["Ys"].double()[a["p"].clamp(min=0).long()] * on[..., None], a["w"].double() * on
+
+
+@pytest.mark.parametrize("case", ROWS, ids=["-".join(map(str, c)) for c in ROWS])
+def test_moe_rows(gbr, case):
+    a = row_inputs(case)
+    T, k, D = case[:3]
+    on = a["p"].flatten() >= 0
+    at, token = a["p"].flatten()[on].long(), torch.arange(T, device="cuda").repeat_interleave(k)[on]
+    for f in (lambda t: t, odd):
+        Xs = gbr.moe_dispatch(f(a["X"]), a["p"], a["o"])
+        want = torch.zeros_like(a["Ys"])
+        want[at] = a["X"][token]
+        assert torch.equal(Xs, want)
+        rows, w = picked(a)
+        for weights, residual in ((a["w"], a["R"]), (a["w"], None), (None, None)):
+            y = gbr.moe_combine(f(a["Ys"]), a["p"], weights, residual=f(residual) if residual is not None else None)
+            ww = w if weights is not None else (a["p"] >= 0).double()
+            r = residual.double() if residual is not None else torch.zeros(T, D, device="cuda", dtype=torch.float64)
+            m = (ww[..., None] * rows).abs().sum(1) + r.abs()
+            within(y, (ww[..., None] * rows).sum(1) + r, (k + 2) * 2.0 ** -23 * m, "Y")
+        dYs, dw = gbr.moe_combine_backward(f(a["dY"]), f(a["Ys"]), a["p"], a["o"], a["w"])
+        want = torch.zeros(T * k, D, device="cuda", dtype=torch.float64)
+        want[at] = (a["w"].double()[..., None] * a["dY"].double()[:, None]).flatten(0, 1)[on]
+        within(dYs, want, 2.0 ** -23 * want.abs(), "dYs")
+        prod = rows * a["dY"].double()[:, None]
+        within(dw, prod.sum(2), 2.0 ** -17 * prod.abs().sum(2), "dweights")
+    gbr.check_device()
+
+
+def test_moe_rows_needs_and_in_place(gbr):
+    a = row_inputs((50, 3, 520, 8, "bf16", 0.2))
+    dYs, dw = gbr.moe_combine_backward(a["dY"], a["Ys"], a["p"], a["o"], a["w"])
+    x, none = gbr.moe_combine_backward(a["dY"], None, a["p"], a["o"], a["w"], needs=(True, False))
+    assert none is None and torch.equal(x, dYs)
+    none, y = gbr.moe_combine_backward(a["dY"], a["Ys"], a["p"], a["o"], a["w"], needs=(False, True))
+    assert none is None and torch.equal(y, dw)
+    want = gbr.moe_combine(a["Ys"], a["p"], a["w"], residual=a["R"])
+    R = a["R"].clone()
+    assert gbr.moe_combine(a["Ys"], a["p"], a["w"], residual=R, Y=R) is R and torch.equal(R, want)
+
+
+def test_moe_struck_out_choices_count_nothing(gbr):
+    """Not even with Inf or NaN as weight, and rows that nobody has are not read."""
+    a = row_inputs((40, 4, 264, 8, "fp32", 0.4))
+    off = a["p"] < 0
+    want = gbr.moe_combine(a["Ys"], a["p"], a["w"])
+    grads = gbr.moe_combine_backward(a["dY"], a["Ys"], a["p"], a["o"], a["w"])
+    a["w"][off] = float("nan")
+    a["Ys"][int(a["o"][-1]):] = float("inf")
+    assert torch.equal(gbr.moe_combine(a["Ys"], a["p"], a["w"]), want)
+    for x, y in zip(gbr.moe_combine_backward(a["dY"], a["Ys"], a["p"], a["o"], a["w"]), grads):
+        assert torch.equal(x, y)
+    assert not grads[1][off].any()
+
+
+def test_moe_positions_outside_are_struck_out(gbr):
+    """As with a shortened Ys: nothing out of range is read or written."""
+    a = row_inputs((20, 3, 72, 4, "bf16", 0.0))
+    short = a["Ys"][:25]
+    p = torch.where(a["p"] < 25, a["p"], torch.full_like(a["p"], -1))
+    assert torch.equal(gbr.moe_combine(short, a["p"], a["w"]), gbr.moe_combine(short, p, a["w"]))
+    wild = a["p"].clone()
+    wild[3, 1], wild[4, 2] = 60, 2 ** 31 - 1
+    Xs = gbr.moe_dispatch(a["X"], wild, a["o"], Xs=torch.zeros_like(a["Ys"]))
+    kept = (wild >= 0) & (wild < 60)
+    want = torch.zeros_like(a["Ys"])
+    want[wild[kept].long()] = a["X"][torch.arange(20, device="cuda")[:, None].expand(20, 3)[kept]]
+    assert torch.equal(Xs, want)
+
+
+def test_moe_rows_empty(gbr):
+    p, o = gbr.moe_sort(torch.empty(0, 3, device="cuda", dtype=torch.long), 5)
+    assert p.shape == (0, 3) and not o.any()
+    e = torch.empty(0, 16, device="cuda")
+    assert gbr.moe_dispatch(e, p, o).shape == (0, 16)
+    assert gbr.moe_combine(e, p, torch.empty(0, 3, device="cuda")).shape == (0, 16)
+    R = torch.randn(4, 16, device="cuda")
+    p = torch.empty(4, 0, device="cuda", dtype=torch.int32)
+    assert torch.equal(gbr.moe_combine(e, p, residual=R), R)
+    p = torch.full((4, 2), -1, device="cuda", dtype=torch.int32)
+    assert torch.equal(gbr.moe_combine(e, p, residual=R), R)
+
+
+# ------------------------------------------------------------ 4 bits
+def check_quantized(Q, X):
+    rows, cols = X.shape
+    want, e = ref.quantize(X)
+    blocks = -(-cols // 32)
+    assert Q.data.shape == (rows, blocks * 16) and Q.columns == cols
+    assert Q.scales.shape == (-(-rows // 128), -(-cols // 128), 512)
+    assert torch.equal(ref.scale_bytes(Q.scales, rows, blocks).long(), e + 127)
+    got = ref.values(Q)
+    assert torch.equal(torch.nan_to_num(got, 1e300), torch.nan_to_num(want, 1e300))
+    # Padding: zeros in the last block's rest and in the tiles' unused places.
+    if cols % 32 and torch.isfinite(X.double()).all():
+        rest = ref.values(Q._replace(columns=blocks * 32))[:, cols:]
+        assert not rest.any()
+    used = torch.zeros_like(Q.scales)
+    n, b = torch.arange(rows, device="cuda")[:, None], torch.arange(blocks, device="cuda")[None]
+    used[n // 128, b // 4, n % 32 * 16 + n % 128 // 32 * 4 + b % 4] = 1
+    assert not Q.scales[used == 0].any()
+
+
+QUANT = [(1, 1), (1, 32), (3, 33), (5, 64), (37, 4096), (128, 128), (129, 160), (130, 1000), (257, 2056), (300, 97)]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("rows,cols", QUANT)
+def test_quantize(gbr, rows, cols, dt):
+    g = rng(rows + cols)
+    X = normal(g, (rows, cols), 1.0, F32) * torch.exp2(torch.randint(-20, 20, (rows, 1), generator=g, device="cuda").float())
+    X = X.to(TYPES[dt])
+    for f in (lambda t: t, odd):
+        Q = gbr.quantize_mxfp4(f(X))
+        check_quantized(Q, X)
+        back = gbr.dequantize_mxfp4(Q, dtype=TYPES[dt])
+        assert torch.equal(back.double(), ref.values(Q))
+        out = f(torch.empty_like(X))
+        assert gbr.dequantize_mxfp4(Q, X=out) is out and torch.equal(out, back)
+        T = gbr.quantize_mxfp4(f(X.t().contiguous()), transposed=True)
+        assert torch.equal(T.data & 0x77, Q.data & 0x77) and torch.equal(T.scales, Q.scales)
+        check_quantized(T, X)
+    again = gbr.quantize_mxfp4(X, out=gbr.Mxfp4(torch.full_like(Q.data, 255), torch.full_like(Q.scales, 255), cols))
+    assert torch.equal(again.data, gbr.quantize_mxfp4(X).data) and torch.equal(again.scales, Q.scales)
+
+
+def test_quantize_every_bf16_and_ties(gbr):
+    """All bf16 values in blocks with others of their size, ties, blocks of zeros, the ends of the range."""
+    bits = torch.arange(65536, device="cuda", dtype=torch.int32).to(torch.int16).view(BF)
+    order = torch.argsort(torch.where(torch.isfinite(bits.float()), bits.float().abs(), torch.full_like(bits, 3e38).float()))
+    X = bits[order][torch.isfinite(bits[order].float())]
+    X = X[:len(X) // 32 * 32].view(-1, 32).contiguous()
+    check_quantized(gbr.quantize_mxfp4(X), X)
+    ties = torch.tensor([0.0, 0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0, 6.9, 7.96, 0.2, 0.3, -0.25, -5.0, -0.0],
+                        device="cuda").repeat(2)
+    X = torch.stack([ties * 2.0 ** e for e in (-130, -126, -125, -100, -1, 0, 1, 60, 124)])
+    X[:, 16] = 4.0 * torch.tensor([2.0 ** e for e in (-130, -126, -125, -100, -1, 0, 1, 60, 124)], device="cuda")
+    check_quantized(gbr.quantize_mxfp4(X), X)
+    X = torch.zeros(4, 64, device="cuda")
+    X[1, 3], X[2, 40], X[3, 5] = float("inf"), float("nan"), 3e38
+    Q = gbr.quantize_mxfp4(X)
+    check_quantized(Q, X)
+    assert torch.isnan(gbr.dequantize_mxfp4(Q)[1, :32].float()).all()
+
+
+GEMM = [
+    # M, N, K, bias, residual
+    (1, 1, 1, True, True), (1, 4096, 4096, True, True), (2, 130, 33, False, False), (16, 128, 256, True, False),
+    (17, 200, 320, True, True), (37, 1000, 1000, True, False), (48, 264, 544, False, True), (64, 4095, 512, True, True),
+    (128, 512, 4096, False, False), (130, 384, 96, True, False), (200, 256, 2080, True, True), (257, 300, 288, True, True),
+    (300, 1024, 14336, True, False), (500, 40, 64, True, True), (1024, 1024, 1024, True, True), (1000, 2000, 3000, True, True),
+    (2049, 2056, 1056, False, True), (2048, 4096, 64, True, False), (2500, 2501, 500, True, True), (4096, 2048, 4128, False, False),
+]
+
+
+def gemm_inputs(gbr, M, N, K, seed=1):
+    g = rng(seed)
+    A = normal(g, (M, K), 1.0, F32) * torch.exp2(torch.randint(-6, 6, (M, 1), generator=g, device="cuda").float())
+    B = normal(g, (N, K), max(K, 1) ** -0.5, F32) * torch.exp2(torch.randint(-3, 3, (N, 1), generator=g, device="cuda").float())
+    # Blocks of different sizes along K.
+    A *= torch.exp2((torch.arange(K, device="cuda") // 32 % 5 - 2).float())
+    B *= torch.exp2((torch.arange(K, device="cuda") // 32 % 7 - 3).float())
+    return gbr.quantize_mxfp4(A), gbr.quantize_mxfp4(B), normal(g, (N,), 1.0, F32), normal(g, (M, N))
+
+
+def gemm_bar(a, b, K):
+    return (K / 64 + 16) * 2.0 ** -22 * (a.abs() @ b.abs().t())
+
+
+@pytest.mark.parametrize("M,N,K,bias,residual", GEMM)
+def test_gemm(gbr, M, N, K, bias, residual):
+    A, B, b, R = gemm_inputs(gbr, M, N, K)
+    b, R = b if bias else None, R if residual else None
+    C = gbr.gemm_mxfp4(A, B, b, residual=R)
+    gbr.check_device()
+    x, y = ref.values(A), ref.values(B)
+    want, bar = ref.linear(x, y, b, R, "none"), gemm_bar(x, y, K)
+    m = (b.double().abs() if bias else 0) + (R.double().abs() if residual else 0)
+    within(C, want, bar + 2.0 ** -22 * (m + want.abs()), "C")
+    # Any stride, and the residual itself as the output.
+    out = odd(torch.empty_like(C))
+    assert torch.equal(gbr.gemm_mxfp4(A, B, b, residual=odd(R), C=out), C)
+    if residual:
+        R2 = R.clone()
+        assert gbr.gemm_mxfp4(A, B, b, residual=R2, C=R2) is R2 and torch.equal(R2, C)
+    gbr.check_device()
+
+
+@pytest.mark.parametrize("act", ["relu", "gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("M,N,K", [(5, 300, 200), (1500, 1600, 320)])
+def test_gemm_activations(gbr, M, N, K, act):
+    A, B, b, R = gemm_inputs(gbr, M, N, K)
+    C = gbr.gemm_mxfp4(A, B, b, residual=R, act=act)
+    want = ref.linear(ref.values(A), ref.values(B), b, R, act)
+    assert (C.double() - want).norm() <= 1.0625 * 2.0 ** -9 * want.norm()
+
+
+def test_gemm_no_contraction_and_empty(gbr):
+    A, B, b, R = gemm_inputs(gbr, 5, 40, 0)
+    assert torch.equal(gbr.gemm_mxfp4(A, B, b, residual=None), b.to(BF).expand(5, 40))
+    A, B, b, R = gemm_inputs(gbr, 0, 40, 64)
+    assert gbr.gemm_mxfp4(A, B, b).shape == (0, 40)
+    A, B, b, R = gemm_inputs(gbr, 5, 0, 64)
+    assert gbr.gemm_mxfp4(A, B, b).shape == (5, 0)
+
+
+@pytest.mark.parametrize("M,N,K", [(20, 200, 512), (1500, 1600, 512)])
+def test_gemm_nan_blocks_stay_in_their_rows(gbr, M, N, K):
+    g = rng(7)
+    X, W = normal(g, (M, K)), normal(g, (N, K))
+    X[3, 40], W[130, 500] = float("nan"), float("inf")
+    C = gbr.gemm_mxfp4(gbr.quantize_mxfp4(X), gbr.quantize_mxfp4(W))
+    bad = torch.zeros(M, N, dtype=torch.bool, device="cuda")
+    bad[3], bad[:, 130] = True, True
+    assert torch.equal(torch.isnan(C), bad)
+
+
+# ------------------------------------------------------------ all of them
+def calls(gbr):
+    """Every operator, as functions of the stream that return their outputs."""
+    g = rng(9)
+    a = norm_inputs((64, 1000, "bf16", True, 8, True, True, 0.5))
+    d = norm_grad_inputs((64, 1000, "bf16", True, 8, True, True, 0.5))
+    long = norm_grad_inputs((8, 9000, "bf16", True, 1, True, True, 0.5))
+    r = row_inputs((64, 3, 520, 8, "bf16", 0.2))
+    ids, X = choices(9000, 2, 16), normal(g, (300, 1000), 1.0, F32)
+    small, large = gemm_inputs(gbr, 20, 300, 1000), gemm_inputs(gbr, 1500, 1600, 320)
+    return [
+        lambda s: list(gbr.residual_norm(**a, stream=s)),
+        lambda s: list(gbr.residual_norm_backward(**d, stream=s)),
+        lambda s: list(gbr.residual_norm_backward(**long, stream=s))[:3],
+        lambda s: list(gbr.moe_sort(ids, 16, stream=s)),
+        lambda s: [gbr.moe_dispatch(r["X"], r["p"], r["o"], stream=s)],
+        lambda s: [gbr.moe_combine(r["Ys"], r["p"], r["w"], residual=r["R"], stream=s)],
+        lambda s: list(gbr.moe_combine_backward(r["dY"], r["Ys"], r["p"], r["o"], r["w"], stream=s)),
+        lambda s: list(gbr.quantize_mxfp4(X, stream=s))[:2],
+        lambda s: [gbr.dequantize_mxfp4(small[0], stream=s)],
+        lambda s: [gbr.gemm_mxfp4(*small[:3], residual=small[3], stream=s)],
+        lambda s: [gbr.gemm_mxfp4(*large[:3], residual=large[3], act="gelu", stream=s)],
+    ]
+
+
+def test_streams(gbr):
+    from test_gpu_operator_streams import owner
+    side = torch.cuda.Stream()
+    for call in calls(gbr):
+        want = call(None)
+        torch.cuda.synchronize()
+        got = call(side)
+        side.synchronize()
+        for x, y in zip(got, want):
+            assert torch.equal(x, y)
+            assert owner(x) == side.cuda_stream and owner(y) == torch.cuda.current_stream().cuda_stream
+    gbr.check_device()
+
+
+def test_captured_together_and_replayed(gbr):
+    """Two graphs of all operators, replayed on two streams at once."""
+    every = calls(gbr)
+    want = [f(None) for f in every]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append([f(None) for f in every])
+        graphs.append(graph)
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(3):
+        for out in outs:
+            for call in out:
+                for t in call:
+                    t.fill_(1)
+        torch.cuda.synchronize()
+        for graph, stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                graph.replay()
+        torch.cuda.synchronize()
+        for out in outs:
+            for call, expected in zip(out, want):
+                for x, y in zip(call, expected):
+                    assert torch.equal(x, y)
+    gbr.check_device()
+
+
+def test_two_streams_at_once(gbr):
+    every = calls(gbr)
+    want = [f(None) for f in every]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got = []
+    for i in range(9):
+        for j, f in enumerate(every):
+            got.append((j, f(streams[(i + j) % 3])))
+    torch.cuda.synchronize()
+    for j, out in got:
+        for x, y in zip(out, want[j]):
+            assert torch.equal(x, y)
+    gbr.check_device()
+
+
+def test_written_tensors_move_their_version(gbr):
+    r = row_inputs((8, 2, 64, 4, "bf16", 0.0))
+    Y = torch.empty_like(r["X"])
+    v = Y._version
+    gbr.moe_combine(r["Ys"], r["p"], r["w"], Y=Y)
+    assert Y._version > v
+    S = torch.empty_like(r["X"])
+    gbr.residual_norm(r["X"], r["R"], S=S)
+    assert S._version > 0
+
+
+def test_a_stage_that_is_never_filled(gbr):
+    for M, N, K in ((20, 300, 4096), (1500, 1600, 4096)):
+        A, B, _, _ = gemm_inputs(gbr, M, N, K)
+        want = gbr.gemm_mxfp4(A, B)
+        gbr.selftest_mxfp4_skip_load(A, B, 0, 1, 20_000_000)
+        with pytest.raises(gbr.GbrError):
+            gbr.check_device()
+        assert torch.equal(gbr.gemm_mxfp4(A, B), want)
+        gbr.check_device()
