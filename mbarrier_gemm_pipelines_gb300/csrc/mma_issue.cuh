@@ -48,4 +48,40 @@ __device__ __forceinline__ void mma_slice(uint32_t d, uint32_t a_lo, uint32_t b_
         : "memory");
 }
 
+// A stage of microscaled 4-bit operands (256 values of a row): the scales' copies into Tensor Memory and four MMAs of
+// K = 64.  At s_lo lies 1 KiB for the 128 rows of A, then 1 KiB for each of
+// N_TILES times 128 rows of B, each two tiles of 512 bytes (4 blocks); they go to 8 columns from sfa and 8 N_TILES from
+// sfb, those of the first 4 blocks first.
+template <int PAIR, int N_TILES>
+__device__ __forceinline__ void mx_copy_scales(uint32_t s_lo, uint32_t s_hi, uint32_t sfa, uint32_t sfb) {
+    auto copy = [&](uint32_t to, uint32_t from) {
+        const uint64_t desc = uint64_t(from) | (uint64_t(s_hi) << 32);
+        if (PAIR == 2) ptx::tmem_copy_32x128b_pair(to, desc);
+        else ptx::tmem_copy_32x128b(to, desc);
+    };
+#pragma unroll
+    for (uint32_t h = 0; h < 2; ++h) {
+        copy(sfa + h * 4u, s_lo + h * 32u);
+#pragma unroll
+        for (uint32_t r = 0; r < uint32_t(N_TILES); ++r)
+            copy(sfb + (h * N_TILES + r) * 4u, s_lo + 64u * (1u + r) + h * 32u);
+    }
+}
+
+// `steps` (1 to 4) of the MMAs; idesc0 and idesc1 name the first and the second two of four blocks.
+template <int PAIR, int N_TILES>
+__device__ __forceinline__ void mx_mmas(int32_t steps, uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t sfa,
+                                        uint32_t sfb, uint32_t idesc0, uint32_t idesc1, uint32_t accumulate) {
+#pragma unroll
+    for (uint32_t k = 0; k < 4; ++k) {
+        if (int32_t(k) >= steps) break;
+        const uint64_t a = uint64_t(a_lo + kStepK * k) | (uint64_t(hi) << 32);
+        const uint64_t b = uint64_t(b_lo + kStepK * k) | (uint64_t(hi) << 32);
+        const uint32_t fa = sfa + k / 2u * 4u, fb = sfb + k / 2u * (4u * N_TILES), id = k % 2u ? idesc1 : idesc0;
+        const uint32_t acc = k == 0 ? accumulate : 1u;
+        if (PAIR == 2) ptx::mma_mxf4_pair(d, a, b, id, fa, fb, acc);
+        else ptx::mma_mxf4(d, a, b, id, fa, fb, acc);
+    }
+}
+
 }  // namespace gbr

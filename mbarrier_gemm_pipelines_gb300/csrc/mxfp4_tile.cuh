@@ -10,9 +10,9 @@
 //
 // Stage: 128 columns of B (16 KiB), BT rows of A (BT x 128 bytes), the scales of
 // both (1 KiB for 128 rows and 8 blocks).  The MMA's thread copies the scales to
-// Tensor Memory in front of the stage's MMAs; the tensor core runs both in
-// order.  Two sets of columns alternate, so that a copy need not wait for the
-// MMAs before it.
+// Tensor Memory; the tensor core runs copies and MMAs in order.  Two sets of
+// columns alternate, and a stage's copies are issued in front of the MMAs of the
+// stage before, so that neither waits for the other.
 #pragma once
 #include "linear_tile.cuh"
 #include "mxfp4.cuh"
@@ -54,10 +54,9 @@ __host__ __device__ constexpr size_t tile_smem_bytes(int32_t bt, int32_t stages)
     return need > least ? need : least;
 }
 
-// 512 bytes of scales in shared memory: 32 rows of 16 bytes, groups of 8 rows 128 bytes apart, no swizzle.
-__device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) {
-    return uint64_t((saddr >> 4) & 0x3FFFu) | (uint64_t(128u >> 4) << 32) | (uint64_t(1) << 46);
-}
+// High word of the matrix descriptor of 512 bytes of scales in shared memory: 32 rows of 16 bytes, groups of 8 rows
+// 128 bytes apart, no swizzle (bit layout: see sw128_desc in gemm_umma.cuh).
+constexpr uint32_t kScaleDescHi = (128u >> 4) | (1u << 14);
 // fp32 += e2m1 x e2m1 with E8M0 scales; `m` and `n` the MMA's shape, `pair` (0 or 1) which two of four scale bytes.
 __host__ __device__ constexpr uint32_t mx_idesc(uint32_t m, uint32_t n, uint32_t pair) {
     return (pair * 2u << 4) | (1u << 7) | (1u << 10) | ((n >> 3) << 17) | (1u << 23) | ((m >> 4) << 24) |
@@ -75,7 +74,7 @@ __global__ void __launch_bounds__(kTileThreads) mxfp4_tile_kernel(const __grid_c
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
     uint8_t* ring = align_1024(reinterpret_cast<uint8_t*>(full) + kTileBarBytes);
 
-    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u;
+    const uint32_t warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31u;
     const uint32_t S = uint32_t(P.split), stages = uint32_t(P.stages);
     const uint32_t tile = blockIdx.x / S, rank = blockIdx.x % S;
     const int32_t i0 = int32_t(tile % uint32_t(P.t_tiles)) * P.bt, j0 = int32_t(tile / uint32_t(P.t_tiles)) * 128;
@@ -104,7 +103,7 @@ __global__ void __launch_bounds__(kTileThreads) mxfp4_tile_kernel(const __grid_c
     ptx::tc_fence_before_sync();
     __syncthreads();
     ptx::tc_fence_after_sync();
-    const uint32_t tmem = *tmem_holder;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_holder, 0);
     const uint32_t ring_base = ptx::smem_addr(ring);
     ptx::griddep_wait();
 
@@ -129,38 +128,44 @@ __global__ void __launch_bounds__(kTileThreads) mxfp4_tile_kernel(const __grid_c
             }
         }
         ptx::griddep_launch_dependents();
-    } else if (warp == 5 && lane == 0) {
+    } else if (warp == 5) {
         const uint32_t idesc0 = mx_idesc(128, uint32_t(P.bt), 0), idesc1 = mx_idesc(128, uint32_t(P.bt), 1);
-        const uint32_t sf = tmem + tile_scale_col(P.bt);
+        constexpr uint32_t hi = desc_hi(1024), s_hi = kScaleDescHi;
+        const uint32_t w_first = desc_lo(ring_base, 16), x_first = desc_lo(ring_base + kWideBytes, 16);
+        const uint32_t s_first = desc_lo(ring_base + kWideBytes + uint32_t(P.bt) * 128u, 0);
+        const uint32_t sf = tmem + tile_scale_col(P.bt), set = 8u * (1u + row_tiles), count = uint32_t(ks1 - ks0);
         const uint32_t x_col = uint32_t(i0 % 128) / 32u;   // a tile may start inside 128 rows, at a multiple of 32
-        uint32_t slot = 0, ph = 0, it = 0;
-        for (int32_t ks = ks0; ks < ks1; ++ks, ++it) {
-            if (!mbar_wait(ptx::smem_addr(full + slot), ph, P.ctl, abort_flag, kSiteMmaFull, it)) break;
+        auto copy_scales = [&](uint32_t slot, uint32_t it) {
+            const uint32_t from = s_first + slot * (stage_bytes / 16), to = sf + (it & 1u) * set;
+            if (row_tiles == 2) mx_copy_scales<1, 2>(from, s_hi, to, to + 8u);
+            else mx_copy_scales<1, 1>(from, s_hi, to, to + 8u);
+        };
+        uint32_t slot = 0, ph = 0, copied = 0;
+        for (uint32_t it = 0; it < count; ++it) {
+            const bool wait = copied == it;
+            if (wait && !mbar_wait_warp(ptx::smem_addr(full + slot), ph, P.ctl, abort_flag, kSiteMmaFull, it)) break;
+            // The next stage's scales, if it is there, in front of this one's MMAs.
+            const uint32_t next = slot + 1 == stages ? 0 : slot + 1, next_ph = next == 0 ? ph ^ 1u : ph;
+            const bool ahead =
+                it + 1 < count && __all_sync(0xffffffffu, mbar_test<false>(ptx::smem_addr(full + next), next_ph));
             ptx::tc_fence_after_sync();
-            const uint32_t w = ring_base + slot * stage_bytes, x = w + kWideBytes, scales = x + uint32_t(P.bt) * 128u;
-            const uint32_t sfw = sf + (it & 1u) * 8u * (1u + row_tiles), sfx = sfw + 8u;
-            // Pairs of blocks that the matrix has.
-            const int32_t steps = min(4, (Q.blocks - ks * 8 + 1) / 2);
-            for (uint32_t h = 0; h < 2; ++h) {
-                ptx::tmem_copy_32x128b(sfw + h * 4u, scale_desc(scales + h * kMxTileBytes));
-                for (uint32_t r = 0; r < row_tiles; ++r)
-                    ptx::tmem_copy_32x128b(sfx + (h * row_tiles + r) * 4u,
-                                           scale_desc(scales + kScaleBytes * (1u + r) + h * kMxTileBytes));
+            if (ptx::elect_one()) {
+                const uint32_t at = slot * (stage_bytes / 16), sfw = sf + (it & 1u) * set, sfx = sfw + 8u + x_col;
+                // Pairs of blocks that the matrix has.
+                const int32_t steps = min(4, (Q.blocks - (ks0 + int32_t(it)) * 8 + 1) / 2);
+                if (wait) copy_scales(slot, it);
+                if (ahead) copy_scales(next, it + 1);
+                if (row_tiles == 2) mx_mmas<1, 2>(steps, tmem, w_first + at, x_first + at, hi, sfw, sfx, idesc0, idesc1, it);
+                else mx_mmas<1, 1>(steps, tmem, w_first + at, x_first + at, hi, sfw, sfx, idesc0, idesc1, it);
+                ptx::mma_commit(ptx::smem_addr(empty + slot));
             }
-            for (int32_t k = 0; k < steps; ++k) {
-                const uint32_t h = uint32_t(k) / 2u;
-                ptx::mma_mxf4(tmem, umma::sw128_desc(w + uint32_t(k) * 32u, 16, 1024),
-                              umma::sw128_desc(x + uint32_t(k) * 32u, 16, 1024), k % 2 ? idesc1 : idesc0, sfw + h * 4u,
-                              sfx + h * row_tiles * 4u + x_col, it != 0 || k != 0 ? 1u : 0u);
-            }
-            ptx::mma_commit(ptx::smem_addr(empty + slot));
-            if (++slot == stages) {
-                slot = 0;
-                ph ^= 1u;
-            }
+            __syncwarp();
+            copied = it + (ahead ? 2u : 1u);
+            slot = next;
+            ph = next_ph;
         }
         // Completes when every MMA issued has: also what the exit path waits for.
-        ptx::mma_commit(ptx::smem_addr(acc_full));
+        if (ptx::elect_one()) ptx::mma_commit(ptx::smem_addr(acc_full));
     }
     __syncwarp();
 
