@@ -101,6 +101,104 @@ __global__ void __launch_bounds__(1024) residual_norm_kernel(const Args<T> a, in
     }
 }
 
+// Many rows: CTAs that stay, a row at a time (blockDim.x = tpr threads), the weights in registers and the next
+// kAhead rows' X, R and gate on their way into shared memory, each thread its own 16 bytes, so that nobody waits for
+// another's copy.  A gate per channel is in registers as well.  `step`: bytes of one row of all inputs.
+template <typename T, int V, int kAhead, int kMost>
+__global__ void __launch_bounds__(kMost, kMost == 256 ? 3 : 1) residual_norm_stream_kernel(const Args<T> a, uint32_t row_bytes,
+                                                                                       uint32_t step) {
+    extern __shared__ __align__(16) uint8_t ring[];
+    __shared__ float buf[2][1][32];
+    ptx::griddep_wait();
+    const int32_t t = int32_t(threadIdx.x), tpr = int32_t(blockDim.x), cols = a.cols;
+    const bool has_r = a.R != nullptr, one_gate = a.G != nullptr && a.per_gate == a.rows, gates = a.G != nullptr && !one_gate;
+    const uint32_t base = ptx::smem_addr(ring);
+    auto fetch = [&](int64_t row, uint32_t slot) {
+        if (row < a.rows) {
+            uint32_t to = base + slot * step;
+#pragma unroll
+            for (int v = 0; v < V; ++v) copy_row8(to, a.X + row * a.ldx, v, t, tpr, cols);
+            if (has_r) {
+                to += row_bytes;
+#pragma unroll
+                for (int v = 0; v < V; ++v) copy_row8(to, a.R + row * a.ldr, v, t, tpr, cols);
+            }
+            if (gates) {
+                to += row_bytes;
+#pragma unroll
+                for (int v = 0; v < V; ++v) copy_row8(to, a.G + row / a.per_gate * a.ldg, v, t, tpr, cols);
+            }
+        }
+        copy_async_commit();
+    };
+    float wpost[V][8], wpre[V][8];
+    Raw8<T> g[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        if (a.post != nullptr) load_row8<float, true>(wpost[v], a.post, v, t, tpr, cols);
+        if (a.pre != nullptr) load_row8<float, true>(wpre[v], a.pre, v, t, tpr, cols);
+        if (one_gate) load_raw8<true>(g[v], a.G, v, t, tpr, cols);
+    }
+    int64_t row = blockIdx.x;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) fetch(row + int64_t(i) * gridDim.x, uint32_t(i));
+    for (uint32_t slot = 0; row < a.rows; row += gridDim.x, slot = slot + 1 == kAhead ? 0 : slot + 1) {
+        copy_async_wait<kAhead - 1>();
+        const uint32_t from = base + slot * step;
+        Raw8<T> x[V], r[V] = {};
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            take_row8(x[v], from, v, t, tpr, cols);
+            if (has_r) take_row8(r[v], from + row_bytes, v, t, tpr, cols);
+            if (gates) take_row8(g[v], from + (has_r ? 2u : 1u) * row_bytes, v, t, tpr, cols);
+        }
+        float s[V][8], q = 1.f;
+        if (a.post != nullptr) {
+            float sum[1] = {};
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum[0] = fmaf(raw_at(x[v], j), raw_at(x[v], j), sum[0]);
+            group_sum(sum, buf[0], tpr);
+            q = root(sum[0], a.inv_cols, a.eps);
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float y = raw_at(x[v], j);
+                if (a.post != nullptr) y = y * q * wpost[v][j];
+                if (a.G != nullptr) y *= raw_at(g[v], j);
+                s[v][j] = fmaf(a.scale, y, raw_at(r[v], j));
+            }
+        if (a.S != nullptr)
+#pragma unroll
+            for (int v = 0; v < V; ++v) store_row8<T, true>(a.S + row * a.lds, s[v], v, t, tpr, cols);
+        float sum[1] = {};
+        if (a.H != nullptr) {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum[0] = fmaf(s[v][j], s[v][j], sum[0]);
+            group_sum(sum, buf[1], tpr);
+        }
+        // The slot has been read into registers that the lines above have used.
+        fetch(row + int64_t(kAhead) * gridDim.x, slot);
+        if (a.H != nullptr) {
+            const float p = root(sum[0], a.inv_cols, a.eps);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                float h[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) h[j] = s[v][j] * p * wpre[v][j];
+                store_row8<T, true>(a.H + row * a.ldh, h, v, t, tpr, cols);
+            }
+        }
+        if (a.post == nullptr || a.H == nullptr) __syncthreads();   // buf, for the next row
+    }
+    copy_async_wait<0>();
+}
+
 // Rows that no CTA can hold: a CTA a row, read again for each mean.
 template <typename T>
 __device__ __forceinline__ float sum_at(const Args<T>& a, int64_t row, float q, int32_t c) {
@@ -161,12 +259,39 @@ struct GradArgs {
     bool want_post, want_pre, want_gate;
 };
 
+// The rows of a CTA's items, `groups` at a time.
+template <typename T>
+struct RowWalk {
+    int32_t item, last;
+    int64_t first, end;                                 // rows of the turn: from `first`, below `end`
+
+    __device__ __forceinline__ void enter(const GradArgs<T>& a) {
+        const int64_t base = int64_t(item / a.segments) * a.span, seg = item % a.segments;
+        first = base + a.span * seg / a.segments;
+        end = base + a.span * (seg + 1) / a.segments;
+    }
+    // Past rows that are none; false after the last item.
+    __device__ __forceinline__ bool settle(const GradArgs<T>& a) {
+        while (first >= end) {
+            if (++item >= last) return false;
+            enter(a);
+        }
+        return true;
+    }
+};
+
 // One CTA: its items' rows, blockDim.x / tpr at a time.  Thread t of each group keeps the sums of
-// its columns; groups are joined in order through shared memory.
-template <typename T, int V, bool VEC>
-__global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<T> a, int32_t tpr) {
+// its columns; groups are joined in order through shared memory.  kAhead > 0 (rows on 16 bytes): that many
+// turns' rows of all inputs are on their way into shared memory, each thread its own 16 bytes, so that nobody
+// waits for another's copy; 0: they are loaded in their turn, any alignment.
+template <typename T, int V, int kAhead>
+__global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<T> a, int32_t tpr, uint32_t row_bytes,
+                                                                 uint32_t step) {
+    constexpr bool VEC = kAhead > 0;
     __shared__ float buf[2][3][32];
-    extern __shared__ float joined[];                   // [groups][tpr * 8 * V] where groups > 1
+    // The ring; behind it, where groups > 1, [groups][tpr * 8 * V] floats.
+    extern __shared__ __align__(16) uint8_t ring[];
+    float* joined = reinterpret_cast<float*>(ring);
     ptx::griddep_wait();
     const int32_t t = int32_t(threadIdx.x) % tpr, group = int32_t(threadIdx.x) / tpr;
     const int32_t groups = int32_t(blockDim.x) / tpr;
@@ -179,6 +304,7 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<
         if (a.pre != nullptr) load_row8<float, VEC>(wpre[v], a.pre, v, t, tpr, a.cols);
     }
     // Adds the groups' sums in order; the result is in group 0.
+    joined += kAhead * step / sizeof(float);
     auto join = [&](float (&s)[V][8]) {
         if (groups == 1) return;
         __syncthreads();
@@ -195,6 +321,41 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<
                 for (int32_t g = 1; g < groups; ++g) s[v][j] += joined[(g * V * 8 + v * 8 + j) * tpr + t];
     };
     const bool gate_rows = a.per_gate == 1;             // dG row by row, nothing to add
+    const bool one_gate = a.G != nullptr && a.per_gate == a.rows, gates = a.G != nullptr && !one_gate;
+    // The inputs of a row in the ring, in this order: dH and S, X, dS, the gate.
+    const uint32_t ring0 = ptx::smem_addr(ring) + uint32_t(group) * row_bytes, at_x = a.pre != nullptr ? 2 : 0;
+    const uint32_t at_ds = at_x + (a.X != nullptr ? 1 : 0), at_g = at_ds + (a.dS != nullptr ? 1 : 0), wide = row_bytes * groups;
+    RowWalk<T> ahead = {i0, i1, 0, 0};
+    ahead.enter(a);
+    bool more = ahead.settle(a);
+    auto fetch = [&](uint32_t slot) {
+        const int64_t row = ahead.first + group;
+        if (more && row < ahead.end) {
+            const uint32_t to = ring0 + slot * step;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                if (a.pre != nullptr) {
+                    copy_row8(to, a.dH + row * a.lddh, v, t, tpr, a.cols);
+                    copy_row8(to + wide, a.S + row * a.lds, v, t, tpr, a.cols);
+                }
+                if (a.X != nullptr) copy_row8(to + at_x * wide, a.X + row * a.ldx, v, t, tpr, a.cols);
+                if (a.dS != nullptr) copy_row8(to + at_ds * wide, a.dS + row * a.ldds, v, t, tpr, a.cols);
+                if (gates) copy_row8(to + at_g * wide, a.G + row / a.per_gate * a.ldg, v, t, tpr, a.cols);
+            }
+        }
+        copy_async_commit();
+        if (more) {
+            ahead.first += groups;
+            more = ahead.settle(a);
+        }
+    };
+    Raw8<T> gt[V] = {};
+    if (one_gate)
+#pragma unroll
+        for (int v = 0; v < V; ++v) load_raw8<VEC>(gt[v], a.G, v, t, tpr, a.cols);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) fetch(uint32_t(i));
+    uint32_t slot = 0;
     for (int32_t item = i0; item < i1; ++item) {
         const int32_t g = item / a.segments, seg = item % a.segments;
         const int64_t base = int64_t(g) * a.span;
@@ -202,7 +363,21 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<
         for (int64_t first = r0; first < r1; first += groups) {
             const int64_t row = first + group;
             const int32_t cols = row < r1 ? a.cols : 0;
-            Raw8<T> x[V] = {}, s[V] = {}, dh[V] = {}, ds[V] = {}, gt[V];
+            Raw8<T> x[V] = {}, s[V] = {}, dh[V] = {}, ds[V] = {};
+            if (kAhead > 0) {
+                copy_async_wait<(kAhead > 0 ? kAhead : 1) - 1>();
+                const uint32_t from = ring0 + slot * step;
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    if (a.pre != nullptr) {
+                        take_row8(dh[v], from, v, t, tpr, cols);
+                        take_row8(s[v], from + wide, v, t, tpr, cols);
+                    }
+                    if (a.X != nullptr) take_row8(x[v], from + at_x * wide, v, t, tpr, cols);
+                    if (a.dS != nullptr) take_row8(ds[v], from + at_ds * wide, v, t, tpr, cols);
+                    if (gates) take_row8(gt[v], from + at_g * wide, v, t, tpr, cols);
+                }
+            } else
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 if (a.X != nullptr) load_raw8<VEC>(x[v], a.X + row * a.ldx, v, t, tpr, cols);
@@ -211,7 +386,7 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<
                     load_raw8<VEC>(dh[v], a.dH + row * a.lddh, v, t, tpr, cols);
                 }
                 if (a.dS != nullptr) load_raw8<VEC>(ds[v], a.dS + row * a.ldds, v, t, tpr, cols);
-                if (a.G != nullptr) load_raw8<VEC>(gt[v], a.G + row / a.per_gate * a.ldg, v, t, tpr, cols);
+                if (gates) load_raw8<VEC>(gt[v], a.G + row / a.per_gate * a.ldg, v, t, tpr, cols);
             }
             float sum[3] = {};
 #pragma unroll
@@ -258,6 +433,11 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<
                     dot[0] = fmaf(e, raw_at(x[v], j), dot[0]);
                 }
                 if (a.want_gate && gate_rows) store_row8<T, VEC>(a.dG + row * a.lddg, dg, v, t, tpr, cols);
+            }
+            // The slot has been read into registers that the lines above have used.
+            if (kAhead > 0) {
+                fetch(slot);
+                slot = slot + 1 == uint32_t(kAhead) ? 0 : slot + 1;
             }
             if (a.dX != nullptr) {
                 if (a.post != nullptr) {
@@ -389,7 +569,7 @@ __global__ void __launch_bounds__(256) residual_norm_grad_long_kernel(const Grad
 }
 
 // Sums of runs of `count` rows of a [runs * count, cols] fp32 matrix, 32 columns a CTA: the rows dealt to
-// 32 warps, then the warps' sums added in order.  blockIdx.y: which of the up to three outputs' runs.
+// 8 warps, then the warps' sums added in order.  blockIdx.y: which of the up to three outputs' runs.
 struct PartSums {
     struct Of {
         const float* in;
@@ -401,28 +581,28 @@ struct PartSums {
     int32_t n, cols;
 };
 
-__global__ void __launch_bounds__(1024) norm_sums_kernel(const PartSums p) {
-    __shared__ float part[32][33];
+__global__ void __launch_bounds__(256) norm_sums_kernel(const __grid_constant__ PartSums p) {
+    __shared__ float part[8][32];
     ptx::griddep_wait();
     int32_t run = int32_t(blockIdx.y), i = 0;
     while (i + 1 < p.n && run >= p.of[i].runs) run -= p.of[i++].runs;
     const PartSums::Of& o = p.of[i];
-    const int32_t lane = int32_t(threadIdx.x) % 32, warp = int32_t(threadIdx.x) / 32;
+    const int32_t lane = int32_t(threadIdx.x) % 32, warp = int32_t(threadIdx.x) / 32, count = o.count;
     const int32_t c = int32_t(blockIdx.x) * 32 + lane;
+    const float* in = o.in + int64_t(run) * count * p.cols + c;
     float s = 0.f;
     if (c < p.cols)
 #pragma unroll 8
-        for (int32_t k = warp; k < o.count; k += 32) s += o.in[(int64_t(run) * o.count + k) * p.cols + c];
+        for (int32_t k = warp; k < count; k += 8) s += in[int64_t(k) * p.cols];
     part[warp][lane] = s;
     __syncthreads();
-    s = warp_sum(part[lane][warp]);                     // column `warp` of the 32
-    const int32_t d = int32_t(blockIdx.x) * 32 + warp;
-    if (lane == 0 && d < p.cols) {
-        if (o.bf16)
-            static_cast<__nv_bfloat16*>(o.out)[run * o.ldo + d] = __float2bfloat16_rn(s);
-        else
-            static_cast<float*>(o.out)[run * o.ldo + d] = s;
-    }
+    if (warp != 0 || c >= p.cols) return;
+#pragma unroll
+    for (int w = 1; w < 8; ++w) s += part[w][lane];
+    if (o.bf16)
+        static_cast<__nv_bfloat16*>(o.out)[run * o.ldo + c] = __float2bfloat16_rn(s);
+    else
+        static_cast<float*>(o.out)[run * o.ldo + c] = s;
 }
 
 // ------------------------------------------------------------ launches
@@ -446,6 +626,18 @@ void* forward_kernel(bool vec) {
                : reinterpret_cast<void*>(&residual_norm_kernel<T, V, false>);
 }
 
+template <typename T, int kAhead, int kMost>
+void* stream_kernel() {
+    return reinterpret_cast<void*>(&residual_norm_stream_kernel<T, 2, kAhead, kMost>);
+}
+
+// Rows of 1024 to 8192 columns, and enough of them for CTAs that stay.
+bool streams(const ResidualNormArgs& s, size_t esize, int sm_count) {
+    const int inputs = 1 + (s.R.p ? 1 : 0) + (s.G.p && s.gates > 1 ? 1 : 0);
+    return s.cols > 1024 && s.cols <= 8192 && s.rows >= 8 * sm_count &&
+           2 * size_t(s.cols) * esize * size_t(inputs) <= 216 * 1024;
+}
+
 template <typename T>
 int run_forward(const ResidualNormArgs& s, const LibCtx& c, cudaStream_t stream) {
     Args<T> a = {static_cast<const T*>(s.X.p), static_cast<const T*>(s.R.p), static_cast<const T*>(s.G.p), s.post, s.pre,
@@ -459,6 +651,19 @@ int run_forward(const ResidualNormArgs& s, const LibCtx& c, cudaStream_t stream)
         void* args[] = {&a};
         e = launch_kernel(reinterpret_cast<void*>(&residual_norm_long_kernel<T>),
                           dim3(unsigned(std::min<int64_t>(s.rows, 2 * c.sm_count))), 1024, 0, 1, args, stream);
+    } else if (vec && streams(s, sizeof(T), c.sm_count)) {
+        const int inputs = 1 + (s.R.p ? 1 : 0) + (s.G.p && s.gates > 1 ? 1 : 0);
+        uint32_t row_bytes = uint32_t(s.cols * sizeof(T)), step = row_bytes * uint32_t(inputs);
+        const int threads = threads_for(s.cols, 2), ctas = threads > 256 ? 1 : 3;
+        const bool three = 3 * step * ctas <= 216 * 1024;
+        void* kernel = threads > 256 ? (three ? stream_kernel<T, 3, 512>() : stream_kernel<T, 2, 512>())
+                                     : (three ? stream_kernel<T, 3, 256>() : stream_kernel<T, 2, 256>());
+        const size_t smem = size_t(three ? 3 : 2) * step;
+        const int r = raise_kernel_smem(kernel, smem, c.device);
+        if (r != GBR_OK) return r;
+        void* args[] = {&a, &row_bytes, &step};
+        e = launch_kernel(kernel, dim3(unsigned(c.sm_count * std::min<int64_t>(ctas, 216 * 1024 / smem))), threads, smem, 1,
+                          args, stream);
     } else {
         const int V = s.cols > 1024 * 16 ? 4 : s.cols > 1024 * 8 ? 2 : 1;
         int32_t tpr = threads_for(s.cols, V);
@@ -473,9 +678,13 @@ int run_forward(const ResidualNormArgs& s, const LibCtx& c, cudaStream_t stream)
 }
 
 template <typename T, int V>
-void* grad_kernel(bool vec) {
-    return vec ? reinterpret_cast<void*>(&residual_norm_grad_kernel<T, V, true>)
-               : reinterpret_cast<void*>(&residual_norm_grad_kernel<T, V, false>);
+void* grad_kernel(int ahead) {
+    switch (ahead) {
+        case 4: return reinterpret_cast<void*>(&residual_norm_grad_kernel<T, V, 4>);
+        case 3: return reinterpret_cast<void*>(&residual_norm_grad_kernel<T, V, 3>);
+        case 2: return reinterpret_cast<void*>(&residual_norm_grad_kernel<T, V, 2>);
+        default: return reinterpret_cast<void*>(&residual_norm_grad_kernel<T, V, 0>);
+    }
 }
 
 // Cuts the rows into items and the items into at most `ctas` shares: without a gate that several
@@ -519,34 +728,37 @@ int run_backward(const ResidualNormGradArgs& s, const LibCtx& c, cudaStream_t st
     const int64_t col_ctas = cdiv(s.cols, 256);
     const int64_t ctas = long_rows ? std::max<int64_t>(1, 8 * c.sm_count / col_ctas) : c.sm_count * (threads > 256 ? 1 : 2);
     const int64_t grid = cut_rows(&a, s.gates, ctas, groups);
-    Scratch ws(c, stream);
-    void* q;
-    int r;
-    const size_t row_bytes = size_t(s.cols) * 4;
+    // Scratch of the sums over rows and of the rows' statistics, in one block.
     PartSums sums = {};
     sums.cols = s.cols;
     int32_t runs = 0;
-    auto part = [&](bool want, int64_t n, int64_t count, void* out, int64_t ldo, bool bf16, float** p) -> int {
-        if (!want) return GBR_OK;
-        const int e = ws.take(size_t(n * count) * row_bytes, "cudaMallocFromPoolAsync(sums over rows)", &q);
-        if (e != GBR_OK) return e;
-        *p = static_cast<float*>(q);
-        sums.of[sums.n++] = {*p, out, ldo, int32_t(n), int32_t(count), bf16};
+    size_t floats = 0;
+    auto part = [&](bool want, int64_t n, int64_t count, void* out, int64_t ldo, bool bf16) -> int {
+        if (!want) return -1;
+        sums.of[sums.n] = {reinterpret_cast<const float*>(floats), out, ldo, int32_t(n), int32_t(count), bf16};
+        floats += (size_t(n * count) * size_t(s.cols) + 3) / 4 * 4;
         runs += int32_t(n);
-        return GBR_OK;
+        return sums.n++;
     };
-    if ((r = part(a.want_post, 1, grid, s.dpost, 0, false, &a.post_part)) != GBR_OK) return r;
-    if ((r = part(a.want_pre, 1, grid, s.dpre, 0, false, &a.pre_part)) != GBR_OK) return r;
-    if ((r = part(a.want_gate && a.per_gate != 1 && a.segments > 1, s.gates, a.segments, s.dG.w(), s.dG.ld, s.bf16,
-                  &a.gate_part)) != GBR_OK)
-        return r;
+    const int i_post = part(a.want_post, 1, grid, s.dpost, 0, false), i_pre = part(a.want_pre, 1, grid, s.dpre, 0, false);
+    const int i_gate = part(a.want_gate && a.per_gate != 1 && a.segments > 1, s.gates, a.segments, s.dG.w(), s.dG.ld, s.bf16);
+    const size_t stats_at = floats;
+    if (long_rows) floats += size_t(s.rows) * 4;
+    Scratch ws(c, stream);
+    void* q = nullptr;
+    int r;
+    if (floats > 0 && (r = ws.take(floats * sizeof(float), "cudaMallocFromPoolAsync(sums over rows)", &q)) != GBR_OK) return r;
+    float* base = static_cast<float*>(q);
+    for (int i = 0; i < sums.n; ++i) sums.of[i].in = base + reinterpret_cast<size_t>(sums.of[i].in);
+    auto of = [&](int i) { return i < 0 ? nullptr : const_cast<float*>(sums.of[i].in); };
+    a.post_part = of(i_post), a.pre_part = of(i_pre), a.gate_part = of(i_gate);
     cudaError_t e;
     if (long_rows) {
-        if ((r = ws.take(size_t(s.rows) * sizeof(float4), "cudaMallocFromPoolAsync(row statistics)", &q)) != GBR_OK) return r;
-        float4* stats = static_cast<float4*>(q);
+        float4* stats = reinterpret_cast<float4*>(base + stats_at);
         void* args[] = {&a, &stats};
         e = launch_kernel(reinterpret_cast<void*>(&residual_norm_stats_kernel<T>),
-                          dim3(unsigned(std::min<int64_t>(s.rows, 2 * c.sm_count))), 1024, 0, 1, args, stream);
+                          dim3(unsigned(std::max<int64_t>(1, std::min<int64_t>(s.rows, 2 * c.sm_count)))), 1024, 0, 1, args,
+                          stream);
         if (e != cudaSuccess) return report_cuda(e, "launching residual_norm_backward");
         count_launch();
         e = launch_kernel(reinterpret_cast<void*>(&residual_norm_grad_long_kernel<T>),
@@ -554,17 +766,24 @@ int run_backward(const ResidualNormGradArgs& s, const LibCtx& c, cudaStream_t st
     } else {
         bool vec = s.cols % 8 == 0 && aligned16<T>(s.G.p, s.G.ld, s.gates) && aligned16<T>(s.dG.p, s.dG.ld, s.gates);
         for (const Mat* m : {&s.dS, &s.dH, &s.X, &s.S, &s.dX, &s.dR}) vec = vec && aligned16<T>(m->p, m->ld, s.rows);
-        for (const float* w : {s.post, s.pre}) vec = vec && aligned16<float>(w, 0, 1);
-        void* kernel = V == 2 ? grad_kernel<T, 2>(vec) : grad_kernel<T, 1>(vec);
-        void* args[] = {&a, &tpr};
-        const size_t smem = groups > 1 ? size_t(threads) * 8 * V * sizeof(float) : 0;
+        for (const float* w : {s.post, s.pre, static_cast<const float*>(s.dpost), static_cast<const float*>(s.dpre)}) vec = vec && aligned16<float>(w, 0, 1);
+        const int inputs = (s.pre ? 2 : 0) + (s.X.p ? 1 : 0) + (s.dS.p ? 1 : 0) + (s.G.p && s.gates > 1 ? 1 : 0);
+        uint32_t row_bytes = uint32_t(s.cols * sizeof(T)), step = vec ? row_bytes * uint32_t(groups * inputs) : 0;
+        const size_t join = groups > 1 ? size_t(threads) * 8 * V * sizeof(float) : 0;
+        const size_t most = size_t(threads > 256 ? 220 : 108) * 1024 - join;
+        const int ahead = !vec ? 0 : 4 * step <= most ? 4 : 3 * step <= most ? 3 : 2 * step <= most ? 2 : 0;
+        if (ahead == 0) step = 0;
+        void* kernel = V == 2 ? grad_kernel<T, 2>(ahead) : grad_kernel<T, 1>(ahead);
+        const size_t smem = join + size_t(ahead) * step;
+        if ((r = raise_kernel_smem(kernel, smem, c.device)) != GBR_OK) return r;
+        void* args[] = {&a, &tpr, &row_bytes, &step};
         e = launch_kernel(kernel, dim3(unsigned(grid)), threads, smem, 1, args, stream);
     }
     if (e != cudaSuccess) return report_cuda(e, "launching residual_norm_backward");
     count_launch();
     if (runs == 0) return GBR_OK;
     void* args[] = {&sums};
-    e = launch_kernel(reinterpret_cast<void*>(&norm_sums_kernel), dim3(unsigned(cdiv(s.cols, 32)), unsigned(runs)), 1024,
+    e = launch_kernel(reinterpret_cast<void*>(&norm_sums_kernel), dim3(unsigned(cdiv(s.cols, 32)), unsigned(runs)), 256,
                       0, 1, args, stream);
     if (e != cudaSuccess) return report_cuda(e, "launching the sums of residual_norm_backward");
     count_launch();
