@@ -139,6 +139,7 @@ __global__ void __launch_bounds__(kMost, kMost == 256 ? 3 : 1) residual_norm_str
         if (a.pre != nullptr) load_row8<float, true>(wpre[v], a.pre, v, t, tpr, cols);
         if (one_gate) load_raw8<true>(g[v], a.G, v, t, tpr, cols);
     }
+    clear_past<T, V>(base, kAhead * step / row_bytes, row_bytes, t, tpr, cols);
     int64_t row = blockIdx.x;
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) fetch(row + int64_t(i) * gridDim.x, uint32_t(i));
@@ -148,9 +149,9 @@ __global__ void __launch_bounds__(kMost, kMost == 256 ? 3 : 1) residual_norm_str
         Raw8<T> x[V], r[V] = {};
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            take_row8(x[v], from, v, t, tpr, cols);
-            if (has_r) take_row8(r[v], from + row_bytes, v, t, tpr, cols);
-            if (gates) take_row8(g[v], from + (has_r ? 2u : 1u) * row_bytes, v, t, tpr, cols);
+            take_row8(x[v], from, v, t, tpr);
+            if (has_r) take_row8(r[v], from + row_bytes, v, t, tpr);
+            if (gates) take_row8(g[v], from + (has_r ? 2u : 1u) * row_bytes, v, t, tpr);
         }
         float s[V][8], q = 1.f;
         if (a.post != nullptr) {
@@ -284,47 +285,59 @@ struct RowWalk {
 // its columns; groups are joined in order through shared memory.  kAhead > 0 (rows on 16 bytes): that many
 // turns' rows of all inputs are on their way into shared memory, each thread its own 16 bytes, so that nobody
 // waits for another's copy; 0: they are loaded in their turn, any alignment.
-template <typename T, int V, int kAhead>
+// FULL: a training step's call, with both norms, dS and all of dX, dR, dpost and dpre, without a gate an element; what
+// is there need not be asked then (4096 x 4096: 631 instructions a warp and row if it is).
+template <typename T, int V, int kAhead, bool FULL>
 __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<T> a, int32_t tpr, uint32_t row_bytes,
                                                                  uint32_t step) {
     constexpr bool VEC = kAhead > 0;
     __shared__ float buf[2][3][32];
     // The ring; behind it, where groups > 1, [groups][tpr * 8 * V] floats.
     extern __shared__ __align__(16) uint8_t ring[];
-    float* joined = reinterpret_cast<float*>(ring);
     ptx::griddep_wait();
     const int32_t t = int32_t(threadIdx.x) % tpr, group = int32_t(threadIdx.x) / tpr;
     const int32_t groups = int32_t(blockDim.x) / tpr;
     const int32_t i0 = int32_t(int64_t(a.items) * blockIdx.x / gridDim.x);
     const int32_t i1 = int32_t(int64_t(a.items) * (blockIdx.x + 1) / gridDim.x);
-    float wpost[V][8], wpre[V][8], spost[V][8] = {}, spre[V][8] = {}, sgate[V][8] = {};
+    const bool post = FULL || a.post != nullptr, pre = FULL || a.pre != nullptr, has_x = FULL || a.X != nullptr;
+    const bool has_ds = FULL || a.dS != nullptr, want_x = FULL || a.dX != nullptr, want_r = FULL || a.dR != nullptr;
+    const bool want_post = FULL || a.want_post, want_pre = FULL || a.want_pre;
+    const bool gate_rows = !FULL && a.G != nullptr && a.per_gate == 1;      // a gate an element: dG row by row, nothing to add
+    const bool run_gate = a.G != nullptr && !gate_rows;            // one for all rows of an item
+    const bool want_run = !gate_rows && (want_post || a.want_gate), weighted = post || a.G != nullptr;
+    // Weights, and sums: dpre and dpost over all rows, ds X q over an item's.  dgate and dpost of rows that share a gate
+    // are that last sum times what does not change with the row.
+    F2 wpost[V][4], wpre[V][4], spost[V][4], spre[V][4], srun[V][4];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        if (a.post != nullptr) load_row8<float, VEC>(wpost[v], a.post, v, t, tpr, a.cols);
-        if (a.pre != nullptr) load_row8<float, VEC>(wpre[v], a.pre, v, t, tpr, a.cols);
+        if (gate_rows && post) load_pairs<float, VEC>(wpost[v], a.post, v, t, tpr, a.cols);
+        if (pre) load_pairs<float, VEC>(wpre[v], a.pre, v, t, tpr, a.cols);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) spost[v][i] = spre[v][i] = srun[v][i] = f2(0.f);
     }
     // Adds the groups' sums in order; the result is in group 0.
-    joined += kAhead * step / sizeof(float);
-    auto join = [&](float (&s)[V][8]) {
+    float* joined = reinterpret_cast<float*>(ring) + kAhead * step / sizeof(float);
+    auto join = [&](F2 (&s)[V][4]) {
         if (groups == 1) return;
         __syncthreads();
 #pragma unroll
         for (int v = 0; v < V; ++v)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) joined[(group * V * 8 + v * 8 + j) * tpr + t] = s[v][j];
+            for (int i = 0; i < 4; ++i)
+                split2(s[v][i], joined[(group * V * 8 + v * 8 + 2 * i) * tpr + t], joined[(group * V * 8 + v * 8 + 2 * i + 1) * tpr + t]);
         __syncthreads();
         if (group != 0) return;
 #pragma unroll
         for (int v = 0; v < V; ++v)
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                for (int32_t g = 1; g < groups; ++g) s[v][j] += joined[(g * V * 8 + v * 8 + j) * tpr + t];
+            for (int i = 0; i < 4; ++i)
+                for (int32_t g = 1; g < groups; ++g)
+                    s[v][i] = add2(s[v][i], f2(joined[(g * V * 8 + v * 8 + 2 * i) * tpr + t],
+                                               joined[(g * V * 8 + v * 8 + 2 * i + 1) * tpr + t]));
     };
-    const bool gate_rows = a.per_gate == 1;             // dG row by row, nothing to add
-    const bool one_gate = a.G != nullptr && a.per_gate == a.rows, gates = a.G != nullptr && !one_gate;
     // The inputs of a row in the ring, in this order: dH and S, X, dS, the gate.
-    const uint32_t ring0 = ptx::smem_addr(ring) + uint32_t(group) * row_bytes, at_x = a.pre != nullptr ? 2 : 0;
-    const uint32_t at_ds = at_x + (a.X != nullptr ? 1 : 0), at_g = at_ds + (a.dS != nullptr ? 1 : 0), wide = row_bytes * groups;
+    const uint32_t ring0 = ptx::smem_addr(ring) + uint32_t(group) * row_bytes, at_x = pre ? 2 : 0;
+    const uint32_t at_ds = at_x + (has_x ? 1 : 0), at_g = at_ds + (has_ds ? 1 : 0), wide = row_bytes * groups;
     RowWalk<T> ahead = {i0, i1, 0, 0};
     ahead.enter(a);
     bool more = ahead.settle(a);
@@ -334,13 +347,13 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<
             const uint32_t to = ring0 + slot * step;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                if (a.pre != nullptr) {
+                if (pre) {
                     copy_row8(to, a.dH + row * a.lddh, v, t, tpr, a.cols);
                     copy_row8(to + wide, a.S + row * a.lds, v, t, tpr, a.cols);
                 }
-                if (a.X != nullptr) copy_row8(to + at_x * wide, a.X + row * a.ldx, v, t, tpr, a.cols);
-                if (a.dS != nullptr) copy_row8(to + at_ds * wide, a.dS + row * a.ldds, v, t, tpr, a.cols);
-                if (gates) copy_row8(to + at_g * wide, a.G + row / a.per_gate * a.ldg, v, t, tpr, a.cols);
+                if (has_x) copy_row8(to + at_x * wide, a.X + row * a.ldx, v, t, tpr, a.cols);
+                if (has_ds) copy_row8(to + at_ds * wide, a.dS + row * a.ldds, v, t, tpr, a.cols);
+                if (gate_rows) copy_row8(to + at_g * wide, a.G + row * a.ldg, v, t, tpr, a.cols);
             }
         }
         copy_async_commit();
@@ -349,10 +362,7 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<
             more = ahead.settle(a);
         }
     };
-    Raw8<T> gt[V] = {};
-    if (one_gate)
-#pragma unroll
-        for (int v = 0; v < V; ++v) load_raw8<VEC>(gt[v], a.G, v, t, tpr, a.cols);
+    if (kAhead > 0) clear_past<T, V>(ptx::smem_addr(ring), kAhead * step / row_bytes, row_bytes, t, tpr, a.cols);
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) fetch(uint32_t(i));
     uint32_t slot = 0;
@@ -360,128 +370,195 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<
         const int32_t g = item / a.segments, seg = item % a.segments;
         const int64_t base = int64_t(g) * a.span;
         const int64_t r0 = base + int64_t(a.span) * seg / a.segments, r1 = base + int64_t(a.span) * (seg + 1) / a.segments;
+        const T* gate = run_gate ? a.G + g * a.ldg : nullptr;
+        F2 gw[V][4];                                    // gate times weight
+        if (!gate_rows && weighted)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                F2 w[4];
+                if (post) load_pairs<float, VEC>(gw[v], a.post, v, t, tpr, a.cols);
+                if (run_gate) load_pairs<T, VEC>(w, gate, v, t, tpr, a.cols);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) gw[v][i] = !run_gate ? gw[v][i] : post ? mul2(gw[v][i], w[i]) : w[i];
+            }
         for (int64_t first = r0; first < r1; first += groups) {
             const int64_t row = first + group;
-            const int32_t cols = row < r1 ? a.cols : 0;
-            Raw8<T> x[V] = {}, s[V] = {}, dh[V] = {}, ds[V] = {};
+            const bool in = row < r1;
+            const int32_t cols = in ? a.cols : 0;
+            Raw8<T> x[V] = {}, s[V] = {}, dh[V] = {}, ds[V] = {}, gt[V] = {};
             if (kAhead > 0) {
                 copy_async_wait<(kAhead > 0 ? kAhead : 1) - 1>();
                 const uint32_t from = ring0 + slot * step;
+                if (in)
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        if (pre) {
+                            take_row8(dh[v], from, v, t, tpr);
+                            take_row8(s[v], from + wide, v, t, tpr);
+                        }
+                        if (has_x) take_row8(x[v], from + at_x * wide, v, t, tpr);
+                        if (has_ds) take_row8(ds[v], from + at_ds * wide, v, t, tpr);
+                        if (gate_rows) take_row8(gt[v], from + at_g * wide, v, t, tpr);
+                    }
+            } else {
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    if (a.pre != nullptr) {
-                        take_row8(dh[v], from, v, t, tpr, cols);
-                        take_row8(s[v], from + wide, v, t, tpr, cols);
+                    if (has_x) load_raw8<VEC>(x[v], a.X + row * a.ldx, v, t, tpr, cols);
+                    if (pre) {
+                        load_raw8<VEC>(s[v], a.S + row * a.lds, v, t, tpr, cols);
+                        load_raw8<VEC>(dh[v], a.dH + row * a.lddh, v, t, tpr, cols);
                     }
-                    if (a.X != nullptr) take_row8(x[v], from + at_x * wide, v, t, tpr, cols);
-                    if (a.dS != nullptr) take_row8(ds[v], from + at_ds * wide, v, t, tpr, cols);
-                    if (gates) take_row8(gt[v], from + at_g * wide, v, t, tpr, cols);
+                    if (has_ds) load_raw8<VEC>(ds[v], a.dS + row * a.ldds, v, t, tpr, cols);
+                    if (gate_rows) load_raw8<VEC>(gt[v], a.G + row * a.ldg, v, t, tpr, cols);
                 }
-            } else
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                if (a.X != nullptr) load_raw8<VEC>(x[v], a.X + row * a.ldx, v, t, tpr, cols);
-                if (a.pre != nullptr) {
-                    load_raw8<VEC>(s[v], a.S + row * a.lds, v, t, tpr, cols);
-                    load_raw8<VEC>(dh[v], a.dH + row * a.lddh, v, t, tpr, cols);
-                }
-                if (a.dS != nullptr) load_raw8<VEC>(ds[v], a.dS + row * a.ldds, v, t, tpr, cols);
-                if (gates) load_raw8<VEC>(gt[v], a.G + row / a.per_gate * a.ldg, v, t, tpr, cols);
             }
-            float sum[3] = {};
+            F2 ss = f2(0.f), us = f2(0.f), xx = f2(0.f);
+            if (pre)
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const F2 S = raw_pair(s[v], i);
+                        ss = fma2(S, S, ss);
+                        us = fma2(mul2(raw_pair(dh[v], i), wpre[v][i]), S, us);
+                    }
+            if (post)
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const F2 X = raw_pair(x[v], i);
+                        xx = fma2(X, X, xx);
+                    }
+            float sum[3] = {sum_pair(ss), sum_pair(us), sum_pair(xx)};
+            if (pre || post) group_sum(sum, buf[0], tpr);
+            // A group without a row adds zeros.
+            const float r = in ? root(sum[0], a.inv_cols, a.eps) : 0.f, rc = r * r * r * sum[1] * a.inv_cols;
+            const float q = !post ? 1.f : in ? root(sum[2], a.inv_cols, a.eps) : 0.f;
+            F2 d[V][4], dot = f2(0.f);
 #pragma unroll
             for (int v = 0; v < V; ++v)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float xs = raw_at(s[v], j), xx = raw_at(x[v], j);
-                    if (a.pre != nullptr) {
-                        sum[0] = fmaf(xs, xs, sum[0]);
-                        sum[1] = fmaf(raw_at(dh[v], j) * wpre[v][j], xs, sum[1]);
-                    }
-                    if (a.post != nullptr) sum[2] = fmaf(xx, xx, sum[2]);
-                }
-            if (a.pre != nullptr || a.post != nullptr) group_sum(sum, buf[0], tpr);
-            const float r = root(sum[0], a.inv_cols, a.eps), rc = r * r * r * sum[1] * a.inv_cols;
-            const float q = a.post != nullptr ? root(sum[2], a.inv_cols, a.eps) : 1.f;
-            float d[V][8], dot[1] = {};
+                for (int i = 0; i < 4; ++i) d[v][i] = raw_pair(ds[v], i);
+            if (pre) {
+                const F2 r2 = f2(r), m2 = f2(-rc);
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                float dg[8];
+                for (int v = 0; v < V; ++v)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    float e = raw_at(ds[v], j);
-                    if (a.pre != nullptr) {
-                        const float h = raw_at(dh[v], j), xs = raw_at(s[v], j);
-                        e = e + r * (h * wpre[v][j]) - xs * rc;
-                        if (cols > 0) spre[v][j] = fmaf(h, xs * r, spre[v][j]);
+                    for (int i = 0; i < 4; ++i) {
+                        const F2 S = raw_pair(s[v], i), H = raw_pair(dh[v], i);
+                        d[v][i] = fma2(S, m2, fma2(r2, mul2(H, wpre[v][i]), d[v][i]));
+                        spre[v][i] = fma2(H, mul2(S, r2), spre[v][i]);
                     }
-                    d[v][j] = e;
-                }
-                if (a.dR != nullptr) store_row8<T, VEC>(a.dR + row * a.lddr, d[v], v, t, tpr, cols);
+            }
+            if (want_r)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float n = raw_at(x[v], j) * q;           // X normalised
-                    float e = a.scale * d[v][j];
-                    dg[j] = e * (a.post != nullptr ? n * wpost[v][j] : n);
-                    if (a.G != nullptr) e *= raw_at(gt[v], j);
-                    if (cols > 0) {
-                        sgate[v][j] += dg[j];
-                        if (a.post != nullptr) spost[v][j] = fmaf(e, n, spost[v][j]);
+                for (int v = 0; v < V; ++v) store_pairs<T, VEC>(a.dR + row * a.lddr, d[v], v, t, tpr, cols);
+            const F2 q2 = f2(q);
+            if (gate_rows) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    F2 dg[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const F2 X = raw_pair(x[v], i), n = mul2(X, q2), y = post ? mul2(n, wpost[v][i]) : n;
+                        dg[i] = mul2(mul2(f2(a.scale), d[v][i]), y);
+                        d[v][i] = mul2(d[v][i], raw_pair(gt[v], i));
+                        if (post) {
+                            spost[v][i] = fma2(mul2(f2(a.scale), d[v][i]), n, spost[v][i]);
+                            d[v][i] = mul2(d[v][i], wpost[v][i]);
+                            dot = fma2(d[v][i], X, dot);
+                        }
                     }
-                    if (a.post != nullptr) e *= wpost[v][j];
-                    d[v][j] = e;
-                    dot[0] = fmaf(e, raw_at(x[v], j), dot[0]);
+                    if (a.want_gate) store_pairs<T, VEC>(a.dG + row * a.lddg, dg, v, t, tpr, cols);
                 }
-                if (a.want_gate && gate_rows) store_row8<T, VEC>(a.dG + row * a.lddg, dg, v, t, tpr, cols);
+            } else if (weighted) {
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const F2 X = raw_pair(x[v], i);
+                        if (want_run) srun[v][i] = fma2(d[v][i], mul2(X, q2), srun[v][i]);
+                        d[v][i] = mul2(d[v][i], gw[v][i]);
+                        dot = fma2(d[v][i], X, dot);
+                    }
             }
             // The slot has been read into registers that the lines above have used.
             if (kAhead > 0) {
                 fetch(slot);
                 slot = slot + 1 == uint32_t(kAhead) ? 0 : slot + 1;
             }
-            if (a.dX != nullptr) {
-                if (a.post != nullptr) {
-                    group_sum(dot, buf[1], tpr);
-                    const float qc = q * q * q * dot[0] * a.inv_cols;
-#pragma unroll
-                    for (int v = 0; v < V; ++v)
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) d[v][j] = q * d[v][j] - raw_at(x[v], j) * qc;
+            if (want_x) {
+                F2 m2 = f2(0.f);
+                if (post) {
+                    float sums[1] = {sum_pair(dot)};
+                    group_sum(sums, buf[1], tpr);
+                    m2 = f2(-a.scale * (q * q * q * sums[0] * a.inv_cols));
                 }
-#pragma unroll
-                for (int v = 0; v < V; ++v) store_row8<T, VEC>(a.dX + row * a.lddx, d[v], v, t, tpr, cols);
-            }
-            if (tpr > 32 && (a.dX == nullptr || a.post == nullptr)) __syncthreads();   // buf[0], for the next rows
-        }
-        if (a.want_gate && !gate_rows) {
-            join(sgate);
-            if (group == 0)
+                const F2 k2 = f2(a.scale * q);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    if (a.segments > 1)
-                        store_row8<float, VEC>(a.gate_part + int64_t(item) * a.cols, sgate[v], v, t, tpr, a.cols);
-                    else
-                        store_row8<T, VEC>(a.dG + g * a.lddg, sgate[v], v, t, tpr, a.cols);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        d[v][i] = mul2(d[v][i], k2);
+                        if (post) d[v][i] = fma2(raw_pair(x[v], i), m2, d[v][i]);
+                    }
+                    store_pairs<T, VEC>(a.dX + row * a.lddx, d[v], v, t, tpr, cols);
                 }
+            }
+            if (tpr > 32 && (!want_x || !post)) __syncthreads();   // buf[0], for the next rows
+        }
+        if (want_run) {
+            // dpost gains scale gate sum, dgate is scale weight sum.
+            if (want_post)
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    F2 w[4];
+                    if (run_gate) load_pairs<T, VEC>(w, gate, v, t, tpr, a.cols);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const F2 k = run_gate ? mul2(f2(a.scale), w[i]) : f2(a.scale);
+                        spost[v][i] = fma2(srun[v][i], k, spost[v][i]);
+                    }
+                }
+            if (a.want_gate) {
+                join(srun);
+                if (group == 0)
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        F2 w[4];
+                        if (post) load_pairs<float, VEC>(w, a.post, v, t, tpr, a.cols);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            srun[v][i] = mul2(srun[v][i], f2(a.scale));
+                            if (post) srun[v][i] = mul2(srun[v][i], w[i]);
+                        }
+                        if (a.segments > 1)
+                            store_pairs<float, VEC>(a.gate_part + int64_t(item) * a.cols, srun[v], v, t, tpr, a.cols);
+                        else
+                            store_pairs<T, VEC>(a.dG + g * a.lddg, srun[v], v, t, tpr, a.cols);
+                    }
+            }
 #pragma unroll
             for (int v = 0; v < V; ++v)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) sgate[v][j] = 0.f;
+                for (int i = 0; i < 4; ++i) srun[v][i] = f2(0.f);
         }
     }
-    if (a.want_post) {
+    if (kAhead > 0) copy_async_wait<0>();
+    if (want_post) {
         join(spost);
         if (group == 0)
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                store_row8<float, VEC>(a.post_part + int64_t(blockIdx.x) * a.cols, spost[v], v, t, tpr, a.cols);
+                store_pairs<float, VEC>(a.post_part + int64_t(blockIdx.x) * a.cols, spost[v], v, t, tpr, a.cols);
     }
-    if (a.want_pre) {
+    if (want_pre) {
         join(spre);
         if (group == 0)
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                store_row8<float, VEC>(a.pre_part + int64_t(blockIdx.x) * a.cols, spre[v], v, t, tpr, a.cols);
+                store_pairs<float, VEC>(a.pre_part + int64_t(blockIdx.x) * a.cols, spre[v], v, t, tpr, a.cols);
     }
 }
 
@@ -569,7 +646,7 @@ __global__ void __launch_bounds__(256) residual_norm_grad_long_kernel(const Grad
 }
 
 // Sums of runs of `count` rows of a [runs * count, cols] fp32 matrix, 32 columns a CTA: the rows dealt to
-// 8 warps, then the warps' sums added in order.  blockIdx.y: which of the up to three outputs' runs.
+// 16 warps, then the warps' sums added in order.  blockIdx.y: which of the up to three outputs' runs.
 struct PartSums {
     struct Of {
         const float* in;
@@ -581,8 +658,8 @@ struct PartSums {
     int32_t n, cols;
 };
 
-__global__ void __launch_bounds__(256) norm_sums_kernel(const __grid_constant__ PartSums p) {
-    __shared__ float part[8][32];
+__global__ void __launch_bounds__(512) norm_sums_kernel(const __grid_constant__ PartSums p) {
+    __shared__ float part[16][32];
     ptx::griddep_wait();
     int32_t run = int32_t(blockIdx.y), i = 0;
     while (i + 1 < p.n && run >= p.of[i].runs) run -= p.of[i++].runs;
@@ -592,13 +669,13 @@ __global__ void __launch_bounds__(256) norm_sums_kernel(const __grid_constant__ 
     const float* in = o.in + int64_t(run) * count * p.cols + c;
     float s = 0.f;
     if (c < p.cols)
-#pragma unroll 8
-        for (int32_t k = warp; k < count; k += 8) s += in[int64_t(k) * p.cols];
+#pragma unroll 10
+        for (int32_t k = warp; k < count; k += 16) s += in[int64_t(k) * p.cols];
     part[warp][lane] = s;
     __syncthreads();
     if (warp != 0 || c >= p.cols) return;
 #pragma unroll
-    for (int w = 1; w < 8; ++w) s += part[w][lane];
+    for (int w = 1; w < 16; ++w) s += part[w][lane];
     if (o.bf16)
         static_cast<__nv_bfloat16*>(o.out)[run * o.ldo + c] = __float2bfloat16_rn(s);
     else
@@ -635,7 +712,7 @@ void* stream_kernel() {
 bool streams(const ResidualNormArgs& s, size_t esize, int sm_count) {
     const int inputs = 1 + (s.R.p ? 1 : 0) + (s.G.p && s.gates > 1 ? 1 : 0);
     return s.cols > 1024 && s.cols <= 8192 && s.rows >= 8 * sm_count &&
-           2 * size_t(s.cols) * esize * size_t(inputs) <= 216 * 1024;
+           2 * size_t(threads_for(s.cols, 2)) * 16 * esize * size_t(inputs) <= 216 * 1024;
 }
 
 template <typename T>
@@ -653,8 +730,9 @@ int run_forward(const ResidualNormArgs& s, const LibCtx& c, cudaStream_t stream)
                           dim3(unsigned(std::min<int64_t>(s.rows, 2 * c.sm_count))), 1024, 0, 1, args, stream);
     } else if (vec && streams(s, sizeof(T), c.sm_count)) {
         const int inputs = 1 + (s.R.p ? 1 : 0) + (s.G.p && s.gates > 1 ? 1 : 0);
-        uint32_t row_bytes = uint32_t(s.cols * sizeof(T)), step = row_bytes * uint32_t(inputs);
-        const int threads = threads_for(s.cols, 2), ctas = threads > 256 ? 1 : 3;
+        const int threads = threads_for(s.cols, 2);
+        uint32_t row_bytes = uint32_t(threads * 16 * sizeof(T)), step = row_bytes * uint32_t(inputs);
+        const int ctas = threads > 256 ? 1 : 3;
         const bool three = 3 * step * ctas <= 216 * 1024;
         void* kernel = threads > 256 ? (three ? stream_kernel<T, 3, 512>() : stream_kernel<T, 2, 512>())
                                      : (three ? stream_kernel<T, 3, 256>() : stream_kernel<T, 2, 256>());
@@ -678,22 +756,23 @@ int run_forward(const ResidualNormArgs& s, const LibCtx& c, cudaStream_t stream)
 }
 
 template <typename T, int V>
-void* grad_kernel(int ahead) {
+void* grad_kernel(int ahead, bool full) {
     switch (ahead) {
-        case 4: return reinterpret_cast<void*>(&residual_norm_grad_kernel<T, V, 4>);
-        case 3: return reinterpret_cast<void*>(&residual_norm_grad_kernel<T, V, 3>);
-        case 2: return reinterpret_cast<void*>(&residual_norm_grad_kernel<T, V, 2>);
-        default: return reinterpret_cast<void*>(&residual_norm_grad_kernel<T, V, 0>);
+        case 3: return full ? reinterpret_cast<void*>(&residual_norm_grad_kernel<T, V, 3, true>)
+                            : reinterpret_cast<void*>(&residual_norm_grad_kernel<T, V, 3, false>);
+        case 2: return full ? reinterpret_cast<void*>(&residual_norm_grad_kernel<T, V, 2, true>)
+                            : reinterpret_cast<void*>(&residual_norm_grad_kernel<T, V, 2, false>);
+        default: return reinterpret_cast<void*>(&residual_norm_grad_kernel<T, V, 0, false>);
     }
 }
 
 // Cuts the rows into items and the items into at most `ctas` shares: without a gate that several
-// rows share, one run of equal pieces; else so many segments a gate that the largest share is the
+// rows share one run of equal pieces; else so many segments a gate that the largest share is the
 // smallest (an item's sums cost about as much as two rows).
 template <typename T>
 int64_t cut_rows(GradArgs<T>* a, int32_t gates, int64_t ctas, int32_t groups) {
     const int64_t turns = cdiv(a->rows, groups);
-    if (!a->want_gate || a->per_gate == 1) {
+    if (gates == 0 || a->per_gate == 1) {
         a->items = a->segments = int32_t(std::max<int64_t>(1, std::min(turns, ctas)));
         a->span = a->rows;
         return a->items;
@@ -767,13 +846,15 @@ int run_backward(const ResidualNormGradArgs& s, const LibCtx& c, cudaStream_t st
         bool vec = s.cols % 8 == 0 && aligned16<T>(s.G.p, s.G.ld, s.gates) && aligned16<T>(s.dG.p, s.dG.ld, s.gates);
         for (const Mat* m : {&s.dS, &s.dH, &s.X, &s.S, &s.dX, &s.dR}) vec = vec && aligned16<T>(m->p, m->ld, s.rows);
         for (const float* w : {s.post, s.pre, static_cast<const float*>(s.dpost), static_cast<const float*>(s.dpre)}) vec = vec && aligned16<float>(w, 0, 1);
-        const int inputs = (s.pre ? 2 : 0) + (s.X.p ? 1 : 0) + (s.dS.p ? 1 : 0) + (s.G.p && s.gates > 1 ? 1 : 0);
-        uint32_t row_bytes = uint32_t(s.cols * sizeof(T)), step = vec ? row_bytes * uint32_t(groups * inputs) : 0;
+        const int inputs = (s.pre ? 2 : 0) + (s.X.p ? 1 : 0) + (s.dS.p ? 1 : 0) + (s.G.p && s.per_gate == 1 ? 1 : 0);
+        uint32_t row_bytes = uint32_t(tpr * 8 * V * sizeof(T)), step = vec ? row_bytes * uint32_t(groups * inputs) : 0;
         const size_t join = groups > 1 ? size_t(threads) * 8 * V * sizeof(float) : 0;
         const size_t most = size_t(threads > 256 ? 220 : 108) * 1024 - join;
-        const int ahead = !vec ? 0 : 4 * step <= most ? 4 : 3 * step <= most ? 3 : 2 * step <= most ? 2 : 0;
+        const int ahead = !vec ? 0 : 3 * step <= most ? 3 : 2 * step <= most ? 2 : 0;
         if (ahead == 0) step = 0;
-        void* kernel = V == 2 ? grad_kernel<T, 2>(ahead) : grad_kernel<T, 1>(ahead);
+        const bool full = s.post && s.pre && s.dS.p && s.dX.p && s.dR.p && a.want_post && a.want_pre &&
+                          !(s.G.p && s.per_gate == 1);
+        void* kernel = V == 2 ? grad_kernel<T, 2>(ahead, full) : grad_kernel<T, 1>(ahead, full);
         const size_t smem = join + size_t(ahead) * step;
         if ((r = raise_kernel_smem(kernel, smem, c.device)) != GBR_OK) return r;
         void* args[] = {&a, &tpr, &row_bytes, &step};
@@ -783,7 +864,7 @@ int run_backward(const ResidualNormGradArgs& s, const LibCtx& c, cudaStream_t st
     count_launch();
     if (runs == 0) return GBR_OK;
     void* args[] = {&sums};
-    e = launch_kernel(reinterpret_cast<void*>(&norm_sums_kernel), dim3(unsigned(cdiv(s.cols, 32)), unsigned(runs)), 256,
+    e = launch_kernel(reinterpret_cast<void*>(&norm_sums_kernel), dim3(unsigned(cdiv(s.cols, 32)), unsigned(runs)), 512,
                       0, 1, args, stream);
     if (e != cudaSuccess) return report_cuda(e, "launching the sums of residual_norm_backward");
     count_launch();

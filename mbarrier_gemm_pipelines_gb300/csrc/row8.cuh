@@ -7,6 +7,7 @@
 // Otherwise they lie `tpr` columns apart, so that a warp touches whole lines at
 // any alignment.
 #pragma once
+#include "activation.cuh"
 #include "gbr_ptx.cuh"
 #include "vec8.cuh"
 
@@ -94,52 +95,85 @@ __device__ __forceinline__ void store_row8(T* row, const float (&x)[8], int v, i
     }
 }
 
+// The same as four pairs, which one instruction multiplies or adds (activation.cuh).
+__device__ __forceinline__ F2 raw_pair(const Raw8<__nv_bfloat16>& r, int i) {
+    return f2(__uint_as_float(r.w[i] << 16), __uint_as_float(r.w[i] & 0xFFFF0000u));
+}
+__device__ __forceinline__ F2 raw_pair(const Raw8<float>& r, int i) {
+    return f2(__uint_as_float(r.w[2 * i]), __uint_as_float(r.w[2 * i + 1]));
+}
+__device__ __forceinline__ float sum_pair(F2 x) {
+    float a, b;
+    split2(x, a, b);
+    return a + b;
+}
+template <typename T, bool VEC>
+__device__ __forceinline__ void load_pairs(F2 (&x)[4], const T* row, int v, int32_t t, int32_t tpr, int32_t cols) {
+    Raw8<T> r;
+    load_raw8<VEC>(r, row, v, t, tpr, cols);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = raw_pair(r, i);
+}
+template <typename T, bool VEC>
+__device__ __forceinline__ void store_pairs(T* row, const F2 (&x)[4], int v, int32_t t, int32_t tpr, int32_t cols) {
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) split2(x[i], y[2 * i], y[2 * i + 1]);
+    store_row8<T, VEC>(row, y, v, t, tpr, cols);
+}
+
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
     for (int d = 16; d > 0; d /= 2) x += __shfl_xor_sync(0xffffffffu, x, d);
     return x;
 }
 
-// Sums of N values (at most 4) over groups of `tpr` threads (a multiple of 32 that divides the block).  Every thread of
-// the block calls it; `buf` is this call's own until the next __syncthreads.  The order of the sum is fixed.
+// Sums of N (1 to 4) values over groups of `tpr` threads (32 times a power of two that divides the block).  Every thread
+// of the block calls it; `buf` is this call's own until the next __syncthreads.  The order of the sum is fixed.
 //
-// Four values take 6 shuffles, not 20: after the first step each half of the warp goes on with two of them, after the
-// second each quarter with one.  (Shuffles bound the gradients' rows: 4096 columns on 16 warps, three sums and one,
-// 50 of them a warp and row one value at a time.)
-template <int N>
-__device__ __forceinline__ void warp_sums(float (&x)[N], int32_t lane) {
-    if (N == 1) {
-        x[0] = warp_sum(x[0]);
-        return;
-    }
+// Several values take the shuffles of little more than one: after the first step each half of the warp goes on with two
+// of four, after the second each quarter with one, whose lanes also join the warps' sums.  (Shuffles and what goes with
+// them bound the gradients' rows: 4096 columns on 16 warps, three sums and one, took 50 shuffles a warp and row one value
+// at a time, 20 this way.)
+__device__ __forceinline__ float fold4(float x0, float x1, float x2, float x3, int32_t lane) {
     const bool upper = lane & 16, odd = lane & 8;
-    const float x2 = N > 2 ? x[N > 2 ? 2 : 0] : 0.f, x3 = N > 3 ? x[N > 3 ? 3 : 0] : 0.f;
-    float a = upper ? x2 : x[0], b = upper ? x3 : x[1];
-    a += __shfl_xor_sync(0xffffffffu, upper ? x[0] : x2, 16);
-    b += __shfl_xor_sync(0xffffffffu, upper ? x[1] : x3, 16);
+    float a = upper ? x2 : x0, b = upper ? x3 : x1;
+    a += __shfl_xor_sync(0xffffffffu, upper ? x0 : x2, 16);
+    b += __shfl_xor_sync(0xffffffffu, upper ? x1 : x3, 16);
     float c = odd ? b : a;
     c += __shfl_xor_sync(0xffffffffu, odd ? a : b, 8);
 #pragma unroll
     for (int d = 4; d > 0; d /= 2) c += __shfl_xor_sync(0xffffffffu, c, d);
-    // Value i is in the lanes from 8 i on.
-#pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = __shfl_sync(0xffffffffu, c, 8 * i);
+    return c;                                           // of value lane / 8
 }
 
 template <int N>
 __device__ __forceinline__ void group_sum(float (&x)[N], float (*buf)[32], int32_t tpr) {
-    const int32_t lane = int32_t(threadIdx.x) % 32;
-    warp_sums(x, lane);
-    if (tpr == 32) return;
-    const int32_t warp = int32_t(threadIdx.x) / 32, warps = tpr / 32;
-    if (lane == 0)
+    const int32_t lane = int32_t(threadIdx.x) % 32, warp = int32_t(threadIdx.x) / 32, warps = tpr / 32;
+    const int32_t first = warp & ~(warps - 1);
+    if (N == 1) {
+        x[0] = warp_sum(x[0]);
+        if (tpr == 32) return;
+        if (lane == 0) buf[0][warp] = x[0];
+        __syncthreads();
+        x[0] = warp_sum(lane < warps ? buf[0][first + lane] : 0.f);
+        return;
+    }
+    float c = fold4(x[0], x[N > 1 ? 1 : 0], N > 2 ? x[N > 2 ? 2 : 0] : 0.f, N > 3 ? x[N > 3 ? 3 : 0] : 0.f, lane);
+    if (tpr > 32) {
+        const int32_t value = lane / 8, l = lane % 8;
+        if (l == 0 && value < N) buf[value][warp] = c;
+        __syncthreads();
+        c = 0.f;
+        if (value < N)
 #pragma unroll
-        for (int i = 0; i < N; ++i) buf[i][warp] = x[i];
-    __syncthreads();
-    const int32_t first = warp / warps * warps;
+            for (int w = 0; w < 32; w += 8)
+                if (w + l < warps) c += buf[value][first + w + l];
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = lane < warps ? buf[i][first + lane] : 0.f;
-    warp_sums(x, lane);
+        for (int d = 4; d > 0; d /= 2) c += __shfl_xor_sync(0xffffffffu, c, d);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = __shfl_sync(0xffffffffu, c, 8 * i);
 }
 
 // Asynchronous copies of a thread's own 16-byte pieces, group by group.
@@ -158,14 +192,28 @@ __device__ __forceinline__ void copy_row8(uint32_t to, const T* row, int v, int3
     for (int i = 0; i < int(sizeof(T) / 2); ++i)
         ptx::cp_async_16(to + uint32_t(c) * uint32_t(sizeof(T)) + 16u * i, reinterpret_cast<const uint8_t*>(row + c) + 16 * i, 16);
 }
+// (What lies past the last column has to be zero there.)
 template <typename T>
-__device__ __forceinline__ void take_row8(Raw8<T>& r, uint32_t from, int v, int32_t t, int32_t tpr, int32_t cols) {
-    const int32_t c = row_col<true>(v, 0, t, tpr);
+__device__ __forceinline__ void take_row8(Raw8<T>& r, uint32_t from, int v, int32_t t, int32_t tpr) {
+    const uint32_t at = from + uint32_t(row_col<true>(v, 0, t, tpr)) * uint32_t(sizeof(T));
 #pragma unroll
     for (int i = 0; i < int(sizeof(T) / 2); ++i) {
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (c < cols) x = ptx::ld_shared_v4(from + uint32_t(c) * uint32_t(sizeof(T)) + 16u * i);
+        const uint4 x = ptx::ld_shared_v4(at + 16u * i);
         r.w[4 * i] = x.x, r.w[4 * i + 1] = x.y, r.w[4 * i + 2] = x.z, r.w[4 * i + 3] = x.w;
+    }
+}
+// Zeroes a thread's places of `rows` rows of `row_bytes` past the last column.
+template <typename T, int V>
+__device__ __forceinline__ void clear_past(uint32_t ring, uint32_t rows, uint32_t row_bytes, int32_t t, int32_t tpr,
+                                           int32_t cols) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int32_t c = row_col<true>(v, 0, t, tpr);
+        if (c < cols) continue;
+        for (uint32_t r = 0; r < rows; ++r)
+#pragma unroll
+            for (int i = 0; i < int(sizeof(T) / 2); ++i)
+                ptx::st_shared_v4(ring + r * row_bytes + uint32_t(c) * uint32_t(sizeof(T)) + 16u * i, 0, 0, 0, 0);
     }
 }
 
