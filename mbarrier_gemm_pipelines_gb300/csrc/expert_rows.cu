@@ -29,7 +29,7 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // then every warp goes over its part again and hands the places out.  Choices
 // of one expert among a warp's 32 are ranked by lane, so the order is that of
 // the choices and nothing depends on timing.
-constexpr int kSortWarps = 32, kSortThreads = kSortWarps * 32, kSortCluster = 8;
+constexpr int kSortThreads = 1024, kSortCluster = 8, kSortBatch = 8;
 
 struct SortParams {
     const int64_t* ids;
@@ -39,40 +39,48 @@ struct SortParams {
 
 __global__ void __launch_bounds__(kSortThreads, 1) moe_sort_kernel(const SortParams p, uint32_t ctas) {
     extern __shared__ int32_t sm[];
+    const int32_t threads = int32_t(blockDim.x), warps = threads / 32;
     int32_t* count = sm;                                // [warps][experts]
-    int32_t* total = count + kSortWarps * p.experts;    // [experts] of this CTA, read by the peers
+    int32_t* total = count + warps * p.experts;         // [experts] of this CTA, read by the peers
     int32_t* start = total + p.experts;                 // [experts] first place of this CTA's choices
     int32_t* sums = start + p.experts;                  // [32]
     ptx::griddep_wait();
     const uint32_t rank = ctas > 1 ? ptx::cluster_ctarank() : 0u;
     const int32_t warp = int32_t(threadIdx.x) / 32, lane = int32_t(threadIdx.x) % 32, E = p.experts;
-    for (int32_t i = int32_t(threadIdx.x); i < kSortWarps * E; i += kSortThreads) count[i] = 0;
+    for (int32_t i = int32_t(threadIdx.x); i < warps * E; i += threads) count[i] = 0;
     __syncthreads();
-    const int64_t part = int64_t(rank) * kSortWarps + warp, parts = int64_t(ctas) * kSortWarps;
+    const int64_t part = int64_t(rank) * warps + warp, parts = int64_t(ctas) * warps;
     const int32_t i0 = int32_t(p.n * part / parts), i1 = int32_t(p.n * (part + 1) / parts);
     int32_t* mine = count + warp * E;
-    auto expert_of = [&](int64_t i) {
-        if (i >= i1) return -1;
-        const int64_t e = p.ids[i];
-        return e >= 0 && e < E ? int32_t(e) : -1;
+    int32_t e[kSortBatch];
+    auto load = [&](int64_t i) {
+#pragma unroll
+        for (int b = 0; b < kSortBatch; ++b) {
+            const int64_t at = i + 32 * b + lane, id = at < i1 ? p.ids[at] : -1;
+            e[b] = id >= 0 && id < E ? int32_t(id) : -1;
+        }
     };
-    for (int64_t i = i0; i < i1; i += 32) {
-        const int32_t e = expert_of(i + lane);
-        const uint32_t same = __match_any_sync(0xffffffffu, e);
-        if (e >= 0 && lane == __ffs(int(same)) - 1) mine[e] += __popc(same);
-        __syncwarp();
+    for (int64_t i = i0; i < i1; i += 32 * kSortBatch) {
+        load(i);
+#pragma unroll
+        for (int b = 0; b < kSortBatch; ++b) {
+            if (i + 32 * b >= i1) break;
+            const uint32_t same = __match_any_sync(0xffffffffu, e[b]);
+            if (e[b] >= 0 && lane == __ffs(int(same)) - 1) mine[e[b]] += __popc(same);
+            __syncwarp();
+        }
     }
     __syncthreads();
     // Over the warps: each warp's count becomes the number of choices of that expert before it.
-    for (int32_t e = int32_t(threadIdx.x); e < E; e += kSortThreads) {
+    for (int32_t x = int32_t(threadIdx.x); x < E; x += threads) {
         int32_t sum = 0;
 #pragma unroll 8
-        for (int32_t w = 0; w < kSortWarps; ++w) {
-            const int32_t c = count[w * E + e];
-            count[w * E + e] = sum;
+        for (int32_t w = 0; w < warps; ++w) {
+            const int32_t c = count[w * E + x];
+            count[w * E + x] = sum;
             sum += c;
         }
-        total[e] = sum;
+        total[x] = sum;
     }
     if (ctas > 1)
         ptx::cluster_sync_all();
@@ -107,15 +115,20 @@ __global__ void __launch_bounds__(kSortThreads, 1) moe_sort_kernel(const SortPar
         }
     }
     __syncthreads();
-    for (int64_t i = i0; i < i1; i += 32) {
-        const int32_t e = expert_of(i + lane);
-        const uint32_t same = __match_any_sync(0xffffffffu, e);
-        int32_t place = -1;
-        if (e >= 0) place = start[e] + mine[e] + __popc(same & ((1u << lane) - 1u));
-        __syncwarp();
-        if (e >= 0 && lane == __ffs(int(same)) - 1) mine[e] += __popc(same);
-        __syncwarp();
-        if (i + lane < i1) p.positions[i + lane] = place;
+    const bool again = i1 - i0 > 32 * kSortBatch;       // else the ids are still in registers
+    for (int64_t i = i0; i < i1; i += 32 * kSortBatch) {
+        if (again) load(i);
+#pragma unroll
+        for (int b = 0; b < kSortBatch; ++b) {
+            if (i + 32 * b >= i1) break;
+            const uint32_t same = __match_any_sync(0xffffffffu, e[b]);
+            int32_t place = -1;
+            if (e[b] >= 0) place = start[e[b]] + mine[e[b]] + __popc(same & ((1u << lane) - 1u));
+            __syncwarp();
+            if (e[b] >= 0 && lane == __ffs(int(same)) - 1) mine[e[b]] += __popc(same);
+            __syncwarp();
+            if (i + 32 * b + lane < i1) p.positions[i + 32 * b + lane] = place;
+        }
     }
     if (ctas > 1) ptx::cluster_sync_all();              // the peers have read `total`
 }
@@ -133,117 +146,209 @@ struct Rows {
     int64_t rows;                                       // of Ys or Xs
 };
 
-// blockDim.x / tpr tokens a CTA; a thread takes every tpr-th vector of the row.
-// The token's k choices stand for k rows of Xs as well: those behind the last
-// expert's are zeroed.
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(512) moe_dispatch_kernel(const Rows<T> a, int32_t tpr) {
-    ptx::griddep_wait();
-    const int32_t t = int32_t(threadIdx.x) % tpr, per = int32_t(blockDim.x) / tpr;
-    const int32_t total = a.offsets[a.experts];
-    for (int64_t row = int64_t(blockIdx.x) * per + int32_t(threadIdx.x) / tpr; row < a.T_; row += int64_t(gridDim.x) * per) {
-        const int32_t* pos = a.positions + row * a.k;
-        for (int32_t c = 0, v = 0; c < a.D; c += tpr * 8, ++v) {
-            float x[8];
-            load_row8<T, VEC>(x, a.X + row * a.ldx, v, t, tpr, a.D);
-            for (int32_t j = 0; j < a.k; ++j) {
-                const int32_t at = pos[j];
-                if (at >= 0 && at < a.rows) store_row8<T, VEC>(a.Xs + at * a.ldxs, x, v, t, tpr, a.D);
-            }
-            const float zero[8] = {};
-            for (int64_t r = row * a.k > total ? row * a.k : int64_t(total); r < (row + 1) * a.k; ++r)
-                store_row8<T, VEC>(a.Xs + r * a.ldxs, zero, v, t, tpr, a.D);
-        }
-    }
+// A CTA takes a run of tokens, whose positions (and weights) it fetches first, so that from then on no load waits for
+// another; blockDim.x / tpr tokens at a time, kV vectors of 8 columns a thread at once.  Taking a token's positions when
+// its turn came: 4096 tokens of 4096 columns and 2 choices 24.8 us dispatched, 42.5 combined.  HELD false: a token is
+// all that a group of threads has, and its places are read as they are wanted (301 tokens of 1000 columns and 6 choices,
+// the gradient: 5.7 us held, 4.5 not); or there are more choices than the CTA holds.
+constexpr int kPlaces = 256;                           // choices that a CTA holds at a time
+
+// The CTA's tokens, in turns of as many as kPlaces choices are of.
+struct TokenRun {
+    int64_t begin, end;
+    int32_t turn;
+};
+template <typename T>
+__device__ __forceinline__ TokenRun token_run(const Rows<T>& a) {
+    return {int64_t(a.T_) * blockIdx.x / gridDim.x, int64_t(a.T_) * (blockIdx.x + 1) / gridDim.x,
+            a.k > 0 && a.k < kPlaces ? kPlaces / a.k : 1};
 }
 
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(512) moe_combine_rows_kernel(const Rows<T> a, int32_t tpr) {
-    ptx::griddep_wait();
-    const int32_t t = int32_t(threadIdx.x) % tpr, per = int32_t(blockDim.x) / tpr;
-    for (int64_t row = int64_t(blockIdx.x) * per + int32_t(threadIdx.x) / tpr; row < a.T_; row += int64_t(gridDim.x) * per) {
-        const int32_t* pos = a.positions + row * a.k;
-        for (int32_t c = 0, v = 0; c < a.D; c += tpr * 8, ++v) {
-            float y[8] = {};
-            for (int32_t j0 = 0; j0 < a.k; j0 += 4) {
-                Raw8<T> x[4];
-                float w[4];
-                bool on[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int32_t at = j0 + j < a.k ? pos[j0 + j] : -1;
-                    on[j] = at >= 0 && at < a.rows;
-                    if (!on[j]) continue;
-                    w[j] = a.weights != nullptr ? a.weights[row * a.k + j0 + j] : 1.f;
-                    load_raw8<VEC>(x[j], a.Ys + at * a.ldys, v, t, tpr, a.D);
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (on[j])
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) y[i] = fmaf(w[j], raw_at(x[j], i), y[i]);
-            }
-            if (a.R != nullptr) {
-                float r[8];
-                load_row8<T, VEC>(r, a.R + row * a.ldr, v, t, tpr, a.D);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] += r[i];
-            }
-            store_row8<T, VEC>(a.Y + row * a.ldy, y, v, t, tpr, a.D);
-        }
+// Positions (-1 where there is no row) and weights of the choices from (token, j0) on into shared memory.
+template <typename T>
+__device__ __forceinline__ void fetch_places(const Rows<T>& a, int64_t first, int32_t n, int32_t* at, float* w) {
+    __syncthreads();                                    // the last turn's have been read
+    for (int32_t i = int32_t(threadIdx.x); i < n; i += int32_t(blockDim.x)) {
+        const int32_t p = a.positions[first + i];
+        at[i] = p >= 0 && p < a.rows ? p : -1;
+        if (w != nullptr) w[i] = a.weights != nullptr ? a.weights[first + i] : 1.f;
     }
+    __syncthreads();
 }
 
-// X is dY, Xs is dYs.  Four choices at a time: their products with dY are summed over the group.
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(512) moe_combine_grad_kernel(const Rows<T> a, int32_t tpr) {
-    __shared__ float buf[4][32];
+template <typename T, bool VEC, int kV, bool HELD>
+__global__ void __launch_bounds__(256, 4) moe_dispatch_kernel(const Rows<T> a, int32_t tpr) {
+    __shared__ int32_t at[kPlaces];
     ptx::griddep_wait();
-    const int32_t t = int32_t(threadIdx.x) % tpr, per = int32_t(blockDim.x) / tpr;
-    const int32_t total = a.Xs != nullptr ? a.offsets[a.experts] : 0;
-    for (int64_t first = int64_t(blockIdx.x) * per; first < a.T_; first += int64_t(gridDim.x) * per) {
-        const int64_t row = first + int32_t(threadIdx.x) / tpr;
-        const bool in = row < a.T_;                     // a group past the end only keeps the barriers
-        for (int32_t j0 = 0; j0 < a.k; j0 += 4) {
-            int32_t at[4];
-            float w[4], dot[4] = {};
+    const int32_t t = int32_t(threadIdx.x) % tpr, group = int32_t(threadIdx.x) / tpr, per = int32_t(blockDim.x) / tpr;
+    const TokenRun run = token_run(a);
+    const int64_t total = a.offsets[a.experts];
+    const float zero[8] = {};
+    for (int64_t first = run.begin; first < run.end; first += run.turn) {
+        const int32_t tokens = int32_t(run.end - first < run.turn ? run.end - first : run.turn);
+        // More choices than the CTA holds: one token, part by part.
+        for (int32_t j0 = 0; j0 < a.k; j0 += kPlaces) {
+            const int32_t k = a.k - j0 < kPlaces ? a.k - j0 : kPlaces;
+            // A piece: kV vectors of a token.  The next one is loaded before this one is stored, the first before the
+            // places are there.
+            const int32_t pieces = (a.D + tpr * 8 * kV - 1) / (tpr * 8 * kV);
+            auto load = [&](Raw8<T> (&x)[kV], int32_t i, int32_t v0) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                at[j] = in && j0 + j < a.k ? a.positions[row * a.k + j0 + j] : -1;
-                if (at[j] >= a.rows) at[j] = -1;
-                w[j] = at[j] >= 0 ? a.weights[row * a.k + j0 + j] : 0.f;
-            }
-            for (int32_t c = 0, v = 0; c < a.D && in; c += tpr * 8, ++v) {
-                float d[8];
-                load_row8<T, VEC>(d, a.X + row * a.ldx, v, t, tpr, a.D);
-                Raw8<T> y[4] = {};
-                if (a.dweights != nullptr)
+                for (int v = 0; v < kV; ++v)
+                    load_raw8<VEC>(x[v], a.X + (first + i) * a.ldx, v0 + v, t, tpr, i < tokens ? a.D : 0);
+            };
+            Raw8<T> next[kV];
+            load(next, group, 0);
+            if (HELD) fetch_places(a, first * a.k + j0, tokens * k, at, nullptr);
+            for (int32_t i = group; i < tokens; i += per) {
+                const int32_t* pos = HELD ? at + i * k : a.positions + (first + i) * a.k + j0;
+                for (int32_t piece = 0; piece < pieces; ++piece) {
+                    const int32_t v0 = piece * kV;
+                    Raw8<T> x[kV];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (at[j] >= 0) load_raw8<VEC>(y[j], a.Ys + at[j] * a.ldys, v, t, tpr, a.D);
+                    for (int v = 0; v < kV; ++v) x[v] = next[v];
+                    if (piece + 1 < pieces) load(next, i, v0 + kV);
+                    else load(next, i + per, 0);
+                    for (int32_t j = 0; j < k; ++j) {
+                        const int32_t to = pos[j];
+                        if (to < 0 || (!HELD && to >= a.rows)) continue;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (at[j] < 0) continue;
-                    float x[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        if (a.dweights != nullptr) dot[j] = fmaf(d[i], raw_at(y[j], i), dot[j]);
-                        x[i] = w[j] * d[i];
+                        for (int v = 0; v < kV; ++v) store_raw8<VEC>(a.Xs + to * a.ldxs, x[v], v0 + v, t, tpr, a.D);
                     }
-                    if (a.Xs != nullptr) store_row8<T, VEC>(a.Xs + at[j] * a.ldxs, x, v, t, tpr, a.D);
-                }
-                if (a.Xs != nullptr && j0 == 0) {
-                    const float zero[8] = {};
-                    for (int64_t r = row * a.k > total ? row * a.k : int64_t(total); r < (row + 1) * a.k; ++r)
-                        store_row8<T, VEC>(a.Xs + r * a.ldxs, zero, v, t, tpr, a.D);
+                    // The token's k choices stand for k rows of Xs as well: those behind the last expert's are zeroed.
+                    const int64_t r0 = (first + i) * a.k + j0;
+                    for (int64_t r = r0 > total ? r0 : total; r < r0 + k; ++r)
+#pragma unroll
+                        for (int v = 0; v < kV; ++v) store_row8<T, VEC>(a.Xs + r * a.ldxs, zero, v0 + v, t, tpr, a.D);
                 }
             }
-            if (a.dweights != nullptr) {
+        }
+    }
+}
+
+// kJ choices at once.
+template <typename T, bool VEC, int kV, int kJ, bool HELD>
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 3) moe_combine_rows_kernel(const Rows<T> a, int32_t tpr) {
+    __shared__ int32_t at[kPlaces];
+    __shared__ float weight[kPlaces];
+    ptx::griddep_wait();
+    const int32_t t = int32_t(threadIdx.x) % tpr, group = int32_t(threadIdx.x) / tpr, per = int32_t(blockDim.x) / tpr;
+    const TokenRun run = token_run(a);
+    for (int64_t first = run.begin; first < run.end; first += run.turn) {
+        const int32_t tokens = int32_t(run.end - first < run.turn ? run.end - first : run.turn);
+        if (HELD) fetch_places(a, first * a.k, tokens * a.k, at, weight);
+        for (int32_t i = group; i < tokens; i += per) {
+            const int64_t row = first + i;
+            for (int32_t v0 = 0; v0 * tpr * 8 < a.D; v0 += kV) {
+                float y[kV][8] = {};
+                Raw8<T> r[kV];
+                if (a.R != nullptr)
+#pragma unroll
+                    for (int v = 0; v < kV; ++v) load_raw8<VEC>(r[v], a.R + row * a.ldr, v0 + v, t, tpr, a.D);
+                for (int32_t j0 = 0; j0 < a.k; j0 += kJ) {
+                    Raw8<T> x[kJ][kV];
+                    float w[kJ];
+                    bool on[kJ];
+#pragma unroll
+                    for (int j = 0; j < kJ; ++j) {
+                        int32_t p = -1;
+                        if (j0 + j < a.k) {
+                            const int64_t c = row * a.k + j0 + j;
+                            p = HELD ? at[i * a.k + j0 + j] : a.positions[c];
+                            w[j] = HELD ? weight[i * a.k + j0 + j] : a.weights != nullptr ? a.weights[c] : 1.f;
+                        }
+                        on[j] = p >= 0 && p < a.rows;
+                        if (!on[j]) continue;
+#pragma unroll
+                        for (int v = 0; v < kV; ++v) load_raw8<VEC>(x[j][v], a.Ys + p * a.ldys, v0 + v, t, tpr, a.D);
+                    }
+#pragma unroll
+                    for (int j = 0; j < kJ; ++j) {
+                        if (!on[j]) continue;
+#pragma unroll
+                        for (int v = 0; v < kV; ++v)
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) y[v][e] = fmaf(w[j], raw_at(x[j][v], e), y[v][e]);
+                    }
+                }
+#pragma unroll
+                for (int v = 0; v < kV; ++v) {
+                    if (a.R != nullptr)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) y[v][e] += raw_at(r[v], e);
+                    store_row8<T, VEC>(a.Y + row * a.ldy, y[v], v0 + v, t, tpr, a.D);
+                }
+            }
+        }
+    }
+}
+
+// X is dY, Xs is dYs.  kJ choices at once: their products with dY are summed over the token's threads.
+template <typename T, bool VEC, int kV, int kJ, bool HELD>
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 3) moe_combine_grad_kernel(const Rows<T> a, int32_t tpr) {
+    __shared__ int32_t at[kPlaces];
+    __shared__ float weight[kPlaces];
+    __shared__ float buf[kJ][32];
+    ptx::griddep_wait();
+    const int32_t t = int32_t(threadIdx.x) % tpr, group = int32_t(threadIdx.x) / tpr, per = int32_t(blockDim.x) / tpr;
+    const TokenRun run = token_run(a);
+    const int64_t total = a.Xs != nullptr ? a.offsets[a.experts] : 0;
+    const bool dots = a.dweights != nullptr, rows_out = a.Xs != nullptr;
+    const float zero[8] = {};
+    for (int64_t first = run.begin; first < run.end; first += run.turn) {
+        const int32_t tokens = int32_t(run.end - first < run.turn ? run.end - first : run.turn);
+        if (HELD) fetch_places(a, first * a.k, tokens * a.k, at, weight);
+        for (int32_t i0 = 0; i0 < tokens; i0 += per) {
+            const int32_t i = i0 + group, cols = i < tokens ? a.D : 0;   // a group past the end only keeps the barriers
+            const int64_t row = first + i;
+            for (int32_t j0 = 0; j0 < a.k; j0 += kJ) {
+                int32_t p[kJ];
+                float w[kJ], dot[kJ];
+#pragma unroll
+                for (int j = 0; j < kJ; ++j) {
+                    p[j] = -1, w[j] = dot[j] = 0.f;
+                    if (i < tokens && j0 + j < a.k) {
+                        const int64_t c = row * a.k + j0 + j;
+                        p[j] = HELD ? at[i * a.k + j0 + j] : a.positions[c];
+                        if (p[j] >= a.rows) p[j] = -1;
+                        if (p[j] >= 0) w[j] = HELD ? weight[i * a.k + j0 + j] : a.weights[c];
+                    }
+                }
+                for (int32_t v0 = 0; v0 * tpr * 8 < cols; v0 += kV) {
+                    Raw8<T> d[kV], y[kJ][kV];
+#pragma unroll
+                    for (int v = 0; v < kV; ++v) load_raw8<VEC>(d[v], a.X + row * a.ldx, v0 + v, t, tpr, cols);
+                    if (dots)
+#pragma unroll
+                        for (int j = 0; j < kJ; ++j)
+#pragma unroll
+                            for (int v = 0; v < kV; ++v)
+                                if (p[j] >= 0) load_raw8<VEC>(y[j][v], a.Ys + p[j] * a.ldys, v0 + v, t, tpr, cols);
+#pragma unroll
+                    for (int j = 0; j < kJ; ++j) {
+                        if (p[j] < 0) continue;
+#pragma unroll
+                        for (int v = 0; v < kV; ++v) {
+                            float x[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                if (dots) dot[j] = fmaf(raw_at(d[v], e), raw_at(y[j][v], e), dot[j]);
+                                x[e] = w[j] * raw_at(d[v], e);
+                            }
+                            if (rows_out) store_row8<T, VEC>(a.Xs + p[j] * a.ldxs, x, v0 + v, t, tpr, cols);
+                        }
+                    }
+                    if (rows_out && j0 == 0)
+                        for (int64_t r = row * a.k > total ? row * a.k : total; r < (row + 1) * a.k; ++r)
+#pragma unroll
+                            for (int v = 0; v < kV; ++v) store_row8<T, VEC>(a.Xs + r * a.ldxs, zero, v0 + v, t, tpr, cols);
+                }
+                if (!dots) continue;
                 group_sum(dot, buf, tpr);
                 if (t == 0)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (in && j0 + j < a.k) a.dweights[row * a.k + j0 + j] = at[j] >= 0 ? dot[j] : 0.f;
+                    for (int j = 0; j < kJ; ++j)
+                        if (i < tokens && j0 + j < a.k) a.dweights[row * a.k + j0 + j] = p[j] >= 0 ? dot[j] : 0.f;
                 if (tpr > 32) __syncthreads();          // buf, for the next choices
             }
         }
@@ -255,30 +360,28 @@ bool aligned16(const Mat& m, int64_t rows) {
     return !m || (reinterpret_cast<uintptr_t>(m.p) % 16 == 0 && (rows <= 1 || m.ld % int64_t(16 / sizeof(T)) == 0));
 }
 
-// Threads a row and in all: the fewest warps that hold a row with one vector each, at most 512.
-struct Shape {
-    int32_t tpr;
-    int threads;
-    unsigned grid;
-};
-Shape shape_for(int32_t D, int32_t T, int sm_count) {
-    Shape s;
-    s.tpr = 32;
-    while (s.tpr < 512 && s.tpr * 8 < D) s.tpr *= 2;
-    s.threads = std::max(256, int(s.tpr));
-    s.grid = unsigned(std::min<int64_t>(cdiv(T, s.threads / s.tpr), int64_t(sm_count) * 16));
-    return s;
+// Threads a row: the fewest warps that hold it with kV vectors each, at most the CTA's 256.
+int32_t threads_for(int32_t D, int kV) {
+    int32_t tpr = 32;
+    while (tpr < 256 && tpr * 8 * kV < D) tpr *= 2;
+    return tpr;
 }
 
+// `kernels`: places held, places read.
 template <typename T>
-int launch_rows(void* kernel, Rows<T> p, const LibCtx& c, const char* what, cudaStream_t stream) {
-    Shape s = shape_for(p.D, p.T_, c.sm_count);
-    void* args[] = {&p, &s.tpr};
-    const cudaError_t e = launch_kernel(kernel, dim3(s.grid), s.threads, 0, 1, args, stream);
+int launch_rows(void* const (&kernels)[2], Rows<T> p, int kV, const LibCtx& c, const char* what, cudaStream_t stream) {
+    int32_t tpr = threads_for(p.D, kV);
+    const int64_t turns = cdiv(p.T_, 256 / tpr), grid = std::min<int64_t>(turns, int64_t(c.sm_count) * 8);
+    void* args[] = {&p, &tpr};
+    void* kernel = kernels[turns > grid && p.k <= kPlaces ? 0 : 1];
+    const cudaError_t e = launch_kernel(kernel, dim3(unsigned(grid)), 256, 0, 1, args, stream);
     if (e != cudaSuccess) return report_cuda(e, what);
     count_launch();
     return GBR_OK;
 }
+
+#define GBR_BOTH(...) \
+    {reinterpret_cast<void*>(&__VA_ARGS__, true>), reinterpret_cast<void*>(&__VA_ARGS__, false>)}
 
 template <typename T>
 int dispatch(const MoeRowsArgs& a, const LibCtx& c, cudaStream_t stream) {
@@ -288,9 +391,9 @@ int dispatch(const MoeRowsArgs& a, const LibCtx& c, cudaStream_t stream) {
     p.positions = a.positions, p.offsets = a.offsets;
     p.T_ = a.T, p.k = a.k, p.D = a.D, p.experts = a.experts, p.rows = int64_t(a.T) * a.k;
     const bool vec = a.D % 8 == 0 && aligned16<T>(a.X, a.T) && aligned16<T>(a.Ys, p.rows);
-    return launch_rows(vec ? reinterpret_cast<void*>(&moe_dispatch_kernel<T, true>)
-                           : reinterpret_cast<void*>(&moe_dispatch_kernel<T, false>),
-                       p, c, "launching moe_dispatch", stream);
+    void* const wide[2] = GBR_BOTH(moe_dispatch_kernel<T, true, 2);
+    void* const any[2] = GBR_BOTH(moe_dispatch_kernel<T, false, 1);
+    return launch_rows(vec ? wide : any, p, vec ? 2 : 1, c, "launching moe_dispatch", stream);
 }
 
 template <typename T>
@@ -302,9 +405,13 @@ int combine(const MoeRowsArgs& a, int64_t rows, const LibCtx& c, cudaStream_t st
     p.positions = a.positions, p.weights = a.weights;
     p.T_ = a.T, p.k = a.k, p.D = a.D, p.rows = rows;
     const bool vec = a.D % 8 == 0 && aligned16<T>(a.Ys, rows) && aligned16<T>(a.R, a.T) && aligned16<T>(a.Y, a.T);
-    return launch_rows(vec ? reinterpret_cast<void*>(&moe_combine_rows_kernel<T, true>)
-                           : reinterpret_cast<void*>(&moe_combine_rows_kernel<T, false>),
-                       p, c, "launching moe_combine", stream);
+    // One or two choices: two vectors a thread; more: one, and four choices at once (eight spill registers: 2000 tokens of
+    // 2048 columns and 6 choices 16.7 us with four, 23.8 with eight).
+    const bool few = vec && a.k <= 2;
+    void* const two[2] = GBR_BOTH(moe_combine_rows_kernel<T, true, 2, 2);
+    void* const four[2] = GBR_BOTH(moe_combine_rows_kernel<T, true, 1, 4);
+    void* const any[2] = GBR_BOTH(moe_combine_rows_kernel<T, false, 1, 4);
+    return launch_rows(!vec ? any : few ? two : four, p, few ? 2 : 1, c, "launching moe_combine", stream);
 }
 
 template <typename T>
@@ -316,22 +423,26 @@ int combine_grad(const MoeCombineGradArgs& a, const LibCtx& c, cudaStream_t stre
     p.positions = a.positions, p.offsets = a.offsets, p.weights = a.weights, p.dweights = a.dweights;
     p.T_ = a.T, p.k = a.k, p.D = a.D, p.experts = a.experts, p.rows = int64_t(a.T) * a.k;
     const bool vec = a.D % 8 == 0 && aligned16<T>(a.dY, a.T) && aligned16<T>(a.Ys, p.rows) && aligned16<T>(a.dYs, p.rows);
-    return launch_rows(vec ? reinterpret_cast<void*>(&moe_combine_grad_kernel<T, true>)
-                           : reinterpret_cast<void*>(&moe_combine_grad_kernel<T, false>),
-                       p, c, "launching moe_combine_backward", stream);
+    const bool few = vec && a.k <= 2;
+    void* const two[2] = GBR_BOTH(moe_combine_grad_kernel<T, true, 2, 2);
+    void* const four[2] = GBR_BOTH(moe_combine_grad_kernel<T, true, 1, 4);
+    void* const any[2] = GBR_BOTH(moe_combine_grad_kernel<T, false, 1, 4);
+    return launch_rows(!vec ? any : few ? two : four, p, few ? 2 : 1, c, "launching moe_combine_backward", stream);
 }
 
 }  // namespace
 
 int launch_moe_sort(const MoeSortArgs& a, const LibCtx& c, cudaStream_t stream) {
     SortParams p = {a.ids, a.positions, a.offsets, a.n, a.experts};
-    uint32_t ctas = a.n > 8192 ? kSortCluster : 1;
-    const size_t smem = (size_t(kSortWarps + 2) * size_t(a.experts) + 32) * sizeof(int32_t);
+    // Few choices: 8 warps, whose counts are sooner added than those of 32 (a thread an expert, so no more experts).
+    uint32_t ctas = a.n > 4096 ? kSortCluster : 1;
+    const int threads = a.n <= 2048 && a.experts <= 256 ? 256 : kSortThreads;
+    const size_t smem = (size_t(threads / 32 + 2) * size_t(a.experts) + 32) * sizeof(int32_t);
     void* kernel = reinterpret_cast<void*>(&moe_sort_kernel);
     const int r = raise_kernel_smem(kernel, smem, c.device);
     if (r != GBR_OK) return r;
     void* args[] = {&p, &ctas};
-    const cudaError_t e = launch_kernel(kernel, dim3(ctas), kSortThreads, smem, int(ctas), args, stream);
+    const cudaError_t e = launch_kernel(kernel, dim3(ctas), threads, smem, int(ctas), args, stream);
     if (e != cudaSuccess) return report_cuda(e, "launching moe_sort");
     count_launch();
     return GBR_OK;

@@ -81,6 +81,36 @@ __device__ __forceinline__ void load_row8(float (&x)[8], const T* row, int v, in
     for (int j = 0; j < 8; ++j) x[j] = raw_at(r, j);
 }
 
+template <bool VEC>
+__device__ __forceinline__ void store_raw8(__nv_bfloat16* row, const Raw8<__nv_bfloat16>& r, int v, int32_t t, int32_t tpr,
+                                           int32_t cols) {
+    if (VEC) {
+        const int32_t c = row_col<true>(v, 0, t, tpr);
+        if (c < cols) *reinterpret_cast<uint4*>(row + c) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int32_t c = row_col<false>(v, j, t, tpr);
+            if (c < cols) row[c] = __ushort_as_bfloat16(uint16_t(j % 2 ? r.w[j / 2] >> 16 : r.w[j / 2] & 0xFFFFu));
+        }
+    }
+}
+template <bool VEC>
+__device__ __forceinline__ void store_raw8(float* row, const Raw8<float>& r, int v, int32_t t, int32_t tpr, int32_t cols) {
+    if (VEC) {
+        const int32_t c = row_col<true>(v, 0, t, tpr);
+        if (c >= cols) return;
+        reinterpret_cast<uint4*>(row + c)[0] = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+        reinterpret_cast<uint4*>(row + c)[1] = make_uint4(r.w[4], r.w[5], r.w[6], r.w[7]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int32_t c = row_col<false>(v, j, t, tpr);
+            if (c < cols) row[c] = __uint_as_float(r.w[j]);
+        }
+    }
+}
+
 template <typename T, bool VEC>
 __device__ __forceinline__ void store_row8(T* row, const float (&x)[8], int v, int32_t t, int32_t tpr, int32_t cols) {
     if (VEC) {
