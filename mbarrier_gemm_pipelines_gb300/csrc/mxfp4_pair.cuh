@@ -21,7 +21,9 @@
 // the two share 64 columns: [0, 256) and [192, 448), scales in [448, 512).  The
 // epilogue takes the shared columns of its tile first, and the next tile's MMAs
 // wait for those alone (and for the tile before, which is done by then): 1.1 us
-// from one tile's last MMA to the next one's first, of 6.8 at K = 4096.
+// from one tile's last MMA to the next one's first, of 6.8 at K = 4096.  Tiles of
+// 192 columns have room for two accumulators, but take in more bytes for the same
+// products: 4096 x 4096 x 14336 90 us with 256 columns, 92 with 192; 8192^3 176 and 196.
 #pragma once
 #include "gemm_umma.cuh"
 #include "mxfp4_tile.cuh"
@@ -37,7 +39,7 @@ constexpr uint32_t kPairStageBytes = 2 * kSliceBytes + 3 * kScaleBytes;
 constexpr int kPairThreads = 640;                      // 4 warps of roles, 16 of the epilogue
 constexpr uint32_t kEpiWarps = 16;
 constexpr uint32_t kSlotBytes = 32 * 64;               // 32 rows x 32 columns bf16
-constexpr uint32_t kPairBarBytes = 256;
+constexpr uint32_t kPairBarBytes = 512;                // 32 barriers and three words
 constexpr size_t kPairSmemBytes = 1024 + kPairStages * kPairStageBytes + kEpiWarps * kSlotBytes + kPairBarBytes;
 constexpr uint32_t kAccStep = 192, kScaleCol = 448, kScaleSet = 32;   // Tensor Memory columns
 

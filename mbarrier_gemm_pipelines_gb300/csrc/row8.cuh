@@ -73,6 +73,16 @@ __device__ __forceinline__ float raw_at(const Raw8<__nv_bfloat16>& r, int j) {
 }
 __device__ __forceinline__ float raw_at(const Raw8<float>& r, int j) { return __uint_as_float(r.w[j]); }
 
+// Eight values of the type, which they hold exactly.
+__device__ __forceinline__ void make_raw8(Raw8<__nv_bfloat16>& r, const float (&x)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.w[i] = (__float_as_uint(x[2 * i]) >> 16) | (__float_as_uint(x[2 * i + 1]) & 0xFFFF0000u);
+}
+__device__ __forceinline__ void make_raw8(Raw8<float>& r, const float (&x)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r.w[i] = __float_as_uint(x[i]);
+}
+
 template <typename T, bool VEC>
 __device__ __forceinline__ void load_row8(float (&x)[8], const T* row, int v, int32_t t, int32_t tpr, int32_t cols) {
     Raw8<T> r;
