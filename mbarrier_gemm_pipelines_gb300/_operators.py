@@ -90,7 +90,8 @@ def residual_norm(X, R=None, post=None, gate=None, scale=1.0, pre=None, eps=1e-6
     X (the block's output), R (the residual stream; None: zero) [rows, cols] bf16
     or fp32; post, pre [cols] fp32 and gate [gates, cols] of X's type may be None.
     gate row i * gates // rows goes with row i: one row is a gate per channel,
-    as many as X has one per element.  Returns (S, H), H None without pre."""
+    as many as X has one per element.  Returns (S, H), H None without pre; S is X
+    itself where nothing is added, scaled or normalised (a model's first norm)."""
     return (_ext or _load()).residual_norm(X, R, post, gate, scale, pre, eps, S, H, stream)
 
 

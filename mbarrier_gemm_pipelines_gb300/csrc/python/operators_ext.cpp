@@ -482,7 +482,10 @@ PyObject* residual_norm_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const bool want_h = a[5] != Py_None;
         if (!want_h && a[8] != Py_None) refuse(PyExc_ValueError, "H needs pre");
         const CallStream st(a[9], dev);
-        const Out S = out_mat(a[7], "S", tX, dev, X.rows, X.cols);
+        // Where nothing is added, scaled or normalised the sum is X itself.
+        const bool same = a[7] == Py_None && a[1] == Py_None && a[2] == Py_None && a[3] == Py_None && scale == 1.0;
+        Out S;
+        if (!same) S = out_mat(a[7], "S", tX, dev, X.rows, X.cols);
         Out H;
         if (want_h) H = out_mat(a[8], "H", tX, dev, X.rows, X.cols);
         // Vectors of no columns have no address.
@@ -491,7 +494,7 @@ PyObject* residual_norm_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
                 return residual_norm(X.p, X.ld, R.p, R.ld, post, G.p, G.ld, G.rows, scale, pre, eps, S.m.p, S.m.ld, H.m.p,
                                      H.m.ld, X.rows, X.cols, type_code(type), st);
             });
-        return Py_BuildValue("NN", S.wrap(), wrap_or_none(want_h, H));
+        return Py_BuildValue("NN", same ? Py_NewRef(a[0]) : S.wrap(), wrap_or_none(want_h, H));
     });
 }
 

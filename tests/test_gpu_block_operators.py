@@ -193,7 +193,8 @@ def test_residual_norm_plain_sum_and_norm_alone(gbr):
     g = rng(3)
     X, w = normal(g, (37, 520)), 1 + normal(g, (520,), 0.1, F32)
     S, H = gbr.residual_norm(X, pre=w)
-    assert torch.equal(S, X)
+    assert S is X
+    assert torch.equal(gbr.residual_norm(X, pre=w, S=torch.empty_like(X))[0], X)
     check_norm(dict(X=X, R=None, post=None, gate=None, scale=1.0, pre=w, eps=1e-6), S, H)
     S, H = gbr.residual_norm(X, X, scale=-1.0)
     assert H is None and not S.any()
@@ -610,3 +611,191 @@ def test_a_stage_that_is_never_filled(gbr):
             gbr.check_device()
         assert torch.equal(gbr.gemm_mxfp4(A, B), want)
         gbr.check_device()
+
+
+# ------------------------------------------------------------ refusals that need tensors of the GPU
+def test_shapes_are_refused(gbr):
+    g = rng(20)
+    X, w = normal(g, (12, 64)), torch.ones(64, device="cuda")
+    ids = torch.zeros(12, 2, device="cuda", dtype=torch.long)
+    p, o = gbr.moe_sort(ids, 4)
+    Q, W = gbr.quantize_mxfp4(X), gbr.quantize_mxfp4(normal(g, (40, 96)))
+    R = normal(g, (12, 63))
+    bad = [
+        lambda: gbr.residual_norm(X, R), lambda: gbr.residual_norm(X, post=w[:63]), lambda: gbr.residual_norm(X, gate=X[:5]),
+        lambda: gbr.residual_norm(X, H=X), lambda: gbr.residual_norm(X, X, pre=w, S=X[:11]), lambda: gbr.residual_norm(X[0]),
+        lambda: gbr.residual_norm(X.t()), lambda: gbr.residual_norm_backward(X, None, None, None, pre=w),
+        lambda: gbr.residual_norm_backward(X, None, None, None, post=w), lambda: gbr.residual_norm_backward(X, X, X, X, needs=(1, 1)),
+        lambda: gbr.moe_sort(ids[0], 4), lambda: gbr.moe_sort(ids, 0), lambda: gbr.moe_sort(ids.t(), 4),
+        lambda: gbr.moe_dispatch(X[:11], p, o), lambda: gbr.moe_dispatch(X, p, o[:1]), lambda: gbr.moe_dispatch(X, p[0], o),
+        lambda: gbr.moe_combine(X, p, w), lambda: gbr.moe_combine(X, p, residual=R),
+        lambda: gbr.moe_combine_backward(X, X, p, o, torch.ones(12, 2, device="cuda")),
+        lambda: gbr.gemm_mxfp4(Q, W), lambda: gbr.gemm_mxfp4(Q, Q, w), lambda: gbr.gemm_mxfp4(Q, Q, act="tanh"),
+        lambda: gbr.gemm_mxfp4(Q._replace(columns=200), Q), lambda: gbr.gemm_mxfp4(Q, Q, C=X),
+        lambda: gbr.dequantize_mxfp4(Q, X=X[:5]), lambda: gbr.quantize_mxfp4(X, out=W),
+    ]
+    for i, call in enumerate(bad):
+        with pytest.raises(ValueError):
+            call()
+            pytest.fail("call %d was taken" % i)
+    for call in (lambda: gbr.residual_norm(X, X.float()), lambda: gbr.moe_sort(ids.int(), 4), lambda: gbr.moe_dispatch(X, p.long(), o),
+                 lambda: gbr.moe_combine(X, p, torch.ones(12, 2, device="cuda", dtype=BF)),
+                 lambda: gbr.dequantize_mxfp4(Q, dtype=torch.float16), lambda: gbr.gemm_mxfp4(Q, Q, residual=X.float())):
+        with pytest.raises(TypeError):
+            call()
+    for call in (lambda: gbr.moe_sort(ids, 1025), lambda: gbr.residual_norm(X, eps=-1.0, pre=w),
+                 lambda: gbr.residual_norm(X, X, S=X[:, :64], scale=float("nan"))):
+        with pytest.raises(gbr.GbrError):
+            call()
+
+
+# ------------------------------------------------------------ as they are used
+def relative(got, want):
+    return (got.double() - want).norm().item() / max(want.norm().item(), 1e-300)
+
+
+ROUNDED = 2.0 ** -9                 # one rounding to bf16, in the norm (see test_gpu_operators.py)
+
+
+def test_normed_feed_forward(gbr):
+    """Outputs and gradients against 64-bit autograd over the same parameters.  Four roundings lie between x and the
+    sum (h, u, y, S) and up to eight on the way back."""
+    import ffn_reference as ffn
+    from mbarrier_gemm_pipelines_gb300 import feed_forward
+    g, T, D, F = rng(30), 300, 264, 520
+    net = feed_forward.NormedFeedForward(D, F, act="gelu_tanh", scale=0.5, seed=3)
+    for t in (net.pre, net.post, net.next):
+        t.copy_(1 + normal(g, (D,), 0.2, F32))
+    net.gate.copy_(normal(g, (1, D)))
+    net.block.b1.copy_(normal(g, (F,), 0.1, F32))
+    x, ds, dn = normal(g, (T, D)), normal(g, (T, D)), normal(g, (T, D))
+    s, n = net.forward(x)
+    grads = net.backward(ds, dn)
+    leaf = {k: v.double().requires_grad_(True) for k, v in dict(x=x, pre=net.pre, post=net.post, gate=net.gate, next=net.next,
+                                                                W1=net.block.W1, b1=net.block.b1, W2=net.block.W2,
+                                                                b2=net.block.b2).items()}
+
+    def rms(t, w):
+        return t / torch.sqrt(t.square().mean(1, keepdim=True) + net.eps) * w
+    h = rms(leaf["x"], leaf["pre"])
+    y = ffn.act(h @ leaf["W1"] + leaf["b1"], "gelu_tanh") @ leaf["W2"] + leaf["b2"]
+    want_s = leaf["x"] + net.scale * leaf["gate"] * rms(y, leaf["post"])
+    want_n = rms(want_s, leaf["next"])
+    want = dict(zip(leaf, torch.autograd.grad((want_s * ds.double()).sum() + (want_n * dn.double()).sum(), list(leaf.values()))))
+    assert relative(s, want_s) <= 4 * ROUNDED and relative(n, want_n) <= 5 * ROUNDED
+    for k, v in want.items():
+        assert relative(grads[k], v) <= 8 * ROUNDED, k
+    gbr.check_device()
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("padded", [False, True])
+def test_sorted_experts(gbr, gated, padded):
+    """More tokens than moe_layer takes, against the definition over the routing that was made; a padded batch."""
+    import ffn_reference as ffn
+    from mbarrier_gemm_pipelines_gb300 import feed_forward
+    g, T, D, F, E, k = rng(31), 200, 136, 264, 6, 2
+    net = feed_forward.ExpertFeedForward(D, F, experts=E, top_k=k, act="silu", gated=gated, seed=4)
+    net.b1.copy_(normal(g, net.b1.shape, 0.1, F32)), net.b2.copy_(normal(g, net.b2.shape, 0.1, F32))
+    x, dy = normal(g, (T, D)), normal(g, (T, D))
+    live = torch.arange(T, device="cuda") < (150 if padded else T)
+    y = net.forward_sorted(x, live if padded else None)
+    _, ids, weights, positions, offsets = net._saved[:5]
+    assert int(offsets[-1]) == int(live.sum()) * k
+    leaf = {n: getattr(net, n).double().requires_grad_(True) for n in ("Wr", "W1", "b1", "W2", "b2")}
+    leaf["x"] = x.double().requires_grad_(True)
+    w = torch.softmax((leaf["x"] @ leaf["Wr"]).gather(1, ids.clamp(min=0)), 1)
+    assert (w - weights)[live].abs().max() <= 1e-5
+    want = torch.zeros(T, D, device="cuda", dtype=torch.float64)
+    for e in range(E):
+        t, j = torch.nonzero(ids == e, as_tuple=True)
+        z = leaf["x"][t] @ leaf["W1"][e] + leaf["b1"][e]
+        h = ffn.act(z[:, :F], "silu") * z[:, F:] if gated else ffn.act(z, "silu")
+        want = want.index_add(0, t, w[t, j][:, None] * (h @ leaf["W2"][e] + leaf["b2"][e]))
+    assert relative(y, want) <= 4 * ROUNDED
+    assert not y[~live].any()
+    if gated:
+        with pytest.raises(NotImplementedError):
+            net.backward(dy)
+        return
+    grads = net.backward(dy)
+    exact = dict(zip(leaf, torch.autograd.grad((want * dy.double()).sum(), list(leaf.values()))))
+    for n, v in exact.items():
+        assert relative(grads[n], v) <= 8 * ROUNDED, n
+    assert not grads["x"][~live].any()
+    gbr.check_device()
+
+
+def test_sorted_experts_agree_with_the_layer_for_few_tokens(gbr):
+    from mbarrier_gemm_pipelines_gb300 import feed_forward
+    net = feed_forward.ExpertFeedForward(264, 520, experts=8, top_k=2, act="gelu", seed=5)
+    x = normal(rng(32), (60, 264))
+    few, many = net.forward(x), net.forward_sorted(x)
+    assert relative(many, few.double()) <= 4 * ROUNDED
+    assert net.forward(torch.cat([x, x])).shape == (120, 264)
+
+
+def test_feed_forward_in_4_bits(gbr):
+    """Against the definition with the same roundings: the hidden values, rounded to bf16, may fall to the other side of
+    a 4-bit border (half a step of up to 1/4 of a value, in about one value of 64), so the second product is compared on
+    the hidden values that were served."""
+    from mbarrier_gemm_pipelines_gb300 import feed_forward
+    block = feed_forward.FeedForward(512, 1056, act="silu", seed=6)
+    x = normal(rng(33), (70, 512))
+    net = feed_forward.FeedForward4Bit(block)
+    y = net.forward(x)
+    xq, W1, W2 = ref.quantize(x)[0], ref.quantize(block.W1.t())[0], ref.quantize(block.W2.t())[0]
+    h = gbr.gemm_mxfp4(gbr.quantize_mxfp4(x), net.W1, net.b1, act="silu")
+    assert relative(h, ref.linear(xq, W1, net.b1, None, "silu")) <= 1.0625 * ROUNDED
+    assert relative(y, ref.linear(ref.quantize(h)[0], W2, net.b2, x, "none")) <= 1.0625 * ROUNDED
+
+
+def test_example_runs(gbr):
+    from mbarrier_gemm_pipelines_gb300 import feed_forward
+    for name, t in feed_forward.example_forms(T=130, D=256, F=512).items():
+        assert t.shape == (130, 256) and torch.isfinite(t.float()).all(), name
+
+
+# ------------------------------------------------------------ past 32-bit offsets
+def test_offsets_past_32_bits(gbr):
+    """Row strides and matrices that leave 2^31 elements behind them: the last rows against the definition."""
+    free = torch.cuda.mem_get_info()[0]
+    if free < 60 << 30:
+        pytest.skip("needs 60 GB")
+    g = rng(40)
+    pitch = 1 << 28
+    wide = torch.zeros(16, pitch, device="cuda", dtype=BF)      # 2^32 elements
+    X = wide[:, 8:1032]
+    X.copy_(normal(g, (16, 1024)))
+    w = 1 + normal(g, (1024,), 0.1, F32)
+    S, H = gbr.residual_norm(X, X, post=w, pre=w)
+    check_norm(dict(X=X.contiguous(), R=X.contiguous(), post=w, gate=None, scale=1.0, pre=w, eps=1e-6), S, H)
+    a = dict(dS=X, dH=X, X=X, S=X, post=w, gate=None, scale=1.0, pre=w, eps=1e-6)
+    check_norm_grads({k: v.contiguous() if torch.is_tensor(v) else v for k, v in a.items()}, gbr.residual_norm_backward(**a))
+    ids = torch.arange(16, device="cuda").flip(0)[:, None].contiguous()
+    p, o = gbr.moe_sort(ids, 16)
+    Xs = gbr.moe_dispatch(X, p, o)
+    assert torch.equal(Xs, X.flip(0))
+    assert torch.equal(gbr.moe_combine(X, p), X.flip(0))
+    dYs, dw = gbr.moe_combine_backward(X, X, p, o, torch.ones(16, 1, device="cuda"))
+    assert torch.equal(dYs, X.flip(0))
+    Q = gbr.quantize_mxfp4(X)
+    check_quantized(Q, X.contiguous())
+    back = gbr.dequantize_mxfp4(Q, X=wide[:, 4096:5120])
+    assert torch.equal(back.double(), ref.values(Q))
+    C = gbr.gemm_mxfp4(Q, Q, C=wide[:, 8192:8208])
+    x = ref.values(Q)
+    within(C, x @ x.t(), gemm_bar(x, x, 1024) + 2.0 ** -22 * (x @ x.t()).abs(), "C")
+    del wide, X, back, C
+    # Data of more than 2^31 bytes: 70000 rows of 65536 values.
+    rows, cols = 70000, 65536
+    X = torch.empty(rows, cols, device="cuda", dtype=BF)
+    X.copy_(normal(g, (1, cols)).expand(rows, cols))
+    X[-1] = normal(g, (cols,), 3.0)
+    Q = gbr.quantize_mxfp4(X)
+    tail = gbr.quantize_mxfp4(X[-1:].contiguous())
+    assert torch.equal(Q.data[-1], tail.data[0])
+    assert torch.equal(ref.scale_bytes(Q.scales, rows, cols // 32)[-1], ref.scale_bytes(tail.scales, 1, cols // 32)[0])
+    back = gbr.dequantize_mxfp4(Q)
+    assert torch.equal(back[-1], gbr.dequantize_mxfp4(tail)[0]) and torch.equal(back[0], back[rows - 2])
+    gbr.check_device()
