@@ -285,14 +285,16 @@ struct RowWalk {
 // its columns; groups are joined in order through shared memory.  kAhead > 0 (rows on 16 bytes): that many
 // turns' rows of all inputs are on their way into shared memory, each thread its own 16 bytes, so that nobody
 // waits for another's copy; 0: they are loaded in their turn, any alignment.
-// FULL: a training step's call, with both norms, dS and all of dX, dR, dpost and dpre, without a gate an element; what
-// is there need not be asked then (4096 x 4096: 631 instructions a warp and row if it is).
+// FULL: a training step's call, with both norms, dS and all of dX, dR, dpost and dpre, without a gate an element.  What
+// is there need not be asked then (4096 x 4096: 631 instructions a warp and row of 8 columns a thread if it is, 447 not),
+// and the registers are kept for the row: the weights lie in shared memory, each thread's where it alone reads them, and
+// dpost's sum in its place in scratch, added to after a gate's rows.
 template <typename T, int V, int kAhead, bool FULL>
 __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<T> a, int32_t tpr, uint32_t row_bytes,
                                                                  uint32_t step) {
     constexpr bool VEC = kAhead > 0;
     __shared__ float buf[2][3][32];
-    // The ring; behind it, where groups > 1, [groups][tpr * 8 * V] floats.
+    // The ring; behind it, where groups > 1, [groups][8][tpr] floats.
     extern __shared__ __align__(16) uint8_t ring[];
     ptx::griddep_wait();
     const int32_t t = int32_t(threadIdx.x) % tpr, group = int32_t(threadIdx.x) / tpr;
@@ -308,32 +310,34 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<
     // Weights, and sums: dpre and dpost over all rows, ds X q over an item's.  dgate and dpost of rows that share a gate
     // are that last sum times what does not change with the row.
     F2 wpost[V][4], wpre[V][4], spost[V][4], spre[V][4], srun[V][4];
+    // FULL: this thread's part of the weights, then of gate times weight.
+    const uint32_t own = ptx::smem_addr(ring) + kAhead * step + (groups > 1 ? 32u * blockDim.x : 0u) + 16u * threadIdx.x;
+    const uint32_t own_gw = own + 32u * V * blockDim.x;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         if (gate_rows && post) load_pairs<float, VEC>(wpost[v], a.post, v, t, tpr, a.cols);
         if (pre) load_pairs<float, VEC>(wpre[v], a.pre, v, t, tpr, a.cols);
+        if (FULL) put_pairs(own + uint32_t(v) * 32u * blockDim.x, wpre[v]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) spost[v][i] = spre[v][i] = srun[v][i] = f2(0.f);
     }
-    // Adds the groups' sums in order; the result is in group 0.
+    // Adds the groups' sums in order, a vector at a time; the result is in group 0.
     float* joined = reinterpret_cast<float*>(ring) + kAhead * step / sizeof(float);
     auto join = [&](F2 (&s)[V][4]) {
         if (groups == 1) return;
-        __syncthreads();
 #pragma unroll
-        for (int v = 0; v < V; ++v)
+        for (int v = 0; v < V; ++v) {
+            __syncthreads();
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                split2(s[v][i], joined[(group * V * 8 + v * 8 + 2 * i) * tpr + t], joined[(group * V * 8 + v * 8 + 2 * i + 1) * tpr + t]);
-        __syncthreads();
-        if (group != 0) return;
-#pragma unroll
-        for (int v = 0; v < V; ++v)
+                split2(s[v][i], joined[(group * 8 + 2 * i) * tpr + t], joined[(group * 8 + 2 * i + 1) * tpr + t]);
+            __syncthreads();
+            if (group != 0) continue;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 for (int32_t g = 1; g < groups; ++g)
-                    s[v][i] = add2(s[v][i], f2(joined[(g * V * 8 + v * 8 + 2 * i) * tpr + t],
-                                               joined[(g * V * 8 + v * 8 + 2 * i + 1) * tpr + t]));
+                    s[v][i] = add2(s[v][i], f2(joined[(g * 8 + 2 * i) * tpr + t], joined[(g * 8 + 2 * i + 1) * tpr + t]));
+        }
     };
     // The inputs of a row in the ring, in this order: dH and S, X, dS, the gate.
     const uint32_t ring0 = ptx::smem_addr(ring) + uint32_t(group) * row_bytes, at_x = pre ? 2 : 0;
@@ -380,6 +384,7 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<
                 if (run_gate) load_pairs<T, VEC>(w, gate, v, t, tpr, a.cols);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) gw[v][i] = !run_gate ? gw[v][i] : post ? mul2(gw[v][i], w[i]) : w[i];
+                if (FULL) put_pairs(own_gw + uint32_t(v) * 32u * blockDim.x, gw[v]);
             }
         for (int64_t first = r0; first < r1; first += groups) {
             const int64_t row = first + group;
@@ -415,13 +420,15 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<
             F2 ss = f2(0.f), us = f2(0.f), xx = f2(0.f);
             if (pre)
 #pragma unroll
-                for (int v = 0; v < V; ++v)
+                for (int v = 0; v < V; ++v) {
+                    if (FULL) get_pairs(wpre[v], own + uint32_t(v) * 32u * blockDim.x);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const F2 S = raw_pair(s[v], i);
                         ss = fma2(S, S, ss);
                         us = fma2(mul2(raw_pair(dh[v], i), wpre[v][i]), S, us);
                     }
+                }
             if (post)
 #pragma unroll
                 for (int v = 0; v < V; ++v)
@@ -443,13 +450,15 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<
             if (pre) {
                 const F2 r2 = f2(r), m2 = f2(-rc);
 #pragma unroll
-                for (int v = 0; v < V; ++v)
+                for (int v = 0; v < V; ++v) {
+                    if (FULL) get_pairs(wpre[v], own + uint32_t(v) * 32u * blockDim.x);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const F2 S = raw_pair(s[v], i), H = raw_pair(dh[v], i);
                         d[v][i] = fma2(S, m2, fma2(r2, mul2(H, wpre[v][i]), d[v][i]));
                         spre[v][i] = fma2(H, mul2(S, r2), spre[v][i]);
                     }
+                }
             }
             if (want_r)
 #pragma unroll
@@ -474,7 +483,8 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<
                 }
             } else if (weighted) {
 #pragma unroll
-                for (int v = 0; v < V; ++v)
+                for (int v = 0; v < V; ++v) {
+                    if (FULL) get_pairs(gw[v], own_gw + uint32_t(v) * 32u * blockDim.x);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const F2 X = raw_pair(x[v], i);
@@ -482,6 +492,7 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<
                         d[v][i] = mul2(d[v][i], gw[v][i]);
                         dot = fma2(d[v][i], X, dot);
                     }
+                }
             }
             // The slot has been read into registers that the lines above have used.
             if (kAhead > 0) {
@@ -510,19 +521,27 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<
         }
         if (want_run) {
             // dpost gains scale gate sum, dgate is scale weight sum.
-            if (want_post)
+            if (FULL) join(srun);
+            if (want_post && (!FULL || group == 0))
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     F2 w[4];
+                    float* sum = a.post_part + int64_t(blockIdx.x) * a.cols;
                     if (run_gate) load_pairs<T, VEC>(w, gate, v, t, tpr, a.cols);
+                    if (FULL && item > i0) load_pairs<float, VEC>(spost[v], sum, v, t, tpr, a.cols);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const F2 k = run_gate ? mul2(f2(a.scale), w[i]) : f2(a.scale);
                         spost[v][i] = fma2(srun[v][i], k, spost[v][i]);
                     }
+                    if (FULL) {
+                        store_pairs<float, VEC>(sum, spost[v], v, t, tpr, a.cols);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) spost[v][i] = f2(0.f);
+                    }
                 }
             if (a.want_gate) {
-                join(srun);
+                if (!FULL) join(srun);
                 if (group == 0)
 #pragma unroll
                     for (int v = 0; v < V; ++v) {
@@ -546,7 +565,7 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<
         }
     }
     if (kAhead > 0) copy_async_wait<0>();
-    if (want_post) {
+    if (want_post && !FULL) {
         join(spost);
         if (group == 0)
 #pragma unroll
@@ -562,87 +581,139 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<
     }
 }
 
-// Rows that no CTA can hold: their means first (a CTA a row), then everything else column by column.
-template <typename T>
-__device__ __forceinline__ float sum_grad_at(const GradArgs<T>& a, int64_t row, int32_t c, float r, float rc) {
-    float e = a.dS != nullptr ? to_f32(a.dS[row * a.ldds + c]) : 0.f;
-    if (a.pre != nullptr) {
-        const float h = to_f32(a.dH[row * a.lddh + c]);
-        e = e + r * (h * a.pre[c]) - to_f32(a.S[row * a.lds + c]) * rc;
-    }
-    return e;
-}
+// Rows that no CTA holds with what goes with them: their means first (a CTA a row), then everything else column by
+// column, 8 of them a thread.
+constexpr int kLongThreads = 256;
 
 // stats[row] = {r, r^3 mean(u S), q, q^3 mean(v X)}
-template <typename T>
-__global__ void __launch_bounds__(1024) residual_norm_stats_kernel(const GradArgs<T> a, float4* stats) {
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(1024, 1) residual_norm_stats_kernel(const GradArgs<T> a, float4* stats) {
     __shared__ float buf[2][3][32];
     ptx::griddep_wait();
+    const bool pre = a.pre != nullptr, post = a.post != nullptr;
+    const int32_t t = int32_t(threadIdx.x), pieces = (a.cols + 8191) / 8192;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-        float sum[3] = {}, dot[1] = {};
-        for (int32_t c = int32_t(threadIdx.x); c < a.cols; c += 1024) {
-            if (a.pre != nullptr) {
-                const float s = to_f32(a.S[row * a.lds + c]);
-                sum[0] = fmaf(s, s, sum[0]);
-                sum[1] = fmaf(to_f32(a.dH[row * a.lddh + c]) * a.pre[c], s, sum[1]);
+        F2 ss = f2(0.f), us = f2(0.f), xx = f2(0.f), vx = f2(0.f);
+        for (int32_t p = 0; p < pieces; ++p) {
+            Raw8<T> s, dh, x;
+            F2 w[4];
+            if (pre) {
+                load_raw8<VEC>(s, a.S + row * a.lds, p, t, 1024, a.cols);
+                load_raw8<VEC>(dh, a.dH + row * a.lddh, p, t, 1024, a.cols);
+                load_pairs<float, VEC>(w, a.pre, p, t, 1024, a.cols);
             }
-            if (a.post != nullptr) {
-                const float x = to_f32(a.X[row * a.ldx + c]);
-                sum[2] = fmaf(x, x, sum[2]);
+            if (post) load_raw8<VEC>(x, a.X + row * a.ldx, p, t, 1024, a.cols);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (pre) {
+                    ss = fma2(raw_pair(s, i), raw_pair(s, i), ss);
+                    us = fma2(mul2(raw_pair(dh, i), w[i]), raw_pair(s, i), us);
+                }
+                if (post) xx = fma2(raw_pair(x, i), raw_pair(x, i), xx);
             }
         }
+        float sum[3] = {sum_pair(ss), sum_pair(us), sum_pair(xx)};
         group_sum(sum, buf[0], 1024);
         const float r = root(sum[0], a.inv_cols, a.eps), rc = r * r * r * sum[1] * a.inv_cols;
-        const float q = a.post != nullptr ? root(sum[2], a.inv_cols, a.eps) : 1.f;
-        if (a.post != nullptr)
-            for (int32_t c = int32_t(threadIdx.x); c < a.cols; c += 1024) {
-                float e = a.scale * sum_grad_at(a, row, c, r, rc);
-                if (a.G != nullptr) e *= to_f32(a.G[row / a.per_gate * a.ldg + c]);
-                dot[0] = fmaf(e * a.post[c], to_f32(a.X[row * a.ldx + c]), dot[0]);
+        const float q = post ? root(sum[2], a.inv_cols, a.eps) : 1.f;
+        if (post)
+            for (int32_t p = 0; p < pieces; ++p) {
+                Raw8<T> s, dh, x, ds = {}, g;
+                F2 w[4], wp[4];
+                if (pre) {
+                    load_raw8<VEC>(s, a.S + row * a.lds, p, t, 1024, a.cols);
+                    load_raw8<VEC>(dh, a.dH + row * a.lddh, p, t, 1024, a.cols);
+                    load_pairs<float, VEC>(w, a.pre, p, t, 1024, a.cols);
+                }
+                load_raw8<VEC>(x, a.X + row * a.ldx, p, t, 1024, a.cols);
+                load_pairs<float, VEC>(wp, a.post, p, t, 1024, a.cols);
+                if (a.dS != nullptr) load_raw8<VEC>(ds, a.dS + row * a.ldds, p, t, 1024, a.cols);
+                if (a.G != nullptr) load_raw8<VEC>(g, a.G + row / a.per_gate * a.ldg, p, t, 1024, a.cols);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    F2 e = raw_pair(ds, i);
+                    if (pre) e = fma2(raw_pair(s, i), f2(-rc), fma2(f2(r), mul2(raw_pair(dh, i), w[i]), e));
+                    if (a.G != nullptr) e = mul2(e, raw_pair(g, i));
+                    vx = fma2(mul2(e, wp[i]), raw_pair(x, i), vx);
+                }
             }
+        float dot[1] = {sum_pair(vx)};
         group_sum(dot, buf[1], 1024);
-        if (threadIdx.x == 0) stats[row] = make_float4(r, rc, q, q * q * q * dot[0] * a.inv_cols);
+        if (threadIdx.x == 0) stats[row] = make_float4(r, rc, q, a.scale * (q * q * q * dot[0] * a.inv_cols));
     }
 }
 
-// A column a thread; blockIdx.y: the share of the items.
-template <typename T>
-__global__ void __launch_bounds__(256) residual_norm_grad_long_kernel(const GradArgs<T> a, const float4* stats) {
+// blockIdx.x: the columns; blockIdx.y: the share of the items.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kLongThreads, 2) residual_norm_grad_long_kernel(const GradArgs<T> a, const float4* stats) {
     ptx::griddep_wait();
-    const int32_t c = int32_t(blockIdx.x) * 256 + int32_t(threadIdx.x);
-    if (c >= a.cols) return;
+    // Eight columns of the CTA's 2048 a thread.
+    const int32_t c0 = int32_t(blockIdx.x) * kLongThreads * 8, t = int32_t(threadIdx.x), tpr = kLongThreads, cols = a.cols - c0;
     const int32_t i0 = int32_t(int64_t(a.items) * blockIdx.y / gridDim.y);
     const int32_t i1 = int32_t(int64_t(a.items) * (blockIdx.y + 1) / gridDim.y);
-    const float wpost = a.post != nullptr ? a.post[c] : 1.f;
-    float spost = 0.f, spre = 0.f;
+    const bool pre = a.pre != nullptr, post = a.post != nullptr, gate_rows = a.G != nullptr && a.per_gate == 1;
+    const bool run_gate = a.G != nullptr && !gate_rows;
+    F2 wpost[4], wpre[4], spost[4], spre[4];
+    if (post) load_pairs<float, VEC>(wpost, a.post + c0, 0, t, tpr, cols);
+    if (pre) load_pairs<float, VEC>(wpre, a.pre + c0, 0, t, tpr, cols);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        spost[i] = spre[i] = f2(0.f);
+        if (!post) wpost[i] = f2(1.f);
+    }
     for (int32_t item = i0; item < i1; ++item) {
         const int32_t g = item / a.segments, seg = item % a.segments;
         const int64_t base = int64_t(g) * a.span;
         const int64_t r0 = base + int64_t(a.span) * seg / a.segments, r1 = base + int64_t(a.span) * (seg + 1) / a.segments;
-        float sgate = 0.f;
+        F2 srun[4], gate[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) srun[i] = f2(0.f), gate[i] = f2(1.f);
+        if (run_gate) load_pairs<T, VEC>(gate, a.G + g * a.ldg + c0, 0, t, tpr, cols);
+#pragma unroll 2
         for (int64_t row = r0; row < r1; ++row) {
             const float4 st = stats[row];
-            float e = sum_grad_at(a, row, c, st.x, st.y);
-            if (a.pre != nullptr) spre = fmaf(to_f32(a.dH[row * a.lddh + c]), to_f32(a.S[row * a.lds + c]) * st.x, spre);
-            if (a.dR != nullptr) from_f32(e, a.dR + row * a.lddr + c);
-            e *= a.scale;
-            const float x = a.X != nullptr ? to_f32(a.X[row * a.ldx + c]) : 0.f, n = x * st.z;
-            const float dg = e * n * wpost;
-            sgate += dg;
-            if (a.want_gate && a.per_gate == 1) from_f32(dg, a.dG + row * a.lddg + c);
-            if (a.G != nullptr) e *= to_f32(a.G[row / a.per_gate * a.ldg + c]);
-            spost = fmaf(e, n, spost);
-            if (a.dX != nullptr) from_f32(a.post != nullptr ? st.z * (e * wpost) - x * st.w : e, a.dX + row * a.lddx + c);
+            Raw8<T> s, dh, x = {}, ds = {};
+            if (pre) {
+                load_raw8<VEC>(s, a.S + row * a.lds + c0, 0, t, tpr, cols);
+                load_raw8<VEC>(dh, a.dH + row * a.lddh + c0, 0, t, tpr, cols);
+            }
+            if (a.X != nullptr) load_raw8<VEC>(x, a.X + row * a.ldx + c0, 0, t, tpr, cols);
+            if (a.dS != nullptr) load_raw8<VEC>(ds, a.dS + row * a.ldds + c0, 0, t, tpr, cols);
+            if (gate_rows) load_pairs<T, VEC>(gate, a.G + row * a.ldg + c0, 0, t, tpr, cols);
+            F2 e[4], dg[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                e[i] = raw_pair(ds, i);
+                if (pre) {
+                    const F2 S = raw_pair(s, i), H = raw_pair(dh, i);
+                    e[i] = fma2(S, f2(-st.y), fma2(f2(st.x), mul2(H, wpre[i]), e[i]));
+                    spre[i] = fma2(H, mul2(S, f2(st.x)), spre[i]);
+                }
+            }
+            if (a.dR != nullptr) store_pairs<T, VEC>(a.dR + row * a.lddr + c0, e, 0, t, tpr, cols);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const F2 X = raw_pair(x, i), n = mul2(X, f2(st.z));
+                e[i] = mul2(e[i], f2(a.scale));
+                dg[i] = mul2(e[i], mul2(n, wpost[i]));
+                srun[i] = add2(srun[i], dg[i]);
+                e[i] = mul2(e[i], gate[i]);
+                spost[i] = fma2(e[i], n, spost[i]);
+                e[i] = mul2(mul2(e[i], wpost[i]), f2(st.z));
+                if (post) e[i] = fma2(X, f2(-st.w), e[i]);
+            }
+            if (a.want_gate && gate_rows) store_pairs<T, VEC>(a.dG + row * a.lddg + c0, dg, 0, t, tpr, cols);
+            if (a.dX != nullptr) store_pairs<T, VEC>(a.dX + row * a.lddx + c0, e, 0, t, tpr, cols);
         }
-        if (a.want_gate && a.per_gate != 1) {
+        if (a.want_gate && !gate_rows) {
             if (a.segments > 1)
-                a.gate_part[int64_t(item) * a.cols + c] = sgate;
+                store_pairs<float, VEC>(a.gate_part + int64_t(item) * a.cols + c0, srun, 0, t, tpr, cols);
             else
-                from_f32(sgate, a.dG + g * a.lddg + c);
+                store_pairs<T, VEC>(a.dG + g * a.lddg + c0, srun, 0, t, tpr, cols);
         }
     }
-    if (a.want_post) a.post_part[int64_t(blockIdx.y) * a.cols + c] = spost;
-    if (a.want_pre) a.pre_part[int64_t(blockIdx.y) * a.cols + c] = spre;
+    if (a.want_post) store_pairs<float, VEC>(a.post_part + int64_t(blockIdx.y) * a.cols + c0, spost, 0, t, tpr, cols);
+    if (a.want_pre) store_pairs<float, VEC>(a.pre_part + int64_t(blockIdx.y) * a.cols + c0, spre, 0, t, tpr, cols);
 }
 
 // Sums of runs of `count` rows of a [runs * count, cols] fp32 matrix, 32 columns a CTA: the rows dealt to
@@ -759,10 +830,10 @@ template <typename T, int V>
 void* grad_kernel(int ahead, bool full) {
     switch (ahead) {
         case 3: return full ? reinterpret_cast<void*>(&residual_norm_grad_kernel<T, V, 3, true>)
-                            : reinterpret_cast<void*>(&residual_norm_grad_kernel<T, V, 3, false>);
+                            : reinterpret_cast<void*>(&residual_norm_grad_kernel<T, 1, 3, false>);
         case 2: return full ? reinterpret_cast<void*>(&residual_norm_grad_kernel<T, V, 2, true>)
-                            : reinterpret_cast<void*>(&residual_norm_grad_kernel<T, V, 2, false>);
-        default: return reinterpret_cast<void*>(&residual_norm_grad_kernel<T, V, 0, false>);
+                            : reinterpret_cast<void*>(&residual_norm_grad_kernel<T, 1, 2, false>);
+        default: return reinterpret_cast<void*>(&residual_norm_grad_kernel<T, 1, 0, false>);
     }
 }
 
@@ -800,13 +871,37 @@ int run_backward(const ResidualNormGradArgs& s, const LibCtx& c, cudaStream_t st
     a.rows = s.rows, a.cols = s.cols, a.per_gate = s.per_gate;
     a.scale = s.scale, a.eps = s.eps, a.inv_cols = float(1.0 / double(s.cols));
     a.want_post = s.dpost != nullptr, a.want_pre = s.dpre != nullptr, a.want_gate = s.dG.p != nullptr && s.gates > 0;
-    const bool long_rows = s.cols > 8192;
-    const int V = s.cols > 4096 ? 2 : 1;
-    int32_t tpr = long_rows ? 1024 : threads_for(s.cols, V);
-    const int threads = std::max(256, int(tpr)), groups = long_rows ? 1 : threads / tpr;
-    const int64_t col_ctas = cdiv(s.cols, 256);
-    const int64_t ctas = long_rows ? std::max<int64_t>(1, 8 * c.sm_count / col_ctas) : c.sm_count * (threads > 256 ? 1 : 2);
-    const int64_t grid = cut_rows(&a, s.gates, ctas, groups);
+    bool vec = s.cols % 8 == 0 && aligned16<T>(s.G.p, s.G.ld, s.gates) && aligned16<T>(s.dG.p, s.dG.ld, s.gates);
+    for (const Mat* m : {&s.dS, &s.dH, &s.X, &s.S, &s.dX, &s.dR}) vec = vec && aligned16<T>(m->p, m->ld, s.rows);
+    for (const float* w : {s.post, s.pre, static_cast<const float*>(s.dpost), static_cast<const float*>(s.dpre)})
+        vec = vec && aligned16<float>(w, 0, 1);
+    const bool gate_rows = s.G.p && s.per_gate == 1;
+    const bool full = vec && s.post && s.pre && s.dS.p && s.dX.p && s.dR.p && a.want_post && a.want_pre && !gate_rows;
+    const int inputs = (s.pre ? 2 : 0) + (s.X.p ? 1 : 0) + (s.dS.p ? 1 : 0) + (gate_rows ? 1 : 0);
+    // V vectors a thread.  Two where the rows go round (the fewer warps a row, the less of what is done once a warp) and
+    // two turns of them fit; rows that do not fit at all have their means taken first (as rows of fp32 of 8192 columns).
+    struct Plan {
+        int V, threads, groups, ahead;
+        int32_t tpr;
+        size_t step, join;
+    } plan = {};
+    auto lay_out = [&](int V) {
+        plan.V = V, plan.tpr = threads_for(s.cols, V), plan.threads = std::max(256, int(plan.tpr));
+        plan.groups = plan.threads / plan.tpr;
+        const size_t mine = size_t(plan.threads) * 8 * sizeof(float);
+        plan.join = (plan.groups > 1 ? mine : 0) + (full ? 2 * mine * V : 0);
+        plan.step = vec ? size_t(plan.threads) * 8 * V * sizeof(T) * size_t(inputs) : 0;
+        const size_t most = size_t(plan.threads > 256 ? 220 : 111) * 1024 - plan.join;
+        plan.ahead = !vec ? 0 : 3 * plan.step <= most ? 3 : 2 * plan.step <= most ? 2 : 0;
+    };
+    const bool many = s.rows >= int64_t(c.sm_count) * 8 * std::max(1, 4096 / s.cols);
+    if (s.cols <= 8192) lay_out(full && (many || s.cols > 4096) ? 2 : 1);
+    if (plan.V == 2 && plan.ahead == 0 && s.cols <= 4096) lay_out(1);
+    const bool long_rows = s.cols > 8192 || plan.tpr > 512 || (plan.V == 2 && plan.ahead == 0);
+    const int64_t col_ctas = cdiv(s.cols, kLongThreads * 8);
+    const int64_t ctas = long_rows ? std::max<int64_t>(1, 4 * c.sm_count / col_ctas)
+                                   : c.sm_count * (plan.threads > 256 ? 1 : 2);
+    const int64_t grid = cut_rows(&a, s.gates, ctas, long_rows ? 1 : plan.groups);
     // Scratch of the sums over rows and of the rows' statistics, in one block.
     PartSums sums = {};
     sums.cols = s.cols;
@@ -835,30 +930,23 @@ int run_backward(const ResidualNormGradArgs& s, const LibCtx& c, cudaStream_t st
     if (long_rows) {
         float4* stats = reinterpret_cast<float4*>(base + stats_at);
         void* args[] = {&a, &stats};
-        e = launch_kernel(reinterpret_cast<void*>(&residual_norm_stats_kernel<T>),
+        e = launch_kernel(vec ? reinterpret_cast<void*>(&residual_norm_stats_kernel<T, true>)
+                              : reinterpret_cast<void*>(&residual_norm_stats_kernel<T, false>),
                           dim3(unsigned(std::max<int64_t>(1, std::min<int64_t>(s.rows, 2 * c.sm_count)))), 1024, 0, 1, args,
                           stream);
         if (e != cudaSuccess) return report_cuda(e, "launching residual_norm_backward");
         count_launch();
-        e = launch_kernel(reinterpret_cast<void*>(&residual_norm_grad_long_kernel<T>),
-                          dim3(unsigned(col_ctas), unsigned(grid)), 256, 0, 1, args, stream);
+        e = launch_kernel(vec ? reinterpret_cast<void*>(&residual_norm_grad_long_kernel<T, true>)
+                              : reinterpret_cast<void*>(&residual_norm_grad_long_kernel<T, false>),
+                          dim3(unsigned(col_ctas), unsigned(grid)), kLongThreads, 0, 1, args, stream);
     } else {
-        bool vec = s.cols % 8 == 0 && aligned16<T>(s.G.p, s.G.ld, s.gates) && aligned16<T>(s.dG.p, s.dG.ld, s.gates);
-        for (const Mat* m : {&s.dS, &s.dH, &s.X, &s.S, &s.dX, &s.dR}) vec = vec && aligned16<T>(m->p, m->ld, s.rows);
-        for (const float* w : {s.post, s.pre, static_cast<const float*>(s.dpost), static_cast<const float*>(s.dpre)}) vec = vec && aligned16<float>(w, 0, 1);
-        const int inputs = (s.pre ? 2 : 0) + (s.X.p ? 1 : 0) + (s.dS.p ? 1 : 0) + (s.G.p && s.per_gate == 1 ? 1 : 0);
-        uint32_t row_bytes = uint32_t(tpr * 8 * V * sizeof(T)), step = vec ? row_bytes * uint32_t(groups * inputs) : 0;
-        const size_t join = groups > 1 ? size_t(threads) * 8 * V * sizeof(float) : 0;
-        const size_t most = size_t(threads > 256 ? 220 : 108) * 1024 - join;
-        const int ahead = !vec ? 0 : 3 * step <= most ? 3 : 2 * step <= most ? 2 : 0;
-        if (ahead == 0) step = 0;
-        const bool full = s.post && s.pre && s.dS.p && s.dX.p && s.dR.p && a.want_post && a.want_pre &&
-                          !(s.G.p && s.per_gate == 1);
-        void* kernel = V == 2 ? grad_kernel<T, 2>(ahead, full) : grad_kernel<T, 1>(ahead, full);
-        const size_t smem = join + size_t(ahead) * step;
+        uint32_t row_bytes = uint32_t(plan.tpr * 8 * plan.V * sizeof(T)), step = plan.ahead > 0 ? uint32_t(plan.step) : 0;
+        // Without a ring: not FULL.
+        void* kernel = plan.V == 2 ? grad_kernel<T, 2>(plan.ahead, full) : grad_kernel<T, 1>(plan.ahead, full);
+        const size_t smem = plan.join + size_t(plan.ahead) * step;
         if ((r = raise_kernel_smem(kernel, smem, c.device)) != GBR_OK) return r;
-        void* args[] = {&a, &tpr, &row_bytes, &step};
-        e = launch_kernel(kernel, dim3(unsigned(grid)), threads, smem, 1, args, stream);
+        void* args[] = {&a, &plan.tpr, &row_bytes, &step};
+        e = launch_kernel(kernel, dim3(unsigned(grid)), plan.threads, smem, 1, args, stream);
     }
     if (e != cudaSuccess) return report_cuda(e, "launching residual_norm_backward");
     count_launch();

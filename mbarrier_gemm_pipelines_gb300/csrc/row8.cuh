@@ -162,6 +162,25 @@ __device__ __forceinline__ void store_pairs(T* row, const F2 (&x)[4], int v, int
     store_row8<T, VEC>(row, y, v, t, tpr, cols);
 }
 
+// Four pairs of a thread in shared memory: two pieces of 16 bytes, each next to its neighbours'.
+__device__ __forceinline__ void put_pairs(uint32_t at, const F2 (&x)[4]) {
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) split2(x[i], y[2 * i], y[2 * i + 1]);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        ptx::st_shared_v4(at + uint32_t(h) * 16u * blockDim.x, __float_as_uint(y[4 * h]), __float_as_uint(y[4 * h + 1]),
+                          __float_as_uint(y[4 * h + 2]), __float_as_uint(y[4 * h + 3]));
+}
+__device__ __forceinline__ void get_pairs(F2 (&x)[4], uint32_t at) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint4 w = ptx::ld_shared_v4(at + uint32_t(h) * 16u * blockDim.x);
+        x[2 * h] = f2(__uint_as_float(w.x), __uint_as_float(w.y));
+        x[2 * h + 1] = f2(__uint_as_float(w.z), __uint_as_float(w.w));
+    }
+}
+
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
     for (int d = 16; d > 0; d /= 2) x += __shfl_xor_sync(0xffffffffu, x, d);
