@@ -131,13 +131,20 @@ __global__ void __launch_bounds__(kMost, kMost == 256 ? 3 : 1) residual_norm_str
         }
         copy_async_commit();
     };
-    float wpost[V][8], wpre[V][8];
-    Raw8<T> g[V];
+    // What X / root is multiplied by: scale, weight and a gate that is the same for all rows.
+    F2 w[V][4], wpre[V][4];
+    const bool post = a.post != nullptr;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        if (a.post != nullptr) load_row8<float, true>(wpost[v], a.post, v, t, tpr, cols);
-        if (a.pre != nullptr) load_row8<float, true>(wpre[v], a.pre, v, t, tpr, cols);
-        if (one_gate) load_raw8<true>(g[v], a.G, v, t, tpr, cols);
+        F2 g[4];
+        if (post) load_pairs<float, true>(w[v], a.post, v, t, tpr, cols);
+        if (a.pre != nullptr) load_pairs<float, true>(wpre[v], a.pre, v, t, tpr, cols);
+        if (one_gate) load_pairs<T, true>(g, a.G, v, t, tpr, cols);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            w[v][i] = post ? mul2(w[v][i], f2(a.scale)) : f2(a.scale);
+            if (one_gate) w[v][i] = mul2(w[v][i], g[i]);
+        }
     }
     clear_past<T, V>(base, kAhead * step / row_bytes, row_bytes, t, tpr, cols);
     int64_t row = blockIdx.x;
@@ -146,56 +153,51 @@ __global__ void __launch_bounds__(kMost, kMost == 256 ? 3 : 1) residual_norm_str
     for (uint32_t slot = 0; row < a.rows; row += gridDim.x, slot = slot + 1 == kAhead ? 0 : slot + 1) {
         copy_async_wait<kAhead - 1>();
         const uint32_t from = base + slot * step;
-        Raw8<T> x[V], r[V] = {};
+        Raw8<T> x[V], r[V] = {}, g[V] = {};
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             take_row8(x[v], from, v, t, tpr);
             if (has_r) take_row8(r[v], from + row_bytes, v, t, tpr);
             if (gates) take_row8(g[v], from + (has_r ? 2u : 1u) * row_bytes, v, t, tpr);
         }
-        float s[V][8], q = 1.f;
-        if (a.post != nullptr) {
-            float sum[1] = {};
+        float q = 1.f;
+        if (post) {
+            F2 xx = f2(0.f);
 #pragma unroll
             for (int v = 0; v < V; ++v)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) sum[0] = fmaf(raw_at(x[v], j), raw_at(x[v], j), sum[0]);
+                for (int i = 0; i < 4; ++i) xx = fma2(raw_pair(x[v], i), raw_pair(x[v], i), xx);
+            float sum[1] = {sum_pair(xx)};
             group_sum(sum, buf[0], tpr);
             q = root(sum[0], a.inv_cols, a.eps);
         }
+        F2 s[V][4], ss = f2(0.f);
 #pragma unroll
-        for (int v = 0; v < V; ++v)
+        for (int v = 0; v < V; ++v) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float y = raw_at(x[v], j);
-                if (a.post != nullptr) y = y * q * wpost[v][j];
-                if (a.G != nullptr) y *= raw_at(g[v], j);
-                s[v][j] = fmaf(a.scale, y, raw_at(r[v], j));
+            for (int i = 0; i < 4; ++i) {
+                s[v][i] = mul2(raw_pair(x[v], i), f2(q));
+                if (gates) s[v][i] = mul2(s[v][i], raw_pair(g[v], i));
+                s[v][i] = fma2(s[v][i], w[v][i], raw_pair(r[v], i));
+                ss = fma2(s[v][i], s[v][i], ss);
             }
-        if (a.S != nullptr)
-#pragma unroll
-            for (int v = 0; v < V; ++v) store_row8<T, true>(a.S + row * a.lds, s[v], v, t, tpr, cols);
-        float sum[1] = {};
-        if (a.H != nullptr) {
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) sum[0] = fmaf(s[v][j], s[v][j], sum[0]);
-            group_sum(sum, buf[1], tpr);
+            if (a.S != nullptr) store_pairs<T, true>(a.S + row * a.lds, s[v], v, t, tpr, cols);
         }
+        float sum[1] = {sum_pair(ss)};
+        if (a.H != nullptr) group_sum(sum, buf[1], tpr);
         // The slot has been read into registers that the lines above have used.
         fetch(row + int64_t(kAhead) * gridDim.x, slot);
         if (a.H != nullptr) {
-            const float p = root(sum[0], a.inv_cols, a.eps);
+            const F2 p = f2(root(sum[0], a.inv_cols, a.eps));
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                float h[8];
+                F2 h[4];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) h[j] = s[v][j] * p * wpre[v][j];
-                store_row8<T, true>(a.H + row * a.ldh, h, v, t, tpr, cols);
+                for (int i = 0; i < 4; ++i) h[i] = mul2(mul2(s[v][i], p), wpre[v][i]);
+                store_pairs<T, true>(a.H + row * a.ldh, h, v, t, tpr, cols);
             }
         }
-        if (a.post == nullptr || a.H == nullptr) __syncthreads();   // buf, for the next row
+        if (!post || a.H == nullptr) __syncthreads();   // buf, for the next row
     }
     copy_async_wait<0>();
 }
