@@ -45,6 +45,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) moe_sort_kernel(const SortPar
     int32_t* start = total + p.experts;                 // [experts] first place of this CTA's choices
     int32_t* sums = start + p.experts;                  // [32]
     ptx::griddep_wait();
+    ptx::griddep_launch_dependents();                   // at most 8 CTAs: what comes next may set itself up
     const uint32_t rank = ctas > 1 ? ptx::cluster_ctarank() : 0u;
     const int32_t warp = int32_t(threadIdx.x) / 32, lane = int32_t(threadIdx.x) % 32, E = p.experts;
     for (int32_t i = int32_t(threadIdx.x); i < warps * E; i += threads) count[i] = 0;

@@ -73,6 +73,7 @@ int run_tile(const Mxfp4Args& a, const LinearPlan& plan, const LibCtx& c, cudaSt
     P.ctl = c.ctl;
     P.inject = c.inject;
     Q.blocks = a.blocks;
+    Q.prefetch = int64_t(a.N) * a.blocks * 17 <= (int64_t(48) << 20);   // well within L2
     const size_t smem = mx::tile_smem_bytes(P.bt, P.stages);
     void* kernel = mxfp4_tile_kernel_ptr(a.act);
     if ((r = raise_kernel_smem(kernel, smem, c.device)) != GBR_OK) return r;

@@ -48,6 +48,8 @@ constexpr int kRows = 2;
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads) mxfp4_quantize_kernel(const QuantArgs<T> a) {
     ptx::griddep_wait();
+    // A few rows: the product behind may set itself up meanwhile.  (More: its CTAs would take this kernel's places.)
+    if (gridDim.x * gridDim.y <= 512) ptx::griddep_launch_dependents();
     const int32_t lane = int32_t(threadIdx.x) % 32, c0 = int32_t(blockIdx.x) * 256, c = c0 + lane * 8, b = c / kMxBlock;
     const int64_t padded = (int64_t(a.rows) + 127) / 128 * 128, step = int64_t(gridDim.y) * (kThreads / 32);
     for (int64_t first = int64_t(blockIdx.y) * (kThreads / 32) + threadIdx.x / 32; first < padded; first += kRows * step) {

@@ -32,6 +32,7 @@ struct TileParams {
     linear::TileParams t;                              // maps, epilogue, split; num_ks: stages' worth of K
     CUtensorMap mapWs, mapXs;                          // scales
     int32_t blocks;
+    uint32_t prefetch;                                 // B into L2 while the launch in front still runs
 };
 
 // Row tiles of 128 whose scales a tile of BT rows needs.
@@ -96,6 +97,12 @@ __global__ void __launch_bounds__(kTileThreads) mxfp4_tile_kernel(const __grid_c
         ptx::prefetch_tensormap(&Q.mapWs);
         ptx::prefetch_tensormap(&Q.mapXs);
     }
+    // B does not come from the launch in front, as A mostly does (just quantised): its way from HBM need not wait.
+    if (threadIdx.x == 128 && Q.prefetch != 0 && i0 == 0)
+        for (int32_t ks = ks0; ks < ks1; ++ks) {
+            ptx::tma_prefetch_2d(&P.mapW, ks * 128, j0);
+            ptx::tma_prefetch_2d(&Q.mapWs, ks * 256, j0 / 128);
+        }
     if (warp == 5) {
         ptx::tmem_alloc(ptx::smem_addr(tmem_holder), tmem_cols);
         ptx::tmem_relinquish_alloc_permit();
