@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kThreads) mxfp4_quantize_kernel(const QuantArg
 #pragma unroll
             for (int i = 0; i < 4; ++i) split2(mul2(raw_pair(r[k], i), inv), x[2 * i], x[2 * i + 1]);
             const uint32_t code = byte == 255u ? 0u : mx_pack8(x);   // of a NaN block any
-            if (row < a.rows && c < a.blocks * kMxBlock)
+            if (row < a.rows && b < a.blocks)
                 *reinterpret_cast<uint32_t*>(a.data + row * int64_t(a.blocks) * 16 + c / 2) = code;
             uint32_t four = byte << (lane / 4 % 4 * 8);
             four |= __shfl_xor_sync(0xffffffffu, four, 4);

@@ -101,30 +101,32 @@ __global__ void __launch_bounds__(1024) residual_norm_kernel(const Args<T> a, in
     }
 }
 
-// Many rows: CTAs that stay, a row at a time (blockDim.x = tpr threads), the weights in registers and the next
-// kAhead rows' X, R and gate on their way into shared memory, each thread its own 16 bytes, so that nobody waits for
-// another's copy.  A gate per channel is in registers as well.  `step`: bytes of one row of all inputs.
+// Many rows: CTAs that stay, blockDim.x / tpr rows a turn, the weights in registers and the next kAhead turns' X, R and
+// gate on their way into shared memory, each thread its own 16 bytes, so that nobody waits for another's copy.  A gate
+// per channel is in the weights.  row_bytes: of a row in shared memory; step: of a turn's rows of all inputs.
+// 16384 x 4096 bf16 with all but row gates: a row a CTA 131 us, this 97 (5.5 TB/s; 88 alone).
 template <typename T, int V, int kAhead, int kMost>
-__global__ void __launch_bounds__(kMost, kMost == 256 ? 3 : 1) residual_norm_stream_kernel(const Args<T> a, uint32_t row_bytes,
-                                                                                       uint32_t step) {
+__global__ void __launch_bounds__(kMost, kMost == 256 ? 3 : 1) residual_norm_stream_kernel(const Args<T> a, int32_t tpr,
+                                                                                       uint32_t row_bytes, uint32_t step) {
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ float buf[2][1][32];
     ptx::griddep_wait();
-    const int32_t t = int32_t(threadIdx.x), tpr = int32_t(blockDim.x), cols = a.cols;
+    const int32_t t = int32_t(threadIdx.x) % tpr, group = int32_t(threadIdx.x) / tpr, groups = int32_t(blockDim.x) / tpr;
+    const int32_t cols = a.cols;
     const bool has_r = a.R != nullptr, one_gate = a.G != nullptr && a.per_gate == a.rows, gates = a.G != nullptr && !one_gate;
-    const uint32_t base = ptx::smem_addr(ring);
+    const uint32_t base = ptx::smem_addr(ring) + uint32_t(group) * row_bytes, wide = row_bytes * uint32_t(groups);
     auto fetch = [&](int64_t row, uint32_t slot) {
         if (row < a.rows) {
             uint32_t to = base + slot * step;
 #pragma unroll
             for (int v = 0; v < V; ++v) copy_row8(to, a.X + row * a.ldx, v, t, tpr, cols);
             if (has_r) {
-                to += row_bytes;
+                to += wide;
 #pragma unroll
                 for (int v = 0; v < V; ++v) copy_row8(to, a.R + row * a.ldr, v, t, tpr, cols);
             }
             if (gates) {
-                to += row_bytes;
+                to += wide;
 #pragma unroll
                 for (int v = 0; v < V; ++v) copy_row8(to, a.G + row / a.per_gate * a.ldg, v, t, tpr, cols);
             }
@@ -146,19 +148,22 @@ __global__ void __launch_bounds__(kMost, kMost == 256 ? 3 : 1) residual_norm_str
             if (one_gate) w[v][i] = mul2(w[v][i], g[i]);
         }
     }
-    clear_past<T, V>(base, kAhead * step / row_bytes, row_bytes, t, tpr, cols);
-    int64_t row = blockIdx.x;
+    clear_past<T, V>(ptx::smem_addr(ring), kAhead * step / row_bytes, row_bytes, t, tpr, cols);
+    const int64_t turn = int64_t(gridDim.x) * groups;
+    int64_t first = int64_t(blockIdx.x) * groups;
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) fetch(row + int64_t(i) * gridDim.x, uint32_t(i));
-    for (uint32_t slot = 0; row < a.rows; row += gridDim.x, slot = slot + 1 == kAhead ? 0 : slot + 1) {
+    for (int i = 0; i < kAhead; ++i) fetch(first + group + i * turn, uint32_t(i));
+    for (uint32_t slot = 0; first < a.rows; first += turn, slot = slot + 1 == kAhead ? 0 : slot + 1) {
+        const int64_t row = first + group;
+        const int32_t out = row < a.rows ? cols : 0;    // a group past the end only keeps the barriers
         copy_async_wait<kAhead - 1>();
         const uint32_t from = base + slot * step;
         Raw8<T> x[V], r[V] = {}, g[V] = {};
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             take_row8(x[v], from, v, t, tpr);
-            if (has_r) take_row8(r[v], from + row_bytes, v, t, tpr);
-            if (gates) take_row8(g[v], from + (has_r ? 2u : 1u) * row_bytes, v, t, tpr);
+            if (has_r) take_row8(r[v], from + wide, v, t, tpr);
+            if (gates) take_row8(g[v], from + (has_r ? 2u : 1u) * wide, v, t, tpr);
         }
         float q = 1.f;
         if (post) {
@@ -181,12 +186,12 @@ __global__ void __launch_bounds__(kMost, kMost == 256 ? 3 : 1) residual_norm_str
                 s[v][i] = fma2(s[v][i], w[v][i], raw_pair(r[v], i));
                 ss = fma2(s[v][i], s[v][i], ss);
             }
-            if (a.S != nullptr) store_pairs<T, true>(a.S + row * a.lds, s[v], v, t, tpr, cols);
+            if (a.S != nullptr) store_pairs<T, true>(a.S + row * a.lds, s[v], v, t, tpr, out);
         }
         float sum[1] = {sum_pair(ss)};
         if (a.H != nullptr) group_sum(sum, buf[1], tpr);
         // The slot has been read into registers that the lines above have used.
-        fetch(row + int64_t(kAhead) * gridDim.x, slot);
+        fetch(row + kAhead * turn, slot);
         if (a.H != nullptr) {
             const F2 p = f2(root(sum[0], a.inv_cols, a.eps));
 #pragma unroll
@@ -194,10 +199,10 @@ __global__ void __launch_bounds__(kMost, kMost == 256 ? 3 : 1) residual_norm_str
                 F2 h[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) h[i] = mul2(mul2(s[v][i], p), wpre[v][i]);
-                store_pairs<T, true>(a.H + row * a.ldh, h, v, t, tpr, cols);
+                store_pairs<T, true>(a.H + row * a.ldh, h, v, t, tpr, out);
             }
         }
-        if (!post || a.H == nullptr) __syncthreads();   // buf, for the next row
+        if (tpr > 32 && (!post || a.H == nullptr)) __syncthreads();   // buf, for the next row
     }
     copy_async_wait<0>();
 }
@@ -763,9 +768,9 @@ bool aligned16(const void* p, int64_t ld, int64_t rows) {
            (reinterpret_cast<uintptr_t>(p) % 16 == 0 && (rows <= 1 || ld % int64_t(16 / sizeof(T)) == 0));
 }
 
-// Threads a row: the fewest warps that hold it with V vectors each.
-int threads_for(int64_t cols, int V) {
-    int tpr = 32;
+// Threads a row: the fewest warps (or less, as `least` lets them) that hold it with V vectors each.
+int threads_for(int64_t cols, int V, int least = 32) {
+    int tpr = least;
     while (int64_t(tpr) * 8 * V < cols) tpr *= 2;
     return tpr;
 }
@@ -781,11 +786,25 @@ void* stream_kernel() {
     return reinterpret_cast<void*>(&residual_norm_stream_kernel<T, 2, kAhead, kMost>);
 }
 
-// Rows of 1024 to 8192 columns, and enough of them for CTAs that stay.
-bool streams(const ResidualNormArgs& s, size_t esize, int sm_count) {
+struct StreamPlan {
+    int32_t tpr;
+    int threads, ctas, ahead;                           // ctas: an SM, by registers
+    size_t step;
+};
+StreamPlan stream_plan(const ResidualNormArgs& s, size_t esize) {
+    StreamPlan p;
     const int inputs = 1 + (s.R.p ? 1 : 0) + (s.G.p && s.gates > 1 ? 1 : 0);
-    return s.cols > 1024 && s.cols <= 8192 && s.rows >= 8 * sm_count &&
-           2 * size_t(threads_for(s.cols, 2)) * 16 * esize * size_t(inputs) <= 216 * 1024;
+    p.tpr = threads_for(s.cols, 2, 4);
+    p.threads = std::max(256, int(p.tpr)), p.ctas = p.threads > 256 ? 1 : 3;
+    p.step = size_t(p.threads) * 16 * esize * size_t(inputs);
+    p.ahead = 3 * p.step * p.ctas <= 216 * 1024 ? 3 : 2;
+    return p;
+}
+// Rows of up to 8192 columns, and enough of them for CTAs that stay: eight turns of all.
+bool streams(const ResidualNormArgs& s, size_t esize, int sm_count) {
+    if (s.cols > 8192) return false;
+    const StreamPlan p = stream_plan(s, esize);
+    return s.rows >= int64_t(8) * sm_count * (p.threads / p.tpr) && size_t(p.ahead) * p.step <= 216 * 1024;
 }
 
 template <typename T>
@@ -803,21 +822,20 @@ int run_forward(const ResidualNormArgs& s, const LibCtx& c, cudaStream_t stream)
                           dim3(unsigned(std::min<int64_t>(s.rows, 2 * c.sm_count))), 1024, 0, 1, args, stream);
     } else if (vec && streams(s, sizeof(T), c.sm_count)) {
         const int inputs = 1 + (s.R.p ? 1 : 0) + (s.G.p && s.gates > 1 ? 1 : 0);
-        const int threads = threads_for(s.cols, 2);
-        uint32_t row_bytes = uint32_t(threads * 16 * sizeof(T)), step = row_bytes * uint32_t(inputs);
-        const int ctas = threads > 256 ? 1 : 3;
-        const bool three = 3 * step * ctas <= 216 * 1024;
-        void* kernel = threads > 256 ? (three ? stream_kernel<T, 3, 512>() : stream_kernel<T, 2, 512>())
-                                     : (three ? stream_kernel<T, 3, 256>() : stream_kernel<T, 2, 256>());
-        const size_t smem = size_t(three ? 3 : 2) * step;
+        const StreamPlan p = stream_plan(s, sizeof(T));
+        int32_t tpr = p.tpr;
+        uint32_t row_bytes = uint32_t(p.tpr * 16 * sizeof(T)), step = uint32_t(p.step);
+        void* kernel = p.threads > 256 ? (p.ahead == 3 ? stream_kernel<T, 3, 512>() : stream_kernel<T, 2, 512>())
+                                       : (p.ahead == 3 ? stream_kernel<T, 3, 256>() : stream_kernel<T, 2, 256>());
+        const size_t smem = size_t(p.ahead) * p.step;
         const int r = raise_kernel_smem(kernel, smem, c.device);
         if (r != GBR_OK) return r;
-        void* args[] = {&a, &row_bytes, &step};
-        e = launch_kernel(kernel, dim3(unsigned(c.sm_count * std::min<int64_t>(ctas, 216 * 1024 / smem))), threads, smem, 1,
-                          args, stream);
+        void* args[] = {&a, &tpr, &row_bytes, &step};
+        e = launch_kernel(kernel, dim3(unsigned(c.sm_count * std::min<int64_t>(p.ctas, 216 * 1024 / smem))), p.threads, smem,
+                          1, args, stream);
     } else {
         const int V = s.cols > 1024 * 16 ? 4 : s.cols > 1024 * 8 ? 2 : 1;
-        int32_t tpr = threads_for(s.cols, V);
+        int32_t tpr = threads_for(s.cols, V, 4);
         const int threads = std::max(256, int(tpr));
         void* kernel = V == 4 ? forward_kernel<T, 4>(vec) : V == 2 ? forward_kernel<T, 2>(vec) : forward_kernel<T, 1>(vec);
         void* args[] = {&a, &tpr};

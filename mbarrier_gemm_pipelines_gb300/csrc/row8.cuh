@@ -187,7 +187,8 @@ __device__ __forceinline__ float warp_sum(float x) {
     return x;
 }
 
-// Sums of N (1 to 4) values over groups of `tpr` threads (32 times a power of two that divides the block).  Every thread
+// Sums of N (1 to 4) values over groups of `tpr` threads (a power of two that divides the block; for several values at
+// least 32).  Every thread
 // of the block calls it; `buf` is this call's own until the next __syncthreads.  The order of the sum is fixed.
 //
 // Several values take the shuffles of little more than one: after the first step each half of the warp goes on with two
@@ -211,6 +212,10 @@ __device__ __forceinline__ void group_sum(float (&x)[N], float (*buf)[32], int32
     const int32_t lane = int32_t(threadIdx.x) % 32, warp = int32_t(threadIdx.x) / 32, warps = tpr / 32;
     const int32_t first = warp & ~(warps - 1);
     if (N == 1) {
+        if (tpr < 32) {                                 // several groups a warp
+            for (int d = tpr / 2; d > 0; d /= 2) x[0] += __shfl_xor_sync(0xffffffffu, x[0], d);
+            return;
+        }
         x[0] = warp_sum(x[0]);
         if (tpr == 32) return;
         if (lane == 0) buf[0][warp] = x[0];

@@ -84,6 +84,17 @@ NORM = [
     (3, 32769, "bf16", True, 1, True, True, 0.5),
     (2, 70000, "fp32", False, 2, True, True, 1.0),
     (700, 8, "fp32", True, 1, True, True, 1.0),
+    # Enough rows for CTAs that stay, one or several rows a turn.
+    (1300, 4096, "bf16", True, 1, True, True, 0.25),
+    (1301, 2048, "fp32", True, 1301, True, True, 1.0),
+    (1290, 8192, "bf16", True, 3, False, True, 1.0),
+    (1217, 8184, "fp32", False, 1, True, False, 0.5),
+    (5004, 1000, "bf16", True, 36, True, True, 0.25),
+    (2500, 2048, "bf16", True, 0, True, True, 1.0),
+    (5000, 1024, "bf16", True, 5000, True, False, 1.0),
+    (40003, 128, "bf16", True, 1, True, True, 1.0),
+    (80001, 40, "fp32", False, 3, True, True, 1.0),
+    (160001, 24, "bf16", True, 0, False, True, 1.0),
 ]
 NORM_IDS = ["-".join(map(str, c)) for c in NORM]
 EPS = 1e-6
