@@ -417,6 +417,12 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
                  : "memory");
 }
 
+// The same for an arrival that hands no memory over, only Tensor Memory (whose order tcgen05.fence and
+// tcgen05.wait::ld keep): with cluster-scope release the thread first waits for its own stores on their way.
+__device__ __forceinline__ void mbar_arrive_cluster_tmem(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // Cluster-scope acquire wait (for barriers that receive arrivals from the peer CTA).
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
     uint32_t ok;

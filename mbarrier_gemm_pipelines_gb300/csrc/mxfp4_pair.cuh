@@ -20,10 +20,12 @@
 // scales, and one would leave the tensor core idle during a tile's epilogue.  So
 // the two share 64 columns: [0, 256) and [192, 448), scales in [448, 512).  The
 // epilogue takes the shared columns of its tile first, and the next tile's MMAs
-// wait for those alone (and for the tile before, which is done by then): 1.1 us
-// from one tile's last MMA to the next one's first, of 6.8 at K = 4096.  Tiles of
-// 192 columns have room for two accumulators, but take in more bytes for the same
-// products: 4096 x 4096 x 14336 90 us with 256 columns, 92 with 192; 8192^3 176 and 196.
+// wait for those alone (and for the tile before, which is done by then): 0.4 us
+// from one tile's last MMA to the next one's first, of 6.2 at K = 4096.  (1.1 us
+// with arrivals that release memory at cluster scope: they wait for the epilogue's
+// stores.  4096 x 4096 x 14336 92 -> 84 us, GELU 99 -> 90.)  Tiles of 192 columns have
+// room for two accumulators, but take in more bytes for the same products: 8192^3
+// 176 us with 256 columns, 196 with 192, before that.
 #pragma once
 #include "gemm_umma.cuh"
 #include "mxfp4_tile.cuh"
@@ -211,14 +213,14 @@ __global__ void __launch_bounds__(kPairThreads, 1) mxfp4_pair_kernel(const __gri
             const int32_t rows = P.M - row0;
             const int32_t chunks = rows <= 0 || n0 >= P.N ? 0 : n0 + 128 >= P.N ? 1 : 2;
             const uint32_t a = tl & 1u, aph = (tl >> 1) & 1u;
-            const uint32_t ae = ptx::smem_addr(acc_empty + a);
             // The 64 columns shared with the other accumulator: the last of the first, the first of the second.
             const bool shares = a == 0 ? strip >= 2 : strip < 2;
             const int32_t first = a == 0 && chunks == 2 ? 1 : 0;
-            auto release_shared = [&]() {
+            // Columns that this warp has read go back to the even CTA's MMAs.
+            auto release = [&](uint64_t* bar) {
                 ptx::tc_fence_before_sync();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_addr(shared_empty), 0));
+                if (lane == 0) ptx::mbar_arrive_cluster_tmem(ptx::mapa_shared(ptx::smem_addr(bar), 0));
             };
             // The residual of a chunk, into the staging slot once its last store has read it.
             auto fetch_residual = [&](int32_t c) {
@@ -236,8 +238,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) mxfp4_pair_kernel(const __gri
             ptx::tc_fence_after_sync();
             const uint32_t acc = tmem_base + ((q * 32u) << 16) + a * kAccStep + uint32_t(col0);
             if (chunks == 0) {
-                if (shares) release_shared();
-                umma::acc_release<2>(ae, lane);
+                if (shares) release(shared_empty);
+                release(acc_empty + a);
                 continue;
             }
             for (int32_t i = 0; i < chunks; ++i) {
@@ -250,8 +252,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) mxfp4_pair_kernel(const __gri
 #pragma unroll
                     for (int j = 0; j < 32; ++j) z[j] = __uint_as_float(raw[j]);
                 }
-                if (i == 0 && shares) release_shared();
-                if (i + 1 == chunks) umma::acc_release<2>(ae, lane);
+                if (i == 0 && shares) release(shared_empty);
+                if (i + 1 == chunks) release(acc_empty + a);
                 if (P.bias != nullptr) {
                     const float* b = P.bias + n;
                     if (P.bias_vec != 0 && n + 32 <= P.N) {
