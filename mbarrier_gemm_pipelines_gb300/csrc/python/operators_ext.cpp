@@ -482,8 +482,9 @@ PyObject* residual_norm_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const bool want_h = a[5] != Py_None;
         if (!want_h && a[8] != Py_None) refuse(PyExc_ValueError, "H needs pre");
         const CallStream st(a[9], dev);
-        // Where nothing is added, scaled or normalised the sum is X itself.
-        const bool same = a[7] == Py_None && a[1] == Py_None && a[2] == Py_None && a[3] == Py_None && scale == 1.0;
+        // Where nothing is added, scaled or normalised the sum is X itself, unless H is written over it.
+        const bool same = a[7] == Py_None && a[1] == Py_None && a[2] == Py_None && a[3] == Py_None && scale == 1.0 &&
+                          (a[8] == Py_None || tensor(a[8], "H").data_ptr() != X.p);
         Out S;
         if (!same) S = out_mat(a[7], "S", tX, dev, X.rows, X.cols);
         Out H;

@@ -221,6 +221,41 @@ def test_residual_norm_in_place(gbr):
             assert out[0] is b[S] and torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
 
 
+def test_residual_norm_over_its_input(gbr):
+    """H written over X leaves the sum in a tensor of its own."""
+    g = rng(7)
+    X, w = normal(g, (9, 512)), 1 + normal(g, (512,), 0.1, F32)
+    want, copy = gbr.residual_norm(X, pre=w)[1], X.clone()
+    S, H = gbr.residual_norm(copy, pre=w, H=copy)
+    assert H is copy and torch.equal(H, want) and torch.equal(S, X)
+
+
+@pytest.mark.parametrize("rows", [40, 2000])
+def test_residual_norm_weights_and_outputs_anywhere(gbr, rows):
+    """Weights that start between 16 bytes, outputs given with strides of their own."""
+    case = (rows, 1024, "bf16", True, 4, True, True, 0.5)
+    a, d = norm_inputs(case), norm_grad_inputs(case)
+    want, grads = gbr.residual_norm(**a), gbr.residual_norm_backward(**d)
+
+    def shifted(v):
+        big = torch.empty(v.numel() + 1, device="cuda")
+        big[1:] = v
+        return big[1:]
+    S, H = (odd(torch.empty_like(t)) for t in want)
+    out = gbr.residual_norm(**dict(a, post=shifted(a["post"]), pre=shifted(a["pre"])), S=S, H=H)
+    assert out[0] is S and out[1] is H
+    check_norm(a, S, H)
+    given = dict(dX=odd(torch.empty_like(grads[0])), dR=odd(torch.empty_like(grads[1])), dpost=shifted(grads[2]),
+                 dgate=odd(torch.empty_like(grads[3])), dpre=shifted(grads[4]))
+    for t in given.values():
+        t.fill_(7)
+    out = gbr.residual_norm_backward(**dict(d, post=shifted(d["post"])), **given)
+    assert all(x is y for x, y in zip(out, given.values()))
+    check_norm_grads(d, out)
+    wide = gbr.residual_norm_backward(**d, dX=torch.empty(rows, 2048, device="cuda", dtype=BF)[:, 1024:])
+    check_norm_grads(d, wide)
+
+
 def test_residual_norm_special_values(gbr):
     """A row of zeros stays zero; Inf and NaN spoil their own row alone."""
     g = rng(4)
@@ -600,6 +635,48 @@ def test_two_streams_at_once(gbr):
         for x, y in zip(out, want[j]):
             assert torch.equal(x, y)
     gbr.check_device()
+
+
+def test_threads_at_once(gbr):
+    """Calls from several host threads, each on a stream of its own."""
+    import threading
+    every = calls(gbr)
+    want = [f(None) for f in every]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        stream = torch.cuda.Stream()
+        try:
+            for n in range(10):
+                j = (i + n) % len(every)
+                got = every[j](stream)
+                stream.synchronize()
+                if not all(torch.equal(x, y) for x, y in zip(got, want[j])):
+                    bad.append(j)
+        except Exception as e:                              # noqa: BLE001 (reported below)
+            bad.append(e)
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+    gbr.check_device()
+
+
+def test_outputs_that_are_given(gbr):
+    r = row_inputs((50, 3, 520, 8, "bf16", 0.2))
+    ids = choices(50, 3, 8, 3, 0.2)
+    p, o = torch.full_like(r["p"], 9), torch.full_like(r["o"], 9)
+    assert gbr.moe_sort(ids, 8, positions=p, offsets=o)[0] is p and torch.equal(p, r["p"]) and torch.equal(o, r["o"])
+    for out in (torch.full_like(r["Ys"], 9), odd(torch.empty_like(r["Ys"]))):
+        assert gbr.moe_dispatch(r["X"], p, o, Xs=out) is out and torch.equal(out, gbr.moe_dispatch(r["X"], p, o))
+        w = torch.full_like(r["w"], 9)
+        x, y = gbr.moe_combine_backward(r["dY"], r["Ys"], p, o, r["w"], dYs=out, dweights=w)
+        want = gbr.moe_combine_backward(r["dY"], r["Ys"], p, o, r["w"])
+        assert x is out and y is w and torch.equal(x, want[0])
+        within(y, want[1].double(), 2.0 ** -17 * want[1].double().abs().max(), "dweights")
 
 
 def test_written_tensors_move_their_version(gbr):
