@@ -95,7 +95,7 @@ def _link_ext(obj: str, torch_dir: str) -> None:
     tmp = EXT_PATH + ".tmp%d" % os.getpid()
     lib = os.path.join(torch_dir, "lib")
     cmd = ["g++", "-shared", "-o", tmp, obj, LIB_PATH, "-Wl,-rpath,$ORIGIN", "-L" + lib, "-ltorch_python", "-ltorch",
-           "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+           "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError("link of the Python binding failed:\n%s\n%s" % (res.stdout, res.stderr))
