@@ -147,6 +147,11 @@ struct Rows {
     int64_t rows;                                       // of Ys or Xs
 };
 
+// CTAs an SM that registers let in.  One round of them is best: 4096 tokens of 4096 columns, 2 choices, with 3 / 4 / 6 / 8
+// an SM of 4: combined 26.1 / 23.9 / 27.4 / 26.0 us, gradients 30.2 / 28.2 / 32.4 / 31.0.
+template <typename T>
+constexpr int kResident = sizeof(T) == 2 ? 4 : 3;
+
 // A CTA takes a run of tokens, whose positions (and weights) it fetches first, so that from then on no load waits for
 // another; blockDim.x / tpr tokens at a time, kV vectors of 8 columns a thread at once.  Taking a token's positions when
 // its turn came: 4096 tokens of 4096 columns and 2 choices 24.8 us dispatched, 42.5 combined.  HELD false: a token is
@@ -178,7 +183,7 @@ __device__ __forceinline__ void fetch_places(const Rows<T>& a, int64_t first, in
 }
 
 template <typename T, bool VEC, int kV, bool HELD>
-__global__ void __launch_bounds__(256, 4) moe_dispatch_kernel(const Rows<T> a, int32_t tpr) {
+__global__ void __launch_bounds__(256, kResident<T>) moe_dispatch_kernel(const Rows<T> a, int32_t tpr) {
     __shared__ int32_t at[kPlaces];
     ptx::griddep_wait();
     const int32_t t = int32_t(threadIdx.x) % tpr, group = int32_t(threadIdx.x) / tpr, per = int32_t(blockDim.x) / tpr;
@@ -229,7 +234,7 @@ __global__ void __launch_bounds__(256, 4) moe_dispatch_kernel(const Rows<T> a, i
 
 // kJ choices at once.
 template <typename T, bool VEC, int kV, int kJ, bool HELD>
-__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 3) moe_combine_rows_kernel(const Rows<T> a, int32_t tpr) {
+__global__ void __launch_bounds__(256, kResident<T>) moe_combine_rows_kernel(const Rows<T> a, int32_t tpr) {
     __shared__ int32_t at[kPlaces];
     __shared__ float weight[kPlaces];
     ptx::griddep_wait();
@@ -286,7 +291,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 3) moe_combine_rows_
 
 // X is dY, Xs is dYs.  kJ choices at once: their products with dY are summed over the token's threads.
 template <typename T, bool VEC, int kV, int kJ, bool HELD>
-__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 3) moe_combine_grad_kernel(const Rows<T> a, int32_t tpr) {
+__global__ void __launch_bounds__(256, kResident<T>) moe_combine_grad_kernel(const Rows<T> a, int32_t tpr) {
     __shared__ int32_t at[kPlaces];
     __shared__ float weight[kPlaces];
     __shared__ float buf[kJ][32];
@@ -372,7 +377,7 @@ int32_t threads_for(int32_t D, int kV) {
 template <typename T>
 int launch_rows(void* const (&kernels)[2], Rows<T> p, int kV, const LibCtx& c, const char* what, cudaStream_t stream) {
     int32_t tpr = threads_for(p.D, kV);
-    const int64_t turns = cdiv(p.T_, 256 / tpr), grid = std::min<int64_t>(turns, int64_t(c.sm_count) * 8);
+    const int64_t turns = cdiv(p.T_, 256 / tpr), grid = std::min<int64_t>(turns, int64_t(c.sm_count) * kResident<T>);
     void* args[] = {&p, &tpr};
     void* kernel = kernels[turns > grid && p.k <= kPlaces ? 0 : 1];
     const cudaError_t e = launch_kernel(kernel, dim3(unsigned(grid)), 256, 0, 1, args, stream);

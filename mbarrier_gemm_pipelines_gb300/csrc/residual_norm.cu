@@ -104,9 +104,10 @@ __global__ void __launch_bounds__(1024) residual_norm_kernel(const Args<T> a, in
 // Many rows: CTAs that stay, blockDim.x / tpr rows a turn, the weights in registers and the next kAhead turns' X, R and
 // gate on their way into shared memory, each thread its own 16 bytes, so that nobody waits for another's copy.  A gate
 // per channel is in the weights.  row_bytes: of a row in shared memory; step: of a turn's rows of all inputs.
-// 16384 x 4096 bf16 with all but row gates: a row a CTA 131 us, this 97 (5.5 TB/s; 88 alone).
+// 16384 x 4096 bf16 with all but row gates: a row a CTA 131 us, this 84 (6.4 TB/s).  More on their way is slower, HBM
+// reading and writing at once: three CTAs an SM and three turns ahead 97, two and three 84 to 88, two and five 95.
 template <typename T, int V, int kAhead, int kMost>
-__global__ void __launch_bounds__(kMost, kMost == 256 ? 3 : 1) residual_norm_stream_kernel(const Args<T> a, int32_t tpr,
+__global__ void __launch_bounds__(kMost, kMost == 256 ? 2 : 1) residual_norm_stream_kernel(const Args<T> a, int32_t tpr,
                                                                                        uint32_t row_bytes, uint32_t step) {
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ float buf[2][1][32];
@@ -795,9 +796,9 @@ StreamPlan stream_plan(const ResidualNormArgs& s, size_t esize) {
     StreamPlan p;
     const int inputs = 1 + (s.R.p ? 1 : 0) + (s.G.p && s.gates > 1 ? 1 : 0);
     p.tpr = threads_for(s.cols, 2, 4);
-    p.threads = std::max(256, int(p.tpr)), p.ctas = p.threads > 256 ? 1 : 3;
+    p.threads = std::max(256, int(p.tpr)), p.ctas = p.threads > 256 ? 1 : 2;
     p.step = size_t(p.threads) * 16 * esize * size_t(inputs);
-    p.ahead = 3 * p.step * p.ctas <= 216 * 1024 ? 3 : 2;
+    p.ahead = p.threads > 256 && 3 * p.step <= 216 * 1024 ? 3 : 2;
     return p;
 }
 // Rows of up to 8192 columns, and enough of them for CTAs that stay: eight turns of all.
@@ -825,8 +826,9 @@ int run_forward(const ResidualNormArgs& s, const LibCtx& c, cudaStream_t stream)
         const StreamPlan p = stream_plan(s, sizeof(T));
         int32_t tpr = p.tpr;
         uint32_t row_bytes = uint32_t(p.tpr * 16 * sizeof(T)), step = uint32_t(p.step);
-        void* kernel = p.threads > 256 ? (p.ahead == 3 ? stream_kernel<T, 3, 512>() : stream_kernel<T, 2, 512>())
-                                       : (p.ahead == 3 ? stream_kernel<T, 3, 256>() : stream_kernel<T, 2, 256>());
+        void* kernel = p.threads <= 256 ? stream_kernel<T, 2, 256>()
+                       : p.ahead == 3   ? stream_kernel<T, 3, 512>()
+                                        : stream_kernel<T, 2, 512>();
         const size_t smem = size_t(p.ahead) * p.step;
         const int r = raise_kernel_smem(kernel, smem, c.device);
         if (r != GBR_OK) return r;
