@@ -111,7 +111,12 @@ int run_pair(const Mxfp4Args& a, const LibCtx& c, cudaStream_t stream) {
     if (tiles >= (int64_t(1) << 30)) return report_errorf(GBR_ERR_INVALID, "gemm_mxfp4: too many output tiles");
     P.num_tiles = int32_t(tiles);
     P.num_ks = int32_t(cdiv(a.blocks, 8));
-    P.group_m = 8;
+    // Tiles that run together share what they read: all of B's columns against the same rows of A where B stays in L2
+    // from one row of tiles to the next (us with bands of 1 / 8 rows of tiles: 4096 x 4096 x 14336 79.6 / 83.5, 8192^3
+    // 161 / 168, 4096 x 16384 x 14336, B 117 MB, 315 / 273), else all of A's rows against the same of B where A does (the
+    // last one: 270), else bands.
+    constexpr int64_t kStays = int64_t(48) << 20;
+    P.group_m = int64_t(a.N) * a.blocks * 17 <= kStays ? 1 : int64_t(a.M) * a.blocks * 17 <= kStays ? P.m_tiles : 8;
     P.ctl = c.ctl;
     P.inject = c.inject;
     void* kernel = mxfp4_pair_kernel_ptr(a.act);

@@ -175,7 +175,7 @@ int quantize(const Mxfp4Quantize& s, const LibCtx& c, cudaStream_t stream) {
                           kThreads, 0, 1, args, stream);
     } else {
         const bool vec = s.cols % 8 == 0 && aligned16<T>(s.X, s.rows);
-        const int64_t gx = cdiv(s.cols, 256), most = std::max<int64_t>(1, int64_t(c.sm_count) * 16 / gx);
+        const int64_t gx = cdiv(s.cols, 256), most = std::max<int64_t>(1, int64_t(c.sm_count) * 12 / gx);
         e = launch_kernel(vec ? reinterpret_cast<void*>(&mxfp4_quantize_kernel<T, true>)
                               : reinterpret_cast<void*>(&mxfp4_quantize_kernel<T, false>),
                           dim3(unsigned(gx), unsigned(std::min<int64_t>(padded / (kThreads / 32) / kRows, most))), kThreads, 0, 1,
