@@ -1,9 +1,8 @@
 // mxfp4_quantize.cu -- matrices to blocks of 4-bit values with a scale each
 // (mxfp4.cuh) and back.  Bound by memory: the matrix is read once and 17 bytes
 // are written for 32 values.
-//   rows kept: a thread takes 8 neighbouring values, four threads a block; the
-//     largest value is found with two shuffles, four blocks' scales are one
-//     32-bit store.
+//   rows kept: a thread takes 16 neighbouring values, two threads a block; four
+//     blocks' scales are one 32-bit store.
 //   transposed (weights stored [K, N], wanted [N, K]): a thread takes 4 blocks of
 //     its own column, neighbouring threads neighbouring columns.
 #include "gbr.h"
@@ -42,52 +41,50 @@ __device__ __forceinline__ uint32_t top8(const Raw8<float>& r) {
     return m;
 }
 
-// A warp a row and 256 columns, two rows at a time; rows up to the next multiple of 128, for the scales' padding.
-// 4096 x 4096 bf16: one row at a time and value by value 12.8 us, two and in pairs 10.9.
-constexpr int kRows = 2;
+// A warp a row and 512 columns, 16 neighbouring values a lane, two lanes a block; rows up to the next multiple of 128,
+// for the scales' padding.  4096 x 4096 bf16, bound by instructions as much as by memory: 8 values a lane, value by
+// value and one row at a time 12.8 us, in pairs and two rows 10.5, 16 values 8.4.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads) mxfp4_quantize_kernel(const QuantArgs<T> a) {
     ptx::griddep_wait();
     // A few rows: the product behind may set itself up meanwhile.  (More: its CTAs would take this kernel's places.)
     if (gridDim.x * gridDim.y <= 512) ptx::griddep_launch_dependents();
-    const int32_t lane = int32_t(threadIdx.x) % 32, c0 = int32_t(blockIdx.x) * 256, c = c0 + lane * 8, b = c / kMxBlock;
+    const int32_t lane = int32_t(threadIdx.x) % 32, b = int32_t(blockIdx.x) * 16 + lane / 2, c = b * kMxBlock + lane % 2 * 16;
     const int64_t padded = (int64_t(a.rows) + 127) / 128 * 128, step = int64_t(gridDim.y) * (kThreads / 32);
-    for (int64_t first = int64_t(blockIdx.y) * (kThreads / 32) + threadIdx.x / 32; first < padded; first += kRows * step) {
-        Raw8<T> r[kRows];
+    for (int64_t row = int64_t(blockIdx.y) * (kThreads / 32) + threadIdx.x / 32; row < padded; row += step) {
+        const T* x = a.X + row * a.ldx + c;
+        const int32_t left = row < a.rows ? a.cols - c : 0;
+        Raw8<T> r[2];
 #pragma unroll
-        for (int k = 0; k < kRows; ++k) {
-            const int64_t row = first + k * step;
-            const T* x = a.X + row * a.ldx + c;
-            const int32_t left = row < a.rows ? a.cols - c : 0;
+        for (int h = 0; h < 2; ++h) {
             if (VEC) {
-                load_raw8<true>(r[k], x, 0, 0, 1, left);        // the columns are a multiple of 8
+                load_raw8<true>(r[h], x, h, 0, 1, left);        // the columns are a multiple of 8
             } else {
                 float y[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) y[j] = j < left ? to_f32(x[j]) : 0.f;
-                make_raw8(r[k], y);
+                for (int j = 0; j < 8; ++j) y[j] = 8 * h + j < left ? to_f32(x[8 * h + j]) : 0.f;
+                make_raw8(r[h], y);
             }
         }
+        uint32_t top = max(top8(r[0]), top8(r[1]));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        const uint32_t byte = mx_scale_byte(top);
+        const F2 inv = f2(mx_inverse(byte));
+        uint32_t code[2];
 #pragma unroll
-        for (int k = 0; k < kRows; ++k) {
-            const int64_t row = first + k * step;
-            uint32_t top = top8(r[k]);
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const uint32_t byte = mx_scale_byte(top);
-            const F2 inv = f2(mx_inverse(byte));
-            float x[8];
+        for (int h = 0; h < 2; ++h) {
+            float y[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) split2(mul2(raw_pair(r[k], i), inv), x[2 * i], x[2 * i + 1]);
-            const uint32_t code = byte == 255u ? 0u : mx_pack8(x);   // of a NaN block any
-            if (row < a.rows && b < a.blocks)
-                *reinterpret_cast<uint32_t*>(a.data + row * int64_t(a.blocks) * 16 + c / 2) = code;
-            uint32_t four = byte << (lane / 4 % 4 * 8);
-            four |= __shfl_xor_sync(0xffffffffu, four, 4);
-            four |= __shfl_xor_sync(0xffffffffu, four, 8);
-            if (lane % 16 == 0 && b / 4 < a.block_tiles && row < padded)
-                *reinterpret_cast<uint32_t*>(a.scales + mx_scale_offset(row, b, a.block_tiles)) = four;
+            for (int i = 0; i < 4; ++i) split2(mul2(raw_pair(r[h], i), inv), y[2 * i], y[2 * i + 1]);
+            code[h] = byte == 255u ? 0u : mx_pack8(y);          // of a NaN block any
         }
+        if (row < a.rows && b < a.blocks)
+            *reinterpret_cast<uint2*>(a.data + row * int64_t(a.blocks) * 16 + c / 2) = make_uint2(code[0], code[1]);
+        uint32_t four = byte << (lane / 2 % 4 * 8);
+        four |= __shfl_xor_sync(0xffffffffu, four, 2);
+        four |= __shfl_xor_sync(0xffffffffu, four, 4);
+        if (lane % 8 == 0 && b / 4 < a.block_tiles)
+            *reinterpret_cast<uint32_t*>(a.scales + mx_scale_offset(row, b, a.block_tiles)) = four;
     }
 }
 
@@ -175,10 +172,10 @@ int quantize(const Mxfp4Quantize& s, const LibCtx& c, cudaStream_t stream) {
                           kThreads, 0, 1, args, stream);
     } else {
         const bool vec = s.cols % 8 == 0 && aligned16<T>(s.X, s.rows);
-        const int64_t gx = cdiv(s.cols, 256), most = std::max<int64_t>(1, int64_t(c.sm_count) * 12 / gx);
+        const int64_t gx = cdiv(s.cols, 512), most = std::max<int64_t>(1, int64_t(c.sm_count) * 12 / gx);
         e = launch_kernel(vec ? reinterpret_cast<void*>(&mxfp4_quantize_kernel<T, true>)
                               : reinterpret_cast<void*>(&mxfp4_quantize_kernel<T, false>),
-                          dim3(unsigned(gx), unsigned(std::min<int64_t>(padded / (kThreads / 32) / kRows, most))), kThreads, 0, 1,
+                          dim3(unsigned(gx), unsigned(std::min<int64_t>(padded / (kThreads / 32), most))), kThreads, 0, 1,
                           args, stream);
     }
     if (e != cudaSuccess) return report_cuda(e, "launching quantize_mxfp4");
