@@ -182,7 +182,7 @@ __device__ __forceinline__ void fetch_places(const Rows<T>& a, int64_t first, in
     __syncthreads();
 }
 
-template <typename T, bool VEC, int kV, bool HELD>
+template <typename T, int A, int kV, bool HELD>
 __global__ void __launch_bounds__(256, kResident<T>) moe_dispatch_kernel(const Rows<T> a, int32_t tpr) {
     __shared__ int32_t at[kPlaces];
     ptx::griddep_wait();
@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(256, kResident<T>) moe_dispatch_kernel(const R
             auto load = [&](Raw8<T> (&x)[kV], int32_t i, int32_t v0) {
 #pragma unroll
                 for (int v = 0; v < kV; ++v)
-                    load_raw8<VEC>(x[v], a.X + (first + i) * a.ldx, v0 + v, t, tpr, i < tokens ? a.D : 0);
+                    load_raw8<A>(x[v], a.X + (first + i) * a.ldx, v0 + v, t, tpr, i < tokens ? a.D : 0);
             };
             Raw8<T> next[kV];
             load(next, group, 0);
@@ -219,13 +219,13 @@ __global__ void __launch_bounds__(256, kResident<T>) moe_dispatch_kernel(const R
                         const int32_t to = pos[j];
                         if (to < 0 || (!HELD && to >= a.rows)) continue;
 #pragma unroll
-                        for (int v = 0; v < kV; ++v) store_raw8<VEC>(a.Xs + to * a.ldxs, x[v], v0 + v, t, tpr, a.D);
+                        for (int v = 0; v < kV; ++v) store_raw8<A>(a.Xs + to * a.ldxs, x[v], v0 + v, t, tpr, a.D);
                     }
                     // The token's k choices stand for k rows of Xs as well: those behind the last expert's are zeroed.
                     const int64_t r0 = (first + i) * a.k + j0;
                     for (int64_t r = r0 > total ? r0 : total; r < r0 + k; ++r)
 #pragma unroll
-                        for (int v = 0; v < kV; ++v) store_row8<T, VEC>(a.Xs + r * a.ldxs, zero, v0 + v, t, tpr, a.D);
+                        for (int v = 0; v < kV; ++v) store_row8<T, A>(a.Xs + r * a.ldxs, zero, v0 + v, t, tpr, a.D);
                 }
             }
         }
@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(256, kResident<T>) moe_dispatch_kernel(const R
 }
 
 // kJ choices at once.
-template <typename T, bool VEC, int kV, int kJ, bool HELD>
+template <typename T, int A, int kV, int kJ, bool HELD>
 __global__ void __launch_bounds__(256, kResident<T>) moe_combine_rows_kernel(const Rows<T> a, int32_t tpr) {
     __shared__ int32_t at[kPlaces];
     __shared__ float weight[kPlaces];
@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(256, kResident<T>) moe_combine_rows_kernel(con
                 Raw8<T> r[kV];
                 if (a.R != nullptr)
 #pragma unroll
-                    for (int v = 0; v < kV; ++v) load_raw8<VEC>(r[v], a.R + row * a.ldr, v0 + v, t, tpr, a.D);
+                    for (int v = 0; v < kV; ++v) load_raw8<A>(r[v], a.R + row * a.ldr, v0 + v, t, tpr, a.D);
                 for (int32_t j0 = 0; j0 < a.k; j0 += kJ) {
                     Raw8<T> x[kJ][kV];
                     float w[kJ];
@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(256, kResident<T>) moe_combine_rows_kernel(con
                         on[j] = p >= 0 && p < a.rows;
                         if (!on[j]) continue;
 #pragma unroll
-                        for (int v = 0; v < kV; ++v) load_raw8<VEC>(x[j][v], a.Ys + p * a.ldys, v0 + v, t, tpr, a.D);
+                        for (int v = 0; v < kV; ++v) load_raw8<A>(x[j][v], a.Ys + p * a.ldys, v0 + v, t, tpr, a.D);
                     }
 #pragma unroll
                     for (int j = 0; j < kJ; ++j) {
@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(256, kResident<T>) moe_combine_rows_kernel(con
                     if (a.R != nullptr)
 #pragma unroll
                         for (int e = 0; e < 8; ++e) y[v][e] += raw_at(r[v], e);
-                    store_row8<T, VEC>(a.Y + row * a.ldy, y[v], v0 + v, t, tpr, a.D);
+                    store_row8<T, A>(a.Y + row * a.ldy, y[v], v0 + v, t, tpr, a.D);
                 }
             }
         }
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(256, kResident<T>) moe_combine_rows_kernel(con
 }
 
 // X is dY, Xs is dYs.  kJ choices at once: their products with dY are summed over the token's threads.
-template <typename T, bool VEC, int kV, int kJ, bool HELD>
+template <typename T, int A, int kV, int kJ, bool HELD>
 __global__ void __launch_bounds__(256, kResident<T>) moe_combine_grad_kernel(const Rows<T> a, int32_t tpr) {
     __shared__ int32_t at[kPlaces];
     __shared__ float weight[kPlaces];
@@ -323,13 +323,13 @@ __global__ void __launch_bounds__(256, kResident<T>) moe_combine_grad_kernel(con
                 for (int32_t v0 = 0; v0 * tpr * 8 < cols; v0 += kV) {
                     Raw8<T> d[kV], y[kJ][kV];
 #pragma unroll
-                    for (int v = 0; v < kV; ++v) load_raw8<VEC>(d[v], a.X + row * a.ldx, v0 + v, t, tpr, cols);
+                    for (int v = 0; v < kV; ++v) load_raw8<A>(d[v], a.X + row * a.ldx, v0 + v, t, tpr, cols);
                     if (dots)
 #pragma unroll
                         for (int j = 0; j < kJ; ++j)
 #pragma unroll
                             for (int v = 0; v < kV; ++v)
-                                if (p[j] >= 0) load_raw8<VEC>(y[j][v], a.Ys + p[j] * a.ldys, v0 + v, t, tpr, cols);
+                                if (p[j] >= 0) load_raw8<A>(y[j][v], a.Ys + p[j] * a.ldys, v0 + v, t, tpr, cols);
 #pragma unroll
                     for (int j = 0; j < kJ; ++j) {
                         if (p[j] < 0) continue;
@@ -341,13 +341,13 @@ __global__ void __launch_bounds__(256, kResident<T>) moe_combine_grad_kernel(con
                                 if (dots) dot[j] = fmaf(raw_at(d[v], e), raw_at(y[j][v], e), dot[j]);
                                 x[e] = w[j] * raw_at(d[v], e);
                             }
-                            if (rows_out) store_row8<T, VEC>(a.Xs + p[j] * a.ldxs, x, v0 + v, t, tpr, cols);
+                            if (rows_out) store_row8<T, A>(a.Xs + p[j] * a.ldxs, x, v0 + v, t, tpr, cols);
                         }
                     }
                     if (rows_out && j0 == 0)
                         for (int64_t r = row * a.k > total ? row * a.k : total; r < (row + 1) * a.k; ++r)
 #pragma unroll
-                            for (int v = 0; v < kV; ++v) store_row8<T, VEC>(a.Xs + r * a.ldxs, zero, v0 + v, t, tpr, cols);
+                            for (int v = 0; v < kV; ++v) store_row8<T, A>(a.Xs + r * a.ldxs, zero, v0 + v, t, tpr, cols);
                 }
                 if (!dots) continue;
                 group_sum(dot, buf, tpr);
@@ -397,8 +397,8 @@ int dispatch(const MoeRowsArgs& a, const LibCtx& c, cudaStream_t stream) {
     p.positions = a.positions, p.offsets = a.offsets;
     p.T_ = a.T, p.k = a.k, p.D = a.D, p.experts = a.experts, p.rows = int64_t(a.T) * a.k;
     const bool vec = a.D % 8 == 0 && aligned16<T>(a.X, a.T) && aligned16<T>(a.Ys, p.rows);
-    void* const wide[2] = GBR_BOTH(moe_dispatch_kernel<T, true, 2);
-    void* const any[2] = GBR_BOTH(moe_dispatch_kernel<T, false, 1);
+    void* const wide[2] = GBR_BOTH(moe_dispatch_kernel<T, kVec, 2);
+    void* const any[2] = GBR_BOTH(moe_dispatch_kernel<T, kShifted, 1);
     return launch_rows(vec ? wide : any, p, vec ? 2 : 1, c, "launching moe_dispatch", stream);
 }
 
@@ -414,9 +414,9 @@ int combine(const MoeRowsArgs& a, int64_t rows, const LibCtx& c, cudaStream_t st
     // One or two choices: two vectors a thread; more: one, and four choices at once (eight spill registers: 2000 tokens of
     // 2048 columns and 6 choices 16.7 us with four, 23.8 with eight).
     const bool few = vec && a.k <= 2;
-    void* const two[2] = GBR_BOTH(moe_combine_rows_kernel<T, true, 2, 2);
-    void* const four[2] = GBR_BOTH(moe_combine_rows_kernel<T, true, 1, 4);
-    void* const any[2] = GBR_BOTH(moe_combine_rows_kernel<T, false, 1, 4);
+    void* const two[2] = GBR_BOTH(moe_combine_rows_kernel<T, kVec, 2, 2);
+    void* const four[2] = GBR_BOTH(moe_combine_rows_kernel<T, kVec, 1, 4);
+    void* const any[2] = GBR_BOTH(moe_combine_rows_kernel<T, kShifted, 1, 4);
     return launch_rows(!vec ? any : few ? two : four, p, few ? 2 : 1, c, "launching moe_combine", stream);
 }
 
@@ -430,9 +430,9 @@ int combine_grad(const MoeCombineGradArgs& a, const LibCtx& c, cudaStream_t stre
     p.T_ = a.T, p.k = a.k, p.D = a.D, p.experts = a.experts, p.rows = int64_t(a.T) * a.k;
     const bool vec = a.D % 8 == 0 && aligned16<T>(a.dY, a.T) && aligned16<T>(a.Ys, p.rows) && aligned16<T>(a.dYs, p.rows);
     const bool few = vec && a.k <= 2;
-    void* const two[2] = GBR_BOTH(moe_combine_grad_kernel<T, true, 2, 2);
-    void* const four[2] = GBR_BOTH(moe_combine_grad_kernel<T, true, 1, 4);
-    void* const any[2] = GBR_BOTH(moe_combine_grad_kernel<T, false, 1, 4);
+    void* const two[2] = GBR_BOTH(moe_combine_grad_kernel<T, kVec, 2, 2);
+    void* const four[2] = GBR_BOTH(moe_combine_grad_kernel<T, kVec, 1, 4);
+    void* const any[2] = GBR_BOTH(moe_combine_grad_kernel<T, kShifted, 1, 4);
     return launch_rows(!vec ? any : few ? two : four, p, few ? 2 : 1, c, "launching moe_combine_backward", stream);
 }
 

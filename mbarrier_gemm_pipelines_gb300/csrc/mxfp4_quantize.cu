@@ -52,20 +52,10 @@ __global__ void __launch_bounds__(kThreads) mxfp4_quantize_kernel(const QuantArg
     const int32_t lane = int32_t(threadIdx.x) % 32, b = int32_t(blockIdx.x) * 16 + lane / 2, c = b * kMxBlock + lane % 2 * 16;
     const int64_t padded = (int64_t(a.rows) + 127) / 128 * 128, step = int64_t(gridDim.y) * (kThreads / 32);
     for (int64_t row = int64_t(blockIdx.y) * (kThreads / 32) + threadIdx.x / 32; row < padded; row += step) {
-        const T* x = a.X + row * a.ldx + c;
-        const int32_t left = row < a.rows ? a.cols - c : 0;
         Raw8<T> r[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if (VEC) {
-                load_raw8<true>(r[h], x, h, 0, 1, left);        // the columns are a multiple of 8
-            } else {
-                float y[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) y[j] = 8 * h + j < left ? to_f32(x[8 * h + j]) : 0.f;
-                make_raw8(r[h], y);
-            }
-        }
+        for (int h = 0; h < 2; ++h)
+            load_raw8<VEC ? kVec : kShifted>(r[h], a.X + row * a.ldx, 0, c / 8 + h, 1, row < a.rows ? a.cols : 0);
         uint32_t top = max(top8(r[0]), top8(r[1]));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         const uint32_t byte = mx_scale_byte(top);

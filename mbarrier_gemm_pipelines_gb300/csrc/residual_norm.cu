@@ -822,7 +822,6 @@ int run_forward(const ResidualNormArgs& s, const LibCtx& c, cudaStream_t stream)
         e = launch_kernel(reinterpret_cast<void*>(&residual_norm_long_kernel<T>),
                           dim3(unsigned(std::min<int64_t>(s.rows, 2 * c.sm_count))), 1024, 0, 1, args, stream);
     } else if (vec && streams(s, sizeof(T), c.sm_count)) {
-        const int inputs = 1 + (s.R.p ? 1 : 0) + (s.G.p && s.gates > 1 ? 1 : 0);
         const StreamPlan p = stream_plan(s, sizeof(T));
         int32_t tpr = p.tpr;
         uint32_t row_bytes = uint32_t(p.tpr * 16 * sizeof(T)), step = uint32_t(p.step);

@@ -2,10 +2,20 @@
 // elements each, as fp32 (the operators that need a whole row at once), and
 // sums over the group.
 //
-// VEC: the thread's eight are neighbours, moved 16 (bf16) or 32 bytes (fp32) at
-// a time; rows start on 16 bytes and the columns are a multiple of 8.
-// Otherwise they lie `tpr` columns apart, so that a warp touches whole lines at
-// any alignment.
+// How rows are moved (Access):
+//   kVec      the thread's eight are neighbours, moved 16 (bf16) or 32 bytes (fp32) at
+//     a time; rows start on 16 bytes and the columns are a multiple of 8.
+//   kStrided  rows start anywhere; the eight lie `tpr` columns apart and go one by one, a
+//     warp's together in whole lines.
+//   kShifted  rows start anywhere; the eight are neighbours.  A thread loads the aligned
+//     16-byte pieces that they lie in, as far as those lie inside the row, and shifts; it
+//     stores the aligned pieces that begin in them, the last with its neighbour's
+//     first elements.  At the ends of the row (and of the warp, for stores) elements go
+//     one by one.
+//     Groups are whole warps.
+// Strided against shifted, us, bf16: combination of 2000 x 2047 with 6 choices 60 / 36,
+// quantisation of 4096 x 4095 16.6 / 11.3; but residual_norm of 16384 x 4095 264 / 308 and
+// its gradients of 4096 x 2047 84 / 100, which instructions bound already.
 #pragma once
 #include "activation.cuh"
 #include "gbr_ptx.cuh"
@@ -18,11 +28,11 @@ __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162flo
 __device__ __forceinline__ void from_f32(float x, float* y) { *y = x; }
 __device__ __forceinline__ void from_f32(float x, __nv_bfloat16* y) { *y = __float2bfloat16_rn(x); }
 
-// Column of element j of vector v of thread `t` of `tpr`.
-template <bool VEC>
-__device__ __forceinline__ int32_t row_col(int v, int j, int32_t t, int32_t tpr) {
-    return VEC ? (v * tpr + t) * 8 + j : (v * 8 + j) * tpr + t;
-}
+enum Access : int { kStrided = 0, kVec = 1, kShifted = 2 };
+
+// First column of vector v of thread `t` of `tpr`, of neighbours; column of element j, strided.
+__device__ __forceinline__ int32_t row_col(int v, int32_t t, int32_t tpr) { return (v * tpr + t) * 8; }
+__device__ __forceinline__ int32_t strided_col(int v, int j, int32_t t, int32_t tpr) { return (v * 8 + j) * tpr + t; }
 
 // Eight elements as they are loaded; columns past the end are zero.
 template <typename T>
@@ -30,41 +40,99 @@ struct Raw8 {
     uint32_t w[sizeof(T) * 2];
 };
 
-template <bool VEC>
+// Elements from the aligned address in front of an element to that element.
+__device__ __forceinline__ int32_t off_16(const __nv_bfloat16* p) { return int32_t(reinterpret_cast<uintptr_t>(p) / 2 % 8); }
+__device__ __forceinline__ int32_t off_16(const float* p) { return int32_t(reinterpret_cast<uintptr_t>(p) / 4 % 4); }
+
+// out = eight elements of `w` from element `by` on (below 8 of bf16, 4 of fp32).
+__device__ __forceinline__ void shift8(Raw8<__nv_bfloat16>& out, const uint32_t (&w)[8], int32_t by) {
+    uint32_t x[7];
+    const bool four = by & 4, two = by & 2, one = by & 1;
+#pragma unroll
+    for (int i = 0; i < 7; ++i) x[i] = four ? (i + 2 < 8 ? w[i + 2] : 0u) : w[i];
+#pragma unroll
+    for (int i = 0; i < 6; ++i) x[i] = two ? x[i + 1] : x[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) out.w[i] = one ? __funnelshift_r(x[i], x[i + 1], 16) : x[i];
+}
+__device__ __forceinline__ void shift8(Raw8<float>& out, const uint32_t (&w)[12], int32_t by) {
+    uint32_t x[10];
+    const bool two = by & 2, one = by & 1;
+#pragma unroll
+    for (int i = 0; i < 10; ++i) x[i] = two ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) out.w[i] = one ? x[i + 1] : x[i];
+}
+
+__device__ __forceinline__ void take_piece(uint32_t* w, const uint4& x) { w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w; }
+
+template <int A>
 __device__ __forceinline__ void load_raw8(Raw8<__nv_bfloat16>& r, const __nv_bfloat16* row, int v, int32_t t,
                                           int32_t tpr, int32_t cols) {
-    if (VEC) {
-        const int32_t c = row_col<true>(v, 0, t, tpr);
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (c < cols) x = *reinterpret_cast<const uint4*>(row + c);
-        r.w[0] = x.x, r.w[1] = x.y, r.w[2] = x.z, r.w[3] = x.w;
+    const int32_t c = row_col(v, t, tpr), left = cols - c;
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (A == kVec) {
+        if (left > 0) x = *reinterpret_cast<const uint4*>(row + c);
+        take_piece(r.w, x);
+        return;
+    }
+    if (A == kStrided) {
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+            const int32_t d = strided_col(v, j, t, tpr), e = d + tpr;
+            const uint32_t lo = d < cols ? __bfloat16_as_ushort(row[d]) : 0u;
+            const uint32_t hi = e < cols ? __bfloat16_as_ushort(row[e]) : 0u;
+            r.w[j / 2] = lo | (hi << 16);
+        }
+        return;
+    }
+    const int32_t off = off_16(row + c);
+    // Inside the row: from `off` elements before the first (c is a multiple of 8) to 8 after those.
+    if (off == 0 ? left >= 8 : c > 0 && left >= 16 - off) {
+        const uint4* p = reinterpret_cast<const uint4*>(row + c - off);
+        uint32_t w[8];
+        take_piece(w, p[0]);
+        take_piece(w + 4, off == 0 ? x : p[1]);
+        shift8(r, w, off);
     } else {
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
-            const int32_t c = row_col<false>(v, j, t, tpr), d = c + tpr;
-            const uint32_t lo = c < cols ? __bfloat16_as_ushort(row[c]) : 0u;
-            const uint32_t hi = d < cols ? __bfloat16_as_ushort(row[d]) : 0u;
+            const uint32_t lo = j < left ? __bfloat16_as_ushort(row[c + j]) : 0u;
+            const uint32_t hi = j + 1 < left ? __bfloat16_as_ushort(row[c + j + 1]) : 0u;
             r.w[j / 2] = lo | (hi << 16);
         }
     }
 }
-template <bool VEC>
+template <int A>
 __device__ __forceinline__ void load_raw8(Raw8<float>& r, const float* row, int v, int32_t t, int32_t tpr, int32_t cols) {
-    if (VEC) {
-        const int32_t c = row_col<true>(v, 0, t, tpr);
-        uint4 x = make_uint4(0, 0, 0, 0), y = x;
-        if (c < cols) {
+    const int32_t c = row_col(v, t, tpr), left = cols - c;
+    uint4 x = make_uint4(0, 0, 0, 0), y = x;
+    if (A == kVec) {
+        if (left > 0) {
             x = reinterpret_cast<const uint4*>(row + c)[0];
             y = reinterpret_cast<const uint4*>(row + c)[1];
         }
-        r.w[0] = x.x, r.w[1] = x.y, r.w[2] = x.z, r.w[3] = x.w;
-        r.w[4] = y.x, r.w[5] = y.y, r.w[6] = y.z, r.w[7] = y.w;
-    } else {
+        take_piece(r.w, x), take_piece(r.w + 4, y);
+        return;
+    }
+    if (A == kStrided) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const int32_t c = row_col<false>(v, j, t, tpr);
-            r.w[j] = c < cols ? __float_as_uint(row[c]) : 0u;
+            const int32_t d = strided_col(v, j, t, tpr);
+            r.w[j] = d < cols ? __float_as_uint(row[d]) : 0u;
         }
+        return;
+    }
+    const int32_t off = off_16(row + c);
+    if (off == 0 ? left >= 8 : c > 0 && left >= 12 - off) {
+        const uint4* p = reinterpret_cast<const uint4*>(row + c - off);
+        uint32_t w[12];
+        take_piece(w, p[0]), take_piece(w + 4, p[1]);
+        take_piece(w + 8, off == 0 ? x : p[2]);
+        shift8(r, w, off);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r.w[j] = j < left ? __float_as_uint(row[c + j]) : 0u;
     }
 }
 
@@ -73,66 +141,106 @@ __device__ __forceinline__ float raw_at(const Raw8<__nv_bfloat16>& r, int j) {
 }
 __device__ __forceinline__ float raw_at(const Raw8<float>& r, int j) { return __uint_as_float(r.w[j]); }
 
-// Eight values of the type, which they hold exactly.
-__device__ __forceinline__ void make_raw8(Raw8<__nv_bfloat16>& r, const float (&x)[8]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r.w[i] = (__float_as_uint(x[2 * i]) >> 16) | (__float_as_uint(x[2 * i + 1]) & 0xFFFF0000u);
-}
-__device__ __forceinline__ void make_raw8(Raw8<float>& r, const float (&x)[8]) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) r.w[i] = __float_as_uint(x[i]);
-}
-
-template <typename T, bool VEC>
+template <typename T, int A>
 __device__ __forceinline__ void load_row8(float (&x)[8], const T* row, int v, int32_t t, int32_t tpr, int32_t cols) {
     Raw8<T> r;
-    load_raw8<VEC>(r, row, v, t, tpr, cols);
+    load_raw8<A>(r, row, v, t, tpr, cols);
 #pragma unroll
     for (int j = 0; j < 8; ++j) x[j] = raw_at(r, j);
 }
 
-template <bool VEC>
+// Shifted, every lane of a warp calls the stores, those without columns too.
+template <int A>
 __device__ __forceinline__ void store_raw8(__nv_bfloat16* row, const Raw8<__nv_bfloat16>& r, int v, int32_t t, int32_t tpr,
                                            int32_t cols) {
-    if (VEC) {
-        const int32_t c = row_col<true>(v, 0, t, tpr);
-        if (c < cols) *reinterpret_cast<uint4*>(row + c) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
-    } else {
+    const int32_t c = row_col(v, t, tpr), left = cols - c;
+    if (A == kVec) {
+        if (left > 0) *reinterpret_cast<uint4*>(row + c) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+        return;
+    }
+    if (A == kStrided) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const int32_t c = row_col<false>(v, j, t, tpr);
-            if (c < cols) row[c] = __ushort_as_bfloat16(uint16_t(j % 2 ? r.w[j / 2] >> 16 : r.w[j / 2] & 0xFFFFu));
+            const int32_t d = strided_col(v, j, t, tpr);
+            if (d < cols) row[d] = __ushort_as_bfloat16(uint16_t(j % 2 ? r.w[j / 2] >> 16 : r.w[j / 2] & 0xFFFFu));
         }
+        return;
+    }
+    const int32_t off = off_16(row + c), lane = t % 32;
+    uint32_t w[8];                                      // this thread's and the next one's
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        w[i] = r.w[i];
+        w[4 + i] = __shfl_down_sync(0xffffffffu, r.w[i], 1);
+    }
+    // The aligned piece that begins in this thread's elements, whole inside the row and with a neighbour for its rest;
+    // the piece in front of it is the last thread's, under the same conditions.
+    const int32_t from = (8 - off) % 8;
+    const bool piece = off == 0 ? left >= 8 : lane < 31 && left >= 16 - off;
+    const bool front = off != 0 && lane > 0 && left >= 8 - off;
+    if (piece) {
+        Raw8<__nv_bfloat16> x;
+        shift8(x, w, from);
+        *reinterpret_cast<uint4*>(row + c + from) = make_uint4(x.w[0], x.w[1], x.w[2], x.w[3]);
+    }
+    if (piece && (front || off == 0)) return;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        if (j >= left || (j < from ? front : piece)) continue;
+        row[c + j] = __ushort_as_bfloat16(uint16_t(j % 2 ? r.w[j / 2] >> 16 : r.w[j / 2] & 0xFFFFu));
     }
 }
-template <bool VEC>
+template <int A>
 __device__ __forceinline__ void store_raw8(float* row, const Raw8<float>& r, int v, int32_t t, int32_t tpr, int32_t cols) {
-    if (VEC) {
-        const int32_t c = row_col<true>(v, 0, t, tpr);
-        if (c >= cols) return;
+    const int32_t c = row_col(v, t, tpr), left = cols - c;
+    if (A == kVec) {
+        if (left <= 0) return;
         reinterpret_cast<uint4*>(row + c)[0] = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
         reinterpret_cast<uint4*>(row + c)[1] = make_uint4(r.w[4], r.w[5], r.w[6], r.w[7]);
-    } else {
+        return;
+    }
+    if (A == kStrided) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const int32_t c = row_col<false>(v, j, t, tpr);
-            if (c < cols) row[c] = __uint_as_float(r.w[j]);
+            const int32_t d = strided_col(v, j, t, tpr);
+            if (d < cols) row[d] = __uint_as_float(r.w[j]);
         }
+        return;
+    }
+    const int32_t off = off_16(row + c), lane = t % 32;
+    uint32_t w[12];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = r.w[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[8 + i] = __shfl_down_sync(0xffffffffu, r.w[i], 1);
+    // Two aligned pieces begin in this thread's elements; the first needs no neighbour.
+    const int32_t from = (4 - off) % 4;
+    const bool first = left >= from + 4, second = off == 0 ? left >= 8 : lane < 31 && left >= 12 - off;
+    const bool front = off != 0 && lane > 0 && left >= 4 - off;
+    Raw8<float> x;
+    shift8(x, w, from);
+    if (first) *reinterpret_cast<uint4*>(row + c + from) = make_uint4(x.w[0], x.w[1], x.w[2], x.w[3]);
+    if (second) *reinterpret_cast<uint4*>(row + c + from + 4) = make_uint4(x.w[4], x.w[5], x.w[6], x.w[7]);
+    if (second && (front || off == 0)) return;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        if (j >= left || (j < from ? front : j < from + 4 ? first : second)) continue;
+        row[c + j] = __uint_as_float(r.w[j]);
     }
 }
 
-template <typename T, bool VEC>
-__device__ __forceinline__ void store_row8(T* row, const float (&x)[8], int v, int32_t t, int32_t tpr, int32_t cols) {
-    if (VEC) {
-        const int32_t c = row_col<true>(v, 0, t, tpr);
-        if (c < cols) store8(row + c, x);
-    } else {
+// Rounded to the type.
+__device__ __forceinline__ void round8(Raw8<__nv_bfloat16>& r, const float (&x)[8]) { take_piece(r.w, pack8(x)); }
+__device__ __forceinline__ void round8(Raw8<float>& r, const float (&x)[8]) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int32_t c = row_col<false>(v, j, t, tpr);
-            if (c < cols) from_f32(x[j], row + c);
-        }
-    }
+    for (int j = 0; j < 8; ++j) r.w[j] = __float_as_uint(x[j]);
+}
+
+template <typename T, int A>
+__device__ __forceinline__ void store_row8(T* row, const float (&x)[8], int v, int32_t t, int32_t tpr, int32_t cols) {
+    Raw8<T> r;
+    round8(r, x);
+    store_raw8<A>(row, r, v, t, tpr, cols);
 }
 
 // The same as four pairs, which one instruction multiplies or adds (activation.cuh).
@@ -147,19 +255,19 @@ __device__ __forceinline__ float sum_pair(F2 x) {
     split2(x, a, b);
     return a + b;
 }
-template <typename T, bool VEC>
+template <typename T, int A>
 __device__ __forceinline__ void load_pairs(F2 (&x)[4], const T* row, int v, int32_t t, int32_t tpr, int32_t cols) {
     Raw8<T> r;
-    load_raw8<VEC>(r, row, v, t, tpr, cols);
+    load_raw8<A>(r, row, v, t, tpr, cols);
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i] = raw_pair(r, i);
 }
-template <typename T, bool VEC>
+template <typename T, int A>
 __device__ __forceinline__ void store_pairs(T* row, const F2 (&x)[4], int v, int32_t t, int32_t tpr, int32_t cols) {
     float y[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) split2(x[i], y[2 * i], y[2 * i + 1]);
-    store_row8<T, VEC>(row, y, v, t, tpr, cols);
+    store_row8<T, A>(row, y, v, t, tpr, cols);
 }
 
 // Four pairs of a thread in shared memory: two pieces of 16 bytes, each next to its neighbours'.
@@ -250,7 +358,7 @@ __device__ __forceinline__ void copy_async_wait() {
 // Vector v of a row into shared memory, where the row lies as it is, and from there.
 template <typename T>
 __device__ __forceinline__ void copy_row8(uint32_t to, const T* row, int v, int32_t t, int32_t tpr, int32_t cols) {
-    const int32_t c = row_col<true>(v, 0, t, tpr);
+    const int32_t c = row_col(v, t, tpr);
     if (c >= cols) return;
 #pragma unroll
     for (int i = 0; i < int(sizeof(T) / 2); ++i)
@@ -259,7 +367,7 @@ __device__ __forceinline__ void copy_row8(uint32_t to, const T* row, int v, int3
 // (What lies past the last column has to be zero there.)
 template <typename T>
 __device__ __forceinline__ void take_row8(Raw8<T>& r, uint32_t from, int v, int32_t t, int32_t tpr) {
-    const uint32_t at = from + uint32_t(row_col<true>(v, 0, t, tpr)) * uint32_t(sizeof(T));
+    const uint32_t at = from + uint32_t(row_col(v, t, tpr)) * uint32_t(sizeof(T));
 #pragma unroll
     for (int i = 0; i < int(sizeof(T) / 2); ++i) {
         const uint4 x = ptx::ld_shared_v4(at + 16u * i);
@@ -272,7 +380,7 @@ __device__ __forceinline__ void clear_past(uint32_t ring, uint32_t rows, uint32_
                                            int32_t cols) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        const int32_t c = row_col<true>(v, 0, t, tpr);
+        const int32_t c = row_col(v, t, tpr);
         if (c < cols) continue;
         for (uint32_t r = 0; r < rows; ++r)
 #pragma unroll

@@ -365,6 +365,53 @@ def test_moe_rows(gbr, case):
     gbr.check_device()
 
 
+def placed(t, start, ld, fill=5.0):
+    """A copy of `t` that begins `start` elements after a 16-byte boundary, rows `ld` apart; and all that lies around it."""
+    whole = torch.full((start + len(t) * ld + 8,), fill, dtype=t.dtype, device=t.device)
+    view = whole.as_strided(t.shape, (ld, 1), start)
+    view.copy_(t)
+    return view, whole
+
+
+def others(view, whole):
+    """What lies around a placed matrix."""
+    rest = whole.clone()
+    rest.as_strided(view.shape, view.stride(), view.storage_offset()).fill_(5.0)
+    return rest
+
+
+@pytest.mark.parametrize("dt", [BF, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("D", [1, 7, 8, 9, 15, 17, 248, 257, 2047])
+def test_moe_rows_and_quantize_start_anywhere(gbr, D, dt):
+    T, k, E = 11, 2, 3
+    ids = choices(T, k, E)
+    positions, offsets = gbr.moe_sort(ids, E)
+    g = rng(D)
+    X, Ys, ones = normal(g, (T, D), dtype=dt), normal(g, (T * k, D), dtype=dt), torch.ones(T, k, device="cuda")
+    at = positions.long()
+    rows = torch.empty_like(Ys)
+    for j in range(k):
+        rows[at[:, j]] = X
+    # two terms, weights of one: exact in fp32, rounded once
+    total = (Ys.float()[at[:, 0]] + Ys.float()[at[:, 1]]).to(dt)
+    want = gbr.quantize_mxfp4(X)
+    for start in range(8):
+        for ld in (D + (-D % 8), D + (-D % 8) + 3):
+            x, _ = placed(X, start, ld)
+            y, _ = placed(Ys, 7 - start, ld)
+            out, around = placed(torch.zeros_like(Ys), start, ld)
+            gbr.moe_dispatch(x, positions, offsets, Xs=out)
+            assert torch.equal(out, rows) and bool((others(out, around) == 5).all())
+            out, around = placed(torch.zeros_like(X), start, ld)
+            gbr.moe_combine(y, positions, Y=out)
+            assert torch.equal(out, total) and bool((others(out, around) == 5).all())
+            out, around = placed(torch.zeros_like(Ys), start, ld)
+            gbr.moe_combine_backward(x, y, positions, offsets, ones, dYs=out, needs=(True, False))
+            assert torch.equal(out, rows) and bool((others(out, around) == 5).all())
+            got = gbr.quantize_mxfp4(x)
+            assert torch.equal(got.data, want.data) and torch.equal(got.scales, want.scales)
+
+
 def test_moe_rows_needs_and_in_place(gbr):
     a = row_inputs((50, 3, 520, 8, "bf16", 0.2))
     dYs, dw = gbr.moe_combine_backward(a["dY"], a["Ys"], a["p"], a["o"], a["w"])
