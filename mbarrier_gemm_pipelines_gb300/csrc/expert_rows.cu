@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(256, kResident<T>) moe_combine_grad_kernel(con
                             for (int v = 0; v < kV; ++v) store_row8<T, A>(a.Xs + r * a.ldxs, zero, v0 + v, t, tpr, cols);
                 }
                 if (!dots) continue;
-                group_sum(dot, buf, tpr);
+                group_sum(dot, buf, tpr, group);
                 if (t == 0)
 #pragma unroll
                     for (int j = 0; j < kJ; ++j)

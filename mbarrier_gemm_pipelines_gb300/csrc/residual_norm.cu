@@ -30,7 +30,7 @@ struct Args {
     const T *X, *R, *G;
     const float *post, *pre;
     T *S, *H;
-    int64_t ldx, ldr, ldg, lds, ldh;
+    int64_t ldx, ldr, ldg, lds, ldh, ld_odd;            // ld_odd: of the rows, whole aligned pieces left out
     int32_t rows, cols, per_gate;      // rows that share a row of G
     float scale, eps, inv_cols;
 };
@@ -43,8 +43,8 @@ template <typename T, int V, bool VEC>
 __global__ void __launch_bounds__(1024) residual_norm_kernel(const Args<T> a, int32_t tpr) {
     __shared__ float buf[2][1][32];
     ptx::griddep_wait();
-    const int32_t t = int32_t(threadIdx.x) % tpr;
-    const int64_t row = int64_t(blockIdx.x) * (int32_t(blockDim.x) / tpr) + int32_t(threadIdx.x) / tpr;
+    const int32_t t = int32_t(threadIdx.x) % tpr, group = int32_t(threadIdx.x) / tpr;
+    const int64_t row = int64_t(blockIdx.x) * (int32_t(blockDim.x) / tpr) + group;
     const int32_t cols = row < a.rows ? a.cols : 0;    // a group past the end only keeps the barriers
     float s[V][8];
 #pragma unroll
@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(1024) residual_norm_kernel(const Args<T> a, in
             for (int v = 0; v < V; ++v)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) sum[0] = fmaf(s[v][j], s[v][j], sum[0]);
-            group_sum(sum, buf[0], tpr);
+            group_sum(sum, buf[0], tpr, group);
             q = root(sum[0], a.inv_cols, a.eps);
         }
 #pragma unroll
@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(1024) residual_norm_kernel(const Args<T> a, in
     for (int v = 0; v < V; ++v)
 #pragma unroll
         for (int j = 0; j < 8; ++j) sum[0] = fmaf(s[v][j], s[v][j], sum[0]);
-    group_sum(sum, buf[1], tpr);
+    group_sum(sum, buf[1], tpr, group);
     const float q = root(sum[0], a.inv_cols, a.eps);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -104,32 +104,53 @@ __global__ void __launch_bounds__(1024) residual_norm_kernel(const Args<T> a, in
 // Many rows: CTAs that stay, blockDim.x / tpr rows a turn, the weights in registers and the next kAhead turns' X, R and
 // gate on their way into shared memory, each thread its own 16 bytes, so that nobody waits for another's copy.  A gate
 // per channel is in the weights.  row_bytes: of a row in shared memory; step: of a turn's rows of all inputs.
+// ODD: rows start off 16 bytes, all operands' alike.  A CTA's are eight apart, so that they too start alike; its threads'
+// pieces begin at the aligned address in front of a row, and only a row's ends go element by element.
 // 16384 x 4096 bf16 with all but row gates: a row a CTA 131 us, this 84 (6.4 TB/s).  More on their way is slower, HBM
 // reading and writing at once: three CTAs an SM and three turns ahead 97, two and three 84 to 88, two and five 95.
-template <typename T, int V, int kAhead, int kMost>
-__global__ void __launch_bounds__(kMost, kMost == 256 ? 2 : 1) residual_norm_stream_kernel(const Args<T> a, int32_t tpr,
+template <typename T, int V, int kAhead, int kMost, bool ODD>
+__global__ void __launch_bounds__(kMost, kMost == 512 ? 1 : 2) residual_norm_stream_kernel(const Args<T> a, int32_t tpr,
                                                                                        uint32_t row_bytes, uint32_t step) {
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ float buf[2][1][32];
     ptx::griddep_wait();
     const int32_t t = int32_t(threadIdx.x) % tpr, group = int32_t(threadIdx.x) / tpr, groups = int32_t(blockDim.x) / tpr;
-    const int32_t cols = a.cols;
+    // ODD: the elements between the aligned address in front of a row and the row, the same for all rows of this CTA.
+    constexpr int32_t kStep = ODD ? 8 : 1;
+    int64_t first = ODD ? int64_t(blockIdx.x / 8) * groups * 8 + blockIdx.x % 8 : int64_t(blockIdx.x) * groups;
+    const int32_t off = ODD ? int32_t(first * a.ld_odd % int32_t(16 / sizeof(T))) : 0, cols = a.cols + off;
     const bool has_r = a.R != nullptr, one_gate = a.G != nullptr && a.per_gate == a.rows, gates = a.G != nullptr && !one_gate;
     const uint32_t base = ptx::smem_addr(ring) + uint32_t(group) * row_bytes, wide = row_bytes * uint32_t(groups);
+    auto copy = [&](uint32_t to, const T* from, int v) {
+        if (ODD) copy_row8_from(to, from - off, v, t, tpr, cols);
+        else copy_row8(to, from, v, t, tpr, cols);
+    };
+    auto take = [&](Raw8<T>& x, uint32_t from, int v) {
+        take_row8(x, from, v, t, tpr);
+        if (ODD && v == 0 && t == 0) clear_front(x, off);
+    };
+    auto load = [&](F2 (&x)[4], const auto* from, int v) {
+        if constexpr (ODD) load_pairs_from(x, from, v, t, tpr, off, cols);
+        else load_pairs<std::remove_cv_t<std::remove_pointer_t<decltype(from)>>, kVec>(x, from, v, t, tpr, cols);
+    };
+    auto store = [&](T* to, const F2 (&x)[4], int v, bool in) {
+        if (ODD) store_pairs_from(to - off, x, v, t, tpr, off, in ? cols : 0);
+        else store_pairs<T, kVec>(to, x, v, t, tpr, in ? cols : 0);
+    };
     auto fetch = [&](int64_t row, uint32_t slot) {
         if (row < a.rows) {
             uint32_t to = base + slot * step;
 #pragma unroll
-            for (int v = 0; v < V; ++v) copy_row8(to, a.X + row * a.ldx, v, t, tpr, cols);
+            for (int v = 0; v < V; ++v) copy(to, a.X + row * a.ldx, v);
             if (has_r) {
                 to += wide;
 #pragma unroll
-                for (int v = 0; v < V; ++v) copy_row8(to, a.R + row * a.ldr, v, t, tpr, cols);
+                for (int v = 0; v < V; ++v) copy(to, a.R + row * a.ldr, v);
             }
             if (gates) {
                 to += wide;
 #pragma unroll
-                for (int v = 0; v < V; ++v) copy_row8(to, a.G + row / a.per_gate * a.ldg, v, t, tpr, cols);
+                for (int v = 0; v < V; ++v) copy(to, a.G + row / a.per_gate * a.ldg, v);
             }
         }
         copy_async_commit();
@@ -140,9 +161,9 @@ __global__ void __launch_bounds__(kMost, kMost == 256 ? 2 : 1) residual_norm_str
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         F2 g[4];
-        if (post) load_pairs<float, true>(w[v], a.post, v, t, tpr, cols);
-        if (a.pre != nullptr) load_pairs<float, true>(wpre[v], a.pre, v, t, tpr, cols);
-        if (one_gate) load_pairs<T, true>(g, a.G, v, t, tpr, cols);
+        if (post) load(w[v], a.post, v);
+        if (a.pre != nullptr) load(wpre[v], a.pre, v);
+        if (one_gate) load(g, a.G, v);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             w[v][i] = post ? mul2(w[v][i], f2(a.scale)) : f2(a.scale);
@@ -151,20 +172,19 @@ __global__ void __launch_bounds__(kMost, kMost == 256 ? 2 : 1) residual_norm_str
     }
     clear_past<T, V>(ptx::smem_addr(ring), kAhead * step / row_bytes, row_bytes, t, tpr, cols);
     const int64_t turn = int64_t(gridDim.x) * groups;
-    int64_t first = int64_t(blockIdx.x) * groups;
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) fetch(first + group + i * turn, uint32_t(i));
+    for (int i = 0; i < kAhead; ++i) fetch(first + group * kStep + i * turn, uint32_t(i));
     for (uint32_t slot = 0; first < a.rows; first += turn, slot = slot + 1 == kAhead ? 0 : slot + 1) {
-        const int64_t row = first + group;
-        const int32_t out = row < a.rows ? cols : 0;    // a group past the end only keeps the barriers
+        const int64_t row = first + group * kStep;
+        const bool in = row < a.rows;                   // a group past the end only keeps the barriers
         copy_async_wait<kAhead - 1>();
         const uint32_t from = base + slot * step;
         Raw8<T> x[V], r[V] = {}, g[V] = {};
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            take_row8(x[v], from, v, t, tpr);
-            if (has_r) take_row8(r[v], from + wide, v, t, tpr);
-            if (gates) take_row8(g[v], from + (has_r ? 2u : 1u) * wide, v, t, tpr);
+            take(x[v], from, v);
+            if (has_r) take(r[v], from + wide, v);
+            if (gates) take(g[v], from + (has_r ? 2u : 1u) * wide, v);
         }
         float q = 1.f;
         if (post) {
@@ -174,7 +194,7 @@ __global__ void __launch_bounds__(kMost, kMost == 256 ? 2 : 1) residual_norm_str
 #pragma unroll
                 for (int i = 0; i < 4; ++i) xx = fma2(raw_pair(x[v], i), raw_pair(x[v], i), xx);
             float sum[1] = {sum_pair(xx)};
-            group_sum(sum, buf[0], tpr);
+            group_sum(sum, buf[0], tpr, group);
             q = root(sum[0], a.inv_cols, a.eps);
         }
         F2 s[V][4], ss = f2(0.f);
@@ -187,10 +207,10 @@ __global__ void __launch_bounds__(kMost, kMost == 256 ? 2 : 1) residual_norm_str
                 s[v][i] = fma2(s[v][i], w[v][i], raw_pair(r[v], i));
                 ss = fma2(s[v][i], s[v][i], ss);
             }
-            if (a.S != nullptr) store_pairs<T, true>(a.S + row * a.lds, s[v], v, t, tpr, out);
+            if (a.S != nullptr) store(a.S + row * a.lds, s[v], v, in);
         }
         float sum[1] = {sum_pair(ss)};
-        if (a.H != nullptr) group_sum(sum, buf[1], tpr);
+        if (a.H != nullptr) group_sum(sum, buf[1], tpr, group);
         // The slot has been read into registers that the lines above have used.
         fetch(row + kAhead * turn, slot);
         if (a.H != nullptr) {
@@ -200,7 +220,7 @@ __global__ void __launch_bounds__(kMost, kMost == 256 ? 2 : 1) residual_norm_str
                 F2 h[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) h[i] = mul2(mul2(s[v][i], p), wpre[v][i]);
-                store_pairs<T, true>(a.H + row * a.ldh, h, v, t, tpr, out);
+                store(a.H + row * a.ldh, h, v, in);
             }
         }
         if (tpr > 32 && (!post || a.H == nullptr)) __syncthreads();   // buf, for the next row
@@ -229,7 +249,7 @@ __global__ void __launch_bounds__(1024) residual_norm_long_kernel(const Args<T> 
                 const float x = to_f32(a.X[row * a.ldx + c]);
                 sum[0] = fmaf(x, x, sum[0]);
             }
-            group_sum(sum, buf[0], 1024);
+            group_sum(sum, buf[0], 1024, 0);
             q = root(sum[0], a.inv_cols, a.eps);
         }
         float r = 0.f;
@@ -239,7 +259,7 @@ __global__ void __launch_bounds__(1024) residual_norm_long_kernel(const Args<T> 
                 const float s = sum_at(a, row, q, c);
                 sum[0] = fmaf(s, s, sum[0]);
             }
-            group_sum(sum, buf[1], 1024);
+            group_sum(sum, buf[1], 1024, 0);
             r = root(sum[0], a.inv_cols, a.eps);
         }
         for (int32_t c = int32_t(threadIdx.x); c < a.cols; c += 1024) {
@@ -257,7 +277,7 @@ struct GradArgs {
     const T *dS, *dH, *X, *S, *G;
     const float *post, *pre;
     T *dX, *dR, *dG;
-    int64_t ldds, lddh, ldx, lds, ldg, lddx, lddr, lddg;
+    int64_t ldds, lddh, ldx, lds, ldg, lddx, lddr, lddg, ld_odd;      // ld_odd: of the rows, whole aligned pieces left out
     int32_t rows, cols, per_gate;
     float scale, eps, inv_cols;
     // Sums over rows: `items` runs of rows, `segments` of them to a gate; each CTA takes a
@@ -290,17 +310,18 @@ struct RowWalk {
 };
 
 // One CTA: its items' rows, blockDim.x / tpr at a time.  Thread t of each group keeps the sums of
-// its columns; groups are joined in order through shared memory.  kAhead > 0 (rows on 16 bytes): that many
+// its columns; groups are joined in order through shared memory.  kAhead > 0 (rows on 16 bytes, or ODD as above): that many
 // turns' rows of all inputs are on their way into shared memory, each thread its own 16 bytes, so that nobody
 // waits for another's copy; 0: they are loaded in their turn, any alignment.
 // FULL: a training step's call, with both norms, dS and all of dX, dR, dpost and dpre, without a gate an element.  What
 // is there need not be asked then (4096 x 4096: 631 instructions a warp and row of 8 columns a thread if it is, 447 not),
 // and the registers are kept for the row: the weights lie in shared memory, each thread's where it alone reads them, and
 // dpost's sum in its place in scratch, added to after a gate's rows.
-template <typename T, int V, int kAhead, bool FULL>
+template <typename T, int V, int kAhead, bool FULL, bool ODD>
 __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<T> a, int32_t tpr, uint32_t row_bytes,
                                                                  uint32_t step) {
-    constexpr bool VEC = kAhead > 0;
+    static_assert(!ODD || kAhead > 0);
+    constexpr int A = kAhead > 0 ? kVec : kStrided;
     __shared__ float buf[2][3][32];
     // The ring; behind it, where groups > 1, [groups][8][tpr] floats.
     extern __shared__ __align__(16) uint8_t ring[];
@@ -309,6 +330,32 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<
     const int32_t groups = int32_t(blockDim.x) / tpr;
     const int32_t i0 = int32_t(int64_t(a.items) * blockIdx.x / gridDim.x);
     const int32_t i1 = int32_t(int64_t(a.items) * (blockIdx.x + 1) / gridDim.x);
+    // ODD: CTA b has rows 8 (b / 8 groups + group) + b % 8 and on, the same number of elements, `off`, behind an aligned
+    // address; columns go from there to `all_cols`.
+    constexpr int32_t kStep = ODD ? 8 : 1;
+    const int64_t odd_row = int64_t(blockIdx.x / 8) * groups * 8 + blockIdx.x % 8;
+    const int64_t turn = ODD ? int64_t(gridDim.x) * groups : groups;
+    const int32_t off = ODD ? int32_t(odd_row * a.ld_odd % int32_t(16 / sizeof(T))) : 0, all_cols = a.cols + off;
+    auto load = [&](F2 (&x)[4], const auto* from, int v) {
+        if constexpr (ODD) load_pairs_from(x, from, v, t, tpr, off, all_cols);
+        else load_pairs<std::remove_cv_t<std::remove_pointer_t<decltype(from)>>, A>(x, from, v, t, tpr, all_cols);
+    };
+    auto store = [&](T* to, const F2 (&x)[4], int v, int32_t cols) {
+        if constexpr (ODD) store_pairs_from(to - off, x, v, t, tpr, off, cols);
+        else store_pairs<T, A>(to, x, v, t, tpr, cols);
+    };
+    auto store_sums = [&](auto* to, const F2 (&x)[4], int v) {
+        if constexpr (ODD) store_pairs_from(to - off, x, v, t, tpr, off, all_cols, true);
+        else store_pairs<std::remove_pointer_t<decltype(to)>, A>(to, x, v, t, tpr, all_cols);
+    };
+    auto copy = [&](uint32_t to, const T* from, int v) {
+        if constexpr (ODD) copy_row8_from(to, from - off, v, t, tpr, all_cols);
+        else copy_row8(to, from, v, t, tpr, all_cols);
+    };
+    auto take = [&](Raw8<T>& x, uint32_t from, int v) {
+        take_row8(x, from, v, t, tpr);
+        if (ODD && v == 0 && t == 0) clear_front(x, off);
+    };
     const bool post = FULL || a.post != nullptr, pre = FULL || a.pre != nullptr, has_x = FULL || a.X != nullptr;
     const bool has_ds = FULL || a.dS != nullptr, want_x = FULL || a.dX != nullptr, want_r = FULL || a.dR != nullptr;
     const bool want_post = FULL || a.want_post, want_pre = FULL || a.want_pre;
@@ -323,8 +370,8 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<
     const uint32_t own_gw = own + 32u * V * blockDim.x;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        if (gate_rows && post) load_pairs<float, VEC>(wpost[v], a.post, v, t, tpr, a.cols);
-        if (pre) load_pairs<float, VEC>(wpre[v], a.pre, v, t, tpr, a.cols);
+        if (gate_rows && post) load(wpost[v], a.post, v);
+        if (pre) load(wpre[v], a.pre, v);
         if (FULL) put_pairs(own + uint32_t(v) * 32u * blockDim.x, wpre[v]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) spost[v][i] = spre[v][i] = srun[v][i] = f2(0.f);
@@ -351,53 +398,55 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<
     const uint32_t ring0 = ptx::smem_addr(ring) + uint32_t(group) * row_bytes, at_x = pre ? 2 : 0;
     const uint32_t at_ds = at_x + (has_x ? 1 : 0), at_g = at_ds + (has_ds ? 1 : 0), wide = row_bytes * groups;
     RowWalk<T> ahead = {i0, i1, 0, 0};
-    ahead.enter(a);
+    if (ODD) ahead.first = odd_row, ahead.end = a.rows;
+    else ahead.enter(a);
     bool more = ahead.settle(a);
     auto fetch = [&](uint32_t slot) {
-        const int64_t row = ahead.first + group;
+        const int64_t row = ahead.first + group * kStep;
         if (more && row < ahead.end) {
             const uint32_t to = ring0 + slot * step;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 if (pre) {
-                    copy_row8(to, a.dH + row * a.lddh, v, t, tpr, a.cols);
-                    copy_row8(to + wide, a.S + row * a.lds, v, t, tpr, a.cols);
+                    copy(to, a.dH + row * a.lddh, v);
+                    copy(to + wide, a.S + row * a.lds, v);
                 }
-                if (has_x) copy_row8(to + at_x * wide, a.X + row * a.ldx, v, t, tpr, a.cols);
-                if (has_ds) copy_row8(to + at_ds * wide, a.dS + row * a.ldds, v, t, tpr, a.cols);
-                if (gate_rows) copy_row8(to + at_g * wide, a.G + row * a.ldg, v, t, tpr, a.cols);
+                if (has_x) copy(to + at_x * wide, a.X + row * a.ldx, v);
+                if (has_ds) copy(to + at_ds * wide, a.dS + row * a.ldds, v);
+                if (gate_rows) copy(to + at_g * wide, a.G + row * a.ldg, v);
             }
         }
         copy_async_commit();
         if (more) {
-            ahead.first += groups;
+            ahead.first += turn;
             more = ahead.settle(a);
         }
     };
-    if (kAhead > 0) clear_past<T, V>(ptx::smem_addr(ring), kAhead * step / row_bytes, row_bytes, t, tpr, a.cols);
+    if (kAhead > 0) clear_past<T, V>(ptx::smem_addr(ring), kAhead * step / row_bytes, row_bytes, t, tpr, all_cols);
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) fetch(uint32_t(i));
     uint32_t slot = 0;
     for (int32_t item = i0; item < i1; ++item) {
         const int32_t g = item / a.segments, seg = item % a.segments;
         const int64_t base = int64_t(g) * a.span;
-        const int64_t r0 = base + int64_t(a.span) * seg / a.segments, r1 = base + int64_t(a.span) * (seg + 1) / a.segments;
+        const int64_t r0 = ODD ? odd_row : base + int64_t(a.span) * seg / a.segments;
+        const int64_t r1 = ODD ? a.rows : base + int64_t(a.span) * (seg + 1) / a.segments;
         const T* gate = run_gate ? a.G + g * a.ldg : nullptr;
         F2 gw[V][4];                                    // gate times weight
         if (!gate_rows && weighted)
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 F2 w[4];
-                if (post) load_pairs<float, VEC>(gw[v], a.post, v, t, tpr, a.cols);
-                if (run_gate) load_pairs<T, VEC>(w, gate, v, t, tpr, a.cols);
+                if (post) load(gw[v], a.post, v);
+                if (run_gate) load(w, gate, v);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) gw[v][i] = !run_gate ? gw[v][i] : post ? mul2(gw[v][i], w[i]) : w[i];
                 if (FULL) put_pairs(own_gw + uint32_t(v) * 32u * blockDim.x, gw[v]);
             }
-        for (int64_t first = r0; first < r1; first += groups) {
-            const int64_t row = first + group;
+        for (int64_t first = r0; first < r1; first += turn) {
+            const int64_t row = first + group * kStep;
             const bool in = row < r1;
-            const int32_t cols = in ? a.cols : 0;
+            const int32_t cols = in ? all_cols : 0;
             Raw8<T> x[V] = {}, s[V] = {}, dh[V] = {}, ds[V] = {}, gt[V] = {};
             if (kAhead > 0) {
                 copy_async_wait<(kAhead > 0 ? kAhead : 1) - 1>();
@@ -406,23 +455,23 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<
 #pragma unroll
                     for (int v = 0; v < V; ++v) {
                         if (pre) {
-                            take_row8(dh[v], from, v, t, tpr);
-                            take_row8(s[v], from + wide, v, t, tpr);
+                            take(dh[v], from, v);
+                            take(s[v], from + wide, v);
                         }
-                        if (has_x) take_row8(x[v], from + at_x * wide, v, t, tpr);
-                        if (has_ds) take_row8(ds[v], from + at_ds * wide, v, t, tpr);
-                        if (gate_rows) take_row8(gt[v], from + at_g * wide, v, t, tpr);
+                        if (has_x) take(x[v], from + at_x * wide, v);
+                        if (has_ds) take(ds[v], from + at_ds * wide, v);
+                        if (gate_rows) take(gt[v], from + at_g * wide, v);
                     }
             } else {
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    if (has_x) load_raw8<VEC>(x[v], a.X + row * a.ldx, v, t, tpr, cols);
+                    if (has_x) load_raw8<A>(x[v], a.X + row * a.ldx, v, t, tpr, cols);
                     if (pre) {
-                        load_raw8<VEC>(s[v], a.S + row * a.lds, v, t, tpr, cols);
-                        load_raw8<VEC>(dh[v], a.dH + row * a.lddh, v, t, tpr, cols);
+                        load_raw8<A>(s[v], a.S + row * a.lds, v, t, tpr, cols);
+                        load_raw8<A>(dh[v], a.dH + row * a.lddh, v, t, tpr, cols);
                     }
-                    if (has_ds) load_raw8<VEC>(ds[v], a.dS + row * a.ldds, v, t, tpr, cols);
-                    if (gate_rows) load_raw8<VEC>(gt[v], a.G + row * a.ldg, v, t, tpr, cols);
+                    if (has_ds) load_raw8<A>(ds[v], a.dS + row * a.ldds, v, t, tpr, cols);
+                    if (gate_rows) load_raw8<A>(gt[v], a.G + row * a.ldg, v, t, tpr, cols);
                 }
             }
             F2 ss = f2(0.f), us = f2(0.f), xx = f2(0.f);
@@ -446,7 +495,7 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<
                         xx = fma2(X, X, xx);
                     }
             float sum[3] = {sum_pair(ss), sum_pair(us), sum_pair(xx)};
-            if (pre || post) group_sum(sum, buf[0], tpr);
+            if (pre || post) group_sum(sum, buf[0], tpr, group);
             // A group without a row adds zeros.
             const float r = in ? root(sum[0], a.inv_cols, a.eps) : 0.f, rc = r * r * r * sum[1] * a.inv_cols;
             const float q = !post ? 1.f : in ? root(sum[2], a.inv_cols, a.eps) : 0.f;
@@ -470,7 +519,7 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<
             }
             if (want_r)
 #pragma unroll
-                for (int v = 0; v < V; ++v) store_pairs<T, VEC>(a.dR + row * a.lddr, d[v], v, t, tpr, cols);
+                for (int v = 0; v < V; ++v) store(a.dR + row * a.lddr, d[v], v, cols);
             const F2 q2 = f2(q);
             if (gate_rows) {
 #pragma unroll
@@ -487,7 +536,7 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<
                             dot = fma2(d[v][i], X, dot);
                         }
                     }
-                    if (a.want_gate) store_pairs<T, VEC>(a.dG + row * a.lddg, dg, v, t, tpr, cols);
+                    if (a.want_gate) store(a.dG + row * a.lddg, dg, v, cols);
                 }
             } else if (weighted) {
 #pragma unroll
@@ -511,7 +560,7 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<
                 F2 m2 = f2(0.f);
                 if (post) {
                     float sums[1] = {sum_pair(dot)};
-                    group_sum(sums, buf[1], tpr);
+                    group_sum(sums, buf[1], tpr, group);
                     m2 = f2(-a.scale * (q * q * q * sums[0] * a.inv_cols));
                 }
                 const F2 k2 = f2(a.scale * q);
@@ -522,7 +571,7 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<
                         d[v][i] = mul2(d[v][i], k2);
                         if (post) d[v][i] = fma2(raw_pair(x[v], i), m2, d[v][i]);
                     }
-                    store_pairs<T, VEC>(a.dX + row * a.lddx, d[v], v, t, tpr, cols);
+                    store(a.dX + row * a.lddx, d[v], v, cols);
                 }
             }
             if (tpr > 32 && (!want_x || !post)) __syncthreads();   // buf[0], for the next rows
@@ -535,15 +584,15 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<
                 for (int v = 0; v < V; ++v) {
                     F2 w[4];
                     float* sum = a.post_part + int64_t(blockIdx.x) * a.cols;
-                    if (run_gate) load_pairs<T, VEC>(w, gate, v, t, tpr, a.cols);
-                    if (FULL && item > i0) load_pairs<float, VEC>(spost[v], sum, v, t, tpr, a.cols);
+                    if (run_gate) load(w, gate, v);
+                    if (FULL && item > i0) load(spost[v], sum, v);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const F2 k = run_gate ? mul2(f2(a.scale), w[i]) : f2(a.scale);
                         spost[v][i] = fma2(srun[v][i], k, spost[v][i]);
                     }
                     if (FULL) {
-                        store_pairs<float, VEC>(sum, spost[v], v, t, tpr, a.cols);
+                        store_sums(sum, spost[v], v);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) spost[v][i] = f2(0.f);
                     }
@@ -554,16 +603,16 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<
 #pragma unroll
                     for (int v = 0; v < V; ++v) {
                         F2 w[4];
-                        if (post) load_pairs<float, VEC>(w, a.post, v, t, tpr, a.cols);
+                        if (post) load(w, a.post, v);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             srun[v][i] = mul2(srun[v][i], f2(a.scale));
                             if (post) srun[v][i] = mul2(srun[v][i], w[i]);
                         }
                         if (a.segments > 1)
-                            store_pairs<float, VEC>(a.gate_part + int64_t(item) * a.cols, srun[v], v, t, tpr, a.cols);
+                            store_sums(a.gate_part + int64_t(item) * a.cols, srun[v], v);
                         else
-                            store_pairs<T, VEC>(a.dG + g * a.lddg, srun[v], v, t, tpr, a.cols);
+                            store_sums(a.dG + g * a.lddg, srun[v], v);
                     }
             }
 #pragma unroll
@@ -578,14 +627,14 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<
         if (group == 0)
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                store_pairs<float, VEC>(a.post_part + int64_t(blockIdx.x) * a.cols, spost[v], v, t, tpr, a.cols);
+                store_sums(a.post_part + int64_t(blockIdx.x) * a.cols, spost[v], v);
     }
     if (want_pre) {
         join(spre);
         if (group == 0)
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                store_pairs<float, VEC>(a.pre_part + int64_t(blockIdx.x) * a.cols, spre[v], v, t, tpr, a.cols);
+                store_sums(a.pre_part + int64_t(blockIdx.x) * a.cols, spre[v], v);
     }
 }
 
@@ -621,7 +670,7 @@ __global__ void __launch_bounds__(1024, 1) residual_norm_stats_kernel(const Grad
             }
         }
         float sum[3] = {sum_pair(ss), sum_pair(us), sum_pair(xx)};
-        group_sum(sum, buf[0], 1024);
+        group_sum(sum, buf[0], 1024, 0);
         const float r = root(sum[0], a.inv_cols, a.eps), rc = r * r * r * sum[1] * a.inv_cols;
         const float q = post ? root(sum[2], a.inv_cols, a.eps) : 1.f;
         if (post)
@@ -646,7 +695,7 @@ __global__ void __launch_bounds__(1024, 1) residual_norm_stats_kernel(const Grad
                 }
             }
         float dot[1] = {sum_pair(vx)};
-        group_sum(dot, buf[1], 1024);
+        group_sum(dot, buf[1], 1024, 0);
         if (threadIdx.x == 0) stats[row] = make_float4(r, rc, q, a.scale * (q * q * q * dot[0] * a.inv_cols));
     }
 }
@@ -769,6 +818,21 @@ bool aligned16(const void* p, int64_t ld, int64_t rows) {
            (reinterpret_cast<uintptr_t>(p) % 16 == 0 && (rows <= 1 || ld % int64_t(16 / sizeof(T)) == 0));
 }
 
+// Rows of all the matrices start alike, seen from the aligned address in front of them: each *ld_odd elements on from the last,
+// but for whole pieces of 16 bytes.
+template <typename T, int N>
+bool start_alike(const Mat* const (&mats)[N], int64_t* ld_odd) {
+    constexpr int64_t kPiece = 16 / sizeof(T);
+    int64_t ld = -1;
+    for (const Mat* m : mats) {
+        if (m->p == nullptr) continue;
+        if (reinterpret_cast<uintptr_t>(m->p) % 16 != 0 || (ld >= 0 && m->ld % kPiece != ld)) return false;
+        ld = m->ld % kPiece;
+    }
+    *ld_odd = ld;
+    return true;
+}
+
 // Threads a row: the fewest warps (or less, as `least` lets them) that hold it with V vectors each.
 int threads_for(int64_t cols, int V, int least = 32) {
     int tpr = least;
@@ -783,57 +847,74 @@ void* forward_kernel(bool vec) {
 }
 
 template <typename T, int kAhead, int kMost>
-void* stream_kernel() {
-    return reinterpret_cast<void*>(&residual_norm_stream_kernel<T, 2, kAhead, kMost>);
+void* stream_kernel(bool odd) {
+    return odd ? reinterpret_cast<void*>(&residual_norm_stream_kernel<T, 2, kAhead, kMost, true>)
+               : reinterpret_cast<void*>(&residual_norm_stream_kernel<T, 2, kAhead, kMost, false>);
+}
+
+// Threads a row where rows are streamed: whole warps, as many as it takes.
+int warps_for(int64_t cols, int V) {
+    return cols <= 32 * 8 * V ? threads_for(cols, V, 4) : int(cdiv(cols, 32 * 8 * V)) * 32;
 }
 
 struct StreamPlan {
     int32_t tpr;
-    int threads, ctas, ahead;                           // ctas: an SM, by registers
+    int threads, ctas, ahead;                           // ctas: an SM
     size_t step;
 };
-StreamPlan stream_plan(const ResidualNormArgs& s, size_t esize) {
+// `cols`: with what may lie between an aligned address and a row.
+// An SM's registers hold 640 threads (bf16; up to 102 registers a thread), 512 (fp32).  Against warps in powers of two and
+// at most two CTAs, us, bf16: 8192 x 5120 53 / 76, 16384 x 2560 55 / 70, 16384 x 1536 34 / 39.
+StreamPlan stream_plan(const ResidualNormArgs& s, int32_t cols, size_t esize) {
     StreamPlan p;
-    const int inputs = 1 + (s.R.p ? 1 : 0) + (s.G.p && s.gates > 1 ? 1 : 0);
-    p.tpr = threads_for(s.cols, 2, 4);
-    p.threads = std::max(256, int(p.tpr)), p.ctas = p.threads > 256 ? 1 : 2;
+    const int inputs = 1 + (s.R.p ? 1 : 0) + (s.G.p && s.gates > 1 ? 1 : 0), most = esize == 2 ? 640 : 512;
+    p.tpr = warps_for(cols, 2);
+    p.threads = std::max(1, 256 / p.tpr) * p.tpr, p.ctas = most / p.threads;
     p.step = size_t(p.threads) * 16 * esize * size_t(inputs);
-    p.ahead = p.threads > 256 && 3 * p.step <= 216 * 1024 ? 3 : 2;
+    p.ahead = p.ctas == 1 && 3 * p.step <= 216 * 1024 ? 3 : 2;
     return p;
 }
 // Rows of up to 8192 columns, and enough of them for CTAs that stay: eight turns of all.
-bool streams(const ResidualNormArgs& s, size_t esize, int sm_count) {
-    if (s.cols > 8192) return false;
-    const StreamPlan p = stream_plan(s, esize);
+bool streams(const ResidualNormArgs& s, int32_t cols, size_t esize, int sm_count) {
+    if (cols > 8192) return false;
+    const StreamPlan p = stream_plan(s, cols, esize);
     return s.rows >= int64_t(8) * sm_count * (p.threads / p.tpr) && size_t(p.ahead) * p.step <= 216 * 1024;
 }
 
 template <typename T>
 int run_forward(const ResidualNormArgs& s, const LibCtx& c, cudaStream_t stream) {
     Args<T> a = {static_cast<const T*>(s.X.p), static_cast<const T*>(s.R.p), static_cast<const T*>(s.G.p), s.post, s.pre,
-                 static_cast<T*>(s.S.w()), static_cast<T*>(s.H.w()), s.X.ld, s.R.ld, s.G.ld, s.S.ld, s.H.ld, s.rows,
-                 s.cols, s.per_gate, s.scale, s.eps, float(1.0 / double(s.cols))};
+                 static_cast<T*>(s.S.w()), static_cast<T*>(s.H.w()), s.X.ld, s.R.ld, s.G.ld, s.S.ld, s.H.ld, 0,
+                 s.rows, s.cols, s.per_gate, s.scale, s.eps, float(1.0 / double(s.cols))};
     bool vec = s.cols % 8 == 0 && aligned16<float>(s.post, 0, 1) && aligned16<float>(s.pre, 0, 1) &&
                aligned16<T>(s.G.p, s.G.ld, s.gates);
     for (const Mat* m : {&s.X, &s.R, &s.S, &s.H}) vec = vec && aligned16<T>(m->p, m->ld, s.rows);
+    // Rows that start anywhere can be streamed where those of all operands start alike, as contiguous tensors' do: us, bf16,
+    // 16384 rows, strided / streamed: 4095 columns 264 / 109, 3001 244 / 76, 1001 64 / 31.
+    const Mat none = {};
+    const bool runs = s.G.p && s.gates > 1 && s.gates < s.rows;
+    const bool odd = !vec && !runs && start_alike<T>({&s.X, &s.R, &s.S, &s.H, s.gates > 1 ? &s.G : &none}, &a.ld_odd);
+    constexpr int32_t kPiece = 16 / sizeof(T);
+    const int32_t wide = odd && a.ld_odd != 0 ? s.cols + kPiece - 1 : s.cols;
     cudaError_t e;
     if (s.cols > 1024 * 32) {
         void* args[] = {&a};
         e = launch_kernel(reinterpret_cast<void*>(&residual_norm_long_kernel<T>),
                           dim3(unsigned(std::min<int64_t>(s.rows, 2 * c.sm_count))), 1024, 0, 1, args, stream);
-    } else if (vec && streams(s, sizeof(T), c.sm_count)) {
-        const StreamPlan p = stream_plan(s, sizeof(T));
+    } else if ((vec || odd) && streams(s, wide, sizeof(T), c.sm_count)) {
+        const StreamPlan p = stream_plan(s, wide, sizeof(T));
         int32_t tpr = p.tpr;
         uint32_t row_bytes = uint32_t(p.tpr * 16 * sizeof(T)), step = uint32_t(p.step);
-        void* kernel = p.threads <= 256 ? stream_kernel<T, 2, 256>()
-                       : p.ahead == 3   ? stream_kernel<T, 3, 512>()
-                                        : stream_kernel<T, 2, 512>();
+        void* kernel = p.ctas > 1     ? stream_kernel<T, 2, sizeof(T) == 2 ? 320 : 256>(odd)
+                       : p.ahead == 3 ? stream_kernel<T, 3, 512>(odd)
+                                      : stream_kernel<T, 2, 512>(odd);
         const size_t smem = size_t(p.ahead) * p.step;
         const int r = raise_kernel_smem(kernel, smem, c.device);
         if (r != GBR_OK) return r;
         void* args[] = {&a, &tpr, &row_bytes, &step};
-        e = launch_kernel(kernel, dim3(unsigned(c.sm_count * std::min<int64_t>(p.ctas, 216 * 1024 / smem))), p.threads, smem,
-                          1, args, stream);
+        int64_t grid = c.sm_count * std::min<int64_t>(p.ctas, 216 * 1024 / smem);
+        if (odd) grid = std::max<int64_t>(8, grid / 8 * 8);     // eight CTAs' rows start in eight ways
+        e = launch_kernel(kernel, dim3(unsigned(grid)), p.threads, smem, 1, args, stream);
     } else {
         const int V = s.cols > 1024 * 16 ? 4 : s.cols > 1024 * 8 ? 2 : 1;
         int32_t tpr = threads_for(s.cols, V, 4);
@@ -848,13 +929,15 @@ int run_forward(const ResidualNormArgs& s, const LibCtx& c, cudaStream_t stream)
 }
 
 template <typename T, int V>
-void* grad_kernel(int ahead, bool full) {
+void* grad_kernel(int ahead, bool full, bool odd) {
+    if (odd) return full ? reinterpret_cast<void*>(&residual_norm_grad_kernel<T, V, 2, true, true>)
+                         : reinterpret_cast<void*>(&residual_norm_grad_kernel<T, 1, 2, false, true>);
     switch (ahead) {
-        case 3: return full ? reinterpret_cast<void*>(&residual_norm_grad_kernel<T, V, 3, true>)
-                            : reinterpret_cast<void*>(&residual_norm_grad_kernel<T, 1, 3, false>);
-        case 2: return full ? reinterpret_cast<void*>(&residual_norm_grad_kernel<T, V, 2, true>)
-                            : reinterpret_cast<void*>(&residual_norm_grad_kernel<T, 1, 2, false>);
-        default: return reinterpret_cast<void*>(&residual_norm_grad_kernel<T, 1, 0, false>);
+        case 3: return full ? reinterpret_cast<void*>(&residual_norm_grad_kernel<T, V, 3, true, false>)
+                            : reinterpret_cast<void*>(&residual_norm_grad_kernel<T, 1, 3, false, false>);
+        case 2: return full ? reinterpret_cast<void*>(&residual_norm_grad_kernel<T, V, 2, true, false>)
+                            : reinterpret_cast<void*>(&residual_norm_grad_kernel<T, 1, 2, false, false>);
+        default: return reinterpret_cast<void*>(&residual_norm_grad_kernel<T, 1, 0, false, false>);
     }
 }
 
@@ -897,32 +980,49 @@ int run_backward(const ResidualNormGradArgs& s, const LibCtx& c, cudaStream_t st
     for (const float* w : {s.post, s.pre, static_cast<const float*>(s.dpost), static_cast<const float*>(s.dpre)})
         vec = vec && aligned16<float>(w, 0, 1);
     const bool gate_rows = s.G.p && s.per_gate == 1;
-    const bool full = vec && s.post && s.pre && s.dS.p && s.dX.p && s.dR.p && a.want_post && a.want_pre && !gate_rows;
+    // Rows that start anywhere, as in the forward pass, if there is one for each SM: us, bf16, strided / streamed: 4096 x 4001
+    // 160 / 61, 4096 x 1001 46 / 27, 301 x 1001 13.6 / 11.9, but 37 x 4001 11.8 / 13.6.
+    constexpr int32_t kPiece = 16 / sizeof(T);
+    const Mat none = {}, &g = gate_rows ? s.G : none, &dg = gate_rows ? s.dG : none;
+    const bool odd = !vec && s.rows >= c.sm_count && (s.gates <= 1 || gate_rows) &&
+                     start_alike<T>({&s.dS, &s.dH, &s.X, &s.S, &s.dX, &s.dR, &g, &dg}, &a.ld_odd);
+    const int32_t wide = odd && a.ld_odd != 0 ? s.cols + kPiece - 1 : s.cols;
+    const bool full = (vec || odd) && s.post && s.pre && s.dS.p && s.dX.p && s.dR.p && a.want_post && a.want_pre && !gate_rows;
     const int inputs = (s.pre ? 2 : 0) + (s.X.p ? 1 : 0) + (s.dS.p ? 1 : 0) + (gate_rows ? 1 : 0);
     // V vectors a thread.  Two where the rows go round (the fewer warps a row, the less of what is done once a warp) and
     // two turns of them fit; rows that do not fit at all have their means taken first (as rows of fp32 of 8192 columns).
     struct Plan {
-        int V, threads, groups, ahead;
+        int V, threads, groups, ctas, ahead;
         int32_t tpr;
         size_t step, join;
     } plan = {};
     auto lay_out = [&](int V) {
-        plan.V = V, plan.tpr = threads_for(s.cols, V), plan.threads = std::max(256, int(plan.tpr));
-        plan.groups = plan.threads / plan.tpr;
+        plan.V = V, plan.tpr = std::max(32, warps_for(wide, V));
+        plan.groups = std::max(1, 256 / plan.tpr), plan.threads = plan.groups * plan.tpr;
+        // An SM: 128 registers a thread.  Against warps in powers of two, at most two CTAs, us, bf16: 4096 x 5120 61 / 71,
+        // 4096 x 2560 33 / 40.
+        plan.ctas = std::max(1, 512 / plan.threads);
         const size_t mine = size_t(plan.threads) * 8 * sizeof(float);
         plan.join = (plan.groups > 1 ? mine : 0) + (full ? 2 * mine * V : 0);
-        plan.step = vec ? size_t(plan.threads) * 8 * V * sizeof(T) * size_t(inputs) : 0;
-        const size_t most = size_t(plan.threads > 256 ? 220 : 111) * 1024 - plan.join;
-        plan.ahead = !vec ? 0 : 3 * plan.step <= most ? 3 : 2 * plan.step <= most ? 2 : 0;
+        plan.step = vec || odd ? size_t(plan.threads) * 8 * V * sizeof(T) * size_t(inputs) : 0;
+        const size_t most = size_t(220 / plan.ctas) * 1024 - plan.join;
+        plan.ahead = !vec && !odd ? 0 : !odd && 3 * plan.step <= most ? 3 : 2 * plan.step <= most ? 2 : 0;
     };
     const bool many = s.rows >= int64_t(c.sm_count) * 8 * std::max(1, 4096 / s.cols);
-    if (s.cols <= 8192) lay_out(full && (many || s.cols > 4096) ? 2 : 1);
-    if (plan.V == 2 && plan.ahead == 0 && s.cols <= 4096) lay_out(1);
-    const bool long_rows = s.cols > 8192 || plan.tpr > 512 || (plan.V == 2 && plan.ahead == 0);
+    if (wide <= 8192) lay_out(full && (many || wide > 4096) ? 2 : 1);
+    if (plan.V == 2 && plan.ahead == 0 && wide <= 4096) lay_out(1);
+    const bool long_rows = wide > 8192 || plan.tpr > 512 || (plan.V == 2 && plan.ahead == 0);
     const int64_t col_ctas = cdiv(s.cols, kLongThreads * 8);
     const int64_t ctas = long_rows ? std::max<int64_t>(1, 4 * c.sm_count / col_ctas)
-                                   : c.sm_count * (plan.threads > 256 ? 1 : 2);
-    const int64_t grid = cut_rows(&a, s.gates, ctas, long_rows ? 1 : plan.groups);
+                                   : c.sm_count * plan.ctas;
+    const bool stream_odd = odd && !long_rows && plan.ahead > 0;
+    int64_t grid;
+    if (stream_odd) {                                   // eight CTAs' rows start in eight ways
+        grid = std::max<int64_t>(8, std::min(ctas, cdiv(s.rows, plan.groups) + 7) / 8 * 8);
+        a.items = a.segments = int32_t(grid), a.span = s.rows;
+    } else {
+        grid = cut_rows(&a, s.gates, ctas, long_rows ? 1 : plan.groups);
+    }
     // Scratch of the sums over rows and of the rows' statistics, in one block.
     PartSums sums = {};
     sums.cols = s.cols;
@@ -963,7 +1063,7 @@ int run_backward(const ResidualNormGradArgs& s, const LibCtx& c, cudaStream_t st
     } else {
         uint32_t row_bytes = uint32_t(plan.tpr * 8 * plan.V * sizeof(T)), step = plan.ahead > 0 ? uint32_t(plan.step) : 0;
         // Without a ring: not FULL.
-        void* kernel = plan.V == 2 ? grad_kernel<T, 2>(plan.ahead, full) : grad_kernel<T, 1>(plan.ahead, full);
+        void* kernel = plan.V == 2 ? grad_kernel<T, 2>(plan.ahead, full, stream_odd) : grad_kernel<T, 1>(plan.ahead, full, stream_odd);
         const size_t smem = plan.join + size_t(plan.ahead) * step;
         if ((r = raise_kernel_smem(kernel, smem, c.device)) != GBR_OK) return r;
         void* args[] = {&a, &plan.tpr, &row_bytes, &step};

@@ -295,9 +295,9 @@ __device__ __forceinline__ float warp_sum(float x) {
     return x;
 }
 
-// Sums of N (1 to 4) values over groups of `tpr` threads (a power of two that divides the block; for several values at
-// least 32).  Every thread
-// of the block calls it; `buf` is this call's own until the next __syncthreads.  The order of the sum is fixed.
+// Sums of N (1 to 4) values over groups of `tpr` threads, whole warps or, for one value, a power of two below 32; this
+// thread's is `group`.  Every
+// thread of the block calls it; `buf` is this call's own until the next __syncthreads.  The order of the sum is fixed.
 //
 // Several values take the shuffles of little more than one: after the first step each half of the warp goes on with two
 // of four, after the second each quarter with one, whose lanes also join the warps' sums.  (Shuffles and what goes with
@@ -316,14 +316,14 @@ __device__ __forceinline__ float fold4(float x0, float x1, float x2, float x3, i
 }
 
 template <int N>
-__device__ __forceinline__ void group_sum(float (&x)[N], float (*buf)[32], int32_t tpr) {
+__device__ __forceinline__ void group_sum(float (&x)[N], float (*buf)[32], int32_t tpr, int32_t group) {
+    if (N == 1 && tpr < 32) {                           // several groups a warp
+        for (int d = tpr / 2; d > 0; d /= 2) x[0] += __shfl_xor_sync(0xffffffffu, x[0], d);
+        return;
+    }
     const int32_t lane = int32_t(threadIdx.x) % 32, warp = int32_t(threadIdx.x) / 32, warps = tpr / 32;
-    const int32_t first = warp & ~(warps - 1);
+    const int32_t first = group * warps;
     if (N == 1) {
-        if (tpr < 32) {                                 // several groups a warp
-            for (int d = tpr / 2; d > 0; d /= 2) x[0] += __shfl_xor_sync(0xffffffffu, x[0], d);
-            return;
-        }
         x[0] = warp_sum(x[0]);
         if (tpr == 32) return;
         if (lane == 0) buf[0][warp] = x[0];
@@ -387,6 +387,58 @@ __device__ __forceinline__ void clear_past(uint32_t ring, uint32_t rows, uint32_
             for (int i = 0; i < int(sizeof(T) / 2); ++i)
                 ptx::st_shared_v4(ring + r * row_bytes + uint32_t(c) * uint32_t(sizeof(T)) + 16u * i, 0, 0, 0, 0);
     }
+}
+
+// Rows that start anywhere but whose operands all start alike: a row from the aligned address in front of it, `off`
+// elements before its first.  Columns are counted from there, up to `end`; those in front of the row become zero.
+template <typename T>
+__device__ __forceinline__ void copy_row8_from(uint32_t to, const T* at, int v, int32_t t, int32_t tpr, int32_t end) {
+    constexpr int32_t kPiece = 16 / int32_t(sizeof(T));
+    const int32_t c = row_col(v, t, tpr);
+    if (c >= end) return;
+#pragma unroll
+    for (int i = 0; i < int(sizeof(T) / 2); ++i) {
+        const int32_t e = c + i * kPiece, n = end - e < kPiece ? end - e : kPiece;
+        ptx::cp_async_16(to + uint32_t(e) * uint32_t(sizeof(T)), at + (n > 0 ? e : c), n > 0 ? uint32_t(n) * uint32_t(sizeof(T)) : 0u);
+    }
+}
+__device__ __forceinline__ void clear_front(Raw8<__nv_bfloat16>& r, int32_t off) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (j < off) r.w[j / 2] &= j % 2 ? 0x0000FFFFu : 0xFFFF0000u;
+}
+__device__ __forceinline__ void clear_front(Raw8<float>& r, int32_t off) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (j < off) r.w[j] = 0u;
+}
+template <typename T>
+__device__ __forceinline__ void load_pairs_from(F2 (&x)[4], const T* row, int v, int32_t t, int32_t tpr, int32_t off,
+                                                int32_t end) {
+    float y[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int32_t c = row_col(v, t, tpr) + j;
+        y[j] = c >= off && c < end ? to_f32(row[c - off]) : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = f2(y[2 * i], y[2 * i + 1]);
+}
+// `at` is the aligned address; element by element where `each`, at row - off, which need not be aligned then.
+template <typename T>
+__device__ __forceinline__ void store_pairs_from(T* at, const F2 (&x)[4], int v, int32_t t, int32_t tpr, int32_t off,
+                                                 int32_t end, bool each = false) {
+    const int32_t c = row_col(v, t, tpr);
+    if (!each && c >= off && c + 8 <= end) {
+        store_pairs<T, kVec>(at, x, v, t, tpr, end);
+        return;
+    }
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) split2(x[i], y[2 * i], y[2 * i + 1]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (c + j >= off && c + j < end) from_f32(y[j], at + c + j);
 }
 
 }  // namespace gbr

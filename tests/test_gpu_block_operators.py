@@ -52,6 +52,21 @@ def odd(t):
     return big[:, 3:3 + t.shape[1]]
 
 
+def placed(t, start, ld, fill=5.0):
+    """A copy of `t` that begins `start` elements after a 16-byte boundary, rows `ld` apart; and all that lies around it."""
+    whole = torch.full((start + len(t) * ld + 8,), fill, dtype=t.dtype, device=t.device)
+    view = whole.as_strided(t.shape, (ld, 1), start)
+    view.copy_(t)
+    return view, whole
+
+
+def others(view, whole):
+    """What lies around a placed matrix."""
+    rest = whole.clone()
+    rest.as_strided(view.shape, view.stride(), view.storage_offset()).fill_(5.0)
+    return rest
+
+
 def within(got, want, slack, name=""):
     assert got.shape == want.shape, name
     bar = torch.finfo(got.dtype).eps / 2 * want.abs() + slack
@@ -256,6 +271,109 @@ def test_residual_norm_weights_and_outputs_anywhere(gbr, rows):
     check_norm_grads(d, wide)
 
 
+# Rows on numbers of warps that are no powers of two, several groups and one.
+WARPS = [
+    (2600, 1536, "bf16", True, 1, True, True, 0.25),
+    (2601, 1440, "fp32", True, 3, True, True, 1.0),
+    (1300, 2560, "bf16", True, 1, True, True, 0.25),
+    (1300, 2568, "fp32", True, 13, True, True, 1.0),
+    (1290, 5120, "bf16", True, 0, True, True, 1.0),
+    (1290, 4104, "bf16", True, 5, True, True, 1.0),
+    (1290, 5128, "bf16", True, 1290, True, True, 1.0),
+    (1230, 5120, "fp32", True, 1, True, False, 1.0),
+    (1230, 7000, "bf16", False, 1, True, True, 1.0),
+    (37, 2560, "bf16", True, 1, True, True, 1.0),
+    (37, 5000, "fp32", True, 37, True, True, 1.0),
+]
+
+
+@pytest.mark.parametrize("case", WARPS, ids=["-".join(map(str, c)) for c in WARPS])
+def test_residual_norm_on_any_number_of_warps(gbr, case):
+    a = norm_inputs(case)
+    check_norm(a, *gbr.residual_norm(**a))
+    d = norm_grad_inputs(case)
+    check_norm_grads(d, gbr.residual_norm_backward(**d))
+    check_norm_grads(d, gbr.residual_norm_backward(**d, needs=(True, False, False, True, False)), ("dX", "dgate"))
+
+
+# Enough rows for CTAs that stay, starting anywhere: rows, cols, type, ..., distance of the rows.
+ANYWHERE = [
+    (1300, 4095, "bf16", True, 1, True, True, 0.25, 4095),
+    (1301, 4089, "bf16", True, 1301, True, True, 1.0, 4091),
+    (1250, 8185, "bf16", True, 0, True, True, 1.0, 8185),
+    (1220, 4097, "fp32", True, 1, True, True, 0.5, 4098),
+    (2500, 2047, "bf16", False, 2500, True, False, 1.0, 2047),
+    (2500, 2045, "fp32", True, 1, False, True, 1.0, 2045),
+    (5003, 1001, "fp32", True, 1, True, True, 0.25, 1001),
+    (5003, 1000, "bf16", True, 0, True, True, 1.0, 1004),
+    (10001, 500, "bf16", True, 1, True, True, 1.0, 504),
+    (80001, 33, "bf16", True, 1, True, True, 1.0, 33),
+    (160003, 7, "fp32", True, 0, True, True, 1.0, 7),
+    (160003, 1, "bf16", True, 1, True, True, 1.0, 1),
+]
+
+
+@pytest.mark.parametrize("case", ANYWHERE, ids=["-".join(map(str, c)) for c in ANYWHERE])
+def test_residual_norm_many_rows_start_anywhere(gbr, case):
+    case, ld = case[:-1], case[-1]
+    a = norm_inputs(case)
+    rows = case[0]
+
+    def apart(t):
+        return placed(t, 0, ld)[0]
+    b = dict(a, X=apart(a["X"]), R=None if a["R"] is None else apart(a["R"]),
+             gate=apart(a["gate"]) if case[4] > 1 else a["gate"])
+    S, around_s = placed(torch.zeros_like(a["X"]), 0, ld)
+    H, around_h = placed(torch.zeros_like(a["X"]), 0, ld) if case[5] else (None, None)
+    want = gbr.residual_norm(**b, S=S, H=H)
+    check_norm(a, *want)
+    assert bool((others(S, around_s) == 5).all()) and (H is None or bool((others(H, around_h) == 5).all()))
+    # Over their inputs, the same.
+    if H is not None and a["R"] is not None:
+        c = dict(b, X=apart(a["X"]), R=apart(a["R"]))
+        out = gbr.residual_norm(**c, S=c["R"], H=c["X"])
+        assert out[0] is c["R"] and torch.equal(out[0], S) and torch.equal(out[1], H)
+    # A row that is not a number spoils itself alone.
+    if rows < 3000:
+        c = dict(b, X=apart(a["X"]))
+        c["X"][rows // 2] = float("nan")
+        keep = torch.arange(rows, device="cuda") != rows // 2
+        # (New outputs lie closer than these: another order of the sums may be taken, the same for both calls.)
+        for given, want in ((None, gbr.residual_norm(**b)[0]), (placed(S, 0, ld)[0], S)):
+            out = gbr.residual_norm(**c, S=given, H=None if H is None or given is None else placed(H, 0, ld)[0])[0]
+            assert torch.equal(out[keep], want[keep]) and bool(out[rows // 2].isnan().all())
+
+
+@pytest.mark.parametrize("case", ANYWHERE + [
+    (301, 1001, "bf16", True, 1, True, True, 0.25, 1001),
+    (300, 1001, "fp32", True, 300, True, True, 0.25, 1003),
+    (9, 2047, "fp32", True, 1, True, True, 0.25, 2047),
+    (13, 33, "bf16", True, 0, True, True, 0.25, 34),
+    (13, 8191, "bf16", False, 0, True, True, 0.25, 8192),
+    (7, 5, "fp32", True, 1, False, True, 1.0, 5),
+], ids=lambda c: "-".join(map(str, c)))
+def test_residual_norm_backward_rows_start_anywhere(gbr, case):
+    case, ld = case[:-1], case[-1]
+    a = norm_grad_inputs(case)
+    b = dict(a, **{n: None if a[n] is None else placed(a[n], 0, ld)[0] for n in ("dS", "dH", "X", "S")})
+    out = {}
+    if case[4] > 1:
+        b["gate"] = placed(a["gate"], 0, ld)[0]
+        out["dgate"] = placed(torch.zeros_like(a["gate"]), 0, ld)
+    for name in ("dX", "dR"):
+        out[name] = placed(torch.zeros_like(a["X"]), 0, ld)
+    grads = gbr.residual_norm_backward(**b, **{n: t[0] for n, t in out.items()})
+    check_norm_grads(a, grads)
+    for view, whole in out.values():
+        assert bool((others(view, whole) == 5).all())
+    for x, y in zip(grads, gbr.residual_norm_backward(**b, **{n: placed(torch.zeros_like(t[0]), 0, ld)[0]
+                                                              for n, t in out.items()})):
+        assert (x is None and y is None) or torch.equal(x, y)
+    # Only some of them.
+    some = gbr.residual_norm_backward(**b, dX=out["dX"][0], needs=(True, False, False, True, True))
+    check_norm_grads(a, some, ("dX", "dgate", "dpre"))
+
+
 def test_residual_norm_special_values(gbr):
     """A row of zeros stays zero; Inf and NaN spoil their own row alone."""
     g = rng(4)
@@ -363,21 +481,6 @@ def test_moe_rows(gbr, case):
         prod = rows * a["dY"].double()[:, None]
         within(dw, prod.sum(2), 2.0 ** -17 * prod.abs().sum(2), "dweights")
     gbr.check_device()
-
-
-def placed(t, start, ld, fill=5.0):
-    """A copy of `t` that begins `start` elements after a 16-byte boundary, rows `ld` apart; and all that lies around it."""
-    whole = torch.full((start + len(t) * ld + 8,), fill, dtype=t.dtype, device=t.device)
-    view = whole.as_strided(t.shape, (ld, 1), start)
-    view.copy_(t)
-    return view, whole
-
-
-def others(view, whole):
-    """What lies around a placed matrix."""
-    rest = whole.clone()
-    rest.as_strided(view.shape, view.stride(), view.storage_offset()).fill_(5.0)
-    return rest
 
 
 @pytest.mark.parametrize("dt", [BF, torch.float32], ids=["bf16", "fp32"])
