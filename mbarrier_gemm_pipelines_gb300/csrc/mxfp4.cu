@@ -77,6 +77,8 @@ int run_tile(const Mxfp4Args& a, const LinearPlan& plan, const LibCtx& c, cudaSt
     const size_t smem = mx::tile_smem_bytes(P.bt, P.stages);
     void* kernel = mxfp4_tile_kernel_ptr(a.act);
     if ((r = raise_kernel_smem(kernel, smem, c.device)) != GBR_OK) return r;
+    if (P.t_tiles > 1 && plan.bt % 64 != 0)             // scales of tiles that start elsewhere start at odd columns
+        return report_errorf(GBR_ERR_INVALID, "gemm_mxfp4: tiles of %d rows", plan.bt);
     const int64_t ctas = int64_t(P.t_tiles) * cdiv(a.N, 128) * plan.split;
     if (ctas >= (int64_t(1) << 31)) return report_errorf(GBR_ERR_INVALID, "gemm_mxfp4: too many output tiles");
     void* args[] = {&Q};
@@ -134,8 +136,8 @@ int run_pair(const Mxfp4Args& a, const LibCtx& c, cudaStream_t stream) {
 
 int launch_mxfp4(const Mxfp4Args& a, const LibCtx& c, cudaStream_t stream) {
     // In bytes of operands and in cycles of the tensor core a contraction of 4-bit values is one of a quarter as many
-    // bf16 values, so the same estimate serves: over 15 products of 1 to 2048 rows and 500 to 14336 columns it picks what
-    // is 2 % slower in the mean than the best of all tiles and splits, and 9 % at worst (128 x 4096 x 14336: 12.8 / 11.7 us).
+    // bf16 values, so the same estimate serves: over 21 products of 100 to 2048 rows and 640 to 14336 columns it picks what
+    // is 3 % slower in the mean than the best of all tiles and splits, and 15 % at worst (346 x 6688 x 6072: 18.1 / 15.7 us).
     const LinearPlan plan = plan_linear(a.M, a.N, a.blocks * 8, c.sm_count);
     return plan.pair && a.blocks > 0 ? run_pair(a, c, stream) : run_tile(a, plan, c, stream);
 }
