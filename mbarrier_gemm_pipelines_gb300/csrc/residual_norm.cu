@@ -286,6 +286,7 @@ struct GradArgs {
     int32_t items, segments, span;     // span: rows of a gate (all rows where the items are one run)
     float *post_part, *pre_part, *gate_part;
     bool want_post, want_pre, want_gate;
+    int32_t parts, each;               // rows cut over a cluster's CTAs, columns for each
 };
 
 // The rows of a CTA's items, `groups` at a time.
@@ -309,48 +310,56 @@ struct RowWalk {
     }
 };
 
+// How rows lie: on 16 bytes; starting anywhere, as ODD above; cut over the CTAs of a cluster.
+enum Lie : int { kWhole, kOdd, kCut };
+
 // One CTA: its items' rows, blockDim.x / tpr at a time.  Thread t of each group keeps the sums of
 // its columns; groups are joined in order through shared memory.  kAhead > 0 (rows on 16 bytes, or ODD as above): that many
 // turns' rows of all inputs are on their way into shared memory, each thread its own 16 bytes, so that nobody
 // waits for another's copy; 0: they are loaded in their turn, any alignment.
+// CUT: rows of more columns than a CTA holds with FULL, a.each for each of a cluster's a.parts CTAs; two exchanges of sums a
+// row, about 0.7 us each.
 // FULL: a training step's call, with both norms, dS and all of dX, dR, dpost and dpre, without a gate an element.  What
 // is there need not be asked then (4096 x 4096: 631 instructions a warp and row of 8 columns a thread if it is, 447 not),
 // and the registers are kept for the row: the weights lie in shared memory, each thread's where it alone reads them, and
 // dpost's sum in its place in scratch, added to after a gate's rows.
-template <typename T, int V, int kAhead, bool FULL, bool ODD>
+template <typename T, int V, int kAhead, bool FULL, int M>
 __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<T> a, int32_t tpr, uint32_t row_bytes,
                                                                  uint32_t step) {
-    static_assert(!ODD || kAhead > 0);
+    static_assert(M == kWhole || kAhead > 0);
+    constexpr bool ODD = M == kOdd, CUT = M == kCut;
     constexpr int A = kAhead > 0 ? kVec : kStrided;
-    __shared__ float buf[2][3][32];
+    __shared__ float buf[2][3][32], slots[2][4][4];
     // The ring; behind it, where groups > 1, [groups][8][tpr] floats.
     extern __shared__ __align__(16) uint8_t ring[];
     ptx::griddep_wait();
     const int32_t t = int32_t(threadIdx.x) % tpr, group = int32_t(threadIdx.x) / tpr;
     const int32_t groups = int32_t(blockDim.x) / tpr;
-    const int32_t i0 = int32_t(int64_t(a.items) * blockIdx.x / gridDim.x);
-    const int32_t i1 = int32_t(int64_t(a.items) * (blockIdx.x + 1) / gridDim.x);
+    const uint32_t parts = CUT ? uint32_t(a.parts) : 1u, rank = CUT ? ptx::cluster_ctarank() : 0u;
+    const uint32_t cta = blockIdx.x / parts, ctas = gridDim.x / parts;
+    const int32_t i0 = int32_t(int64_t(a.items) * cta / ctas), i1 = int32_t(int64_t(a.items) * (cta + 1) / ctas);
     // ODD: CTA b has rows 8 (b / 8 groups + group) + b % 8 and on, the same number of elements, `off`, behind an aligned
     // address; columns go from there to `all_cols`.
     constexpr int32_t kStep = ODD ? 8 : 1;
     const int64_t odd_row = int64_t(blockIdx.x / 8) * groups * 8 + blockIdx.x % 8;
     const int64_t turn = ODD ? int64_t(gridDim.x) * groups : groups;
-    const int32_t off = ODD ? int32_t(odd_row * a.ld_odd % int32_t(16 / sizeof(T))) : 0, all_cols = a.cols + off;
+    const int32_t off = ODD ? int32_t(odd_row * a.ld_odd % int32_t(16 / sizeof(T))) : 0, c0 = CUT ? int32_t(rank) * a.each : 0;
+    const int32_t all_cols = CUT ? min(a.each, a.cols - c0) : a.cols + off;
     auto load = [&](F2 (&x)[4], const auto* from, int v) {
         if constexpr (ODD) load_pairs_from(x, from, v, t, tpr, off, all_cols);
-        else load_pairs<std::remove_cv_t<std::remove_pointer_t<decltype(from)>>, A>(x, from, v, t, tpr, all_cols);
+        else load_pairs<std::remove_cv_t<std::remove_pointer_t<decltype(from)>>, A>(x, from + c0, v, t, tpr, all_cols);
     };
     auto store = [&](T* to, const F2 (&x)[4], int v, int32_t cols) {
         if constexpr (ODD) store_pairs_from(to - off, x, v, t, tpr, off, cols);
-        else store_pairs<T, A>(to, x, v, t, tpr, cols);
+        else store_pairs<T, A>(to + c0, x, v, t, tpr, cols);
     };
     auto store_sums = [&](auto* to, const F2 (&x)[4], int v) {
         if constexpr (ODD) store_pairs_from(to - off, x, v, t, tpr, off, all_cols, true);
-        else store_pairs<std::remove_pointer_t<decltype(to)>, A>(to, x, v, t, tpr, all_cols);
+        else store_pairs<std::remove_pointer_t<decltype(to)>, A>(to + c0, x, v, t, tpr, all_cols);
     };
     auto copy = [&](uint32_t to, const T* from, int v) {
         if constexpr (ODD) copy_row8_from(to, from - off, v, t, tpr, all_cols);
-        else copy_row8(to, from, v, t, tpr, all_cols);
+        else copy_row8(to, from + c0, v, t, tpr, all_cols);
     };
     auto take = [&](Raw8<T>& x, uint32_t from, int v) {
         take_row8(x, from, v, t, tpr);
@@ -426,6 +435,8 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) fetch(uint32_t(i));
     uint32_t slot = 0;
+    int which = 0;
+    if (CUT) ptx::cluster_sync_all();                   // the others' slots are there
     for (int32_t item = i0; item < i1; ++item) {
         const int32_t g = item / a.segments, seg = item % a.segments;
         const int64_t base = int64_t(g) * a.span;
@@ -496,6 +507,7 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<
                     }
             float sum[3] = {sum_pair(ss), sum_pair(us), sum_pair(xx)};
             if (pre || post) group_sum(sum, buf[0], tpr, group);
+            if (CUT) cluster_sum(sum, slots[which], parts, rank), which ^= 1;
             // A group without a row adds zeros.
             const float r = in ? root(sum[0], a.inv_cols, a.eps) : 0.f, rc = r * r * r * sum[1] * a.inv_cols;
             const float q = !post ? 1.f : in ? root(sum[2], a.inv_cols, a.eps) : 0.f;
@@ -561,6 +573,7 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<
                 if (post) {
                     float sums[1] = {sum_pair(dot)};
                     group_sum(sums, buf[1], tpr, group);
+                    if (CUT) cluster_sum(sums, slots[which], parts, rank), which ^= 1;
                     m2 = f2(-a.scale * (q * q * q * sums[0] * a.inv_cols));
                 }
                 const F2 k2 = f2(a.scale * q);
@@ -583,7 +596,7 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     F2 w[4];
-                    float* sum = a.post_part + int64_t(blockIdx.x) * a.cols;
+                    float* sum = a.post_part + int64_t(cta) * a.cols;
                     if (run_gate) load(w, gate, v);
                     if (FULL && item > i0) load(spost[v], sum, v);
 #pragma unroll
@@ -627,15 +640,16 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<
         if (group == 0)
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                store_sums(a.post_part + int64_t(blockIdx.x) * a.cols, spost[v], v);
+                store_sums(a.post_part + int64_t(cta) * a.cols, spost[v], v);
     }
     if (want_pre) {
         join(spre);
         if (group == 0)
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                store_sums(a.pre_part + int64_t(blockIdx.x) * a.cols, spre[v], v);
+                store_sums(a.pre_part + int64_t(cta) * a.cols, spre[v], v);
     }
+    if (CUT) ptx::cluster_sync_all();                   // no CTA leaves while another writes its slots
 }
 
 // Rows that no CTA holds with what goes with them: their means first (a CTA a row), then everything else column by
@@ -928,16 +942,20 @@ int run_forward(const ResidualNormArgs& s, const LibCtx& c, cudaStream_t stream)
     return GBR_OK;
 }
 
+// Columns for each of `parts` CTAs, and the clusters of them that fit at once, a CTA an SM (of fours, 144 of 152 SMs' worth).
+int32_t part_cols(int64_t cols, int parts) { return int32_t(cdiv(cdiv(cols, parts), 8) * 8); }
+int64_t clusters_for(int parts, int sms) { return parts == 4 ? sms * 18 / 19 / 4 : sms / parts; }
+
 template <typename T, int V>
 void* grad_kernel(int ahead, bool full, bool odd) {
-    if (odd) return full ? reinterpret_cast<void*>(&residual_norm_grad_kernel<T, V, 2, true, true>)
-                         : reinterpret_cast<void*>(&residual_norm_grad_kernel<T, 1, 2, false, true>);
+    if (odd) return full ? reinterpret_cast<void*>(&residual_norm_grad_kernel<T, V, 2, true, kOdd>)
+                         : reinterpret_cast<void*>(&residual_norm_grad_kernel<T, 1, 2, false, kOdd>);
     switch (ahead) {
-        case 3: return full ? reinterpret_cast<void*>(&residual_norm_grad_kernel<T, V, 3, true, false>)
-                            : reinterpret_cast<void*>(&residual_norm_grad_kernel<T, 1, 3, false, false>);
-        case 2: return full ? reinterpret_cast<void*>(&residual_norm_grad_kernel<T, V, 2, true, false>)
-                            : reinterpret_cast<void*>(&residual_norm_grad_kernel<T, 1, 2, false, false>);
-        default: return reinterpret_cast<void*>(&residual_norm_grad_kernel<T, 1, 0, false, false>);
+        case 3: return full ? reinterpret_cast<void*>(&residual_norm_grad_kernel<T, V, 3, true, kWhole>)
+                            : reinterpret_cast<void*>(&residual_norm_grad_kernel<T, 1, 3, false, kWhole>);
+        case 2: return full ? reinterpret_cast<void*>(&residual_norm_grad_kernel<T, V, 2, true, kWhole>)
+                            : reinterpret_cast<void*>(&residual_norm_grad_kernel<T, 1, 2, false, kWhole>);
+        default: return reinterpret_cast<void*>(&residual_norm_grad_kernel<T, 1, 0, false, kWhole>);
     }
 }
 
@@ -986,7 +1004,7 @@ int run_backward(const ResidualNormGradArgs& s, const LibCtx& c, cudaStream_t st
     const Mat none = {}, &g = gate_rows ? s.G : none, &dg = gate_rows ? s.dG : none;
     const bool odd = !vec && s.rows >= c.sm_count && (s.gates <= 1 || gate_rows) &&
                      start_alike<T>({&s.dS, &s.dH, &s.X, &s.S, &s.dX, &s.dR, &g, &dg}, &a.ld_odd);
-    const int32_t wide = odd && a.ld_odd != 0 ? s.cols + kPiece - 1 : s.cols;
+    int32_t wide = odd && a.ld_odd != 0 ? s.cols + kPiece - 1 : s.cols;
     const bool full = (vec || odd) && s.post && s.pre && s.dS.p && s.dX.p && s.dR.p && a.want_post && a.want_pre && !gate_rows;
     const int inputs = (s.pre ? 2 : 0) + (s.X.p ? 1 : 0) + (s.dS.p ? 1 : 0) + (gate_rows ? 1 : 0);
     // V vectors a thread.  Two where the rows go round (the fewer warps a row, the less of what is done once a warp) and
@@ -996,12 +1014,12 @@ int run_backward(const ResidualNormGradArgs& s, const LibCtx& c, cudaStream_t st
         int32_t tpr;
         size_t step, join;
     } plan = {};
-    auto lay_out = [&](int V) {
+    auto lay_out = [&](int V, int most_ctas = 16) {
         plan.V = V, plan.tpr = std::max(32, warps_for(wide, V));
         plan.groups = std::max(1, 256 / plan.tpr), plan.threads = plan.groups * plan.tpr;
         // An SM: 128 registers a thread.  Against warps in powers of two, at most two CTAs, us, bf16: 4096 x 5120 61 / 71,
         // 4096 x 2560 33 / 40.
-        plan.ctas = std::max(1, 512 / plan.threads);
+        plan.ctas = std::min(most_ctas, std::max(1, 512 / plan.threads));
         const size_t mine = size_t(plan.threads) * 8 * sizeof(float);
         plan.join = (plan.groups > 1 ? mine : 0) + (full ? 2 * mine * V : 0);
         plan.step = vec || odd ? size_t(plan.threads) * 8 * V * sizeof(T) * size_t(inputs) : 0;
@@ -1011,9 +1029,20 @@ int run_backward(const ResidualNormGradArgs& s, const LibCtx& c, cudaStream_t st
     const bool many = s.rows >= int64_t(c.sm_count) * 8 * std::max(1, 4096 / s.cols);
     if (wide <= 8192) lay_out(full && (many || wide > 4096) ? 2 : 1);
     if (plan.V == 2 && plan.ahead == 0 && wide <= 4096) lay_out(1);
-    const bool long_rows = wide > 8192 || plan.tpr > 512 || (plan.V == 2 && plan.ahead == 0);
+    bool long_rows = wide > 8192 || plan.tpr > 512 || (plan.V == 2 && plan.ahead == 0);
+    // FULL: such rows are cut over two or four CTAs, if their ring fits, and read once then: us, means taken first / cut, 4096 x
+    // 16384 bf16 349 / 235, 2048 x 8192 fp32 223 / 136, 400 x 11008 fp32 80 / 48, 5 x 8344 bf16 11.7 / 11.9.  (Forwards, where
+    // rows of 16384 columns fit on a CTA, it loses: 4096 x 16384 131 / 152.)
+    a.parts = 1;
+    for (int parts = 2; parts <= 4 && long_rows && vec && full; parts *= 2) {
+        a.each = part_cols(s.cols, parts);
+        if (a.each > 8192) continue;
+        wide = a.each;
+        lay_out(2, 1);
+        if (plan.ahead > 0 && plan.groups == 1) a.parts = parts, plan.ahead = 2, long_rows = false;
+    }
     const int64_t col_ctas = cdiv(s.cols, kLongThreads * 8);
-    const int64_t ctas = long_rows ? std::max<int64_t>(1, 4 * c.sm_count / col_ctas)
+    const int64_t ctas = a.parts > 1 ? clusters_for(a.parts, c.sm_count) : long_rows ? std::max<int64_t>(1, 4 * c.sm_count / col_ctas)
                                    : c.sm_count * plan.ctas;
     const bool stream_odd = odd && !long_rows && plan.ahead > 0;
     int64_t grid;
@@ -1063,11 +1092,12 @@ int run_backward(const ResidualNormGradArgs& s, const LibCtx& c, cudaStream_t st
     } else {
         uint32_t row_bytes = uint32_t(plan.tpr * 8 * plan.V * sizeof(T)), step = plan.ahead > 0 ? uint32_t(plan.step) : 0;
         // Without a ring: not FULL.
-        void* kernel = plan.V == 2 ? grad_kernel<T, 2>(plan.ahead, full, stream_odd) : grad_kernel<T, 1>(plan.ahead, full, stream_odd);
+        void* kernel = a.parts > 1 ? reinterpret_cast<void*>(&residual_norm_grad_kernel<T, 2, 2, true, kCut>)
+                       : plan.V == 2 ? grad_kernel<T, 2>(plan.ahead, full, stream_odd) : grad_kernel<T, 1>(plan.ahead, full, stream_odd);
         const size_t smem = plan.join + size_t(plan.ahead) * step;
         if ((r = raise_kernel_smem(kernel, smem, c.device)) != GBR_OK) return r;
         void* args[] = {&a, &plan.tpr, &row_bytes, &step};
-        e = launch_kernel(kernel, dim3(unsigned(grid)), plan.threads, smem, 1, args, stream);
+        e = launch_kernel(kernel, dim3(unsigned(grid * a.parts)), plan.threads, smem, a.parts, args, stream);
     }
     if (e != cudaSuccess) return report_cuda(e, "launching residual_norm_backward");
     count_launch();

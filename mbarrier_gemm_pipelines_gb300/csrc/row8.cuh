@@ -348,6 +348,27 @@ __device__ __forceinline__ void group_sum(float (&x)[N], float (*buf)[32], int32
     for (int i = 0; i < N; ++i) x[i] = __shfl_sync(0xffffffffu, c, 8 * i);
 }
 
+// A row cut over the `parts` (at most 4) CTAs of a cluster: x, each CTA's sums, become the cluster's, added in rank order.
+// Every thread of the cluster calls it; `slot` is this and the next call's in turn (a CTA writes the next call's when
+// others may still read this one's, but the one after only when all have come to the next).
+template <int N>
+__device__ __forceinline__ void cluster_sum(float (&x)[N], float (*slot)[4], uint32_t parts, uint32_t rank) {
+    static_assert(N <= 4);
+    if (threadIdx.x < parts) {
+        const uint32_t to = ptx::mapa_shared(ptx::smem_addr(&slot[rank][0]), threadIdx.x);
+#pragma unroll
+        for (int i = 0; i < N; ++i) ptx::st_shared_cluster_u32(to + 4u * uint32_t(i), __float_as_uint(x[i]));
+    }
+    ptx::cluster_sync_all();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        x[i] = slot[0][i];
+#pragma unroll
+        for (uint32_t r = 1; r < 4; ++r)
+            if (r < parts) x[i] += slot[r][i];
+    }
+}
+
 // Asynchronous copies of a thread's own 16-byte pieces, group by group.
 __device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>

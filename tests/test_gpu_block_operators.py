@@ -296,6 +296,36 @@ def test_residual_norm_on_any_number_of_warps(gbr, case):
     check_norm_grads(d, gbr.residual_norm_backward(**d, needs=(True, False, False, True, False)), ("dX", "dgate"))
 
 
+# Rows whose gradients two or four CTAs share.
+LONG = [
+    (650, 16384, "bf16", True, 1, True, True, 0.25),
+    (650, 8200, "fp32", True, 13, True, True, 1.0),
+    (640, 12288, "bf16", False, 640, True, True, 1.0),
+    (640, 9008, "bf16", True, 0, False, True, 1.0),
+    (309, 32768, "bf16", True, 1, True, False, 1.0),
+    (310, 17000, "fp32", True, 5, True, True, 0.5),
+    (100, 16384, "bf16", True, 10, True, True, 1.0),
+    (80, 8192, "fp32", True, 1, True, True, 1.0),
+    (78, 6000, "fp32", True, 3, True, True, 1.0),
+    (41, 20008, "bf16", True, 41, True, True, 1.0),
+    (1, 8208, "bf16", True, 0, True, True, 1.0),
+]
+
+
+@pytest.mark.parametrize("case", LONG, ids=["-".join(map(str, c)) for c in LONG])
+def test_residual_norm_of_rows_cut_over_ctas(gbr, case):
+    a = norm_inputs(case)
+    out = gbr.residual_norm(**a)
+    check_norm(a, *out)
+    d = norm_grad_inputs(case)
+    grads = gbr.residual_norm_backward(**d)
+    check_norm_grads(d, grads)
+    for _ in range(3):
+        for x, y in zip(out + grads, gbr.residual_norm(**a) + gbr.residual_norm_backward(**d)):
+            assert (x is None and y is None) or torch.equal(x, y)
+    gbr.check_device()
+
+
 # Enough rows for CTAs that stay, starting anywhere: rows, cols, type, ..., distance of the rows.
 ANYWHERE = [
     (1300, 4095, "bf16", True, 1, True, True, 0.25, 4095),
