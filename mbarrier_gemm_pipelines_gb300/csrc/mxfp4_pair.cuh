@@ -23,7 +23,7 @@
 // wait for those alone (and for the tile before, which is done by then): 0.4 us
 // from one tile's last MMA to the next one's first, of 6.2 at K = 4096.  (1.1 us
 // with arrivals that release memory at cluster scope: they wait for the epilogue's
-// stores.  4096 x 4096 x 14336 92 -> 84 us, GELU 99 -> 90.)  Tiles of 192 columns have
+// stores.  4096 x 4096 x 14336 92 -> 84 us, GELU 99 -> 90; with the host's order of the tiles 79.5 and 88.)  Tiles of 192 columns have
 // room for two accumulators, but take in more bytes for the same products: 8192^3
 // 176 us with 256 columns, 196 with 192, before that.
 #pragma once

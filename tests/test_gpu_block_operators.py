@@ -545,6 +545,20 @@ def test_moe_rows_and_quantize_start_anywhere(gbr, D, dt):
             assert torch.equal(got.data, want.data) and torch.equal(got.scales, want.scales)
 
 
+@pytest.mark.parametrize("dt", [BF, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("D", [9, 333, 2047])
+def test_moe_rows_that_start_anywhere_in_place(gbr, D, dt):
+    T, k, E = 300, 3, 5
+    ids = choices(T, k, E)
+    positions, offsets = gbr.moe_sort(ids, E)
+    g = rng(D)
+    Ys, R, w = normal(g, (T * k, D), dtype=dt), normal(g, (T, D), dtype=dt), normal(g, (T, k), 1.0, F32)
+    want = gbr.moe_combine(Ys, positions, w, R)
+    for _ in range(5):
+        Y = R.clone()
+        assert gbr.moe_combine(Ys, positions, w, Y, Y=Y) is Y and torch.equal(Y, want)
+
+
 def test_moe_rows_needs_and_in_place(gbr):
     a = row_inputs((50, 3, 520, 8, "bf16", 0.2))
     dYs, dw = gbr.moe_combine_backward(a["dY"], a["Ys"], a["p"], a["o"], a["w"])
