@@ -1039,7 +1039,11 @@ int run_backward(const ResidualNormGradArgs& s, const LibCtx& c, cudaStream_t st
         if (plan.ahead > 0 && plan.groups == 1) a.parts = parts, plan.ahead = 2, long_rows = false;
     }
     const int64_t col_ctas = cdiv(s.cols, kLongThreads * 8);
-    const int64_t ctas = a.parts > 1 ? clusters_for(a.parts, c.sm_count) : long_rows ? std::max<int64_t>(1, 4 * c.sm_count / col_ctas)
+    // One CTA (or cluster) takes two turns of rows by itself, one without a ring, and writes its sums as they are wanted: us,
+    // bf16, two kernels / one, 1 x 2048 6.2 / 4.4, 2 x 2048 6.2 / 5.2, 3 x 2048 6.2 / 6.2; element by element 3 x 2047 8.6 / 13.
+    const int64_t turns = s.gates > 1 && !gate_rows ? s.gates * cdiv(s.per_gate, plan.groups) : cdiv(s.rows, plan.groups);
+    const bool few = !long_rows && turns <= (plan.ahead > 0 ? 2 : 1);
+    const int64_t ctas = few ? 1 : a.parts > 1 ? clusters_for(a.parts, c.sm_count) : long_rows ? std::max<int64_t>(1, 4 * c.sm_count / col_ctas)
                                    : c.sm_count * plan.ctas;
     const bool stream_odd = odd && !long_rows && plan.ahead > 0;
     int64_t grid;
@@ -1061,7 +1065,8 @@ int run_backward(const ResidualNormGradArgs& s, const LibCtx& c, cudaStream_t st
         runs += int32_t(n);
         return sums.n++;
     };
-    const int i_post = part(a.want_post, 1, grid, s.dpost, 0, false), i_pre = part(a.want_pre, 1, grid, s.dpre, 0, false);
+    const bool direct = grid == 1 && !long_rows;
+    const int i_post = part(a.want_post && !direct, 1, grid, s.dpost, 0, false), i_pre = part(a.want_pre && !direct, 1, grid, s.dpre, 0, false);
     const int i_gate = part(a.want_gate && a.per_gate != 1 && a.segments > 1, s.gates, a.segments, s.dG.w(), s.dG.ld, s.bf16);
     const size_t stats_at = floats;
     if (long_rows) floats += size_t(s.rows) * 4;
@@ -1072,7 +1077,7 @@ int run_backward(const ResidualNormGradArgs& s, const LibCtx& c, cudaStream_t st
     float* base = static_cast<float*>(q);
     for (int i = 0; i < sums.n; ++i) sums.of[i].in = base + reinterpret_cast<size_t>(sums.of[i].in);
     auto of = [&](int i) { return i < 0 ? nullptr : const_cast<float*>(sums.of[i].in); };
-    a.post_part = of(i_post), a.pre_part = of(i_pre), a.gate_part = of(i_gate);
+    a.post_part = direct ? s.dpost : of(i_post), a.pre_part = direct ? s.dpre : of(i_pre), a.gate_part = of(i_gate);
     cudaError_t e;
     if (long_rows) {
         float4* stats = reinterpret_cast<float4*>(base + stats_at);

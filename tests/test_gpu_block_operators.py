@@ -326,6 +326,22 @@ def test_residual_norm_of_rows_cut_over_ctas(gbr, case):
     gbr.check_device()
 
 
+@pytest.mark.parametrize("rows,cols,dt", [(1, 2048, "bf16"), (2, 2048, "fp32"), (3, 2048, "bf16"), (1, 2047, "bf16"),
+                                          (2, 33, "fp32"), (8, 256, "bf16"), (17, 256, "bf16"), (2, 8192, "bf16"),
+                                          (2, 16384, "bf16"), (3, 16384, "bf16")])
+@pytest.mark.parametrize("gates", ["none", "one", "row"])
+def test_residual_norm_backward_of_few_rows(gbr, rows, cols, dt, gates):
+    """One CTA's sums, and those of several."""
+    a = norm_grad_inputs((rows, cols, dt, True, {"none": 0, "one": 1, "row": rows}[gates], True, True, 0.5))
+    check_norm_grads(a, gbr.residual_norm_backward(**a))
+    if gates == "one":
+        check_norm_grads(a, gbr.residual_norm_backward(**a, needs=(True, False, True, False, False)), ("dX", "dpost"))
+        check_norm_grads(a, gbr.residual_norm_backward(**a, needs=(False, False, False, True, True)), ("dgate", "dpre"))
+    if rows % 2 == 0:
+        a = norm_grad_inputs((rows, cols, dt, True, 2, True, True, 0.5))
+        check_norm_grads(a, gbr.residual_norm_backward(**a))
+
+
 # Enough rows for CTAs that stay, starting anywhere: rows, cols, type, ..., distance of the rows.
 ANYWHERE = [
     (1300, 4095, "bf16", True, 1, True, True, 0.25, 4095),
