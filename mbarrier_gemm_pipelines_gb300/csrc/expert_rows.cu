@@ -215,6 +215,7 @@ __global__ void __launch_bounds__(256, kResident<T>) moe_dispatch_kernel(const R
                     for (int v = 0; v < kV; ++v) x[v] = next[v];
                     if (piece + 1 < pieces) load(next, i, v0 + kV);
                     else load(next, i + per, 0);
+                    if (row_col(v0, t & ~31, tpr) >= a.D) continue;     // the warp has no columns
                     for (int32_t j = 0; j < k; ++j) {
                         const int32_t to = pos[j];
                         if (to < 0 || (!HELD && to >= a.rows)) continue;
@@ -245,7 +246,7 @@ __global__ void __launch_bounds__(256, kResident<T>) moe_combine_rows_kernel(con
         if (HELD) fetch_places(a, first * a.k, tokens * a.k, at, weight);
         for (int32_t i = group; i < tokens; i += per) {
             const int64_t row = first + i;
-            for (int32_t v0 = 0; v0 * tpr * 8 < a.D; v0 += kV) {
+            for (int32_t v0 = 0; row_col(v0, t & ~31, tpr) < a.D; v0 += kV) {        // while the warp has columns
                 float y[kV][8] = {};
                 Raw8<T> r[kV];
                 if (a.R != nullptr)
@@ -320,7 +321,7 @@ __global__ void __launch_bounds__(256, kResident<T>) moe_combine_grad_kernel(con
                         if (p[j] >= 0) w[j] = HELD ? weight[i * a.k + j0 + j] : a.weights[c];
                     }
                 }
-                for (int32_t v0 = 0; v0 * tpr * 8 < cols; v0 += kV) {
+                for (int32_t v0 = 0; row_col(v0, t & ~31, tpr) < cols; v0 += kV) {   // while the warp has columns
                     Raw8<T> d[kV], y[kJ][kV];
 #pragma unroll
                     for (int v = 0; v < kV; ++v) load_raw8<A>(d[v], a.X + row * a.ldx, v0 + v, t, tpr, cols);
