@@ -531,7 +531,7 @@ int moe_layer(const void *X, const float *Wr, const void *W1, const float *b1, c
  *   S = R + scale * gate * y
  *   H = norm(S) * pre    (with pre)
  * where norm divides a row by sqrt(mean of its squares + eps).
- *   X, R, S, H [rows, cols], ld... elements from row to row, >= cols, any
+ *   X, R, S, H [rows, cols], cols below 2^30, ld... elements from row to row, >= cols, any
  *   alignment that the elements have; R may be NULL (zero).  post, pre [cols] fp32.  gate
  *   [gates, cols] or NULL (one): rows must be a multiple of gates, and row i uses
  *   gate row i / (rows / gates), so gates = 1 is a gate per channel and
@@ -584,7 +584,7 @@ int residual_norm_backward(const void *dS, int64_t ldds, const void *dH, int64_t
  *   dYs or dweights may be NULL (not wanted; Ys may be NULL without dweights).
  *   The residual's gradient is dY itself.
  * Positions and offsets are those of moe_sort (a position twice would leave either
- * row).  dtype as in residual_norm; D any, row strides >= D, any alignment that the
+ * row).  dtype as in residual_norm; D below 2^30, row strides >= D, any alignment that the
  * elements have.  Outputs overlap nothing else.
  */
 int moe_sort(const int64_t *expert_ids, int64_t choices, int num_experts, int32_t *positions,
@@ -612,7 +612,7 @@ int moe_combine_backward(const void *dY, int64_t lddy, const void *Ys, int64_t l
  *           rows one after the other; in a tile, row r and block b are byte
  *           (r % 32) * 16 + (r % 128) / 32 * 4 + b % 4.  Bytes of rows and blocks that are not
  *           there are 0 (gemm_mxfp4 wants no NaN in them).
- * Both 16-byte aligned (GBR_ERR_ALIGN).
+ * Both 16-byte aligned (GBR_ERR_ALIGN).  The calls below take sizes below 2^30.
  *
  * quantize_mxfp4 -- the scale of a block is 2^(floor(log2 of its largest size) - 2),
  *   at least 2^-127; values are divided by it and rounded to the nearest (ties to the

@@ -3,6 +3,7 @@
 #include "gbr.h"
 #include "operators.h"
 
+#include <algorithm>
 #include <cmath>
 #include <exception>
 #include <initializer_list>
@@ -75,6 +76,12 @@ int check_sizes(const char* fn, int64_t M, int64_t N, int64_t K) {
     return GBR_OK;
 }
 
+// Kernels count past a row's end in 32 bits.
+int check_columns(const char* fn, int64_t cols) {
+    if (cols >= kLim / 2) return report_errorf(GBR_ERR_INVALID, "%s: columns must be below 2^30", fn);
+    return GBR_OK;
+}
+
 int check_type(const char* fn, int dtype, bool* bf16) {
     if (dtype != GBR_BF16 && dtype != GBR_F32_FFMA && dtype != GBR_F32_TF32)
         return report_errorf(GBR_ERR_UNSUPPORTED, "%s: bf16 or fp32 elements only", fn);
@@ -86,7 +93,7 @@ int check_type(const char* fn, int dtype, bool* bf16) {
 int check_norm(const char* fn, int64_t rows, int64_t cols, int64_t gates, const void* gate, double scale, double eps,
                int dtype, ResidualNormArgs* a) {
     int r = check_type(fn, dtype, &a->bf16);
-    if (r != GBR_OK || (r = check_sizes(fn, rows, cols, 0)) != GBR_OK) return r;
+    if (r != GBR_OK || (r = check_sizes(fn, rows, cols, 0)) != GBR_OK || (r = check_columns(fn, cols)) != GBR_OK) return r;
     if (!(eps >= 0.0) || std::isinf(eps) || !std::isfinite(scale))
         return report_errorf(GBR_ERR_INVALID, "%s: eps must be finite and not negative, scale finite", fn);
     if (gate == nullptr) gates = 0;
@@ -100,7 +107,7 @@ int check_norm(const char* fn, int64_t rows, int64_t cols, int64_t gates, const 
 
 int check_rows(const char* fn, int64_t T, int64_t top_k, int64_t D, int num_experts, int dtype, bool* bf16) {
     int r = check_type(fn, dtype, bf16);
-    if (r != GBR_OK || (r = check_sizes(fn, T, top_k, D)) != GBR_OK) return r;
+    if (r != GBR_OK || (r = check_sizes(fn, T, top_k, D)) != GBR_OK || (r = check_columns(fn, D)) != GBR_OK) return r;
     if (T * top_k >= kLim) return report_errorf(GBR_ERR_INVALID, "%s: T * top_k must be below 2^31", fn);
     if (num_experts < 1 || num_experts > kSortMaxExperts)
         return report_errorf(GBR_ERR_INVALID, "%s: num_experts must be 1..%d", fn, kSortMaxExperts);
@@ -121,8 +128,9 @@ int check_outputs(const char* fn, std::initializer_list<const View*> in, std::in
 }
 
 int check_mx(const char* fn, int64_t rows, int64_t cols, int dtype, bool* bf16) {
-    const int r = check_type(fn, dtype, bf16);
-    return r != GBR_OK ? r : check_sizes(fn, rows, cols, 0);
+    int r = check_type(fn, dtype, bf16);
+    if (r != GBR_OK || (r = check_sizes(fn, rows, cols, 0)) != GBR_OK) return r;
+    return check_columns(fn, std::max(rows, cols));     // either may lie along X's rows
 }
 
 int check_mx_pointers(const char* fn, const void* data, const void* scales) {
@@ -610,6 +618,7 @@ int gemm_mxfp4(const void* A, const void* A_scales, const void* B, const void* B
     return guarded(fn, [&]() -> int {
         if (act < 0 || act >= kActs) return report_errorf(GBR_ERR_INVALID, "%s: unknown activation %d", fn, act);
         int r = check_sizes(fn, M, N, K);
+        if (r == GBR_OK) r = check_columns(fn, std::max({M, N, K}));
         if (r != GBR_OK || M == 0 || N == 0) return r;
         if (!C || (K > 0 && (!A || !A_scales || !B || !B_scales)))
             return report_errorf(GBR_ERR_INVALID, "%s: NULL buffer", fn);

@@ -123,6 +123,16 @@ def test_refused(lib, call, kw, code):
     assert lib.gbr_last_error() != b""
 
 
+@pytest.mark.parametrize("call,kw", [
+    (norm, dict(cols=1 << 30)), (norm_backward, dict(cols=(1 << 31) - 1)), (dispatch, dict(D=1 << 30)), (combine, dict(D=1 << 30)),
+    (combine_backward, dict(D=(1 << 31) - 1)), (quantize, dict(cols=1 << 30)), (quantize, dict(rows=1 << 30, transposed=1)),
+    (dequantize, dict(cols=(1 << 31) - 1)), (gemm, dict(M=1 << 30)), (gemm, dict(N=(1 << 31) - 1)), (gemm, dict(K=1 << 30)),
+])
+def test_rows_longer_than_kernels_count_are_refused(lib, call, kw):
+    assert call(lib, **kw) == INVALID
+    assert b"2^30" in lib.gbr_last_error()
+
+
 def test_empty_calls_launch_nothing(lib):
     before = lib.gbr_launch_count()
     assert norm(lib, rows=0, gates=0) == 0 and norm(lib, cols=0) == 0 and norm(lib, S=None, H=None) == 0
