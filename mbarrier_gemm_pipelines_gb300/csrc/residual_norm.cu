@@ -5,9 +5,12 @@
 //   S = R + scale gate y
 //   H = S r pre,   r = 1 / sqrt(mean S^2 + eps)
 //
-//   u = dH pre;  ds = dS + r u - S r^3 mean(u S)      dR = ds, dpre = sum dH S r
+//   u = dH pre;  ds = dS + r (u - S r^2 mean(u S))    dR = ds, dpre = sum dH S r
 //   dy = scale gate ds                                dgate = sum scale y ds
-//   v = dy post; dX = q v - X q^3 mean(v X)           dpost = sum dy X q
+//   v = dy post; dX = q (v - X q^2 mean(v X))         dpost = sum dy X q
+//
+// No square or cube of a root is formed alone: of a row's mean m, r m comes first, which is about as large as u, then
+// r (r m).  r^3 is subnormal for rows of 10^13 and more and infinite for rows below 10^-13.
 //
 // Bound by memory: every operand is read once and every output written once; a
 // group of threads holds its row in registers between the passes that the two
@@ -509,7 +512,7 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<
             if (pre || post) group_sum(sum, buf[0], tpr, group);
             if (CUT) cluster_sum(sum, slots[which], parts, rank), which ^= 1;
             // A group without a row adds zeros.
-            const float r = in ? root(sum[0], a.inv_cols, a.eps) : 0.f, rc = r * r * r * sum[1] * a.inv_cols;
+            const float r = in ? root(sum[0], a.inv_cols, a.eps) : 0.f, rm = r * (r * sum[1] * a.inv_cols);
             const float q = !post ? 1.f : in ? root(sum[2], a.inv_cols, a.eps) : 0.f;
             F2 d[V][4], dot = f2(0.f);
 #pragma unroll
@@ -517,14 +520,14 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<
 #pragma unroll
                 for (int i = 0; i < 4; ++i) d[v][i] = raw_pair(ds[v], i);
             if (pre) {
-                const F2 r2 = f2(r), m2 = f2(-rc);
+                const F2 r2 = f2(r), m2 = f2(-rm);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     if (FULL) get_pairs(wpre[v], own + uint32_t(v) * 32u * blockDim.x);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const F2 S = raw_pair(s[v], i), H = raw_pair(dh[v], i);
-                        d[v][i] = fma2(S, m2, fma2(r2, mul2(H, wpre[v][i]), d[v][i]));
+                        d[v][i] = fma2(r2, fma2(S, m2, mul2(H, wpre[v][i])), d[v][i]);
                         spre[v][i] = fma2(H, mul2(S, r2), spre[v][i]);
                     }
                 }
@@ -574,15 +577,15 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<
                     float sums[1] = {sum_pair(dot)};
                     group_sum(sums, buf[1], tpr, group);
                     if (CUT) cluster_sum(sums, slots[which], parts, rank), which ^= 1;
-                    m2 = f2(-a.scale * (q * q * q * sums[0] * a.inv_cols));
+                    m2 = f2(-q * (q * sums[0] * a.inv_cols));
                 }
                 const F2 k2 = f2(a.scale * q);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        d[v][i] = mul2(d[v][i], k2);
                         if (post) d[v][i] = fma2(raw_pair(x[v], i), m2, d[v][i]);
+                        d[v][i] = mul2(d[v][i], k2);
                     }
                     store(a.dX + row * a.lddx, d[v], v, cols);
                 }
@@ -656,7 +659,7 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<
 // column, 8 of them a thread.
 constexpr int kLongThreads = 256;
 
-// stats[row] = {r, r^3 mean(u S), q, q^3 mean(v X)}
+// stats[row] = {r, r^2 mean(u S), q, q^2 mean(v X)}
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(1024, 1) residual_norm_stats_kernel(const GradArgs<T> a, float4* stats) {
     __shared__ float buf[2][3][32];
@@ -685,7 +688,7 @@ __global__ void __launch_bounds__(1024, 1) residual_norm_stats_kernel(const Grad
         }
         float sum[3] = {sum_pair(ss), sum_pair(us), sum_pair(xx)};
         group_sum(sum, buf[0], 1024, 0);
-        const float r = root(sum[0], a.inv_cols, a.eps), rc = r * r * r * sum[1] * a.inv_cols;
+        const float r = root(sum[0], a.inv_cols, a.eps), rm = r * (r * sum[1] * a.inv_cols);
         const float q = post ? root(sum[2], a.inv_cols, a.eps) : 1.f;
         if (post)
             for (int32_t p = 0; p < pieces; ++p) {
@@ -703,14 +706,14 @@ __global__ void __launch_bounds__(1024, 1) residual_norm_stats_kernel(const Grad
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     F2 e = raw_pair(ds, i);
-                    if (pre) e = fma2(raw_pair(s, i), f2(-rc), fma2(f2(r), mul2(raw_pair(dh, i), w[i]), e));
+                    if (pre) e = fma2(f2(r), fma2(raw_pair(s, i), f2(-rm), mul2(raw_pair(dh, i), w[i])), e);
                     if (a.G != nullptr) e = mul2(e, raw_pair(g, i));
                     vx = fma2(mul2(e, wp[i]), raw_pair(x, i), vx);
                 }
             }
         float dot[1] = {sum_pair(vx)};
         group_sum(dot, buf[1], 1024, 0);
-        if (threadIdx.x == 0) stats[row] = make_float4(r, rc, q, a.scale * (q * q * q * dot[0] * a.inv_cols));
+        if (threadIdx.x == 0) stats[row] = make_float4(r, rm, q, a.scale * (q * (q * dot[0] * a.inv_cols)));
     }
 }
 
@@ -757,7 +760,7 @@ __global__ void __launch_bounds__(kLongThreads, 2) residual_norm_grad_long_kerne
                 e[i] = raw_pair(ds, i);
                 if (pre) {
                     const F2 S = raw_pair(s, i), H = raw_pair(dh, i);
-                    e[i] = fma2(S, f2(-st.y), fma2(f2(st.x), mul2(H, wpre[i]), e[i]));
+                    e[i] = fma2(f2(st.x), fma2(S, f2(-st.y), mul2(H, wpre[i])), e[i]);
                     spre[i] = fma2(H, mul2(S, f2(st.x)), spre[i]);
                 }
             }
@@ -770,8 +773,9 @@ __global__ void __launch_bounds__(kLongThreads, 2) residual_norm_grad_long_kerne
                 srun[i] = add2(srun[i], dg[i]);
                 e[i] = mul2(e[i], gate[i]);
                 spost[i] = fma2(e[i], n, spost[i]);
-                e[i] = mul2(mul2(e[i], wpost[i]), f2(st.z));
+                e[i] = mul2(e[i], wpost[i]);
                 if (post) e[i] = fma2(X, f2(-st.w), e[i]);
+                e[i] = mul2(e[i], f2(st.z));
             }
             if (a.want_gate && gate_rows) store_pairs<T, VEC>(a.dG + row * a.lddg + c0, dg, 0, t, tpr, cols);
             if (a.dX != nullptr) store_pairs<T, VEC>(a.dX + row * a.lddx + c0, e, 0, t, tpr, cols);
