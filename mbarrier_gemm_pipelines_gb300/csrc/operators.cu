@@ -541,8 +541,10 @@ int moe_combine_backward(const void* dY, int64_t lddy, const void* Ys, int64_t l
     return guarded(fn, [&]() -> int {
         MoeCombineGradArgs a = {};
         int r = check_rows(fn, T, top_k, D, num_experts, dtype, &a.bf16);
-        if (r != GBR_OK || T == 0 || top_k == 0 || (!dYs && !dweights)) return r;
-        if (!positions || !weights || (D > 0 && (!dY || (dYs && !offsets) || (dweights && !Ys))))
+        if (r != GBR_OK) return r;
+        if (D == 0) dYs = nullptr;                      // no element to write
+        if (T == 0 || top_k == 0 || (!dYs && !dweights)) return r;
+        if (!positions || !weights || (dYs && !offsets) || (D > 0 && (!dY || (dweights && !Ys))))
             return report_errorf(GBR_ERR_INVALID, "%s: NULL buffer", fn);
         const int64_t es = a.bf16 ? 2 : 4, n = T * top_k;
         const View vd = {"dY", dY, T, D, lddy, es}, vi = {"Ys", dweights ? Ys : nullptr, n, D, ldys, es},
