@@ -428,6 +428,7 @@ int residual_norm_backward(const void* dS, int64_t ldds, const void* dH, int64_t
             return report_errorf(GBR_ERR_INVALID, "%s: a gradient of a weight or gate that is not there", fn);
         if (cols == 0 || (!dX && !dR && !dpost && !dgate && !dpre)) return GBR_OK;
         const bool some = rows > 0;
+        if (f.gates == 0) gate = nullptr;               // none of its rows is there
         const bool need_x = post || gate;
         if (some && ((need_x && !X) || (pre && (!dH || !S)) || (!dS && !pre)))
             return report_errorf(GBR_ERR_INVALID, "%s: NULL buffer", fn);

@@ -593,7 +593,8 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<
             if (tpr > 32 && (!want_x || !post)) __syncthreads();   // buf[0], for the next rows
         }
         if (want_run) {
-            // dpost gains scale gate sum, dgate is scale weight sum.
+            // dpost gains scale gate sum, dgate is scale weight sum.  Of no rows both are zero, whatever gate and weight hold.
+            const bool some = r0 < r1;
             if (FULL) join(srun);
             if (want_post && (!FULL || group == 0))
 #pragma unroll
@@ -605,7 +606,7 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const F2 k = run_gate ? mul2(f2(a.scale), w[i]) : f2(a.scale);
-                        spost[v][i] = fma2(srun[v][i], k, spost[v][i]);
+                        if (some) spost[v][i] = fma2(srun[v][i], k, spost[v][i]);
                     }
                     if (FULL) {
                         store_sums(sum, spost[v], v);
@@ -623,7 +624,7 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             srun[v][i] = mul2(srun[v][i], f2(a.scale));
-                            if (post) srun[v][i] = mul2(srun[v][i], w[i]);
+                            if (post && some) srun[v][i] = mul2(srun[v][i], w[i]);
                         }
                         if (a.segments > 1)
                             store_sums(a.gate_part + int64_t(item) * a.cols, srun[v], v);

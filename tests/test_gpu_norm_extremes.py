@@ -37,3 +37,26 @@ def test_gradients_of_large_and_small_rows(gbr, case, size):  # noqa: F811
              dS=(a["dS"].double() / size).to(a["dS"].dtype))
     block.check_norm_grads(a, gbr.residual_norm_backward(**a))
     gbr.check_device()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("cols", [64, 65, 9000])
+@pytest.mark.parametrize("post", [False, True])
+def test_sums_over_no_rows_are_zero(gbr, cols, post, dtype):  # noqa: F811
+    """Whatever gate and weights hold; and a gate without rows is not read (the buffer behind the pointer has some here)."""
+    x = torch.empty(0, cols, device="cuda", dtype=dtype)
+    w = torch.full((cols,), float("inf"), device="cuda")
+    gate = torch.full((5, cols), float("nan"), device="cuda", dtype=dtype)
+    dX, dR, dpost, dgate, dpre = gbr.residual_norm_backward(x, x, x, x, post=w if post else None, gate=gate, pre=w)
+    assert dX.shape == dR.shape == x.shape and dgate.shape == gate.shape
+    for t in (dgate, dpre) + ((dpost,) if post else ()):
+        assert (t == 0).all()
+    if post:
+        sums = torch.ones(2, cols, device="cuda")
+        code = gbr.BF16 if dtype == torch.bfloat16 else gbr.F32_FFMA
+        gbr.check(gbr.lib().residual_norm_backward(None, cols, None, cols, None, cols, None, cols, w.data_ptr(), gate.data_ptr(),
+                                                   cols, 0, 1.0, w.data_ptr(), 1e-6, None, cols, None, cols,
+                                                   sums[0].data_ptr(), None, cols, sums[1].data_ptr(), 0, cols, code,
+                                                   torch.cuda.current_stream().cuda_stream))
+        assert (sums == 0).all()
+    gbr.check_device()
