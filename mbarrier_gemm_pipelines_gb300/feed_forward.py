@@ -71,15 +71,18 @@ class ExpertFeedForward:
         self.W1, self.W2 = _weights((experts, D, F1), D ** -0.5, g), _weights((experts, F, D), F ** -0.5, g)
         self.b1 = torch.zeros(experts, F1, device="cuda")
         self.b2 = torch.zeros(experts, D, device="cuda")
+        self._saved = None
 
     def forward(self, x):
         if x.shape[0] <= 64:
+            self._saved = None              # nothing of an earlier pass for backward
             return ops.moe_layer(x, self.Wr, self.W1, self.b1, self.W2, self.b2, top_k=self.top_k, act=self.act,
                                  gated=self.gated)
         return self.forward_sorted(x)
 
     def forward_sorted(self, x, live=None):
-        """Any number of tokens; `live` [T] (bool) strikes out the others, whose output is zero."""
+        """Any number of tokens; `live` [T] (bool) strikes out the others, whose output is zero.  Keeps what backward needs."""
+        self._saved = None
         logits = x.float() @ self.Wr
         best, ids = logits.topk(self.top_k, dim=1)
         weights = torch.softmax(best, 1)
@@ -108,9 +111,12 @@ class ExpertFeedForward:
         return ops.moe_combine(out, positions, weights)
 
     def backward(self, dy):
-        """Gradients of x and of the parameters (by name) for dy, after forward_sorted of experts that are not gated."""
+        """Gradients of x and of the parameters (by name) for dy, after forward_sorted (which forward calls for more than 64
+        tokens) of experts that are not gated."""
         if self.gated:
             raise NotImplementedError("gated experts have no backward pass")
+        if self._saved is None:
+            raise RuntimeError("backward needs forward_sorted before it: forward of up to 64 tokens keeps nothing")
         x, ids, weights, positions, offsets, runs, rows, hidden, saved, out = self._saved
         dout, dweights = ops.moe_combine_backward(dy, out, positions, offsets, weights)
         drows = torch.zeros_like(rows)
