@@ -165,10 +165,19 @@ def gemm_mxfp4(A, B, bias=None, residual=None, act="none", C=None, stream=None):
                                         stream)
 
 
+def _shaped(t, name, shape):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s, got %s" % (name, list(shape), list(t.shape)))
+
+
 def selftest_mxfp4_skip_load(A, B, cta, item, limit_ns, stream=None):
     """Runs gemm_mxfp4 (A @ B.T alone) with one stage left unfilled, as
     selftest_linear_skip_load; returns the undefined output."""
     import torch
+    for Q, n in ((A, "A"), (B, "B")):
+        rows = Q.data.shape[0]
+        _shaped(Q.data, n, (rows, (A.columns + 31) // 32 * 16))
+        _shaped(Q.scales, n + "'s scales", ((rows + 127) // 128, (A.columns + 127) // 128, 512))
     with _outputs_on(stream):
         C = torch.empty((A.data.shape[0], B.data.shape[0]), dtype=torch.bfloat16, device=A.data.device)
     tensors = [_cuda_tensor(t, "operand", (torch.uint8,)) for t in (A.data, A.scales, B.data, B.scales)]
@@ -180,6 +189,7 @@ def selftest_mxfp4_skip_load(A, B, cta, item, limit_ns, stream=None):
 def selftest_linear_skip_load(A, B, cta, item, limit_ns, stream=None):
     """Runs gemm_bias_act (A @ B alone) with one stage of CTA (or CTA pair) `cta`,
     ring item `item`, left unfilled (see gbr.h); returns the undefined output."""
+    _shaped(B, "B", (A.shape[1], B.shape[1]))
     with _outputs_on(stream):
         C = A.new_empty(A.shape[0], B.shape[1])
     check(lib().gbr_selftest_linear_skip_load(
@@ -193,10 +203,12 @@ def selftest_moe_skip_load(X, Wr, W1, W2, top_k, cta, item, limit_ns, stream=Non
     `item`, left unfilled (see gbr.h); returns the undefined output."""
     with _outputs_on(stream):
         Y = X.new_empty(X.shape)
-    E, F = W2.shape[:2]
+    (T, D), (E, F) = X.shape, W2.shape[:2]
+    for t, n, shape in ((Wr, "Wr", (D, E)), (W1, "W1", (E, D, F)), (W2, "W2", (E, F, D))):
+        _shaped(t, n, shape)
     for t, n in ((X, "X"), (Wr, "Wr"), (W1, "W1"), (W2, "W2")):
         _cuda_tensor(t, n, (Wr.dtype if n == "Wr" else X.dtype,))
     check(lib().gbr_selftest_moe_skip_load(X.data_ptr(), Wr.data_ptr(), W1.data_ptr(), W2.data_ptr(), Y.data_ptr(),
-                                           X.shape[0], X.shape[1], F, E, top_k, cta, item, limit_ns,
+                                           T, D, F, E, top_k, cta, item, limit_ns,
                                            _stream_ptr(stream)))
     return Y
