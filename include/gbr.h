@@ -530,7 +530,8 @@ int moe_layer(const void *X, const float *Wr, const void *W1, const float *b1, c
  *   y = norm(X) * post   (post NULL: y = X)
  *   S = R + scale * gate * y
  *   H = norm(S) * pre    (with pre)
- * where norm divides a row by sqrt(mean of its squares + eps).
+ * where norm divides a row by sqrt(mean of its squares + eps); eps >= 0 and scale are
+ * within fp32's range (GBR_ERR_INVALID).
  *   X, R, S, H [rows, cols], cols below 2^30, ld... elements from row to row, >= cols, any
  *   alignment that the elements have; R may be NULL (zero).  post, pre [cols] fp32.  gate
  *   [gates, cols] or NULL (one): rows must be a multiple of gates, and row i uses

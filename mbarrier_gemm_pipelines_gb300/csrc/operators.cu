@@ -7,6 +7,7 @@
 #include <cmath>
 #include <exception>
 #include <initializer_list>
+#include <limits>
 #include <map>
 #include <mutex>
 #include <utility>
@@ -94,8 +95,11 @@ int check_norm(const char* fn, int64_t rows, int64_t cols, int64_t gates, const 
                int dtype, ResidualNormArgs* a) {
     int r = check_type(fn, dtype, &a->bf16);
     if (r != GBR_OK || (r = check_sizes(fn, rows, cols, 0)) != GBR_OK || (r = check_columns(fn, cols)) != GBR_OK) return r;
-    if (!(eps >= 0.0) || std::isinf(eps) || !std::isfinite(scale))
-        return report_errorf(GBR_ERR_INVALID, "%s: eps must be finite and not negative, scale finite", fn);
+    // Both go to the kernels as fp32, where a larger one would be infinite and an eps that vanishes no longer keep rows of
+    // zeros from 0 / 0.
+    constexpr double kMost = std::numeric_limits<float>::max();
+    if (!(eps >= 0.0 && eps <= kMost) || (eps > 0.0 && float(eps) == 0.f) || !(std::fabs(scale) <= kMost))
+        return report_errorf(GBR_ERR_INVALID, "%s: eps must not be negative, eps and scale within fp32", fn);
     if (gate == nullptr) gates = 0;
     else if (gates < 0 || (gates == 0 ? rows != 0 : rows % gates != 0))
         return report_errorf(GBR_ERR_INVALID, "%s: the rows must be a multiple of the gate's", fn);
