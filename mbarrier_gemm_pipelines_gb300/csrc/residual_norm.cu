@@ -21,6 +21,7 @@
 #include "row8.cuh"
 
 #include <algorithm>
+#include <cfloat>
 #include <cstdint>
 
 namespace gbr {
@@ -231,7 +232,41 @@ __global__ void __launch_bounds__(kMost, kMost == 512 ? 1 : 2) residual_norm_str
     copy_async_wait<0>();
 }
 
-// Rows that no CTA can hold: a CTA a row, read again for each mean.
+// Rows that no CTA can hold: a CTA a row, read again for each mean.  A thread has up to 2^20 terms of a sum, each addition
+// off by up to 2^-24 of it (4096 equal terms one after another: 2^-15).  So kRun terms are added as they come, and the runs
+// with what each addition lost handed on to the next one (Kahan's compensated summation: two roundings for any number).
+constexpr int32_t kRun = 16;
+struct LongSum {
+    float sum = 0.f, lost = 0.f;
+    __device__ __forceinline__ void add(float x) {
+        const float y = x - lost, t = sum + y;
+        lost = fabsf(t) <= FLT_MAX ? (t - sum) - y : 0.f;     // an infinite sum stays one
+        sum = t;
+    }
+};
+
+template <typename F>
+__device__ __forceinline__ float sum_in_runs(int32_t cols, F&& at) {
+    LongSum total;
+    int32_t c = int32_t(threadIdx.x);
+    for (; c + (kRun - 1) * 1024 < cols; c += kRun * 1024) {
+        float part = 0.f;
+#pragma unroll
+        for (int32_t i = 0; i < kRun; ++i) {
+            const float x = at(c + i * 1024);
+            part = fmaf(x, x, part);
+        }
+        total.add(part);
+    }
+    float part = 0.f;
+    for (; c < cols; c += 1024) {
+        const float x = at(c);
+        part = fmaf(x, x, part);
+    }
+    total.add(part);
+    return total.sum;
+}
+
 template <typename T>
 __device__ __forceinline__ float sum_at(const Args<T>& a, int64_t row, float q, int32_t c) {
     float y = to_f32(a.X[row * a.ldx + c]);
@@ -242,26 +277,19 @@ __device__ __forceinline__ float sum_at(const Args<T>& a, int64_t row, float q, 
 }
 
 template <typename T>
-__global__ void __launch_bounds__(1024) residual_norm_long_kernel(const Args<T> a) {
+__global__ void __launch_bounds__(1024, 1) residual_norm_long_kernel(const Args<T> a) {
     __shared__ float buf[2][1][32];
     ptx::griddep_wait();
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-        float sum[1] = {}, q = 1.f;
+        float sum[1], q = 1.f;
         if (a.post != nullptr) {
-            for (int32_t c = int32_t(threadIdx.x); c < a.cols; c += 1024) {
-                const float x = to_f32(a.X[row * a.ldx + c]);
-                sum[0] = fmaf(x, x, sum[0]);
-            }
+            sum[0] = sum_in_runs(a.cols, [&](int32_t c) { return to_f32(a.X[row * a.ldx + c]); });
             group_sum(sum, buf[0], 1024, 0);
             q = root(sum[0], a.inv_cols, a.eps);
         }
         float r = 0.f;
         if (a.H != nullptr) {
-            sum[0] = 0.f;
-            for (int32_t c = int32_t(threadIdx.x); c < a.cols; c += 1024) {
-                const float s = sum_at(a, row, q, c);
-                sum[0] = fmaf(s, s, sum[0]);
-            }
+            sum[0] = sum_in_runs(a.cols, [&](int32_t c) { return sum_at(a, row, q, c); });
             group_sum(sum, buf[1], 1024, 0);
             r = root(sum[0], a.inv_cols, a.eps);
         }
@@ -660,7 +688,9 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<
 // column, 8 of them a thread.
 constexpr int kLongThreads = 256;
 
-// stats[row] = {r, r^2 mean(u S), q, q^2 mean(v X)}
+// stats[row] = {r, r^2 mean(u S), q, q^2 mean(v X)}.  Sums as in the forward pass's long rows, in runs
+// of four pieces (16 terms).
+constexpr int32_t kRunPieces = 4;
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(1024, 1) residual_norm_stats_kernel(const GradArgs<T> a, float4* stats) {
     __shared__ float buf[2][3][32];
@@ -668,51 +698,63 @@ __global__ void __launch_bounds__(1024, 1) residual_norm_stats_kernel(const Grad
     const bool pre = a.pre != nullptr, post = a.post != nullptr;
     const int32_t t = int32_t(threadIdx.x), pieces = (a.cols + 8191) / 8192;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-        F2 ss = f2(0.f), us = f2(0.f), xx = f2(0.f), vx = f2(0.f);
-        for (int32_t p = 0; p < pieces; ++p) {
-            Raw8<T> s, dh, x;
-            F2 w[4];
-            if (pre) {
-                load_raw8<VEC>(s, a.S + row * a.lds, p, t, 1024, a.cols);
-                load_raw8<VEC>(dh, a.dH + row * a.lddh, p, t, 1024, a.cols);
-                load_pairs<float, VEC>(w, a.pre, p, t, 1024, a.cols);
-            }
-            if (post) load_raw8<VEC>(x, a.X + row * a.ldx, p, t, 1024, a.cols);
+        LongSum all_ss, all_us, all_xx, all_vx;
+        for (int32_t p0 = 0; p0 < pieces; p0 += kRunPieces) {
+            F2 ss = f2(0.f), us = f2(0.f), xx = f2(0.f);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (pre) {
-                    ss = fma2(raw_pair(s, i), raw_pair(s, i), ss);
-                    us = fma2(mul2(raw_pair(dh, i), w[i]), raw_pair(s, i), us);
-                }
-                if (post) xx = fma2(raw_pair(x, i), raw_pair(x, i), xx);
-            }
-        }
-        float sum[3] = {sum_pair(ss), sum_pair(us), sum_pair(xx)};
-        group_sum(sum, buf[0], 1024, 0);
-        const float r = root(sum[0], a.inv_cols, a.eps), rm = r * (r * sum[1] * a.inv_cols);
-        const float q = post ? root(sum[2], a.inv_cols, a.eps) : 1.f;
-        if (post)
-            for (int32_t p = 0; p < pieces; ++p) {
-                Raw8<T> s, dh, x, ds = {}, g;
-                F2 w[4], wp[4];
+            for (int32_t p = p0; p < p0 + kRunPieces; ++p) {
+                if (p >= pieces) break;
+                Raw8<T> s, dh, x;
+                F2 w[4];
                 if (pre) {
                     load_raw8<VEC>(s, a.S + row * a.lds, p, t, 1024, a.cols);
                     load_raw8<VEC>(dh, a.dH + row * a.lddh, p, t, 1024, a.cols);
                     load_pairs<float, VEC>(w, a.pre, p, t, 1024, a.cols);
                 }
-                load_raw8<VEC>(x, a.X + row * a.ldx, p, t, 1024, a.cols);
-                load_pairs<float, VEC>(wp, a.post, p, t, 1024, a.cols);
-                if (a.dS != nullptr) load_raw8<VEC>(ds, a.dS + row * a.ldds, p, t, 1024, a.cols);
-                if (a.G != nullptr) load_raw8<VEC>(g, a.G + row / a.per_gate * a.ldg, p, t, 1024, a.cols);
+                if (post) load_raw8<VEC>(x, a.X + row * a.ldx, p, t, 1024, a.cols);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    F2 e = raw_pair(ds, i);
-                    if (pre) e = fma2(f2(r), fma2(raw_pair(s, i), f2(-rm), mul2(raw_pair(dh, i), w[i])), e);
-                    if (a.G != nullptr) e = mul2(e, raw_pair(g, i));
-                    vx = fma2(mul2(e, wp[i]), raw_pair(x, i), vx);
+                    if (pre) {
+                        ss = fma2(raw_pair(s, i), raw_pair(s, i), ss);
+                        us = fma2(mul2(raw_pair(dh, i), w[i]), raw_pair(s, i), us);
+                    }
+                    if (post) xx = fma2(raw_pair(x, i), raw_pair(x, i), xx);
                 }
             }
-        float dot[1] = {sum_pair(vx)};
+            all_ss.add(sum_pair(ss)), all_us.add(sum_pair(us)), all_xx.add(sum_pair(xx));
+        }
+        float sum[3] = {all_ss.sum, all_us.sum, all_xx.sum};
+        group_sum(sum, buf[0], 1024, 0);
+        const float r = root(sum[0], a.inv_cols, a.eps), rm = r * (r * sum[1] * a.inv_cols);
+        const float q = post ? root(sum[2], a.inv_cols, a.eps) : 1.f;
+        if (post)
+            for (int32_t p0 = 0; p0 < pieces; p0 += kRunPieces) {
+                F2 vx = f2(0.f);
+#pragma unroll
+                for (int32_t p = p0; p < p0 + kRunPieces; ++p) {
+                    if (p >= pieces) break;
+                    Raw8<T> s, dh, x, ds = {}, g;
+                    F2 w[4], wp[4];
+                    if (pre) {
+                        load_raw8<VEC>(s, a.S + row * a.lds, p, t, 1024, a.cols);
+                        load_raw8<VEC>(dh, a.dH + row * a.lddh, p, t, 1024, a.cols);
+                        load_pairs<float, VEC>(w, a.pre, p, t, 1024, a.cols);
+                    }
+                    load_raw8<VEC>(x, a.X + row * a.ldx, p, t, 1024, a.cols);
+                    load_pairs<float, VEC>(wp, a.post, p, t, 1024, a.cols);
+                    if (a.dS != nullptr) load_raw8<VEC>(ds, a.dS + row * a.ldds, p, t, 1024, a.cols);
+                    if (a.G != nullptr) load_raw8<VEC>(g, a.G + row / a.per_gate * a.ldg, p, t, 1024, a.cols);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        F2 e = raw_pair(ds, i);
+                        if (pre) e = fma2(f2(r), fma2(raw_pair(s, i), f2(-rm), mul2(raw_pair(dh, i), w[i])), e);
+                        if (a.G != nullptr) e = mul2(e, raw_pair(g, i));
+                        vx = fma2(mul2(e, wp[i]), raw_pair(x, i), vx);
+                    }
+                }
+                all_vx.add(sum_pair(vx));
+            }
+        float dot[1] = {all_vx.sum};
         group_sum(dot, buf[1], 1024, 0);
         if (threadIdx.x == 0) stats[row] = make_float4(r, rm, q, a.scale * (q * (q * dot[0] * a.inv_cols)));
     }

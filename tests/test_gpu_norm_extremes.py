@@ -60,3 +60,44 @@ def test_sums_over_no_rows_are_zero(gbr, cols, post, dtype):  # noqa: F811
                                                    torch.cuda.current_stream().cuda_stream))
         assert (sums == 0).all()
     gbr.check_device()
+
+
+def equal_terms(cols, dtype, **kw):
+    """Two rows of one value: each of thousands of roundings of a sum then goes the same way for long, where those of random
+    values would cancel."""
+    def full(v, shape, t=dtype):
+        return torch.full(shape, v, device="cuda", dtype=t)
+    return dict({n: full(v, (2, cols)) for n, v in kw.items()}, post=full(0.7, (cols,), torch.float32),
+                pre=full(1.1, (cols,), torch.float32), gate=None, scale=1.0, eps=block.EPS)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("cols", [(1 << 22) + 3, 1 << 23])
+def test_sums_of_millions_of_columns(gbr, cols, dtype):  # noqa: F811
+    """Bars in units u = 2^-24 of a value, the rounding of one operation.  A sum adds at most 16 terms, the runs with two
+    roundings, 10 levels over the CTA: 28 u.  A root halves that and has 4 u of its own (2 ulp), eps and the
+    mean 1 u: 19 u.
+      S      root, five operations: 24 u of m                             below 2^-19 m
+      H      S, its root, two products: 24 + 24 + 19 + 2 = 69 u           below 2^-17 m (|H| is at most its m)
+      dR     root twice (38), the signed mean (28, its terms two), eight operations: 80 u of m      2^-17 m
+      dX     what dR has, and the same once more: 160 u of m               2^-16 m
+      dpost, dpre   dR's or less, 19 for the root, two rows: below         2^-17 m
+    One after another, 4096 terms of 0.3^2 were off by 2^-15 of their sum.
+    """
+    a = equal_terms(cols, dtype, X=0.3, R=0.2)
+    S, H = gbr.residual_norm(**a)
+    s, h, m = block.ref.residual_norm(**a)
+    block.within(S, s, 2.0 ** -19 * m, "S")
+    block.within(H, h, 2.0 ** -17 * m * block.ref.root(s, a["eps"]) * a["pre"].double(), "H")
+    del s, h, m
+    # Half of dH and dS the other way: no projection cancels its other term.
+    a = equal_terms(cols, dtype, X=0.3, S=0.3, dH=0.7, dS=0.1)
+    a["dH"][:, ::2], a["dS"][:, ::2] = -0.2, 0.4
+    grads = gbr.residual_norm_backward(**a)
+    g, m = block.ref.residual_norm_backward(**a)
+    for name, got in zip(block.NAMES, grads):
+        if name == "dgate":
+            assert got is None
+            continue
+        block.within(got, g[name], 2.0 ** (-16 if name == "dX" else -17) * m[name], name)
+    gbr.check_device()
