@@ -84,8 +84,9 @@ class ExpertFeedForward:
         """Any number of tokens; `live` [T] (bool) strikes out the others, whose output is zero.  Keeps what backward needs."""
         self._saved = None
         logits = x.float() @ self.Wr
-        best, ids = logits.topk(self.top_k, dim=1)
-        weights = torch.softmax(best, 1)
+        # As moe_layer chooses: of equal logits the lowest expert, NaN behind all others (topk puts NaN first, ties anyhow).
+        ids = (-logits).sort(dim=1, stable=True).indices[:, :self.top_k].contiguous()
+        weights = torch.softmax(logits.gather(1, ids), 1)
         if live is not None:
             ids = torch.where(live[:, None], ids, -1)
         positions, offsets = ops.moe_sort(ids, self.Wr.shape[1])
