@@ -11,7 +11,9 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/record_function.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/impl/LocalDispatchKeySet.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
@@ -158,12 +160,20 @@ bool truth(PyObject* o) {
     return v != 0;
 }
 
+// Whether somebody would see at::empty: a dispatch mode or another key that was added to this thread, or a profiler.  (The
+// fill of new memory under deterministic algorithms is left out: the library writes every output whole.)
+bool outputs_watched() {
+    const c10::DispatchKeySet added = c10::impl::tls_local_dispatch_key_set().included_ - c10::default_included_set;
+    return !added.empty() || at::getStepCallbacksUnlessEmpty(at::RecordScope::FUNCTION).has_value();
+}
+
 // The call's stream: the current one, or the `stream` argument, which is then the current one until the call
 // ends, so that the outputs made here are that stream's to PyTorch's allocator.  From the current stream's share it could
 // hand out memory that a kernel there still reads, and give an output away while the other stream writes it.
 class CallStream {
 public:
-    CallStream(PyObject* o, int dev) : handle_(c10::cuda::getCurrentCUDAStream(dev).stream()) {
+    CallStream(PyObject* o, int dev)
+        : handle_(c10::cuda::getCurrentCUDAStream(dev).stream()), device_(dev), watched_(outputs_watched()) {
         if (o == Py_None) return;
         PyObject* v = PyLong_Check(o) ? Py_NewRef(o) : PyObject_GetAttrString(o, "cuda_stream");
         if (v == nullptr) throw Refused();
@@ -178,9 +188,13 @@ public:
                                 : c10::cuda::getStreamFromExternal(given, c10::DeviceIndex(dev)));
     }
     operator gbr_stream_t() const { return reinterpret_cast<gbr_stream_t>(handle_); }
+    int device() const { return device_; }
+    bool watched() const { return watched_; }
 
 private:
     cudaStream_t handle_;
+    int device_;
+    bool watched_;
     c10::cuda::OptionalCUDAStreamGuard guard_;
 };
 
@@ -192,10 +206,15 @@ PyObject* written(PyObject* o) {
     return Py_NewRef(o);
 }
 
-// A new tensor on the call's stream, past the dispatcher: at::empty took 1.3 us of the host's time, more than half of a
-// call with two outputs and one launch.
-at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, int dev) {
-    return at::Tensor(at::detail::empty_cuda(shape, type, c10::Device(c10::kCUDA, c10::DeviceIndex(dev)), std::nullopt));
+// A new tensor on the call's stream, past the dispatcher where nobody watches it: at::empty took 1.3 us of the host's time,
+// more than half of a call with two outputs and one launch.
+[[gnu::cold, gnu::noinline]] at::Tensor fresh_seen(at::IntArrayRef shape, at::ScalarType type, c10::Device on) {
+    return at::empty(shape, at::TensorOptions(type).device(on));
+}
+at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const CallStream& st) {
+    const c10::Device on(c10::kCUDA, c10::DeviceIndex(st.device()));
+    if (C10_UNLIKELY(st.watched())) return fresh_seen(shape, type, on);
+    return at::Tensor(at::detail::empty_cuda(shape, type, on, std::nullopt));
 }
 
 // An output: the caller's, or a new one.
@@ -206,13 +225,13 @@ struct Out {
     PyObject* wrap() const { return given != nullptr ? written(given) : THPVariable_Wrap(made); }
 };
 
-Out out_mat(PyObject* o, const char* name, const at::Tensor& like, int dev, int64_t rows, int64_t cols) {
+Out out_mat(PyObject* o, const char* name, const at::Tensor& like, const CallStream& st, int64_t rows, int64_t cols) {
     Out r;
     if (o != Py_None) {
         r.given = o;
-        r.m = mat_of(o, name, like.scalar_type(), dev, rows, cols);
+        r.m = mat_of(o, name, like.scalar_type(), st.device(), rows, cols);
     } else {
-        r.made = fresh({rows, cols}, like.scalar_type(), dev);
+        r.made = fresh({rows, cols}, like.scalar_type(), st);
         r.m.p = r.made.data_ptr();
         r.m.rows = rows, r.m.cols = cols, r.m.ld = cols > 0 ? cols : 1;
     }
@@ -264,7 +283,7 @@ PyObject* dropout_add_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const CallStream st(a[6], dev);
         const bool has_r = a[1] != Py_None, has_y = a[5] != Py_None;
         at::Tensor made;
-        if (!has_y) made = fresh(X.sizes(), type, dev);
+        if (!has_y) made = fresh(X.sizes(), type, st);
         const at::Tensor& Y = has_y ? tensor(a[5], "Y") : made;
         Mat x, r, y;
         if (X.dim() == 2) {
@@ -311,9 +330,9 @@ PyObject* gemm_bias_act_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const uint64_t seed = bits64(a[6], "seed"), offset = bits64(a[7], "offset");
         const bool want_z = a[9] != Py_None || truth(a[10]);
         const CallStream st(a[11], dev);
-        const Out C = out_mat(a[8], "C", tA, dev, M, N);
+        const Out C = out_mat(a[8], "C", tA, st, M, N);
         Out Z;
-        if (want_z) Z = out_mat(a[9], "Z", tA, dev, M, N);
+        if (want_z) Z = out_mat(a[9], "Z", tA, st, M, N);
         call([&] {
             return gemm_bias_act(A.p, A.ld, B.p, B.ld, bias, R.p, R.ld, C.m.p, C.m.ld, Z.m.p, Z.m.ld, M, N, A.cols,
                                  GBR_BF16, act, p, seed, offset, st);
@@ -356,14 +375,14 @@ PyObject* gemm_bias_act_backward_py(PyObject*, PyObject* const* a, Py_ssize_t n)
         if (!three) refuse(PyExc_ValueError, "needs must be three truth values");
         const CallStream st(a[12], dev);
         Out dA, dB, db;
-        if (want[0]) dA = out_mat(a[8], "dA", tA, dev, M, K);
-        if (want[1]) dB = out_mat(a[9], "dB", tA, dev, K, N);
+        if (want[0]) dA = out_mat(a[8], "dA", tA, st, M, K);
+        if (want[1]) dB = out_mat(a[9], "dB", tA, st, K, N);
         if (want[2]) {
             if (a[10] != Py_None) {
                 db.given = a[10];
                 db.m.p = packed(tensor(a[10], "dbias"), "dbias", at::kFloat, dev, {N});
             } else {
-                db.made = fresh({N}, at::kFloat, dev);
+                db.made = fresh({N}, at::kFloat, st);
                 db.m.p = db.made.data_ptr();
             }
         }
@@ -399,15 +418,15 @@ PyObject* moe_layer_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
             Y.given = a[9];
             Y.m.p = packed(tensor(a[9], "Y"), "Y", at::kBFloat16, dev, {T, D});
         } else {
-            Y.made = fresh({T, D}, at::kBFloat16, dev);
+            Y.made = fresh({T, D}, at::kBFloat16, st);
             Y.m.p = Y.made.data_ptr();
         }
         const bool routing = truth(a[10]);
         at::Tensor ids, weights;
         if (routing) {
             const int64_t k = top_k < 0 || top_k > E ? 0 : top_k;       // a wrong top_k is refused by the call
-            ids = fresh({T, k}, at::kLong, dev);
-            weights = fresh({T, k}, at::kFloat, dev);
+            ids = fresh({T, k}, at::kLong, st);
+            weights = fresh({T, k}, at::kFloat, st);
         }
         call([&] {
             return moe_layer(x, static_cast<const float*>(wr), w1, static_cast<const float*>(b1), w2,
@@ -451,13 +470,13 @@ void truths(PyObject* o, bool* want, int count) {
 }
 
 // A contiguous output: the caller's, or a new one.
-Out out_packed(PyObject* o, const char* name, at::ScalarType type, int dev, at::IntArrayRef shape) {
+Out out_packed(PyObject* o, const char* name, at::ScalarType type, const CallStream& st, at::IntArrayRef shape) {
     Out r;
     if (o != Py_None) {
         r.given = o;
-        r.m.p = packed(tensor(o, name), name, type, dev, shape);
+        r.m.p = packed(tensor(o, name), name, type, st.device(), shape);
     } else {
-        r.made = fresh(shape, type, dev);
+        r.made = fresh(shape, type, st);
         r.m.p = r.made.data_ptr();
     }
     return r;
@@ -493,9 +512,9 @@ PyObject* residual_norm_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const bool same = a[7] == Py_None && a[1] == Py_None && a[2] == Py_None && a[3] == Py_None && scale == 1.0 &&
                           (a[8] == Py_None || tensor(a[8], "H").data_ptr() != X.p);
         Out S;
-        if (!same) S = out_mat(a[7], "S", tX, dev, X.rows, X.cols);
+        if (!same) S = out_mat(a[7], "S", tX, st, X.rows, X.cols);
         Out H;
-        if (want_h) H = out_mat(a[8], "H", tX, dev, X.rows, X.cols);
+        if (want_h) H = out_mat(a[8], "H", tX, st, X.rows, X.cols);
         // Vectors of no columns have no address.
         if (X.cols > 0)
             call([&] {
@@ -543,11 +562,11 @@ PyObject* residual_norm_backward_py(PyObject*, PyObject* const* a, Py_ssize_t n)
         want[2] = want[2] && has_post, want[3] = want[3] && has_gate, want[4] = want[4] && has_pre;
         const CallStream st(a[15], dev);
         Out dX, dR, dpost, dG, dpre;
-        if (want[0]) dX = out_mat(a[9], "dX", like, dev, rows, cols);
-        if (want[1]) dR = out_mat(a[10], "dR", like, dev, rows, cols);
-        if (want[2]) dpost = out_packed(a[11], "dpost", at::kFloat, dev, {cols});
-        if (want[3]) dG = out_mat(a[12], "dgate", like, dev, G.rows, cols);
-        if (want[4]) dpre = out_packed(a[13], "dpre", at::kFloat, dev, {cols});
+        if (want[0]) dX = out_mat(a[9], "dX", like, st, rows, cols);
+        if (want[1]) dR = out_mat(a[10], "dR", like, st, rows, cols);
+        if (want[2]) dpost = out_packed(a[11], "dpost", at::kFloat, st, {cols});
+        if (want[3]) dG = out_mat(a[12], "dgate", like, st, G.rows, cols);
+        if (want[4]) dpre = out_packed(a[13], "dpre", at::kFloat, st, {cols});
         if (cols > 0)
             call([&] {
                 return residual_norm_backward(dS.p, dS.ld, dH.p, dH.ld, X.p, X.ld, S.p, S.ld, post, G.p, G.ld, G.rows, scale,
@@ -570,8 +589,8 @@ PyObject* moe_sort_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int64_t E = integer(a[1]);
         if (E < 1 || E > INT32_MAX - 1) refuse(PyExc_ValueError, "num_experts must be positive");
         const CallStream st(a[4], dev);
-        const Out pos = out_packed(a[2], "positions", at::kInt, dev, ids.sizes());
-        const Out off = out_packed(a[3], "offsets", at::kInt, dev, {std::min<int64_t>(E, 1 << 20) + 1});
+        const Out pos = out_packed(a[2], "positions", at::kInt, st, ids.sizes());
+        const Out off = out_packed(a[3], "offsets", at::kInt, st, {std::min<int64_t>(E, 1 << 20) + 1});
         call([&] {
             return moe_sort(static_cast<const int64_t*>(p), ids.numel(), as_int(E), static_cast<int32_t*>(pos.m.p),
                             static_cast<int32_t*>(off.m.p), st);
@@ -612,7 +631,7 @@ PyObject* moe_dispatch_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
             refuse(PyExc_ValueError, "positions are of %lld tokens, X has %lld rows", static_cast<long long>(p.T),
                    static_cast<long long>(X.rows));
         const CallStream st(a[4], dev);
-        const Out Xs = out_mat(a[3], "Xs", tX, dev, p.T * p.k, X.cols);
+        const Out Xs = out_mat(a[3], "Xs", tX, st, p.T * p.k, X.cols);
         call([&] {
             return moe_dispatch(X.p, X.ld, p.positions, p.offsets, as_int(p.experts), Xs.m.p, Xs.m.ld, p.T, p.k, X.cols,
                                 type_code(type), st);
@@ -633,7 +652,7 @@ PyObject* moe_combine_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
         Mat R;
         if (a[3] != Py_None) R = mat_of(a[3], "residual", type, dev, p.T, Ys.cols);
         const CallStream st(a[5], dev);
-        const Out Y = out_mat(a[4], "Y", tYs, dev, p.T, Ys.cols);
+        const Out Y = out_mat(a[4], "Y", tYs, st, p.T, Ys.cols);
         call([&] {
             return moe_combine(Ys.p, Ys.ld, Ys.rows, p.positions, static_cast<const float*>(w), R.p, R.ld, Y.m.p, Y.m.ld,
                                p.T, p.k, Ys.cols, type_code(type), st);
@@ -660,8 +679,8 @@ PyObject* moe_combine_backward_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (want[1]) Ys = mat_of(a[1], "Ys", type, dev, p.T * p.k, dY.cols);
         const CallStream st(a[8], dev);
         Out dYs, dw;
-        if (want[0]) dYs = out_mat(a[5], "dYs", tdY, dev, p.T * p.k, dY.cols);
-        if (want[1]) dw = out_packed(a[6], "dweights", at::kFloat, dev, {p.T, p.k});
+        if (want[0]) dYs = out_mat(a[5], "dYs", tdY, st, p.T * p.k, dY.cols);
+        if (want[1]) dw = out_packed(a[6], "dweights", at::kFloat, st, {p.T, p.k});
         call([&] {
             return moe_combine_backward(dY.p, dY.ld, Ys.p, Ys.ld, p.positions, p.offsets, as_int(p.experts),
                                         static_cast<const float*>(w), dYs.m.p, dYs.m.ld, static_cast<float*>(dw.m.p), p.T,
@@ -698,8 +717,8 @@ PyObject* quantize_mxfp4_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const bool transposed = truth(a[1]);
         const int64_t rows = transposed ? X.cols : X.rows, cols = transposed ? X.rows : X.cols;
         const CallStream st(a[4], dev);
-        const Out data = out_packed(a[2], "data", at::kByte, dev, {rows, (cols + 31) / 32 * 16});
-        const Out scales = out_packed(a[3], "scales", at::kByte, dev, {(rows + 127) / 128, (cols + 127) / 128, 512});
+        const Out data = out_packed(a[2], "data", at::kByte, st, {rows, (cols + 31) / 32 * 16});
+        const Out scales = out_packed(a[3], "scales", at::kByte, st, {(rows + 127) / 128, (cols + 127) / 128, 512});
         call([&] {
             return quantize_mxfp4(X.p, X.ld, data.m.p, scales.m.p, rows, cols, transposed ? 1 : 0, type_code(type), st);
         });
@@ -728,7 +747,7 @@ PyObject* dequantize_mxfp4_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
             X.given = a[4];
             X.m = mat_of(a[4], "X", type, dev, q.rows, q.cols);
         } else {
-            X.made = fresh({q.rows, q.cols}, type, dev);
+            X.made = fresh({q.rows, q.cols}, type, st);
             X.m.p = X.made.data_ptr();
             X.m.ld = q.cols > 0 ? q.cols : 1;
         }
@@ -756,7 +775,7 @@ PyObject* gemm_mxfp4_py(PyObject*, PyObject* const* a, Py_ssize_t n) {
             C.given = a[9];
             C.m = mat_of(a[9], "C", at::kBFloat16, dev, A.rows, B.rows);
         } else {
-            C.made = fresh({A.rows, B.rows}, at::kBFloat16, dev);
+            C.made = fresh({A.rows, B.rows}, at::kBFloat16, st);
             C.m.p = C.made.data_ptr();
             C.m.ld = B.rows > 0 ? B.rows : 1;
         }
