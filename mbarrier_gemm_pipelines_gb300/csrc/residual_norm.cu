@@ -555,8 +555,9 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const F2 S = raw_pair(s[v], i), H = raw_pair(dh[v], i);
-                        d[v][i] = fma2(r2, fma2(S, m2, mul2(H, wpre[v][i])), d[v][i]);
-                        spre[v][i] = fma2(H, mul2(S, r2), spre[v][i]);
+                        const F2 n = mul2(S, r2);
+                        d[v][i] = fma2(n, m2, fma2(r2, mul2(H, wpre[v][i]), d[v][i]));
+                        spre[v][i] = fma2(H, n, spre[v][i]);
                     }
                 }
             }
