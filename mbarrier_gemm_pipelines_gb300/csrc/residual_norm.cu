@@ -622,8 +622,7 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<
             if (tpr > 32 && (!want_x || !post)) __syncthreads();   // buf[0], for the next rows
         }
         if (want_run) {
-            // dpost gains scale gate sum, dgate is scale weight sum.  Of no rows both are zero, whatever gate and weight hold.
-            const bool some = r0 < r1;
+            // dpost gains scale gate sum, dgate is scale weight sum.
             if (FULL) join(srun);
             if (want_post && (!FULL || group == 0))
 #pragma unroll
@@ -635,7 +634,7 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const F2 k = run_gate ? mul2(f2(a.scale), w[i]) : f2(a.scale);
-                        if (some) spost[v][i] = fma2(srun[v][i], k, spost[v][i]);
+                        spost[v][i] = fma2(srun[v][i], k, spost[v][i]);
                     }
                     if (FULL) {
                         store_sums(sum, spost[v], v);
@@ -653,7 +652,7 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const GradArgs<
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             srun[v][i] = mul2(srun[v][i], f2(a.scale));
-                            if (post && some) srun[v][i] = mul2(srun[v][i], w[i]);
+                            if (post) srun[v][i] = mul2(srun[v][i], w[i]);
                         }
                         if (a.segments > 1)
                             store_sums(a.gate_part + int64_t(item) * a.cols, srun[v], v);
@@ -1026,6 +1025,36 @@ int64_t cut_rows(GradArgs<T>* a, int32_t gates, int64_t ctas, int32_t groups) {
     return std::min<int64_t>(a->items, ctas);
 }
 
+int launch_sums(PartSums sums, int32_t runs, cudaStream_t stream) {
+    void* args[] = {&sums};
+    const cudaError_t e = launch_kernel(reinterpret_cast<void*>(&norm_sums_kernel),
+                                        dim3(unsigned(cdiv(sums.cols, 32)), unsigned(runs)), 512, 0, 1, args, stream);
+    if (e != cudaSuccess) return report_cuda(e, "launching the sums of residual_norm_backward");
+    count_launch();
+    return GBR_OK;
+}
+
+// Sums over no rows: zeros, whatever weights and gates hold (factors that the kernels above apply to sums).
+int no_rows(const ResidualNormGradArgs& s, cudaStream_t stream) {
+    constexpr int64_t kGates = 65533;                   // of a launch, whose grid has 65535 runs at most
+    for (int64_t first = 0; first == 0 || first < s.gates; first += kGates) {
+        PartSums sums = {};
+        sums.cols = s.cols;
+        int32_t runs = 0;
+        if (first == 0)
+            for (float* out : {s.dpost, s.dpre})
+                if (out != nullptr) sums.of[sums.n++] = {nullptr, out, 0, 1, 0, false}, ++runs;
+        const int32_t n = s.dG.p ? int32_t(std::min<int64_t>(kGates, s.gates - first)) : 0;
+        if (n > 0) {
+            uint8_t* out = static_cast<uint8_t*>(s.dG.w()) + first * s.dG.ld * (s.bf16 ? 2 : 4);
+            sums.of[sums.n++] = {nullptr, out, s.dG.ld, n, 0, s.bf16}, runs += n;
+        }
+        const int r = runs > 0 ? launch_sums(sums, runs, stream) : GBR_OK;
+        if (r != GBR_OK) return r;
+    }
+    return GBR_OK;
+}
+
 template <typename T>
 int run_backward(const ResidualNormGradArgs& s, const LibCtx& c, cudaStream_t stream) {
     GradArgs<T> a = {};
@@ -1151,13 +1180,7 @@ int run_backward(const ResidualNormGradArgs& s, const LibCtx& c, cudaStream_t st
     }
     if (e != cudaSuccess) return report_cuda(e, "launching residual_norm_backward");
     count_launch();
-    if (runs == 0) return GBR_OK;
-    void* args[] = {&sums};
-    e = launch_kernel(reinterpret_cast<void*>(&norm_sums_kernel), dim3(unsigned(cdiv(s.cols, 32)), unsigned(runs)), 512,
-                      0, 1, args, stream);
-    if (e != cudaSuccess) return report_cuda(e, "launching the sums of residual_norm_backward");
-    count_launch();
-    return GBR_OK;
+    return runs == 0 ? GBR_OK : launch_sums(sums, runs, stream);
 }
 
 }  // namespace
@@ -1167,6 +1190,7 @@ int launch_residual_norm(const ResidualNormArgs& a, const LibCtx& c, cudaStream_
 }
 
 int launch_residual_norm_grad(const ResidualNormGradArgs& a, const LibCtx& c, cudaStream_t stream) {
+    if (a.rows == 0) return no_rows(a, stream);
     return a.bf16 ? run_backward<__nv_bfloat16>(a, c, stream) : run_backward<float>(a, c, stream);
 }
 

@@ -101,3 +101,13 @@ def test_sums_of_millions_of_columns(gbr, cols, dtype):  # noqa: F811
             continue
         block.within(got, g[name], 2.0 ** (-16 if name == "dX" else -17) * m[name], name)
     gbr.check_device()
+
+
+def test_many_gates_over_no_rows(gbr):  # noqa: F811
+    """More of them than one launch's grid has places."""
+    x = torch.empty(0, 33, device="cuda", dtype=torch.bfloat16)
+    gate = torch.full((140001, 33), float("inf"), device="cuda", dtype=torch.bfloat16)
+    view, whole = block.placed(torch.ones_like(gate), 3, 35)
+    got = gbr.residual_norm_backward(x, None, x, None, gate=gate, dgate=view)[3]
+    assert got is view and not view.any() and (block.others(view, whole) == 5).all()
+    gbr.check_device()
