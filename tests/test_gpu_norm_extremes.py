@@ -111,3 +111,19 @@ def test_many_gates_over_no_rows(gbr):  # noqa: F811
     got = gbr.residual_norm_backward(x, None, x, None, gate=gate, dgate=view)[3]
     assert got is view and not view.any() and (block.others(view, whole) == 5).all()
     gbr.check_device()
+
+
+FORWARD = [(1, 4096, "bf16", True, 1, True, True, 1.0), (301, 1001, "fp32", True, 7, True, True, 0.25), (2500, 2048, "bf16", True, 1, True, True, 0.5),
+           (3, 20000, "fp32", True, 0, True, True, 1.0), (2, 40000, "bf16", True, 1, True, True, 1.0)]
+
+
+@pytest.mark.parametrize("size", [1e15, 1e-15])
+@pytest.mark.parametrize("case", FORWARD, ids=["-".join(map(str, c)) for c in FORWARD])
+def test_large_and_small_rows(gbr, case, size):  # noqa: F811
+    """A block's output of any size beside a residual stream of it, whose gate brings both together."""
+    a = block.norm_inputs(case)
+    a.update(eps=0.0, X=(a["X"].double() * size).to(a["X"].dtype), R=(a["R"].double() * size).to(a["R"].dtype))
+    if a["gate"] is not None:
+        a["gate"] = (a["gate"].double() * size).to(a["gate"].dtype)
+    block.check_norm(a, *gbr.residual_norm(**a))
+    gbr.check_device()
