@@ -415,7 +415,8 @@ int combine(const MoeRowsArgs& a, int64_t rows, const LibCtx& c, cudaStream_t st
     p.T_ = a.T, p.k = a.k, p.D = a.D, p.rows = rows;
     const bool vec = a.D % 8 == 0 && aligned16<T>(a.Ys, rows) && aligned16<T>(a.R, a.T) && aligned16<T>(a.Y, a.T);
     // One or two choices: two vectors a thread; more: one, and four choices at once (eight spill registers: 2000 tokens of
-    // 2048 columns and 6 choices 16.7 us with four, 23.8 with eight).
+    // 2048 columns and 6 choices, bf16, 16.7 us with four, 23.8 with eight; fp32 spills 16 to 44 bytes with four, its
+    // gradients 124 to 156).
     const bool few = vec && a.k <= 2;
     void* const two[2] = GBR_BOTH(moe_combine_rows_kernel<T, kVec, 2, 2);
     void* const four[2] = GBR_BOTH(moe_combine_rows_kernel<T, kVec, 1, 4);
