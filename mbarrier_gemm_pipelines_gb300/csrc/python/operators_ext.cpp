@@ -209,7 +209,9 @@ PyObject* written(PyObject* o) {
 // A new tensor on the call's stream, past the dispatcher where nobody watches it: at::empty took 1.3 us of the host's time,
 // more than half of a call with two outputs and one launch.
 [[gnu::cold, gnu::noinline]] at::Tensor fresh_seen(at::IntArrayRef shape, at::ScalarType type, c10::Device on) {
-    return at::empty(shape, at::TensorOptions(type).device(on));
+    at::Tensor t = at::empty(shape, at::TensorOptions(type).device(on));
+    packed(t, "a new output", type, on.index(), shape);      // a mode may give anything
+    return t;
 }
 at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const CallStream& st) {
     const c10::Device on(c10::kCUDA, c10::DeviceIndex(st.device()));

@@ -78,3 +78,28 @@ def test_deterministic_algorithms_change_no_result(gbr):  # noqa: F811
             torch.use_deterministic_algorithms(before)
         assert all(torch.equal(a, b) for a, b in zip(got, want)), name
     gbr.check_device()
+
+
+class Elsewhere(TorchDispatchMode):
+    """Gives memory that is not what was asked for."""
+    def __init__(self, **how):
+        super().__init__()
+        self.how = how
+
+    def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+        kwargs = dict(kwargs or {})
+        if func.overloadpacket is torch.ops.aten.empty:
+            kwargs.update(self.how)
+        return func(*args, **kwargs)
+
+
+def test_a_mode_that_gives_something_else_is_refused(gbr):  # noqa: F811
+    """Before its address goes to a kernel."""
+    todo = calls(gbr)
+    before = gbr.launch_count()
+    for how in (dict(device=torch.device("cpu")), dict(device=torch.device("meta")), dict(dtype=torch.float64)):
+        for name, call, _ in todo:
+            with Elsewhere(**how), pytest.raises((ValueError, TypeError)):
+                call()
+    assert gbr.launch_count() == before
+    gbr.check_device()
