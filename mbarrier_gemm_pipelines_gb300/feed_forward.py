@@ -83,6 +83,8 @@ class ExpertFeedForward:
     def forward_sorted(self, x, live=None):
         """Any number of tokens; `live` [T] (bool) strikes out the others, whose output is zero.  Keeps what backward needs."""
         self._saved = None
+        if not 1 <= self.top_k <= self.Wr.shape[1]:
+            raise ValueError("top_k must be 1 to %d, the number of experts, got %d" % (self.Wr.shape[1], self.top_k))
         logits = x.float() @ self.Wr
         # As moe_layer chooses: of equal logits the lowest expert, NaN behind all others (topk puts NaN first, ties anyhow).
         ids = (-logits).sort(dim=1, stable=True).indices[:, :self.top_k].contiguous()
